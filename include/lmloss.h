@@ -50,10 +50,12 @@ typedef enum {
     LMLOSS_ERR_BAD_TARGET = 4,    /* device: target not in [0, V) and not -100             */
     LMLOSS_ERR_BAD_SEGMENT = 5,   /* device: segment id >= num_segments                    */
     LMLOSS_ERR_RANGE = 6,         /* device: GSPO log-ratio sum beyond +-2^31              */
-    LMLOSS_ERR_TIMEOUT = 7        /* device: a bounded wait on a copy expired              */
+    LMLOSS_ERR_TIMEOUT = 7,       /* device: a bounded wait on a copy expired              */
+    LMLOSS_ERR_BAD_PARENT = 8     /* device: a beam's parent outside [0, K)                */
 } lmloss_status;
 
-typedef enum { LMLOSS_BF16 = 0, LMLOSS_FP32 = 1 } lmloss_dtype;
+/* FP16 is taken by the vocabulary operators below only. */
+typedef enum { LMLOSS_BF16 = 0, LMLOSS_FP32 = 1, LMLOSS_FP16 = 2 } lmloss_dtype;
 
 typedef enum {
     LMLOSS_REDUCE_SUM = 0,        /* every term scaled by 1 / denominator                  */
@@ -302,6 +304,172 @@ lmloss_status lmloss_shard_merge(lmloss_handle handle, const lmloss_args* args, 
                                  int32_t K, cudaStream_t stream);
 lmloss_status lmloss_shard_grad(lmloss_handle handle, const lmloss_args* args, int64_t v0, int64_t V_total,
                                 cudaStream_t stream);
+
+/* ---- Vocabulary operators: the two ends of the vocabulary around the loss
+ *
+ * Embedding lookup and its gradient (the table the tokens come in through, often
+ * the same matrix as the LM head), and beam search's step over [rows, V] logits
+ * with the reordering of the beams' states (what the LM head answers with).
+ *
+ * They share a handle of their own: a workspace of the caller's size and a
+ * device error word.  The conventions at the top of this header hold: caller-owned
+ * device memory, asynchronous on the given stream, no allocation and no host
+ * synchronisation per call (so a call can be captured in a CUDA graph), argument
+ * errors returned before anything is launched, data errors in the error word, one
+ * handle per stream.  Results do not depend on the timing of the GPU's blocks:
+ * the same inputs give the same bits.
+ */
+typedef struct lmloss_vocab_ctx* lmloss_vocab_handle;
+
+/* A handle on `device` with `workspace_bytes` of workspace: the most that any of
+ * its calls needs by lmloss_embedding_workspace / lmloss_beam_workspace (0 serves
+ * the lookup and the reordering, which need none). */
+lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_t workspace_bytes);
+
+/* Free the handle and its workspace.  Synchronises the handle's device. */
+lmloss_status lmloss_vocab_destroy(lmloss_vocab_handle handle);
+
+/* Read and clear the handle's device error word.  Synchronises the device. */
+lmloss_status lmloss_vocab_get_device_error(lmloss_vocab_handle handle);
+
+typedef enum { LMLOSS_INT64 = 0, LMLOSS_INT32 = 1 } lmloss_id_dtype;
+
+/*
+ * Arguments of an embedding call.  `table` is [V, ld_table], `rows` is
+ * [T, ld_rows], the first D columns of each used; elements naturally aligned.
+ * An id of LMLOSS_IGNORE_INDEX marks a position without a token.
+ */
+typedef struct {
+    const void* ids;             /* [T] token of each position                             */
+    int64_t T;                   /* positions, >= 0 and < 2^30                             */
+    int64_t V;                   /* rows of the table, >= 1 and < 2^31 - 1                 */
+    int64_t D;                   /* columns, >= 1                                          */
+    void* table;                 /* forward: the weights (read);                           */
+                                 /* backward: the weights' gradient (written)              */
+    int64_t ld_table;            /* row stride in elements, >= D                           */
+    void* rows;                  /* forward: the embeddings (written);                     */
+                                 /* backward: the embeddings' gradient (read)              */
+    int64_t ld_rows;             /* row stride in elements, >= D                           */
+    int32_t ids_dtype;           /* lmloss_id_dtype                                        */
+    int32_t table_dtype;         /* lmloss_dtype, each of the three with each              */
+    int32_t rows_dtype;          /* lmloss_dtype                                           */
+    float scale;                 /* finite                                                 */
+    int32_t accumulate;          /* backward: 0 writes the whole gradient (zeros where no  */
+                                 /* position holds the token), 1 adds to what is there     */
+                                 /* and leaves the other rows alone                        */
+} lmloss_embedding_args;
+
+/* Host-only validation of `args` (no CUDA call). */
+lmloss_status lmloss_embedding_check_args(const lmloss_embedding_args* args);
+
+/* The workspace that lmloss_embedding_backward needs for `args` (pointers are
+ * not looked at).  It grows with T and D. */
+lmloss_status lmloss_embedding_workspace(const lmloss_embedding_args* args, size_t* bytes);
+
+/*
+ * rows[t] = scale * table[ids[t]], rounded once to the rows' type; zeros where
+ * ids[t] is LMLOSS_IGNORE_INDEX.  Any other id outside [0, V) sets
+ * LMLOSS_ERR_BAD_TARGET and gives a row of NaN.
+ */
+lmloss_status lmloss_embedding_forward(lmloss_vocab_handle handle, const lmloss_embedding_args* args,
+                                       cudaStream_t stream);
+
+/*
+ * table[v] (+)= scale * sum of rows[t] over the positions t with ids[t] = v.
+ * The positions are sorted by token; each token's rows are added in fp32, in an
+ * order that the ids alone fix, and the result is rounded once.  An id outside
+ * [0, V) that is not LMLOSS_IGNORE_INDEX sets LMLOSS_ERR_BAD_TARGET and adds
+ * nothing.
+ */
+lmloss_status lmloss_embedding_backward(lmloss_vocab_handle handle, const lmloss_embedding_args* args,
+                                        cudaStream_t stream);
+
+#define LMLOSS_MAX_BEAMS 64      /* beams of a sequence, and candidates of a beam step     */
+
+/*
+ * Arguments of a beam step over B sequences of K beams: logits is
+ * [B * K, ld], row b * K + k for beam k of sequence b.
+ */
+typedef struct {
+    const void* logits;          /* [B * K, ld] dtype, first V columns used                */
+    int64_t B;                   /* sequences, >= 0                                        */
+    int64_t V;                   /* vocabulary columns, >= 1 and < 2^31 - 1                */
+    int64_t ld;                  /* row stride in elements, >= V                           */
+    int32_t K;                   /* beams of a sequence, 1 .. LMLOSS_MAX_BEAMS             */
+    int32_t M;                   /* candidates wanted, 1 .. LMLOSS_MAX_BEAMS               */
+    int32_t dtype;               /* lmloss_dtype, any of the three                         */
+    float length_penalty;        /* alpha >= 0 (0 without lengths): candidates are ranked  */
+                                 /* by score / length^alpha                                */
+    int64_t eos_token;           /* the end token, -1 = none (not with `finished`)         */
+    const float* scores;         /* [B, K] summed log-probability of each beam             */
+    const uint8_t* finished;     /* [B, K] or NULL: 1 = the beam has ended                 */
+    const int32_t* lengths;      /* [B, K] or NULL: tokens of each beam so far             */
+    const int32_t* token_mask;   /* NULL, or rows of ceil(V / 32) words: bit v % 32 of     */
+                                 /* word v / 32 is set where token v may follow            */
+    int64_t mask_stride;         /* words between rows of the mask; 0 = one row for all    */
+    float* scores_out;           /* [B, M]                                                 */
+    int32_t* parents_out;        /* [B, M] beam of the sequence that the candidate goes on */
+    int64_t* tokens_out;         /* [B, M]                                                 */
+    float* lse_out;              /* optional [B, K]: logsumexp of each row (0 if finished) */
+    uint8_t* finished_out;       /* optional [B, M]                                        */
+    int32_t* lengths_out;        /* optional [B, M], only with lengths                     */
+} lmloss_beam_args;
+
+/* Host-only validation of `args` (no CUDA call). */
+lmloss_status lmloss_beam_check_args(const lmloss_beam_args* args);
+
+/* The workspace that lmloss_beam_step needs for `args` (pointers are not looked at). */
+lmloss_status lmloss_beam_workspace(const lmloss_beam_args* args, size_t* bytes);
+
+/*
+ * For each sequence, the M best candidates (k, v) by score
+ *   scores[k] + logits[k][v] - lse_k,   lse_k = logsumexp of the whole row,
+ * (divided by length^alpha for the ranking), best first, equal ones by k, then by
+ * v.  Rows are ranked against one another in fp64; scores_out holds the score
+ * before the division, rounded to fp32.
+ *   - A finished beam's row is not read: its one candidate is (k, eos_token) with
+ *     its score as it is, and its length does not grow.
+ *   - A token whose mask bit is 0 is no candidate; the row's logsumexp still
+ *     covers it.
+ *   - A candidate whose score is not finite is none (a masked token, a -inf logit,
+ *     a beam at -inf; NaN or +inf in a row take the whole row out).
+ *   - Where fewer than M are left, the rest gets score -inf, token
+ *     LMLOSS_IGNORE_INDEX, parent m % K, finished 0 and that parent's length.
+ * finished_out: the parent had ended, or the token is eos_token.
+ */
+lmloss_status lmloss_beam_step(lmloss_vocab_handle handle, const lmloss_beam_args* args, cudaStream_t stream);
+
+/*
+ * One state of the beams, as bytes: for each outer index (o0, o1, o2) and each row
+ * r = b * K + k a run of `inner` bytes at
+ *   base + r * row_stride + o0 * outer_stride[0] + o1 * outer_stride[1] + o2 * outer_stride[2].
+ * dst == src reorders in place (then with the same strides and K_out == K);
+ * otherwise the two must not overlap.  Strides are in bytes and not negative; no
+ * two runs of dst may overlap.
+ */
+typedef struct {
+    const void* src;
+    void* dst;
+    int64_t inner;               /* bytes of a run, >= 0                                   */
+    int64_t src_row_stride;
+    int64_t dst_row_stride;
+    int64_t outer[3];            /* outer counts, >= 0; 1 where unused                     */
+    int64_t src_outer_stride[3];
+    int64_t dst_outer_stride[3];
+} lmloss_beam_state;
+
+/* Host-only validation of a reordering (no CUDA call). */
+lmloss_status lmloss_beam_check_states(const lmloss_beam_state* states, int32_t num_states, int64_t B, int32_t K,
+                                       int32_t K_out);
+
+/*
+ * Every state's row b * K_out + m becomes its row b * K + parents[b, m]
+ * (parents: [B, K_out] int32, device).  `states` is a host array, read during the
+ * call.  A parent outside [0, K) sets LMLOSS_ERR_BAD_PARENT and leaves that row of
+ * dst as it is.
+ */
+lmloss_status lmloss_beam_reorder(lmloss_vocab_handle handle, const lmloss_beam_state* states, int32_t num_states,
+                                  const int32_t* parents, int64_t B, int32_t K, int32_t K_out, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,8 +19,11 @@ HEADER = os.path.join(_ROOT, "include", "lmloss.h")
 # staged-row kernel's eight (dtype, teacher, temperature, entropy) instantiation
 # sets, one object each so that they compile in parallel
 UNITS = [("lmloss.cu", [], "lmloss.o")] + [
-    ("fused_inst.cu", [f"-DLMLOSS_FUSED_VARIANT={k}"], f"fused_{k}.o") for k in range(8)]
-DEPENDS = ["lmloss.cu", "fused_inst.cu", "fused_entry.cuh", "kernels.cuh", "aux_kernels.cuh", "ptx.cuh"]
+    ("fused_inst.cu", [f"-DLMLOSS_FUSED_VARIANT={k}"], f"fused_{k}.o") for k in range(8)] + [
+    # the vocabulary operators
+    (f"{name}.cu", [], f"{name}.o") for name in ("vocab_handle", "embedding", "beam_step", "beam_reorder")]
+DEPENDS = ["lmloss.cu", "fused_inst.cu", "fused_entry.cuh", "kernels.cuh", "aux_kernels.cuh", "ptx.cuh",
+           "vocab_common.cuh", "vocab_handle.cu", "embedding.cu", "beam_step.cu", "beam_reorder.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC"]
@@ -33,8 +36,13 @@ LMLOSS_ERR_BAD_TARGET = 4
 LMLOSS_ERR_BAD_SEGMENT = 5
 LMLOSS_ERR_RANGE = 6
 LMLOSS_ERR_TIMEOUT = 7
+LMLOSS_ERR_BAD_PARENT = 8
 LMLOSS_BF16 = 0
 LMLOSS_FP32 = 1
+LMLOSS_FP16 = 2
+LMLOSS_INT64 = 0
+LMLOSS_INT32 = 1
+LMLOSS_MAX_BEAMS = 64
 LMLOSS_REDUCE_SUM = 0
 LMLOSS_REDUCE_TOKEN_MEAN = 1
 LMLOSS_IGNORE_INDEX = -100
@@ -122,6 +130,62 @@ class lmloss_call_info(ctypes.Structure):
                 ("launches", "path", "cluster", "threads", "nbuf", "grid", "smem_bytes", "reserved")]
 
 
+class lmloss_embedding_args(ctypes.Structure):
+    _fields_ = [
+        ("ids", ctypes.c_void_p),
+        ("T", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("rows", ctypes.c_void_p),
+        ("ld_rows", ctypes.c_int64),
+        ("ids_dtype", ctypes.c_int32),
+        ("table_dtype", ctypes.c_int32),
+        ("rows_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("accumulate", ctypes.c_int32),
+    ]
+
+
+class lmloss_beam_args(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("B", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("K", ctypes.c_int32),
+        ("M", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("length_penalty", ctypes.c_float),
+        ("eos_token", ctypes.c_int64),
+        ("scores", ctypes.c_void_p),
+        ("finished", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("token_mask", ctypes.c_void_p),
+        ("mask_stride", ctypes.c_int64),
+        ("scores_out", ctypes.c_void_p),
+        ("parents_out", ctypes.c_void_p),
+        ("tokens_out", ctypes.c_void_p),
+        ("lse_out", ctypes.c_void_p),
+        ("finished_out", ctypes.c_void_p),
+        ("lengths_out", ctypes.c_void_p),
+    ]
+
+
+class lmloss_beam_state(ctypes.Structure):
+    _fields_ = [
+        ("src", ctypes.c_void_p),
+        ("dst", ctypes.c_void_p),
+        ("inner", ctypes.c_int64),
+        ("src_row_stride", ctypes.c_int64),
+        ("dst_row_stride", ctypes.c_int64),
+        ("outer", ctypes.c_int64 * 3),
+        ("src_outer_stride", ctypes.c_int64 * 3),
+        ("dst_outer_stride", ctypes.c_int64 * 3),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -154,6 +218,20 @@ def load() -> ctypes.CDLL:
         "lmloss_shard_merge": ([h, ctypes.POINTER(lmloss_args), ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32,
                                 ctypes.c_void_p], st),
         "lmloss_shard_grad": ([h, ctypes.POINTER(lmloss_args), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p], st),
+        "lmloss_vocab_create": ([ctypes.POINTER(h), ctypes.c_int, ctypes.c_size_t], st),
+        "lmloss_vocab_destroy": ([h], st),
+        "lmloss_vocab_get_device_error": ([h], st),
+        "lmloss_embedding_check_args": ([ctypes.POINTER(lmloss_embedding_args)], st),
+        "lmloss_embedding_workspace": ([ctypes.POINTER(lmloss_embedding_args), ctypes.POINTER(ctypes.c_size_t)], st),
+        "lmloss_embedding_forward": ([h, ctypes.POINTER(lmloss_embedding_args), ctypes.c_void_p], st),
+        "lmloss_embedding_backward": ([h, ctypes.POINTER(lmloss_embedding_args), ctypes.c_void_p], st),
+        "lmloss_beam_check_args": ([ctypes.POINTER(lmloss_beam_args)], st),
+        "lmloss_beam_workspace": ([ctypes.POINTER(lmloss_beam_args), ctypes.POINTER(ctypes.c_size_t)], st),
+        "lmloss_beam_step": ([h, ctypes.POINTER(lmloss_beam_args), ctypes.c_void_p], st),
+        "lmloss_beam_check_states": ([ctypes.POINTER(lmloss_beam_state), ctypes.c_int32, ctypes.c_int64,
+                                      ctypes.c_int32, ctypes.c_int32], st),
+        "lmloss_beam_reorder": ([h, ctypes.POINTER(lmloss_beam_state), ctypes.c_int32, ctypes.c_void_p,
+                                 ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -256,3 +334,65 @@ def lmloss_forward_backward_noalloc(args: lmloss_args, stream: int) -> int:
     fn.argtypes = [ctypes.POINTER(lmloss_args), ctypes.c_void_p]
     fn.restype = ctypes.c_int
     return fn(ctypes.byref(args), ctypes.c_void_p(stream))
+
+
+# ---- vocabulary operators
+def lmloss_vocab_create(device: int, workspace_bytes: int) -> ctypes.c_void_p:
+    h = ctypes.c_void_p()
+    st = load().lmloss_vocab_create(ctypes.byref(h), int(device), int(workspace_bytes))
+    if st != LMLOSS_OK:
+        raise LMLossError(st, "lmloss_vocab_create")
+    return h
+
+
+def lmloss_vocab_destroy(handle) -> int:
+    return load().lmloss_vocab_destroy(handle)
+
+
+def lmloss_vocab_get_device_error(handle) -> int:
+    return load().lmloss_vocab_get_device_error(handle)
+
+
+def lmloss_embedding_check_args(args: lmloss_embedding_args) -> int:
+    return load().lmloss_embedding_check_args(ctypes.byref(args))
+
+
+def lmloss_embedding_workspace(args: lmloss_embedding_args) -> int:
+    n = ctypes.c_size_t()
+    st = load().lmloss_embedding_workspace(ctypes.byref(args), ctypes.byref(n))
+    if st != LMLOSS_OK:
+        raise LMLossError(st, "lmloss_embedding_workspace")
+    return n.value
+
+
+def lmloss_embedding_forward(handle, args: lmloss_embedding_args, stream: int) -> int:
+    return load().lmloss_embedding_forward(handle, ctypes.byref(args), stream)
+
+
+def lmloss_embedding_backward(handle, args: lmloss_embedding_args, stream: int) -> int:
+    return load().lmloss_embedding_backward(handle, ctypes.byref(args), stream)
+
+
+def lmloss_beam_check_args(args: lmloss_beam_args) -> int:
+    return load().lmloss_beam_check_args(ctypes.byref(args))
+
+
+def lmloss_beam_workspace(args: lmloss_beam_args) -> int:
+    n = ctypes.c_size_t()
+    st = load().lmloss_beam_workspace(ctypes.byref(args), ctypes.byref(n))
+    if st != LMLOSS_OK:
+        raise LMLossError(st, "lmloss_beam_workspace")
+    return n.value
+
+
+def lmloss_beam_step(handle, args: lmloss_beam_args, stream: int) -> int:
+    return load().lmloss_beam_step(handle, ctypes.byref(args), stream)
+
+
+def lmloss_beam_check_states(states, B: int, K: int, K_out: int) -> int:
+    """states: a ctypes array of lmloss_beam_state."""
+    return load().lmloss_beam_check_states(states, len(states), B, K, K_out)
+
+
+def lmloss_beam_reorder(handle, states, parents: int, B: int, K: int, K_out: int, stream: int) -> int:
+    return load().lmloss_beam_reorder(handle, states, len(states), parents, B, K, K_out, stream)

@@ -1,0 +1,229 @@
+// Reordering of the beams' states: row b * K_out + m of every state becomes its row
+// b * K + parents[b, m].  Nothing is computed: the kernel is bound by memory, each
+// surviving beam's run of bytes read once and each new one written once.  In
+// place, beams that keep their slot are not touched at all.
+#include <climits>
+
+#include "vocab_common.cuh"
+
+namespace lmloss {
+namespace {
+
+constexpr int kMaxK = LMLOSS_MAX_BEAMS;
+constexpr int kThreads = 128;
+constexpr int kStates = 16;                  // states of one launch
+
+struct State {
+    const unsigned char* src;
+    unsigned char* dst;
+    int64_t src_row, dst_row;
+    int64_t src_outer[3], dst_outer[3];
+    int64_t units;               // of a run
+    int64_t chunks;              // blocks over a run
+    int64_t first;               // first block of this state in the launch
+    int outer[3];
+    int unit;                    // bytes moved at a time: 16, 8, 4, 2 or 1
+    int in_place;
+};
+
+struct ReorderParams {
+    State st[kStates];
+    int n;
+    int B, K, K_out;
+    const int32_t* parents;
+    int* err;
+};
+
+// The runs of one outer index and sequence, columns [u0, u0 + kThreads) in units.
+template <class U>
+__device__ void move_runs(const ReorderParams& p, const State& st, const int* parent, int b, int64_t o, int64_t u0,
+                          unsigned char* stage)
+{
+    const int64_t o2 = o % st.outer[2], o1 = o / st.outer[2] % st.outer[1], o0 = o / st.outer[2] / st.outer[1];
+    const int64_t u = u0 + threadIdx.x;
+    const bool in = u < st.units;
+    const unsigned char* src = st.src + static_cast<int64_t>(b) * p.K * st.src_row + o0 * st.src_outer[0] +
+                               o1 * st.src_outer[1] + o2 * st.src_outer[2] + u * sizeof(U);
+    unsigned char* dst = st.dst + static_cast<int64_t>(b) * p.K_out * st.dst_row + o0 * st.dst_outer[0] +
+                         o1 * st.dst_outer[1] + o2 * st.dst_outer[2] + u * sizeof(U);
+    if (!in) return;
+    if (!st.in_place) {
+        for (int m = 0; m < p.K_out; ++m)
+            if (parent[m] >= 0)
+                *reinterpret_cast<U*>(dst + m * st.dst_row) = *reinterpret_cast<const U*>(src + parent[m] * st.src_row);
+        return;
+    }
+    // every beam that another slot takes is read before any slot is written; a
+    // thread reads and writes its own columns only
+    U* own = reinterpret_cast<U*>(stage) + threadIdx.x;
+    for (int m = 0; m < p.K_out; ++m)
+        if (parent[m] >= 0 && parent[m] != m)
+            own[m * kThreads] = *reinterpret_cast<const U*>(src + parent[m] * st.src_row);
+    for (int m = 0; m < p.K_out; ++m)
+        if (parent[m] >= 0 && parent[m] != m) *reinterpret_cast<U*>(dst + m * st.dst_row) = own[m * kThreads];
+}
+
+__global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_constant__ ReorderParams p)
+{
+    extern __shared__ __align__(16) unsigned char stage[];   // [K][kThreads] units, in place only
+    __shared__ int parent[kMaxK];
+    int i = 0;
+    while (i + 1 < p.n && blockIdx.x >= p.st[i + 1].first) ++i;
+    const State& st = p.st[i];
+    int64_t k = blockIdx.x - st.first;
+    const int64_t chunk = k % st.chunks;
+    k /= st.chunks;
+    const int b = static_cast<int>(k % p.B);
+    const int64_t o = k / p.B;
+    for (int m = threadIdx.x; m < p.K_out; m += kThreads) {
+        const int q = p.parents[static_cast<int64_t>(b) * p.K_out + m];
+        const bool ok = q >= 0 && q < p.K;
+        if (!ok) set_error(p.err, kErrBadParent);
+        parent[m] = ok ? q : -1;
+    }
+    __syncthreads();
+    const int64_t u0 = chunk * kThreads;
+    switch (st.unit) {
+    case 16: move_runs<uint4>(p, st, parent, b, o, u0, stage); break;
+    case 8: move_runs<uint2>(p, st, parent, b, o, u0, stage); break;
+    case 4: move_runs<uint32_t>(p, st, parent, b, o, u0, stage); break;
+    case 2: move_runs<uint16_t>(p, st, parent, b, o, u0, stage); break;
+    default: move_runs<uint8_t>(p, st, parent, b, o, u0, stage); break;
+    }
+}
+
+// ------------------------------------------------------------------- host
+// The last byte offset that a side of a state reaches, or -1 if it passes 2^62.
+int64_t reach(int64_t row_stride, int64_t rows, const int64_t* outer, const int64_t* outer_stride, int64_t inner)
+{
+    __int128 r = static_cast<__int128>(rows - 1) * row_stride + inner;
+    for (int i = 0; i < 3; ++i) r += static_cast<__int128>(outer[i] - 1) * outer_stride[i];
+    return r > (static_cast<__int128>(1) << 62) ? -1 : static_cast<int64_t>(r);
+}
+
+bool empty(const lmloss_beam_state& s)
+{
+    return s.inner == 0 || s.outer[0] == 0 || s.outer[1] == 0 || s.outer[2] == 0;
+}
+
+lmloss_status check_states(const lmloss_beam_state* states, int32_t n, int64_t B, int32_t K, int32_t K_out)
+{
+    if (n < 0 || (n > 0 && !states) || B < 0 || K < 1 || K_out < 1) return LMLOSS_ERR_INVALID_ARG;
+    if (K > LMLOSS_MAX_BEAMS || K_out > LMLOSS_MAX_BEAMS) return LMLOSS_ERR_INVALID_ARG;
+    if (B > (int64_t(1) << 24)) return LMLOSS_ERR_UNSUPPORTED;
+    for (int i = 0; i < n; ++i) {
+        const lmloss_beam_state& s = states[i];
+        if (s.inner < 0 || s.src_row_stride < 0 || s.dst_row_stride < 0) return LMLOSS_ERR_INVALID_ARG;
+        for (int k = 0; k < 3; ++k) {
+            if (s.outer[k] < 0 || s.src_outer_stride[k] < 0 || s.dst_outer_stride[k] < 0) return LMLOSS_ERR_INVALID_ARG;
+            if (s.outer[k] > INT_MAX) return LMLOSS_ERR_UNSUPPORTED;
+        }
+        if (B == 0 || empty(s)) continue;
+        if (!s.src || !s.dst) return LMLOSS_ERR_INVALID_ARG;
+        // the runs of one sequence's new beams are apart
+        if (K_out > 1 && s.dst_row_stride == 0) return LMLOSS_ERR_INVALID_ARG;
+        if (s.src == s.dst) {
+            if (K != K_out || s.src_row_stride != s.dst_row_stride) return LMLOSS_ERR_INVALID_ARG;
+            for (int k = 0; k < 3; ++k)
+                if (s.outer[k] > 1 && s.src_outer_stride[k] != s.dst_outer_stride[k]) return LMLOSS_ERR_INVALID_ARG;
+        }
+        const int64_t rs = reach(s.src_row_stride, B * K, s.outer, s.src_outer_stride, s.inner);
+        const int64_t rd = reach(s.dst_row_stride, B * K_out, s.outer, s.dst_outer_stride, s.inner);
+        if (rs < 0 || rd < 0) return LMLOSS_ERR_INVALID_ARG;
+        if (s.src != s.dst) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(s.src), d = reinterpret_cast<uintptr_t>(s.dst);
+            if (a < d + static_cast<uintptr_t>(rd) && d < a + static_cast<uintptr_t>(rs)) return LMLOSS_ERR_INVALID_ARG;
+        }
+    }
+    return LMLOSS_OK;
+}
+
+// the widest unit that every run starts at and is a multiple of
+int unit_of(const lmloss_beam_state& s)
+{
+    uint64_t all = reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst) |
+                   static_cast<uint64_t>(s.inner) | static_cast<uint64_t>(s.src_row_stride) |
+                   static_cast<uint64_t>(s.dst_row_stride);
+    for (int k = 0; k < 3; ++k)
+        if (s.outer[k] > 1)
+            all |= static_cast<uint64_t>(s.src_outer_stride[k]) | static_cast<uint64_t>(s.dst_outer_stride[k]);
+    int u = 16;
+    while (all & static_cast<uint64_t>(u - 1)) u /= 2;
+    return u;
+}
+
+}  // namespace
+}  // namespace lmloss
+
+using namespace lmloss;
+
+extern "C" {
+
+lmloss_status lmloss_beam_check_states(const lmloss_beam_state* states, int32_t n, int64_t B, int32_t K, int32_t K_out)
+{
+    return check_states(states, n, B, K, K_out);
+}
+
+lmloss_status lmloss_beam_reorder(lmloss_vocab_handle h, const lmloss_beam_state* states, int32_t n,
+                                  const int32_t* parents, int64_t B, int32_t K, int32_t K_out, cudaStream_t stream)
+{
+    if (!h) return LMLOSS_ERR_INVALID_ARG;
+    lmloss_status st = check_states(states, n, B, K, K_out);
+    if (st != LMLOSS_OK) return st;
+    if (B > 0 && n > 0 && !parents) return LMLOSS_ERR_INVALID_ARG;
+    if (B == 0) return LMLOSS_OK;
+    // block counts first: nothing is launched if one state is too large
+    for (int i = 0; i < n; ++i) {
+        const lmloss_beam_state& s = states[i];
+        if (empty(s)) continue;
+        const __int128 blocks = static_cast<__int128>((s.inner / unit_of(s) + kThreads - 1) / kThreads) * B *
+                                s.outer[0] * s.outer[1] * s.outer[2];
+        if (blocks > INT_MAX / kStates) return LMLOSS_ERR_UNSUPPORTED;
+    }
+    VocabDeviceGuard g(h->device);
+    if (!g.ok) return LMLOSS_ERR_CUDA;
+    for (int i = 0; i < n;) {
+        ReorderParams p{};
+        p.B = static_cast<int>(B);
+        p.K = K;
+        p.K_out = K_out;
+        p.parents = parents;
+        p.err = h->err;
+        int64_t blocks = 0;
+        bool staged = false;
+        for (; i < n && p.n < kStates; ++i) {
+            const lmloss_beam_state& s = states[i];
+            if (empty(s)) continue;
+            State& d = p.st[p.n++];
+            d.src = static_cast<const unsigned char*>(s.src);
+            d.dst = static_cast<unsigned char*>(s.dst);
+            d.src_row = s.src_row_stride;
+            d.dst_row = s.dst_row_stride;
+            for (int k = 0; k < 3; ++k) {
+                d.outer[k] = static_cast<int>(s.outer[k]);
+                d.src_outer[k] = s.src_outer_stride[k];
+                d.dst_outer[k] = s.dst_outer_stride[k];
+            }
+            d.unit = unit_of(s);
+            d.units = s.inner / d.unit;
+            d.chunks = (d.units + kThreads - 1) / kThreads;
+            d.in_place = s.src == s.dst;
+            staged = staged || d.in_place;
+            d.first = blocks;
+            blocks += d.chunks * B * s.outer[0] * s.outer[1] * s.outer[2];
+        }
+        if (blocks == 0) continue;
+        size_t smem = staged ? static_cast<size_t>(K) * kThreads * 16 : 0;
+        if (smem > 48 * 1024 &&
+            cudaFuncSetAttribute(beam_reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 LMLOSS_MAX_BEAMS * kThreads * 16) != cudaSuccess) {
+            cudaGetLastError();
+            return LMLOSS_ERR_CUDA;
+        }
+        beam_reorder_kernel<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
+        if ((st = vocab_launch_err()) != LMLOSS_OK) return st;
+    }
+    return LMLOSS_OK;
+}
+
+}  // extern "C"

@@ -384,6 +384,7 @@ const char* lmloss_status_string(lmloss_status s)
     case LMLOSS_ERR_BAD_SEGMENT: return "segment id outside [0, num_segments)";
     case LMLOSS_ERR_RANGE: return "GSPO log-ratio sum out of range";
     case LMLOSS_ERR_TIMEOUT: return "bounded wait on a copy expired";
+    case LMLOSS_ERR_BAD_PARENT: return "beam parent outside [0, K)";
     }
     return "unknown status";
 }
