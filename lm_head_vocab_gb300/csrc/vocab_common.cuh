@@ -11,13 +11,19 @@
 #include "../../include/lmloss.h"
 #include "kernels.cuh"
 
+// Counters of blocks that have finished, apart from the workspace: all zero
+// between calls, each returned to zero by the block that finds it full.
+constexpr int kVocabCounters = 1 << 16;
+
 struct lmloss_vocab_ctx {
     int device = 0;
     int num_sms = 0;
     int smem_optin = 0;
-    unsigned char* ws = nullptr;   // [ws_bytes], after the error word's 256 bytes
-    size_t ws_bytes = 0;
+    unsigned char* mem = nullptr;    // what was allocated: the error word, the counters, the workspace
     int* err = nullptr;
+    unsigned* counters = nullptr;    // [kVocabCounters]
+    unsigned char* ws = nullptr;     // [ws_bytes]
+    size_t ws_bytes = 0;
 };
 
 namespace lmloss {
@@ -134,6 +140,46 @@ struct Pack {
         for (int i = 0; i < kWords; ++i) w[i] = 0u;
     }
 };
+
+// N elements from an address aligned to one element only: the aligned 16-byte
+// blocks around it, shifted into place in registers.  Every block must lie inside
+// memory that may be read, [lo, hi); `inside_blocks` says so.
+template <class T, int N>
+__device__ __forceinline__ bool inside_blocks(const unsigned char* p, const unsigned char* lo, const unsigned char* hi)
+{
+    const unsigned char* a = reinterpret_cast<const unsigned char*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+    return a >= lo && a + N * T::kBytes + 16 <= hi;
+}
+template <class T, int N>
+__device__ __forceinline__ void load_shifted(Pack<T, N>& q, const unsigned char* p)
+{
+    constexpr int kVecs = N * T::kBytes / 16 + 1;
+    const uintptr_t ad = reinterpret_cast<uintptr_t>(p);
+    const uint4* a = reinterpret_cast<const uint4*>(ad & ~uintptr_t(15));
+    uint32_t w[4 * kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const uint4 v = __ldg(a + i);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+    const uint32_t b = static_cast<uint32_t>(ad);
+    if (b & 8u) {
+#pragma unroll
+        for (int i = 0; i + 2 < 4 * kVecs; ++i) w[i] = w[i + 2];
+    }
+    if (b & 4u) {
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * kVecs; ++i) w[i] = w[i + 1];
+    }
+    if constexpr (T::kBytes == 2) {
+        const uint32_t sh = (b & 2u) * 8u;   // 0 or 16 bits
+#pragma unroll
+        for (int i = 0; i < Pack<T, N>::kWords; ++i) q.w[i] = __funnelshift_r(w[i], w[i + 1], sh);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Pack<T, N>::kWords; ++i) q.w[i] = w[i];
+    }
+}
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,4 +1,5 @@
-// The vocabulary operators' handle: a workspace of the caller's size and an error word.
+// The vocabulary operators' handle: a workspace of the caller's size, an error word
+// and the counters.
 #include <new>
 
 #include "vocab_common.cuh"
@@ -18,22 +19,25 @@ lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_
     if (!h) return LMLOSS_ERR_CUDA;
     h->device = device;
     h->ws_bytes = vocab_align(workspace_bytes);
+    constexpr size_t kHead = 256 + kVocabCounters * sizeof(unsigned);
     unsigned char* mem = nullptr;
     if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) != cudaSuccess ||
-        cudaMalloc(&mem, 256 + h->ws_bytes) != cudaSuccess) {
+        cudaMalloc(&mem, kHead + h->ws_bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return LMLOSS_ERR_CUDA;
     }
-    if (cudaMemset(mem, 0, 256 + h->ws_bytes) != cudaSuccess) {
+    if (cudaMemset(mem, 0, kHead + h->ws_bytes) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(mem);
         delete h;
         return LMLOSS_ERR_CUDA;
     }
+    h->mem = mem;
     h->err = reinterpret_cast<int*>(mem);
-    h->ws = mem + 256;
+    h->counters = reinterpret_cast<unsigned*>(mem + 256);
+    h->ws = mem + kHead;
     *handle = h;
     return LMLOSS_OK;
 }
@@ -43,7 +47,7 @@ lmloss_status lmloss_vocab_destroy(lmloss_vocab_handle h)
     if (!h) return LMLOSS_ERR_INVALID_ARG;
     VocabDeviceGuard g(h->device);
     cudaDeviceSynchronize();
-    const cudaError_t e = cudaFree(h->err);
+    const cudaError_t e = cudaFree(h->mem);
     delete h;
     return e == cudaSuccess ? LMLOSS_OK : LMLOSS_ERR_CUDA;
 }

@@ -111,8 +111,7 @@ def check(ops, logits, scores, *, M, finished=None, eos=-1, lengths=None, alpha=
             k = got[m][0]
             assert abs(S[b, m] - s) <= (0 if fin[b, k] else tol[b, k]) + 2.0 ** -24 * abs(s) + 1e-45, (b, m, S[b, m], s)
             assert abs(key - c[m][0]) <= t
-            near = [abs(c[m][0] - c[i][0]) <= t and c[i][1] != c[m][1] for i in (m - 1, m + 1) if 0 <= i < len(c)]
-            if not any(near):
+            if not any(abs(c[m][0] - x[0]) <= t and x[1] != c[m][1] for x in c):
                 assert got[m] == (c[m][1], c[m][2]), (b, m, got[m], c[m])
             assert fo[b, m] == (fin[b, k] or got[m][1] == eos)
             if lo is not None:
