@@ -393,7 +393,7 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle handle, const lmloss
 typedef struct {
     const void* logits;          /* [B * K, ld] dtype, first V columns used                */
     int64_t B;                   /* sequences, >= 0                                        */
-    int64_t V;                   /* vocabulary columns, >= 1 and < 2^31 - 1                */
+    int64_t V;                   /* vocabulary columns, >= 1 and <= 2^31 - 2^16            */
     int64_t ld;                  /* row stride in elements, >= V                           */
     int32_t K;                   /* beams of a sequence, 1 .. LMLOSS_MAX_BEAMS             */
     int32_t M;                   /* candidates wanted, 1 .. LMLOSS_MAX_BEAMS               */

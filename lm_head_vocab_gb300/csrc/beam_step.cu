@@ -4,10 +4,10 @@
 //   score(k, v) = scores[k] + z[k][v] - lse_k,   lse_k = ln sum_v e^z[k][v]
 //
 // The logits are read once.  Within a row the order of the candidates is the
-// order of the logits, whatever the row's normaliser, so one pass over a slice of
-// a row can keep both its softmax partials and its M largest logits; a
-// second, small kernel joins the slices of a row, turns logits into scores in fp64
-// and picks the M best of the sequence's rows.
+// order of the logits, whatever the row's normaliser, so one pass over a part of
+// a row can keep both its softmax partials and its M largest logits; the block that
+// finishes a sequence's last part joins the parts of its rows, turns logits into
+// scores in fp64 and picks the M best.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -20,17 +20,20 @@ namespace {
 constexpr int kMaxM = LMLOSS_MAX_BEAMS;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCap = 2048;                   // candidate keys of a slice held at once
+constexpr int kCap = 2048;                   // candidate keys of a part held at once
+constexpr int kHits = 2048;                  // vectors of a part that reach its first threshold
 constexpr int kSmall = 256;                  // few enough to be ranked by counting
 constexpr int kFinal = 768;                  // candidates of a sequence held at once
-constexpr int kDepths = 8;                   // lists a thread: rows * slices <= 8 * kThreads
+constexpr int kDepths = 8;                   // lists (parts of a sequence's rows) a thread
 constexpr int kMaxLists = kDepths * kThreads;
+static_assert(kMaxLists <= kHits, "a sequence's lists fit");
 
 struct BeamParams {
     const void* logits;
     int64_t ld;
     int B, K, M, V;
-    int slices;                  // of a row
+    int slices;                  // parts of a row
+    int tiles;                   // tiles of a part
     float alpha;
     int64_t eos;
     const float* scores;
@@ -44,9 +47,9 @@ struct BeamParams {
     float* lse_out;
     uint8_t* finished_out;
     int32_t* lengths_out;
-    uint64_t* keys;              // [rows][M][slices]: each slice's candidates, best first, 0 = none
-    float2* stats;               // [rows][slices] (m, s): the slice's sum of e^z is s e^m
-    unsigned* done;              // [B] slices finished; 0 between calls
+    uint64_t* keys;              // [rows][M][slices]: each part's candidates, best first, 0 = none
+    float2* stats;               // [rows][slices] (m, s): the part's sum of e^z is s e^m
+    unsigned* done;              // [B] parts finished; 0 between calls
 };
 
 // Order of the candidates of a row as one 64-bit number, larger is better: the
@@ -91,52 +94,47 @@ __device__ __noinline__ uint64_t mth_largest(const uint64_t* keys, int n, int M)
     return t;
 }
 
-// Groups of neighbouring threads whose maxima give the threshold: 32 of eight
-// threads for M <= 16, 64 of four for more.  At least M candidates reach the M-th
-// largest of at least 2 M (or 64) maxima, and few more do: with random order about
-// ln 2 of a candidate a group lies above the middle one.
-__device__ __forceinline__ int group_threads(int M) { return M <= 16 ? 8 : 4; }
-
-// The group maxima of `v` (0 = none) into group[], by every thread of the block.
-__device__ __forceinline__ void group_maxima(uint32_t v, int gt, uint32_t* group)
+// The threshold of a set of values spread over the block's threads: the M-th largest
+// of the maxima of groups of neighbouring threads, 0 where fewer than M groups have
+// one.  At least M values reach it, and few more do: G groups leave about
+// -G ln(1 - M / G) of them, so with 32 groups for M <= 16, 64 for M <= 32 and 128
+// above, at most 1.4 M.
+//
+// v: the thread's largest value, ordered, 0 = none.  *thr has to be 0 before the
+// barrier in here, and holds the threshold after the next one.
+__device__ __forceinline__ void rank_groups(uint32_t v, int M, uint32_t* group, uint32_t* thr)
 {
+    const int tid = threadIdx.x;
+    const int gt = M <= 16 ? 8 : (M <= 32 ? 4 : 2), groups = kThreads / gt;
     v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    v = max(v, __shfl_xor_sync(0xffffffffu, v, 2));
-    if (gt == 8) v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
-    if ((threadIdx.x & (gt - 1)) == 0) group[threadIdx.x / gt] = v;
-}
-
-// The M-th largest of the group maxima, 0 where there are fewer; one warp, after
-// a barrier.
-__device__ __forceinline__ uint32_t group_threshold(const uint32_t* group, int gt, int M)
-{
-    const int lane = threadIdx.x & 31;
-    const int groups = kThreads / gt;
-    uint32_t found = 0;
-    for (int g0 = 0; g0 < groups; g0 += 32) {
-        const uint32_t v = group[g0 + lane];
-        int above = 0;
-        for (int i = 0; i < groups; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(group + i);
-            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+    if (gt >= 4) v = max(v, __shfl_xor_sync(0xffffffffu, v, 2));
+    if (gt >= 8) v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    if ((tid & (gt - 1)) == 0) group[tid / gt] = v;
+    __syncthreads();
+    if (tid >= groups) return;
+    const uint32_t mine = group[tid];
+    int above = 0;
+#pragma unroll 4
+    for (int i = 0; i < groups; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(group + i);
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) above += (w[k] > v || (w[k] == v && i + k < g0 + lane)) ? 1 : 0;
-        }
-        if (above == M - 1) found = v;
+        for (int k = 0; k < 4; ++k) above += (w[k] > mine || (w[k] == mine && i + k < tid)) ? 1 : 0;
     }
-    return __reduce_max_sync(0xffffffffu, found);
+    if (above == M - 1) *thr = mine;
 }
 
 struct __align__(16) Shared {
-    uint64_t buf[kCap];                      // a slice's candidates; a sequence's finalists
-    uint32_t group[64];
-    float red[kWarps];
-    uint32_t thr;
-    int count;
+    uint64_t buf[kCap];                      // a part's candidates; a sequence's finalists
+    int32_t hits[kHits];                     // columns of a part's vectors; a sequence's lists
+    uint32_t group[kThreads / 2];
+    uint32_t thr, thr_end;                   // of the first tile, of all
+    float red_m[kWarps], red_s[kWarps];
+    int count, hit_count;
     int last;
     // of a sequence's rows
     double base[kMaxM], norm[kMaxM];
-    float m[kMaxM], hi[kMaxM], lo[kMaxM], base_f[kMaxM], inv_f[kMaxM];
+    float base_f[kMaxM], inv_f[kMaxM];
     uint8_t done[kMaxM];
     // the slow way of picking
     uint64_t wbest[kWarps], wplace[kWarps];
@@ -149,15 +147,18 @@ __device__ __forceinline__ bool exact_score(const BeamParams& p, const Shared& s
 {
     const double score = sm.done[k] ? sm.base[k] : sm.base[k] + static_cast<double>(z);
     if (!isfinite(score)) return false;
-    rank = ordered64(p.lengths ? score / sm.norm[k] : score);
+    rank = ordered64(p.alpha != 0.f ? score / sm.norm[k] : score);
     return true;
 }
 
-__device__ __forceinline__ uint64_t list_key(const BeamParams& p, const Shared& sm, int64_t r0, int list, int d)
+// Entry e of a sequence's candidates, [K][M][slices]; a finished row has one, any
+// non-zero key.
+__device__ __forceinline__ uint64_t entry_key(const BeamParams& p, const Shared& sm, int64_t r0, int64_t e, int& k)
 {
-    const int k = list / p.slices, s = list - k * p.slices;
-    if (sm.done[k]) return s == 0 && d == 0 ? 1 : 0;
-    return __ldcg(p.keys + ((r0 + k) * p.M + d) * p.slices + s);
+    const int per = p.M * p.slices;
+    k = static_cast<int>(e) / per;
+    if (sm.done[k]) return e == static_cast<int64_t>(k) * per ? 1 : 0;
+    return __ldcg(p.keys + r0 * per + e);
 }
 
 __device__ __forceinline__ void write_pick(const BeamParams& p, const Shared& sm, int b, int out, int k, float z, int token)
@@ -183,7 +184,7 @@ __device__ __forceinline__ void write_empty(const BeamParams& p, int b, int out)
     if (p.lengths_out) p.lengths_out[o] = p.lengths[static_cast<int64_t>(b) * p.K + k];
 }
 
-// M rounds of taking the best head of the sorted lists (one a row and slice): for
+// M rounds of taking the best head of the sorted lists (one a row and part): for
 // sequences with more equal or nearly equal candidates than kFinal.
 __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, const int b)
 {
@@ -194,6 +195,10 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
     uint64_t rank = 0, place = 0;
     int list = -1;
     bool stale = true;
+    auto head = [&](int i, int d, int& k) -> uint64_t {
+        const int row = i / p.slices;
+        return entry_key(p, sm, r0, (static_cast<int64_t>(row) * p.M + d) * p.slices + (i - row * p.slices), k);
+    };
     for (int out = 0; out < p.M; ++out) {
         if (stale) {
             rank = 0;
@@ -202,8 +207,8 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
             for (int j = 0; j < kDepths; ++j) {
                 const int i = tid + j * kThreads, d = static_cast<int>(depth >> (8 * j)) & 255;
                 if (i >= lists || d >= p.M) continue;
-                const uint64_t key = list_key(p, sm, r0, i, d);
-                const int k = i / p.slices;
+                int k;
+                const uint64_t key = head(i, d, k);
                 uint64_t cr;
                 if (key == 0 || !exact_score(p, sm, k, key_logit(key), cr)) continue;
                 const uint64_t cp = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.done[k] ? 0 : key_col(key));
@@ -245,79 +250,101 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
         } else if (won % kThreads == tid) {
             const int j = won / kThreads, d = static_cast<int>(depth >> (8 * j)) & 255;
             depth += uint64_t(1) << (8 * j);
-            const uint64_t key = list_key(p, sm, r0, won, d);
-            write_pick(p, sm, b, out, won / p.slices, key_logit(key), key_col(key));
+            int k;
+            const uint64_t key = head(won, d, k);
+            write_pick(p, sm, b, out, k, key_logit(key), key_col(key));
             stale = true;
         }
     }
 }
 
-// The block that finishes a sequence's last slice picks its M best.
+// ln(hi + lo) for a sum of at least 1, to about 1e-9, from fp32 operations alone but
+// for its last three additions (fp64 runs at a sixty-fourth of fp32's rate here).
+// hi + lo = 2^e f with f in [0.7, 1.42), ln f = 2 artanh(q) with q = (f - 1) / (f + 1):
+// q is carried as a quotient and its remainder, the series' higher terms in fp32.
+__device__ __forceinline__ double log_of_sum(float hi, float lo)
+{
+    if (!(hi < INFINITY)) return static_cast<double>(hi);   // NaN
+    int e = static_cast<int>(__float_as_uint(hi) >> 23) - 127;
+    float scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    if (hi * scale > 1.4142135f) {
+        ++e;
+        scale *= 0.5f;
+    }
+    const float f = hi * scale, g = lo * scale;
+    const float num = f - 1.f, den = f + 1.f, den_lo = (f - (den - 1.f)) + g;
+    const float q = num / den;
+    const float rest = (fmaf(-q, den, num) + fmaf(-q, den_lo, g)) / den;
+    const float q2 = q * q;
+    const float t = q2 * fmaf(q2, fmaf(q2, fmaf(q2, fmaf(q2, 1.f / 11, 1.f / 9), 1.f / 7), 0.2f), 1.f / 3);
+    return fma(static_cast<double>(e), 0.693147180559945309417, 2.0 * static_cast<double>(q)) +
+           static_cast<double>(2.f * fmaf(q, t, rest));
+}
+
+// The block that finishes a sequence's last part picks its M best.
 __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.K, M = p.M, S = p.slices;
     const int64_t r0 = static_cast<int64_t>(b) * K;
 
-    // ---- the rows' normalisers: the slices' sums are added as pairs of fp32 (an
-    // error-free sum and what it leaves), since fp64 is slow on this GPU; only the
-    // logarithm is taken in fp64, one lane a row
+    // ---- the rows' normalisers: the parts' sums are added as pairs of fp32, an
+    // error-free sum and what it leaves
     for (int k = warp; k < K; k += kWarps) {
         const int64_t r = r0 + k;
         const bool done = p.finished && p.finished[r];
-        float m = -INFINITY, hi = 0.f, lo = 0.f;
+        const float score = p.scores[r];
+        const int len0 = p.lengths ? p.lengths[r] : 0;
+        double lse = 0.0;
         if (!done) {
-            for (int s = lane; s < S; s += 32) m = fmaxf(m, __ldcg(&p.stats[r * S + s]).x);
+            float m = -INFINITY, hi = 0.f, lo = 0.f;
+            const float2 q0 = lane < S ? __ldcg(&p.stats[r * S + lane]) : make_float2(-INFINITY, 0.f);
+            m = q0.x;
+            for (int s = lane + 32; s < S; s += 32) m = fmaxf(m, __ldcg(&p.stats[r * S + s]).x);
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             auto add = [&](float x, float e) {
                 const float t = hi + x, v = t - hi;
                 lo += ((hi - (t - v)) + (x - v)) + e;
                 hi = t;
             };
-            for (int s = lane; s < S; s += 32) {
-                const float2 q = __ldcg(&p.stats[r * S + s]);
-                // an empty slice (-inf, 0) adds nothing; NaN stays
-                add(q.x == m ? q.y : q.y * exp2f((q.x - m) * kLog2e), 0.f);
-            }
+            // an empty part (-inf, 0) adds nothing; NaN stays
+            auto part = [&](float2 q) { return q.x == m ? q.y : q.y * exp2f((q.x - m) * kLog2e); };
+            add(part(q0), 0.f);
+            for (int s = lane + 32; s < S; s += 32) add(part(__ldcg(&p.stats[r * S + s])), 0.f);
             for (int o = 16; o > 0; o >>= 1) {
                 const float x = __shfl_xor_sync(0xffffffffu, hi, o), e = __shfl_xor_sync(0xffffffffu, lo, o);
                 add(x, e);
             }
+            lse = m == -INFINITY && hi == 0.f ? -INFINITY : static_cast<double>(m) + log_of_sum(hi, lo);
         }
         if (lane == 0) {
-            sm.m[k] = m;
-            sm.hi[k] = hi;
-            sm.lo[k] = lo;
+            if (p.lse_out) p.lse_out[r] = static_cast<float>(lse);
+            const double base = static_cast<double>(score) - lse;
+            double d = 1.0;
+            float inv = 1.f;
+            if (p.alpha != 0.f) {
+                const int64_t len = static_cast<int64_t>(len0) + (done ? 0 : 1);
+                d = static_cast<double>(len < 1 ? 1 : len);
+                if (p.alpha != 1.f) d = pow(d, static_cast<double>(p.alpha));
+                inv = 1.f / static_cast<float>(d);
+            }
+            sm.base[k] = base;
+            sm.norm[k] = d;
+            sm.base_f[k] = static_cast<float>(base);
+            sm.inv_f[k] = inv;
             sm.done[k] = done ? 1 : 0;
         }
     }
-    __syncthreads();
-    if (tid < K) {
-        const int64_t r = r0 + tid;
-        const bool done = sm.done[tid];
-        const double score = static_cast<double>(p.scores[r]);
-        double lse = 0.0;
-        if (!done) {
-            const double sum = static_cast<double>(sm.hi[tid]) + static_cast<double>(sm.lo[tid]);
-            lse = sm.m[tid] == -INFINITY && sum == 0.0 ? -INFINITY : static_cast<double>(sm.m[tid]) + log(sum);
-        }
-        if (p.lse_out) p.lse_out[r] = static_cast<float>(lse);
-        double d = 1.0;
-        if (p.lengths) {
-            const int64_t len = static_cast<int64_t>(p.lengths[r]) + (done ? 0 : 1);
-            d = pow(static_cast<double>(len < 1 ? 1 : len), static_cast<double>(p.alpha));
-        }
-        sm.base[tid] = score - lse;
-        sm.norm[tid] = d;
-        sm.base_f[tid] = static_cast<float>(score - lse);
-        sm.inv_f[tid] = static_cast<float>(1.0 / d);
+    if (tid == 0) {
+        sm.count = 0;
+        sm.hit_count = 0;
+        sm.thr = 0;
+        sm.thr_end = 0;
     }
-    if (tid == 0) sm.count = 0;
     __syncthreads();
 
     // ---- a threshold in fp32.  Each candidate's rank key lies within `err` of its
-    // fp32 value: four roundings of at most 2^-24 of the terms.
-    const int lists = K * S;
+    // fp32 value: at most six roundings of 2^-24 of the terms.
     auto bounds = [&](int k, uint64_t key, float& low, float& high) {
         const float z = sm.done[k] ? 0.f : key_logit(key);
         const float x = (sm.base_f[k] + z) * sm.inv_f[k];
@@ -330,51 +357,71 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
         }
         if (!isfinite(sm.base[k])) high = low = -INFINITY;   // the row is out
     };
-    const int gt = group_threads(M);
+    // heads of the lists first (one a row and part); a list whose head stays below
+    // the threshold has nothing above it
+    const int lists = K * S;
+    auto key_at = [&](int list, int d, int& k) {
+        const int row = list / S;
+        return entry_key(p, sm, r0, (static_cast<int64_t>(row) * M + d) * S + (list - row * S), k);
+    };
     {
-        // heads first, and deeper where there are few lists
-        const int depths = lists >= kThreads ? 1 : min(M, (kThreads + lists - 1) / lists);
         float best = -INFINITY;
-        for (int e = tid; e < lists * depths; e += kThreads) {
-            const int d = e / lists, i = e - d * lists;
-            const uint64_t key = list_key(p, sm, r0, i, d);
-            if (key == 0) continue;
-            float low, high;
-            bounds(i / S, key, low, high);
+        for (int i = tid; i < lists; i += kThreads) {
+            int k;
+            const uint64_t key = key_at(i, 0, k);
+            float low = -INFINITY, high;
+            if (key) bounds(k, key, low, high);
             best = fmaxf(best, low);
         }
-        group_maxima(best > -INFINITY ? ordered(best) : 0u, gt, sm.group);
-        __syncthreads();
-        if (warp == 0) {
-            const uint32_t t = group_threshold(sm.group, gt, M);
-            if (lane == 0) sm.thr = t;
-        }
+        rank_groups(best > -INFINITY ? ordered(best) : 0u, M, sm.group, &sm.thr);
         __syncthreads();
     }
-    const float thr = sm.thr ? unordered(sm.thr) : -INFINITY;
+    float thr = sm.thr ? unordered(sm.thr) : -INFINITY;
+    for (int i = tid; i < lists; i += kThreads) {
+        int k;
+        const uint64_t key = key_at(i, 0, k);
+        float low, high = -INFINITY;
+        if (key) bounds(k, key, low, high);
+        if (high >= thr && high > -INFINITY) sm.hits[atomicAdd(&sm.hit_count, 1)] = i;
+    }
+    __syncthreads();
+    const int entries = sm.hit_count * M;
+    if (entries > 2 * 32) {
+        // few lists, or many alike: a threshold from all of their entries.  (Ranking by
+        // counting costs the square of what is left: 768 candidates took 100 us.)
+        float best = -INFINITY;
+        for (int e = tid; e < entries; e += kThreads) {
+            int k;
+            const uint64_t key = key_at(sm.hits[e / M], e % M, k);
+            float low = -INFINITY, high;
+            if (key) bounds(k, key, low, high);
+            best = fmaxf(best, low);
+        }
+        rank_groups(best > -INFINITY ? ordered(best) : 0u, M, sm.group, &sm.thr_end);
+        __syncthreads();
+        if (sm.thr_end) thr = fmaxf(thr, unordered(sm.thr_end));
+    }
 
     // ---- the candidates that may reach it, ranked by counting in fp64
     uint64_t* rank_of = sm.buf;
     uint64_t* place_of = sm.buf + kFinal;
     float* z_of = reinterpret_cast<float*>(sm.buf + 2 * kFinal);
     static_assert(2 * kFinal + kFinal / 2 <= kCap, "finalists fit");
-    for (int i = tid; i < lists; i += kThreads) {
-        const int k = i / S;
-        for (int d = 0; d < M; ++d) {
-            const uint64_t key = list_key(p, sm, r0, i, d);
-            if (key == 0) break;
-            float low, high;
-            bounds(k, key, low, high);
-            // the list goes down: nothing after this one either
-            if (high < thr || high == -INFINITY) break;
+    for (int e = tid; e < entries; e += kThreads) {
+        int k;
+        const uint64_t key = key_at(sm.hits[e / M], e % M, k);
+        float low, high = -INFINITY;
+        if (key) bounds(k, key, low, high);
+        if (high >= thr && high > -INFINITY) {
             uint64_t rank;
             const float z = sm.done[k] ? 0.f : key_logit(key);
-            if (!exact_score(p, sm, k, z, rank)) continue;
-            const int to = atomicAdd(&sm.count, 1);
-            if (to < kFinal) {
-                rank_of[to] = rank;
-                place_of[to] = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.done[k] ? 0 : key_col(key));
-                z_of[to] = z;
+            if (exact_score(p, sm, k, z, rank)) {
+                const int to = atomicAdd(&sm.count, 1);
+                if (to < kFinal) {
+                    rank_of[to] = rank;
+                    place_of[to] = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.done[k] ? 0 : key_col(key));
+                    z_of[to] = z;
+                }
             }
         }
     }
@@ -394,7 +441,7 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
     for (int i = n + tid; i < M; i += kThreads) write_empty(p, b, i);
 }
 
-// ------------------------------------------------------------- one slice
+// ------------------------------------------------------------- one part
 template <class T>
 struct Logits {
     static constexpr int E = 16 / T::kBytes;
@@ -413,131 +460,212 @@ struct Logits {
     }
 };
 
-// E logits from column c on, those past V as -inf.
-template <class T, bool ALIGNED>
-__device__ __forceinline__ void load_logits(Pack<T, Logits<T>::E>& q, const typename T::raw* z, int64_t c, int V,
-                                            const unsigned char* lo, const unsigned char* hi)
+// What is read of one row.  Vectors from column lo to hi are read as they lie in
+// memory (around an unaligned one two aligned blocks, both inside the call's logits);
+// the few at the ends of a row, or of the logits, one by one.
+template <class T>
+struct RowLogits {
+    const typename T::raw* z;
+    int V, lo, hi;
+};
+
+template <class T>
+__device__ __noinline__ uint4 load_ends(const RowLogits<T>& r, int c)
 {
     constexpr int E = Logits<T>::E;
-    if (ALIGNED && c + E <= V) {
-        q.load(z + c);
-    } else if (!ALIGNED && c + E <= V && inside_blocks<T, E>(reinterpret_cast<const unsigned char*>(z + c), lo, hi)) {
-        load_shifted<T, E>(q, reinterpret_cast<const unsigned char*>(z + c));
-    } else {
-        q.zero();
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < E; ++i) q.set(i, c + i < V ? T::widen(z[c + i]) : -INFINITY);
+    for (int i = 0; i < E; ++i) {
+        const uint32_t x = c + i < r.V ? static_cast<uint32_t>(r.z[c + i]) : static_cast<uint32_t>(T::round(-INFINITY));
+        if constexpr (T::kBytes == 4) w[i] = x;
+        else w[i / 2] |= x << (16 * (i & 1));
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Slice s of row r: kThreads * VPT vectors of E columns, vector j of a thread at
-// column ((s * VPT + j) * kThreads + thread) * E.  Columns, not addresses, fix
-// which thread adds what, so equal rows give equal bits wherever they start.
+// E logits from column c on, in flight.
+template <class T, bool ALIGNED>
+struct InFlight {
+    static constexpr int E = Logits<T>::E;
+    static constexpr int kVecs = ALIGNED ? 1 : 2;
+    uint4 v[kVecs];
+
+    __device__ __forceinline__ void issue(const RowLogits<T>& r, int c)
+    {
+        if (c >= r.lo && c <= r.hi) {
+            const uint4* a = ALIGNED ? reinterpret_cast<const uint4*>(r.z + c)
+                                     : reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(r.z + c) & ~uintptr_t(15));
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i] = __ldg(a + i);
+        }
+    }
+    __device__ __forceinline__ void take(Pack<T, E>& q, const RowLogits<T>& r, int c) const
+    {
+        if (c >= r.lo && c <= r.hi) {
+            if constexpr (ALIGNED) {
+                q.w[0] = v[0].x; q.w[1] = v[0].y; q.w[2] = v[0].z; q.w[3] = v[0].w;
+            } else {
+                shift_blocks<T, E>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z + c)));
+            }
+        } else {
+            const uint4 x = load_ends(r, c);
+            q.w[0] = x.x; q.w[1] = x.y; q.w[2] = x.z; q.w[3] = x.w;
+        }
+    }
+};
+
+// A block takes `tiles` tiles of one row, one after the other, with the next tile's
+// loads in flight.  A tile is kThreads * VPT vectors of E columns, vector j of a
+// thread at column (tile * VPT + j) * kThreads * E + thread * E: columns, not
+// addresses, fix which thread adds what, so equal rows give equal bits wherever
+// they start.
 //
-// The whole slice is in registers at once, so its maximum is known before the
-// first exponential and nothing is rescaled.  Only vectors whose largest logit
-// reaches the threshold are looked at a second time.
+// Each thread keeps its own running maximum and sum.  The first tile gives a
+// threshold; after it the loop has no barrier, and of later vectors only those that
+// reach it are noted.  The threads' running maxima give the threshold of the whole
+// part, and the noted vectors are looked through once for logits that reach that.
 template <class T, int VPT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_constant__ BeamParams p)
+__global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int E = Logits<T>::E;
+    constexpr int kTileCols = VPT * kThreads * E;
     __shared__ Shared sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / p.slices, slice = blockIdx.x - row * p.slices;
+    const int row = blockIdx.x / p.slices, part = blockIdx.x - row * p.slices;
     const int b = row / p.K;
     if (!(p.finished && p.finished[row])) {
-        const typename T::raw* z = static_cast<const typename T::raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
-        const unsigned char* lo = static_cast<const unsigned char*>(p.logits);
-        const unsigned char* hi = lo + ((static_cast<int64_t>(p.B) * p.K - 1) * p.ld + p.V) * T::kBytes;
-        const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
-        // V is at most kMaxLists slices long, far below 2^31
-        const int first = slice * (VPT * kThreads * E) + tid * E;
-
-        Pack<T, E> q[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) load_logits<T, ALIGNED>(q[j], z, first + j * (kThreads * E), p.V, lo, hi);
-
-        // ---- maxima: of all logits (for the sum) and of the allowed ones (for the order)
-        float m = -INFINITY, vmax[VPT], best = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            vmax[j] = Logits<T>::largest(q[j]);
-            m = fmaxf(m, vmax[j]);
+        // columns fit in 32 bits: V is at most kMaxLists parts of few tiles
+        RowLogits<T> r;
+        r.z = static_cast<const typename T::raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
+        r.V = p.V;
+        r.lo = 0;
+        r.hi = p.V - E;
+        if (!ALIGNED) {
+            // at the first and last row: nothing before or after the logits is read
+            const int64_t after = (static_cast<int64_t>(p.B) * p.K - 1 - row) * p.ld;
+            if (row == 0) r.lo = E;
+            if (after < E) r.hi = p.V - 2 * E;
         }
-        if (mask) {
+        const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
+        const int begin = part * p.tiles * kTileCols;
+        const int end = min(begin + p.tiles * kTileCols, p.V);
+
+        if (tid == 0) {
+            sm.count = 0;
+            sm.hit_count = 0;
+            sm.thr = 0;
+            sm.thr_end = 0;
+        }
+        float m = -INFINITY, s = 0.f, best = -INFINITY, least = 0.f;
+        InFlight<T, ALIGNED> next[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) next[j].issue(r, begin + (j * kThreads + tid) * E);
+        for (int c0 = begin + tid * E; c0 - tid * E < end; c0 += kTileCols) {
+            const bool first = c0 - tid * E == begin;
+            Pack<T, E> q[VPT];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) next[j].take(q[j], r, c0 + j * (kThreads * E));
+            if (c0 - tid * E + kTileCols < end) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) next[j].issue(r, c0 + kTileCols + j * (kThreads * E));
+            }
+            // ---- maxima: of all logits (for the sum) and of the allowed ones (for the order)
+            float vmax[VPT], top = m;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int c = first + j * (kThreads * E);
-                const uint32_t allow = c < p.V ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0u;
-                float x = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (allow >> i & 1u) x = fmaxf(x, q[j].get(i));
-                vmax[j] = x;
+                vmax[j] = Logits<T>::largest(q[j]);
+                top = fmaxf(top, vmax[j]);
             }
-        }
+            if (mask) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) best = fmaxf(best, vmax[j]);
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int gt = group_threads(p.M);
-        group_maxima(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, gt, sm.group);
-        if (lane == 0) sm.red[warp] = m;
-        if (tid == 0) sm.count = 0;
-        __syncthreads();
+                for (int j = 0; j < VPT; ++j) {
+                    const int c = c0 + j * (kThreads * E);
+                    const uint32_t allow = c < p.V ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0u;
+                    vmax[j] = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.red[w]);
-        if (warp == 0) {
-            const uint32_t t = group_threshold(sm.group, gt, p.M);
-            if (lane == 0) sm.thr = t;
-        }
-
-        // ---- sum of exponentials.  The maximum is taken off before the change to
-        // base 2: z log2 e alone would overflow at the type's lowest values.
-        const float shift = m == -INFINITY ? 0.f : m;
-        const uint64_t off2 = f2_pack(-shift, -shift), l2 = f2_pack(kLog2e, kLog2e);
-        uint64_t s2 = f2_pack(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            uint64_t part = f2_pack(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                float a, c;
-                f2_unpack(f2_mul(f2_add(f2_pack(q[j].get(i), q[j].get(i + 1)), off2), l2), a, c);
-                part = f2_add(part, f2_pack(ex2(a), ex2(c)));
+                    for (int i = 0; i < E; ++i)
+                        if (allow >> i & 1u) vmax[j] = fmaxf(vmax[j], q[j].get(i));
+                }
             }
-            s2 = f2_add(s2, part);
-        }
-        float s, s1;
-        f2_unpack(s2, s, s1);
-        s += s1;
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        __syncthreads();   // thr written, red read
-        if (lane == 0) sm.red[warp] = s;
-
-        // ---- collect the candidates from the threshold up, raising it while they
-        // are more than the buffer holds (many equal logits, or the best ones side
-        // by side in one group)
-        uint64_t thr = static_cast<uint64_t>(sm.thr) << 32;
-        if (thr == 0) thr = 1;   // fewer than M groups have one: all of them
-        int n;
-        while (true) {
-            const float least = thr > 1 ? key_logit(thr) : -INFINITY;
-            uint32_t hits = 0;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) best = fmaxf(best, vmax[j]);
+            if (first) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr);
+            // ---- sum of exponentials.  The maximum is taken off before the change to
+            // base 2: z log2 e alone would overflow at the type's lowest values.
+            if (top > m) {
+                s *= ex2((m - top) * kLog2e);
+                m = top;
+            }
+            const float shift = m == -INFINITY ? 0.f : m;
+            const uint64_t off2 = f2_pack(-shift, -shift), l2 = f2_pack(kLog2e, kLog2e);
+            uint64_t s2 = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+                for (int i = 0; i < E; i += 2) {
+                    float a, c;
+                    f2_unpack(f2_mul(f2_add(f2_pack(q[j].get(i), q[j].get(i + 1)), off2), l2), a, c);
+                    s2 = f2_add(s2, f2_pack(ex2(a), ex2(c)));
+                }
+            }
+            float sa, sb;
+            f2_unpack(s2, sa, sb);
+            s += sa + sb;
+            if (first) {
+                __syncthreads();   // the threshold; without one (fewer than M groups) every logit but -inf
+                least = sm.thr ? unordered(sm.thr) : __uint_as_float(0xff7fffffu);
+            }
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
-                if (vmax[j] >= least && vmax[j] > -INFINITY) hits |= 1u << j;
-            while (hits) {
-                const int j = __ffs(hits) - 1;
-                hits &= hits - 1;
-                const int c = first + j * (kThreads * E);
+                if (vmax[j] >= least) {
+                    const int to = atomicAdd(&sm.hit_count, 1);
+                    if (to < kHits) sm.hits[to] = c0 + j * (kThreads * E);
+                }
+        }
+
+        // ---- the part's sum, and the threshold of all of it
+        float top = m;
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (m < top) s *= ex2((m - top) * kLog2e);
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) {
+            sm.red_m[warp] = top;
+            sm.red_s[warp] = s;
+        }
+        rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr_end);
+        __syncthreads();
+        if (warp == kWarps - 1) {
+            const float mw = lane < kWarps ? sm.red_m[lane] : -INFINITY;
+            float all = mw;
+            for (int o = 4; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+            float total = lane < kWarps ? (mw == all ? sm.red_s[lane] : sm.red_s[lane] * ex2((mw - all) * kLog2e)) : 0.f;
+            for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            if (lane == 0) p.stats[blockIdx.x] = make_float2(all, total);
+        }
+
+        // ---- candidates: the logits of the noted vectors that reach the threshold.
+        // With more vectors noted than are kept (the largest logits late in the part)
+        // all are looked at; with more candidates than are kept (many equal logits) the
+        // threshold rises to the M-th largest of those held.
+        uint64_t thr = sm.thr_end ? static_cast<uint64_t>(sm.thr_end) << 32 : 1;
+        int n;
+        while (true) {
+            const int noted = sm.hit_count;
+            const bool all = noted > kHits;
+            const int vecs = all ? (end - begin + E - 1) / E : noted;
+            for (int i = tid; i < vecs; i += kThreads) {
+                const int c = all ? begin + i * E : sm.hits[i];
+                InFlight<T, ALIGNED> f;
                 Pack<T, E> v;
-                load_logits<T, ALIGNED>(v, z, c, p.V, lo, hi);
+                f.issue(r, c);
+                f.take(v, r, c);
                 const uint32_t allow = mask ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0xffffffffu;
+                const float from = thr > 1 ? key_logit(thr) : __uint_as_float(0xff7fffffu);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float x = v.get(i);
-                    if (x >= least && x > -INFINITY && (allow >> i & 1u)) {
-                        const uint64_t k = key_of(x, c + i);
+                for (int x = 0; x < E; ++x) {
+                    const float z = v.get(x);
+                    if (z >= from && (allow >> x & 1u)) {
+                        const uint64_t k = key_of(z, c + x);
                         if (k >= thr) {
                             const int to = atomicAdd(&sm.count, 1);
                             if (to < kCap) sm.buf[to] = k;
@@ -553,15 +681,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
             if (tid == 0) sm.count = 0;
             __syncthreads();
         }
-        if (tid == 0) {
-            float total = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) total += sm.red[w];
-            p.stats[blockIdx.x] = make_float2(m, total);
-        }
-        uint64_t* out = p.keys + static_cast<int64_t>(row) * p.M * p.slices + slice;
+
+        // ---- the M best of them, best first: ranked by counting (exact: the keys are
+        // all different)
+        uint64_t* out = p.keys + static_cast<int64_t>(row) * p.M * p.slices + part;
         const uint64_t cut = n > kSmall ? mth_largest(sm.buf, n, p.M) : 0;
-        // rank by counting: exact, and the keys are all different
         for (int i = tid; i < n; i += kThreads) {
             const uint64_t k = sm.buf[i];
             if (k < cut) continue;
@@ -575,12 +699,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
     // ---- the sequence's last block goes on to pick
     __syncthreads();
     if (tid == 0) {
-        __threadfence();
         const unsigned all = static_cast<unsigned>(p.K) * static_cast<unsigned>(p.slices);
-        const bool last = atomicAdd(&p.done[b], 1u) == all - 1;
-        if (last) p.done[b] = 0;
-        sm.last = last;
-        __threadfence();
+        sm.last = count_done(&p.done[b]) == all - 1;
+        if (sm.last) p.done[b] = 0;
     }
     __syncthreads();
     if (sm.last) pick(p, sm, b);
@@ -595,7 +716,8 @@ lmloss_status check_beam(const lmloss_beam_args* a, bool pointers)
     if (!float_dtype(a->dtype)) return LMLOSS_ERR_INVALID_ARG;
     if (!(a->length_penalty >= 0.f) || !std::isfinite(a->length_penalty)) return LMLOSS_ERR_INVALID_ARG;
     if (a->eos_token < -1 || a->eos_token >= a->V || a->mask_stride < 0) return LMLOSS_ERR_INVALID_ARG;
-    if (a->V >= (int64_t(1) << 31) - 1 || a->B > (int64_t(1) << 24)) return LMLOSS_ERR_UNSUPPORTED;
+    // a block's columns run a little past V in 32 bits
+    if (a->V > (int64_t(1) << 31) - (1 << 16) || a->B > (int64_t(1) << 24)) return LMLOSS_ERR_UNSUPPORTED;
     if (a->B > 0 && a->ld > INT64_MAX / 16 / (a->B * a->K)) return LMLOSS_ERR_INVALID_ARG;
     if (!pointers) return LMLOSS_OK;
     if (a->length_penalty > 0.f && !a->lengths) return LMLOSS_ERR_INVALID_ARG;
@@ -610,33 +732,28 @@ lmloss_status check_beam(const lmloss_beam_args* a, bool pointers)
     return LMLOSS_OK;
 }
 
-constexpr int kMaxVpt = 8;
-
 struct BeamPlan {
-    int vpt, slices;
+    int vpt, tiles, slices;
     size_t keys, stats, total;
 };
 
-// The slice length: 8 vectors a thread, or fewer while that leaves the GPU's
-// SMs without two blocks each.
+// Tiles of four vectors a thread, several to a block while that leaves about four
+// blocks for each place on the GPU's SMs (four blocks a SM): the threshold and the
+// candidates' ranking are paid once a block.  Where tiles of four give fewer than
+// two blocks a SM, tiles of one, four blocks a SM.
 lmloss_status plan_beam(const lmloss_beam_args* a, int num_sms, BeamPlan& P)
 {
     const int64_t rows = a->B * a->K, E = 16 / float_bytes(a->dtype);
-    int vpt = kMaxVpt;
-    int64_t slices = 0;
-    for (;; vpt /= 2) {
-        const int64_t len = static_cast<int64_t>(vpt) * kThreads * E;
-        slices = (a->V + len - 1) / len;
-        if (vpt == 1 || rows * slices >= 2 * num_sms) break;
-    }
-    while (slices * a->K > kMaxLists && vpt < kMaxVpt) {
-        vpt *= 2;
-        const int64_t len = static_cast<int64_t>(vpt) * kThreads * E;
-        slices = (a->V + len - 1) / len;
-    }
-    if (slices * a->K > kMaxLists) return LMLOSS_ERR_UNSUPPORTED;
-    if (rows * slices >= (int64_t(1) << 31)) return LMLOSS_ERR_UNSUPPORTED;
-    P.vpt = vpt;
+    auto tiles_of = [&](int vpt) { return (a->V + vpt * kThreads * E - 1) / (vpt * kThreads * E); };
+    P.vpt = rows * tiles_of(4) >= 2 * num_sms ? 4 : 1;
+    const int64_t all = tiles_of(P.vpt);
+    int64_t tiles = std::max<int64_t>(1, rows * all / ((P.vpt == 4 ? 16 : 4) * static_cast<int64_t>(num_sms)));
+    // at most kMaxLists parts in a sequence's rows
+    const int64_t most = kMaxLists / a->K;
+    tiles = std::max(tiles, (all + most - 1) / most);
+    const int64_t slices = (all + tiles - 1) / tiles;
+    if (tiles > (1 << 30) || rows * slices >= (int64_t(1) << 31)) return LMLOSS_ERR_UNSUPPORTED;
+    P.tiles = static_cast<int>(tiles);
     P.slices = static_cast<int>(slices);
     P.keys = 0;
     P.stats = vocab_align(sizeof(uint64_t) * static_cast<size_t>(rows * slices * a->M));
@@ -645,7 +762,7 @@ lmloss_status plan_beam(const lmloss_beam_args* a, int num_sms, BeamPlan& P)
 }
 
 template <class T, int VPT>
-lmloss_status launch_slices(const BeamParams& p, bool aligned, cudaStream_t stream)
+lmloss_status launch_parts(const BeamParams& p, bool aligned, cudaStream_t stream)
 {
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.K * p.slices);
     if (aligned) beam_step_kernel<T, VPT, true><<<grid, kThreads, 0, stream>>>(p);
@@ -654,14 +771,9 @@ lmloss_status launch_slices(const BeamParams& p, bool aligned, cudaStream_t stre
 }
 
 template <class T>
-lmloss_status launch_slices(const BeamParams& p, int vpt, bool aligned, cudaStream_t stream)
+lmloss_status launch_parts(const BeamParams& p, int vpt, bool aligned, cudaStream_t stream)
 {
-    switch (vpt) {
-    case 1: return launch_slices<T, 1>(p, aligned, stream);
-    case 2: return launch_slices<T, 2>(p, aligned, stream);
-    case 4: return launch_slices<T, 4>(p, aligned, stream);
-    default: return launch_slices<T, 8>(p, aligned, stream);
-    }
+    return vpt == 4 ? launch_parts<T, 4>(p, aligned, stream) : launch_parts<T, 1>(p, aligned, stream);
 }
 
 }  // namespace
@@ -708,6 +820,7 @@ lmloss_status lmloss_beam_step(lmloss_vocab_handle h, const lmloss_beam_args* a,
         p.M = a->M;
         p.V = static_cast<int>(a->V);
         p.slices = P.slices;
+        p.tiles = P.tiles;
         p.alpha = a->length_penalty;
         p.eos = a->eos_token;
         p.scores = a->scores + r0;
@@ -725,9 +838,9 @@ lmloss_status lmloss_beam_step(lmloss_vocab_handle h, const lmloss_beam_args* a,
         p.stats = reinterpret_cast<float2*>(h->ws + P.stats);
         p.done = h->counters;
         switch (a->dtype) {
-        case LMLOSS_BF16: st = launch_slices<Bf16>(p, P.vpt, aligned, stream); break;
-        case LMLOSS_FP16: st = launch_slices<Fp16>(p, P.vpt, aligned, stream); break;
-        default: st = launch_slices<Fp32>(p, P.vpt, aligned, stream); break;
+        case LMLOSS_BF16: st = launch_parts<Bf16>(p, P.vpt, aligned, stream); break;
+        case LMLOSS_FP16: st = launch_parts<Fp16>(p, P.vpt, aligned, stream); break;
+        default: st = launch_parts<Fp32>(p, P.vpt, aligned, stream); break;
         }
         if (st != LMLOSS_OK) return st;
     }

@@ -150,35 +150,42 @@ __device__ __forceinline__ bool inside_blocks(const unsigned char* p, const unsi
     const unsigned char* a = reinterpret_cast<const unsigned char*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
     return a >= lo && a + N * T::kBytes + 16 <= hi;
 }
-template <class T, int N>
-__device__ __forceinline__ void load_shifted(Pack<T, N>& q, const unsigned char* p)
+// The N elements that begin `addr` % 16 bytes into the blocks v.
+template <class T, int N, int VECS>
+__device__ __forceinline__ void shift_blocks(Pack<T, N>& q, const uint4 (&v)[VECS], uint32_t addr)
 {
-    constexpr int kVecs = N * T::kBytes / 16 + 1;
-    const uintptr_t ad = reinterpret_cast<uintptr_t>(p);
-    const uint4* a = reinterpret_cast<const uint4*>(ad & ~uintptr_t(15));
-    uint32_t w[4 * kVecs];
+    static_assert(VECS == N * T::kBytes / 16 + 1, "one block more than the elements fill");
+    uint32_t w[4 * VECS];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const uint4 v = __ldg(a + i);
-        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    for (int i = 0; i < VECS; ++i) {
+        w[4 * i] = v[i].x; w[4 * i + 1] = v[i].y; w[4 * i + 2] = v[i].z; w[4 * i + 3] = v[i].w;
     }
-    const uint32_t b = static_cast<uint32_t>(ad);
-    if (b & 8u) {
+    if (addr & 8u) {
 #pragma unroll
-        for (int i = 0; i + 2 < 4 * kVecs; ++i) w[i] = w[i + 2];
+        for (int i = 0; i + 2 < 4 * VECS; ++i) w[i] = w[i + 2];
     }
-    if (b & 4u) {
+    if (addr & 4u) {
 #pragma unroll
-        for (int i = 0; i + 1 < 4 * kVecs; ++i) w[i] = w[i + 1];
+        for (int i = 0; i + 1 < 4 * VECS; ++i) w[i] = w[i + 1];
     }
     if constexpr (T::kBytes == 2) {
-        const uint32_t sh = (b & 2u) * 8u;   // 0 or 16 bits
+        const uint32_t sh = (addr & 2u) * 8u;   // 0 or 16 bits
 #pragma unroll
         for (int i = 0; i < Pack<T, N>::kWords; ++i) q.w[i] = __funnelshift_r(w[i], w[i + 1], sh);
     } else {
 #pragma unroll
         for (int i = 0; i < Pack<T, N>::kWords; ++i) q.w[i] = w[i];
     }
+}
+
+// Counts this block's arrival; what the block wrote before a barrier that this
+// thread has passed is visible to whoever sees the count, and what others wrote
+// before theirs to this one.
+__device__ __forceinline__ unsigned count_done(unsigned* counter)
+{
+    unsigned old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+    return old;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -144,6 +144,8 @@ def test_workspace_grows_with_its_arguments(lib):
 
 
 def test_rows_too_long_for_a_step_are_refused(lib):
+    longest = (1 << 31) - (1 << 16)
+    assert L.lmloss_beam_workspace(_beam(K=64, V=longest, ld=longest)) > 0
     with pytest.raises(L.LMLossError) as e:
-        L.lmloss_beam_workspace(_beam(K=64, V=1 << 30, ld=1 << 30))
+        L.lmloss_beam_workspace(_beam(K=64, V=longest + 1, ld=longest + 1))
     assert e.value.status == UNS
