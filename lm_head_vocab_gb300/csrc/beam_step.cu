@@ -20,13 +20,13 @@ namespace {
 constexpr int kMaxM = LMLOSS_MAX_BEAMS;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCap = 2048;                   // candidate keys of a part held at once
-constexpr int kHits = 2048;                  // vectors of a part that reach its first threshold
+constexpr int kCap = 1024;                   // candidate keys of a part held at once
+constexpr int kHits = 1024;                  // vectors of a part that reach its first threshold
 constexpr int kSmall = 256;                  // few enough to be ranked by counting
-constexpr int kFinal = 768;                  // candidates of a sequence held at once
+constexpr int kFinal = 512;                  // candidates of a sequence held at once
+constexpr int kEntries = 8;                  // entries a thread holds when a sequence has few
 constexpr int kDepths = 8;                   // lists (parts of a sequence's rows) a thread
 constexpr int kMaxLists = kDepths * kThreads;
-static_assert(kMaxLists <= kHits, "a sequence's lists fit");
 
 struct BeamParams {
     const void* logits;
@@ -94,6 +94,11 @@ __device__ __noinline__ uint64_t mth_largest(const uint64_t* keys, int n, int M)
     return t;
 }
 
+__device__ __forceinline__ float warp_max(float x)
+{
+    return unordered(__reduce_max_sync(0xffffffffu, ordered(x)));
+}
+
 // The threshold of a set of values spread over the block's threads: the M-th largest
 // of the maxima of groups of neighbouring threads, 0 where fewer than M groups have
 // one.  At least M values reach it, and few more do: G groups leave about
@@ -125,8 +130,18 @@ __device__ __forceinline__ void rank_groups(uint32_t v, int M, uint32_t* group, 
 }
 
 struct __align__(16) Shared {
-    uint64_t buf[kCap];                      // a part's candidates; a sequence's finalists
-    int32_t hits[kHits];                     // columns of a part's vectors; a sequence's lists
+    uint64_t buf[kCap];                      // a part's candidates
+    union {
+        struct {
+            uint4 data[kHits];               // a part's noted vectors
+            int32_t col[kHits];
+        } hit;
+        struct {
+            uint64_t rank[kFinal], place[kFinal];   // a sequence's finalists
+            float z[kFinal];
+            uint16_t lists[kMaxLists];       // its lists that reach the first threshold
+        } pick;
+    };
     uint32_t group[kThreads / 2];
     uint32_t thr, thr_end;                   // of the first tile, of all
     float red_m[kWarps], red_s[kWarps];
@@ -287,21 +302,30 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.K, M = p.M, S = p.slices;
     const int64_t r0 = static_cast<int64_t>(b) * K;
+    const int per = M * S, total = K * per;
+
+    // with few entries all of them are read at once, under the way of the rows' sums
+    const bool few = total <= kEntries * kThreads;
+    uint64_t held[kEntries];
+#pragma unroll
+    for (int j = 0; j < kEntries; ++j) {
+        const int e = tid + j * kThreads;
+        held[j] = few && e < total ? __ldcg(p.keys + r0 * per + e) : 0;
+    }
 
     // ---- the rows' normalisers: the parts' sums are added as pairs of fp32, an
     // error-free sum and what it leaves
     for (int k = warp; k < K; k += kWarps) {
         const int64_t r = r0 + k;
+        const float2 q0 = lane < S ? __ldcg(&p.stats[r * S + lane]) : make_float2(-INFINITY, 0.f);
         const bool done = p.finished && p.finished[r];
         const float score = p.scores[r];
         const int len0 = p.lengths ? p.lengths[r] : 0;
         double lse = 0.0;
         if (!done) {
-            float m = -INFINITY, hi = 0.f, lo = 0.f;
-            const float2 q0 = lane < S ? __ldcg(&p.stats[r * S + lane]) : make_float2(-INFINITY, 0.f);
-            m = q0.x;
+            float m = q0.x, hi = 0.f, lo = 0.f;
             for (int s = lane + 32; s < S; s += 32) m = fmaxf(m, __ldcg(&p.stats[r * S + s]).x);
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = warp_max(m);
             auto add = [&](float x, float e) {
                 const float t = hi + x, v = t - hi;
                 lo += ((hi - (t - v)) + (x - v)) + e;
@@ -357,59 +381,7 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
         }
         if (!isfinite(sm.base[k])) high = low = -INFINITY;   // the row is out
     };
-    // heads of the lists first (one a row and part); a list whose head stays below
-    // the threshold has nothing above it
-    const int lists = K * S;
-    auto key_at = [&](int list, int d, int& k) {
-        const int row = list / S;
-        return entry_key(p, sm, r0, (static_cast<int64_t>(row) * M + d) * S + (list - row * S), k);
-    };
-    {
-        float best = -INFINITY;
-        for (int i = tid; i < lists; i += kThreads) {
-            int k;
-            const uint64_t key = key_at(i, 0, k);
-            float low = -INFINITY, high;
-            if (key) bounds(k, key, low, high);
-            best = fmaxf(best, low);
-        }
-        rank_groups(best > -INFINITY ? ordered(best) : 0u, M, sm.group, &sm.thr);
-        __syncthreads();
-    }
-    float thr = sm.thr ? unordered(sm.thr) : -INFINITY;
-    for (int i = tid; i < lists; i += kThreads) {
-        int k;
-        const uint64_t key = key_at(i, 0, k);
-        float low, high = -INFINITY;
-        if (key) bounds(k, key, low, high);
-        if (high >= thr && high > -INFINITY) sm.hits[atomicAdd(&sm.hit_count, 1)] = i;
-    }
-    __syncthreads();
-    const int entries = sm.hit_count * M;
-    if (entries > 2 * 32) {
-        // few lists, or many alike: a threshold from all of their entries.  (Ranking by
-        // counting costs the square of what is left: 768 candidates took 100 us.)
-        float best = -INFINITY;
-        for (int e = tid; e < entries; e += kThreads) {
-            int k;
-            const uint64_t key = key_at(sm.hits[e / M], e % M, k);
-            float low = -INFINITY, high;
-            if (key) bounds(k, key, low, high);
-            best = fmaxf(best, low);
-        }
-        rank_groups(best > -INFINITY ? ordered(best) : 0u, M, sm.group, &sm.thr_end);
-        __syncthreads();
-        if (sm.thr_end) thr = fmaxf(thr, unordered(sm.thr_end));
-    }
-
-    // ---- the candidates that may reach it, ranked by counting in fp64
-    uint64_t* rank_of = sm.buf;
-    uint64_t* place_of = sm.buf + kFinal;
-    float* z_of = reinterpret_cast<float*>(sm.buf + 2 * kFinal);
-    static_assert(2 * kFinal + kFinal / 2 <= kCap, "finalists fit");
-    for (int e = tid; e < entries; e += kThreads) {
-        int k;
-        const uint64_t key = key_at(sm.hits[e / M], e % M, k);
+    auto offer = [&](int k, uint64_t key, float thr) {
         float low, high = -INFINITY;
         if (key) bounds(k, key, low, high);
         if (high >= thr && high > -INFINITY) {
@@ -418,13 +390,80 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
             if (exact_score(p, sm, k, z, rank)) {
                 const int to = atomicAdd(&sm.count, 1);
                 if (to < kFinal) {
-                    rank_of[to] = rank;
-                    place_of[to] = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.done[k] ? 0 : key_col(key));
-                    z_of[to] = z;
+                    sm.pick.rank[to] = rank;
+                    sm.pick.place[to] = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.done[k] ? 0 : key_col(key));
+                    sm.pick.z[to] = z;
                 }
             }
         }
+    };
+    auto lower = [&](int k, uint64_t key) {
+        float low = -INFINITY, high;
+        if (key) bounds(k, key, low, high);
+        return low;
+    };
+    auto threshold = [&](float best, uint32_t* to) {
+        rank_groups(best > -INFINITY ? ordered(best) : 0u, M, sm.group, to);
+        __syncthreads();
+        return *to ? unordered(*to) : -INFINITY;
+    };
+    if (few) {
+        const uint32_t magic = static_cast<uint32_t>(((uint64_t(1) << 32) + per - 1) / per);   // e < 2^11
+        float best = -INFINITY;
+        int k[kEntries];
+#pragma unroll
+        for (int j = 0; j < kEntries; ++j) {
+            const int e = tid + j * kThreads;
+            k[j] = min(per == 1 ? e : static_cast<int>(__umulhi(static_cast<uint32_t>(e), magic)), K - 1);
+            if (sm.done[k[j]]) held[j] = e == k[j] * per ? 1 : 0;
+            best = fmaxf(best, lower(k[j], held[j]));
+        }
+        const float thr = threshold(best, &sm.thr);
+#pragma unroll
+        for (int j = 0; j < kEntries; ++j) offer(k[j], held[j], thr);
+    } else {
+        // heads of the lists first (one a row and part); a list whose head stays below
+        // the threshold has nothing above it
+        const int lists = K * S;
+        auto key_at = [&](int list, int d, int& k) {
+            const int row = list / S;
+            return entry_key(p, sm, r0, (static_cast<int64_t>(row) * M + d) * S + (list - row * S), k);
+        };
+        float best = -INFINITY;
+        for (int i = tid; i < lists; i += kThreads) {
+            int k;
+            const uint64_t key = key_at(i, 0, k);
+            best = fmaxf(best, lower(k, key));
+        }
+        float thr = threshold(best, &sm.thr);
+        for (int i = tid; i < lists; i += kThreads) {
+            int k;
+            const uint64_t key = key_at(i, 0, k);
+            float low, high = -INFINITY;
+            if (key) bounds(k, key, low, high);
+            if (high >= thr && high > -INFINITY) sm.pick.lists[atomicAdd(&sm.hit_count, 1)] = static_cast<uint16_t>(i);
+        }
+        __syncthreads();
+        const int entries = sm.hit_count * M;
+        if (entries > 2 * 32) {
+            // few lists, or many alike: a threshold from all of their entries.  (Ranking by
+            // counting costs the square of what is left: 768 candidates took 100 us.)
+            best = -INFINITY;
+            for (int e = tid; e < entries; e += kThreads) {
+                int k;
+                const uint64_t key = key_at(sm.pick.lists[e / M], e % M, k);
+                best = fmaxf(best, lower(k, key));
+            }
+            thr = fmaxf(thr, threshold(best, &sm.thr_end));
+        }
+        for (int e = tid; e < entries; e += kThreads) {
+            int k;
+            const uint64_t key = key_at(sm.pick.lists[e / M], e % M, k);
+            offer(k, key, thr);
+        }
     }
+
+    // ---- what is left, ranked by counting in fp64
     __syncthreads();
     const int n = sm.count;
     if (n > kFinal) {
@@ -432,11 +471,15 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
         return;
     }
     for (int i = tid; i < n; i += kThreads) {
-        const uint64_t rank = rank_of[i], place = place_of[i];
+        const uint64_t rank = sm.pick.rank[i], place = sm.pick.place[i];
         int above = 0;
-        for (int o = 0; o < n; ++o) above += (rank_of[o] > rank || (rank_of[o] == rank && place_of[o] < place)) ? 1 : 0;
+#pragma unroll 8
+        for (int o = 0; o < n; ++o) {
+            const uint64_t x = sm.pick.rank[o], y = sm.pick.place[o];
+            above += static_cast<int>(x > rank) | (static_cast<int>(x == rank) & static_cast<int>(y < place));
+        }
         if (above < M)
-            write_pick(p, sm, b, above, static_cast<int>(place >> 32), z_of[i], static_cast<int>(place & 0xffffffffu));
+            write_pick(p, sm, b, above, static_cast<int>(place >> 32), sm.pick.z[i], static_cast<int>(place & 0xffffffffu));
     }
     for (int i = n + tid; i < M; i += kThreads) write_empty(p, b, i);
 }
@@ -520,10 +563,11 @@ struct InFlight {
 // addresses, fix which thread adds what, so equal rows give equal bits wherever
 // they start.
 //
-// Each thread keeps its own running maximum and sum.  The first tile gives a
-// threshold; after it the loop has no barrier, and of later vectors only those that
-// reach it are noted.  The threads' running maxima give the threshold of the whole
-// part, and the noted vectors are looked through once for logits that reach that.
+// Each thread keeps its own running maximum and sum.  The threads' running maxima
+// give a threshold after the first tile, and a higher one after the second, fourth
+// and so on; vectors that reach it are noted, the other tiles pass without a barrier.
+// At the end the noted vectors are looked through once for logits that reach the
+// threshold of the whole part.
 template <class T, int VPT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(const __grid_constant__ BeamParams p)
 {
@@ -560,8 +604,9 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
         InFlight<T, ALIGNED> next[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) next[j].issue(r, begin + (j * kThreads + tid) * E);
-        for (int c0 = begin + tid * E; c0 - tid * E < end; c0 += kTileCols) {
-            const bool first = c0 - tid * E == begin;
+        for (int tile = 0, c0 = begin + tid * E; c0 - tid * E < end; ++tile, c0 += kTileCols) {
+            // tiles 0, 1, 3, 7, ... raise the threshold
+            const bool raise = (tile & (tile + 1)) == 0;
             Pack<T, E> q[VPT];
 #pragma unroll
             for (int j = 0; j < VPT; ++j) next[j].take(q[j], r, c0 + j * (kThreads * E));
@@ -589,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) best = fmaxf(best, vmax[j]);
-            if (first) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr);
+            if (raise) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr);
             // ---- sum of exponentials.  The maximum is taken off before the change to
             // base 2: z log2 e alone would overflow at the type's lowest values.
             if (top > m) {
@@ -611,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
             float sa, sb;
             f2_unpack(s2, sa, sb);
             s += sa + sb;
-            if (first) {
+            if (raise) {
                 __syncthreads();   // the threshold; without one (fewer than M groups) every logit but -inf
                 least = sm.thr ? unordered(sm.thr) : __uint_as_float(0xff7fffffu);
             }
@@ -619,13 +664,15 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
             for (int j = 0; j < VPT; ++j)
                 if (vmax[j] >= least) {
                     const int to = atomicAdd(&sm.hit_count, 1);
-                    if (to < kHits) sm.hits[to] = c0 + j * (kThreads * E);
+                    if (to < kHits) {
+                        sm.hit.data[to] = make_uint4(q[j].w[0], q[j].w[1], q[j].w[2], q[j].w[3]);
+                        sm.hit.col[to] = c0 + j * (kThreads * E);
+                    }
                 }
         }
 
         // ---- the part's sum, and the threshold of all of it
-        float top = m;
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float top = warp_max(m);
         if (m < top) s *= ex2((m - top) * kLog2e);
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) {
@@ -654,11 +701,16 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
             const bool all = noted > kHits;
             const int vecs = all ? (end - begin + E - 1) / E : noted;
             for (int i = tid; i < vecs; i += kThreads) {
-                const int c = all ? begin + i * E : sm.hits[i];
-                InFlight<T, ALIGNED> f;
+                const int c = all ? begin + i * E : sm.hit.col[i];
                 Pack<T, E> v;
-                f.issue(r, c);
-                f.take(v, r, c);
+                if (all) {
+                    InFlight<T, ALIGNED> f;
+                    f.issue(r, c);
+                    f.take(v, r, c);
+                } else {
+                    const uint4 x = sm.hit.data[i];
+                    v.w[0] = x.x; v.w[1] = x.y; v.w[2] = x.z; v.w[3] = x.w;
+                }
                 const uint32_t allow = mask ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0xffffffffu;
                 const float from = thr > 1 ? key_logit(thr) : __uint_as_float(0xff7fffffu);
 #pragma unroll
@@ -690,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
             const uint64_t k = sm.buf[i];
             if (k < cut) continue;
             int above = 0;
+#pragma unroll 8
             for (int o = 0; o < n; ++o) above += sm.buf[o] > k ? 1 : 0;
             if (above < p.M) out[static_cast<int64_t>(above) * p.slices] = k;
         }
@@ -747,7 +800,7 @@ lmloss_status plan_beam(const lmloss_beam_args* a, int num_sms, BeamPlan& P)
     auto tiles_of = [&](int vpt) { return (a->V + vpt * kThreads * E - 1) / (vpt * kThreads * E); };
     P.vpt = rows * tiles_of(4) >= 2 * num_sms ? 4 : 1;
     const int64_t all = tiles_of(P.vpt);
-    int64_t tiles = std::max<int64_t>(1, rows * all / ((P.vpt == 4 ? 16 : 4) * static_cast<int64_t>(num_sms)));
+    int64_t tiles = std::max<int64_t>(1, rows * all / ((P.vpt == 4 ? 8 : 4) * static_cast<int64_t>(num_sms)));
     // at most kMaxLists parts in a sequence's rows
     const int64_t most = kMaxLists / a->K;
     tiles = std::max(tiles, (all + most - 1) / most);
