@@ -105,12 +105,12 @@ __device__ __forceinline__ float warp_max(float x)
 // -G ln(1 - M / G) of them, so with 32 groups for M <= 16, 64 for M <= 32 and 128
 // above, at most 1.4 M.
 //
-// v: the thread's largest value, ordered, 0 = none.  *thr has to be 0 before the
-// barrier in here, and holds the threshold after the next one.
+// v: the thread's largest value, ordered, 0 = none.  *thr has to be 0, or an earlier
+// threshold, before the barrier in here, and holds the threshold after the next one.
 __device__ __forceinline__ void rank_groups(uint32_t v, int M, uint32_t* group, uint32_t* thr)
 {
     const int tid = threadIdx.x;
-    const int gt = M <= 16 ? 8 : (M <= 32 ? 4 : 2), groups = kThreads / gt;
+    const int groups = M <= 16 ? 32 : (M <= 32 ? 64 : 128), gt = kThreads / groups;
     v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
     if (gt >= 4) v = max(v, __shfl_xor_sync(0xffffffffu, v, 2));
     if (gt >= 8) v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
@@ -126,7 +126,7 @@ __device__ __forceinline__ void rank_groups(uint32_t v, int M, uint32_t* group, 
 #pragma unroll
         for (int k = 0; k < 4; ++k) above += (w[k] > mine || (w[k] == mine && i + k < tid)) ? 1 : 0;
     }
-    if (above == M - 1) *thr = mine;
+    if (above == M - 1 && mine) *thr = mine;
 }
 
 struct __align__(16) Shared {
@@ -526,36 +526,43 @@ __device__ __noinline__ uint4 load_ends(const RowLogits<T>& r, int c)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// E logits from column c on, in flight.
+// E logits from column c on, in flight; c between lo and hi.
 template <class T, bool ALIGNED>
 struct InFlight {
     static constexpr int E = Logits<T>::E;
     static constexpr int kVecs = ALIGNED ? 1 : 2;
     uint4 v[kVecs];
 
-    __device__ __forceinline__ void issue(const RowLogits<T>& r, int c)
+    __device__ __forceinline__ void load(const RowLogits<T>& r, int c)
     {
-        if (c >= r.lo && c <= r.hi) {
-            const uint4* a = ALIGNED ? reinterpret_cast<const uint4*>(r.z + c)
-                                     : reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(r.z + c) & ~uintptr_t(15));
+        const uint4* a = ALIGNED ? reinterpret_cast<const uint4*>(r.z + c)
+                                 : reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(r.z + c) & ~uintptr_t(15));
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) v[i] = __ldg(a + i);
-        }
+        for (int i = 0; i < kVecs; ++i) v[i] = __ldg(a + i);
     }
-    __device__ __forceinline__ void take(Pack<T, E>& q, const RowLogits<T>& r, int c) const
+    __device__ __forceinline__ void unpack(Pack<T, E>& q, const RowLogits<T>& r, int c) const
     {
-        if (c >= r.lo && c <= r.hi) {
-            if constexpr (ALIGNED) {
-                q.w[0] = v[0].x; q.w[1] = v[0].y; q.w[2] = v[0].z; q.w[3] = v[0].w;
-            } else {
-                shift_blocks<T, E>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z + c)));
-            }
+        if constexpr (ALIGNED) {
+            q.w[0] = v[0].x; q.w[1] = v[0].y; q.w[2] = v[0].z; q.w[3] = v[0].w;
         } else {
-            const uint4 x = load_ends(r, c);
-            q.w[0] = x.x; q.w[1] = x.y; q.w[2] = x.z; q.w[3] = x.w;
+            shift_blocks<T, E>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z + c)));
         }
     }
 };
+
+// E logits from any column on, those past V as -inf.
+template <class T, bool ALIGNED>
+__device__ __forceinline__ void load_logits(Pack<T, Logits<T>::E>& q, const RowLogits<T>& r, int c)
+{
+    if (c >= r.lo && c <= r.hi) {
+        InFlight<T, ALIGNED> f;
+        f.load(r, c);
+        f.unpack(q, r, c);
+    } else {
+        const uint4 x = load_ends(r, c);
+        q.w[0] = x.x; q.w[1] = x.y; q.w[2] = x.z; q.w[3] = x.w;
+    }
+}
 
 // A block takes `tiles` tiles of one row, one after the other, with the next tile's
 // loads in flight.  A tile is kThreads * VPT vectors of E columns, vector j of a
@@ -565,7 +572,9 @@ struct InFlight {
 //
 // Each thread keeps its own running maximum and sum.  The threads' running maxima
 // give a threshold after the first tile, and a higher one after the second, fourth
-// and so on; vectors that reach it are noted, the other tiles pass without a barrier.
+// and so on; vectors that reach it are noted, and the other tiles pass without a
+// barrier.  (A warp raising it on its own, from whatever maxima it saw, took as long
+// at M = 16 and half as long again at M = 64.)
 // At the end the noted vectors are looked through once for logits that reach the
 // threshold of the whole part.
 template <class T, int VPT, bool ALIGNED>
@@ -601,27 +610,18 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
             sm.thr_end = 0;
         }
         float m = -INFINITY, s = 0.f, best = -INFINITY, least = 0.f;
-        InFlight<T, ALIGNED> next[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) next[j].issue(r, begin + (j * kThreads + tid) * E);
-        for (int tile = 0, c0 = begin + tid * E; c0 - tid * E < end; ++tile, c0 += kTileCols) {
-            // tiles 0, 1, 3, 7, ... raise the threshold
-            const bool raise = (tile & (tile + 1)) == 0;
-            Pack<T, E> q[VPT];
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) next[j].take(q[j], r, c0 + j * (kThreads * E));
-            if (c0 - tid * E + kTileCols < end) {
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) next[j].issue(r, c0 + kTileCols + j * (kThreads * E));
-            }
+        int tile = 0;
+        auto use_tile = [&](const Pack<T, E> (&q)[VPT], int c0) {
             // ---- maxima: of all logits (for the sum) and of the allowed ones (for the order)
-            float vmax[VPT], top = m;
+            float vmax[VPT], tmax;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                vmax[j] = Logits<T>::largest(q[j]);
-                top = fmaxf(top, vmax[j]);
-            }
+            for (int j = 0; j < VPT; ++j) vmax[j] = Logits<T>::largest(q[j]);
+            tmax = vmax[0];
+#pragma unroll
+            for (int j = 1; j < VPT; ++j) tmax = fmaxf(tmax, vmax[j]);
+            const float top = fmaxf(m, tmax);
             if (mask) {
+                tmax = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
                     const int c = c0 + j * (kThreads * E);
@@ -630,11 +630,15 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
 #pragma unroll
                     for (int i = 0; i < E; ++i)
                         if (allow >> i & 1u) vmax[j] = fmaxf(vmax[j], q[j].get(i));
+                    tmax = fmaxf(tmax, vmax[j]);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) best = fmaxf(best, vmax[j]);
-            if (raise) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr);
+            best = fmaxf(best, tmax);
+            const uint32_t now = best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u;
+            // tiles 0, 1, 3, 7, ... raise the threshold
+            const bool raise = (tile & (tile + 1)) == 0;
+            ++tile;
+            if (raise) rank_groups(now, p.M, sm.group, &sm.thr);
             // ---- sum of exponentials.  The maximum is taken off before the change to
             // base 2: z log2 e alone would overflow at the type's lowest values.
             if (top > m) {
@@ -660,15 +664,41 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
                 __syncthreads();   // the threshold; without one (fewer than M groups) every logit but -inf
                 least = sm.thr ? unordered(sm.thr) : __uint_as_float(0xff7fffffu);
             }
+            if (tmax >= least) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if (vmax[j] >= least) {
-                    const int to = atomicAdd(&sm.hit_count, 1);
-                    if (to < kHits) {
-                        sm.hit.data[to] = make_uint4(q[j].w[0], q[j].w[1], q[j].w[2], q[j].w[3]);
-                        sm.hit.col[to] = c0 + j * (kThreads * E);
+                for (int j = 0; j < VPT; ++j)
+                    if (vmax[j] >= least) {
+                        const int to = atomicAdd(&sm.hit_count, 1);
+                        if (to < kHits) {
+                            sm.hit.data[to] = make_uint4(q[j].w[0], q[j].w[1], q[j].w[2], q[j].w[3]);
+                            sm.hit.col[to] = c0 + j * (kThreads * E);
+                        }
                     }
-                }
+            }
+        };
+        // whole tiles, the next one in flight; then what is left
+        int t0 = begin;
+        if (t0 >= r.lo) {
+            InFlight<T, ALIGNED> next[VPT];
+            auto issue = [&](int c) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) next[j].load(r, c + (j * kThreads + tid) * E);
+            };
+            const int last = min(end, r.hi + E) - kTileCols;   // the last whole tile begins here or before
+            if (t0 <= last) issue(t0);
+            for (; t0 <= last; t0 += kTileCols) {
+                Pack<T, E> q[VPT];
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) next[j].unpack(q[j], r, t0 + (j * kThreads + tid) * E);
+                if (t0 + kTileCols <= last) issue(t0 + kTileCols);
+                use_tile(q, t0 + tid * E);
+            }
+        }
+        for (; t0 < end; t0 += kTileCols) {
+            Pack<T, E> q[VPT];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) load_logits<T, ALIGNED>(q[j], r, t0 + (j * kThreads + tid) * E);
+            use_tile(q, t0 + tid * E);
         }
 
         // ---- the part's sum, and the threshold of all of it
@@ -704,9 +734,7 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
                 const int c = all ? begin + i * E : sm.hit.col[i];
                 Pack<T, E> v;
                 if (all) {
-                    InFlight<T, ALIGNED> f;
-                    f.issue(r, c);
-                    f.take(v, r, c);
+                    load_logits<T, ALIGNED>(v, r, c);
                 } else {
                     const uint4 x = sm.hit.data[i];
                     v.w[0] = x.x; v.w[1] = x.y; v.w[2] = x.z; v.w[3] = x.w;
@@ -790,20 +818,28 @@ struct BeamPlan {
     size_t keys, stats, total;
 };
 
-// Tiles of four vectors a thread, several to a block while that leaves about four
-// blocks for each place on the GPU's SMs (four blocks a SM): the threshold and the
-// candidates' ranking are paid once a block.  Where tiles of four give fewer than
-// two blocks a SM, tiles of one, four blocks a SM.
+// Tiles of four vectors a thread, or of one where those would not give every SM a
+// block.  The parts of a row: a block costs its tiles and about eight more (the
+// thresholds' barriers, the ranking, the count; tiles of one are a quarter as long),
+// and an SM's blocks run together up to about three, one after another beyond.
+// Measured at 512 rows of 262144 bf16: one part 58 us, two 69, six 72.
 lmloss_status plan_beam(const lmloss_beam_args* a, int num_sms, BeamPlan& P)
 {
     const int64_t rows = a->B * a->K, E = 16 / float_bytes(a->dtype);
     auto tiles_of = [&](int vpt) { return (a->V + vpt * kThreads * E - 1) / (vpt * kThreads * E); };
-    P.vpt = rows * tiles_of(4) >= 2 * num_sms ? 4 : 1;
-    const int64_t all = tiles_of(P.vpt);
-    int64_t tiles = std::max<int64_t>(1, rows * all / ((P.vpt == 4 ? 8 : 4) * static_cast<int64_t>(num_sms)));
+    P.vpt = rows * tiles_of(4) >= num_sms ? 4 : 1;
+    const int64_t all = tiles_of(P.vpt), fixed = P.vpt == 4 ? 8 : 32;
     // at most kMaxLists parts in a sequence's rows
-    const int64_t most = kMaxLists / a->K;
-    tiles = std::max(tiles, (all + most - 1) / most);
+    const int64_t most = kMaxLists / a->K, least = (all + most - 1) / most;
+    int64_t tiles = all, best = INT64_MAX;
+    for (int64_t t = least; t <= all && t <= least + 63; ++t) {
+        const int64_t blocks = rows * ((all + t - 1) / t);
+        const int64_t cost = std::max<int64_t>((blocks + num_sms - 1) / num_sms, 3) * (t + fixed);
+        if (cost < best) {
+            best = cost;
+            tiles = t;
+        }
+    }
     const int64_t slices = (all + tiles - 1) / tiles;
     if (tiles > (1 << 30) || rows * slices >= (int64_t(1) << 31)) return LMLOSS_ERR_UNSUPPORTED;
     P.tiles = static_cast<int>(tiles);
@@ -843,9 +879,12 @@ lmloss_status lmloss_beam_workspace(const lmloss_beam_args* a, size_t* bytes)
     if (!bytes) return LMLOSS_ERR_INVALID_ARG;
     lmloss_status st = check_beam(a, false);
     if (st != LMLOSS_OK) return st;
-    // the shortest slices that any GPU's plan takes: enough for every plan
     BeamPlan P{};
-    if ((st = plan_beam(a, 1 << 20, P)) != LMLOSS_OK) return st;
+    if ((st = plan_beam(a, 1, P)) != LMLOSS_OK) return st;
+    // enough for any plan: tiles of one, as many parts as a sequence's rows may have
+    const int64_t rows = a->B * a->K, cols = kThreads * (16 / float_bytes(a->dtype));
+    const size_t parts = static_cast<size_t>(std::min<int64_t>((a->V + cols - 1) / cols, kMaxLists / a->K));
+    P.total = vocab_align(sizeof(uint64_t) * rows * parts * a->M) + vocab_align(sizeof(float2) * rows * parts);
     *bytes = P.total;
     return LMLOSS_OK;
 }
