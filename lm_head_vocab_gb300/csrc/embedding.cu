@@ -8,8 +8,9 @@
 // rows that occur).  The gradient's sums run over the positions sorted by token,
 // so each table row is written once, by one block, in an order that the ids alone
 // fix: no float atomics.
+#include <algorithm>
 #include <cmath>
-#include <new>
+#include <type_traits>
 
 #include "vocab_common.cuh"
 
@@ -31,6 +32,8 @@ struct EmbParams {
     float scale;
     int accumulate;
     int* err;
+    // all memory that may be read as `rows` and as `table`
+    const unsigned char *rows_end, *table_end;
 };
 
 __device__ __forceinline__ int64_t load_id(const EmbParams& p, int64_t t)
@@ -49,50 +52,108 @@ __device__ __forceinline__ unsigned char* at(void* base, int64_t row, int64_t ld
     return static_cast<unsigned char*>(base) + (row * ld + c) * T::kBytes;
 }
 
-// Columns [c, c + N) of a row, those past D as zeros / not stored.
-// RW: memory that this kernel also writes.
-template <class T, int N, bool RW = false>
-__device__ __forceinline__ void load_cols(Pack<T, N>& q, const void* base, int64_t row, int64_t ld, int64_t c, int64_t D)
+
+// ------------------------------------------------------- unaligned rows
+// A thread works on N columns that start on a 16-byte boundary of the row it WRITES;
+// where rows do not (odd widths), the first vector of a row begins before its first
+// column, and what it reads is put together from aligned blocks.  Vectors at a row's
+// ends go element by element, out of line.
+template <class T>
+constexpr int kGranule = 16 / T::kBytes;
+
+template <class T>
+__device__ __noinline__ uint4 gather_ends(const unsigned char* row, int64_t c, int64_t D)
 {
-    if (c + N <= D) {
-        if constexpr (RW) q.load_rw(at<T>(base, row, ld, c));
-        else q.load(at<T>(base, row, ld, c));
-    } else {
-        q.zero();
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (c + i < D) {
-                Pack<T, 1> e;
-                e.load_rw(at<T>(base, row, ld, c + i));
-                q.set(i, e.get(0));
-            }
+    for (int i = 0; i < kGranule<T>; ++i)
+        if (c + i >= 0 && c + i < D) {
+            const uint32_t x = reinterpret_cast<const typename T::raw*>(row)[c + i];
+            if constexpr (T::kBytes == 4) w[i] = x;
+            else w[i / 2] |= x << (16 * (i & 1));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <class T>
+__device__ __noinline__ void scatter_ends(unsigned char* row, int64_t c, int64_t D, uint4 v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < kGranule<T>; ++i)
+        if (c + i >= 0 && c + i < D) {
+            if constexpr (T::kBytes == 4) reinterpret_cast<uint32_t*>(row)[c + i] = w[i];
+            else reinterpret_cast<uint16_t*>(row)[c + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        }
+}
+
+template <class T, int N>
+__device__ __forceinline__ void load_ends(Pack<T, N>& q, const unsigned char* row, int64_t c, int64_t D)
+{
+#pragma unroll
+    for (int g = 0; g < N / kGranule<T>; ++g) {
+        const uint4 x = gather_ends<T>(row, c + g * kGranule<T>, D);
+        q.w[4 * g] = x.x; q.w[4 * g + 1] = x.y; q.w[4 * g + 2] = x.z; q.w[4 * g + 3] = x.w;
     }
 }
-template <class T, int N>
-__device__ __forceinline__ void store_cols(const Pack<T, N>& q, void* base, int64_t row, int64_t ld, int64_t c, int64_t D)
+
+// Columns [c, c + N) of a row of an input, whatever its alignment; zeros outside [0, D).
+// lo, hi: the memory that may be read.
+template <class T, int N, bool ALIGNED>
+__device__ __forceinline__ void load_row(Pack<T, N>& q, const unsigned char* row, int64_t c, int64_t D,
+                                         const unsigned char* lo, const unsigned char* hi)
 {
-    if (c + N <= D) {
-        q.store(at<T>(base, row, ld, c));
+    const unsigned char* p = row + c * T::kBytes;
+    if (c >= 0 && c + N <= D && (ALIGNED || inside_blocks<T, N>(p, lo, hi))) {
+        if constexpr (ALIGNED) {
+            q.load(p);
+        } else {
+            constexpr int kVecs = N * T::kBytes / 16 + 1;
+            const uint4* a = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+            uint4 v[kVecs];
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i] = __ldg(a + i);
+            shift_blocks<T, N>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)));
+        }
+    } else {
+        load_ends(q, row, c, D);
+    }
+}
+// The same columns of a row that is being written: row + c is on a 16-byte boundary.
+template <class T, int N>
+__device__ __forceinline__ void load_own(Pack<T, N>& q, const unsigned char* row, int64_t c, int64_t D)
+{
+    if (c >= 0 && c + N <= D) q.load_rw(row + c * T::kBytes);
+    else load_ends(q, row, c, D);
+}
+template <class T, int N>
+__device__ __forceinline__ void store_row(const Pack<T, N>& q, unsigned char* row, int64_t c, int64_t D)
+{
+    if (c >= 0 && c + N <= D) {
+        q.store(row + c * T::kBytes);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (c + i < D) {
-                Pack<T, 1> e;
-                e.zero();
-                e.set(0, q.get(i));
-                e.store(at<T>(base, row, ld, c + i));
-            }
+        for (int g = 0; g < N / kGranule<T>; ++g)
+            scatter_ends<T>(row, c + g * kGranule<T>, D,
+                            make_uint4(q.w[4 * g], q.w[4 * g + 1], q.w[4 * g + 2], q.w[4 * g + 3]));
     }
+}
+// elements from the 16-byte boundary at or before the row to its first column
+template <class T, bool ALIGNED>
+__device__ __forceinline__ int row_offset(const unsigned char* row)
+{
+    return ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / T::kBytes;
 }
 
 // ------------------------------------------------------------------ lookup
 // `tpr` threads a row (a power of two), each with four vectors in flight.
+constexpr int kVec = 8;                      // columns of a vector
 constexpr int kFwdThreads = 128;
 constexpr int kFwdUnroll = 4;
 
-template <class TW, class TO, int N>
+template <class TW, class TO, bool ALIGNED>
 __global__ void __launch_bounds__(kFwdThreads) embedding_forward_kernel(const EmbParams p, const int tpr)
 {
+    constexpr int N = kVec;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kFwdThreads / tpr) + threadIdx.x / tpr;
     if (t >= p.T) return;
     const int lane = threadIdx.x & (tpr - 1);
@@ -100,29 +161,162 @@ __global__ void __launch_bounds__(kFwdThreads) embedding_forward_kernel(const Em
     const bool valid = id >= 0 && id < p.V;
     if (!valid && id != kIgnore && lane == 0) set_error(p.err, kErrBadTarget);
     const int64_t step = static_cast<int64_t>(tpr) * N;
+    unsigned char* out = at<TO>(p.rows, t, p.ld_rows, 0);
+    const int64_t begin = lane * N - row_offset<TO, ALIGNED>(out);
     if (!valid) {
         const float fill = id == kIgnore ? 0.f : __int_as_float(0x7fc00000);
         Pack<TO, N> o;
         o.zero();
 #pragma unroll
         for (int i = 0; i < N; ++i) o.set(i, fill);
-        for (int64_t c = lane * N; c < p.D; c += step) store_cols<TO, N>(o, p.rows, t, p.ld_rows, c, p.D);
+        for (int64_t c = begin; c < p.D; c += step) store_row<TO, N>(o, out, c, p.D);
         return;
     }
-    for (int64_t c0 = lane * N; c0 < p.D; c0 += step * kFwdUnroll) {
-        Pack<TW, N> w[kFwdUnroll];
+    const unsigned char* w = at<TW>(const_cast<const void*>(p.table), id, p.ld_table, 0);
+    const unsigned char* lo = static_cast<const unsigned char*>(p.table);
+    for (int64_t c0 = begin; c0 < p.D; c0 += step * kFwdUnroll) {
+        Pack<TW, N> x[kFwdUnroll];
 #pragma unroll
         for (int u = 0; u < kFwdUnroll; ++u)
-            if (c0 + u * step < p.D) load_cols<TW, N>(w[u], p.table, id, p.ld_table, c0 + u * step, p.D);
+            if (c0 + u * step < p.D) load_row<TW, N, ALIGNED>(x[u], w, c0 + u * step, p.D, lo, p.table_end);
 #pragma unroll
         for (int u = 0; u < kFwdUnroll; ++u)
             if (c0 + u * step < p.D) {
                 Pack<TO, N> o;
                 o.zero();
 #pragma unroll
-                for (int i = 0; i < N; ++i) o.set(i, w[u].get(i) * p.scale);
-                store_cols<TO, N>(o, p.rows, t, p.ld_rows, c0 + u * step, p.D);
+                for (int i = 0; i < N; ++i) o.set(i, x[u].get(i) * p.scale);
+                store_row<TO, N>(o, out, c0 + u * step, p.D);
             }
+    }
+}
+
+// One table row's columns [c, c + N) from their sum.
+template <class TO>
+__device__ __forceinline__ void write_sum(const EmbParams& p, unsigned char* row, int64_t c, const float (&acc)[kVec])
+{
+    Pack<TO, kVec> o;
+    o.zero();
+    if (p.accumulate) {
+        Pack<TO, kVec> old;
+        load_own<TO, kVec>(old, row, c, p.D);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) o.set(i, fmaf(acc[i], p.scale, old.get(i)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) o.set(i, acc[i] * p.scale);
+    }
+    store_row<TO, kVec>(o, row, c, p.D);
+}
+
+// ------------------------------------------- gradient of a few positions
+// One launch and no workspace: a block owns `span` table rows and a range of columns,
+// looks through all ids for its own, orders them by row (a counting sort with stable
+// ranks, so positions stay in order) and writes every row once, zeros included.  Reading
+// all ids in every block is what this costs; it ends where that outweighs the sort
+// (kFewPositions).
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewSpan = 64;                 // table rows of a block, at most
+constexpr int kFewPositions = 2048;
+constexpr int kRowsAhead = 8;
+
+template <class TG, class TO, bool ALIGNED>
+__global__ void __launch_bounds__(kFewThreads) few_positions_kernel(const EmbParams p, const int span, const int tpr)
+{
+    __shared__ uint16_t bin[kFewWarps][kFewSpan];
+    __shared__ uint16_t start[kFewSpan + 1];
+    __shared__ uint16_t list[kFewPositions];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * span;
+    for (int i = tid; i < kFewWarps * kFewSpan; i += kFewThreads) (&bin[0][0])[i] = 0;
+    __syncthreads();
+    // a warp's positions are consecutive, so ranks count up in position order
+    constexpr int kRounds = kFewPositions / kFewThreads;
+    const int per = ((p.T + kFewThreads - 1) / kFewThreads) * 32;   // positions of a warp
+    int64_t id[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int t = warp * per + i * 32 + lane;
+        id[i] = i * 32 < per && t < p.T ? load_id(p, t) : kIgnore;
+    }
+    uint32_t rank[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const bool valid = id[i] >= 0 && id[i] < p.V;
+        if (!valid && id[i] != kIgnore) set_error(p.err, kErrBadTarget);
+        const int64_t d = id[i] - v0;
+        const bool mine = valid && d >= 0 && d < span;
+        id[i] = mine ? d : -1;
+        if (!__any_sync(0xffffffffu, mine)) continue;
+        const uint32_t same = __match_any_sync(0xffffffffu, mine ? static_cast<int>(d) : -1);
+        if (mine) rank[i] = bin[warp][d] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (mine && lane == __ffs(same) - 1) bin[warp][d] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // rows' totals, then their places in the list
+        int total[kFewSpan / 32], sum = 0;
+#pragma unroll
+        for (int j = 0; j < kFewSpan / 32; ++j) {
+            total[j] = 0;
+            for (int w = 0; w < kFewWarps; ++w) total[j] += bin[w][lane * (kFewSpan / 32) + j];
+            sum += total[j];
+        }
+        int inc = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        int at0 = inc - sum;
+#pragma unroll
+        for (int j = 0; j < kFewSpan / 32; ++j) {
+            const int r = lane * (kFewSpan / 32) + j;
+            start[r] = static_cast<uint16_t>(at0);
+            int run = at0;
+            for (int w = 0; w < kFewWarps; ++w) {
+                const int n = bin[w][r];
+                bin[w][r] = static_cast<uint16_t>(run);
+                run += n;
+            }
+            at0 += total[j];
+        }
+        if (lane == 31) start[kFewSpan] = static_cast<uint16_t>(at0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+        if (id[i] >= 0) list[bin[warp][id[i]] + rank[i]] = static_cast<uint16_t>(warp * per + i * 32 + lane);
+    __syncthreads();
+
+    // `tpr` threads a row, a vector each
+    const unsigned char* lo = static_cast<const unsigned char*>(p.rows);
+    const int64_t vec = static_cast<int64_t>(blockIdx.y) * tpr + (tid & (tpr - 1));
+    const int rows = static_cast<int>(min(static_cast<int64_t>(span), p.V - v0));
+    for (int r = tid / tpr; r < rows; r += kFewThreads / tpr) {
+        const int n0 = start[r], n1 = start[r + 1];
+        if (n0 == n1 && p.accumulate) continue;
+        unsigned char* row = at<TO>(p.table, v0 + r, p.ld_table, 0);
+        const int64_t c = vec * kVec - row_offset<TO, ALIGNED>(row);
+        if (c >= p.D) continue;
+        float acc[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+        for (int i = n0; i < n1; i += kRowsAhead) {
+            Pack<TG, kVec> g[kRowsAhead];
+#pragma unroll
+            for (int a = 0; a < kRowsAhead; ++a)
+                if (i + a < n1) load_row<TG, kVec, ALIGNED>(g[a], at<TG>(const_cast<const void*>(p.rows), list[i + a], p.ld_rows, 0), c, p.D, lo, p.rows_end);
+#pragma unroll
+            for (int a = 0; a < kRowsAhead; ++a)
+                if (i + a < n1) {
+#pragma unroll
+                    for (int k = 0; k < kVec; ++k) acc[k] += g[a].get(k);
+                }
+        }
+        write_sum<TO>(p, row, c, acc);
     }
 }
 
@@ -240,15 +434,210 @@ sort_place_kernel(const EmbParams p, const uint32_t* keys, const uint32_t* pos, 
     }
 }
 
+// The same by one thread-block cluster, for as many positions as its shared
+// memory holds: each block keeps an equal share, and a pass moves keys between the
+// blocks' shared memories.  (The passes above are nine launches of a few microseconds
+// each, whose latency is most of a gradient's time at 10^4 positions.)  The launch's
+// other clusters write zeros into the first `blind` table rows meanwhile.
+constexpr int kClusterBits = 9;
+constexpr int kClusterDigits = 1 << kClusterBits;
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterMax = 16;              // blocks
+constexpr int kClusterRounds = 8;            // keys a thread
+constexpr int kClusterPositions = kClusterMax * kClusterRounds * kClusterThreads;
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// zeros in columns [0, D) of rows [r0, r1), by threads `me` of `all`
+template <class TO, bool ALIGNED>
+__device__ void zero_rows(const EmbParams& p, int64_t r0, int64_t r1, int64_t me, int64_t all)
+{
+    Pack<TO, kVec> z;
+    z.zero();
+    if (!ALIGNED && p.ld_table == p.D) {
+        // one run of memory
+        unsigned char* base = at<TO>(p.table, r0, p.ld_table, 0);
+        const int64_t n = (r1 - r0) * p.D, off = row_offset<TO, ALIGNED>(base);
+        for (int64_t c = me * kVec - off; c < n; c += all * kVec) store_row<TO, kVec>(z, base, c, n);
+        return;
+    }
+    const int64_t per = (p.D + (ALIGNED ? 0 : kGranule<TO> - 1) + kVec - 1) / kVec, n = per * (r1 - r0);
+    for (int64_t i = me; i < n; i += all) {
+        const int64_t r = i / per;
+        unsigned char* row = at<TO>(p.table, r0 + r, p.ld_table, 0);
+        const int64_t c = (i - r * per) * kVec - row_offset<TO, ALIGNED>(row);
+        if (c < p.D) store_row<TO, kVec>(z, row, c, p.D);
+    }
+}
+
+struct ClusterSort {
+    int blocks, share;           // of the cluster; keys of a block
+    int fill;                    // blocks that write zeros
+    int bits, passes;            // of a digit
+    int64_t blind;
+    uint32_t *keys, *pos;        // [T] out
+};
+
+// dynamic shared memory: [2][share] (key, position), [warps][digits] 16-bit counts,
+// [digits] totals, [digits] bases
+__host__ __device__ constexpr size_t cluster_smem(int share)
+{
+    return sizeof(uint2) * 2 * static_cast<size_t>(share) + sizeof(uint16_t) * kClusterWarps * kClusterDigits +
+           2 * sizeof(uint32_t) * kClusterDigits;
+}
+
+template <class TO, bool ALIGNED>
+__global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const EmbParams p, const ClusterSort q)
+{
+    extern __shared__ __align__(16) unsigned char mem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x >= static_cast<unsigned>(q.blocks)) {
+        const int64_t me = static_cast<int64_t>(blockIdx.x - q.blocks) * kClusterThreads + tid;
+        zero_rows<TO, ALIGNED>(p, 0, q.blind, me, static_cast<int64_t>(gridDim.x - q.blocks) * kClusterThreads);
+        return;
+    }
+    uint2* buf = reinterpret_cast<uint2*>(mem);
+    uint16_t* bin = reinterpret_cast<uint16_t*>(buf + 2 * q.share);
+    uint32_t* total = reinterpret_cast<uint32_t*>(bin + kClusterWarps * kClusterDigits);
+    uint32_t* base = total + kClusterDigits;
+    __shared__ uint32_t part[32], valid;
+    const int me = static_cast<int>(cluster_rank());
+    const uint32_t magic = static_cast<uint32_t>(((uint64_t(1) << 32) + q.share - 1) / q.share);
+    int held = max(0, min(q.share, p.T - me * q.share));
+    // a warp's keys are consecutive, so ranks count up in position order
+    const int per = (q.share + kClusterWarps - 1) / kClusterWarps;
+    const int i0 = warp * per;
+
+    for (int pass = 0; pass < q.passes; ++pass) {
+        const int shift = pass * q.bits, digits = 1 << q.bits;
+        const uint2* in = buf + (pass & 1) * q.share;
+        uint4* z = reinterpret_cast<uint4*>(bin);
+        for (int i = tid; i < kClusterWarps * kClusterDigits / 8; i += kClusterThreads) z[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        uint2 kp[kClusterRounds];
+        uint32_t rank[kClusterRounds];
+#pragma unroll
+        for (int r = 0; r < kClusterRounds; ++r) {
+            const int i = i0 + r * 32 + lane;
+            const bool have = r * 32 + lane < per && i < held;
+            if (have) {
+                if (pass == 0) {
+                    const int64_t t = static_cast<int64_t>(me) * q.share + i;
+                    const uint32_t k = first_key(p, t);
+                    kp[r] = make_uint2(k, k < static_cast<uint32_t>(p.V) ? static_cast<uint32_t>(t) : 0xffffffffu);
+                } else {
+                    kp[r] = in[i];
+                }
+            } else {
+                kp[r] = make_uint2(0, 0xffffffffu);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kClusterRounds; ++r) {
+            if (r * 32 >= per) break;
+            const bool have = kp[r].y != 0xffffffffu;
+            const uint32_t d = have ? (kp[r].x >> shift) & (digits - 1) : kClusterDigits;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            uint16_t* c = bin + warp * kClusterDigits + d;
+            uint32_t before = 0;
+            if (have) before = *c;
+            __syncwarp();
+            if (have && lane == __ffs(same) - 1) *c = static_cast<uint16_t>(before + __popc(same));
+            __syncwarp();
+            rank[r] = before + __popc(same & ((1u << lane) - 1u));
+        }
+        __syncthreads();
+        // digit `tid`: the warps' offsets, and the block's total
+        if (tid < digits) {
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const uint32_t n = bin[w * kClusterDigits + tid];
+                bin[w * kClusterDigits + tid] = static_cast<uint16_t>(run);
+                run += n;
+            }
+            total[tid] = run;
+        }
+        cluster_sync_all();
+        // where the digit begins: after all smaller digits, and after the same digit of
+        // the blocks before this one
+        uint32_t all = 0, mine = 0;
+        if (tid < digits) {
+            const uint32_t own = smem_addr(total + tid);
+            for (int b = 0; b < q.blocks; ++b) {
+                const uint32_t n = ld_cluster(dsmem_map(own, b));
+                all += n;
+                mine += b < me ? n : 0;
+            }
+        }
+        uint32_t inc = all;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) part[warp] = inc;
+        __syncthreads();
+        if (warp == 0) {
+            const uint32_t own = part[lane];
+            uint32_t w = own;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, w, o);
+                if (lane >= o) w += v;
+            }
+            part[lane] = w - own;
+            if (lane == 31) valid = w;
+        }
+        __syncthreads();
+        if (tid < digits) base[tid] = part[warp] + inc - all + mine;
+        __syncthreads();
+        const bool last = pass + 1 == q.passes;
+        const uint32_t out = smem_addr(buf + ((pass + 1) & 1) * q.share);
+#pragma unroll
+        for (int r = 0; r < kClusterRounds; ++r) {
+            if (kp[r].y == 0xffffffffu) continue;
+            const uint32_t d = (kp[r].x >> shift) & (digits - 1);
+            const uint32_t to = base[d] + bin[warp * kClusterDigits + d] + rank[r];
+            if (last) {
+                q.keys[to] = kp[r].x;
+                q.pos[to] = kp[r].y;
+            } else {
+                const uint32_t b = q.share == 1 ? to : __umulhi(to, magic);
+                st_cluster(dsmem_map(out + static_cast<uint32_t>(sizeof(uint2)) * (to - b * q.share), b), kp[r].x, kp[r].y);
+            }
+        }
+        // positions without a valid token were left out; they are the list's end
+        held = max(0, min(q.share, static_cast<int>(valid) - me * q.share));
+        if (last)
+            for (int i = static_cast<int>(valid) + me * kClusterThreads + tid; i < p.T; i += q.blocks * kClusterThreads)
+                q.keys[i] = static_cast<uint32_t>(p.V);
+        // the next pass's keys are in place, and no block's totals are read any more
+        cluster_sync_all();
+    }
+}
+
 // ------------------------------------------------------- sums by token
-// A block takes a window of kWindow sorted positions and a range of columns.  A
-// token whose positions all lie in the window is summed and written.  One that
-// crosses a window's border leaves the window's part of its sum, in fp32: in slot 1
-// where it begins in this window, in slot 0 where it came from the window before;
-// the join adds a token's parts in window order.
+// A group of `tpr` threads takes a window of kWindow sorted positions and a vector of
+// columns each.  A token whose positions all lie in the window is summed and written.
+// One that crosses a window's border leaves the window's part of its sum, in fp32: in
+// slot 1 where it begins in this window, in slot 0 where it came from the window
+// before; the join adds a token's parts in an order that the windows fix.
+//
+// The blocks after these write zeros where no position holds the token: a block
+// finds its rows' range in the sorted keys and passes over those that occur.
 constexpr int kWindow = 32;
 constexpr int kSumThreads = 128;
-constexpr int kRowsAhead = 8;
+constexpr int kZeroSpan = 32;                // table rows of a block that writes zeros
+constexpr int kMaxGroups = 16;               // of a block: tpr >= 8
 
 struct SumParams {
     EmbParams e;
@@ -257,148 +646,196 @@ struct SumParams {
     float* parts;           // [windows][2][ld_parts]
     int64_t ld_parts;
     int windows;
+    int tpr;
+    int sum_blocks;
+    int64_t blind;          // rows already zero
+    uint32_t* crossing;     // [windows] windows in which a crossing token begins
+    unsigned* counters;     // [2] how many; blocks of the join finished
 };
 
-// acc: NP packs of N columns, pack j at column c + j * kSumThreads * N
-template <class TO, int N, int NP>
-__device__ __forceinline__ void write_sum(const EmbParams& e, uint32_t v, int64_t c, const float (&acc)[NP * N])
+// the first sorted position whose key is at least v, by a block of kSumThreads
+__device__ __forceinline__ int lower_bound(const uint32_t* keys, int n, uint32_t v)
 {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int64_t cj = c + static_cast<int64_t>(j) * kSumThreads * N;
-        if (cj >= e.D) break;
-        Pack<TO, N> o;
-        o.zero();
-        if (e.accumulate) {
-            Pack<TO, N> old;
-            load_cols<TO, N, true>(old, e.table, v, e.ld_table, cj, e.D);
-#pragma unroll
-            for (int i = 0; i < N; ++i) o.set(i, fmaf(acc[j * N + i], e.scale, old.get(i)));
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) o.set(i, acc[j * N + i] * e.scale);
-        }
-        store_cols<TO, N>(o, e.table, v, e.ld_table, cj, e.D);
+    int lo = 0, hi = n;                                       // in [lo, hi]
+    while (hi - lo > 0) {
+        // each thread one probe; the probes below v come first
+        const int step = (hi - lo + kSumThreads) / (kSumThreads + 1);
+        const int64_t at = lo + static_cast<int64_t>(threadIdx.x + 1) * step - 1;
+        const int below = __syncthreads_count(at < hi && keys[at] < v);
+        lo += below * step;
+        if (below < kSumThreads) hi = min(hi, lo + step - 1);   // the next probe is at least v
     }
+    return lo;
 }
 
-template <class TG, class TO, int N, int NP>
+template <class TG, class TO, bool ALIGNED>
 __global__ void __launch_bounds__(kSumThreads) token_sum_kernel(const SumParams p)
 {
-    __shared__ uint32_t key[kWindow], row[kWindow];
-    __shared__ uint32_t before, after;
+    __shared__ uint32_t key[kMaxGroups][kWindow + 2], row[kMaxGroups][kWindow];
     const EmbParams& e = p.e;
     const uint32_t none = static_cast<uint32_t>(e.V);
     const int tid = threadIdx.x;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kWindow;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kWindow), e.T - i0));
-    if (tid < n) {
-        key[tid] = p.keys[i0 + tid];
-        row[tid] = p.pos[i0 + tid];
+    if (blockIdx.x >= static_cast<unsigned>(p.sum_blocks)) {
+        if (blockIdx.y) return;
+        const int64_t v0 = p.blind + static_cast<int64_t>(blockIdx.x - p.sum_blocks) * kZeroSpan;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroSpan), e.V - v0));
+        uint8_t* held = reinterpret_cast<uint8_t*>(row);
+        if (tid < kZeroSpan) held[tid] = 0;
+        int i = lower_bound(p.keys, e.T, static_cast<uint32_t>(v0)) + tid;
+        __syncthreads();
+        for (; i < e.T; i += kSumThreads) {
+            const uint32_t k = p.keys[i];
+            if (k >= v0 + rows) break;
+            held[k - v0] = 1;
+        }
+        __syncthreads();
+        const int64_t per = (e.D + (ALIGNED ? 0 : kGranule<TO> - 1) + kVec - 1) / kVec;
+        Pack<TO, kVec> z;
+        z.zero();
+        for (int r = 0; r < rows; ++r) {
+            if (held[r]) continue;
+            unsigned char* out = at<TO>(e.table, v0 + r, e.ld_table, 0);
+            const int off = row_offset<TO, ALIGNED>(out);
+            for (int64_t x = tid; x < per; x += kSumThreads)
+                if (x * kVec - off < e.D) store_row<TO, kVec>(z, out, x * kVec - off, e.D);
+        }
+        return;
     }
-    if (tid == 32) before = i0 > 0 ? p.keys[i0 - 1] : none;
-    if (tid == 33) after = i0 + n < e.T ? p.keys[i0 + n] : none;
+    const int groups = kSumThreads / p.tpr, g = tid / p.tpr, lane = tid & (p.tpr - 1);
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * groups + g;
+    const int64_t i0 = w * kWindow;
+    const int n = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(kWindow), e.T - i0)));
+    // key[.][0] and key[.][n + 1]: the keys before and after the window
+    for (int i = lane; i < kWindow + 2; i += p.tpr) {
+        const int64_t at = i0 - 1 + i;
+        key[g][i] = at >= 0 && at < e.T ? p.keys[at] : none;
+        if (i < kWindow && i0 + i < e.T) row[g][i] = p.pos[i0 + i];
+    }
     __syncthreads();
-    const int64_t c = (static_cast<int64_t>(blockIdx.y) * kSumThreads * NP + tid) * N;
-    if (c >= e.D) return;
+    const int64_t vec = static_cast<int64_t>(blockIdx.y) * p.tpr + lane;
+    if (n == 0) return;
+    const uint32_t* k = key[g] + 1;
+    const unsigned char* lo = static_cast<const unsigned char*>(e.rows);
+    // the vector's first column in table row v
+    auto column = [&](uint32_t v) {
+        return vec * kVec - (ALIGNED ? 0 : row_offset<TO, ALIGNED>(at<TO>(e.table, v, e.ld_table, 0)));
+    };
 
-    float acc[NP * N];
+    float acc[kVec];
 #pragma unroll
-    for (int i = 0; i < NP * N; ++i) acc[i] = 0.f;
+    for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
     int first = 0;   // where the current token's run begins in the window
     for (int b = 0; b < n; b += kRowsAhead) {
-        if (key[b] == none) break;
-        Pack<TG, N> g[kRowsAhead][NP];
+        if (k[b] == none) break;
+        Pack<TG, kVec> x[kRowsAhead];
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r)
-            if (b + r < n && key[b + r] != none) {
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const int64_t cj = c + static_cast<int64_t>(j) * kSumThreads * N;
-                    if (cj < e.D) load_cols<TG, N>(g[r][j], e.rows, row[b + r], e.ld_rows, cj, e.D);
-                    else g[r][j].zero();
-                }
+        for (int r = 0; r < kRowsAhead; ++r) {
+            x[r].zero();
+            if (b + r < n && k[b + r] != none) {
+                const int64_t c = column(k[b + r]);
+                if (c < e.D)
+                    load_row<TG, kVec, ALIGNED>(x[r], at<TG>(const_cast<const void*>(e.rows), row[g][b + r], e.ld_rows, 0), c, e.D, lo, e.rows_end);
             }
+        }
 #pragma unroll
         for (int r = 0; r < kRowsAhead; ++r) {
             const int i = b + r;
-            if (i >= n || key[i] == none) break;
+            if (i >= n || k[i] == none) break;
 #pragma unroll
-            for (int j = 0; j < NP; ++j)
-#pragma unroll
-                for (int k = 0; k < N; ++k) acc[j * N + k] += g[r][j].get(k);
-            const uint32_t next = i + 1 < n ? key[i + 1] : after;
-            if (i + 1 < n && next == key[i]) continue;
+            for (int j = 0; j < kVec; ++j) acc[j] += x[r].get(j);
+            if (i + 1 < n && k[i + 1] == k[i]) continue;
             // the run ends here, or goes on in the next window
-            const bool from = first == 0 && before == key[i];
-            const bool on = i + 1 == n && next == key[i];
-            if (!from && !on) {
-                write_sum<TO, N, NP>(e, key[i], c, acc);
-            } else {
-                float* part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (from ? 0 : 1)) * p.ld_parts;
+            const bool from = first == 0 && k[-1] == k[i];
+            const bool on = i + 1 == n && k[n] == k[i];
+            const int64_t c = column(k[i]);
+            if (c < e.D) {
+                if (!from && !on) {
+                    write_sum<TO>(e, at<TO>(e.table, k[i], e.ld_table, 0), c, acc);
+                } else {
+                    float* part = p.parts + (2 * w + (from ? 0 : 1)) * p.ld_parts;
 #pragma unroll
-                for (int j = 0; j < NP; ++j)
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        const int64_t ck = c + static_cast<int64_t>(j) * kSumThreads * N + k;
-                        if (ck < e.D) part[ck] = acc[j * N + k];
-                    }
+                    for (int j = 0; j < kVec; ++j)
+                        if (c + j >= 0 && c + j < e.D) part[c + j] = acc[j];
+                }
             }
+            if (on && !from && lane == 0 && blockIdx.y == 0) p.crossing[atomicAdd(&p.counters[0], 1u)] = static_cast<uint32_t>(w);
 #pragma unroll
-            for (int k = 0; k < NP * N; ++k) acc[k] = 0.f;
+            for (int j = 0; j < kVec; ++j) acc[j] = 0.f;
             first = i + 1;
         }
     }
 }
 
-// The block of the window in which a crossing token begins adds its parts.
-template <class TO, int N, int NP>
-__global__ void __launch_bounds__(kSumThreads) token_join_kernel(const SumParams p)
+// A block adds up one crossing token's parts in kJoinCols columns: its warps take every
+// eighth window, and their sums are added in warp order.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinCols = 128;
+
+template <class TO>
+__global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const SumParams p)
 {
+    __shared__ float4 sum[kJoinWarps][32];
     const EmbParams& e = p.e;
-    const uint32_t none = static_cast<uint32_t>(e.V);
-    const int64_t w = blockIdx.x;
-    const int64_t end = (w + 1) * kWindow;   // the next window's first position
-    if (end >= e.T) return;
-    const uint32_t v = p.keys[end];
-    if (v == none || p.keys[end - 1] != v) return;
-    // it began before this window
-    if (w > 0 && p.keys[w * kWindow - 1] == v) return;
-    const int64_t c = (static_cast<int64_t>(blockIdx.y) * kSumThreads * NP + threadIdx.x) * N;
-    if (c >= e.D) return;
-    float acc[NP * N];
-    auto add = [&](int64_t slot, bool first) {
-        const float* part = p.parts + slot * p.ld_parts;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int64_t ck = c + static_cast<int64_t>(j) * kSumThreads * N + k;
-                const float x = ck < e.D ? part[ck] : 0.f;
-                acc[j * N + k] = first ? x : acc[j * N + k] + x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t ranges = (e.D + kJoinCols - 1) / kJoinCols;
+    const int64_t items = static_cast<int64_t>(p.counters[0]) * ranges;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t w = p.crossing[item / ranges];
+        const int64_t c = (item % ranges) * kJoinCols + lane * 4;
+        const uint32_t v = p.keys[(w + 1) * kWindow];
+        // windows after this one that begin with the token
+        int64_t more = 0;
+        while (true) {
+            const int64_t next = (w + 1 + more + tid) * kWindow;
+            const int n = __syncthreads_count(next < e.T && p.keys[next] == v);
+            more += n;
+            if (n < kJoinThreads) break;
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < e.D) {
+#pragma unroll 4
+            for (int64_t x = warp; x <= more; x += kJoinWarps) {
+                const int64_t slot = x == 0 ? 2 * w + 1 : 2 * (w + x);
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(p.parts + slot * p.ld_parts + c));
+                acc.x += y.x;
+                acc.y += y.y;
+                acc.z += y.z;
+                acc.w += y.w;
             }
-    };
-    add(2 * w + 1, true);
-    for (int64_t x = w + 1;; ++x) {
-        add(2 * x, false);
-        const int64_t next = (x + 1) * kWindow;
-        if (next >= e.T || p.keys[next] != v) break;
+        }
+        sum[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0) {
+            for (int x = 1; x < kJoinWarps; ++x) {
+                const float4 y = sum[x][lane];
+                acc.x += y.x;
+                acc.y += y.y;
+                acc.z += y.z;
+                acc.w += y.w;
+            }
+            const float total[4] = {acc.x, acc.y, acc.z, acc.w};
+            typename TO::raw* out = reinterpret_cast<typename TO::raw*>(at<TO>(e.table, v, e.ld_table, 0));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < e.D)
+                    out[c + j] = TO::round(e.accumulate ? fmaf(total[j], e.scale, TO::widen(out[c + j])) : total[j] * e.scale);
+        }
+        __syncthreads();
     }
-    write_sum<TO, N, NP>(e, v, c, acc);
+    // the last block leaves the counters at zero
+    __syncthreads();
+    if (tid == 0 && count_done(&p.counters[1]) == gridDim.x - 1) {
+        p.counters[0] = 0;
+        p.counters[1] = 0;
+    }
 }
 
-// zeros in the first D columns of every row
-template <class TO, int N>
-__global__ void __launch_bounds__(256) zero_rows_kernel(const EmbParams p)
+template <class TO, bool ALIGNED>
+__global__ void __launch_bounds__(256) zero_table_kernel(const EmbParams p)
 {
-    const int64_t per = (p.D + N - 1) / N, total = per * p.V;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    Pack<TO, N> z;
-    z.zero();
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t r = i / per;
-        store_cols<TO, N>(z, p.table, r, p.ld_table, (i - r * per) * N, p.D);
-    }
+    zero_rows<TO, ALIGNED>(p, 0, p.V, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                           static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 // ------------------------------------------------------------------- host
@@ -424,8 +861,8 @@ lmloss_status check_embedding(const lmloss_embedding_args* a, bool pointers)
     return LMLOSS_OK;
 }
 
-// every row of both matrices starts on a 16-byte boundary: vectors of 8 columns
-bool vector_rows(const lmloss_embedding_args* a)
+// every row of both matrices starts on a 16-byte boundary
+bool aligned_rows(const lmloss_embedding_args* a)
 {
     return aligned16(a->table) && aligned16(a->rows) && a->ld_table * float_bytes(a->table_dtype) % 16 == 0 &&
            a->ld_rows * float_bytes(a->rows_dtype) % 16 == 0;
@@ -446,11 +883,14 @@ EmbParams params(const lmloss_vocab_ctx* h, const lmloss_embedding_args* a)
     p.scale = a->scale;
     p.accumulate = a->accumulate;
     p.err = h->err;
+    p.table_end = static_cast<const unsigned char*>(a->table) + ((a->V - 1) * a->ld_table + a->D) * float_bytes(a->table_dtype);
+    p.rows_end = static_cast<const unsigned char*>(a->rows) +
+                 (a->T > 0 ? ((a->T - 1) * a->ld_rows + a->D) * float_bytes(a->rows_dtype) : 0);
     return p;
 }
 
 struct SortSpace {
-    size_t keys[2], pos[2], counts, parts, total;
+    size_t keys[2], pos[2], counts, crossing, parts, total;
     int tiles, windows;
     int64_t ld_parts;
 };
@@ -469,6 +909,7 @@ SortSpace sort_space(const lmloss_embedding_args* a)
         s.pos[i] = take(4 * T);
     }
     s.counts = take(sizeof(uint32_t) * kDigits * static_cast<size_t>(s.tiles));
+    s.crossing = take(sizeof(uint32_t) * static_cast<size_t>(s.windows));
     s.parts = take(sizeof(float) * 2 * static_cast<size_t>(s.windows) * static_cast<size_t>(s.ld_parts));
     s.total = off;
     return s;
@@ -483,40 +924,91 @@ lmloss_status by_type(int32_t dtype, F&& f)
     default: return f(Fp32{});
     }
 }
-
-template <class TW, class TO, int N>
-lmloss_status launch_forward(const EmbParams& p, cudaStream_t stream)
+template <class F>
+lmloss_status by_types(const lmloss_embedding_args* a, F&& f)
 {
-    const int64_t vecs = (p.D + N - 1) / N;
+    const bool aligned = aligned_rows(a);
+    return by_type(a->table_dtype, [&](auto table) {
+        return by_type(a->rows_dtype, [&](auto rows) {
+            return aligned ? f(table, rows, std::true_type{}) : f(table, rows, std::false_type{});
+        });
+    });
+}
+
+// vectors of the longest row, its first one possibly begun early
+int64_t row_vectors(const lmloss_embedding_args* a, int32_t written, bool aligned)
+{
+    return (a->D + (aligned ? 0 : 16 / float_bytes(written) - 1) + kVec - 1) / kVec;
+}
+
+// threads of a row: a power of two from 8 to `most`, as many as it has vectors
+int threads_of_row(int64_t vecs, int most)
+{
     int tpr = 8;
-    while (tpr < kFwdThreads && tpr < vecs) tpr *= 2;
-    const int rows = kFwdThreads / tpr;
-    embedding_forward_kernel<TW, TO, N><<<(p.T + rows - 1) / rows, kFwdThreads, 0, stream>>>(p, tpr);
-    return vocab_launch_err();
+    while (tpr < most && tpr < vecs) tpr *= 2;
+    return tpr;
 }
 
-template <class TG, class TO, int N, int NP>
-lmloss_status launch_sums(const SumParams& p, cudaStream_t stream)
+template <class TO, bool ALIGNED>
+lmloss_status launch_cluster_sort(const lmloss_vocab_ctx* h, const EmbParams& p, ClusterSort& q, cudaStream_t stream)
 {
-    const int64_t cols = static_cast<int64_t>(kSumThreads) * N * NP;
-    const dim3 grid(static_cast<unsigned>(p.windows), static_cast<unsigned>((p.e.D + cols - 1) / cols));
-    token_sum_kernel<TG, TO, N, NP><<<grid, kSumThreads, 0, stream>>>(p);
-    lmloss_status st = vocab_launch_err();
-    if (st != LMLOSS_OK) return st;
-    token_join_kernel<TO, N, NP><<<grid, kSumThreads, 0, stream>>>(p);
-    return vocab_launch_err();
+    auto* fn = cluster_sort_kernel<TO, ALIGNED>;
+    const size_t smem = cluster_smem(q.share);
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(cluster_smem(kClusterRounds * kClusterThreads))) != cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        cudaGetLastError();
+        return LMLOSS_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(q.blocks);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(q.blocks + q.fill));
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, p, q) != cudaSuccess) {
+        cudaGetLastError();
+        return LMLOSS_ERR_CUDA;
+    }
+    return LMLOSS_OK;
 }
 
-template <class TO, int N>
-lmloss_status launch_zero(const lmloss_vocab_ctx* h, const EmbParams& p, cudaStream_t stream)
+lmloss_status sort_in_cluster(const lmloss_vocab_ctx* h, const lmloss_embedding_args* a, const SortSpace& s, SumParams& p,
+                              cudaStream_t stream)
 {
-    zero_rows_kernel<TO, N><<<8 * h->num_sms, 256, 0, stream>>>(p);
-    return vocab_launch_err();
+    ClusterSort q{};
+    q.blocks = p.e.T <= 1024 ? 1 : (p.e.T <= 8192 ? 8 : kClusterMax);
+    q.share = (p.e.T + q.blocks - 1) / q.blocks;
+    int bits = 1;
+    while ((static_cast<int64_t>(p.e.V - 1) >> bits) != 0) ++bits;
+    q.passes = (bits + kClusterBits - 1) / kClusterBits;
+    q.bits = (bits + q.passes - 1) / q.passes;
+    q.keys = reinterpret_cast<uint32_t*>(h->ws + s.keys[0]);
+    q.pos = reinterpret_cast<uint32_t*>(h->ws + s.pos[0]);
+    // about what the other SMs write while the cluster sorts (10 us at 4 TB/s)
+    const int64_t row_bytes = a->D * float_bytes(a->table_dtype);
+    // by the SMs that the cluster leaves
+    q.fill = a->accumulate ? 0 : (h->num_sms - q.blocks) / q.blocks * q.blocks;
+    if (q.fill > 0) q.blind = std::min<int64_t>(a->V, (int64_t(40) << 20) / row_bytes);
+    p.keys = q.keys;
+    p.pos = q.pos;
+    p.blind = q.blind;
+    const bool aligned = aligned_rows(a);
+    return by_type(a->table_dtype, [&](auto to) {
+        using TO = decltype(to);
+        return aligned ? launch_cluster_sort<TO, true>(h, p.e, q, stream) : launch_cluster_sort<TO, false>(h, p.e, q, stream);
+    });
 }
 
-lmloss_status sort_tokens(const lmloss_vocab_ctx* h, const EmbParams& p, const SortSpace& s, SumParams& q,
-                          cudaStream_t stream)
+lmloss_status sort_in_passes(const lmloss_vocab_ctx* h, const SortSpace& s, SumParams& q, cudaStream_t stream)
 {
+    const EmbParams& p = q.e;
     int bits = 1;
     while ((static_cast<int64_t>(p.V) >> bits) != 0) ++bits;   // the keys are 0 .. V
     uint32_t* counts = reinterpret_cast<uint32_t*>(h->ws + s.counts);
@@ -536,6 +1028,7 @@ lmloss_status sort_tokens(const lmloss_vocab_ctx* h, const EmbParams& p, const S
     }
     q.keys = keys;
     q.pos = pos;
+    q.blind = 0;
     return LMLOSS_OK;
 }
 
@@ -566,13 +1059,11 @@ lmloss_status lmloss_embedding_forward(lmloss_vocab_handle h, const lmloss_embed
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
     const EmbParams p = params(h, a);
-    const bool vec = vector_rows(a);
-    return by_type(a->table_dtype, [&](auto tw) {
-        return by_type(a->rows_dtype, [&](auto to) {
-            using TW = decltype(tw);
-            using TO = decltype(to);
-            return vec ? launch_forward<TW, TO, 8>(p, stream) : launch_forward<TW, TO, 1>(p, stream);
-        });
+    return by_types(a, [&](auto tw, auto to, auto aligned) {
+        const int tpr = threads_of_row(row_vectors(a, a->rows_dtype, aligned.value), kFwdThreads), rows = kFwdThreads / tpr;
+        embedding_forward_kernel<decltype(tw), decltype(to), aligned.value>
+            <<<static_cast<unsigned>((p.T + rows - 1) / rows), kFwdThreads, 0, stream>>>(p, tpr);
+        return vocab_launch_err();
     });
 }
 
@@ -583,31 +1074,51 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
     if (st != LMLOSS_OK) return st;
     const SortSpace s = sort_space(a);
     if (s.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
-    // blocks are numbered by windows and column ranges
-    if (a->D > 65535LL * kSumThreads * 4) return LMLOSS_ERR_UNSUPPORTED;
+    // column ranges are numbered by the grid's second dimension
+    const bool aligned = aligned_rows(a);
+    const int64_t vecs = row_vectors(a, a->table_dtype, aligned);
+    if (vecs > 65535LL * kSumThreads) return LMLOSS_ERR_UNSUPPORTED;
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
     SumParams q{};
     q.e = params(h, a);
-    const bool vec = vector_rows(a);
-    if (!a->accumulate) {
-        st = by_type(a->table_dtype, [&](auto to) {
-            using TO = decltype(to);
-            return vec ? launch_zero<TO, 8>(h, q.e, stream) : launch_zero<TO, 1>(h, q.e, stream);
+    if (a->T == 0) {
+        if (a->accumulate) return LMLOSS_OK;
+        return by_types(a, [&](auto to, auto, auto al) {
+            zero_table_kernel<decltype(to), al.value><<<8 * h->num_sms, 256, 0, stream>>>(q.e);
+            return vocab_launch_err();
         });
-        if (st != LMLOSS_OK) return st;
     }
-    if (a->T == 0) return LMLOSS_OK;
-    if ((st = sort_tokens(h, q.e, s, q, stream)) != LMLOSS_OK) return st;
+    if (a->T <= kFewPositions) {
+        const int tpr = threads_of_row(vecs, kFewThreads);
+        const int64_t ranges = (vecs + tpr - 1) / tpr;
+        // about eight blocks a SM
+        int span = kFewSpan;
+        while (span > 1 && (a->V + span - 1) / span * ranges < 8 * h->num_sms) span /= 2;
+        const dim3 grid(static_cast<unsigned>((a->V + span - 1) / span), static_cast<unsigned>(ranges));
+        return by_types(a, [&](auto to, auto tg, auto al) {
+            few_positions_kernel<decltype(tg), decltype(to), al.value><<<grid, kFewThreads, 0, stream>>>(q.e, span, tpr);
+            return vocab_launch_err();
+        });
+    }
+    st = a->T <= kClusterPositions ? sort_in_cluster(h, a, s, q, stream) : sort_in_passes(h, s, q, stream);
+    if (st != LMLOSS_OK) return st;
     q.parts = reinterpret_cast<float*>(h->ws + s.parts);
     q.ld_parts = s.ld_parts;
     q.windows = s.windows;
-    return by_type(a->rows_dtype, [&](auto tg) {
-        return by_type(a->table_dtype, [&](auto to) {
-            using TG = decltype(tg);
-            using TO = decltype(to);
-            return vec ? launch_sums<TG, TO, 8, 1>(q, stream) : launch_sums<TG, TO, 1, 4>(q, stream);
-        });
+    q.crossing = reinterpret_cast<uint32_t*>(h->ws + s.crossing);
+    q.counters = h->counters;
+    q.tpr = threads_of_row(vecs, kSumThreads);
+    const int groups = kSumThreads / q.tpr;
+    q.sum_blocks = (s.windows + groups - 1) / groups;
+    const int64_t zero_blocks = a->accumulate ? 0 : (a->V - q.blind + kZeroSpan - 1) / kZeroSpan;
+    const dim3 grid(static_cast<unsigned>(q.sum_blocks + zero_blocks), static_cast<unsigned>((vecs + q.tpr - 1) / q.tpr));
+    return by_types(a, [&](auto to, auto tg, auto al) {
+        token_sum_kernel<decltype(tg), decltype(to), al.value><<<grid, kSumThreads, 0, stream>>>(q);
+        const lmloss_status e = vocab_launch_err();
+        if (e != LMLOSS_OK) return e;
+        token_join_kernel<decltype(to)><<<2 * h->num_sms, kJoinThreads, 0, stream>>>(q);
+        return vocab_launch_err();
     });
 }
 

@@ -321,3 +321,38 @@ def test_refusals(ops):
     with pytest.raises(LMLossError) as e:                            # more than the handle's workspace
         ops.embedding_backward(torch.empty(20001, 4200, device="cuda"), many, num_embeddings=3)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("T,V", [(131072, 50000), (131073, 50000), (150001, 7)])
+def test_gradient_of_many_positions(T, V):
+    from lm_head_vocab_gb300 import VocabOps
+    h = VocabOps(0, max_tokens=T, max_dim=16, max_rows=0)
+    g = gen(T)
+    rows = torch.randint(-4, 5, (T, 13), device="cuda", generator=g).to(BF)
+    ids = make_ids(T, V, "text", torch.int64, g)
+    for accumulate in (False, True):
+        old = torch.full((V, 13), 3.0, device="cuda")
+        total = h.embedding_backward(rows, ids, old.clone(), accumulate=accumulate)
+        ref, _, _ = reference(rows, ids, V, 1.0, old if accumulate else None)
+        assert torch.equal(total.double().cpu(), ref)
+    h.close()
+
+
+@pytest.mark.parametrize("T", [5, 2049])
+@pytest.mark.parametrize("D", [1, 3, 7, 8, 9, 15, 17, 100, 1001, 2047])
+def test_gradient_widths(ops, T, D):
+    # rows that start at every offset from a vector boundary, exact in whole numbers
+    g = gen(T + D)
+    V = 130
+    ids = make_ids(T, V, "text", torch.int64, g)
+    for gt, ot in PAIRS:
+        rows = torch.randint(-3, 4, (T, D), device="cuda", generator=g).to(gt)
+        for accumulate in (False, True):
+            old = torch.randint(-3, 4, (V, D), device="cuda", generator=g).to(ot)
+            total = ops.embedding_backward(rows, ids, old.clone(), accumulate=accumulate)
+            ref, _, _ = reference(rows, ids, V, 1.0, old if accumulate else None)
+            assert torch.equal(total.double().cpu(), ref.to(ot).double())
+        w = torch.randn(V, D, device="cuda", generator=g).to(gt)
+        out = ops.embedding_forward(w, ids, out_dtype=ot)
+        ref = torch.where((ids >= 0)[:, None], w[ids.clamp(min=0)].float(), 0.0).to(ot)
+        assert torch.equal(out, ref)
