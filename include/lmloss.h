@@ -343,7 +343,7 @@ typedef struct {
     const void* ids;             /* [T] token of each position                             */
     int64_t T;                   /* positions, >= 0 and < 2^30                             */
     int64_t V;                   /* rows of the table, >= 1 and < 2^31 - 1                 */
-    int64_t D;                   /* columns, >= 1                                          */
+    int64_t D;                   /* columns, >= 1 and <= 2^30                              */
     void* table;                 /* forward: the weights (read);                           */
                                  /* backward: the weights' gradient (written)              */
     int64_t ld_table;            /* row stride in elements, >= D                           */

@@ -96,14 +96,15 @@ __device__ __forceinline__ void load_ends(Pack<T, N>& q, const unsigned char* ro
     }
 }
 
-// Columns [c, c + N) of a row of an input, whatever its alignment; zeros outside [0, D).
-// lo, hi: the memory that may be read.
+// Columns [c, c + N) of a row of an input, whatever its alignment; what lies outside
+// [0, D) has no meaning.  lo, hi: the memory that may be read.  A vector at a row's end
+// reads on into its neighbour; only at the ends of that memory columns go one by one.
 template <class T, int N, bool ALIGNED>
 __device__ __forceinline__ void load_row(Pack<T, N>& q, const unsigned char* row, int64_t c, int64_t D,
                                          const unsigned char* lo, const unsigned char* hi)
 {
     const unsigned char* p = row + c * T::kBytes;
-    if (c >= 0 && c + N <= D && (ALIGNED || inside_blocks<T, N>(p, lo, hi))) {
+    if (ALIGNED ? p + N * T::kBytes <= hi : inside_blocks<T, N>(p, lo, hi)) {
         if constexpr (ALIGNED) {
             q.load(p);
         } else {
@@ -119,10 +120,14 @@ __device__ __forceinline__ void load_row(Pack<T, N>& q, const unsigned char* row
     }
 }
 // The same columns of a row that is being written: row + c is on a 16-byte boundary.
+// (At a row's ends the vector holds columns of a neighbouring row, which another block
+// may be writing: those are not used.)
 template <class T, int N>
-__device__ __forceinline__ void load_own(Pack<T, N>& q, const unsigned char* row, int64_t c, int64_t D)
+__device__ __forceinline__ void load_own(Pack<T, N>& q, const unsigned char* row, int64_t c, int64_t D,
+                                         const unsigned char* lo, const unsigned char* hi)
 {
-    if (c >= 0 && c + N <= D) q.load_rw(row + c * T::kBytes);
+    const unsigned char* p = row + c * T::kBytes;
+    if (p >= lo && p + N * T::kBytes <= hi) q.load_rw(p);
     else load_ends(q, row, c, D);
 }
 template <class T, int N>
@@ -160,34 +165,45 @@ __global__ void __launch_bounds__(kFwdThreads) embedding_forward_kernel(const Em
     const int64_t id = load_id(p, t);
     const bool valid = id >= 0 && id < p.V;
     if (!valid && id != kIgnore && lane == 0) set_error(p.err, kErrBadTarget);
-    const int64_t step = static_cast<int64_t>(tpr) * N;
     unsigned char* out = at<TO>(p.rows, t, p.ld_rows, 0);
-    const int64_t begin = lane * N - row_offset<TO, ALIGNED>(out);
+    const int off = row_offset<TO, ALIGNED>(out), D = static_cast<int>(p.D);
+    const int step = tpr * N;
     if (!valid) {
         const float fill = id == kIgnore ? 0.f : __int_as_float(0x7fc00000);
+        const float all[N] = {fill, fill, fill, fill, fill, fill, fill, fill};
         Pack<TO, N> o;
-        o.zero();
-#pragma unroll
-        for (int i = 0; i < N; ++i) o.set(i, fill);
-        for (int64_t c = begin; c < p.D; c += step) store_row<TO, N>(o, out, c, p.D);
+        o.set_all(all);
+        for (int c = lane * N - off; c < D; c += step) store_row<TO, N>(o, out, c, D);
         return;
     }
     const unsigned char* w = at<TW>(const_cast<const void*>(p.table), id, p.ld_table, 0);
     const unsigned char* lo = static_cast<const unsigned char*>(p.table);
-    for (int64_t c0 = begin; c0 < p.D; c0 += step * kFwdUnroll) {
+    // aligned rows: a row's last vector reads on into the next row, which the last one lacks
+    const int whole = id + 1 < p.V ? D : D - N + 1;
+    for (int c0 = lane * N - off; c0 < D; c0 += step * kFwdUnroll) {
         Pack<TW, N> x[kFwdUnroll];
 #pragma unroll
-        for (int u = 0; u < kFwdUnroll; ++u)
-            if (c0 + u * step < p.D) load_row<TW, N, ALIGNED>(x[u], w, c0 + u * step, p.D, lo, p.table_end);
-#pragma unroll
-        for (int u = 0; u < kFwdUnroll; ++u)
-            if (c0 + u * step < p.D) {
-                Pack<TO, N> o;
-                o.zero();
-#pragma unroll
-                for (int i = 0; i < N; ++i) o.set(i, x[u].get(i) * p.scale);
-                store_row<TO, N>(o, out, c0 + u * step, p.D);
+        for (int u = 0; u < kFwdUnroll; ++u) {
+            const int c = c0 + u * step;
+            if (c >= D) continue;
+            if constexpr (ALIGNED) {
+                if (c < whole) x[u].load(w + static_cast<int64_t>(c) * TW::kBytes);
+                else load_ends(x[u], w, c, D);
+            } else {
+                load_row<TW, N, false>(x[u], w, c, D, lo, p.table_end);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < kFwdUnroll; ++u) {
+            const int c = c0 + u * step;
+            if (c >= D) continue;
+            float y[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[i] = x[u].get(i) * p.scale;
+            Pack<TO, N> o;
+            o.set_all(y);
+            store_row<TO, N>(o, out, c, D);
+        }
     }
 }
 
@@ -195,17 +211,18 @@ __global__ void __launch_bounds__(kFwdThreads) embedding_forward_kernel(const Em
 template <class TO>
 __device__ __forceinline__ void write_sum(const EmbParams& p, unsigned char* row, int64_t c, const float (&acc)[kVec])
 {
-    Pack<TO, kVec> o;
-    o.zero();
+    float y[kVec];
     if (p.accumulate) {
         Pack<TO, kVec> old;
-        load_own<TO, kVec>(old, row, c, p.D);
+        load_own<TO, kVec>(old, row, c, p.D, static_cast<const unsigned char*>(p.table), p.table_end);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) o.set(i, fmaf(acc[i], p.scale, old.get(i)));
+        for (int i = 0; i < kVec; ++i) y[i] = fmaf(acc[i], p.scale, old.get(i));
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) o.set(i, acc[i] * p.scale);
+        for (int i = 0; i < kVec; ++i) y[i] = acc[i] * p.scale;
     }
+    Pack<TO, kVec> o;
+    o.set_all(y);
     store_row<TO, kVec>(o, row, c, p.D);
 }
 
@@ -447,11 +464,9 @@ constexpr int kClusterMax = 16;              // blocks
 constexpr int kClusterRounds = 8;            // keys a thread
 constexpr int kClusterPositions = kClusterMax * kClusterRounds * kClusterThreads;
 
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr)
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t a)
 {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t a, uint32_t b)
 {
@@ -464,7 +479,7 @@ __device__ void zero_rows(const EmbParams& p, int64_t r0, int64_t r1, int64_t me
 {
     Pack<TO, kVec> z;
     z.zero();
-    if (!ALIGNED && p.ld_table == p.D) {
+    if (p.ld_table == p.D) {
         // one run of memory
         unsigned char* base = at<TO>(p.table, r0, p.ld_table, 0);
         const int64_t n = (r1 - r0) * p.D, off = row_offset<TO, ALIGNED>(base);
@@ -489,11 +504,11 @@ struct ClusterSort {
 };
 
 // dynamic shared memory: [2][share] (key, position), [warps][digits] 16-bit counts,
-// [digits] totals, [digits] bases
+// [blocks][digits] 16-bit totals, [4][digits / 2] sums of a quarter of the warps, [digits] bases
 __host__ __device__ constexpr size_t cluster_smem(int share)
 {
-    return sizeof(uint2) * 2 * static_cast<size_t>(share) + sizeof(uint16_t) * kClusterWarps * kClusterDigits +
-           2 * sizeof(uint32_t) * kClusterDigits;
+    return sizeof(uint2) * 2 * static_cast<size_t>(share) +
+           sizeof(uint16_t) * (kClusterWarps + kClusterMax) * kClusterDigits + 3 * sizeof(uint32_t) * kClusterDigits;
 }
 
 template <class TO, bool ALIGNED>
@@ -508,9 +523,11 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
     }
     uint2* buf = reinterpret_cast<uint2*>(mem);
     uint16_t* bin = reinterpret_cast<uint16_t*>(buf + 2 * q.share);
-    uint32_t* total = reinterpret_cast<uint32_t*>(bin + kClusterWarps * kClusterDigits);
-    uint32_t* base = total + kClusterDigits;
-    __shared__ uint32_t part[32], valid;
+    uint32_t* totals = reinterpret_cast<uint32_t*>(bin + kClusterWarps * kClusterDigits);
+    uint32_t* quarters = totals + kClusterMax * kClusterDigits / 2;
+    uint32_t* base = quarters + 2 * kClusterDigits;
+    __shared__ uint32_t part[kClusterDigits / 32];
+    uint32_t valid = 0;
     const int me = static_cast<int>(cluster_rank());
     const uint32_t magic = static_cast<uint32_t>(((uint64_t(1) << 32) + q.share - 1) / q.share);
     int held = max(0, min(q.share, p.T - me * q.share));
@@ -557,27 +574,46 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
             rank[r] = before + __popc(same & ((1u << lane) - 1u));
         }
         __syncthreads();
-        // digit `tid`: the warps' offsets, and the block's total
-        if (tid < digits) {
-            uint32_t run = 0;
-#pragma unroll 8
-            for (int w = 0; w < kClusterWarps; ++w) {
-                const uint32_t n = bin[w * kClusterDigits + tid];
-                bin[w * kClusterDigits + tid] = static_cast<uint16_t>(run);
-                run += n;
+        // digits 2 d and 2 d + 1 together, in the halves of a word: the warps' offsets by
+        // quarters, and the block's totals, sent to every block of the cluster
+        {
+            constexpr int kPairs = kClusterDigits / 2, kQuarter = kClusterWarps / 4;
+            const int d = tid & (kPairs - 1), quarter = tid / kPairs;
+            uint32_t* word = reinterpret_cast<uint32_t*>(bin) + quarter * kQuarter * kPairs + d;
+            uint32_t n[kQuarter], sum = 0;
+#pragma unroll
+            for (int w = 0; w < kQuarter; ++w) {
+                n[w] = word[w * kPairs];
+                sum += n[w];
             }
-            total[tid] = run;
+            quarters[quarter * kPairs + d] = sum;
+            __syncthreads();
+            uint32_t run = 0, total = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t y = quarters[x * kPairs + d];
+                run += x < quarter ? y : 0;
+                total += y;
+            }
+#pragma unroll
+            for (int w = 0; w < kQuarter; ++w) {
+                word[w * kPairs] = run;
+                run += n[w];
+            }
+            const uint32_t mine = smem_addr(totals + me * kPairs + d);
+            for (int b = quarter; b < q.blocks; b += 4) st_cluster(dsmem_map(mine, b), total);
         }
         cluster_sync_all();
         // where the digit begins: after all smaller digits, and after the same digit of
         // the blocks before this one
-        uint32_t all = 0, mine = 0;
-        if (tid < digits) {
-            const uint32_t own = smem_addr(total + tid);
+        uint32_t all = 0, before_me = 0;
+        if (tid < kClusterDigits) {
+            const uint16_t* t = reinterpret_cast<const uint16_t*>(totals) + tid;
+#pragma unroll 8
             for (int b = 0; b < q.blocks; ++b) {
-                const uint32_t n = ld_cluster(dsmem_map(own, b));
+                const uint32_t n = t[b * kClusterDigits];
                 all += n;
-                mine += b < me ? n : 0;
+                before_me += b < me ? n : 0;
             }
         }
         uint32_t inc = all;
@@ -585,20 +621,17 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
             const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        if (lane == 31) part[warp] = inc;
+        if (lane == 31 && warp < kClusterDigits / 32) part[warp] = inc;
         __syncthreads();
-        if (warp == 0) {
-            const uint32_t own = part[lane];
-            uint32_t w = own;
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, w, o);
-                if (lane >= o) w += v;
-            }
-            part[lane] = w - own;
-            if (lane == 31) valid = w;
+        uint32_t smaller = 0;
+        valid = 0;
+#pragma unroll
+        for (int x = 0; x < kClusterDigits / 32; ++x) {
+            const uint32_t y = part[x];
+            smaller += x < warp ? y : 0;
+            valid += y;
         }
-        __syncthreads();
-        if (tid < digits) base[tid] = part[warp] + inc - all + mine;
+        if (tid < kClusterDigits) base[tid] = smaller + inc - all + before_me;
         __syncthreads();
         const bool last = pass + 1 == q.passes;
         const uint32_t out = smem_addr(buf + ((pass + 1) & 1) * q.share);
@@ -626,17 +659,17 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
 }
 
 // ------------------------------------------------------- sums by token
-// A group of `tpr` threads takes a window of kWindow sorted positions and a vector of
-// columns each.  A token whose positions all lie in the window is summed and written.
-// One that crosses a window's border leaves the window's part of its sum, in fp32: in
-// slot 1 where it begins in this window, in slot 0 where it came from the window
-// before; the join adds a token's parts in an order that the windows fix.
+// A group of `tpr` threads takes a window of sorted positions and a vector of columns
+// each.  A token whose positions all lie in the window is summed and written.  One that
+// crosses a window's border leaves the window's part of its sum, in fp32: in slot 1
+// where it begins in this window, in slot 0 where it came from the window before; the
+// join adds a token's parts in an order that the windows fix.
 //
 // The blocks after these write zeros where no position holds the token: a block
 // finds its rows' range in the sorted keys and passes over those that occur.
-constexpr int kWindow = 32;
+constexpr int kWindow = 32;                  // positions of a window, at most
 constexpr int kSumThreads = 128;
-constexpr int kZeroSpan = 32;                // table rows of a block that writes zeros
+constexpr int kZeroSpan = 64;                // table rows of a block that writes zeros
 constexpr int kMaxGroups = 16;               // of a block: tpr >= 8
 
 struct SumParams {
@@ -645,7 +678,7 @@ struct SumParams {
     const uint32_t* pos;
     float* parts;           // [windows][2][ld_parts]
     int64_t ld_parts;
-    int windows;
+    int window, windows;
     int tpr;
     int sum_blocks;
     int64_t blind;          // rows already zero
@@ -668,97 +701,138 @@ __device__ __forceinline__ int lower_bound(const uint32_t* keys, int n, uint32_t
     return lo;
 }
 
-template <class TG, class TO, bool ALIGNED>
-__global__ void __launch_bounds__(kSumThreads) token_sum_kernel(const SumParams p)
+template <class TO, bool ALIGNED>
+__device__ void zero_absent_rows(const SumParams& p, int64_t v0, uint8_t* held)
 {
+    const EmbParams& e = p.e;
+    const int tid = threadIdx.x;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroSpan), e.V - v0));
+    if (tid < kZeroSpan) held[tid] = 0;
+    int i = lower_bound(p.keys, e.T, static_cast<uint32_t>(v0)) + tid;
+    __syncthreads();
+    for (; i < e.T; i += kSumThreads) {
+        const uint32_t k = p.keys[i];
+        if (k >= v0 + rows) break;
+        held[k - v0] = 1;
+    }
+    __syncthreads();
+    const int per = static_cast<int>((e.D + (ALIGNED ? 0 : kGranule<TO> - 1) + kVec - 1) / kVec);
+    Pack<TO, kVec> z;
+    z.zero();
+    const int step = kSumThreads * gridDim.y;
+    for (int r = 0; r < rows; ++r) {
+        if (held[r]) continue;
+        unsigned char* out = at<TO>(e.table, v0 + r, e.ld_table, 0);
+        const int off = row_offset<TO, ALIGNED>(out);
+        for (int x = blockIdx.y * kSumThreads + tid; x < per; x += step) {
+            const int64_t c = static_cast<int64_t>(x) * kVec - off;
+            if (c < e.D) store_row<TO, kVec>(z, out, c, e.D);
+        }
+    }
+}
+
+// Adds to memory without reading it first; every element is added to once, so the
+// order of the blocks does not matter.
+__device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float d)
+{
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
+template <class TG, class TO, bool ALIGNED>
+__global__ void __launch_bounds__(kSumThreads, ALIGNED ? 8 : 6) token_sum_kernel(const SumParams p)
+{
+    constexpr int kAhead = TG::kBytes == 4 ? kRowsAhead / 2 : kRowsAhead;   // rows on their way
     __shared__ uint32_t key[kMaxGroups][kWindow + 2], row[kMaxGroups][kWindow];
+    __shared__ int8_t shift[kMaxGroups][kWindow];   // from a 16-byte boundary to the table row
+    __shared__ uint32_t ends_of[kMaxGroups];
+    grid_dep_wait();
     const EmbParams& e = p.e;
     const uint32_t none = static_cast<uint32_t>(e.V);
     const int tid = threadIdx.x;
     if (blockIdx.x >= static_cast<unsigned>(p.sum_blocks)) {
-        if (blockIdx.y) return;
-        const int64_t v0 = p.blind + static_cast<int64_t>(blockIdx.x - p.sum_blocks) * kZeroSpan;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroSpan), e.V - v0));
-        uint8_t* held = reinterpret_cast<uint8_t*>(row);
-        if (tid < kZeroSpan) held[tid] = 0;
-        int i = lower_bound(p.keys, e.T, static_cast<uint32_t>(v0)) + tid;
-        __syncthreads();
-        for (; i < e.T; i += kSumThreads) {
-            const uint32_t k = p.keys[i];
-            if (k >= v0 + rows) break;
-            held[k - v0] = 1;
-        }
-        __syncthreads();
-        const int64_t per = (e.D + (ALIGNED ? 0 : kGranule<TO> - 1) + kVec - 1) / kVec;
-        Pack<TO, kVec> z;
-        z.zero();
-        for (int r = 0; r < rows; ++r) {
-            if (held[r]) continue;
-            unsigned char* out = at<TO>(e.table, v0 + r, e.ld_table, 0);
-            const int off = row_offset<TO, ALIGNED>(out);
-            for (int64_t x = tid; x < per; x += kSumThreads)
-                if (x * kVec - off < e.D) store_row<TO, kVec>(z, out, x * kVec - off, e.D);
-        }
+        zero_absent_rows<TO, ALIGNED>(p, p.blind + static_cast<int64_t>(blockIdx.x - p.sum_blocks) * kZeroSpan,
+                                      reinterpret_cast<uint8_t*>(row));
         return;
     }
     const int groups = kSumThreads / p.tpr, g = tid / p.tpr, lane = tid & (p.tpr - 1);
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * groups + g;
-    const int64_t i0 = w * kWindow;
-    const int n = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(kWindow), e.T - i0)));
-    // key[.][0] and key[.][n + 1]: the keys before and after the window
-    for (int i = lane; i < kWindow + 2; i += p.tpr) {
-        const int64_t at = i0 - 1 + i;
-        key[g][i] = at >= 0 && at < e.T ? p.keys[at] : none;
-        if (i < kWindow && i0 + i < e.T) row[g][i] = p.pos[i0 + i];
+    const int w = static_cast<int>(blockIdx.x) * groups + g;
+    const int64_t i0 = static_cast<int64_t>(w) * p.window;
+    if (lane == 0) ends_of[g] = 0;
+    // key[.][0] and key[.][window + 1]: the keys before and after the window
+    for (int i = lane; i < p.window + 2; i += p.tpr) {
+        const int64_t at_ = i0 - 1 + i;
+        key[g][i] = at_ >= 0 && at_ < e.T ? p.keys[at_] : none;
+        if (i < p.window) row[g][i] = i0 + i < e.T ? p.pos[i0 + i] : 0;
     }
     __syncthreads();
-    const int64_t vec = static_cast<int64_t>(blockIdx.y) * p.tpr + lane;
-    if (n == 0) return;
     const uint32_t* k = key[g] + 1;
+    for (int i = lane; i < p.window; i += p.tpr) {
+        if (k[i] != none && (k[i + 1] != k[i] || i + 1 == p.window)) atomicOr(&ends_of[g], 1u << i);
+        if (!ALIGNED)
+            shift[g][i] = k[i] == none ? 0 : static_cast<int8_t>(row_offset<TO, ALIGNED>(at<TO>(e.table, k[i], e.ld_table, 0)));
+    }
+    __syncthreads();
+    const uint32_t ends = ends_of[g];       // positions after which a run's sum is due
+    if (ends == 0) return;
+    const int n = 32 - __clz(ends);         // the last valid position ends a run
+    const int64_t vec = static_cast<int64_t>(blockIdx.y) * p.tpr + lane;
+    if (vec * kVec - (ALIGNED ? 0 : kGranule<TO> - 1) >= e.D) return;
+    const int64_t c0 = vec * kVec;          // the vector's first column, where table rows are aligned
     const unsigned char* lo = static_cast<const unsigned char*>(e.rows);
-    // the vector's first column in table row v
-    auto column = [&](uint32_t v) {
-        return vec * kVec - (ALIGNED ? 0 : row_offset<TO, ALIGNED>(at<TO>(e.table, v, e.ld_table, 0)));
-    };
+    const unsigned char* base = lo + c0 * TG::kBytes;
+    const int64_t ld_bytes = e.ld_rows * TG::kBytes;
+    const uint32_t whole = c0 + kVec <= e.D ? 0xffffffffu : static_cast<uint32_t>(e.T - 1);
 
     float acc[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
     int first = 0;   // where the current token's run begins in the window
-    for (int b = 0; b < n; b += kRowsAhead) {
-        if (k[b] == none) break;
-        Pack<TG, kVec> x[kRowsAhead];
+    for (int b = 0; b < n; b += kAhead) {
+        Pack<TG, kVec> x[kAhead];
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r) {
-            x[r].zero();
-            if (b + r < n && k[b + r] != none) {
-                const int64_t c = column(k[b + r]);
-                if (c < e.D)
-                    load_row<TG, kVec, ALIGNED>(x[r], at<TG>(const_cast<const void*>(e.rows), row[g][b + r], e.ld_rows, 0), c, e.D, lo, e.rows_end);
+        for (int r = 0; r < kAhead; ++r) {
+            if (b + r >= n) continue;
+            const uint32_t t = row[g][b + r];
+            if constexpr (ALIGNED) {
+                // a row's last vector reads on into the next row, which the last one lacks
+                if (t < whole) x[r].load(base + t * ld_bytes);
+                else load_ends(x[r], lo + t * ld_bytes, c0, e.D);
+            } else {
+                load_row<TG, kVec, false>(x[r], lo + t * ld_bytes, c0 - shift[g][b + r], e.D, lo, e.rows_end);
             }
         }
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r) {
+        for (int r = 0; r < kAhead; ++r) {
             const int i = b + r;
-            if (i >= n || k[i] == none) break;
+            if (i >= n) continue;
 #pragma unroll
             for (int j = 0; j < kVec; ++j) acc[j] += x[r].get(j);
-            if (i + 1 < n && k[i + 1] == k[i]) continue;
+            if (!(ends >> i & 1u)) continue;
             // the run ends here, or goes on in the next window
-            const bool from = first == 0 && k[-1] == k[i];
-            const bool on = i + 1 == n && k[n] == k[i];
-            const int64_t c = column(k[i]);
-            if (c < e.D) {
-                if (!from && !on) {
-                    write_sum<TO>(e, at<TO>(e.table, k[i], e.ld_table, 0), c, acc);
+            const uint32_t v = k[i];
+            const bool from = first == 0 && k[-1] == v, on = i + 1 == p.window && k[i + 1] == v;
+            const int64_t c = c0 - (ALIGNED ? 0 : shift[g][i]);
+            if (from || on) {
+                float* part = p.parts + (2 * static_cast<int64_t>(w) + (from ? 0 : 1)) * p.ld_parts;
+                if (ALIGNED && c + kVec <= e.D) {
+                    reinterpret_cast<float4*>(part + c)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    reinterpret_cast<float4*>(part + c)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
                 } else {
-                    float* part = p.parts + (2 * w + (from ? 0 : 1)) * p.ld_parts;
 #pragma unroll
                     for (int j = 0; j < kVec; ++j)
                         if (c + j >= 0 && c + j < e.D) part[c + j] = acc[j];
                 }
+                if (on && !from && lane == 0 && blockIdx.y == 0) p.crossing[atomicAdd(&p.counters[0], 1u)] = static_cast<uint32_t>(w);
+            } else if (c < e.D) {
+                unsigned char* out = at<TO>(e.table, v, e.ld_table, 0);
+                if (TO::kBytes == 4 && e.accumulate && c >= 0 && c + kVec <= e.D) {
+                    float* f = reinterpret_cast<float*>(out) + c;
+                    red_add4(f, acc[0] * e.scale, acc[1] * e.scale, acc[2] * e.scale, acc[3] * e.scale);
+                    red_add4(f + 4, acc[4] * e.scale, acc[5] * e.scale, acc[6] * e.scale, acc[7] * e.scale);
+                } else {
+                    write_sum<TO>(e, out, c, acc);
+                }
             }
-            if (on && !from && lane == 0 && blockIdx.y == 0) p.crossing[atomicAdd(&p.counters[0], 1u)] = static_cast<uint32_t>(w);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) acc[j] = 0.f;
             first = i + 1;
@@ -766,60 +840,102 @@ __global__ void __launch_bounds__(kSumThreads) token_sum_kernel(const SumParams 
     }
 }
 
-// A block adds up one crossing token's parts in kJoinCols columns: its warps take every
-// eighth window, and their sums are added in warp order.
+// Crossing tokens' sums, kJoinCols columns an item.  A warp adds up the few windows of
+// most tokens by itself, in window order; a token of more than kJoinAlone windows is left
+// to the whole block, whose warps take every eighth window and are added in warp order.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinCols = 128;
+constexpr int kJoinAlone = 7;
 
 template <class TO>
 __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const SumParams p)
 {
     __shared__ float4 sum[kJoinWarps][32];
+    __shared__ int64_t long_item[kJoinWarps];
+    __shared__ int long_more[kJoinWarps];
     const EmbParams& e = p.e;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
     const int64_t ranges = (e.D + kJoinCols - 1) / kJoinCols;
-    const int64_t items = static_cast<int64_t>(p.counters[0]) * ranges;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t w = p.crossing[item / ranges];
-        const int64_t c = (item % ranges) * kJoinCols + lane * 4;
-        const uint32_t v = p.keys[(w + 1) * kWindow];
-        // windows after this one that begin with the token
-        int64_t more = 0;
-        while (true) {
-            const int64_t next = (w + 1 + more + tid) * kWindow;
-            const int n = __syncthreads_count(next < e.T && p.keys[next] == v);
-            more += n;
-            if (n < kJoinThreads) break;
-        }
+    const int64_t items = static_cast<int64_t>(__ldcg(p.counters)) * ranges;
+    // windows first, first + step, ... of the `more` after window w, and w itself (x = 0);
+    // eight are on their way at a time
+    auto add = [&](int64_t w, int64_t c, int first, int more, int step) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < e.D) {
-#pragma unroll 4
-            for (int64_t x = warp; x <= more; x += kJoinWarps) {
+        if (c >= e.D) return acc;
+        for (int x0 = first; x0 <= more; x0 += 8 * step) {
+            float4 y[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int x = x0 + u * step;
                 const int64_t slot = x == 0 ? 2 * w + 1 : 2 * (w + x);
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(p.parts + slot * p.ld_parts + c));
-                acc.x += y.x;
-                acc.y += y.y;
-                acc.z += y.z;
-                acc.w += y.w;
+                y[u] = x <= more ? __ldcg(reinterpret_cast<const float4*>(p.parts + slot * p.ld_parts + c))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                acc.x += y[u].x;
+                acc.y += y[u].y;
+                acc.z += y[u].z;
+                acc.w += y[u].w;
             }
         }
-        sum[warp][lane] = acc;
-        __syncthreads();
-        if (warp == 0) {
-            for (int x = 1; x < kJoinWarps; ++x) {
-                const float4 y = sum[x][lane];
-                acc.x += y.x;
-                acc.y += y.y;
-                acc.z += y.z;
-                acc.w += y.w;
-            }
-            const float total[4] = {acc.x, acc.y, acc.z, acc.w};
-            typename TO::raw* out = reinterpret_cast<typename TO::raw*>(at<TO>(e.table, v, e.ld_table, 0));
+        return acc;
+    };
+    auto write = [&](uint32_t v, int64_t c, float4 acc) {
+        const float total[4] = {acc.x, acc.y, acc.z, acc.w};
+        typename TO::raw* out = reinterpret_cast<typename TO::raw*>(at<TO>(e.table, v, e.ld_table, 0));
+        float old[4] = {0.f, 0.f, 0.f, 0.f};
+        if (e.accumulate) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (c + j < e.D)
-                    out[c + j] = TO::round(e.accumulate ? fmaf(total[j], e.scale, TO::widen(out[c + j])) : total[j] * e.scale);
+                if (c + j < e.D) old[j] = TO::widen(out[c + j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < e.D) out[c + j] = TO::round(e.accumulate ? fmaf(total[j], e.scale, old[j]) : total[j] * e.scale);
+    };
+    // neighbouring items, likely of one long token, go to different blocks
+    for (int64_t item0 = blockIdx.x; item0 < items; item0 += static_cast<int64_t>(gridDim.x) * kJoinWarps) {
+        const int64_t item = item0 + static_cast<int64_t>(warp) * gridDim.x;
+        if (lane == 0) long_item[warp] = -1;
+        if (item < items) {
+            const int64_t w = __ldcg(p.crossing + item / ranges), c = (item % ranges) * kJoinCols + lane * 4;
+            const uint32_t v = __ldcg(p.keys + (w + 1) * p.window);
+            // windows after this one that begin with the token
+            int more = 0;
+            while (true) {
+                const int64_t next = (w + 1 + more + lane) * p.window;
+                const int n = __popc(__ballot_sync(0xffffffffu, next < e.T && __ldcg(p.keys + next) == v));
+                more += n;
+                if (n < 32) break;
+            }
+            if (more <= kJoinAlone) {
+                write(v, c, add(w, c, 0, more, 1));
+            } else if (lane == 0) {
+                long_item[warp] = item;
+                long_more[warp] = more;
+            }
+        }
+        __syncthreads();
+        for (int l = 0; l < kJoinWarps; ++l) {
+            if (long_item[l] < 0) continue;
+            const int64_t w = __ldcg(p.crossing + long_item[l] / ranges), c = (long_item[l] % ranges) * kJoinCols + lane * 4;
+            float4 acc = add(w, c, warp, long_more[l], kJoinWarps);
+            sum[warp][lane] = acc;
+            __syncthreads();
+            if (warp == 0) {
+                for (int x = 1; x < kJoinWarps; ++x) {
+                    const float4 y = sum[x][lane];
+                    acc.x += y.x;
+                    acc.y += y.y;
+                    acc.z += y.z;
+                    acc.w += y.w;
+                }
+                write(__ldcg(p.keys + (w + 1) * p.window), c, acc);
+            }
+            __syncthreads();
         }
         __syncthreads();
     }
@@ -850,6 +966,7 @@ lmloss_status check_embedding(const lmloss_embedding_args* a, bool pointers)
     if (a->accumulate != 0 && a->accumulate != 1) return LMLOSS_ERR_INVALID_ARG;
     // 32-bit positions and tokens in the kernels; byte offsets fit in 64 bits
     if (a->T >= (int64_t(1) << 30) || a->V >= (int64_t(1) << 31) - 1) return LMLOSS_ERR_UNSUPPORTED;
+    if (a->D > (int64_t(1) << 30)) return LMLOSS_ERR_UNSUPPORTED;
     if (a->ld_table > INT64_MAX / 16 / a->V || (a->T > 0 && a->ld_rows > INT64_MAX / 16 / a->T))
         return LMLOSS_ERR_INVALID_ARG;
     if (!pointers) return LMLOSS_OK;
@@ -891,7 +1008,7 @@ EmbParams params(const lmloss_vocab_ctx* h, const lmloss_embedding_args* a)
 
 struct SortSpace {
     size_t keys[2], pos[2], counts, crossing, parts, total;
-    int tiles, windows;
+    int tiles, window, windows;
     int64_t ld_parts;
 };
 
@@ -900,7 +1017,11 @@ SortSpace sort_space(const lmloss_embedding_args* a)
     SortSpace s{};
     const size_t T = static_cast<size_t>(a->T);
     s.tiles = static_cast<int>((a->T + kTile - 1) / kTile);
-    s.windows = static_cast<int>((a->T + kWindow - 1) / kWindow);
+    // windows of 32 positions, or fewer where those leave SMs without four blocks
+    const int64_t ranges = (a->D + kVec * kSumThreads - 1) / (kVec * kSumThreads);
+    s.window = kWindow;
+    while (s.window > 8 && (a->T + s.window - 1) / s.window * ranges < 600) s.window /= 2;
+    s.windows = static_cast<int>((a->T + s.window - 1) / s.window);
     s.ld_parts = (a->D + 7) / 8 * 8;
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off = vocab_align(off + bytes); return o; };
@@ -949,6 +1070,27 @@ int threads_of_row(int64_t vecs, int most)
     return tpr;
 }
 
+// A kernel that may be launched while the one before it on the stream still runs (it
+// waits for that one's writes itself).
+template <class K, class P>
+lmloss_status launch_after(K* fn, dim3 grid, int threads, cudaStream_t stream, const P& p)
+{
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
+        cudaGetLastError();
+        return LMLOSS_ERR_CUDA;
+    }
+    return LMLOSS_OK;
+}
+
 template <class TO, bool ALIGNED>
 lmloss_status launch_cluster_sort(const lmloss_vocab_ctx* h, const EmbParams& p, ClusterSort& q, cudaStream_t stream)
 {
@@ -983,7 +1125,8 @@ lmloss_status sort_in_cluster(const lmloss_vocab_ctx* h, const lmloss_embedding_
                               cudaStream_t stream)
 {
     ClusterSort q{};
-    q.blocks = p.e.T <= 1024 ? 1 : (p.e.T <= 8192 ? 8 : kClusterMax);
+    q.blocks = 1;
+    while (q.blocks < kClusterMax && q.blocks * kClusterThreads < p.e.T) q.blocks *= 2;
     q.share = (p.e.T + q.blocks - 1) / q.blocks;
     int bits = 1;
     while ((static_cast<int64_t>(p.e.V - 1) >> bits) != 0) ++bits;
@@ -991,11 +1134,12 @@ lmloss_status sort_in_cluster(const lmloss_vocab_ctx* h, const lmloss_embedding_
     q.bits = (bits + q.passes - 1) / q.passes;
     q.keys = reinterpret_cast<uint32_t*>(h->ws + s.keys[0]);
     q.pos = reinterpret_cast<uint32_t*>(h->ws + s.pos[0]);
-    // about what the other SMs write while the cluster sorts (10 us at 4 TB/s)
-    const int64_t row_bytes = a->D * float_bytes(a->table_dtype);
+    // about what the other SMs write while the cluster sorts (measured: 12 us and 1 us more for
+    // every 4700 positions, at 5 TB/s)
+    const int64_t row_bytes = a->D * float_bytes(a->table_dtype), while_sorting = (12 + a->T / 4700) * 5000000;
     // by the SMs that the cluster leaves
     q.fill = a->accumulate ? 0 : (h->num_sms - q.blocks) / q.blocks * q.blocks;
-    if (q.fill > 0) q.blind = std::min<int64_t>(a->V, (int64_t(40) << 20) / row_bytes);
+    if (q.fill > 0) q.blind = std::min<int64_t>(a->V, while_sorting / row_bytes);
     p.keys = q.keys;
     p.pos = q.pos;
     p.blind = q.blind;
@@ -1105,6 +1249,7 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
     if (st != LMLOSS_OK) return st;
     q.parts = reinterpret_cast<float*>(h->ws + s.parts);
     q.ld_parts = s.ld_parts;
+    q.window = s.window;
     q.windows = s.windows;
     q.crossing = reinterpret_cast<uint32_t*>(h->ws + s.crossing);
     q.counters = h->counters;
@@ -1114,11 +1259,10 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
     const int64_t zero_blocks = a->accumulate ? 0 : (a->V - q.blind + kZeroSpan - 1) / kZeroSpan;
     const dim3 grid(static_cast<unsigned>(q.sum_blocks + zero_blocks), static_cast<unsigned>((vecs + q.tpr - 1) / q.tpr));
     return by_types(a, [&](auto to, auto tg, auto al) {
-        token_sum_kernel<decltype(tg), decltype(to), al.value><<<grid, kSumThreads, 0, stream>>>(q);
-        const lmloss_status e = vocab_launch_err();
+        const lmloss_status e =
+            launch_after(token_sum_kernel<decltype(tg), decltype(to), al.value>, grid, kSumThreads, stream, q);
         if (e != LMLOSS_OK) return e;
-        token_join_kernel<decltype(to)><<<2 * h->num_sms, kJoinThreads, 0, stream>>>(q);
-        return vocab_launch_err();
+        return launch_after(token_join_kernel<decltype(to)>, dim3(static_cast<unsigned>(4 * h->num_sms)), kJoinThreads, stream, q);
     });
 }
 

@@ -61,12 +61,22 @@ struct Bf16 {
     static constexpr int kBytes = 2;
     __device__ static __forceinline__ float widen(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
     __device__ static __forceinline__ uint16_t round(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+    __device__ static __forceinline__ uint32_t round2(float lo, float hi)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
 };
 struct Fp16 {
     using raw = uint16_t;
     static constexpr int kBytes = 2;
     __device__ static __forceinline__ float widen(uint16_t b) { return __half2float(__ushort_as_half(b)); }
     __device__ static __forceinline__ uint16_t round(float x) { return __half_as_ushort(__float2half_rn(x)); }
+    __device__ static __forceinline__ uint32_t round2(float lo, float hi)
+    {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
 };
 struct Fp32 {
     using raw = uint32_t;
@@ -132,6 +142,20 @@ struct Pack {
             const uint32_t b = T::round(x);
             if (i & 1) w[i / 2] = (w[i / 2] & 0xffffu) | (b << 16);
             else w[i / 2] = (N > 1 ? (w[i / 2] & 0xffff0000u) : 0u) | b;
+        }
+    }
+    // all N elements, rounded in pairs
+    __device__ __forceinline__ void set_all(const float (&x)[N])
+    {
+        static_assert(N % 2 == 0, "pairs");
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            if constexpr (T::kBytes == 4) {
+                w[i] = __float_as_uint(x[i]);
+                w[i + 1] = __float_as_uint(x[i + 1]);
+            } else {
+                w[i / 2] = T::round2(x[i], x[i + 1]);
+            }
         }
     }
     __device__ __forceinline__ void zero()
