@@ -739,7 +739,7 @@ __device__ __forceinline__ void red_add4(float* p, float a, float b, float c, fl
 }
 
 template <class TG, class TO, bool ALIGNED>
-__global__ void __launch_bounds__(kSumThreads, ALIGNED ? 8 : 6) token_sum_kernel(const SumParams p)
+__global__ void __launch_bounds__(kSumThreads, !ALIGNED ? 6 : (TO::kBytes == 4 ? 5 : 8)) token_sum_kernel(const SumParams p)
 {
     constexpr int kAhead = TG::kBytes == 4 ? kRowsAhead / 2 : kRowsAhead;   // rows on their way
     __shared__ uint32_t key[kMaxGroups][kWindow + 2], row[kMaxGroups][kWindow];
@@ -883,18 +883,25 @@ __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const SumParam
         }
         return acc;
     };
-    auto write = [&](uint32_t v, int64_t c, float4 acc) {
-        const float total[4] = {acc.x, acc.y, acc.z, acc.w};
-        typename TO::raw* out = reinterpret_cast<typename TO::raw*>(at<TO>(e.table, v, e.ld_table, 0));
-        float old[4] = {0.f, 0.f, 0.f, 0.f};
+    struct Old {
+        float x[4];
+    };
+    auto read_old = [&](uint32_t v, int64_t c) {
+        const typename TO::raw* out = reinterpret_cast<const typename TO::raw*>(at<TO>(e.table, v, e.ld_table, 0));
+        Old o{{0.f, 0.f, 0.f, 0.f}};
         if (e.accumulate) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (c + j < e.D) old[j] = TO::widen(out[c + j]);
+                if (c + j < e.D) o.x[j] = TO::widen(out[c + j]);
         }
+        return o;
+    };
+    auto write = [&](uint32_t v, int64_t c, float4 acc, const Old& o) {
+        const float total[4] = {acc.x, acc.y, acc.z, acc.w};
+        typename TO::raw* out = reinterpret_cast<typename TO::raw*>(at<TO>(e.table, v, e.ld_table, 0));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c + j < e.D) out[c + j] = TO::round(e.accumulate ? fmaf(total[j], e.scale, old[j]) : total[j] * e.scale);
+            if (c + j < e.D) out[c + j] = TO::round(e.accumulate ? fmaf(total[j], e.scale, o.x[j]) : total[j] * e.scale);
     };
     // neighbouring items, likely of one long token, go to different blocks
     for (int64_t item0 = blockIdx.x; item0 < items; item0 += static_cast<int64_t>(gridDim.x) * kJoinWarps) {
@@ -902,17 +909,20 @@ __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const SumParam
         if (lane == 0) long_item[warp] = -1;
         if (item < items) {
             const int64_t w = __ldcg(p.crossing + item / ranges), c = (item % ranges) * kJoinCols + lane * 4;
-            const uint32_t v = __ldcg(p.keys + (w + 1) * p.window);
-            // windows after this one that begin with the token
+            // the windows after this one that begin with its last token
             int more = 0;
+            uint32_t v = 0;
             while (true) {
                 const int64_t next = (w + 1 + more + lane) * p.window;
-                const int n = __popc(__ballot_sync(0xffffffffu, next < e.T && __ldcg(p.keys + next) == v));
+                const uint32_t k = next < e.T ? __ldcg(p.keys + next) : static_cast<uint32_t>(e.V);
+                if (more == 0) v = __shfl_sync(0xffffffffu, k, 0);
+                const int n = __popc(__ballot_sync(0xffffffffu, k == v));
                 more += n;
                 if (n < 32) break;
             }
             if (more <= kJoinAlone) {
-                write(v, c, add(w, c, 0, more, 1));
+                const Old o = read_old(v, c);
+                write(v, c, add(w, c, 0, more, 1), o);
             } else if (lane == 0) {
                 long_item[warp] = item;
                 long_more[warp] = more;
@@ -933,7 +943,8 @@ __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const SumParam
                     acc.z += y.z;
                     acc.w += y.w;
                 }
-                write(__ldcg(p.keys + (w + 1) * p.window), c, acc);
+                const uint32_t v = __ldcg(p.keys + (w + 1) * p.window);
+                write(v, c, acc, read_old(v, c));
             }
             __syncthreads();
         }
@@ -1139,7 +1150,8 @@ lmloss_status sort_in_cluster(const lmloss_vocab_ctx* h, const lmloss_embedding_
     const int64_t row_bytes = a->D * float_bytes(a->table_dtype), while_sorting = (12 + a->T / 4700) * 5000000;
     // by the SMs that the cluster leaves
     q.fill = a->accumulate ? 0 : (h->num_sms - q.blocks) / q.blocks * q.blocks;
-    if (q.fill > 0) q.blind = std::min<int64_t>(a->V, while_sorting / row_bytes);
+    if (q.fill > 0) q.blind = while_sorting / row_bytes;
+    if (q.blind > a->V * 3 / 4) q.blind = a->V;   // little is left to be found out
     p.keys = q.keys;
     p.pos = q.pos;
     p.blind = q.blind;
@@ -1262,7 +1274,7 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
         const lmloss_status e =
             launch_after(token_sum_kernel<decltype(tg), decltype(to), al.value>, grid, kSumThreads, stream, q);
         if (e != LMLOSS_OK) return e;
-        return launch_after(token_join_kernel<decltype(to)>, dim3(static_cast<unsigned>(4 * h->num_sms)), kJoinThreads, stream, q);
+        return launch_after(token_join_kernel<decltype(to)>, dim3(static_cast<unsigned>(5 * h->num_sms)), kJoinThreads, stream, q);
     });
 }
 
