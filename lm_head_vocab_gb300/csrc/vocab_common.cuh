@@ -32,15 +32,17 @@ enum : int { kErrBadParent = 8 };
 
 struct VocabDeviceGuard {
     int prev = -1;
-    bool ok = true;
+    bool ok = true, moved = false;
     explicit VocabDeviceGuard(int dev)
     {
         if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+        if (prev == dev) return;
+        if (cudaSetDevice(dev) != cudaSuccess) ok = false;
+        else moved = true;
     }
     ~VocabDeviceGuard()
     {
-        if (prev >= 0) cudaSetDevice(prev);
+        if (moved) cudaSetDevice(prev);
     }
 };
 

@@ -19,28 +19,40 @@ _FLOATS = {torch.bfloat16: _lib.LMLOSS_BF16, torch.float32: _lib.LMLOSS_FP32, to
 _IDS = {torch.int64: _lib.LMLOSS_INT64, torch.int32: _lib.LMLOSS_INT32}
 
 
-def _check(t: torch.Tensor, name: str, dtype, shape, device):
+# a call's time on the host is a good part of a small call's: devices are compared by
+# number, and the current stream is asked for as a number
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _check(t: torch.Tensor, name: str, dtype, rows: int, cols: int, index: int):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+        raise ValueError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the handle on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the handle on cuda:{index}")
 
 
-def _matrix(t: torch.Tensor, name: str, device):
-    """(row stride) of a 2-d float tensor with unit column stride and rows that do not overlap."""
-    if t.dtype not in _FLOATS:
+def _matrix(t: torch.Tensor, name: str, index: int):
+    """(type, rows, columns, row stride) of a 2-d float tensor with unit column stride and
+    rows that do not overlap."""
+    dtype = _FLOATS.get(t.dtype)
+    if dtype is None:
         raise TypeError(f"{name}: must be bfloat16, float16 or float32, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the handle on {device}")
-    rows, cols = t.shape
-    if cols < 1 or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the handle on cuda:{index}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: must have two dimensions")
+    rows, cols = t.size(0), t.size(1)
+    ld, unit = t.stride()
+    if rows <= 1:
+        ld = cols
+    if cols < 1 or (cols > 1 and unit != 1) or ld < cols:
         raise ValueError(f"{name}: must have at least one column, unit column stride and a row stride of at least "
                          f"its columns")
-    return t.stride(0) if rows > 1 else cols
+    return dtype, rows, cols, ld
 
 
 @dataclass
@@ -72,6 +84,10 @@ class VocabOps:
         elif not isinstance(device, int):
             device = torch.device(device).index or 0
         self.device = torch.device("cuda", device)
+        self._index = device
+        lib = _lib.load()
+        self._forward, self._backward = lib.lmloss_embedding_forward, lib.lmloss_embedding_backward
+        self._step, self._reorder = lib.lmloss_beam_step, lib.lmloss_beam_reorder
         need = 0
         if max_tokens > 0:
             a = _lib.lmloss_embedding_args(T=max_tokens, V=max_vocab, D=max_dim, ld_table=max_dim, ld_rows=max_dim,
@@ -100,25 +116,27 @@ class VocabOps:
         return _lib.lmloss_vocab_get_device_error(self.handle)
 
     # ------------------------------------------------------------- streams
-    def _stream(self, stream, *tensors):
-        """(stream, context for allocations): on a stream that is not the current one the outputs
-        belong to it, and the caching allocator learns that it uses the inputs."""
-        cur = torch.cuda.current_stream(self.device)
-        if stream is None or stream == cur:
-            return cur.cuda_stream, contextlib.nullcontext()
+    def _enter(self, stream, *tensors):
+        """(stream, context for allocations) for a call on a stream of the caller's: where that is not
+        the current one the outputs belong to it, and the caching allocator learns that it uses the
+        inputs."""
+        if stream == torch.cuda.current_stream(self.device):
+            return stream.cuda_stream, contextlib.nullcontext()
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
         return stream.cuda_stream, torch.cuda.stream(stream)
 
     # ----------------------------------------------------------- embedding
-    def _ids(self, ids: torch.Tensor):
-        if ids.dtype not in _IDS:
+    def _ids(self, ids: torch.Tensor) -> int:
+        dtype = _IDS.get(ids.dtype)
+        if dtype is None:
             raise TypeError(f"ids: must be int64 or int32, got {ids.dtype}")
         if not ids.is_contiguous():
             raise ValueError("ids: must be contiguous")
-        if ids.device != self.device:
+        if ids.get_device() != self._index:
             raise ValueError(f"ids: on {ids.device}, the handle on {self.device}")
+        return dtype
 
     def embedding_forward(self, weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
                           out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
@@ -126,23 +144,29 @@ class VocabOps:
         """scale * weight[ids], [*ids.shape, D]: weight [V, D] and the result each
         bfloat16, float16 or float32 (the weight's type if not said).  An id of -100
         gives zeros; another outside [0, V) NaN and the error word."""
-        self._ids(ids)
-        if weight.dim() != 2:
-            raise ValueError("weight: must be [V, D]")
-        ld = _matrix(weight, "weight", self.device)
-        V, D = weight.shape
-        raw, ctx = self._stream(stream, weight, ids, out)
-        if out is None:
-            with ctx:
-                out = torch.empty(*ids.shape, D, dtype=out_dtype or weight.dtype, device=self.device)
-        elif out.shape != (*ids.shape, D) or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError(f"out: expected {(*ids.shape, D)}{'' if out_dtype is None else f' of {out_dtype}'}")
+        id_type = self._ids(ids)
+        w_type, V, D, ld = _matrix(weight, "weight", self._index)
+        if stream is None:
+            raw, ctx = _raw_stream(self._index), None
+        else:
+            raw, ctx = self._enter(stream, weight, ids, out)
         T = ids.numel()
+        shape = (T, D) if ids.dim() == 1 else (*ids.shape, D)
+        if out is None:
+            if out_dtype is None:
+                out_dtype = weight.dtype
+            if ctx is None:
+                out = torch.empty(shape, dtype=out_dtype, device=self.device)
+            else:
+                with ctx:
+                    out = torch.empty(shape, dtype=out_dtype, device=self.device)
+        elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out: expected {shape}{'' if out_dtype is None else f' of {out_dtype}'}")
         rows = out if out.dim() == 2 else out.view(T, D)
-        a = _lib.lmloss_embedding_args(ids.data_ptr(), T, V, D, weight.data_ptr(), ld, rows.data_ptr(),
-                                       _matrix(rows, "out", self.device), _IDS[ids.dtype], _FLOATS[weight.dtype],
-                                       _FLOATS[rows.dtype], scale, 0)
-        st = _lib.lmloss_embedding_forward(self.handle, a, raw)
+        r_type, _, _, ld_rows = _matrix(rows, "out", self._index)
+        a = _lib.lmloss_embedding_args(ids.data_ptr(), T, V, D, weight.data_ptr(), ld, rows.data_ptr(), ld_rows,
+                                       id_type, w_type, r_type, scale, 0)
+        st = self._forward(self.handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_embedding_forward")
         return out
@@ -156,25 +180,27 @@ class VocabOps:
         to the LM head: the head's own gradient is there already); without it one of
         num_embeddings rows in grad's type is made.  Sums run in fp32 in an order
         that the ids alone fix."""
-        self._ids(ids)
-        if grad.shape[:-1] != ids.shape or grad.dim() != ids.dim() + 1:
+        id_type = self._ids(ids)
+        if grad.shape[:-1] != ids.shape:
             raise ValueError(f"grad: expected [*{tuple(ids.shape)}, D], got {tuple(grad.shape)}")
-        T, D = ids.numel(), grad.shape[-1]
-        rows = grad if grad.dim() == 2 else grad.view(T, D)
-        ld = _matrix(rows, "grad", self.device)
-        raw, ctx = self._stream(stream, grad, ids, grad_weight)
+        T = ids.numel()
+        rows = grad if grad.dim() == 2 else grad.view(T, grad.shape[-1])
+        r_type, _, D, ld_rows = _matrix(rows, "grad", self._index)
+        if stream is None:
+            raw, ctx = _raw_stream(self._index), contextlib.nullcontext()
+        else:
+            raw, ctx = self._enter(stream, grad, ids, grad_weight)
         if grad_weight is None:
             if num_embeddings is None or accumulate:
                 raise ValueError("without grad_weight: num_embeddings and no accumulate")
             with ctx:
-                grad_weight = torch.empty(num_embeddings, D, dtype=grad.dtype, device=self.device)
-        elif grad_weight.dim() != 2 or grad_weight.shape[1] != D or num_embeddings not in (None, grad_weight.shape[0]):
+                grad_weight = torch.empty((num_embeddings, D), dtype=grad.dtype, device=self.device)
+        t_type, V, cols, ld = _matrix(grad_weight, "grad_weight", self._index)
+        if cols != D or num_embeddings not in (None, V):
             raise ValueError("grad_weight: must be [num_embeddings, D]")
-        a = _lib.lmloss_embedding_args(ids.data_ptr(), T, grad_weight.shape[0], D, grad_weight.data_ptr(),
-                                       _matrix(grad_weight, "grad_weight", self.device), rows.data_ptr(), ld,
-                                       _IDS[ids.dtype], _FLOATS[grad_weight.dtype], _FLOATS[rows.dtype], scale,
-                                       1 if accumulate else 0)
-        st = _lib.lmloss_embedding_backward(self.handle, a, raw)
+        a = _lib.lmloss_embedding_args(ids.data_ptr(), T, V, D, grad_weight.data_ptr(), ld, rows.data_ptr(), ld_rows,
+                                       id_type, t_type, r_type, scale, 1 if accumulate else 0)
+        st = self._backward(self.handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_embedding_backward")
         return grad_weight
@@ -196,45 +222,52 @@ class VocabOps:
         token."""
         if scores.dim() != 2:
             raise ValueError("scores: must be [B, K]")
-        dev = self.device
-        B, K = scores.shape
-        _check(scores, "scores", torch.float32, (B, K), dev)
-        if logits.dim() != 2 or logits.shape[0] != B * K:
+        dev, index = self.device, self._index
+        B, K = scores.size(0), scores.size(1)
+        _check(scores, "scores", torch.float32, B, K, index)
+        dtype, rows, V, ld = _matrix(logits, "logits", index)
+        if rows != B * K:
             raise ValueError(f"logits: must be [B * K, V] with B * K = {B * K}")
-        ld = _matrix(logits, "logits", dev)
-        V = logits.shape[1]
         M = K if num_candidates is None else num_candidates
         if not 1 <= M <= _lib.LMLOSS_MAX_BEAMS or not 1 <= K <= _lib.LMLOSS_MAX_BEAMS:
             raise ValueError(f"beams and candidates: 1 to {_lib.LMLOSS_MAX_BEAMS}, got {K} and {M}")
-        if finished is not None:
-            _check(finished, "finished", torch.uint8, (B, K), dev)
-        if lengths is not None:
-            _check(lengths, "lengths", torch.int32, (B, K), dev)
+        fin = length = mask = None
         stride = 0
+        if finished is not None:
+            _check(finished, "finished", torch.uint8, B, K, index)
+            fin = finished.data_ptr()
+        if lengths is not None:
+            _check(lengths, "lengths", torch.int32, B, K, index)
+            length = lengths.data_ptr()
         if token_mask is not None:
             words = (V + 31) // 32
-            if token_mask.dim() != 2 or token_mask.shape[0] not in (1, B * K):
+            if token_mask.dim() != 2 or token_mask.size(0) not in (1, B * K):
                 raise ValueError(f"token_mask: must be [{B * K} or 1, {words}]")
-            _check(token_mask, "token_mask", torch.int32, (token_mask.shape[0], words), dev)
-            stride = 0 if token_mask.shape[0] == 1 else words
-        raw, ctx = self._stream(stream, logits, scores, finished, lengths, token_mask)
-        with ctx:
-            r = BeamStep(torch.empty((B, M), dtype=torch.float32, device=dev),
-                         torch.empty((B, M), dtype=torch.int32, device=dev),
-                         torch.empty((B, M), dtype=torch.int64, device=dev),
-                         torch.empty((B, K), dtype=torch.float32, device=dev),
-                         torch.empty((B, M), dtype=torch.uint8, device=dev),
-                         None if lengths is None else torch.empty((B, M), dtype=torch.int32, device=dev))
-        a = _lib.lmloss_beam_args(logits.data_ptr(), B, V, ld, K, M, _FLOATS[logits.dtype], length_penalty, eos_token,
-                                  scores.data_ptr(), None if finished is None else finished.data_ptr(),
-                                  None if lengths is None else lengths.data_ptr(),
-                                  None if token_mask is None else token_mask.data_ptr(), stride,
+            _check(token_mask, "token_mask", torch.int32, token_mask.size(0), words, index)
+            mask = token_mask.data_ptr()
+            stride = 0 if token_mask.size(0) == 1 else words
+        if stream is None:
+            raw, r = _raw_stream(index), self._beam_out(B, K, M, dev, lengths is not None)
+        else:
+            raw, ctx = self._enter(stream, logits, scores, finished, lengths, token_mask)
+            with ctx:
+                r = self._beam_out(B, K, M, dev, lengths is not None)
+        a = _lib.lmloss_beam_args(logits.data_ptr(), B, V, ld, K, M, dtype, length_penalty, eos_token,
+                                  scores.data_ptr(), fin, length, mask, stride,
                                   r.scores.data_ptr(), r.parents.data_ptr(), r.tokens.data_ptr(), r.lse.data_ptr(),
-                                  r.finished.data_ptr(), None if lengths is None else r.lengths.data_ptr())
-        st = _lib.lmloss_beam_step(self.handle, a, raw)
+                                  r.finished.data_ptr(), None if length is None else r.lengths.data_ptr())
+        st = self._step(self.handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_beam_step")
         return r
+
+    @staticmethod
+    def _beam_out(B, K, M, dev, lengths):
+        empty, f32, i32, shape = torch.empty, torch.float32, torch.int32, (B, M)
+        return BeamStep(empty(shape, dtype=f32, device=dev), empty(shape, dtype=i32, device=dev),
+                        empty(shape, dtype=torch.int64, device=dev), empty((B, K), dtype=f32, device=dev),
+                        empty(shape, dtype=torch.uint8, device=dev),
+                        empty(shape, dtype=i32, device=dev) if lengths else None)
 
     def beam_reorder(self, states: Sequence[torch.Tensor], parents: torch.Tensor, *,
                      out: Union[None, str, Sequence[torch.Tensor]] = None, dim: int = 0,
@@ -248,18 +281,21 @@ class VocabOps:
         Otherwise out must not overlap the states."""
         if parents.dim() != 2:
             raise ValueError("parents: must be [B, K_out]")
-        B, Ko = parents.shape
-        _check(parents, "parents", torch.int32, (B, Ko), self.device)
+        B, Ko = parents.size(0), parents.size(1)
+        _check(parents, "parents", torch.int32, B, Ko, self._index)
         if not states:
             return []
-        rows = states[0].shape[dim]
+        rows = states[0].size(dim)
         if B == 0 or rows % B:
             raise ValueError(f"states: {rows} rows along dim {dim} for {B} sequences")
         K = rows // B
         if not 1 <= Ko <= _lib.LMLOSS_MAX_BEAMS or not 1 <= K <= _lib.LMLOSS_MAX_BEAMS:
             raise ValueError(f"beams: 1 to {_lib.LMLOSS_MAX_BEAMS} a sequence, got {K} and {Ko}")
-        named = out if isinstance(out, (list, tuple)) else ()
-        raw, ctx = self._stream(stream, parents, *states, *named)
+        if stream is None:
+            raw, ctx = _raw_stream(self._index), contextlib.nullcontext()
+        else:
+            named = out if isinstance(out, (list, tuple)) else ()
+            raw, ctx = self._enter(stream, parents, *states, *named)
         if out is None:
             with ctx:
                 out = [torch.empty([B * Ko if i == dim % t.dim() else n for i, n in enumerate(t.shape)], dtype=t.dtype,
@@ -270,37 +306,36 @@ class VocabOps:
             out = list(states)
         elif len(out) != len(states):
             raise ValueError("out: as many tensors as states")
-        arr = (_lib.lmloss_beam_state * len(states))()
-        for s, t, o in zip(arr, states, out):
-            self._describe(s, t, o, dim, rows, B * Ko)
-        st = _lib.lmloss_beam_reorder(self.handle, arr, parents.data_ptr(), B, K, Ko, raw)
+        n = len(states)
+        arr = (_lib.lmloss_beam_state * n)(*[self._describe(t, o, dim, rows, B * Ko) for t, o in zip(states, out)])
+        st = self._reorder(self.handle, arr, n, parents.data_ptr(), B, K, Ko, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_beam_reorder")
         return list(out)
 
-    def _describe(self, s, t: torch.Tensor, o: torch.Tensor, dim: int, rows: int, rows_out: int):
-        """Fill one lmloss_beam_state: the dimensions that both sides keep contiguous become the run,
-        the rest outer counts."""
-        if t.device != self.device or o.device != self.device:
+    def _describe(self, t: torch.Tensor, o: torch.Tensor, dim: int, rows: int, rows_out: int):
+        """One state's lmloss_beam_state: the dimensions that both sides keep contiguous become the
+        run, the rest outer counts."""
+        if t.get_device() != self._index or o.get_device() != self._index:
             raise ValueError(f"states: on {t.device} and {o.device}, the handle on {self.device}")
         if t.dtype != o.dtype:
             raise TypeError(f"out: {o.dtype} for a state of {t.dtype}")
-        d = dim % t.dim()
-        want = list(t.shape)
-        if want[d] != rows:
-            raise ValueError(f"states: {want[d]} and {rows} rows along dim {dim}")
-        want[d] = rows_out
-        if list(o.shape) != want:
-            raise ValueError(f"out: expected shape {want}, got {list(o.shape)}")
+        shape, oshape, ts, os_ = t.shape, o.shape, t.stride(), o.stride()
+        d = dim if dim >= 0 else dim + len(shape)
+        if shape[d] != rows:
+            raise ValueError(f"states: {shape[d]} and {rows} rows along dim {dim}")
+        if len(oshape) != len(shape) or oshape[d] != rows_out:
+            raise ValueError(f"out: {tuple(oshape)} for a state of {tuple(shape)} and {rows_out} rows")
         es = t.element_size()
-        ts, os_ = t.stride(), o.stride()
         dims = []
-        for i, n in enumerate(t.shape):
+        for i, n in enumerate(shape):
             if i == d:
                 continue
-            if n > 1 and os_[i] == 0:
-                raise ValueError("out: must not overlap itself")
+            if oshape[i] != n:
+                raise ValueError(f"out: {tuple(oshape)} for a state of {tuple(shape)} and {rows_out} rows")
             if n != 1:
+                if os_[i] == 0:
+                    raise ValueError("out: must not overlap itself")
                 dims.append((os_[i], ts[i], n))
         dims.sort()
         run, outer = 1, []
@@ -315,13 +350,8 @@ class VocabOps:
                 outer.append((so, si, n))
         if len(outer) > 3:
             raise ValueError("states: more than three strided dimensions beside the rows")
-        s.src = t.data_ptr()
-        s.dst = o.data_ptr()
-        s.inner = run * es
-        s.src_row_stride = ts[d] * es
-        s.dst_row_stride = os_[d] * es
-        for k in range(3):
-            so, si, n = outer[k] if k < len(outer) else (0, 0, 1)
-            s.outer[k] = n
-            s.src_outer_stride[k] = si * es
-            s.dst_outer_stride[k] = so * es
+        while len(outer) < 3:
+            outer.append((0, 0, 1))
+        (s0, r0, n0), (s1, r1, n1), (s2, r2, n2) = outer
+        return _lib.lmloss_beam_state(t.data_ptr(), o.data_ptr(), run * es, ts[d] * es, os_[d] * es, (n0, n1, n2),
+                                      (r0 * es, r1 * es, r2 * es), (s0 * es, s1 * es, s2 * es))
