@@ -12,6 +12,8 @@ namespace {
 constexpr int kMaxK = LMLOSS_MAX_BEAMS;
 constexpr int kThreads = 128;
 constexpr int kStates = 16;                  // states of one launch
+constexpr int kColumns = 4;                  // units a thread moves of each run
+constexpr int kMoves = 8;                    // runs on their way at a time
 
 struct State {
     const unsigned char* src;
@@ -19,9 +21,9 @@ struct State {
     int64_t src_row, dst_row;
     int64_t src_outer[3], dst_outer[3];
     int64_t units;               // of a run
-    int64_t chunks;              // blocks over a run
-    int64_t first;               // first block of this state in the launch
-    int outer[3];
+    unsigned chunks;             // blocks over a run
+    unsigned first;              // first block of this state in the launch
+    unsigned outer[3];
     int unit;                    // bytes moved at a time: 16, 8, 4, 2 or 1
     int in_place;
 };
@@ -34,61 +36,121 @@ struct ReorderParams {
     int* err;
 };
 
-// The runs of one outer index and sequence, columns [u0, u0 + kThreads) in units.
-template <class U>
-__device__ void move_runs(const ReorderParams& p, const State& st, const int* parent, int b, int64_t o, int64_t u0,
-                          unsigned char* stage)
+// What a block moves: runs from and to these byte offsets.
+struct Moves {
+    int64_t src[kMaxK], dst[kMaxK];
+    int n;
+};
+
+// C columns of at most kMoves / C runs, all on their way at once.
+template <class U, int C>
+__device__ __forceinline__ void move_few(const Moves& mv, const unsigned char* src, unsigned char* dst, int64_t u0, int64_t units)
 {
-    const int64_t o2 = o % st.outer[2], o1 = o / st.outer[2] % st.outer[1], o0 = o / st.outer[2] / st.outer[1];
-    const int64_t u = u0 + threadIdx.x;
-    const bool in = u < st.units;
-    const unsigned char* src = st.src + static_cast<int64_t>(b) * p.K * st.src_row + o0 * st.src_outer[0] +
-                               o1 * st.src_outer[1] + o2 * st.src_outer[2] + u * sizeof(U);
-    unsigned char* dst = st.dst + static_cast<int64_t>(b) * p.K_out * st.dst_row + o0 * st.dst_outer[0] +
-                         o1 * st.dst_outer[1] + o2 * st.dst_outer[2] + u * sizeof(U);
-    if (!in) return;
-    if (!st.in_place) {
-        for (int m = 0; m < p.K_out; ++m)
-            if (parent[m] >= 0)
-                *reinterpret_cast<U*>(dst + m * st.dst_row) = *reinterpret_cast<const U*>(src + parent[m] * st.src_row);
-        return;
+    constexpr int N = kMoves / C;
+    const int n = mv.n;
+#pragma unroll 1
+    for (int x = 0; x < kColumns; x += C) {
+        const int64_t u = u0 + x * kThreads + threadIdx.x;
+        U v[C][N];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < n && u + c * kThreads < units)
+                    v[c][j] = *reinterpret_cast<const U*>(src + (u + c * kThreads) * sizeof(U) + mv.src[j]);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < n && u + c * kThreads < units)
+                    *reinterpret_cast<U*>(dst + (u + c * kThreads) * sizeof(U) + mv.dst[j]) = v[c][j];
     }
-    // every beam that another slot takes is read before any slot is written; a
-    // thread reads and writes its own columns only
-    U* own = reinterpret_cast<U*>(stage) + threadIdx.x;
-    for (int m = 0; m < p.K_out; ++m)
-        if (parent[m] >= 0 && parent[m] != m)
-            own[m * kThreads] = *reinterpret_cast<const U*>(src + parent[m] * st.src_row);
-    for (int m = 0; m < p.K_out; ++m)
-        if (parent[m] >= 0 && parent[m] != m) *reinterpret_cast<U*>(dst + m * st.dst_row) = own[m * kThreads];
+}
+
+// Units [u0, u0 + kThreads * kColumns) of the runs.  A thread reads and writes its own
+// columns only.  In place, every run that another slot takes is read before any slot is
+// written: in registers where there are few, else through shared memory.
+template <class U>
+__device__ __forceinline__ void move_runs(const Moves& mv, const unsigned char* src, unsigned char* dst, int64_t u0,
+                                          int64_t units, bool in_place, unsigned char* stage)
+{
+    const int n = mv.n;
+    if (n <= 2) return move_few<U, 4>(mv, src, dst, u0, units);
+    if (n <= 4) return move_few<U, 2>(mv, src, dst, u0, units);
+    if (n <= kMoves) return move_few<U, 1>(mv, src, dst, u0, units);
+#pragma unroll 1
+    for (int x = 0; x < kColumns; ++x) {
+        const int64_t u = u0 + x * kThreads + threadIdx.x;
+        if (u >= units) return;
+        const unsigned char* from = src + u * sizeof(U);
+        unsigned char* to = dst + u * sizeof(U);
+        if (in_place) {
+            U* own = reinterpret_cast<U*>(stage) + threadIdx.x;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) own[j * kThreads] = *reinterpret_cast<const U*>(from + mv.src[j]);
+            for (int j = 0; j < n; ++j) *reinterpret_cast<U*>(to + mv.dst[j]) = own[j * kThreads];
+            continue;
+        }
+        for (int j0 = 0; j0 < n; j0 += kMoves) {
+            U v[kMoves];
+#pragma unroll
+            for (int j = 0; j < kMoves; ++j)
+                if (j0 + j < n) v[j] = *reinterpret_cast<const U*>(from + mv.src[j0 + j]);
+#pragma unroll
+            for (int j = 0; j < kMoves; ++j)
+                if (j0 + j < n) *reinterpret_cast<U*>(to + mv.dst[j0 + j]) = v[j];
+        }
+    }
 }
 
 __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_constant__ ReorderParams p)
 {
     extern __shared__ __align__(16) unsigned char stage[];   // [K][kThreads] units, in place only
-    __shared__ int parent[kMaxK];
+    __shared__ Moves mv;
     int i = 0;
     while (i + 1 < p.n && blockIdx.x >= p.st[i + 1].first) ++i;
     const State& st = p.st[i];
-    int64_t k = blockIdx.x - st.first;
-    const int64_t chunk = k % st.chunks;
+    unsigned k = blockIdx.x - st.first;
+    const unsigned chunk = k % st.chunks;
     k /= st.chunks;
-    const int b = static_cast<int>(k % p.B);
-    const int64_t o = k / p.B;
-    for (int m = threadIdx.x; m < p.K_out; m += kThreads) {
-        const int q = p.parents[static_cast<int64_t>(b) * p.K_out + m];
-        const bool ok = q >= 0 && q < p.K;
-        if (!ok) set_error(p.err, kErrBadParent);
-        parent[m] = ok ? q : -1;
+    const unsigned b = k % static_cast<unsigned>(p.B);
+    const unsigned o = k / static_cast<unsigned>(p.B);
+    const unsigned o2 = o % st.outer[2], o1 = o / st.outer[2] % st.outer[1], o0 = o / st.outer[2] / st.outer[1];
+    if (threadIdx.x < 32) {
+        // the slots that something is moved to, in order
+        int n = 0;
+        for (int m0 = 0; m0 < p.K_out; m0 += 32) {
+            const int m = m0 + static_cast<int>(threadIdx.x);
+            bool moved = false;
+            int q = 0;
+            if (m < p.K_out) {
+                q = p.parents[static_cast<int64_t>(b) * p.K_out + m];
+                moved = q >= 0 && q < p.K;
+                if (!moved) set_error(p.err, kErrBadParent);
+                if (st.in_place && q == m) moved = false;
+            }
+            const unsigned who = __ballot_sync(0xffffffffu, moved);
+            if (moved) {
+                const int at = n + __popc(who & ((1u << threadIdx.x) - 1u));
+                mv.src[at] = q * st.src_row;
+                mv.dst[at] = m * st.dst_row;
+            }
+            n += __popc(who);
+        }
+        if (threadIdx.x == 0) mv.n = n;
     }
     __syncthreads();
-    const int64_t u0 = chunk * kThreads;
+    const unsigned char* src = st.src + static_cast<int64_t>(b) * p.K * st.src_row + o0 * st.src_outer[0] +
+                               o1 * st.src_outer[1] + o2 * st.src_outer[2];
+    unsigned char* dst = st.dst + static_cast<int64_t>(b) * p.K_out * st.dst_row + o0 * st.dst_outer[0] +
+                         o1 * st.dst_outer[1] + o2 * st.dst_outer[2];
+    const int64_t u0 = static_cast<int64_t>(chunk) * (kThreads * kColumns);
     switch (st.unit) {
-    case 16: move_runs<uint4>(p, st, parent, b, o, u0, stage); break;
-    case 8: move_runs<uint2>(p, st, parent, b, o, u0, stage); break;
-    case 4: move_runs<uint32_t>(p, st, parent, b, o, u0, stage); break;
-    case 2: move_runs<uint16_t>(p, st, parent, b, o, u0, stage); break;
-    default: move_runs<uint8_t>(p, st, parent, b, o, u0, stage); break;
+    case 16: move_runs<uint4>(mv, src, dst, u0, st.units, st.in_place, stage); break;
+    case 8: move_runs<uint2>(mv, src, dst, u0, st.units, st.in_place, stage); break;
+    case 4: move_runs<uint32_t>(mv, src, dst, u0, st.units, st.in_place, stage); break;
+    case 2: move_runs<uint16_t>(mv, src, dst, u0, st.units, st.in_place, stage); break;
+    default: move_runs<uint8_t>(mv, src, dst, u0, st.units, st.in_place, stage); break;
     }
 }
 
@@ -176,7 +238,7 @@ lmloss_status lmloss_beam_reorder(lmloss_vocab_handle h, const lmloss_beam_state
     for (int i = 0; i < n; ++i) {
         const lmloss_beam_state& s = states[i];
         if (empty(s)) continue;
-        const __int128 blocks = static_cast<__int128>((s.inner / unit_of(s) + kThreads - 1) / kThreads) * B *
+        const __int128 blocks = static_cast<__int128>((s.inner / unit_of(s) + kThreads * kColumns - 1) / (kThreads * kColumns)) * B *
                                 s.outer[0] * s.outer[1] * s.outer[2];
         if (blocks > INT_MAX / kStates) return LMLOSS_ERR_UNSUPPORTED;
     }
@@ -200,17 +262,17 @@ lmloss_status lmloss_beam_reorder(lmloss_vocab_handle h, const lmloss_beam_state
             d.src_row = s.src_row_stride;
             d.dst_row = s.dst_row_stride;
             for (int k = 0; k < 3; ++k) {
-                d.outer[k] = static_cast<int>(s.outer[k]);
+                d.outer[k] = static_cast<unsigned>(s.outer[k]);
                 d.src_outer[k] = s.src_outer_stride[k];
                 d.dst_outer[k] = s.dst_outer_stride[k];
             }
             d.unit = unit_of(s);
             d.units = s.inner / d.unit;
-            d.chunks = (d.units + kThreads - 1) / kThreads;
+            d.chunks = static_cast<unsigned>((d.units + kThreads * kColumns - 1) / (kThreads * kColumns));
             d.in_place = s.src == s.dst;
-            staged = staged || d.in_place;
-            d.first = blocks;
-            blocks += d.chunks * B * s.outer[0] * s.outer[1] * s.outer[2];
+            staged = staged || (d.in_place && K > kMoves);
+            d.first = static_cast<unsigned>(blocks);
+            blocks += static_cast<int64_t>(d.chunks) * B * s.outer[0] * s.outer[1] * s.outer[2];
         }
         if (blocks == 0) continue;
         size_t smem = staged ? static_cast<size_t>(K) * kThreads * 16 : 0;

@@ -1216,7 +1216,8 @@ lmloss_status lmloss_embedding_forward(lmloss_vocab_handle h, const lmloss_embed
     if (!g.ok) return LMLOSS_ERR_CUDA;
     const EmbParams p = params(h, a);
     return by_types(a, [&](auto tw, auto to, auto aligned) {
-        const int tpr = threads_of_row(row_vectors(a, a->rows_dtype, aligned.value), kFwdThreads), rows = kFwdThreads / tpr;
+        const int64_t vecs = row_vectors(a, a->rows_dtype, aligned.value);
+        const int tpr = threads_of_row((vecs + kFwdUnroll - 1) / kFwdUnroll, kFwdThreads), rows = kFwdThreads / tpr;
         embedding_forward_kernel<decltype(tw), decltype(to), aligned.value>
             <<<static_cast<unsigned>((p.T + rows - 1) / rows), kFwdThreads, 0, stream>>>(p, tpr);
         return vocab_launch_err();
