@@ -398,7 +398,7 @@ typedef struct {
     int32_t K;                   /* beams of a sequence, 1 .. LMLOSS_MAX_BEAMS             */
     int32_t M;                   /* candidates wanted, 1 .. LMLOSS_MAX_BEAMS               */
     int32_t dtype;               /* lmloss_dtype, any of the three                         */
-    float length_penalty;        /* alpha >= 0 (0 without lengths): candidates are ranked  */
+    double length_penalty;       /* alpha >= 0 (0 without lengths): candidates are ranked  */
                                  /* by score / length^alpha                                */
     int64_t eos_token;           /* the end token, -1 = none (not with `finished`)         */
     const float* scores;         /* [B, K] summed log-probability of each beam             */

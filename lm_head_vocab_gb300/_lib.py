@@ -157,7 +157,7 @@ class lmloss_beam_args(ctypes.Structure):
         ("K", ctypes.c_int32),
         ("M", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
-        ("length_penalty", ctypes.c_float),
+        ("length_penalty", ctypes.c_double),
         ("eos_token", ctypes.c_int64),
         ("scores", ctypes.c_void_p),
         ("finished", ctypes.c_void_p),

@@ -24,7 +24,6 @@ constexpr int kCap = 1024;                   // candidate keys of a part held at
 constexpr int kHits = 1024;                  // vectors of a part that reach its first threshold
 constexpr int kSmall = 256;                  // few enough to be ranked by counting
 constexpr int kFinal = 512;                  // candidates of a sequence held at once
-constexpr int kEntries = 8;                  // entries a thread holds when a sequence has few
 constexpr int kDepths = 8;                   // lists (parts of a sequence's rows) a thread
 constexpr int kMaxLists = kDepths * kThreads;
 
@@ -34,7 +33,7 @@ struct BeamParams {
     int B, K, M, V;
     int slices;                  // parts of a row
     int tiles;                   // tiles of a part
-    float alpha;
+    double alpha;
     int64_t eos;
     const float* scores;
     const uint8_t* finished;
@@ -129,6 +128,9 @@ __device__ __forceinline__ void rank_groups(uint32_t v, int M, uint32_t* group, 
     if (above == M - 1 && mine) *thr = mine;
 }
 
+// of a row: has candidates, goes on as it is, has none
+enum : uint8_t { kAlive = 0, kFinished = 1, kOut = 2 };
+
 struct __align__(16) Shared {
     uint64_t buf[kCap];                      // a part's candidates
     union {
@@ -150,7 +152,8 @@ struct __align__(16) Shared {
     // of a sequence's rows
     double base[kMaxM], norm[kMaxM];
     float base_f[kMaxM], inv_f[kMaxM];
-    uint8_t done[kMaxM];
+    float row_m[kMaxM], row_hi[kMaxM], row_lo[kMaxM];
+    uint8_t state[kMaxM];
     // the slow way of picking
     uint64_t wbest[kWarps], wplace[kWarps];
     int wlist[kWarps];
@@ -160,9 +163,9 @@ struct __align__(16) Shared {
 // A candidate's score and rank key in fp64; false where it is none.
 __device__ __forceinline__ bool exact_score(const BeamParams& p, const Shared& sm, int k, float z, uint64_t& rank)
 {
-    const double score = sm.done[k] ? sm.base[k] : sm.base[k] + static_cast<double>(z);
+    const double score = sm.state[k] == kFinished ? sm.base[k] : sm.base[k] + static_cast<double>(z);
     if (!isfinite(score)) return false;
-    rank = ordered64(p.alpha != 0.f ? score / sm.norm[k] : score);
+    rank = ordered64(p.alpha != 0.0 ? score / sm.norm[k] : score);
     return true;
 }
 
@@ -172,14 +175,14 @@ __device__ __forceinline__ uint64_t entry_key(const BeamParams& p, const Shared&
 {
     const int per = p.M * p.slices;
     k = static_cast<int>(e) / per;
-    if (sm.done[k]) return e == static_cast<int64_t>(k) * per ? 1 : 0;
+    if (sm.state[k] == kFinished) return e == static_cast<int64_t>(k) * per ? 1 : 0;
     return __ldcg(p.keys + r0 * per + e);
 }
 
 __device__ __forceinline__ void write_pick(const BeamParams& p, const Shared& sm, int b, int out, int k, float z, int token)
 {
     const int64_t o = static_cast<int64_t>(b) * p.M + out, r = static_cast<int64_t>(b) * p.K + k;
-    const bool done = sm.done[k];
+    const bool done = sm.state[k] == kFinished;
     const int64_t t = done ? p.eos : token;
     p.scores_out[o] = static_cast<float>(done ? sm.base[k] : sm.base[k] + static_cast<double>(z));
     p.parents_out[o] = k;
@@ -226,7 +229,7 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
                 const uint64_t key = head(i, d, k);
                 uint64_t cr;
                 if (key == 0 || !exact_score(p, sm, k, key_logit(key), cr)) continue;
-                const uint64_t cp = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.done[k] ? 0 : key_col(key));
+                const uint64_t cp = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.state[k] == kFinished ? 0 : key_col(key));
                 if (cr > rank || (cr == rank && cp < place)) {
                     rank = cr;
                     place = cp;
@@ -296,67 +299,68 @@ __device__ __forceinline__ double log_of_sum(float hi, float lo)
            static_cast<double>(2.f * fmaf(q, t, rest));
 }
 
+// n^a for n >= 1 and a > 0, to about 1e-9: e^(a ln n) = 2^i e^r with |r| <= ln 2 / 2, the
+// series' terms from r^3 on in fp32.
+__device__ __forceinline__ double power(int n, double a)
+{
+    if (a == 1.0) return static_cast<double>(n);
+    const float hi = static_cast<float>(n);
+    const double y = a * log_of_sum(hi, static_cast<float>(n - static_cast<int64_t>(hi)));
+    const float i = rintf(static_cast<float>(y) * kLog2e);
+    if (!(i < 1000.f)) return pow(static_cast<double>(n), a);   // near the range's end
+    const double r = fma(static_cast<double>(i), -0.693147180559945309417, y);
+    const float f = static_cast<float>(r);
+    const float tail = f * f * f * fmaf(f, fmaf(f, fmaf(f, fmaf(f, 1.f / 5040, 1.f / 720), 1.f / 120), 1.f / 24), 1.f / 6);
+    const double e = 1.0 + (r + (0.5 * r * r + static_cast<double>(tail)));
+    return e * __longlong_as_double((static_cast<long long>(i) + 1023LL) << 52);
+}
+
 // The block that finishes a sequence's last part picks its M best.
 __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.K, M = p.M, S = p.slices;
     const int64_t r0 = static_cast<int64_t>(b) * K;
-    const int per = M * S, total = K * per;
+    const int lists = K * S;   // one a row and part, best first
 
-    // with few entries all of them are read at once, under the way of the rows' sums
-    const bool few = total <= kEntries * kThreads;
-    uint64_t held[kEntries];
-#pragma unroll
-    for (int j = 0; j < kEntries; ++j) {
-        const int e = tid + j * kThreads;
-        held[j] = few && e < total ? __ldcg(p.keys + r0 * per + e) : 0;
-    }
+    // The first candidates of the lists, as many of each as give every thread one, are
+    // read under the way of the rows' sums.
+    const int depths = lists < kThreads ? min(M, kThreads / lists) : 1;
+    const int list0 = tid / depths, depth0 = tid - list0 * depths;
+    auto key_at = [&](int list, int d) {
+        const int k = list / S;
+        return __ldcg(p.keys + ((r0 + k) * M + d) * S + (list - k * S));
+    };
+    uint64_t key0 = list0 < lists ? key_at(list0, depth0) : 0;
 
     // ---- the rows' normalisers: the parts' sums are added as pairs of fp32, an
-    // error-free sum and what it leaves
+    // error-free sum and what it leaves; then one thread a row goes on (fp64 is slow on
+    // this GPU, and slower when several warps want it)
+#pragma unroll 1
     for (int k = warp; k < K; k += kWarps) {
         const int64_t r = r0 + k;
         const float2 q0 = lane < S ? __ldcg(&p.stats[r * S + lane]) : make_float2(-INFINITY, 0.f);
-        const bool done = p.finished && p.finished[r];
-        const float score = p.scores[r];
-        const int len0 = p.lengths ? p.lengths[r] : 0;
-        double lse = 0.0;
-        if (!done) {
-            float m = q0.x, hi = 0.f, lo = 0.f;
-            for (int s = lane + 32; s < S; s += 32) m = fmaxf(m, __ldcg(&p.stats[r * S + s]).x);
-            m = warp_max(m);
-            auto add = [&](float x, float e) {
-                const float t = hi + x, v = t - hi;
-                lo += ((hi - (t - v)) + (x - v)) + e;
-                hi = t;
-            };
-            // an empty part (-inf, 0) adds nothing; NaN stays
-            auto part = [&](float2 q) { return q.x == m ? q.y : q.y * exp2f((q.x - m) * kLog2e); };
-            add(part(q0), 0.f);
-            for (int s = lane + 32; s < S; s += 32) add(part(__ldcg(&p.stats[r * S + s])), 0.f);
-            for (int o = 16; o > 0; o >>= 1) {
-                const float x = __shfl_xor_sync(0xffffffffu, hi, o), e = __shfl_xor_sync(0xffffffffu, lo, o);
-                add(x, e);
-            }
-            lse = m == -INFINITY && hi == 0.f ? -INFINITY : static_cast<double>(m) + log_of_sum(hi, lo);
+        float m = q0.x, hi = 0.f, lo = 0.f;
+        for (int s = lane + 32; s < S; s += 32) m = fmaxf(m, __ldcg(&p.stats[r * S + s]).x);
+        m = warp_max(m);
+        auto add = [&](float x, float e) {
+            const float t = hi + x, v = t - hi;
+            lo += ((hi - (t - v)) + (x - v)) + e;
+            hi = t;
+        };
+        // an empty part (-inf, 0) adds nothing; NaN stays
+        auto part = [&](float2 q) { return q.x == m ? q.y : q.y * exp2f((q.x - m) * kLog2e); };
+        add(part(q0), 0.f);
+        for (int s = lane + 32; s < S; s += 32) add(part(__ldcg(&p.stats[r * S + s])), 0.f);
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, hi, o), e = __shfl_xor_sync(0xffffffffu, lo, o);
+            add(x, e);
         }
         if (lane == 0) {
-            if (p.lse_out) p.lse_out[r] = static_cast<float>(lse);
-            const double base = static_cast<double>(score) - lse;
-            double d = 1.0;
-            float inv = 1.f;
-            if (p.alpha != 0.f) {
-                const int64_t len = static_cast<int64_t>(len0) + (done ? 0 : 1);
-                d = static_cast<double>(len < 1 ? 1 : len);
-                if (p.alpha != 1.f) d = pow(d, static_cast<double>(p.alpha));
-                inv = 1.f / static_cast<float>(d);
-            }
-            sm.base[k] = base;
-            sm.norm[k] = d;
-            sm.base_f[k] = static_cast<float>(base);
-            sm.inv_f[k] = inv;
-            sm.done[k] = done ? 1 : 0;
+            sm.row_m[k] = m;
+            sm.row_hi[k] = hi;
+            sm.row_lo[k] = lo;
         }
     }
     if (tid == 0) {
@@ -365,102 +369,115 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
         sm.thr = 0;
         sm.thr_end = 0;
     }
+    const int own = min(tid, K - 1);
+    const bool own_done = p.finished && p.finished[r0 + own];
+    const float own_score = p.scores[r0 + own];
+    const int own_len = p.lengths ? p.lengths[r0 + own] : 0;
+    __syncthreads();
+    if (tid < K) {
+        double lse = 0.0;
+        if (!own_done) {
+            const float m = sm.row_m[tid], hi = sm.row_hi[tid];
+            lse = m == -INFINITY && hi == 0.f ? -INFINITY : static_cast<double>(m) + log_of_sum(hi, sm.row_lo[tid]);
+        }
+        if (p.lse_out) p.lse_out[r0 + tid] = static_cast<float>(lse);
+        const double base = static_cast<double>(own_score) - lse;
+        double d = 1.0;
+        float inv = 1.f;
+        if (p.alpha != 0.0) {
+            const int64_t len = static_cast<int64_t>(own_len) + (own_done ? 0 : 1);
+            d = power(static_cast<int>(min(max(len, int64_t(1)), int64_t(0x7fffffff))), p.alpha);
+            inv = 1.f / static_cast<float>(d);
+        }
+        sm.base[tid] = base;
+        sm.norm[tid] = d;
+        sm.base_f[tid] = static_cast<float>(base);
+        sm.inv_f[tid] = inv;
+        sm.state[tid] = own_done ? kFinished : (isfinite(base) ? kAlive : kOut);
+    }
     __syncthreads();
 
     // ---- a threshold in fp32.  Each candidate's rank key lies within `err` of its
     // fp32 value: at most six roundings of 2^-24 of the terms.
     auto bounds = [&](int k, uint64_t key, float& low, float& high) {
-        const float z = sm.done[k] ? 0.f : key_logit(key);
-        const float x = (sm.base_f[k] + z) * sm.inv_f[k];
-        const float err = (fabsf(sm.base_f[k]) + fabsf(z)) * sm.inv_f[k] * 4.8e-7f + 1e-37f;
-        low = x - err;
-        high = x + err;
-        if (!(fabsf(x) < INFINITY && err < INFINITY)) {
-            low = -INFINITY;
-            high = INFINITY;
-        }
-        if (!isfinite(sm.base[k])) high = low = -INFINITY;   // the row is out
+        low = high = -INFINITY;
+        const float base = sm.base_f[k], inv = sm.inv_f[k];
+        if (key == 0 || sm.state[k] == kOut) return;
+        const float z = sm.state[k] == kFinished ? 0.f : key_logit(key);
+        const float x = (base + z) * inv, err = (fabsf(base) + fabsf(z)) * inv * 4.8e-7f + 1e-37f;
+        const bool fine = fabsf(x) < INFINITY && err < INFINITY;
+        low = fine ? x - err : -INFINITY;
+        high = fine ? x + err : INFINITY;
     };
-    auto offer = [&](int k, uint64_t key, float thr) {
-        float low, high = -INFINITY;
-        if (key) bounds(k, key, low, high);
-        if (high >= thr && high > -INFINITY) {
-            uint64_t rank;
-            const float z = sm.done[k] ? 0.f : key_logit(key);
-            if (exact_score(p, sm, k, z, rank)) {
-                const int to = atomicAdd(&sm.count, 1);
-                if (to < kFinal) {
-                    sm.pick.rank[to] = rank;
-                    sm.pick.place[to] = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.done[k] ? 0 : key_col(key));
-                    sm.pick.z[to] = z;
-                }
-            }
-        }
+    // a finished row has one candidate
+    auto own_key = [&](int list, int d, uint64_t key) {
+        const int k = list / S;
+        return sm.state[k] == kFinished ? (list == k * S && d == 0 ? uint64_t(1) : uint64_t(0)) : key;
     };
-    auto lower = [&](int k, uint64_t key) {
-        float low = -INFINITY, high;
-        if (key) bounds(k, key, low, high);
+    auto lower = [&](int list, uint64_t key) {
+        float low, high;
+        bounds(list / S, key, low, high);
         return low;
+    };
+    auto reaches = [&](int list, uint64_t key, float thr) {
+        float low, high;
+        bounds(list / S, key, low, high);
+        return high >= thr && high > -INFINITY;
+    };
+    auto offer = [&](int list, uint64_t key, float thr) {
+        if (!reaches(list, key, thr)) return;
+        const int k = list / S;
+        uint64_t rank;
+        const float z = sm.state[k] == kFinished ? 0.f : key_logit(key);
+        if (!exact_score(p, sm, k, z, rank)) return;
+        const int to = atomicAdd(&sm.count, 1);
+        if (to < kFinal) {
+            sm.pick.rank[to] = rank;
+            sm.pick.place[to] = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.state[k] == kFinished ? 0 : key_col(key));
+            sm.pick.z[to] = z;
+        }
     };
     auto threshold = [&](float best, uint32_t* to) {
         rank_groups(best > -INFINITY ? ordered(best) : 0u, M, sm.group, to);
         __syncthreads();
         return *to ? unordered(*to) : -INFINITY;
     };
-    if (few) {
-        const uint32_t magic = static_cast<uint32_t>(((uint64_t(1) << 32) + per - 1) / per);   // e < 2^11
-        float best = -INFINITY;
-        int k[kEntries];
-#pragma unroll
-        for (int j = 0; j < kEntries; ++j) {
-            const int e = tid + j * kThreads;
-            k[j] = min(per == 1 ? e : static_cast<int>(__umulhi(static_cast<uint32_t>(e), magic)), K - 1);
-            if (sm.done[k[j]]) held[j] = e == k[j] * per ? 1 : 0;
-            best = fmaxf(best, lower(k[j], held[j]));
+    float best = -INFINITY;
+#pragma unroll 1
+    for (int i = list0; i < lists; i += kThreads) {
+        if (i != list0) key0 = key_at(i, 0);
+        best = fmaxf(best, lower(i, own_key(i, depth0, key0)));
+    }
+    float thr = threshold(best, &sm.thr);
+    // a list whose last of these stays below the threshold has nothing more
+    if (depths < M && depth0 == depths - 1) {
+#pragma unroll 1
+        for (int i = list0; i < lists; i += kThreads) {
+            if (lists > kThreads) key0 = key_at(i, 0);
+            if (reaches(i, own_key(i, depth0, key0), thr)) sm.pick.lists[atomicAdd(&sm.hit_count, 1)] = static_cast<uint16_t>(i);
         }
-        const float thr = threshold(best, &sm.thr);
-#pragma unroll
-        for (int j = 0; j < kEntries; ++j) offer(k[j], held[j], thr);
-    } else {
-        // heads of the lists first (one a row and part); a list whose head stays below
-        // the threshold has nothing above it
-        const int lists = K * S;
-        auto key_at = [&](int list, int d, int& k) {
-            const int row = list / S;
-            return entry_key(p, sm, r0, (static_cast<int64_t>(row) * M + d) * S + (list - row * S), k);
-        };
-        float best = -INFINITY;
-        for (int i = tid; i < lists; i += kThreads) {
-            int k;
-            const uint64_t key = key_at(i, 0, k);
-            best = fmaxf(best, lower(k, key));
-        }
-        float thr = threshold(best, &sm.thr);
-        for (int i = tid; i < lists; i += kThreads) {
-            int k;
-            const uint64_t key = key_at(i, 0, k);
-            float low, high = -INFINITY;
-            if (key) bounds(k, key, low, high);
-            if (high >= thr && high > -INFINITY) sm.pick.lists[atomicAdd(&sm.hit_count, 1)] = static_cast<uint16_t>(i);
-        }
-        __syncthreads();
-        const int entries = sm.hit_count * M;
-        if (entries > 2 * 32) {
-            // few lists, or many alike: a threshold from all of their entries.  (Ranking by
-            // counting costs the square of what is left: 768 candidates took 100 us.)
-            best = -INFINITY;
-            for (int e = tid; e < entries; e += kThreads) {
-                int k;
-                const uint64_t key = key_at(sm.pick.lists[e / M], e % M, k);
-                best = fmaxf(best, lower(k, key));
-            }
-            thr = fmaxf(thr, threshold(best, &sm.thr_end));
-        }
+    }
+    __syncthreads();
+    const int more = M - depths, entries = sm.hit_count * more;
+    if (entries > kThreads / 2) {
+        // many: a threshold from all of them as well.  (Ranking by counting costs the square
+        // of what is left: 768 candidates took 100 us.)
+#pragma unroll 1
         for (int e = tid; e < entries; e += kThreads) {
-            int k;
-            const uint64_t key = key_at(sm.pick.lists[e / M], e % M, k);
-            offer(k, key, thr);
+            const int x = e / more, list = sm.pick.lists[x], d = depths + e - x * more;
+            best = fmaxf(best, lower(list, own_key(list, d, key_at(list, d))));
         }
+        thr = fmaxf(thr, threshold(best, &sm.thr_end));
+    }
+#pragma unroll 1
+    for (int i = list0; i < lists; i += kThreads) {
+        if (lists > kThreads) key0 = key_at(i, 0);
+        offer(i, own_key(i, depth0, key0), thr);
+    }
+#pragma unroll 1
+    for (int e = tid; e < entries; e += kThreads) {
+        const int x = e / more, list = sm.pick.lists[x], d = depths + e - x * more;
+        offer(list, own_key(list, d, key_at(list, d)), thr);
     }
 
     // ---- what is left, ranked by counting in fp64
@@ -540,13 +557,26 @@ struct InFlight {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = __ldg(a + i);
     }
-    __device__ __forceinline__ void unpack(Pack<T, E>& q, const RowLogits<T>& r, int c) const
+    // WORDS: whole words from the first block's start to the vector; half: 2 if it starts
+    // in the middle of one
+    template <int WORDS>
+    __device__ __forceinline__ void unpack(Pack<T, E>& q, uint32_t half) const
     {
         if constexpr (ALIGNED) {
             q.w[0] = v[0].x; q.w[1] = v[0].y; q.w[2] = v[0].z; q.w[3] = v[0].w;
         } else {
-            shift_blocks<T, E>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z + c)));
+            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (T::kBytes == 4) q.w[i] = w[i + WORDS];
+                else q.w[i] = __funnelshift_r(w[i + WORDS], w[i + WORDS + 1], half * 8u);
+            }
         }
+    }
+    __device__ __forceinline__ void unpack(Pack<T, E>& q, const RowLogits<T>& r, int c) const
+    {
+        if constexpr (ALIGNED) unpack<0>(q, 0);
+        else shift_blocks<T, E>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z + c)));
     }
 };
 
@@ -676,22 +706,37 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
                     }
             }
         };
-        // whole tiles, the next one in flight; then what is left
+        // whole tiles, the next one in flight; then what is left.  (The whole words between
+        // a 16-byte boundary and the row's vectors are the same for all of a row, and a loop
+        // for each of the four shifts saves the selects that one for all would need.)
         int t0 = begin;
-        if (t0 >= r.lo) {
+        auto whole_tiles = [&](auto words) {
             InFlight<T, ALIGNED> next[VPT];
             auto issue = [&](int c) {
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) next[j].load(r, c + (j * kThreads + tid) * E);
             };
+            const uint32_t half = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z)) & 2u;
             const int last = min(end, r.hi + E) - kTileCols;   // the last whole tile begins here or before
             if (t0 <= last) issue(t0);
             for (; t0 <= last; t0 += kTileCols) {
                 Pack<T, E> q[VPT];
 #pragma unroll
-                for (int j = 0; j < VPT; ++j) next[j].unpack(q[j], r, t0 + (j * kThreads + tid) * E);
+                for (int j = 0; j < VPT; ++j) next[j].template unpack<words.value>(q[j], half);
                 if (t0 + kTileCols <= last) issue(t0 + kTileCols);
                 use_tile(q, t0 + tid * E);
+            }
+        };
+        if (t0 >= r.lo) {
+            if constexpr (ALIGNED) {
+                whole_tiles(std::integral_constant<int, 0>{});
+            } else {
+                switch (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z)) >> 2 & 3u) {
+                case 0: whole_tiles(std::integral_constant<int, 0>{}); break;
+                case 1: whole_tiles(std::integral_constant<int, 1>{}); break;
+                case 2: whole_tiles(std::integral_constant<int, 2>{}); break;
+                default: whole_tiles(std::integral_constant<int, 3>{}); break;
+                }
             }
         }
         for (; t0 < end; t0 += kTileCols) {
@@ -727,29 +772,20 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
         uint64_t thr = sm.thr_end ? static_cast<uint64_t>(sm.thr_end) << 32 : 1;
         int n;
         while (true) {
+            // a thread an element: little code, which is fetched once a block
             const int noted = sm.hit_count;
             const bool all = noted > kHits;
-            const int vecs = all ? (end - begin + E - 1) / E : noted;
-            for (int i = tid; i < vecs; i += kThreads) {
-                const int c = all ? begin + i * E : sm.hit.col[i];
-                Pack<T, E> v;
-                if (all) {
-                    load_logits<T, ALIGNED>(v, r, c);
-                } else {
-                    const uint4 x = sm.hit.data[i];
-                    v.w[0] = x.x; v.w[1] = x.y; v.w[2] = x.z; v.w[3] = x.w;
-                }
-                const uint32_t allow = mask ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0xffffffffu;
-                const float from = thr > 1 ? key_logit(thr) : __uint_as_float(0xff7fffffu);
-#pragma unroll
-                for (int x = 0; x < E; ++x) {
-                    const float z = v.get(x);
-                    if (z >= from && (allow >> x & 1u)) {
-                        const uint64_t k = key_of(z, c + x);
-                        if (k >= thr) {
-                            const int to = atomicAdd(&sm.count, 1);
-                            if (to < kCap) sm.buf[to] = k;
-                        }
+            const int elements = all ? end - begin : noted * E;
+#pragma unroll 1
+            for (int i = tid; i < elements; i += kThreads) {
+                const int c = all ? begin + i : sm.hit.col[i / E] + i % E;
+                const float z = T::widen(all ? r.z[c] : reinterpret_cast<const typename T::raw*>(&sm.hit.data[i / E])[i % E]);
+                // past V: -inf
+                if (z > -INFINITY && (!mask || (static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) & 1u))) {
+                    const uint64_t k = key_of(z, c);
+                    if (k >= thr) {
+                        const int to = atomicAdd(&sm.count, 1);
+                        if (to < kCap) sm.buf[to] = k;
                     }
                 }
             }
@@ -795,13 +831,13 @@ lmloss_status check_beam(const lmloss_beam_args* a, bool pointers)
     if (a->B < 0 || a->V < 1 || a->ld < a->V) return LMLOSS_ERR_INVALID_ARG;
     if (a->K < 1 || a->K > LMLOSS_MAX_BEAMS || a->M < 1 || a->M > LMLOSS_MAX_BEAMS) return LMLOSS_ERR_INVALID_ARG;
     if (!float_dtype(a->dtype)) return LMLOSS_ERR_INVALID_ARG;
-    if (!(a->length_penalty >= 0.f) || !std::isfinite(a->length_penalty)) return LMLOSS_ERR_INVALID_ARG;
+    if (!(a->length_penalty >= 0.0) || !std::isfinite(a->length_penalty)) return LMLOSS_ERR_INVALID_ARG;
     if (a->eos_token < -1 || a->eos_token >= a->V || a->mask_stride < 0) return LMLOSS_ERR_INVALID_ARG;
     // a block's columns run a little past V in 32 bits
     if (a->V > (int64_t(1) << 31) - (1 << 16) || a->B > (int64_t(1) << 24)) return LMLOSS_ERR_UNSUPPORTED;
     if (a->B > 0 && a->ld > INT64_MAX / 16 / (a->B * a->K)) return LMLOSS_ERR_INVALID_ARG;
     if (!pointers) return LMLOSS_OK;
-    if (a->length_penalty > 0.f && !a->lengths) return LMLOSS_ERR_INVALID_ARG;
+    if (a->length_penalty > 0.0 && !a->lengths) return LMLOSS_ERR_INVALID_ARG;
     if (a->lengths_out && !a->lengths) return LMLOSS_ERR_INVALID_ARG;
     if (a->finished && a->eos_token < 0) return LMLOSS_ERR_INVALID_ARG;
     if (a->token_mask && a->mask_stride != 0 && a->mask_stride < (a->V + 31) / 32) return LMLOSS_ERR_INVALID_ARG;
