@@ -557,26 +557,13 @@ struct InFlight {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = __ldg(a + i);
     }
-    // WORDS: whole words from the first block's start to the vector; half: 2 if it starts
-    // in the middle of one
-    template <int WORDS>
-    __device__ __forceinline__ void unpack(Pack<T, E>& q, uint32_t half) const
+    __device__ __forceinline__ void unpack(Pack<T, E>& q, const RowLogits<T>& r, int c) const
     {
         if constexpr (ALIGNED) {
             q.w[0] = v[0].x; q.w[1] = v[0].y; q.w[2] = v[0].z; q.w[3] = v[0].w;
         } else {
-            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (T::kBytes == 4) q.w[i] = w[i + WORDS];
-                else q.w[i] = __funnelshift_r(w[i + WORDS], w[i + WORDS + 1], half * 8u);
-            }
+            shift_blocks<T, E>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z + c)));
         }
-    }
-    __device__ __forceinline__ void unpack(Pack<T, E>& q, const RowLogits<T>& r, int c) const
-    {
-        if constexpr (ALIGNED) unpack<0>(q, 0);
-        else shift_blocks<T, E>(q, v, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z + c)));
     }
 };
 
@@ -608,7 +595,7 @@ __device__ __forceinline__ void load_logits(Pack<T, Logits<T>::E>& q, const RowL
 // At the end the noted vectors are looked through once for logits that reach the
 // threshold of the whole part.
 template <class T, int VPT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(const __grid_constant__ BeamParams p)
+__global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int E = Logits<T>::E;
     constexpr int kTileCols = VPT * kThreads * E;
@@ -706,44 +693,36 @@ __global__ void __launch_bounds__(kThreads, ALIGNED ? 4 : 3) beam_step_kernel(co
                     }
             }
         };
-        // whole tiles, the next one in flight; then what is left.  (The whole words between
-        // a 16-byte boundary and the row's vectors are the same for all of a row, and a loop
-        // for each of the four shifts saves the selects that one for all would need.)
+        // whole tiles, the next one in flight; then what is left
         int t0 = begin;
-        auto whole_tiles = [&](auto words) {
+        auto whole_tiles = [&] {
             InFlight<T, ALIGNED> next[VPT];
             auto issue = [&](int c) {
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) next[j].load(r, c + (j * kThreads + tid) * E);
             };
-            const uint32_t half = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z)) & 2u;
             const int last = min(end, r.hi + E) - kTileCols;   // the last whole tile begins here or before
             if (t0 <= last) issue(t0);
             for (; t0 <= last; t0 += kTileCols) {
                 Pack<T, E> q[VPT];
 #pragma unroll
-                for (int j = 0; j < VPT; ++j) next[j].template unpack<words.value>(q[j], half);
+                for (int j = 0; j < VPT; ++j) next[j].unpack(q[j], r, t0 + (j * kThreads + tid) * E);
                 if (t0 + kTileCols <= last) issue(t0 + kTileCols);
                 use_tile(q, t0 + tid * E);
             }
         };
-        if (t0 >= r.lo) {
-            if constexpr (ALIGNED) {
-                whole_tiles(std::integral_constant<int, 0>{});
-            } else {
-                switch (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.z)) >> 2 & 3u) {
-                case 0: whole_tiles(std::integral_constant<int, 0>{}); break;
-                case 1: whole_tiles(std::integral_constant<int, 1>{}); break;
-                case 2: whole_tiles(std::integral_constant<int, 2>{}); break;
-                default: whole_tiles(std::integral_constant<int, 3>{}); break;
-                }
-            }
-        }
-        for (; t0 < end; t0 += kTileCols) {
-            Pack<T, E> q[VPT];
+        for (bool before = true;; before = false) {
+            // before the whole tiles only the first tile of the logits' first row, if that is
+            // not whole; after them what is left
+            const int to = before ? min(r.lo, end) : end;
+            for (; t0 < to; t0 += kTileCols) {
+                Pack<T, E> q[VPT];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) load_logits<T, ALIGNED>(q[j], r, t0 + (j * kThreads + tid) * E);
-            use_tile(q, t0 + tid * E);
+                for (int j = 0; j < VPT; ++j) load_logits<T, ALIGNED>(q[j], r, t0 + (j * kThreads + tid) * E);
+                use_tile(q, t0 + tid * E);
+            }
+            if (!before) break;
+            whole_tiles();
         }
 
         // ---- the part's sum, and the threshold of all of it
