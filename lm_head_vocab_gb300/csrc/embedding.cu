@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
 {
     extern __shared__ __align__(16) unsigned char mem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_launch();
     if (blockIdx.x >= static_cast<unsigned>(q.blocks)) {
         const int64_t me = static_cast<int64_t>(blockIdx.x - q.blocks) * kClusterThreads + tid;
         zero_rows<TO, ALIGNED>(p, 0, q.blind, me, static_cast<int64_t>(gridDim.x - q.blocks) * kClusterThreads);
@@ -746,6 +747,7 @@ __global__ void __launch_bounds__(kSumThreads, !ALIGNED ? 6 : (TO::kBytes == 4 ?
     __shared__ int8_t shift[kMaxGroups][kWindow];   // from a 16-byte boundary to the table row
     __shared__ uint32_t ends_of[kMaxGroups];
     grid_dep_wait();
+    grid_dep_launch();
     const EmbParams& e = p.e;
     const uint32_t none = static_cast<uint32_t>(e.V);
     const int tid = threadIdx.x;
@@ -1103,15 +1105,20 @@ lmloss_status launch_after(K* fn, dim3 grid, int threads, cudaStream_t stream, c
 }
 
 template <class TO, bool ALIGNED>
-lmloss_status launch_cluster_sort(const lmloss_vocab_ctx* h, const EmbParams& p, ClusterSort& q, cudaStream_t stream)
+lmloss_status launch_cluster_sort(lmloss_vocab_ctx* h, const EmbParams& p, ClusterSort& q, cudaStream_t stream)
 {
     auto* fn = cluster_sort_kernel<TO, ALIGNED>;
     const size_t smem = cluster_smem(q.share);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(cluster_smem(kClusterRounds * kClusterThreads))) != cudaSuccess ||
-        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-        cudaGetLastError();
-        return LMLOSS_ERR_CUDA;
+    // the kernel's limits, raised to the most that any call needs, once a handle
+    const uint32_t bit = 1u << (2 * TO::kIndex + (ALIGNED ? 1 : 0));
+    if (!(h->limits_raised & bit)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(cluster_smem(kClusterRounds * kClusterThreads))) != cudaSuccess ||
+            cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();
+            return LMLOSS_ERR_CUDA;
+        }
+        h->limits_raised |= bit;
     }
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
@@ -1132,7 +1139,7 @@ lmloss_status launch_cluster_sort(const lmloss_vocab_ctx* h, const EmbParams& p,
     return LMLOSS_OK;
 }
 
-lmloss_status sort_in_cluster(const lmloss_vocab_ctx* h, const lmloss_embedding_args* a, const SortSpace& s, SumParams& p,
+lmloss_status sort_in_cluster(lmloss_vocab_ctx* h, const lmloss_embedding_args* a, const SortSpace& s, SumParams& p,
                               cudaStream_t stream)
 {
     ClusterSort q{};

@@ -24,6 +24,7 @@ struct lmloss_vocab_ctx {
     unsigned* counters = nullptr;    // [kVocabCounters]
     unsigned char* ws = nullptr;     // [ws_bytes]
     size_t ws_bytes = 0;
+    uint32_t limits_raised = 0;      // sorting kernels whose launch limits were raised
 };
 
 namespace lmloss {
@@ -59,6 +60,7 @@ inline bool float_dtype(int32_t dtype) { return dtype == LMLOSS_BF16 || dtype ==
 
 // ------------------------------------------------------------- float types
 struct Bf16 {
+    static constexpr int kIndex = 0;
     using raw = uint16_t;
     static constexpr int kBytes = 2;
     __device__ static __forceinline__ float widen(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
@@ -70,6 +72,7 @@ struct Bf16 {
     }
 };
 struct Fp16 {
+    static constexpr int kIndex = 1;
     using raw = uint16_t;
     static constexpr int kBytes = 2;
     __device__ static __forceinline__ float widen(uint16_t b) { return __half2float(__ushort_as_half(b)); }
@@ -81,6 +84,7 @@ struct Fp16 {
     }
 };
 struct Fp32 {
+    static constexpr int kIndex = 2;
     using raw = uint32_t;
     static constexpr int kBytes = 4;
     __device__ static __forceinline__ float widen(uint32_t b) { return __uint_as_float(b); }
