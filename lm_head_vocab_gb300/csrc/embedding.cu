@@ -467,7 +467,9 @@ sort_place_kernel(const EmbParams p, const uint32_t* keys, const uint32_t* pos, 
 // memory holds: each block keeps an equal share, and a pass moves keys between the
 // blocks' shared memories.  (The passes above are nine launches of a few microseconds
 // each, whose latency is most of a gradient's time at 10^4 positions.)  The launch's
-// other clusters write zeros into the first `blind` table rows meanwhile.
+// other clusters write zeros into the first `blind` table rows meanwhile, or, where the
+// table is added to, bring the first `ahead` bytes of the gradient's rows into L2, from
+// where the sums then read them (16384 x 4096 bf16 into fp32: 87.8 -> 84.1 us).
 constexpr int kClusterBits = 9;
 constexpr int kClusterDigits = 1 << kClusterBits;
 constexpr int kClusterThreads = 1024;
@@ -475,6 +477,12 @@ constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterMax = 16;              // blocks
 constexpr int kClusterRounds = 8;            // keys a thread
 constexpr int kClusterPositions = kClusterMax * kClusterRounds * kClusterThreads;
+
+// Memory into L2, by the 16 bytes: a hint.
+__device__ __forceinline__ void prefetch_l2(uintptr_t addr, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(addr), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t a)
 {
@@ -511,7 +519,7 @@ struct ClusterSort {
     int blocks, share;           // of the cluster; keys of a block
     int fill;                    // blocks that write zeros
     int bits, passes;            // of a digit
-    int64_t blind;
+    int64_t blind, ahead;
     uint32_t *keys, *pos;        // [T] out
 };
 
@@ -531,7 +539,11 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
     grid_dep_launch();
     if (blockIdx.x >= static_cast<unsigned>(q.blocks)) {
         const int64_t me = static_cast<int64_t>(blockIdx.x - q.blocks) * kClusterThreads + tid;
-        zero_rows<TO, ALIGNED>(p, 0, q.blind, me, static_cast<int64_t>(gridDim.x - q.blocks) * kClusterThreads);
+        const int64_t all = static_cast<int64_t>(gridDim.x - q.blocks) * kClusterThreads;
+        zero_rows<TO, ALIGNED>(p, 0, q.blind, me, all);
+        constexpr int kPiece = 2048;
+        const uintptr_t from = (reinterpret_cast<uintptr_t>(p.rows) + 15) & ~uintptr_t(15);
+        for (int64_t b = me * kPiece; b + kPiece <= q.ahead; b += all * kPiece) prefetch_l2(from + b, kPiece);
         return;
     }
     uint2* buf = reinterpret_cast<uint2*>(mem);
@@ -1156,9 +1168,15 @@ lmloss_status sort_in_cluster(lmloss_vocab_ctx* h, const lmloss_embedding_args* 
     // every 4700 positions, at 5 TB/s)
     const int64_t row_bytes = a->D * float_bytes(a->table_dtype), while_sorting = (12 + a->T / 4700) * 5000000;
     // by the SMs that the cluster leaves
-    q.fill = a->accumulate ? 0 : (h->num_sms - q.blocks) / q.blocks * q.blocks;
-    if (q.fill > 0) q.blind = while_sorting / row_bytes;
-    if (q.blind > a->V * 3 / 4) q.blind = a->V;   // little is left to be found out
+    q.fill = (h->num_sms - q.blocks) / q.blocks * q.blocks;
+    if (a->accumulate) {
+        // whole rows' memory less the bytes before its first 16-byte boundary; half of L2
+        const int64_t held = static_cast<int64_t>(p.e.rows_end - static_cast<const unsigned char*>(a->rows));
+        q.ahead = std::min<int64_t>({held - 16, while_sorting, int64_t(64) << 20});
+    } else if (q.fill > 0) {
+        q.blind = while_sorting / row_bytes;
+        if (q.blind > a->V * 3 / 4) q.blind = a->V;   // little is left to be found out
+    }
     p.keys = q.keys;
     p.pos = q.pos;
     p.blind = q.blind;
