@@ -797,6 +797,9 @@ __global__ void __launch_bounds__(kSumThreads, !ALIGNED ? 6 : (TO::kBytes == 4 ?
     const int64_t ld_bytes = e.ld_rows * TG::kBytes;
     const uint32_t whole = c0 + kVec <= e.D ? 0xffffffffu : static_cast<uint32_t>(e.T - 1);
 
+    // whole warps of whole vectors, of one window
+    const bool pairs = ALIGNED && p.tpr >= 32 && (vec - (lane & 31) + 32) * kVec <= e.D;
+
     float acc[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
@@ -841,8 +844,27 @@ __global__ void __launch_bounds__(kSumThreads, !ALIGNED ? 6 : (TO::kBytes == 4 ?
                 unsigned char* out = at<TO>(e.table, v, e.ld_table, 0);
                 if (TO::kBytes == 4 && e.accumulate && c >= 0 && c + kVec <= e.D) {
                     float* f = reinterpret_cast<float*>(out) + c;
-                    red_add4(f, acc[0] * e.scale, acc[1] * e.scale, acc[2] * e.scale, acc[3] * e.scale);
-                    red_add4(f + 4, acc[4] * e.scale, acc[5] * e.scale, acc[6] * e.scale, acc[7] * e.scale);
+                    float y[kVec];
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) y[j] = acc[j] * e.scale;
+                    if (pairs) {
+                        // neighbours exchange halves, so that two of them fill a 32-byte sector at a time
+                        const bool odd = lane & 1;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float mine = odd ? y[j] : y[j + 4];
+                            const float theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
+                            if (odd) y[j] = theirs;
+                            else y[j + 4] = theirs;
+                        }
+                        // even: own first half, the neighbour's first half; odd: the neighbour's second, own second
+                        float* even = f - (odd ? 8 : 0);
+                        red_add4(even + (odd ? 4 : 0), y[0], y[1], y[2], y[3]);
+                        red_add4(even + (odd ? 12 : 8), y[4], y[5], y[6], y[7]);
+                    } else {
+                        red_add4(f, y[0], y[1], y[2], y[3]);
+                        red_add4(f + 4, y[4], y[5], y[6], y[7]);
+                    }
                 } else {
                     write_sum<TO>(e, out, c, acc);
                 }
