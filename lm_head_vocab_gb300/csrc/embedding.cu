@@ -149,6 +149,37 @@ __device__ __forceinline__ int row_offset(const unsigned char* row)
     return ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / T::kBytes;
 }
 
+// Eight fp32 columns of a thread are a 32-byte sector, written by two instructions of 16
+// bytes: each would touch every sector of its warp's columns, by halves.  (Measured where
+// a table is added to: 84 us with halves, 75 with whole sectors.)  So neighbouring threads
+// exchange halves first.  `put` gets the addresses and four columns at a time; pairs: all
+// threads of the warp have whole vectors of one row, next to one another.
+template <class F>
+__device__ __forceinline__ void put_columns(float* f, const float (&x)[8], bool pairs, F&& put)
+{
+    if (!pairs) {
+        put(f, x[0], x[1], x[2], x[3]);
+        put(f + 4, x[4], x[5], x[6], x[7]);
+        return;
+    }
+    const bool odd = threadIdx.x & 1;
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float theirs = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[j + 4], 1);
+        y[j] = odd ? theirs : x[j];
+        y[j + 4] = odd ? x[j + 4] : theirs;
+    }
+    // even: its own first half and its neighbour's; odd: its neighbour's second half and its own
+    float* even = f - (odd ? 8 : 0);
+    put(even + (odd ? 4 : 0), y[0], y[1], y[2], y[3]);
+    put(even + (odd ? 12 : 8), y[4], y[5], y[6], y[7]);
+}
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+
 // ------------------------------------------------------------------ lookup
 // `tpr` threads a row (a power of two), each with four vectors in flight.
 constexpr int kVec = 8;                      // columns of a vector
@@ -180,6 +211,7 @@ __global__ void __launch_bounds__(kFwdThreads) embedding_forward_kernel(const Em
     const unsigned char* lo = static_cast<const unsigned char*>(p.table);
     // aligned rows: a row's last vector reads on into the next row, which the last one lacks
     const int whole = id + 1 < p.V ? D : D - N + 1;
+    const bool warp_row = ALIGNED && tpr >= 32;
     for (int c0 = lane * N - off; c0 < D; c0 += step * kFwdUnroll) {
         Pack<TW, N> x[kFwdUnroll];
 #pragma unroll
@@ -200,6 +232,10 @@ __global__ void __launch_bounds__(kFwdThreads) embedding_forward_kernel(const Em
             float y[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) y[i] = x[u].get(i) * p.scale;
+            if (TO::kBytes == 4 && warp_row && c - (lane & 31) * N + 32 * N <= D) {
+                put_columns(reinterpret_cast<float*>(out) + c, y, true, store4);
+                continue;
+            }
             Pack<TO, N> o;
             o.set_all(y);
             store_row<TO, N>(o, out, c, D);
@@ -232,7 +268,8 @@ __device__ __forceinline__ void write_sum(const EmbParams& p, unsigned char* row
 template <class TO, bool ALIGNED, int THREADS>
 __device__ __forceinline__ void zero_rows_not_held(const EmbParams& p, int64_t v0, int rows, const uint8_t* held)
 {
-    Pack<TO, kVec> z;
+    constexpr int kCols = kGranule<TO>;
+    Pack<TO, kCols> z;
     z.zero();
     const int step = THREADS * gridDim.y;
     if (!ALIGNED && p.ld_table == p.D) {
@@ -246,20 +283,20 @@ __device__ __forceinline__ void zero_rows_not_held(const EmbParams& p, int64_t v
             while (r1 < rows && !held[r1]) ++r1;
             unsigned char* out = at<TO>(p.table, v0 + r, p.ld_table, 0);
             const int64_t n = (r1 - r) * p.D, off = row_offset<TO, ALIGNED>(out);
-            for (int64_t c = static_cast<int64_t>(blockIdx.y * THREADS + threadIdx.x) * kVec - off; c < n; c += static_cast<int64_t>(step) * kVec)
-                store_row<TO, kVec>(z, out, c, n);
+            for (int64_t c = static_cast<int64_t>(blockIdx.y * THREADS + threadIdx.x) * kCols - off; c < n; c += static_cast<int64_t>(step) * kCols)
+                store_row<TO, kCols>(z, out, c, n);
             r = r1;
         }
         return;
     }
-    const int per = static_cast<int>((p.D + (ALIGNED ? 0 : kGranule<TO> - 1) + kVec - 1) / kVec);
+    const int per = static_cast<int>((p.D + (ALIGNED ? 0 : kGranule<TO> - 1) + kCols - 1) / kCols);
     for (int r = 0; r < rows; ++r) {
         if (held[r]) continue;
         unsigned char* out = at<TO>(p.table, v0 + r, p.ld_table, 0);
         const int off = row_offset<TO, ALIGNED>(out);
         for (int x = blockIdx.y * THREADS + threadIdx.x; x < per; x += step) {
-            const int64_t c = static_cast<int64_t>(x) * kVec - off;
-            if (c < p.D) store_row<TO, kVec>(z, out, c, p.D);
+            const int64_t c = static_cast<int64_t>(x) * kCols - off;
+            if (c < p.D) store_row<TO, kCols>(z, out, c, p.D);
         }
     }
 }
@@ -497,21 +534,22 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t a, uint32_t b
 template <class TO, bool ALIGNED>
 __device__ void zero_rows(const EmbParams& p, int64_t r0, int64_t r1, int64_t me, int64_t all)
 {
-    Pack<TO, kVec> z;
+    constexpr int kCols = kGranule<TO>;
+    Pack<TO, kCols> z;
     z.zero();
     if (p.ld_table == p.D) {
         // one run of memory
         unsigned char* base = at<TO>(p.table, r0, p.ld_table, 0);
         const int64_t n = (r1 - r0) * p.D, off = row_offset<TO, ALIGNED>(base);
-        for (int64_t c = me * kVec - off; c < n; c += all * kVec) store_row<TO, kVec>(z, base, c, n);
+        for (int64_t c = me * kCols - off; c < n; c += all * kCols) store_row<TO, kCols>(z, base, c, n);
         return;
     }
-    const int64_t per = (p.D + (ALIGNED ? 0 : kGranule<TO> - 1) + kVec - 1) / kVec, n = per * (r1 - r0);
+    const int64_t per = (p.D + (ALIGNED ? 0 : kCols - 1) + kCols - 1) / kCols, n = per * (r1 - r0);
     for (int64_t i = me; i < n; i += all) {
         const int64_t r = i / per;
         unsigned char* row = at<TO>(p.table, r0 + r, p.ld_table, 0);
-        const int64_t c = (i - r * per) * kVec - row_offset<TO, ALIGNED>(row);
-        if (c < p.D) store_row<TO, kVec>(z, row, c, p.D);
+        const int64_t c = (i - r * per) * kCols - row_offset<TO, ALIGNED>(row);
+        if (c < p.D) store_row<TO, kCols>(z, row, c, p.D);
     }
 }
 
@@ -798,7 +836,7 @@ __global__ void __launch_bounds__(kSumThreads, !ALIGNED ? 6 : (TO::kBytes == 4 ?
     const uint32_t whole = c0 + kVec <= e.D ? 0xffffffffu : static_cast<uint32_t>(e.T - 1);
 
     // whole warps of whole vectors, of one window
-    const bool pairs = ALIGNED && p.tpr >= 32 && (vec - (lane & 31) + 32) * kVec <= e.D;
+    const bool pairs = ALIGNED && TO::kBytes == 4 && p.tpr >= 32 && (vec - (lane & 31) + 32) * kVec <= e.D;
 
     float acc[kVec];
 #pragma unroll
@@ -832,8 +870,7 @@ __global__ void __launch_bounds__(kSumThreads, !ALIGNED ? 6 : (TO::kBytes == 4 ?
             if (from || on) {
                 float* part = p.parts + (2 * static_cast<int64_t>(w) + (from ? 0 : 1)) * p.ld_parts;
                 if (ALIGNED && c + kVec <= e.D) {
-                    reinterpret_cast<float4*>(part + c)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    reinterpret_cast<float4*>(part + c)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                    put_columns(part + c, acc, pairs, store4);
                 } else {
 #pragma unroll
                     for (int j = 0; j < kVec; ++j)
@@ -847,24 +884,12 @@ __global__ void __launch_bounds__(kSumThreads, !ALIGNED ? 6 : (TO::kBytes == 4 ?
                     float y[kVec];
 #pragma unroll
                     for (int j = 0; j < kVec; ++j) y[j] = acc[j] * e.scale;
-                    if (pairs) {
-                        // neighbours exchange halves, so that two of them fill a 32-byte sector at a time
-                        const bool odd = lane & 1;
+                    put_columns(f, y, pairs, red_add4);
+                } else if (TO::kBytes == 4 && pairs) {
+                    float y[kVec];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float mine = odd ? y[j] : y[j + 4];
-                            const float theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
-                            if (odd) y[j] = theirs;
-                            else y[j + 4] = theirs;
-                        }
-                        // even: own first half, the neighbour's first half; odd: the neighbour's second, own second
-                        float* even = f - (odd ? 8 : 0);
-                        red_add4(even + (odd ? 4 : 0), y[0], y[1], y[2], y[3]);
-                        red_add4(even + (odd ? 12 : 8), y[4], y[5], y[6], y[7]);
-                    } else {
-                        red_add4(f, y[0], y[1], y[2], y[3]);
-                        red_add4(f + 4, y[4], y[5], y[6], y[7]);
-                    }
+                    for (int j = 0; j < kVec; ++j) y[j] = acc[j] * e.scale;
+                    put_columns(reinterpret_cast<float*>(out) + c, y, true, store4);
                 } else {
                     write_sum<TO>(e, out, c, acc);
                 }
