@@ -16,6 +16,7 @@ from . import _lib
 from ._lib import LMLossError
 
 _FLOATS = {torch.bfloat16: _lib.LMLOSS_BF16, torch.float32: _lib.LMLOSS_FP32, torch.float16: _lib.LMLOSS_FP16}
+_ONES = (1, 1, 1)
 _IDS = {torch.int64: _lib.LMLOSS_INT64, torch.int32: _lib.LMLOSS_INT32}
 
 
@@ -155,16 +156,19 @@ class VocabOps:
         if out is None:
             if out_dtype is None:
                 out_dtype = weight.dtype
+            r_type, ld_rows = _FLOATS.get(out_dtype), D
+            if r_type is None:
+                raise TypeError(f"out_dtype: must be bfloat16, float16 or float32, got {out_dtype}")
             if ctx is None:
                 out = torch.empty(shape, dtype=out_dtype, device=self.device)
             else:
                 with ctx:
                     out = torch.empty(shape, dtype=out_dtype, device=self.device)
-        elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError(f"out: expected {shape}{'' if out_dtype is None else f' of {out_dtype}'}")
-        rows = out if out.dim() == 2 else out.view(T, D)
-        r_type, _, _, ld_rows = _matrix(rows, "out", self._index)
-        a = _lib.lmloss_embedding_args(ids.data_ptr(), T, V, D, weight.data_ptr(), ld, rows.data_ptr(), ld_rows,
+        else:
+            if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+                raise ValueError(f"out: expected {shape}{'' if out_dtype is None else f' of {out_dtype}'}")
+            r_type, _, _, ld_rows = _matrix(out if out.dim() == 2 else out.view(T, D), "out", self._index)
+        a = _lib.lmloss_embedding_args(ids.data_ptr(), T, V, D, weight.data_ptr(), ld, out.data_ptr(), ld_rows,
                                        id_type, w_type, r_type, scale, 0)
         st = self._forward(self.handle, a, raw)
         if st != _lib.LMLOSS_OK:
@@ -327,6 +331,9 @@ class VocabOps:
         if len(oshape) != len(shape) or oshape[d] != rows_out:
             raise ValueError(f"out: {tuple(oshape)} for a state of {tuple(shape)} and {rows_out} rows")
         es = t.element_size()
+        if len(shape) == 2 and d == 0 and ts[1] == 1 and os_[1] == 1 and oshape[1] == shape[1]:
+            # a matrix: a row is a run
+            return _lib.lmloss_beam_state(t.data_ptr(), o.data_ptr(), shape[1] * es, ts[0] * es, os_[0] * es, _ONES)
         dims = []
         for i, n in enumerate(shape):
             if i == d:
