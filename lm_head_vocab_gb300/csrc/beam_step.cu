@@ -86,20 +86,42 @@ __device__ __forceinline__ uint64_t ordered64(double x)
     return (b >> 63) ? ~b : (b | (uint64_t(1) << 63));
 }
 
-// the M-th largest of n > M different keys in shared memory, found bit by bit
-__device__ __noinline__ uint64_t mth_largest(const uint64_t* keys, int n, int M)
+// The M-th largest of n > M different keys in shared memory, found eight bits at a time:
+// counts of the next eight bits among the keys that share what was found so far.
+// (Bit by bit, with a barrier for each, it took 25 us of a block.)
+__device__ __noinline__ uint64_t mth_largest(const uint64_t* keys, int n, int M, uint32_t* counts)
 {
-    uint64_t t = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-        const uint64_t cand = t | (uint64_t(1) << bit);
-        int c = 0;
-        for (int i0 = 0; i0 < n; i0 += kThreads) {
-            const int i = i0 + threadIdx.x;
-            c += __syncthreads_count(i < n && keys[i] >= cand);
+    const int tid = threadIdx.x, lane = tid & 31;
+    uint64_t found = 0;
+    int want = M;
+#pragma unroll 1
+    for (int shift = 56; shift >= 0; shift -= 8) {
+        counts[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const uint64_t k = keys[i];
+            if (shift == 56 || (k ^ found) >> (shift + 8) == 0) atomicAdd(&counts[static_cast<uint32_t>(k >> shift) & 255u], 1u);
         }
-        if (c >= M) t = cand;
+        __syncthreads();
+        // every warp for itself: lane l's eight counts from 8 (31 - l) on, so that lower lanes have the larger bits
+        uint32_t sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += counts[8 * (31 - lane) + j];
+        uint32_t inc = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, inc >= static_cast<uint32_t>(want));
+        const int in = __ffs(has) - 1;   // the first lane by which there are enough: n > M
+        uint32_t above = __shfl_sync(0xffffffffu, inc - sum, in);
+        int digit = 8 * (31 - in) + 7;
+        while (above + counts[digit] < static_cast<uint32_t>(want)) above += counts[digit--];
+        found |= static_cast<uint64_t>(digit) << shift;
+        want -= static_cast<int>(above);
+        __syncthreads();
     }
-    return t;
+    return found;
 }
 
 __device__ __forceinline__ float warp_max(float x)
@@ -153,10 +175,10 @@ struct __align__(16) Shared {
             uint16_t lists[kMaxLists];       // its lists that reach the first threshold
         } pick;
     };
-    uint32_t group[kThreads / 2];
+    uint32_t group[kThreads / 2], counts[kThreads];
     uint32_t thr, thr_end;                   // of the first tile, of all
     float red_m[kWarps], red_s[kWarps];
-    int count, hit_count;
+    int count, hit_count, few;
     int last;
     // of a sequence's rows
     double base[kMaxM], norm[kMaxM];
@@ -468,14 +490,27 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
     }
     __syncthreads();
     const int more = M - depths, entries = sm.hit_count * more;
+    auto each_entry = [&](auto&& use) {
+        constexpr int kAhead = 4;   // on their way
+#pragma unroll 1
+        for (int e0 = tid; e0 < entries; e0 += kAhead * kThreads) {
+            uint64_t key[kAhead];
+            int list[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int e = e0 + j * kThreads, x = min(e, entries - 1) / more;
+                list[j] = sm.pick.lists[x];
+                key[j] = e < entries ? own_key(list[j], 1, key_at(list[j], depths + e - x * more)) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (key[j]) use(list[j], key[j]);
+        }
+    };
     if (entries > kThreads / 2) {
         // many: a threshold from all of them as well.  (Ranking by counting costs the square
         // of what is left: 768 candidates took 100 us.)
-#pragma unroll 1
-        for (int e = tid; e < entries; e += kThreads) {
-            const int x = e / more, list = sm.pick.lists[x], d = depths + e - x * more;
-            best = fmaxf(best, lower(list, own_key(list, d, key_at(list, d))));
-        }
+        each_entry([&](int list, uint64_t key) { best = fmaxf(best, lower(list, key)); });
         thr = fmaxf(thr, threshold(best, &sm.thr_end));
     }
 #pragma unroll 1
@@ -483,11 +518,7 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
         if (lists > kThreads) key0 = key_at(i, 0);
         offer(i, own_key(i, depth0, key0), thr);
     }
-#pragma unroll 1
-    for (int e = tid; e < entries; e += kThreads) {
-        const int x = e / more, list = sm.pick.lists[x], d = depths + e - x * more;
-        offer(list, own_key(list, d, key_at(list, d)), thr);
-    }
+    each_entry([&](int list, uint64_t key) { offer(list, key, thr); });
 
     // ---- what is left, ranked by counting in fp64
     __syncthreads();
@@ -632,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
         if (tid == 0) {
             sm.count = 0;
             sm.hit_count = 0;
+            sm.few = 0;
             sm.thr = 0;
             sm.thr_end = 0;
         }
@@ -780,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
             __syncthreads();
             n = sm.count;
             if (n <= kCap) break;
-            thr = mth_largest(sm.buf, kCap, p.M);
+            thr = mth_largest(sm.buf, kCap, p.M, sm.counts);
             __syncthreads();
             if (tid == 0) sm.count = 0;
             __syncthreads();
@@ -789,13 +821,22 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
         // ---- the M best of them, best first: ranked by counting (exact: the keys are
         // all different)
         uint64_t* out = p.keys + static_cast<int64_t>(row) * p.M * p.slices + part;
-        const uint64_t cut = n > kSmall ? mth_largest(sm.buf, n, p.M) : 0;
+        const uint64_t cut = n > kSmall ? mth_largest(sm.buf, n, p.M, sm.counts) : 0;
+        const uint64_t* set = sm.buf;
+        if (cut) {
+            // exactly M are left: a row's short end, where few groups have a logit, or equal ones
+            uint64_t* few = reinterpret_cast<uint64_t*>(sm.hit.data);
+            for (int i = tid; i < n; i += kThreads)
+                if (sm.buf[i] >= cut) few[atomicAdd(&sm.few, 1)] = sm.buf[i];
+            __syncthreads();
+            n = p.M;
+            set = few;
+        }
         for (int i = tid; i < n; i += kThreads) {
-            const uint64_t k = sm.buf[i];
-            if (k < cut) continue;
+            const uint64_t k = set[i];
             int above = 0;
 #pragma unroll 8
-            for (int o = 0; o < n; ++o) above += sm.buf[o] > k ? 1 : 0;
+            for (int o = 0; o < n; ++o) above += set[o] > k ? 1 : 0;
             if (above < p.M) out[static_cast<int64_t>(above) * p.slices] = k;
         }
         for (int i = n + tid; i < p.M; i += kThreads) out[static_cast<int64_t>(i) * p.slices] = 0;
