@@ -55,7 +55,7 @@ struct BeamParams {
     float* lse_out;
     uint8_t* finished_out;
     int32_t* lengths_out;
-    uint64_t* keys;              // [rows][M][slices]: each part's candidates, best first, 0 = none
+    uint64_t* keys;              // [rows][slices][M]: each part's candidates, best first, 0 = none
     float2* stats;               // [rows][slices] (m, s): the part's sum of e^z is s e^m
     unsigned* done;              // [B] parts finished; 0 between calls
 };
@@ -200,14 +200,13 @@ __device__ __forceinline__ bool exact_score(const BeamParams& p, const Shared& s
     return true;
 }
 
-// Entry e of a sequence's candidates, [K][M][slices]; a finished row has one, any
+// Candidate d of a sequence's list (list / slices: its row); a finished row has one, any
 // non-zero key.
-__device__ __forceinline__ uint64_t entry_key(const BeamParams& p, const Shared& sm, int64_t r0, int64_t e, int& k)
+__device__ __forceinline__ uint64_t list_key(const BeamParams& p, const Shared& sm, int64_t r0, int list, int d, int& k)
 {
-    const int per = p.M * p.slices;
-    k = static_cast<int>(e) / per;
-    if (sm.state[k] == kFinished) return e == static_cast<int64_t>(k) * per ? 1 : 0;
-    return __ldcg(p.keys + r0 * per + e);
+    k = list / p.slices;
+    if (sm.state[k] == kFinished) return list == k * p.slices && d == 0 ? 1 : 0;
+    return __ldcg(p.keys + (r0 * p.slices + list) * p.M + d);
 }
 
 __device__ __forceinline__ void write_pick(const BeamParams& p, const Shared& sm, int b, int out, int k, float z, int token)
@@ -244,10 +243,6 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
     uint64_t rank = 0, place = 0;
     int list = -1;
     bool stale = true;
-    auto head = [&](int i, int d, int& k) -> uint64_t {
-        const int row = i / p.slices;
-        return entry_key(p, sm, r0, (static_cast<int64_t>(row) * p.M + d) * p.slices + (i - row * p.slices), k);
-    };
     for (int out = 0; out < p.M; ++out) {
         if (stale) {
             rank = 0;
@@ -257,7 +252,7 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
                 const int i = tid + j * kThreads, d = static_cast<int>(depth >> (8 * j)) & 255;
                 if (i >= lists || d >= p.M) continue;
                 int k;
-                const uint64_t key = head(i, d, k);
+                const uint64_t key = list_key(p, sm, r0, i, d, k);
                 uint64_t cr;
                 if (key == 0 || !exact_score(p, sm, k, key_logit(key), cr)) continue;
                 const uint64_t cp = (static_cast<uint64_t>(k) << 32) | static_cast<uint32_t>(sm.state[k] == kFinished ? 0 : key_col(key));
@@ -300,7 +295,7 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
             const int j = won / kThreads, d = static_cast<int>(depth >> (8 * j)) & 255;
             depth += uint64_t(1) << (8 * j);
             int k;
-            const uint64_t key = head(won, d, k);
+            const uint64_t key = list_key(p, sm, r0, won, d, k);
             write_pick(p, sm, b, out, k, key_logit(key), key_col(key));
             stale = true;
         }
@@ -358,10 +353,7 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
     // read under the way of the rows' sums.
     const int depths = lists < kThreads ? min(M, kThreads / lists) : 1;
     const int list0 = tid / depths, depth0 = tid - list0 * depths;
-    auto key_at = [&](int list, int d) {
-        const int k = list / S;
-        return __ldcg(p.keys + ((r0 + k) * M + d) * S + (list - k * S));
-    };
+    auto key_at = [&](int list, int d) { return __ldcg(p.keys + (r0 * S + list) * M + d); };
     uint64_t key0 = list0 < lists ? key_at(list0, depth0) : 0;
 
     // ---- the rows' normalisers: the parts' sums are added as pairs of fp32, an
@@ -558,6 +550,19 @@ struct Logits {
             return fmaxf(T::widen(static_cast<uint16_t>(w & 0xffffu)), T::widen(static_cast<uint16_t>(w >> 16)));
         }
     }
+    // The same of those whose bit is set.
+    __device__ static __forceinline__ float largest_allowed(Pack<T, E> q, uint32_t allow)
+    {
+        constexpr uint32_t kNone = T::kBytes == 4 ? 0xff800000u : (std::is_same<T, Bf16>::value ? 0xff80ff80u : 0xfc00fc00u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t keep;
+            if constexpr (T::kBytes == 4) keep = 0u - (allow >> i & 1u);
+            else keep = ((0u - (allow >> (2 * i) & 1u)) & 0xffffu) | ((0u - (allow >> (2 * i + 1) & 1u)) << 16);
+            q.w[i] = (q.w[i] & keep) | (kNone & ~keep);
+        }
+        return largest(q);
+    }
 };
 
 // What is read of one row.  Vectors from column lo to hi are read as they lie in
@@ -684,10 +689,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
                 for (int j = 0; j < VPT; ++j) {
                     const int c = c0 + j * (kThreads * E);
                     const uint32_t allow = c < p.V ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0u;
-                    vmax[j] = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        if (allow >> i & 1u) vmax[j] = fmaxf(vmax[j], q[j].get(i));
+                    vmax[j] = Logits<T>::largest_allowed(q[j], allow);
                     tmax = fmaxf(tmax, vmax[j]);
                 }
             }
@@ -820,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
 
         // ---- the M best of them, best first: ranked by counting (exact: the keys are
         // all different)
-        uint64_t* out = p.keys + static_cast<int64_t>(row) * p.M * p.slices + part;
+        uint64_t* out = p.keys + static_cast<int64_t>(blockIdx.x) * p.M;
         const uint64_t cut = n > kSmall ? mth_largest(sm.buf, n, p.M, sm.counts) : 0;
         const uint64_t* set = sm.buf;
         if (cut) {
@@ -837,9 +839,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
             int above = 0;
 #pragma unroll 8
             for (int o = 0; o < n; ++o) above += set[o] > k ? 1 : 0;
-            if (above < p.M) out[static_cast<int64_t>(above) * p.slices] = k;
+            if (above < p.M) out[above] = k;
         }
-        for (int i = n + tid; i < p.M; i += kThreads) out[static_cast<int64_t>(i) * p.slices] = 0;
+        for (int i = n + tid; i < p.M; i += kThreads) out[i] = 0;
     }
 
     // ---- the sequence's last block goes on to pick
