@@ -20,6 +20,7 @@
 //             4097 of bf16 32003 x 1001 (no row on a vector boundary), whole: 30 us = 2.4 TB/s,
 //             three kernels of about 10 us, each a chain of latencies
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -318,8 +319,8 @@ __device__ __forceinline__ void zero_rows_not_held(const EmbParams& p, int64_t v
 // looks through all ids for its own token, leaves if the token has an earlier position,
 // and otherwise adds up all of them in order.  The blocks after these write zeros in
 // the rows that no id names.  Every block reads all ids, so this is for few of them
-// (measured, bf16 added to an fp32 table of 128256 x 4096: 64 positions 3.2 us here and
-// 15.7 us sorted, 1024 positions 15.3 and 23.0).
+// (measured, bf16 added to an fp32 table of 128256 x 4096: 192 positions 4.5 us here and
+// 12.8 us sorted, 1024 positions 14.8 and 17.1).
 constexpr int kFewThreads = 128;
 constexpr int kFewSpan = 64;                 // table rows of a block that writes zeros, at most
 constexpr int kFewPositions = 1024;
@@ -517,9 +518,9 @@ sort_place_kernel(const EmbParams p, const uint32_t* keys, const uint32_t* pos, 
 // memory holds: each block keeps an equal share, and a pass moves keys between the
 // blocks' shared memories.  (The passes above are nine launches of a few microseconds
 // each, whose latency is most of a gradient's time at 10^4 positions.)  The launch's
-// other clusters write zeros into the first `blind` table rows meanwhile, or, where the
-// table is added to, bring the first `ahead` bytes of the gradient's rows into L2, from
-// where the sums then read them (16384 x 4096 bf16 into fp32: 87.8 -> 84.1 us).
+// other clusters write zeros into the first table rows meanwhile, or, where the table is
+// added to, bring the gradient's first rows into L2, from where the sums then read them
+// (16384 x 4096 bf16 into fp32: 87.8 -> 84.1 us).
 constexpr int kClusterBits = 9;
 constexpr int kClusterDigits = 1 << kClusterBits;
 constexpr int kClusterThreads = 1024;
@@ -566,6 +567,17 @@ __device__ void zero_rows(const EmbParams& p, int64_t r0, int64_t r1, int64_t me
     }
 }
 
+// What the SMs that do not sort do meanwhile, by threads `me` of `all`: zeros in the first
+// `blind` rows of the table, the first `ahead` bytes of the gradient's rows into L2.
+template <class TO, bool ALIGNED>
+__device__ __forceinline__ void fill_or_fetch(const EmbParams& p, int64_t blind, int64_t ahead, int64_t me, int64_t all)
+{
+    zero_rows<TO, ALIGNED>(p, 0, blind, me, all);
+    constexpr int kPiece = 2048;
+    const uintptr_t from = (reinterpret_cast<uintptr_t>(p.rows) + 15) & ~uintptr_t(15);
+    for (int64_t b = me * kPiece; b + kPiece <= ahead; b += all * kPiece) prefetch_l2(from + b, kPiece);
+}
+
 struct ClusterSort {
     int blocks, share;           // of the cluster; keys of a block
     int fill;                    // blocks that write zeros
@@ -589,12 +601,8 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_launch();
     if (blockIdx.x >= static_cast<unsigned>(q.blocks)) {
-        const int64_t me = static_cast<int64_t>(blockIdx.x - q.blocks) * kClusterThreads + tid;
-        const int64_t all = static_cast<int64_t>(gridDim.x - q.blocks) * kClusterThreads;
-        zero_rows<TO, ALIGNED>(p, 0, q.blind, me, all);
-        constexpr int kPiece = 2048;
-        const uintptr_t from = (reinterpret_cast<uintptr_t>(p.rows) + 15) & ~uintptr_t(15);
-        for (int64_t b = me * kPiece; b + kPiece <= q.ahead; b += all * kPiece) prefetch_l2(from + b, kPiece);
+        fill_or_fetch<TO, ALIGNED>(p, q.blind, q.ahead, static_cast<int64_t>(blockIdx.x - q.blocks) * kClusterThreads + tid,
+                                   static_cast<int64_t>(gridDim.x - q.blocks) * kClusterThreads);
         return;
     }
     uint2* buf = reinterpret_cast<uint2*>(mem);
@@ -732,6 +740,78 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
         // the next pass's keys are in place, and no block's totals are read any more
         cluster_sync_all();
     }
+}
+
+// A few thousand positions by counting: a position's place is the number of those that
+// come before it, with a smaller token or the same one earlier.  A block takes kRanked
+// positions, its threads take the others' keys from memory.  Nothing is passed between blocks,
+// so T^2 comparisons spread over all SMs take less time than a cluster's passes, for as long
+// as there are few of them (measured, whole gradients, bf16 rows of 4096 added to fp32 and of
+// 512 to bf16, by counting and by a cluster: 1500 positions 17.6 and 23.6 us, 15.2 and 19.9;
+// 4097 positions 28.2 and 32.5, 19.1 and 21.7; 6000 positions 32.6 and 35.7, 20.8 and 22.7;
+// 8192 positions 52.3 and 50.5, 25.8 and 23.5).
+// The blocks after these do what the cluster sort's other clusters do.
+constexpr int kRankThreads = 256;
+constexpr int kRankWarps = kRankThreads / 32;
+constexpr int kRanked = 16;
+constexpr int kRankAhead = 8;
+constexpr int kRankPositions = 6144;
+
+struct RankSort {
+    int blocks;
+    int64_t blind, ahead;
+    uint32_t *keys, *pos;        // [T] out
+};
+
+template <class TO, bool ALIGNED>
+__global__ void __launch_bounds__(kRankThreads) rank_sort_kernel(const EmbParams p, const RankSort q)
+{
+    __shared__ uint32_t own[kRanked];
+    __shared__ uint32_t below[kRankWarps][kRanked];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_launch();
+    if (blockIdx.x >= static_cast<unsigned>(q.blocks)) {
+        fill_or_fetch<TO, ALIGNED>(p, q.blind, q.ahead, static_cast<int64_t>(blockIdx.x - q.blocks) * kRankThreads + tid,
+                                   static_cast<int64_t>(gridDim.x - q.blocks) * kRankThreads);
+        return;
+    }
+    const int i0 = static_cast<int>(blockIdx.x) * kRanked;
+    if (tid < kRanked) own[tid] = i0 + tid < p.T ? first_key(p, i0 + tid) : 0;
+    __syncthreads();
+    int key[kRanked];
+    uint32_t n[kRanked];
+#pragma unroll
+    for (int c = 0; c < kRanked; ++c) {
+        key[c] = static_cast<int>(own[c]);
+        n[c] = 0;
+    }
+    for (int j0 = tid; j0 < p.T; j0 += kRankAhead * kRankThreads) {
+        int other[kRankAhead];
+#pragma unroll
+        for (int r = 0; r < kRankAhead; ++r) {
+            const int j = j0 + r * kRankThreads;
+            const int64_t id = j < p.T ? load_id(p, j) : p.V;
+            // one less where it comes first among equals; keys are below 2^31
+            other[r] = j < p.T ? (id >= 0 && id < p.V ? static_cast<int>(id) : p.V) - (j < i0 ? 1 : 0) : INT_MAX;
+        }
+#pragma unroll
+        for (int r = 0; r < kRankAhead; ++r)
+#pragma unroll
+            for (int c = 0; c < kRanked; ++c) n[c] += other[r] < key[c] ? 1 : 0;
+    }
+#pragma unroll
+    for (int c = 0; c < kRanked; ++c) {
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, n[c]);
+        if (lane == 0) below[warp][c] = sum;
+    }
+    __syncthreads();
+    if (tid >= kRanked || i0 + tid >= p.T) return;
+    uint32_t to = 0;
+#pragma unroll
+    for (int w = 0; w < kRankWarps; ++w) to += below[w][tid];
+    for (int c = 0; c < tid; ++c) to += own[c] == own[tid] ? 1 : 0;
+    q.keys[to] = own[tid];
+    q.pos[to] = static_cast<uint32_t>(i0 + tid);
 }
 
 // ------------------------------------------------------- sums by token
@@ -1211,6 +1291,45 @@ lmloss_status launch_cluster_sort(lmloss_vocab_ctx* h, const EmbParams& p, Clust
     return LMLOSS_OK;
 }
 
+// The table rows to fill blindly, or the bytes to fetch, in the `us` microseconds of a sort:
+// about what the other SMs write in that time, at 5 TB/s.
+void meanwhile(const lmloss_embedding_args* a, const EmbParams& p, int64_t us, int64_t& blind, int64_t& ahead)
+{
+    const int64_t row_bytes = a->D * float_bytes(a->table_dtype), bytes = us * 5000000;
+    if (a->accumulate) {
+        // whole rows' memory less the bytes before its first 16-byte boundary; half of L2
+        const int64_t held = static_cast<int64_t>(p.rows_end - static_cast<const unsigned char*>(a->rows));
+        ahead = std::min<int64_t>({held - 16, bytes, int64_t(64) << 20});
+    } else {
+        blind = bytes / row_bytes;
+        if (blind > a->V * 3 / 4) blind = a->V;   // little is left to be found out
+    }
+}
+
+lmloss_status sort_by_rank(const lmloss_vocab_ctx* h, const lmloss_embedding_args* a, const SortSpace& s, SumParams& p,
+                           cudaStream_t stream)
+{
+    RankSort q{};
+    q.blocks = (p.e.T + kRanked - 1) / kRanked;
+    q.keys = reinterpret_cast<uint32_t*>(h->ws + s.keys[0]);
+    q.pos = reinterpret_cast<uint32_t*>(h->ws + s.pos[0]);
+    // more than fits beside the counting, which takes 2 to 6 us: zeros written here need no
+    // look at the keys (bf16 tables of 32003 x 1001, 128256 x 512 and 100000 x 1024, 2048 positions:
+    // 26.2, 34.8 and 49.1 us with 4 us of zeros, 24.6, 30.4 and 44.1 with 13, 24.5, 33.5 and 50 with 30)
+    meanwhile(a, p.e, 13, q.blind, q.ahead);
+    p.keys = q.keys;
+    p.pos = q.pos;
+    p.blind = q.blind;
+    const bool aligned = aligned_rows(a);
+    const unsigned grid = static_cast<unsigned>(q.blocks + 12 * h->num_sms);
+    return by_type(a->table_dtype, [&](auto to) {
+        using TO = decltype(to);
+        if (aligned) rank_sort_kernel<TO, true><<<grid, kRankThreads, 0, stream>>>(p.e, q);
+        else rank_sort_kernel<TO, false><<<grid, kRankThreads, 0, stream>>>(p.e, q);
+        return vocab_launch_err();
+    });
+}
+
 lmloss_status sort_in_cluster(lmloss_vocab_ctx* h, const lmloss_embedding_args* a, const SortSpace& s, SumParams& p,
                               cudaStream_t stream)
 {
@@ -1224,19 +1343,10 @@ lmloss_status sort_in_cluster(lmloss_vocab_ctx* h, const lmloss_embedding_args* 
     q.bits = (bits + q.passes - 1) / q.passes;
     q.keys = reinterpret_cast<uint32_t*>(h->ws + s.keys[0]);
     q.pos = reinterpret_cast<uint32_t*>(h->ws + s.pos[0]);
-    // about what the other SMs write while the cluster sorts (measured: 12 us and 1 us more for
-    // every 4700 positions, at 5 TB/s)
-    const int64_t row_bytes = a->D * float_bytes(a->table_dtype), while_sorting = (12 + a->T / 4700) * 5000000;
     // by the SMs that the cluster leaves
     q.fill = (h->num_sms - q.blocks) / q.blocks * q.blocks;
-    if (a->accumulate) {
-        // whole rows' memory less the bytes before its first 16-byte boundary; half of L2
-        const int64_t held = static_cast<int64_t>(p.e.rows_end - static_cast<const unsigned char*>(a->rows));
-        q.ahead = std::min<int64_t>({held - 16, while_sorting, int64_t(64) << 20});
-    } else if (q.fill > 0) {
-        q.blind = while_sorting / row_bytes;
-        if (q.blind > a->V * 3 / 4) q.blind = a->V;   // little is left to be found out
-    }
+    // measured: 12 us and 1 us more for every 4700 positions
+    if (q.fill > 0) meanwhile(a, p.e, 12 + a->T / 4700, q.blind, q.ahead);
     p.keys = q.keys;
     p.pos = q.pos;
     p.blind = q.blind;
@@ -1342,7 +1452,9 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
             return vocab_launch_err();
         });
     }
-    st = a->T <= kClusterPositions ? sort_in_cluster(h, a, s, q, stream) : sort_in_passes(h, s, q, stream);
+    st = a->T <= kRankPositions      ? sort_by_rank(h, a, s, q, stream)
+         : a->T <= kClusterPositions ? sort_in_cluster(h, a, s, q, stream)
+                                     : sort_in_passes(h, s, q, stream);
     if (st != LMLOSS_OK) return st;
     q.parts = reinterpret_cast<float*>(h->ws + s.parts);
     q.ld_parts = s.ld_parts;

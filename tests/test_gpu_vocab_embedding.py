@@ -167,7 +167,7 @@ def test_gradient(ops, gt, ot, accumulate, T, V, D, pad, off, kind):
 
 
 @pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 511, 512, 513, 1023, 1024, 1025, 2047, 2048, 2049, 4096,
-                               4097, 8191, 16385, 20000])
+                               4097, 6143, 6144, 6145, 8191, 16385, 20000])
 @pytest.mark.parametrize("kind", ["same", "text", "all", "runs", "none"])
 def test_gradient_lengths(ops, T, kind):
     g = gen(T)
