@@ -1171,6 +1171,20 @@ EmbParams params(const lmloss_vocab_ctx* h, const lmloss_embedding_args* a)
     return p;
 }
 
+// vectors of the longest row, its first one possibly begun early
+int64_t row_vectors(const lmloss_embedding_args* a, int32_t written, bool aligned)
+{
+    return (a->D + (aligned ? 0 : 16 / float_bytes(written) - 1) + kVec - 1) / kVec;
+}
+
+// threads of a row: a power of two from 8 to `most`, as many as it has vectors
+int threads_of_row(int64_t vecs, int most)
+{
+    int tpr = 8;
+    while (tpr < most && tpr < vecs) tpr *= 2;
+    return tpr;
+}
+
 struct SortSpace {
     size_t keys[2], pos[2], counts, crossing, parts, total;
     int tiles, window, windows;
@@ -1182,10 +1196,19 @@ SortSpace sort_space(const lmloss_embedding_args* a)
     SortSpace s{};
     const size_t T = static_cast<size_t>(a->T);
     s.tiles = static_cast<int>((a->T + kTile - 1) / kTile);
-    // windows of 32 positions, or fewer where those leave SMs without four blocks
-    const int64_t ranges = (a->D + kVec * kSumThreads - 1) / (kVec * kSumThreads);
+    // Windows of 32 positions, or fewer where those leave an SM without four windows, or without
+    // two blocks; four where the rows are fp32, of which a thread has half as many on their way
+    // (fp32 rows, 21064 x 64: 42 blocks 32.0 us, 165 blocks 26.5; 57897 x 137: 452 blocks 48.5, 905
+    // blocks 44.1; bf16 rows, 65536 x 128: 512 blocks 39.9, 1024 blocks 45.6).
+    const int64_t vecs = (a->D + kVec - 1) / kVec;
+    const int tpr = threads_of_row(vecs, kSumThreads);
+    const int64_t ranges = (vecs + tpr - 1) / tpr;
     s.window = kWindow;
-    while (s.window > 8 && (a->T + s.window - 1) / s.window * ranges < 600) s.window /= 2;
+    while (s.window > 8) {
+        const int64_t groups = (a->T + s.window - 1) / s.window * ranges;
+        if (groups >= 600 && groups * tpr / kSumThreads >= (a->rows_dtype == LMLOSS_FP32 ? 600 : 300)) break;
+        s.window /= 2;
+    }
     s.windows = static_cast<int>((a->T + s.window - 1) / s.window);
     s.ld_parts = (a->D + 7) / 8 * 8;
     size_t off = 0;
@@ -1219,20 +1242,6 @@ lmloss_status by_types(const lmloss_embedding_args* a, F&& f)
             return aligned ? f(table, rows, std::true_type{}) : f(table, rows, std::false_type{});
         });
     });
-}
-
-// vectors of the longest row, its first one possibly begun early
-int64_t row_vectors(const lmloss_embedding_args* a, int32_t written, bool aligned)
-{
-    return (a->D + (aligned ? 0 : 16 / float_bytes(written) - 1) + kVec - 1) / kVec;
-}
-
-// threads of a row: a power of two from 8 to `most`, as many as it has vectors
-int threads_of_row(int64_t vecs, int most)
-{
-    int tpr = 8;
-    while (tpr < most && tpr < vecs) tpr *= 2;
-    return tpr;
 }
 
 // A kernel that may be launched while the one before it on the stream still runs (it
