@@ -14,9 +14,10 @@
 // what the memory leaves waiting (0.57 instructions a cycle and scheduler, 7.4 for each
 // logit: the unpacking, the maximum, ex2 and the sum; long-scoreboard stalls the most),
 // with 512 blocks over 152 SMs, four on some and three on the others.  One sequence
-// of four beams at 128256: 10 to 11.5 us, latency from end to end: 1 us of loads, 2.5 us to
-// the part's candidates, 1 us to count the block, 6 us to pick.  512 rows that start at
-// no vector boundary: 82 us, each vector from two blocks.
+// of four beams at 128256: 10 to 11 us, latency from end to end: 1 us of loads, 2.5 us to
+// the part's candidates, 1 us to count the block, 5 us to pick.  512 rows of 262143, which start
+// at no vector boundary: 67.5 us, each vector from five words; rows of 262144 with one mask 60 us,
+// with a mask each 63.5.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -17,8 +17,8 @@
 //             join 17;
 //             16384 bf16 rows added to fp32 128256 x 4096: 76 us = 4.7 TB/s: sort 14 us, which
 //             nothing but a prefetch runs beside, sums 55 (72% of the DRAM's time), join 12;
-//             4097 of bf16 32003 x 1001 (no row on a vector boundary), whole: 30 us = 2.4 TB/s,
-//             three kernels of about 10 us, each a chain of latencies
+//             4097 of bf16 32003 x 1001 (no row on a vector boundary), whole: 25 us = 2.9 TB/s,
+//             three kernels of 6 to 10 us, each a chain of latencies
 #include <algorithm>
 #include <climits>
 #include <cmath>
