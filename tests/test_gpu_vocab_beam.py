@@ -165,6 +165,33 @@ def test_masks_lengths_and_finished(ops, dtype, B, K, M, V, per_row):
 
 
 @pytest.mark.parametrize("dtype", [BF, H, F])
+@pytest.mark.parametrize("V", [40007, 40008])
+@pytest.mark.parametrize("kind", ["lowest", "late", "few", "one late"])
+def test_masks_over_long_rows(ops, dtype, V, kind):
+    """The allowed logits lie far below the others, or come long after the first ones: rows that
+    one block reads alone, in several tiles."""
+    B, K, M = 57, 8, 12
+    z, s = inputs(B, K, V, dtype, V)
+    c = torch.arange(V, device="cuda")
+    if kind == "lowest":
+        may = (z < -6) & (c % 8 != 3)
+    elif kind == "late":
+        may = ((c > V - 500) & (c % 2 == 0)).expand(B * K, V)
+    elif kind == "few":
+        may = ((c % 997 == 0) & (c > 9000)).expand(B * K, V)
+    else:
+        may = (c == V - 2).expand(B * K, V).clone()
+        may[::3, 5] = True
+        may[1::5] = False
+    words = (V + 31) // 32
+    bits = torch.zeros(B * K, words * 32, device="cuda", dtype=torch.int64)
+    bits[:, :V] = may
+    word = (bits.view(B * K, words, 32) << torch.arange(32, device="cuda")).sum(2)
+    mask = torch.where(word >= 2 ** 31, word - 2 ** 32, word).int()
+    check(ops, z, s, M=M, mask=mask)
+
+
+@pytest.mark.parametrize("dtype", [BF, H, F])
 @pytest.mark.parametrize("V", [7, 513, 2048, 16384, 40000])
 @pytest.mark.parametrize("M", [1, 8, 64])
 @pytest.mark.parametrize("kind", ["constant", "few", "up", "down", "one_thread", "zeros"])
