@@ -363,7 +363,8 @@ typedef struct {
 lmloss_status lmloss_embedding_check_args(const lmloss_embedding_args* args);
 
 /* The workspace that lmloss_embedding_backward needs for `args` (pointers are
- * not looked at).  It grows with T and D. */
+ * not looked at) and for any call of no more positions and columns, whatever its
+ * types: it grows with T and D and depends on nothing else. */
 lmloss_status lmloss_embedding_workspace(const lmloss_embedding_args* args, size_t* bytes);
 
 /*

@@ -1224,6 +1224,23 @@ SortSpace sort_space(const lmloss_embedding_args* a)
     return s;
 }
 
+// What any gradient of up to T positions and D columns needs, whatever its rows' type.
+// A window is halved, from 2 w to w, only where 2 w leaves fewer than 600 groups or fewer than
+// 600 blocks of them: then ceil(T / 2 w) x ranges x tpr < 600 kSumThreads, where ranges x tpr is
+// at least the row's vectors and at least 8.  So a call has windows of 32, or at most `most` of
+// them and of their vectors; the bound on each grows with T and D, though a call's own need does
+// not (4800 positions of 4096 columns: 16 a window; 4096 positions: 8 a window, and more parts).
+size_t most_space(int64_t T, int64_t D)
+{
+    const int64_t vecs = (D + kVec - 1) / kVec, most = 2 * (600 * kSumThreads - 1);
+    const int64_t long_ = (T + kWindow - 1) / kWindow, short_ = (T + 7) / 8;
+    const int64_t windows = std::max(long_, std::min(short_, most / 8));
+    const int64_t parts = std::max(long_ * vecs, std::min(short_ * vecs, most)) * kVec;
+    const int64_t tiles = (T + kTile - 1) / kTile;
+    return 4 * vocab_align(4 * static_cast<size_t>(T)) + vocab_align(sizeof(uint32_t) * kDigits * static_cast<size_t>(tiles)) +
+           vocab_align(sizeof(uint32_t) * static_cast<size_t>(windows)) + vocab_align(sizeof(float) * 2 * static_cast<size_t>(parts));
+}
+
 template <class F>
 lmloss_status by_type(int32_t dtype, F&& f)
 {
@@ -1406,7 +1423,7 @@ lmloss_status lmloss_embedding_workspace(const lmloss_embedding_args* a, size_t*
     if (!bytes) return LMLOSS_ERR_INVALID_ARG;
     const lmloss_status st = check_embedding(a, false);
     if (st != LMLOSS_OK) return st;
-    *bytes = sort_space(a).total;
+    *bytes = most_space(a->T, a->D);
     return LMLOSS_OK;
 }
 
