@@ -323,7 +323,8 @@ typedef struct lmloss_vocab_ctx* lmloss_vocab_handle;
 
 /* A handle on `device` with `workspace_bytes` of workspace: the most that any of
  * its calls needs by lmloss_embedding_workspace / lmloss_beam_workspace (0 serves
- * the lookup and the reordering, which need none). */
+ * the lookup, the reordering and gradients of up to 1024 positions, which need
+ * none). */
 lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_t workspace_bytes);
 
 /* Free the handle and its workspace.  Synchronises the handle's device. */

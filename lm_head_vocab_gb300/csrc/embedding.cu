@@ -1423,7 +1423,7 @@ lmloss_status lmloss_embedding_workspace(const lmloss_embedding_args* a, size_t*
     if (!bytes) return LMLOSS_ERR_INVALID_ARG;
     const lmloss_status st = check_embedding(a, false);
     if (st != LMLOSS_OK) return st;
-    *bytes = most_space(a->T, a->D);
+    *bytes = a->T <= kFewPositions ? 0 : most_space(a->T, a->D);
     return LMLOSS_OK;
 }
 
@@ -1450,7 +1450,8 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
     if (!h) return LMLOSS_ERR_INVALID_ARG;
     lmloss_status st = check_embedding(a, true);
     if (st != LMLOSS_OK) return st;
-    const SortSpace s = sort_space(a);
+    const bool few = a->T <= kFewPositions;   // one launch, no workspace
+    const SortSpace s = few ? SortSpace{} : sort_space(a);
     if (s.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
     // column ranges are numbered by the grid's second dimension
     const bool aligned = aligned_rows(a);
@@ -1467,7 +1468,7 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
             return vocab_launch_err();
         });
     }
-    if (a->T <= kFewPositions) {
+    if (few) {
         const int64_t ranges = (vecs + kFewThreads - 1) / kFewThreads;
         int span = kFewSpan;   // or fewer rows, where that leaves SMs without four blocks
         while (span > 1 && (a->V + span - 1) / span * ranges < 4 * h->num_sms) span /= 2;

@@ -79,3 +79,27 @@ def test_smaller_calls_and_other_types_on_a_gpu(most, D, T, dtype):
     want = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, ids, rows.double())
     assert torch.equal(total.double(), want) and ops.device_error() == 0      # whole numbers: exact
     ops.close()
+
+
+def test_few_positions_need_none():
+    assert need(0, 8192) == need(1, 1) == need(1024, 8192) == 0 < need(1025, 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [0, 1, 1000, 1024])
+def test_few_positions_without_a_workspace(T):
+    import torch
+    import __graft_entry__
+    __graft_entry__.build()
+    from lm_head_vocab_gb300 import LMLossError, VocabOps
+    ops = VocabOps(0, max_tokens=0, max_rows=0)
+    assert ops.workspace_bytes == 0
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ids = torch.randint(0, 40, (T,), device="cuda", generator=g)
+    rows = torch.randint(-4, 5, (T, 33), device="cuda", generator=g).float()
+    total = ops.embedding_backward(rows, ids, num_embeddings=40)
+    assert torch.equal(total, torch.zeros(40, 33, device="cuda").index_add_(0, ids, rows))
+    with pytest.raises(LMLossError) as e:
+        ops.embedding_backward(torch.zeros(1025, 33, device="cuda"), torch.zeros(1025, device="cuda").long(), num_embeddings=40)
+    assert e.value.status == L.LMLOSS_ERR_INVALID_ARG
+    ops.close()
