@@ -605,6 +605,9 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
                                    static_cast<int64_t>(gridDim.x - q.blocks) * kClusterThreads);
         return;
     }
+    // No block writes to another's shared memory before that one has started: the wait is
+    // before the first such write, after the first pass's counting.
+    cluster_arrive_relaxed();
     uint2* buf = reinterpret_cast<uint2*>(mem);
     uint16_t* bin = reinterpret_cast<uint16_t*>(buf + 2 * q.share);
     uint32_t* totals = reinterpret_cast<uint32_t*>(bin + kClusterWarps * kClusterDigits);
@@ -685,6 +688,7 @@ __global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const Emb
                 run += n[w];
             }
             const uint32_t mine = smem_addr(totals + me * kPairs + d);
+            if (pass == 0) cluster_wait();
             for (int b = quarter; b < q.blocks; b += 4) st_cluster(dsmem_map(mine, b), total);
         }
         cluster_sync_all();
