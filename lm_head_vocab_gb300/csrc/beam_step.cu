@@ -22,20 +22,17 @@
 #include <cmath>
 #include <type_traits>
 
-#include "vocab_common.cuh"
+#include "beam_plan.cuh"
 
 namespace lmloss {
 namespace {
 
 constexpr int kMaxM = LMLOSS_MAX_BEAMS;
-constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;                   // candidate keys of a part held at once
 constexpr int kHits = 1024;                  // vectors of a part that reach its first threshold
 constexpr int kSmall = 256;                  // few enough to be ranked by counting
 constexpr int kFinal = 512;                  // candidates of a sequence held at once
-constexpr int kDepths = 8;                   // lists (parts of a sequence's rows) a thread
-constexpr int kMaxLists = kDepths * kThreads;
 
 struct BeamParams {
     const void* logits;
@@ -657,7 +654,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
     const int row = blockIdx.x / p.slices, part = blockIdx.x - row * p.slices;
     const int b = row / p.K;
     if (!(p.finished && p.finished[row])) {
-        // columns fit in 32 bits: V is at most kMaxLists parts of few tiles
         RowLogits<T> r;
         r.z = static_cast<const typename T::raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
         r.V = p.V;
@@ -670,8 +666,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_step_kernel(const __grid_con
             if (after < E) r.hi = p.V - 2 * E;
         }
         const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
-        const int begin = part * p.tiles * kTileCols;
-        const int end = min(begin + p.tiles * kTileCols, p.V);
+        const int begin = part * p.tiles * kTileCols, end = part_end(begin, p.tiles, kTileCols, p.V);
 
         if (tid == 0) {
             sm.count = 0;
@@ -889,44 +884,6 @@ lmloss_status check_beam(const lmloss_beam_args* a, bool pointers)
             return LMLOSS_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(a->logits) % float_bytes(a->dtype)) return LMLOSS_ERR_INVALID_ARG;
     }
-    return LMLOSS_OK;
-}
-
-struct BeamPlan {
-    int vpt, tiles, slices;
-    size_t keys, stats, total;
-};
-
-// Tiles of four vectors a thread, or of one where those would not give every SM a
-// block.  The parts of a row: a block costs its tiles and about eight more (the
-// thresholds' barriers, the ranking, the count; tiles of one are a quarter as long),
-// and an SM's blocks run together up to about three, one after another beyond.
-// Measured at 512 rows of 262144 bf16: one part 52 us, two 57; 32 rows: eleven parts 23.6
-// us, thirty-two 34.
-lmloss_status plan_beam(const lmloss_beam_args* a, int num_sms, BeamPlan& P)
-{
-    const int64_t rows = a->B * a->K, E = 16 / float_bytes(a->dtype);
-    auto tiles_of = [&](int vpt) { return (a->V + vpt * kThreads * E - 1) / (vpt * kThreads * E); };
-    P.vpt = rows * tiles_of(4) >= num_sms ? 4 : 1;
-    const int64_t all = tiles_of(P.vpt), fixed = P.vpt == 4 ? 8 : 32;
-    // at most kMaxLists parts in a sequence's rows
-    const int64_t most = kMaxLists / a->K, least = (all + most - 1) / most;
-    int64_t tiles = all, best = INT64_MAX;
-    for (int64_t t = least; t <= all && t <= least + 63; ++t) {
-        const int64_t blocks = rows * ((all + t - 1) / t);
-        const int64_t cost = std::max<int64_t>((blocks + num_sms - 1) / num_sms, 3) * (t + fixed);
-        if (cost < best) {
-            best = cost;
-            tiles = t;
-        }
-    }
-    const int64_t slices = (all + tiles - 1) / tiles;
-    if (tiles > (1 << 30) || rows * slices >= (int64_t(1) << 31)) return LMLOSS_ERR_UNSUPPORTED;
-    P.tiles = static_cast<int>(tiles);
-    P.slices = static_cast<int>(slices);
-    P.keys = 0;
-    P.stats = vocab_align(sizeof(uint64_t) * static_cast<size_t>(rows * slices * a->M));
-    P.total = P.stats + vocab_align(sizeof(float2) * static_cast<size_t>(rows * slices));
     return LMLOSS_OK;
 }
 
