@@ -28,7 +28,9 @@ lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_
         delete h;
         return LMLOSS_ERR_CUDA;
     }
-    if (cudaMemset(mem, 0, kHead + h->ws_bytes) != cudaSuccess) {
+    // A memset may return before it is done, and a stream that is not ordered after the legacy one
+    // would count blocks from what the memory held.
+    if (cudaMemset(mem, 0, kHead + h->ws_bytes) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(mem);
         delete h;
