@@ -61,7 +61,9 @@ lmloss_status lmloss_vocab_get_device_error(lmloss_vocab_handle h)
     if (!g.ok || cudaDeviceSynchronize() != cudaSuccess) return LMLOSS_ERR_CUDA;
     int code = 0;
     if (cudaMemcpy(&code, h->err, sizeof code, cudaMemcpyDeviceToHost) != cudaSuccess) return LMLOSS_ERR_CUDA;
-    if (cudaMemset(h->err, 0, sizeof code) != cudaSuccess) return LMLOSS_ERR_CUDA;
+    // done before it returns: it must not clear what the next call reports
+    if (cudaMemset(h->err, 0, sizeof code) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess)
+        return LMLOSS_ERR_CUDA;
     return static_cast<lmloss_status>(code);
 }
 

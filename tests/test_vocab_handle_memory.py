@@ -39,6 +39,15 @@ def test_counters_are_zero_when_create_returns(tmp_path):
 """)
 
 
+def test_the_error_word_is_clear_when_it_has_been_read(tmp_path):
+    run(tmp_path, "vocab_handle.cu", """
+    lmloss_vocab_handle h;
+    if (lmloss_vocab_create(&h, 0, 0) != LMLOSS_OK || lmloss_vocab_get_device_error(h) != LMLOSS_OK) return 1;
+    if (unfinished_fills() != 0) return std::printf("the next call's error may still be cleared\\n"), 2;
+    if (lmloss_vocab_destroy(h) != LMLOSS_OK) return 3;
+""")
+
+
 @pytest.mark.gpu
 def test_first_call_on_a_side_stream_under_work_on_the_default_one():
     import torch
