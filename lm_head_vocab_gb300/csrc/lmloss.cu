@@ -444,7 +444,9 @@ lmloss_status lmloss_create(lmloss_handle* handle, int device, int64_t max_T, in
     h->ws.done = reinterpret_cast<unsigned*>(base + o_done);
     h->ws.err = reinterpret_cast<int*>(base + o_err);
     h->ev = static_cast<cudaEvent_t*>(std::calloc(2 * lmloss_ctx::kMaxTimed, sizeof(cudaEvent_t)));
-    if (!h->ev || cudaMemset(h->ws_mem, 0, off) != cudaSuccess) {
+    // A memset may return before it is done, and a stream that is not ordered after the legacy one
+    // would count blocks from what the memory held.
+    if (!h->ev || cudaMemset(h->ws_mem, 0, off) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
         std::free(h->ev);
         cudaFree(h->ws_mem);
         delete h;
@@ -521,7 +523,8 @@ lmloss_status lmloss_get_device_error(lmloss_handle h)
     if (!g.ok || cudaDeviceSynchronize() != cudaSuccess) return LMLOSS_ERR_CUDA;
     int code = 0;
     if (cudaMemcpy(&code, h->ws.err, sizeof code, cudaMemcpyDeviceToHost) != cudaSuccess) return LMLOSS_ERR_CUDA;
-    if (cudaMemset(h->ws.err, 0, sizeof code) != cudaSuccess) return LMLOSS_ERR_CUDA;
+    if (cudaMemset(h->ws.err, 0, sizeof code) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess)
+        return LMLOSS_ERR_CUDA;
     return static_cast<lmloss_status>(code);
 }
 
@@ -536,7 +539,8 @@ lmloss_status lmloss_selftest_bounded_wait(lmloss_handle h, long long limit_cycl
     if (cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return LMLOSS_ERR_CUDA;
     int code = 0;
     if (cudaMemcpy(&code, h->ws.err, sizeof code, cudaMemcpyDeviceToHost) != cudaSuccess) return LMLOSS_ERR_CUDA;
-    if (cudaMemset(h->ws.err, 0, sizeof code) != cudaSuccess) return LMLOSS_ERR_CUDA;
+    if (cudaMemset(h->ws.err, 0, sizeof code) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess)
+        return LMLOSS_ERR_CUDA;
     return static_cast<lmloss_status>(code);
 }
 
@@ -879,10 +883,10 @@ struct NoAllocLayout {
     static constexpr size_t total = err + na_align(16);
 };
 
-// The workspace itself (about 1.2 MB).  The set-up below clears it once per
-// device, so the block counters that must start every call at zero do; the
-// kernels return those counters to zero at the end of each call and clear the
-// per-call accumulators themselves at its start.
+// The workspace itself (about 1.2 MB).  It is zero when the module loads, so the
+// block counters that must start every call at zero do (a memset from here could
+// land while the first call runs); the kernels return those counters to zero at
+// the end of each call and clear the per-call accumulators themselves at its start.
 static __device__ __align__(256) unsigned char g_noalloc_scratch[NoAllocLayout::total];
 
 constexpr int kNoAllocMaxDevices = 64;
@@ -912,13 +916,6 @@ lmloss_status noalloc_setup(int device, NoAllocDevice** out)
         if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
             cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) != cudaSuccess)
             return LMLOSS_ERR_CUDA;
-        // the block counters must start at zero; the array is zero when the
-        // module loads, and clearing it here states that rather than relying on it
-        // (a synchronous memset of memory the library owns: no allocation)
-        if (cudaMemset(ptr, 0, NoAllocLayout::total) != cudaSuccess) {
-            cudaGetLastError();
-            return LMLOSS_ERR_CUDA;
-        }
         d.scratch = static_cast<unsigned char*>(ptr);
         d.ready = true;
     }

@@ -18,14 +18,16 @@ def run(tmp_path, unit, body):
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         pytest.skip("no C++ compiler")
-    main, obj, exe = str(tmp_path / "main.cpp"), str(tmp_path / "unit.o"), str(tmp_path / "main")
+    main, obj, lib, exe = (str(tmp_path / n) for n in ("main.cpp", "unit.o", "libunit.so", "main"))
     with open(main, "w") as f:
         f.write('#include <cstdio>\n#include "lmloss.h"\nint unfinished_fills();\nint main()\n{\n' + body + "    return 0;\n}\n")
     subprocess.run([L._nvcc(), "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-O1", "-Xcompiler", "-fPIC",
                     "-c", "-o", obj, os.path.join(CSRC, unit)], check=True)
-    subprocess.run([cxx, "-std=c++17", "-I", os.path.join(HERE, "..", "include"), "-I", os.path.join(CUDA, "include"),
-                    "-o", exe, main, os.path.join(HERE, "vocab_fake_runtime.cpp"), obj, "-lpthread",
-                    "-Wl,--unresolved-symbols=ignore-all", "-Wl,-z,lazy"], check=True)
+    cxx = [cxx, "-std=c++17", "-fPIC", "-I", os.path.join(HERE, "..", "include"), "-I", os.path.join(CUDA, "include")]
+    # what `body` does not reach stays unresolved
+    subprocess.run([*cxx, "-shared", "-Wl,-z,lazy", "-o", lib, os.path.join(HERE, "vocab_fake_runtime.cpp"), obj], check=True)
+    subprocess.run([*cxx, "-Wl,-z,lazy", "-Wl,--allow-shlib-undefined", "-o", exe, main, lib, "-Wl,-rpath," + str(tmp_path),
+                    "-lpthread"], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
 
@@ -46,6 +48,24 @@ def test_the_error_word_is_clear_when_it_has_been_read(tmp_path):
     if (unfinished_fills() != 0) return std::printf("the next call's error may still be cleared\\n"), 2;
     if (lmloss_vocab_destroy(h) != LMLOSS_OK) return 3;
 """)
+
+
+def test_the_loss_handle_keeps_to_the_same(tmp_path):
+    run(tmp_path, "lmloss.cu", """
+    lmloss_handle h;
+    if (lmloss_create(&h, 0, 1024, 4) != LMLOSS_OK) return 1;
+    if (unfinished_fills() != 0) return std::printf("create returned before its memory was zero\\n"), 2;
+    if (lmloss_get_device_error(h) != LMLOSS_OK) return 3;
+    if (unfinished_fills() != 0) return std::printf("the next call's error may still be cleared\\n"), 4;
+    if (lmloss_destroy(h) != LMLOSS_OK) return 5;
+""")
+
+
+def test_the_fixed_workspace_is_not_cleared_under_its_first_call():
+    # it is zero when the module loads; its set-up runs inside the first call
+    text = open(os.path.join(CSRC, "lmloss.cu")).read()
+    setup = text[text.index("lmloss_status noalloc_setup"):text.index('extern "C" lmloss_status lmloss_forward_backward_noalloc')]
+    assert "static __device__ __align__(256) unsigned char g_noalloc_scratch" in text and "Memset" not in setup
 
 
 @pytest.mark.gpu
