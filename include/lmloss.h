@@ -426,7 +426,8 @@ lmloss_status lmloss_beam_workspace(const lmloss_beam_args* args, size_t* bytes)
 /*
  * For each sequence, the M best candidates (k, v) by score
  *   scores[k] + logits[k][v] - lse_k,   lse_k = logsumexp of the whole row,
- * (divided by length^alpha for the ranking), best first, equal ones by k, then by
+ * (divided by length^alpha for the ranking, or by the largest double where that
+ * passes it), best first, equal ones by k, then by
  * v.  Rows are ranked against one another in fp64; scores_out holds the score
  * before the division, rounded to fp32.
  *   - A finished beam's row is not read: its one candidate is (k, eos_token) with

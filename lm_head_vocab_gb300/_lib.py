@@ -23,7 +23,7 @@ UNITS = [("lmloss.cu", [], "lmloss.o")] + [
     # the vocabulary operators
     (f"{name}.cu", [], f"{name}.o") for name in ("vocab_handle", "embedding", "beam_step", "beam_reorder")]
 DEPENDS = ["lmloss.cu", "fused_inst.cu", "fused_entry.cuh", "kernels.cuh", "aux_kernels.cuh", "ptx.cuh",
-           "vocab_common.cuh", "vocab_handle.cu", "embedding.cu", "beam_plan.cuh", "beam_step.cu", "beam_reorder.cu"]
+           "vocab_common.cuh", "vocab_handle.cu", "embedding.cu", "beam_math.cuh", "beam_plan.cuh", "beam_step.cu", "beam_reorder.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC"]

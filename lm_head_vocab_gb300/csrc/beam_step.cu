@@ -22,6 +22,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "beam_math.cuh"
 #include "beam_plan.cuh"
 
 namespace lmloss {
@@ -300,45 +301,6 @@ __device__ __noinline__ void pick_by_rounds(const BeamParams& p, Shared& sm, con
     }
 }
 
-// ln(hi + lo) for a sum of at least 1, to about 1e-9, from fp32 operations alone but
-// for its last three additions (fp64 runs at a sixty-fourth of fp32's rate here).
-// hi + lo = 2^e f with f in [0.7, 1.42), ln f = 2 artanh(q) with q = (f - 1) / (f + 1):
-// q is carried as a quotient and its remainder, the series' higher terms in fp32.
-__device__ __forceinline__ double log_of_sum(float hi, float lo)
-{
-    if (!(hi < INFINITY)) return static_cast<double>(hi);   // NaN
-    int e = static_cast<int>(__float_as_uint(hi) >> 23) - 127;
-    float scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    if (hi * scale > 1.4142135f) {
-        ++e;
-        scale *= 0.5f;
-    }
-    const float f = hi * scale, g = lo * scale;
-    const float num = f - 1.f, den = f + 1.f, den_lo = (f - (den - 1.f)) + g;
-    const float q = num / den;
-    const float rest = (fmaf(-q, den, num) + fmaf(-q, den_lo, g)) / den;
-    const float q2 = q * q;
-    const float t = q2 * fmaf(q2, fmaf(q2, fmaf(q2, fmaf(q2, 1.f / 11, 1.f / 9), 1.f / 7), 0.2f), 1.f / 3);
-    return fma(static_cast<double>(e), 0.693147180559945309417, 2.0 * static_cast<double>(q)) +
-           static_cast<double>(2.f * fmaf(q, t, rest));
-}
-
-// n^a for n >= 1 and a > 0, to about 1e-9: e^(a ln n) = 2^i e^r with |r| <= ln 2 / 2, the
-// series' terms from r^3 on in fp32.
-__device__ __forceinline__ double power(int n, double a)
-{
-    if (a == 1.0) return static_cast<double>(n);
-    const float hi = static_cast<float>(n);
-    const double y = a * log_of_sum(hi, static_cast<float>(n - static_cast<int64_t>(hi)));
-    const float i = rintf(static_cast<float>(y) * kLog2e);
-    if (!(i < 1000.f)) return pow(static_cast<double>(n), a);   // near the range's end
-    const double r = fma(static_cast<double>(i), -0.693147180559945309417, y);
-    const float f = static_cast<float>(r);
-    const float tail = f * f * f * fmaf(f, fmaf(f, fmaf(f, fmaf(f, 1.f / 5040, 1.f / 720), 1.f / 120), 1.f / 24), 1.f / 6);
-    const double e = 1.0 + (r + (0.5 * r * r + static_cast<double>(tail)));
-    return e * __longlong_as_double((static_cast<long long>(i) + 1023LL) << 52);
-}
-
 // The block that finishes a sequence's last part picks its M best.
 __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
 {
@@ -418,17 +380,11 @@ __device__ __noinline__ void pick(const BeamParams& p, Shared& sm, const int b)
     }
     __syncthreads();
 
-    // ---- a threshold in fp32.  Each candidate's rank key lies within `err` of its
-    // fp32 value: at most six roundings of 2^-24 of the terms.
+    // ---- a threshold in fp32, from bounds on the candidates' rank keys
     auto bounds = [&](int k, uint64_t key, float& low, float& high) {
         low = high = -INFINITY;
-        const float base = sm.base_f[k], inv = sm.inv_f[k];
         if (key == 0 || sm.state[k] == kOut) return;
-        const float z = sm.state[k] == kFinished ? 0.f : key_logit(key);
-        const float x = (base + z) * inv, err = (fabsf(base) + fabsf(z)) * inv * 4.8e-7f + 1e-37f;
-        const bool fine = fabsf(x) < INFINITY && err < INFINITY;
-        low = fine ? x - err : -INFINITY;
-        high = fine ? x + err : INFINITY;
+        rank_bounds(sm.base_f[k], sm.state[k] == kFinished ? 0.f : key_logit(key), sm.inv_f[k], low, high);
     };
     // a finished row has one candidate
     auto own_key = [&](int list, int d, uint64_t key) {
