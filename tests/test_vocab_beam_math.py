@@ -1,7 +1,5 @@
 """The logarithms, powers and bounds by which a beam step orders its candidates, on the host against
 fp64 and long double."""
-import pytest
-
 from tests import vocab_host
 
 HEAD = r"""
@@ -38,3 +36,37 @@ int main()
 
 def test_rank_keys_lie_within_their_bounds(tmp_path):
     vocab_host.run(tmp_path, BOUNDS)
+
+
+ERRORS = HEAD + r"""
+// largest error of the logarithm, then for each exponent largest relative error of the power
+int main()
+{
+    std::mt19937_64 gen(2);
+    std::uniform_real_distribution<double> u(0, 1);
+    double worst = 0;
+    for (int i = 0; i < 3000000; ++i) {
+        const float hi = i < 100000 ? 1 + i * 1e-5f : static_cast<float>(std::exp(u(gen) * 22));
+        const float lo = static_cast<float>(hi * (u(gen) - 0.5) * 1.1920929e-7);
+        worst = std::max(worst, static_cast<double>(std::fabs(log_of_sum(hi, lo) - std::log(static_cast<long double>(hi) + lo))));
+    }
+    std::printf("0 %g\n", worst);
+    for (double a : {0.01, 0.1, 0.3, 0.6, 0.9, 1.0, 1.5, 2.0, 2.5, 5.0, 10.0, 16.0, 40.0, 50.0, 60.0}) {
+        double w = 0;
+        for (int i = 1; i < 200000; ++i) {
+            const int n = i < 100000 ? i : 100000 + static_cast<int>(u(gen) * 2147383647.0);
+            const long double exact = std::pow(static_cast<long double>(n), static_cast<long double>(a));
+            if (exact < 1.7e308L) w = std::max(w, static_cast<double>(std::fabs(power(n, a) / exact - 1)));
+        }
+        std::printf("%g %g\n", a, w);
+    }
+    return 0;
+}
+"""
+
+
+def test_logarithm_and_power_are_as_close_as_they_say(tmp_path):
+    # what beam_math.cuh states: 3e-9, and of itself 3e-9 (1 + exponent)
+    for line in vocab_host.run(tmp_path, ERRORS):
+        a, error = map(float, line.split())
+        assert error <= 3e-9 * (1 + a), line
