@@ -447,7 +447,9 @@ lmloss_status lmloss_beam_step(lmloss_vocab_handle handle, const lmloss_beam_arg
  * r = b * K + k a run of `inner` bytes at
  *   base + r * row_stride + o0 * outer_stride[0] + o1 * outer_stride[1] + o2 * outer_stride[2].
  * dst == src reorders in place (then with the same strides and K_out == K);
- * otherwise the two must not overlap.  Strides are in bytes and not negative; no
+ * otherwise the two must not overlap (halves of a double buffer may lie
+ * interleaved, at any dimension; sides entangled in other ways are refused).
+ * Strides are in bytes and not negative; no
  * two runs of dst may overlap.
  */
 typedef struct {

@@ -8,6 +8,7 @@
 // (a beam taken twice is read once from DRAM); 4 caches of 64 x 4 x 777 x 80 in place, 2 of 4
 // beams moving, 20 us = 6.3 TB/s; token histories, 2.7 us.
 #include <climits>
+#include <numeric>
 
 #include "vocab_common.cuh"
 
@@ -168,6 +169,36 @@ int64_t reach(int64_t row_stride, int64_t rows, const int64_t* outer, const int6
     return r > (static_cast<__int128>(1) << 62) ? -1 : static_cast<int64_t>(r);
 }
 
+// No byte of one side of a state is one of the other's.  The sides may lie interleaved (halves of
+// a double buffer with the halves inside a row): where all strides above some size are multiples
+// of g, each side's bytes are those of a block of the smaller dimensions, repeated every so many
+// times g, so the two are apart if such blocks are, modulo g.
+bool apart(const lmloss_beam_state& s, int64_t rows, int64_t rows_out, int64_t reach_src, int64_t reach_dst)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(s.src), d = reinterpret_cast<uintptr_t>(s.dst);
+    if (a + static_cast<uintptr_t>(reach_src) <= d || d + static_cast<uintptr_t>(reach_dst) <= a) return true;
+    const int64_t stride[2][4] = {{s.src_row_stride, s.src_outer_stride[0], s.src_outer_stride[1], s.src_outer_stride[2]},
+                                  {s.dst_row_stride, s.dst_outer_stride[0], s.dst_outer_stride[1], s.dst_outer_stride[2]}};
+    const int64_t count[2][4] = {{rows, s.outer[0], s.outer[1], s.outer[2]}, {rows_out, s.outer[0], s.outer[1], s.outer[2]}};
+    for (int i = 0; i < 8; ++i) {
+        // what counts as large: a stride of either side, and all above it
+        const int64_t least = stride[i / 4][i % 4];
+        if (least == 0) continue;
+        int64_t g = 0, block[2] = {s.inner, s.inner};
+        for (int x = 0; x < 2; ++x)
+            for (int k = 0; k < 4; ++k) {
+                if (count[x][k] < 2) continue;
+                if (stride[x][k] >= least) g = std::gcd(g, stride[x][k]);
+                else block[x] += (count[x][k] - 1) * stride[x][k];
+            }
+        if (g == 0) continue;
+        const uint64_t u = static_cast<uint64_t>(g);
+        const int64_t from = a <= d ? static_cast<int64_t>((d - a) % u) : static_cast<int64_t>((u - (a - d) % u) % u);
+        if (block[0] <= from && block[1] <= g - from) return true;
+    }
+    return false;
+}
+
 bool empty(const lmloss_beam_state& s)
 {
     return s.inner == 0 || s.outer[0] == 0 || s.outer[1] == 0 || s.outer[2] == 0;
@@ -197,10 +228,7 @@ lmloss_status check_states(const lmloss_beam_state* states, int32_t n, int64_t B
         const int64_t rs = reach(s.src_row_stride, B * K, s.outer, s.src_outer_stride, s.inner);
         const int64_t rd = reach(s.dst_row_stride, B * K_out, s.outer, s.dst_outer_stride, s.inner);
         if (rs < 0 || rd < 0) return LMLOSS_ERR_INVALID_ARG;
-        if (s.src != s.dst) {
-            const uintptr_t a = reinterpret_cast<uintptr_t>(s.src), d = reinterpret_cast<uintptr_t>(s.dst);
-            if (a < d + static_cast<uintptr_t>(rd) && d < a + static_cast<uintptr_t>(rs)) return LMLOSS_ERR_INVALID_ARG;
-        }
+        if (s.src != s.dst && !apart(s, B * K, B * K_out, rs, rd)) return LMLOSS_ERR_INVALID_ARG;
     }
     return LMLOSS_OK;
 }
