@@ -218,8 +218,10 @@ lmloss_status check_states(const lmloss_beam_state* states, int32_t n, int64_t B
         }
         if (B == 0 || empty(s)) continue;
         if (!s.src || !s.dst) return LMLOSS_ERR_INVALID_ARG;
-        // the runs of one sequence's new beams are apart
-        if (K_out > 1 && s.dst_row_stride == 0) return LMLOSS_ERR_INVALID_ARG;
+        // neighbouring runs of dst are apart
+        if (B * K_out > 1 && s.dst_row_stride < s.inner) return LMLOSS_ERR_INVALID_ARG;
+        for (int k = 0; k < 3; ++k)
+            if (s.outer[k] > 1 && s.dst_outer_stride[k] < s.inner) return LMLOSS_ERR_INVALID_ARG;
         if (s.src == s.dst) {
             if (K != K_out || s.src_row_stride != s.dst_row_stride) return LMLOSS_ERR_INVALID_ARG;
             for (int k = 0; k < 3; ++k)

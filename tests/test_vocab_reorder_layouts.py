@@ -72,6 +72,20 @@ def test_interleaved_halves_are_taken(swap):
     assert check(state(a, a + 4, 4, (32, 32), [1, 1, 1], [0, 0, 0], [0, 0, 0])) == OK
 
 
+def test_runs_written_on_top_of_one_another_are_refused():
+    def st(dst_row, dst_outer, outer=(1, 1, 1), inner=16):
+        return state(0x10000, 0x40000, inner, (64, dst_row), list(outer), [16, 16, 16], [dst_outer] * 3)
+    assert check(st(64, 0)) == OK and check(st(16, 0)) == OK
+    assert check(st(0, 0)) == BAD and check(st(15, 0)) == BAD
+    assert check(st(0, 0), B=3, K=1, K_out=1) == BAD          # one beam a sequence: rows of three sequences
+    assert check(st(0, 0), B=1, K=1, K_out=1) == OK
+    assert check(st(0, 0, inner=0), B=3, K=1, K_out=1) == OK  # nothing is written
+    for k in range(3):
+        outer = [3 if i == k else 1 for i in range(3)]
+        assert check(st(64, 16, outer)) == OK
+        assert check(st(64, 0, outer)) == BAD and check(st(64, 15, outer)) == BAD
+
+
 @pytest.fixture(scope="module")
 def ops():
     import __graft_entry__
