@@ -99,7 +99,7 @@ def test_few_positions_without_a_workspace(T):
     rows = torch.randint(-4, 5, (T, 33), device="cuda", generator=g).float()
     total = ops.embedding_backward(rows, ids, num_embeddings=40)
     assert torch.equal(total, torch.zeros(40, 33, device="cuda").index_add_(0, ids, rows))
-    with pytest.raises(LMLossError) as e:
+    # (the exception is not kept: it would hold this call's tensors)
+    with pytest.raises(LMLossError, match=f"status {L.LMLOSS_ERR_INVALID_ARG}"):
         ops.embedding_backward(torch.zeros(1025, 33, device="cuda"), torch.zeros(1025, device="cuda").long(), num_embeddings=40)
-    assert e.value.status == L.LMLOSS_ERR_INVALID_ARG
     ops.close()
