@@ -449,8 +449,7 @@ lmloss_status lmloss_beam_step(lmloss_vocab_handle handle, const lmloss_beam_arg
  * dst == src reorders in place (then with the same strides and K_out == K);
  * otherwise the two must not overlap (halves of a double buffer may lie
  * interleaved, at any dimension; sides entangled in other ways are refused).
- * Strides are in bytes and not negative; no
- * two runs of dst may overlap.
+ * Strides are in bytes and not negative; no two runs of dst may overlap.
  */
 typedef struct {
     const void* src;
@@ -470,7 +469,9 @@ lmloss_status lmloss_beam_check_states(const lmloss_beam_state* states, int32_t 
 /*
  * Every state's row b * K_out + m becomes its row b * K + parents[b, m]
  * (parents: [B, K_out] int32, device).  `states` is a host array, read during the
- * call.  A parent outside [0, K) sets LMLOSS_ERR_BAD_PARENT and leaves that row of
+ * call.  The states move side by side, in no order: no state's dst may overlap
+ * another's src or dst (two that begin at the same byte are refused, so a swap
+ * of two buffers, or one state given twice in place).  A parent outside [0, K) sets LMLOSS_ERR_BAD_PARENT and leaves that row of
  * dst as it is.
  */
 lmloss_status lmloss_beam_reorder(lmloss_vocab_handle handle, const lmloss_beam_state* states, int32_t num_states,

@@ -230,6 +230,11 @@ lmloss_status check_states(const lmloss_beam_state* states, int32_t n, int64_t B
         const int64_t rs = reach(s.src_row_stride, B * K, s.outer, s.src_outer_stride, s.inner);
         const int64_t rd = reach(s.dst_row_stride, B * K_out, s.outer, s.dst_outer_stride, s.inner);
         if (rs < 0 || rd < 0) return LMLOSS_ERR_INVALID_ARG;
+        // states move side by side: what one writes is not another's (the same start is seen here)
+        for (int j = 0; j < n; ++j)
+            if (j != i && !empty(states[j]) &&
+                (s.dst == states[j].src || (s.dst == states[j].dst && s.src != states[j].src)))
+                return LMLOSS_ERR_INVALID_ARG;
         if (s.src != s.dst && !apart(s, B * K, B * K_out, rs, rd)) return LMLOSS_ERR_INVALID_ARG;
     }
     return LMLOSS_OK;

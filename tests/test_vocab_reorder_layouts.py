@@ -86,6 +86,20 @@ def test_runs_written_on_top_of_one_another_are_refused():
         assert check(st(64, 0, outer)) == BAD and check(st(64, 15, outer)) == BAD
 
 
+def test_states_that_write_to_one_another_are_refused():
+    def st(src, dst, inner=64):
+        return state(src, dst, inner, (64, 64), [1, 1, 1], [0, 0, 0], [0, 0, 0])
+    a, b, c, d = 0x10000, 0x20000, 0x30000, 0x40000
+    assert check(st(a, c), st(b, d)) == OK and check(st(a, a), st(b, b)) == OK
+    assert check(st(a, c), st(a, d)) == OK                 # one source for two
+    assert check(st(a, b), st(b, a)) == BAD                # a swap
+    assert check(st(a, b), st(c, a)) == BAD and check(st(c, a), st(a, b)) == BAD
+    assert check(st(a, c), st(b, c)) == BAD
+    assert check(st(a, a), st(a, a)) == BAD                # twice in place
+    assert check(st(a, a), st(a, b)) == BAD and check(st(a, b), st(b, b)) == BAD
+    assert check(st(a, b), st(b, a, inner=0)) == OK        # nothing moves
+
+
 @pytest.fixture(scope="module")
 def ops():
     import __graft_entry__
