@@ -46,6 +46,8 @@ def _matrix(t: torch.Tensor, name: str, index: int):
         raise ValueError(f"{name}: on {t.device}, the handle on cuda:{index}")
     if t.dim() != 2:
         raise ValueError(f"{name}: must have two dimensions")
+    if t.is_neg():
+        raise ValueError(f"{name}: a lazily negated or conjugated view; resolve it first")
     rows, cols = t.size(0), t.size(1)
     ld, unit = t.stride()
     if rows <= 1:
@@ -324,6 +326,8 @@ class VocabOps:
             raise ValueError(f"states: on {t.device} and {o.device}, the handle on {self.device}")
         if t.dtype != o.dtype:
             raise TypeError(f"out: {o.dtype} for a state of {t.dtype}")
+        if t.is_conj() != o.is_conj() or t.is_neg() != o.is_neg():
+            raise ValueError("states: a lazily negated or conjugated view on one side; resolve it first")
         shape, oshape, ts, os_ = t.shape, o.shape, t.stride(), o.stride()
         d = dim if dim >= 0 else dim + len(shape)
         if shape[d] != rows:
