@@ -292,9 +292,9 @@ class VocabOps:
         if not states:
             return []
         rows = states[0].size(dim)
-        if B == 0 or rows % B:
+        if rows % B if B else rows:
             raise ValueError(f"states: {rows} rows along dim {dim} for {B} sequences")
-        K = rows // B
+        K = rows // B if B else Ko
         if not 1 <= Ko <= _lib.LMLOSS_MAX_BEAMS or not 1 <= K <= _lib.LMLOSS_MAX_BEAMS:
             raise ValueError(f"beams: 1 to {_lib.LMLOSS_MAX_BEAMS} a sequence, got {K} and {Ko}")
         if stream is None:

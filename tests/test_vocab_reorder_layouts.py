@@ -130,3 +130,17 @@ def test_halves_at_any_place_of_a_cache(ops, dim):
     assert torch.equal(dst, want) and ops.device_error() == 0
     dst.copy_(before.select(dim, 1)[:, :, :7])
     assert torch.equal(kv, before)                    # nothing else was written
+
+
+@pytest.mark.gpu
+def test_no_sequences(ops):
+    # what a beam step over no sequences leaves can be reordered too
+    parents = torch.empty(0, 4, dtype=torch.int32, device="cuda")
+    states = [torch.empty(0, 7, device="cuda"), torch.empty(0, 2, 3, device="cuda", dtype=torch.bfloat16)]
+    got = ops.beam_reorder(states, parents)
+    assert [t.shape for t in got] == [t.shape for t in states] and [t.dtype for t in got] == [t.dtype for t in states]
+    assert ops.beam_reorder(states, parents, out="inplace") == states
+    kv = torch.empty(2, 0, 5, device="cuda")
+    assert ops.beam_reorder([kv], parents, dim=1)[0].shape == (2, 0, 5)
+    with pytest.raises(ValueError):
+        ops.beam_reorder([torch.empty(4, 7, device="cuda")], parents)
