@@ -118,6 +118,15 @@ class VocabOps:
         """Read and clear the handle's error word (synchronises the device)."""
         return _lib.lmloss_vocab_get_device_error(self.handle)
 
+    def _refused(self, status, where, args, check, workspace):
+        """The error for a refused call: where the arguments are in order, what the workspace lacks."""
+        if status == _lib.LMLOSS_ERR_INVALID_ARG and check(args) == _lib.LMLOSS_OK:
+            need = workspace(args)
+            if need > self.workspace_bytes:
+                where += (f" ({need} bytes of workspace needed, {self.workspace_bytes} there: the handle's max_tokens, "
+                          f"max_dim, max_rows or max_vocab is too small)")
+        return LMLossError(status, where)
+
     # ------------------------------------------------------------- streams
     def _enter(self, stream, *tensors):
         """(stream, context for allocations) for a call on a stream of the caller's: where that is not
@@ -208,7 +217,8 @@ class VocabOps:
                                        id_type, t_type, r_type, scale, 1 if accumulate else 0)
         st = self._backward(self.handle, a, raw)
         if st != _lib.LMLOSS_OK:
-            raise LMLossError(st, "lmloss_embedding_backward")
+            raise self._refused(st, "lmloss_embedding_backward", a, _lib.lmloss_embedding_check_args,
+                                _lib.lmloss_embedding_workspace)
         return grad_weight
 
     # ---------------------------------------------------------------- beams
@@ -264,7 +274,7 @@ class VocabOps:
                                   r.finished.data_ptr(), None if length is None else r.lengths.data_ptr())
         st = self._step(self.handle, a, raw)
         if st != _lib.LMLOSS_OK:
-            raise LMLossError(st, "lmloss_beam_step")
+            raise self._refused(st, "lmloss_beam_step", a, _lib.lmloss_beam_check_args, _lib.lmloss_beam_workspace)
         return r
 
     @staticmethod
