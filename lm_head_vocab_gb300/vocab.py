@@ -58,6 +58,16 @@ def _matrix(t: torch.Tensor, name: str, index: int):
     return dtype, rows, cols, ld
 
 
+def _flat(t: torch.Tensor, name: str, T: int, D: int):
+    """[..., D] as the [T, D] that a call takes."""
+    if t.dim() == 2:
+        return t
+    try:
+        return t.view(T, D)
+    except RuntimeError:
+        raise ValueError(f"{name}: the positions of a tensor of more dimensions must lie one row stride apart") from None
+
+
 @dataclass
 class BeamStep:
     scores: torch.Tensor                        # [B, M] float32
@@ -155,7 +165,8 @@ class VocabOps:
                           stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """scale * weight[ids], [*ids.shape, D]: weight [V, D] and the result each
         bfloat16, float16 or float32 (the weight's type if not said).  An id of -100
-        gives zeros; another outside [0, V) NaN and the error word."""
+        gives zeros; another outside [0, V) NaN and the error word.  ids are contiguous;
+        out's rows may be strided, one stride between them all."""
         id_type = self._ids(ids)
         w_type, V, D, ld = _matrix(weight, "weight", self._index)
         if stream is None:
@@ -178,7 +189,7 @@ class VocabOps:
         else:
             if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
                 raise ValueError(f"out: expected {shape}{'' if out_dtype is None else f' of {out_dtype}'}")
-            r_type, _, _, ld_rows = _matrix(out if out.dim() == 2 else out.view(T, D), "out", self._index)
+            r_type, _, _, ld_rows = _matrix(_flat(out, "out", T, D), "out", self._index)
         a = _lib.lmloss_embedding_args(ids.data_ptr(), T, V, D, weight.data_ptr(), ld, out.data_ptr(), ld_rows,
                                        id_type, w_type, r_type, scale, 0)
         st = self._forward(self.handle, a, raw)
@@ -194,12 +205,13 @@ class VocabOps:
         grad_weight is written as a whole, or with accumulate added to (a table tied
         to the LM head: the head's own gradient is there already); without it one of
         num_embeddings rows in grad's type is made.  Sums run in fp32 in an order
-        that the ids alone fix."""
+        that the ids alone fix.  ids are contiguous; grad's rows may be strided, one
+        stride between them all."""
         id_type = self._ids(ids)
         if grad.shape[:-1] != ids.shape:
             raise ValueError(f"grad: expected [*{tuple(ids.shape)}, D], got {tuple(grad.shape)}")
         T = ids.numel()
-        rows = grad if grad.dim() == 2 else grad.view(T, grad.shape[-1])
+        rows = _flat(grad, "grad", T, grad.shape[-1])
         r_type, _, D, ld_rows = _matrix(rows, "grad", self._index)
         if stream is None:
             raw, ctx = _raw_stream(self._index), contextlib.nullcontext()

@@ -43,6 +43,16 @@ def test_a_workspace_that_is_too_small_is_named(ops):
     assert e.status == L.LMLOSS_ERR_CUDA and "bytes" not in str(e)
 
 
+def test_positions_without_one_row_stride_are_a_value_error(ops, monkeypatch):
+    monkeypatch.setattr("lm_head_vocab_gb300.vocab._raw_stream", lambda index: 0)
+    ids = torch.zeros(2, 4, dtype=torch.int64)
+    whole = torch.randn(2, 5, 8)
+    with pytest.raises(ValueError, match="one row stride"):
+        ops.embedding_backward(whole[:, :-1], ids, torch.zeros(9, 8))
+    with pytest.raises(ValueError, match="one row stride"):
+        ops.embedding_forward(torch.randn(9, 8), ids, out=whole[:, :-1])
+
+
 @pytest.mark.gpu
 def test_a_call_past_the_handle_says_so():
     import __graft_entry__
