@@ -379,7 +379,10 @@ lmloss_status lmloss_embedding_forward(lmloss_vocab_handle handle, const lmloss_
 /*
  * table[v] (+)= scale * sum of rows[t] over the positions t with ids[t] = v.
  * The positions are sorted by token; each token's rows are added in fp32, in an
- * order that the ids alone fix, and the result is rounded once.  An id outside
+ * order that the ids alone fix, and the result is rounded once to a 16-bit table.
+ * Added to an fp32 table, the product with the scale is rounded and then its sum with
+ * the old value (most additions are the memory's own, which takes subnormals as 0:
+ * the old value, the product and the sum alike; the others are fused and keep them).  An id outside
  * [0, V) that is not LMLOSS_IGNORE_INDEX sets LMLOSS_ERR_BAD_TARGET and adds
  * nothing.
  */
