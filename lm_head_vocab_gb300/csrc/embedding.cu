@@ -838,7 +838,7 @@ struct SumParams {
     const uint32_t* pos;
     float* parts;           // [windows][2][ld_parts]
     int64_t ld_parts;
-    int window, windows;
+    int window;
     int tpr;
     int sum_blocks;
     int64_t blind;          // rows already zero
@@ -1493,7 +1493,6 @@ lmloss_status lmloss_embedding_backward(lmloss_vocab_handle h, const lmloss_embe
     q.parts = reinterpret_cast<float*>(h->ws + s.parts);
     q.ld_parts = s.ld_parts;
     q.window = s.window;
-    q.windows = s.windows;
     q.crossing = reinterpret_cast<uint32_t*>(h->ws + s.crossing);
     q.counters = h->counters;
     q.tpr = threads_of_row(vecs, kSumThreads);

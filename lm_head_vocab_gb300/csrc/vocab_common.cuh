@@ -18,7 +18,6 @@ constexpr int kVocabCounters = 1 << 16;
 struct lmloss_vocab_ctx {
     int device = 0;
     int num_sms = 0;
-    int smem_optin = 0;
     unsigned char* mem = nullptr;    // what was allocated: the error word, the counters, the workspace
     int* err = nullptr;
     unsigned* counters = nullptr;    // [kVocabCounters]

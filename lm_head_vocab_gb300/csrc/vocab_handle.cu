@@ -22,7 +22,6 @@ lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_
     constexpr size_t kHead = 256 + kVocabCounters * sizeof(unsigned);
     unsigned char* mem = nullptr;
     if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&h->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) != cudaSuccess ||
         cudaMalloc(&mem, kHead + h->ws_bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
