@@ -432,9 +432,9 @@ lmloss_status lmloss_beam_workspace(const lmloss_beam_args* args, size_t* bytes)
  * (divided by length^alpha for the ranking, or by the largest double where that
  * passes it), best first, equal ones by k, then by v.  The candidates of a row are in
  * the exact order of their logits.  Rows are ranked against one another by a score and a
- * division in fp64, from a sum of exponentials in fp32 (an lse_k within about 1e-6 where
- * it is near 1) and a power within 3e-9 (1 + alpha) of itself.  scores_out holds the
- * score before the division, rounded to fp32.
+ * division in fp64, from a sum of exponentials in fp32 (an lse_k about as close as
+ * lse_out's own rounding brings it) and a power within 3e-9 (1 + alpha) of itself.
+ * scores_out holds the score before the division, rounded to fp32.
  *   - A finished beam's row is not read: its one candidate is (k, eos_token) with
  *     its score as it is, and its length does not grow.
  *   - A token whose mask bit is 0 is no candidate; the row's logsumexp still

@@ -26,15 +26,24 @@ def ops():
     h.close()
 
 
-def check(ops, z, s, M, alpha, lengths, finished=None, eos=-1):
+def check(ops, z, s, M, alpha, lengths, finished=None, eos=-1, may=None):
     """Each candidate is one of the row's best, in an order that its exact ranks allow."""
     B, K = s.shape
     V = z.shape[1]
-    r = ops.beam_step(z, s, num_candidates=M, lengths=lengths, length_penalty=alpha, finished=finished, eos_token=eos)
+    mask = None
+    if may is not None:                                   # [B * K or 1, V] truth values
+        bits = torch.zeros(may.shape[0], (V + 31) // 32 * 32, dtype=torch.int64, device="cuda")
+        bits[:, :V] = may
+        word = (bits.view(may.shape[0], -1, 32) << torch.arange(32, device="cuda")).sum(2)
+        mask = torch.where(word >= 2 ** 31, word - 2 ** 32, word).int()
+    r = ops.beam_step(z, s, num_candidates=M, lengths=lengths, length_penalty=alpha, finished=finished, eos_token=eos,
+                      token_mask=mask)
     assert ops.device_error() == 0
     fin = torch.zeros(B, K, dtype=torch.bool) if finished is None else finished.bool().cpu()
     zd = z.double().cpu().view(B, K, V)
     score = s.double().cpu()[:, :, None] + zd - torch.logsumexp(zd, 2, keepdim=True)
+    if may is not None:
+        score = torch.where(may.cpu().expand(B * K, V).view(B, K, V), score, -INF)
     if finished is not None:
         stay = torch.full((B, K, V), -INF, dtype=torch.float64)
         stay[:, :, eos] = s.double().cpu()
@@ -91,6 +100,11 @@ def test_order_of_normalised_scores(ops, dtype, alpha):
     z, s, n, fin = inputs(3, 5, 2500, dtype, int(alpha * 10))
     check(ops, z, s, 10, alpha, n)
     check(ops, z, s, 10, alpha, n, fin, 17)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    may = torch.rand(15, 2500, device="cuda", generator=g) < 0.1
+    may[4] = False                                         # nothing may follow one beam
+    check(ops, z, s, 10, alpha, n, fin, 17, may)
+    check(ops, z, s, 10, alpha, n, None, -1, may[:1])
 
 
 @pytest.mark.parametrize("alpha", [85.0, 1e4])
