@@ -46,10 +46,11 @@ def _matrix(t: torch.Tensor, name: str, index: int):
         raise ValueError(f"{name}: on {t.device}, the handle on cuda:{index}")
     if t.dim() != 2:
         raise ValueError(f"{name}: must have two dimensions")
-    if t.is_neg():
-        raise ValueError(f"{name}: a lazily negated or conjugated view; resolve it first")
     rows, cols = t.size(0), t.size(1)
     ld, unit = t.stride()
+    # (a lazily negated view is every second number of a conjugated one: never of unit stride)
+    if unit != 1 and t.is_neg():
+        raise ValueError(f"{name}: a lazily conjugated or negated view; resolve it first")
     if rows <= 1:
         ld = cols
     if cols < 1 or (cols > 1 and unit != 1) or ld < cols:
@@ -348,9 +349,11 @@ class VocabOps:
             raise ValueError(f"states: on {t.device} and {o.device}, the handle on {self.device}")
         if t.dtype != o.dtype:
             raise TypeError(f"out: {o.dtype} for a state of {t.dtype}")
-        if t.is_conj() != o.is_conj() or t.is_neg() != o.is_neg():
-            raise ValueError("states: a lazily negated or conjugated view on one side; resolve it first")
         shape, oshape, ts, os_ = t.shape, o.shape, t.stride(), o.stride()
+        # (real views that are lazily negated are every second number of a conjugated one)
+        if (t.is_complex() or ts[-1] != 1 or os_[-1] != 1) and \
+                (t.is_conj() != o.is_conj() or t.is_neg() != o.is_neg()):
+            raise ValueError("states: a lazily conjugated or negated view on one side; resolve it first")
         d = dim if dim >= 0 else dim + len(shape)
         if shape[d] != rows:
             raise ValueError(f"states: {shape[d]} and {rows} rows along dim {dim}")
