@@ -50,7 +50,10 @@ struct DeviceGuard {
     explicit DeviceGuard(int dev)
     {
         if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) {
+            cudaGetLastError();   // not left for the next launch's check
+            ok = false;
+        }
     }
     ~DeviceGuard()
     {

@@ -37,8 +37,11 @@ struct VocabDeviceGuard {
     {
         if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
         if (prev == dev) return;
-        if (cudaSetDevice(dev) != cudaSuccess) ok = false;
-        else moved = true;
+        moved = cudaSetDevice(dev) == cudaSuccess;
+        if (!moved) {
+            cudaGetLastError();   // not left for the next launch's check
+            ok = false;
+        }
     }
     ~VocabDeviceGuard()
     {

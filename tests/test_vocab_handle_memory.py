@@ -20,7 +20,7 @@ def run(tmp_path, unit, body):
         pytest.skip("no C++ compiler")
     main, obj, lib, exe = (str(tmp_path / n) for n in ("main.cpp", "unit.o", "libunit.so", "main"))
     with open(main, "w") as f:
-        f.write('#include <cstdio>\n#include "lmloss.h"\nint unfinished_fills();\nint main()\n{\n' + body + "    return 0;\n}\n")
+        f.write('#include <cstdio>\n#include "lmloss.h"\n#include <cuda_runtime_api.h>\nint unfinished_fills();\nint main()\n{\n' + body + "    return 0;\n}\n")
     subprocess.run([L._nvcc(), "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-O1", "-Xcompiler", "-fPIC",
                     "-c", "-o", obj, os.path.join(CSRC, unit)], check=True)
     cxx = [cxx, "-std=c++17", "-fPIC", "-I", os.path.join(HERE, "..", "include"), "-I", os.path.join(CUDA, "include")]
@@ -61,11 +61,36 @@ def test_the_loss_handle_keeps_to_the_same(tmp_path):
 """)
 
 
+@pytest.mark.parametrize("unit,handle,create", [("vocab_handle.cu", "lmloss_vocab_handle", "lmloss_vocab_create(&h, 9, 0)"),
+                                                ("lmloss.cu", "lmloss_handle", "lmloss_create(&h, 9, 16, 1)")])
+def test_a_device_that_is_not_there_leaves_no_error_behind(tmp_path, unit, handle, create):
+    # the next call's check of its launch would find it
+    run(tmp_path, unit, f"""
+    {handle} h;
+    if ({create} != LMLOSS_ERR_CUDA) return 1;
+    if (cudaGetLastError() != cudaSuccess) return std::printf("an error is left for the next call\\n"), 2;
+""")
+
+
 def test_the_fixed_workspace_is_not_cleared_under_its_first_call():
     # it is zero when the module loads; its set-up runs inside the first call
     text = open(os.path.join(CSRC, "lmloss.cu")).read()
     setup = text[text.index("lmloss_status noalloc_setup"):text.index('extern "C" lmloss_status lmloss_forward_backward_noalloc')]
     assert "static __device__ __align__(256) unsigned char g_noalloc_scratch" in text and "Memset" not in setup
+
+
+@pytest.mark.gpu
+def test_calls_after_a_handle_on_a_device_that_is_not_there():
+    import torch
+    import __graft_entry__
+    __graft_entry__.build()
+    from lm_head_vocab_gb300 import VocabOps
+    ops = VocabOps(0, max_tokens=0, max_rows=0)
+    w, ids = torch.randn(9, 8, device="cuda"), torch.tensor([3, 1], device="cuda")
+    with pytest.raises(L.LMLossError):
+        L.lmloss_vocab_create(torch.cuda.device_count(), 0)
+    assert torch.equal(ops.embedding_forward(w, ids), w[ids])
+    ops.close()
 
 
 @pytest.mark.gpu

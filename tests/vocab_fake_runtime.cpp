@@ -1,5 +1,6 @@
-// A stand-in for the CUDA runtime under the library's host code: device memory is host memory,
-// and a cudaMemset is done when its stream is waited for, not when it returns.
+// A stand-in for the CUDA runtime under the library's host code: one device, whose memory is host
+// memory; a cudaMemset is done when its stream is waited for, not when it returns; an error stays
+// until it is asked for.
 #include <cstdlib>
 #include <cstring>
 #include <vector>
@@ -22,12 +23,18 @@ static cudaError_t finish()
     fills().clear();
     return cudaSuccess;
 }
+static cudaError_t last = cudaSuccess;
 int unfinished_fills() { return static_cast<int>(fills().size()); }
 
 extern "C" {
 cudaError_t cudaGetDevice(int* d) { return *d = 0, cudaSuccess; }
-cudaError_t cudaSetDevice(int) { return cudaSuccess; }
-cudaError_t cudaGetLastError() { return cudaSuccess; }
+cudaError_t cudaSetDevice(int d) { return d == 0 ? cudaSuccess : (last = cudaErrorInvalidDevice); }
+cudaError_t cudaGetLastError()
+{
+    const cudaError_t e = last;
+    last = cudaSuccess;
+    return e;
+}
 cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { return *v = 152, cudaSuccess; }
 cudaError_t cudaMalloc(void** p, size_t n)
 {
