@@ -7,6 +7,7 @@
 // positions x 128 bf16 into the other buffer, 5 of 8 beams surviving, 380 us = 6.9 TB/s
 // (a beam taken twice is read once from DRAM); 4 caches of 64 x 4 x 777 x 80 in place, 2 of 4
 // beams moving, 20 us = 6.3 TB/s; token histories, 2.7 us.
+#include <algorithm>
 #include <climits>
 #include <numeric>
 
@@ -204,6 +205,40 @@ bool empty(const lmloss_beam_state& s)
     return s.inner == 0 || s.outer[0] == 0 || s.outer[1] == 0 || s.outer[2] == 0;
 }
 
+// States move side by side, so none may write what another reads or writes.  Seen where the two begin
+// at the same byte, by a table of up to kTabled states' dst at a time (comparing all pairs took 40 us
+// for 160 states, a launch's time and more).
+bool apart_from_one_another(const lmloss_beam_state* states, int n)
+{
+    constexpr int kTabled = 512;
+    int32_t table[4 * kTabled];
+    for (int first = 0; first < n; first += kTabled) {
+        const int last = std::min(n, first + kTabled);
+        int bits = 3;
+        while ((1 << bits) < 4 * (last - first)) ++bits;
+        std::fill_n(table, 1 << bits, -1);
+        // the place of the state whose dst is p, or where it would be
+        auto find = [&](const void* p) {
+            uint64_t at = (reinterpret_cast<uintptr_t>(p) * 0x9e3779b97f4a7c15ull) >> (64 - bits);
+            while (table[at] >= 0 && states[table[at]].dst != p) at = (at + 1) & ((1u << bits) - 1);
+            return table + at;
+        };
+        for (int i = first; i < last; ++i) {
+            if (empty(states[i])) continue;
+            int32_t* held = find(states[i].dst);
+            if (*held < 0) *held = i;
+        }
+        for (int i = 0; i < n; ++i) {
+            if (empty(states[i])) continue;
+            const int writes = *find(states[i].dst), read = *find(states[i].src);
+            if (read >= 0 && read != i) return false;
+            // one state given twice, not in place, is written twice alike
+            if (writes >= 0 && states[writes].src != states[i].src) return false;
+        }
+    }
+    return true;
+}
+
 lmloss_status check_states(const lmloss_beam_state* states, int32_t n, int64_t B, int32_t K, int32_t K_out)
 {
     if (n < 0 || (n > 0 && !states) || B < 0 || K < 1 || K_out < 1) return LMLOSS_ERR_INVALID_ARG;
@@ -230,14 +265,9 @@ lmloss_status check_states(const lmloss_beam_state* states, int32_t n, int64_t B
         const int64_t rs = reach(s.src_row_stride, B * K, s.outer, s.src_outer_stride, s.inner);
         const int64_t rd = reach(s.dst_row_stride, B * K_out, s.outer, s.dst_outer_stride, s.inner);
         if (rs < 0 || rd < 0) return LMLOSS_ERR_INVALID_ARG;
-        // states move side by side: what one writes is not another's (the same start is seen here)
-        for (int j = 0; j < n; ++j)
-            if (j != i && !empty(states[j]) &&
-                (s.dst == states[j].src || (s.dst == states[j].dst && s.src != states[j].src)))
-                return LMLOSS_ERR_INVALID_ARG;
         if (s.src != s.dst && !apart(s, B * K, B * K_out, rs, rd)) return LMLOSS_ERR_INVALID_ARG;
     }
-    return LMLOSS_OK;
+    return B == 0 || apart_from_one_another(states, n) ? LMLOSS_OK : LMLOSS_ERR_INVALID_ARG;
 }
 
 // the widest unit that every run starts at and is a multiple of

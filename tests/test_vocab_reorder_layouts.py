@@ -100,6 +100,23 @@ def test_states_that_write_to_one_another_are_refused():
     assert check(st(a, b), st(b, a, inner=0)) == OK        # nothing moves
 
 
+@pytest.mark.parametrize("n", [2, 3, 100, 511, 512, 513, 1500])
+def test_states_that_write_to_one_another_among_many(n):
+    rng = random.Random(n)
+    place = [0x100000 + 256 * i for i in rng.sample(range(10 * n), 2 * n)]
+
+    def run(edit=lambda st: None):
+        st = [state(place[2 * i], place[2 * i + (i % 3 != 0)], 16, (16, 16), [1, 1, 1], [0, 0, 0], [0, 0, 0]) for i in range(n)]
+        edit(st)
+        return check(*st)
+    assert run() == OK
+    for a, b in ((0, n - 1), (n - 1, 0), (n // 2, (n // 2 + 1) % n), (rng.randrange(1, n), 0)):
+        assert run(lambda st: setattr(st[a], "src", st[b].dst)) == BAD
+        assert run(lambda st: setattr(st[a], "dst", st[b].dst)) == BAD
+        # every third is in place: what another reads there is written
+        assert run(lambda st: setattr(st[a], "src", st[b].src)) == (BAD if b % 3 == 0 else OK)
+
+
 @pytest.fixture(scope="module")
 def ops():
     import __graft_entry__
