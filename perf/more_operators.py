@@ -243,13 +243,14 @@ def _quantize(s, c):
     w = torch.nn.functional.pad(s["weight"].float(), (0, _groups(c) * g - D)).view(V, -1, g)
     if c["zeros"]:
         lo, hi = w.amin(2, keepdim=True).clamp(max=0), w.amax(2, keepdim=True).clamp(min=0)
-        scale = ((hi - lo) / 15).to(_TYPES[c["scales"]])
+        scale = ((hi - lo) / torch.full_like(hi, 15)).to(_TYPES[c["scales"]])    # (a quotient: by a number it would be a product)
         by = torch.where(scale > 0, scale, 1.0).double()     # next to a border 32 bits would round a quotient
         z = (-lo.double() / by).round().clamp(0, 15)
         q = ((w.double() / by).round_() + z).clamp_(0, 15)
         q -= z
     else:
-        scale = (w.abs().amax(2, keepdim=True) / 7).to(_TYPES[c["scales"]])
+        most = w.abs().amax(2, keepdim=True)
+        scale = (most / torch.full_like(most, 7)).to(_TYPES[c["scales"]])
         q = (w.double() / torch.where(scale > 0, scale, 1.0).double()).round_().clamp_(-8, 7)
     return (q.float() * scale.float()).view(V, -1)[:, :D].contiguous()
 
@@ -376,12 +377,12 @@ def exact(case, seed):
             if c["zeros"]:
                 hi = torch.maximum(w.float().max(1)[0], torch.zeros(1, device="cuda"))
                 lo = torch.minimum(w.float().min(1)[0], torch.zeros(1, device="cuda"))
-                scale = ((hi - lo) / 15).to(_TYPES[c["scales"]]).double()[:, None]
+                scale = ((hi - lo).double() / 15).float().to(_TYPES[c["scales"]]).double()[:, None]
                 by = scale.masked_fill(scale == 0, 1.0)
                 z = torch.round(-lo.double()[:, None] / by).clamp(0, 15)
                 q = torch.minimum(torch.maximum(torch.round(w.double() / by), -z), 15 - z)
             else:
-                scale = (w.float().abs().max(1)[0] / 7).to(_TYPES[c["scales"]]).double()[:, None]
+                scale = (w.double().abs().max(1)[0] / 7).float().to(_TYPES[c["scales"]]).double()[:, None]
                 q = torch.round(w.double() / scale.masked_fill(scale == 0, 1.0)).clamp(-8, 7)
             out[:, k * c["group"]:(k + 1) * c["group"]] = q * scale
         return out
