@@ -482,6 +482,188 @@ lmloss_status lmloss_beam_check_states(const lmloss_beam_state* states, int32_t 
 lmloss_status lmloss_beam_reorder(lmloss_vocab_handle handle, const lmloss_beam_state* states, int32_t num_states,
                                   const int32_t* parents, int64_t B, int32_t K, int32_t K_out, cudaStream_t stream);
 
+/* ---- Log-probabilities of given tokens
+ *
+ * Over rows of [T, V] logits, at a temperature tau and over the columns that a mask allows
+ * (y = logits / tau; columns that are not allowed count as -inf):
+ *   lse = ln sum_v e^y_v,   logp_j = y_{t_j} - lse,   H = -sum_v p_v ln p_v,  p = e^(y - lse)
+ * and the M largest log-probabilities with their tokens.  The handle, the conventions and the
+ * error word are those of the vocabulary operators.
+ */
+#define LMLOSS_MAX_ALTERNATIVES 64
+#define LMLOSS_MAX_GIVEN 1024    /* given tokens a row of a gradient                       */
+
+typedef struct {
+    const void* logits;          /* [T, ld] dtype, first V columns used                    */
+    int64_t T;                   /* rows, >= 0 and < 2^30                                  */
+    int64_t V;                   /* vocabulary columns, >= 1 and <= 2^31 - 2^16            */
+    int64_t ld;                  /* row stride in elements, >= V                           */
+    int32_t dtype;               /* lmloss_dtype, any of the three                         */
+    int32_t ids_dtype;           /* lmloss_id_dtype of tokens                              */
+    const void* tokens;          /* [T, n] given tokens, LMLOSS_IGNORE_INDEX = none;       */
+                                 /* NULL with n = 0                                        */
+    int64_t n;                   /* given tokens a row, 0 .. 2^20                          */
+    float temperature;           /* 2^-20 .. 2^20                                          */
+    int32_t M;                   /* alternatives, 0 .. LMLOSS_MAX_ALTERNATIVES             */
+    const int32_t* token_mask;   /* NULL, or rows of ceil(V / 32) words: bit v % 32 of     */
+                                 /* word v / 32 is set where token v is allowed            */
+    int64_t mask_stride;         /* words between rows of the mask; 0 = one row for all    */
+    float* logp_out;             /* [T, n]                                                 */
+    float* lse_out;              /* optional [T]                                           */
+    float* entropy_out;          /* optional [T]                                           */
+    float* top_logp_out;         /* [T, M]                                                 */
+    int64_t* top_tokens_out;     /* [T, M]                                                 */
+} lmloss_logprobs_args;
+
+/* Host-only validation of `args` (no CUDA call). */
+lmloss_status lmloss_logprobs_check_args(const lmloss_logprobs_args* args);
+
+/* The workspace that lmloss_logprobs_forward needs for `args` (pointers are not
+ * looked at); it grows with M and T and has a bound of about 2.2 MB. */
+lmloss_status lmloss_logprobs_workspace(const lmloss_logprobs_args* args, size_t* bytes);
+
+/*
+ * One read of the logits.  Sums of exponentials in fp32 (an lse and an entropy
+ * within a few fp32 steps of the exact ones), log-probabilities from their difference in fp64,
+ * rounded to fp32.
+ *   - LMLOSS_IGNORE_INDEX gives a log-probability of 0; another token outside [0, V)
+ *     NaN and LMLOSS_ERR_BAD_TARGET; one that is not allowed, or whose logit is -inf, -inf.
+ *   - Alternatives come in the exact order of their logits, equal ones by token.  Where
+ *     fewer than M have a finite logit and are allowed, the rest gets -inf and
+ *     LMLOSS_IGNORE_INDEX.
+ *   - A row in which nothing is allowed (or every allowed logit is -inf): lse -inf, entropy 0,
+ *     log-probabilities -inf.
+ *   - NaN or +inf in an allowed column: lse, entropy and log-probabilities are NaN, and the
+ *     row has no alternatives.  What stands in columns that are not allowed has no effect.
+ */
+lmloss_status lmloss_logprobs_forward(lmloss_vocab_handle handle, const lmloss_logprobs_args* args,
+                                      cudaStream_t stream);
+
+typedef struct {
+    const void* logits;          /* as for the forward call, up to the mask                */
+    int64_t T;
+    int64_t V;
+    int64_t ld;
+    int32_t dtype;
+    int32_t ids_dtype;
+    const void* tokens;          /* [T, n] or NULL with n = 0                              */
+    int64_t n;                   /* 0 .. LMLOSS_MAX_GIVEN                                  */
+    float temperature;
+    const int32_t* token_mask;
+    int64_t mask_stride;
+    const float* lse;            /* [T] of the forward call                                */
+    const float* grad_logp;      /* [T, n] or NULL with n = 0                              */
+    const float* entropy;        /* [T] of the forward call, with grad_entropy             */
+    const float* grad_entropy;   /* optional [T]                                           */
+    void* grad_out;              /* [T, ld_grad] dtype, written whole; == logits with the  */
+                                 /* same ld writes in place, otherwise no overlap          */
+    int64_t ld_grad;             /* row stride in elements, >= V                           */
+} lmloss_logprobs_grad_args;
+
+/* Host-only validation of `args` (no CUDA call). */
+lmloss_status lmloss_logprobs_check_grad_args(const lmloss_logprobs_grad_args* args);
+
+/*
+ * grad_out[r][v] = ( sum_{j: t_j = v} g_j - p_v (sum_j g_j + gH (ln p_v + H)) ) / tau
+ * in fp32, rounded once; 0 in columns that are not allowed, and in a whole row whose lse
+ * is -inf.  A token given twice counts twice; one that is not allowed still takes its
+ * -g p from the others, as its logp = -inf - lse does.  Tokens outside [0, V) that are not
+ * LMLOSS_IGNORE_INDEX set LMLOSS_ERR_BAD_TARGET and add nothing.  No workspace.
+ */
+lmloss_status lmloss_logprobs_backward(lmloss_vocab_handle handle, const lmloss_logprobs_grad_args* args,
+                                       cudaStream_t stream);
+
+/* ---- A vocabulary table in 4 bits
+ *
+ * A [V, D] table with one scale, and on request one zero point, for each row and group of
+ * `group` columns:  w[v][c] = scales[g][v] * (q[v][c] - zeros[g][v]),  g = c / group, q in 0 .. 15,
+ * and 8 in the zeros' place where there are none.  It is made from float weights, looked up
+ * (an embedding) and multiplied with hidden rows (an LM head); a tied model uses one for both.
+ */
+typedef struct {
+    uint8_t* values;             /* [V, ld_values]: column c in the low (c even) or high   */
+                                 /* half of byte c / 2; 16-byte aligned                    */
+    int64_t ld_values;           /* row stride in bytes, >= (D + 1) / 2, a multiple of 16  */
+    void* scales;                /* [ceil(D / group), ld_scales] scale_dtype, 16-byte      */
+                                 /* aligned                                                */
+    int64_t ld_scales;           /* elements, >= V; as bytes a multiple of 16              */
+    uint8_t* zeros;              /* [ceil(D / group), ld_zeros] or NULL; 16-byte aligned   */
+    int64_t ld_zeros;            /* >= V, a multiple of 16 (not looked at without zeros)   */
+    int64_t V;                   /* rows, 1 .. 2^31 - 2^16                                 */
+    int64_t D;                   /* columns, 1 .. 2^20                                     */
+    int32_t group;               /* 32, 64 or 128                                          */
+    int32_t scale_dtype;         /* lmloss_dtype                                           */
+} lmloss_table4;
+
+/* Host-only validation of a table (no CUDA call). */
+lmloss_status lmloss_table4_check(const lmloss_table4* table);
+
+typedef struct {
+    lmloss_table4 table;         /* written                                                */
+    const void* weight;          /* [V, ld_weight] weight_dtype                            */
+    int64_t ld_weight;           /* row stride in elements, >= D                           */
+    int32_t weight_dtype;        /* lmloss_dtype                                           */
+} lmloss_table4_quantize_args;
+
+/*
+ * The table nearest to float weights, group by group (R rounds to the scales' type, quotients
+ * w / s are rounded to the nearest whole number, halves to the even one):
+ *   without zeros  s = R(max |w| / 7),          q = clamp(w / s, -8, 7) + 8
+ *   with zeros     s = R((hi - lo) / 15),       z = clamp(-lo / s, 0, 15),  q = clamp(w / s + z, 0, 15)
+ *                  lo = min(0, w), hi = max(0, w)
+ * the quotient before R in fp32.  A group of s = 0 holds zeros.  A group with a weight that is
+ * not finite, or whose scale leaves its type's range, gets a scale of NaN, and
+ * LMLOSS_ERR_RANGE is set.  In the last byte of a row of odd D the high half is 0; bytes past it
+ * are left alone.
+ */
+lmloss_status lmloss_table4_quantize(lmloss_vocab_handle handle, const lmloss_table4_quantize_args* args,
+                                     cudaStream_t stream);
+
+typedef struct {
+    lmloss_table4 table;         /* read                                                   */
+    const void* ids;             /* [T]                                                    */
+    int64_t T;                   /* >= 0 and < 2^30                                        */
+    void* rows;                  /* [T, ld_rows] rows_dtype, written                       */
+    int64_t ld_rows;             /* >= D                                                   */
+    int32_t ids_dtype;           /* lmloss_id_dtype                                        */
+    int32_t rows_dtype;          /* lmloss_dtype                                           */
+    float scale;                 /* finite                                                 */
+} lmloss_table4_lookup_args;
+
+/* rows[t] = scale * w[ids[t]], computed in fp32 and rounded once more; ids as for
+ * lmloss_embedding_forward. */
+lmloss_status lmloss_table4_lookup(lmloss_vocab_handle handle, const lmloss_table4_lookup_args* args,
+                                   cudaStream_t stream);
+
+typedef struct {
+    lmloss_table4 table;         /* read                                                   */
+    const void* hidden;          /* [T, ld_hidden] hidden_dtype, first D columns used      */
+    int64_t T;                   /* rows, >= 0 and < 2^24                                  */
+    int64_t ld_hidden;           /* >= D                                                   */
+    void* logits;                /* [T, ld_logits] logits_dtype, written                   */
+    int64_t ld_logits;           /* >= V                                                   */
+    int32_t hidden_dtype;        /* lmloss_dtype                                           */
+    int32_t logits_dtype;        /* lmloss_dtype                                           */
+    float scale;                 /* finite                                                 */
+} lmloss_table4_logits_args;
+
+/* Host-only validation (no CUDA call). */
+lmloss_status lmloss_table4_check_quantize_args(const lmloss_table4_quantize_args* args);
+lmloss_status lmloss_table4_check_lookup_args(const lmloss_table4_lookup_args* args);
+lmloss_status lmloss_table4_check_logits_args(const lmloss_table4_logits_args* args);
+
+/* The workspace that lmloss_table4_logits needs for `args` (pointers are not looked at)
+ * and for any call of no more rows and columns, whatever its types. */
+lmloss_status lmloss_table4_logits_workspace(const lmloss_table4_logits_args* args, size_t* bytes);
+
+/*
+ * logits[t][v] = scale * sum_c hidden[t][c] * w[v][c]: from one row (a decoding step) to a
+ * prompt's.  Within a group the products with the whole numbers q - z are summed, and the sum
+ * is scaled by the group's scale: no weight is rounded.  Sums in fp32, one rounding at the end.
+ */
+lmloss_status lmloss_table4_logits(lmloss_vocab_handle handle, const lmloss_table4_logits_args* args,
+                                   cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,9 +21,11 @@ HEADER = os.path.join(_ROOT, "include", "lmloss.h")
 UNITS = [("lmloss.cu", [], "lmloss.o")] + [
     ("fused_inst.cu", [f"-DLMLOSS_FUSED_VARIANT={k}"], f"fused_{k}.o") for k in range(8)] + [
     # the vocabulary operators
-    (f"{name}.cu", [], f"{name}.o") for name in ("vocab_handle", "embedding", "beam_step", "beam_reorder")]
+    (f"{name}.cu", [], f"{name}.o") for name in ("vocab_handle", "embedding", "beam_step", "beam_reorder", "logprobs", "table4",
+                                               "table4_logits")]
 DEPENDS = ["lmloss.cu", "fused_inst.cu", "fused_entry.cuh", "kernels.cuh", "aux_kernels.cuh", "ptx.cuh",
-           "vocab_common.cuh", "vocab_handle.cu", "embedding.cu", "beam_math.cuh", "beam_plan.cuh", "beam_step.cu", "beam_reorder.cu"]
+           "vocab_common.cuh", "vocab_handle.cu", "embedding.cu", "beam_math.cuh", "beam_plan.cuh", "row_stream.cuh", "beam_step.cu", "beam_reorder.cu",
+           "logprobs.cu", "table4.cuh", "table4.cu", "table4_logits.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC"]
@@ -43,6 +45,8 @@ LMLOSS_FP16 = 2
 LMLOSS_INT64 = 0
 LMLOSS_INT32 = 1
 LMLOSS_MAX_BEAMS = 64
+LMLOSS_MAX_ALTERNATIVES = 64
+LMLOSS_MAX_GIVEN = 1024
 LMLOSS_REDUCE_SUM = 0
 LMLOSS_REDUCE_TOKEN_MEAN = 1
 LMLOSS_IGNORE_INDEX = -100
@@ -186,6 +190,101 @@ class lmloss_beam_state(ctypes.Structure):
     ]
 
 
+class lmloss_logprobs_args(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("T", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("ids_dtype", ctypes.c_int32),
+        ("tokens", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("temperature", ctypes.c_float),
+        ("M", ctypes.c_int32),
+        ("token_mask", ctypes.c_void_p),
+        ("mask_stride", ctypes.c_int64),
+        ("logp_out", ctypes.c_void_p),
+        ("lse_out", ctypes.c_void_p),
+        ("entropy_out", ctypes.c_void_p),
+        ("top_logp_out", ctypes.c_void_p),
+        ("top_tokens_out", ctypes.c_void_p),
+    ]
+
+
+class lmloss_logprobs_grad_args(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("T", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("ids_dtype", ctypes.c_int32),
+        ("tokens", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("temperature", ctypes.c_float),
+        ("token_mask", ctypes.c_void_p),
+        ("mask_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+        ("grad_logp", ctypes.c_void_p),
+        ("entropy", ctypes.c_void_p),
+        ("grad_entropy", ctypes.c_void_p),
+        ("grad_out", ctypes.c_void_p),
+        ("ld_grad", ctypes.c_int64),
+    ]
+
+
+class lmloss_table4(ctypes.Structure):
+    _fields_ = [
+        ("values", ctypes.c_void_p),
+        ("ld_values", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+        ("ld_scales", ctypes.c_int64),
+        ("zeros", ctypes.c_void_p),
+        ("ld_zeros", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("group", ctypes.c_int32),
+        ("scale_dtype", ctypes.c_int32),
+    ]
+
+
+class lmloss_table4_quantize_args(ctypes.Structure):
+    _fields_ = [
+        ("table", lmloss_table4),
+        ("weight", ctypes.c_void_p),
+        ("ld_weight", ctypes.c_int64),
+        ("weight_dtype", ctypes.c_int32),
+    ]
+
+
+class lmloss_table4_lookup_args(ctypes.Structure):
+    _fields_ = [
+        ("table", lmloss_table4),
+        ("ids", ctypes.c_void_p),
+        ("T", ctypes.c_int64),
+        ("rows", ctypes.c_void_p),
+        ("ld_rows", ctypes.c_int64),
+        ("ids_dtype", ctypes.c_int32),
+        ("rows_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class lmloss_table4_logits_args(ctypes.Structure):
+    _fields_ = [
+        ("table", lmloss_table4),
+        ("hidden", ctypes.c_void_p),
+        ("T", ctypes.c_int64),
+        ("ld_hidden", ctypes.c_int64),
+        ("logits", ctypes.c_void_p),
+        ("ld_logits", ctypes.c_int64),
+        ("hidden_dtype", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -232,6 +331,20 @@ def load() -> ctypes.CDLL:
                                       ctypes.c_int32, ctypes.c_int32], st),
         "lmloss_beam_reorder": ([h, ctypes.POINTER(lmloss_beam_state), ctypes.c_int32, ctypes.c_void_p,
                                  ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p], st),
+        "lmloss_logprobs_check_args": ([ctypes.POINTER(lmloss_logprobs_args)], st),
+        "lmloss_logprobs_workspace": ([ctypes.POINTER(lmloss_logprobs_args), ctypes.POINTER(ctypes.c_size_t)], st),
+        "lmloss_logprobs_forward": ([h, ctypes.POINTER(lmloss_logprobs_args), ctypes.c_void_p], st),
+        "lmloss_logprobs_check_grad_args": ([ctypes.POINTER(lmloss_logprobs_grad_args)], st),
+        "lmloss_logprobs_backward": ([h, ctypes.POINTER(lmloss_logprobs_grad_args), ctypes.c_void_p], st),
+        "lmloss_table4_check": ([ctypes.POINTER(lmloss_table4)], st),
+        "lmloss_table4_check_quantize_args": ([ctypes.POINTER(lmloss_table4_quantize_args)], st),
+        "lmloss_table4_check_lookup_args": ([ctypes.POINTER(lmloss_table4_lookup_args)], st),
+        "lmloss_table4_check_logits_args": ([ctypes.POINTER(lmloss_table4_logits_args)], st),
+        "lmloss_table4_quantize": ([h, ctypes.POINTER(lmloss_table4_quantize_args), ctypes.c_void_p], st),
+        "lmloss_table4_lookup": ([h, ctypes.POINTER(lmloss_table4_lookup_args), ctypes.c_void_p], st),
+        "lmloss_table4_logits_workspace": ([ctypes.POINTER(lmloss_table4_logits_args),
+                                            ctypes.POINTER(ctypes.c_size_t)], st),
+        "lmloss_table4_logits": ([h, ctypes.POINTER(lmloss_table4_logits_args), ctypes.c_void_p], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -396,3 +509,62 @@ def lmloss_beam_check_states(states, B: int, K: int, K_out: int) -> int:
 
 def lmloss_beam_reorder(handle, states, parents: int, B: int, K: int, K_out: int, stream: int) -> int:
     return load().lmloss_beam_reorder(handle, states, len(states), parents, B, K, K_out, stream)
+
+def lmloss_logprobs_check_args(args: lmloss_logprobs_args) -> int:
+    return load().lmloss_logprobs_check_args(ctypes.byref(args))
+
+
+def lmloss_logprobs_workspace(args: lmloss_logprobs_args) -> int:
+    n = ctypes.c_size_t()
+    st = load().lmloss_logprobs_workspace(ctypes.byref(args), ctypes.byref(n))
+    if st != LMLOSS_OK:
+        raise LMLossError(st, "lmloss_logprobs_workspace")
+    return n.value
+
+
+def lmloss_logprobs_forward(handle, args: lmloss_logprobs_args, stream: int) -> int:
+    return load().lmloss_logprobs_forward(handle, ctypes.byref(args), stream)
+
+
+def lmloss_logprobs_check_grad_args(args: lmloss_logprobs_grad_args) -> int:
+    return load().lmloss_logprobs_check_grad_args(ctypes.byref(args))
+
+
+def lmloss_logprobs_backward(handle, args: lmloss_logprobs_grad_args, stream: int) -> int:
+    return load().lmloss_logprobs_backward(handle, ctypes.byref(args), stream)
+
+
+def lmloss_table4_check(args: lmloss_table4) -> int:
+    return load().lmloss_table4_check(ctypes.byref(args))
+
+
+def lmloss_table4_check_quantize_args(args: lmloss_table4_quantize_args) -> int:
+    return load().lmloss_table4_check_quantize_args(ctypes.byref(args))
+
+
+def lmloss_table4_check_lookup_args(args: lmloss_table4_lookup_args) -> int:
+    return load().lmloss_table4_check_lookup_args(ctypes.byref(args))
+
+
+def lmloss_table4_check_logits_args(args: lmloss_table4_logits_args) -> int:
+    return load().lmloss_table4_check_logits_args(ctypes.byref(args))
+
+
+def lmloss_table4_logits_workspace(args: lmloss_table4_logits_args) -> int:
+    n = ctypes.c_size_t()
+    st = load().lmloss_table4_logits_workspace(ctypes.byref(args), ctypes.byref(n))
+    if st != LMLOSS_OK:
+        raise LMLossError(st, "lmloss_table4_logits_workspace")
+    return n.value
+
+
+def lmloss_table4_quantize(handle, args: lmloss_table4_quantize_args, stream: int) -> int:
+    return load().lmloss_table4_quantize(handle, ctypes.byref(args), stream)
+
+
+def lmloss_table4_lookup(handle, args: lmloss_table4_lookup_args, stream: int) -> int:
+    return load().lmloss_table4_lookup(handle, ctypes.byref(args), stream)
+
+
+def lmloss_table4_logits(handle, args: lmloss_table4_logits_args, stream: int) -> int:
+    return load().lmloss_table4_logits(handle, ctypes.byref(args), stream)

@@ -3,12 +3,11 @@
 
 #include <algorithm>
 
-#include "vocab_common.cuh"
+#include "row_stream.cuh"
 
 namespace lmloss {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kDepths = 8;                   // lists (parts of a sequence's rows) a thread
 constexpr int kMaxLists = kDepths * kThreads;
 

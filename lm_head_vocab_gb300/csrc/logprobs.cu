@@ -1,0 +1,799 @@
+// Log-probabilities of given tokens over rows of logits, with the rows' entropies and
+// their largest alternatives, and the gradient of the logits.
+//
+// With y = z / tau over the allowed columns, u = (z - m) log2(e) / tau and m the row's maximum:
+//
+//   s = sum 2^u,   e = sum u 2^u
+//   lse = m / tau + ln s,   H = ln s - ln2 e / s,   logp_j = z[t_j] / tau - lse
+//
+// so one pass with a running maximum gives all of it: a part of a row keeps (m, s, e), and
+// when m rises by d (in u's units) s becomes s 2^-d and e becomes (e - d s) 2^-d.  Alternatives
+// are kept as in a beam step: a threshold from group maxima, vectors noted against it.
+//
+// The gradient is one more pass, from lse and H alone: p = e^(y - lse).
+#include <algorithm>
+#include <cmath>
+
+#include "beam_math.cuh"
+#include "beam_plan.cuh"
+#include "row_stream.cuh"
+
+namespace lmloss {
+namespace {
+
+constexpr int kMaxTop = LMLOSS_MAX_ALTERNATIVES;
+constexpr int kCap = 1024;                   // candidate keys held at once
+constexpr int kHits = 512;                   // vectors of a part that reach its first threshold
+constexpr int kSmall = 256;                  // few enough to be ranked by counting
+constexpr int kMaxParts = 4096;              // parts of all rows, where rows are cut
+constexpr float kLeast = -1000.f;            // an exponent whose power is 0: 0 * -inf would be NaN
+constexpr double kLn2 = 0.693147180559945309417;
+
+struct LogprobsParams {
+    const void* logits;
+    int64_t ld;
+    int T, V;
+    int64_t n;
+    int M;
+    int slices, tiles;           // parts of a row, tiles of a part
+    float mul;                   // log2(e) / tau
+    double inv_tau;
+    const void* tokens;
+    int ids32;
+    const int32_t* mask;
+    int64_t mask_stride;
+    float* logp_out;
+    float* lse_out;
+    float* entropy_out;
+    float* top_logp_out;
+    int64_t* top_tokens_out;
+    uint64_t* keys;              // [T][slices][M] where rows are cut: each part's best, 0 = none
+    float4* stats;               // [T][slices] (m, s, e, -)
+    unsigned* done;              // [T] parts finished; 0 between calls
+    int* err;
+};
+
+__device__ __forceinline__ int64_t load_token(const void* tokens, int ids32, int64_t i)
+{
+    return ids32 ? static_cast<int64_t>(static_cast<const int32_t*>(tokens)[i]) : static_cast<const int64_t*>(tokens)[i];
+}
+
+__device__ __forceinline__ bool allowed(const int32_t* mask, int c)
+{
+    return !mask || (static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) & 1u);
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A running sum of 2^u and u 2^u about a maximum.
+struct Sums {
+    float m = -INFINITY, s = 0.f, e = 0.f;
+    __device__ __forceinline__ void raise(float top, float mul)
+    {
+        if (top > m) {
+            // (from -inf: s and e are 0)
+            const float d = fmaxf((m - top) * mul, kLeast), f = ex2(d);
+            e = fmaf(s, d, e) * f;
+            s *= f;
+            m = top;
+        }
+    }
+};
+
+struct __align__(16) LogprobsShared {
+    uint64_t buf[kCap];                      // candidates
+    uint4 data[kHits];                       // noted vectors
+    int32_t col[kHits];
+    uint64_t best[kMaxTop];                  // the part's or row's best, in order
+    uint32_t group[kThreads / 2], counts[kThreads];
+    uint32_t thr, thr_end;
+    float red_m[kWarps], red_s[kWarps], red_e[kWarps];
+    int count, hit_count, few, last;
+    double lse;
+};
+
+// The M best of the candidates in sm.buf (n of them, all different) into sm.best, best
+// first, 0 where there are none.
+__device__ __noinline__ void rank_best(LogprobsShared& sm, int n, int M)
+{
+    const int tid = threadIdx.x;
+    const uint64_t cut = n > kSmall ? mth_largest(sm.buf, n, M, sm.counts) : 0;
+    const uint64_t* set = sm.buf;
+    if (cut) {
+        uint64_t* few = reinterpret_cast<uint64_t*>(sm.data);
+        for (int i = tid; i < n; i += kThreads)
+            if (sm.buf[i] >= cut) few[atomicAdd(&sm.few, 1)] = sm.buf[i];
+        __syncthreads();
+        n = M;
+        set = few;
+    }
+    for (int i = tid; i < n; i += kThreads) {
+        const uint64_t k = set[i];
+        int above = 0;
+#pragma unroll 8
+        for (int o = 0; o < n; ++o) above += set[o] > k ? 1 : 0;
+        if (above < M) sm.best[above] = k;
+    }
+    for (int i = n + tid; i < M; i += kThreads) sm.best[i] = 0;
+    __syncthreads();
+}
+
+// What follows a row's sums: its statistics (thread 0 holds them), given tokens and, from
+// sm.best, alternatives.
+template <class T>
+__device__ void write_row(const LogprobsParams& p, LogprobsShared& sm, int row, float m, float hi, float lo, float e)
+{
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        const bool none = m == -INFINITY && hi == 0.f;
+        const double log_s = none ? 0.0 : log_of_sum(hi, lo);
+        const double lse = none ? -INFINITY : static_cast<double>(m) * p.inv_tau + log_s;
+        sm.lse = lse;
+        if (p.lse_out) p.lse_out[row] = static_cast<float>(lse);
+        if (p.entropy_out) p.entropy_out[row] = none ? 0.f : static_cast<float>(log_s - kLn2 * static_cast<double>(e / hi));
+    }
+    __syncthreads();
+    const double lse = sm.lse;
+    const typename T::raw* z = static_cast<const typename T::raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
+    const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
+    for (int64_t j = tid; j < p.n; j += kThreads) {
+        const int64_t o = static_cast<int64_t>(row) * p.n + j, t = load_token(p.tokens, p.ids32, o);
+        float out;
+        if (t == LMLOSS_IGNORE_INDEX) {
+            out = 0.f;
+        } else if (t < 0 || t >= p.V) {
+            set_error(p.err, kErrBadTarget);
+            out = NAN;
+        } else {
+            const float x = allowed(mask, static_cast<int>(t)) ? T::widen(z[t]) : -INFINITY;
+            const double y = static_cast<double>(x) * p.inv_tau - lse;
+            out = lse == -INFINITY ? -INFINITY : static_cast<float>(y);
+        }
+        p.logp_out[o] = out;
+    }
+    for (int i = tid; i < p.M; i += kThreads) {
+        const uint64_t k = sm.best[i];
+        const int64_t o = static_cast<int64_t>(row) * p.M + i;
+        // a row with NaN or +inf has an lse of NaN
+        const bool some = k != 0 && lse == lse && key_logit(k) < INFINITY;
+        p.top_logp_out[o] = some ? static_cast<float>(static_cast<double>(key_logit(k)) * p.inv_tau - lse) : -INFINITY;
+        p.top_tokens_out[o] = some ? key_col(k) : LMLOSS_IGNORE_INDEX;
+    }
+}
+
+// The block that finishes a row's last part joins the parts.
+template <class T>
+__device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& sm, int row)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = p.slices, M = p.M;
+    // sums: error-free pairs of fp32
+    float m = -INFINITY, hi = 0.f, lo = 0.f, e = 0.f;
+    if (warp == 0) {
+        const float4* st = p.stats + static_cast<int64_t>(row) * S;
+        for (int s = lane; s < S; s += 32) m = fmaxf(m, __ldcg(&st[s]).x);
+        m = warp_max(m);
+        auto add = [&](float x, float err) {
+            const float t = hi + x, v = t - hi;
+            lo += ((hi - (t - v)) + (x - v)) + err;
+            hi = t;
+        };
+        for (int s = lane; s < S; s += 32) {
+            const float4 q = __ldcg(&st[s]);
+            const float d = q.x == m ? 0.f : fmaxf((q.x - m) * p.mul, kLeast), f = exp2f(d);
+            add(q.y * f, 0.f);
+            e += fmaf(q.y, d, q.z) * f;
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, hi, o), y = __shfl_xor_sync(0xffffffffu, lo, o);
+            add(x, y);
+            e += __shfl_xor_sync(0xffffffffu, e, o);
+        }
+    }
+    if (M > 0) {
+        // candidates: below the M-th largest of the parts' best there are none
+        const uint64_t* keys = p.keys + static_cast<int64_t>(row) * S * M;
+        uint64_t thr = 1;
+        const int all = S * M;
+        if (all > kCap && S > M && S <= kCap) {
+            for (int s = tid; s < S; s += kThreads) sm.buf[s] = __ldcg(keys + static_cast<int64_t>(s) * M);
+            __syncthreads();
+            // (equal zeros, of parts without a candidate, count as the smallest)
+            thr = max(mth_largest(sm.buf, S, M, sm.counts), uint64_t(1));
+            __syncthreads();
+        }
+        int n;
+        while (true) {
+            if (tid == 0) sm.count = 0;
+            __syncthreads();
+            for (int i = tid; i < all; i += kThreads) {
+                const uint64_t k = __ldcg(keys + i);
+                if (k >= thr) {
+                    const int to = atomicAdd(&sm.count, 1);
+                    if (to < kCap) sm.buf[to] = k;
+                }
+            }
+            __syncthreads();
+            n = sm.count;
+            if (n <= kCap) break;
+            thr = mth_largest(sm.buf, kCap, M, sm.counts);
+            __syncthreads();
+        }
+        if (tid == 0) sm.few = 0;
+        __syncthreads();
+        rank_best(sm, n, M);
+    }
+    write_row<T>(p, sm, row, m, hi, lo, e);
+}
+
+// A block takes `tiles` tiles of one row, one after the other, with the next tile's loads in
+// flight; columns, not addresses, fix which thread adds what.
+template <class T, int VPT, bool ALIGNED, bool ENT>
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ LogprobsParams p)
+{
+    constexpr int E = Logits<T>::E;
+    constexpr int kTileCols = VPT * kThreads * E;
+    constexpr uint32_t kNone = T::kBytes == 4 ? 0xff800000u : (std::is_same<T, Bf16>::value ? 0xff80ff80u : 0xfc00fc00u);
+    __shared__ LogprobsShared sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / p.slices, part = blockIdx.x - row * p.slices;
+    RowLogits<T> r;
+    r.z = static_cast<const typename T::raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
+    r.V = p.V;
+    r.lo = 0;
+    r.hi = p.V - E;
+    if (!ALIGNED) {
+        // at the first and last row: nothing before or after the logits is read
+        const int64_t after = (static_cast<int64_t>(p.T) - 1 - row) * p.ld;
+        if (row == 0) r.lo = E;
+        if (after < E) r.hi = p.V - 2 * E;
+    }
+    const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
+    const int begin = part * p.tiles * kTileCols, end = part_end(begin, p.tiles, kTileCols, p.V);
+    if (tid == 0) {
+        sm.count = 0;
+        sm.hit_count = 0;
+        sm.few = 0;
+        sm.thr = 0;
+        sm.thr_end = 0;
+    }
+    Sums sum;
+    float best = -INFINITY, least = 0.f;
+    int tile = 0;
+    auto use_tile = [&](Pack<T, E> (&q)[VPT], int c0) {
+        if (mask) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int c = c0 + j * (kThreads * E);
+                const uint32_t allow = c < p.V ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t keep;
+                    if constexpr (T::kBytes == 4) keep = 0u - (allow >> i & 1u);
+                    else keep = ((0u - (allow >> (2 * i) & 1u)) & 0xffffu) | ((0u - (allow >> (2 * i + 1) & 1u)) << 16);
+                    q[j].w[i] = (q[j].w[i] & keep) | (kNone & ~keep);
+                }
+            }
+        }
+        float vmax[VPT], tmax;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) vmax[j] = Logits<T>::largest(q[j]);
+        tmax = vmax[0];
+#pragma unroll
+        for (int j = 1; j < VPT; ++j) tmax = fmaxf(tmax, vmax[j]);
+        bool raise = false;
+        if (p.M > 0) {
+            best = fmaxf(best, tmax);
+            raise = (tile & (tile + 1)) == 0;   // tiles 0, 1, 3, 7, ... raise the threshold
+            ++tile;
+            if (raise) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr);
+        }
+        sum.raise(tmax, p.mul);
+        // (the maximum is taken off before the product: z log2 e alone would overflow at the
+        // type's lowest values)
+        const float shift = sum.m == -INFINITY ? 0.f : sum.m;
+        const uint64_t off2 = f2_pack(-shift, -shift), mul2 = f2_pack(p.mul, p.mul);
+        uint64_t s2 = f2_pack(0.f, 0.f), e2 = f2_pack(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                float a, c;
+                f2_unpack(f2_mul(f2_add(f2_pack(q[j].get(i), q[j].get(i + 1)), off2), mul2), a, c);
+                const uint64_t w2 = f2_pack(ex2(a), ex2(c));
+                s2 = f2_add(s2, w2);
+                if (ENT) e2 = f2_fma(w2, f2_pack(max_nan(a, kLeast), max_nan(c, kLeast)), e2);
+            }
+        }
+        float a, c;
+        f2_unpack(s2, a, c);
+        sum.s += a + c;
+        if (ENT) {
+            f2_unpack(e2, a, c);
+            sum.e += a + c;
+        }
+        if (p.M > 0) {
+            if (raise) {
+                __syncthreads();   // the threshold; without one every logit but -inf
+                least = sm.thr ? unordered(sm.thr) : __uint_as_float(0xff7fffffu);
+            }
+            if (tmax >= least) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+                    if (vmax[j] >= least) {
+                        const int to = atomicAdd(&sm.hit_count, 1);
+                        if (to < kHits) {
+                            sm.data[to] = make_uint4(q[j].w[0], q[j].w[1], q[j].w[2], q[j].w[3]);
+                            sm.col[to] = c0 + j * (kThreads * E);
+                        }
+                    }
+            }
+        }
+    };
+    int t0 = begin;
+    auto whole_tiles = [&] {
+        InFlight<T, ALIGNED> next[VPT];
+        auto issue = [&](int c) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) next[j].load(r, c + (j * kThreads + tid) * E);
+        };
+        const int last = min(end, r.hi + E) - kTileCols;   // the last whole tile begins here or before
+        if (t0 <= last) issue(t0);
+        for (; t0 <= last; t0 += kTileCols) {
+            Pack<T, E> q[VPT];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) next[j].unpack(q[j], r, t0 + (j * kThreads + tid) * E);
+            if (t0 + kTileCols <= last) issue(t0 + kTileCols);
+            use_tile(q, t0 + tid * E);
+        }
+    };
+    __syncthreads();
+    for (bool before = true;; before = false) {
+        const int to = before ? min(r.lo, end) : end;
+        for (; t0 < to; t0 += kTileCols) {
+            Pack<T, E> q[VPT];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) load_logits<T, ALIGNED>(q[j], r, t0 + (j * kThreads + tid) * E);
+            use_tile(q, t0 + tid * E);
+        }
+        if (!before) break;
+        whole_tiles();
+    }
+
+    // ---- the part's sums
+    {
+        const float top = warp_max(sum.m);
+        sum.raise(top, p.mul);
+        for (int o = 16; o > 0; o >>= 1) {
+            sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
+            if (ENT) sum.e += __shfl_xor_sync(0xffffffffu, sum.e, o);
+        }
+        if (lane == 0) {
+            sm.red_m[warp] = top;
+            sm.red_s[warp] = sum.s;
+            sm.red_e[warp] = sum.e;
+        }
+    }
+    if (p.M > 0) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr_end);
+    __syncthreads();
+    float m = -INFINITY, s = 0.f, e = 0.f;
+    if (warp == 0) {
+        Sums w;
+        w.m = lane < kWarps ? sm.red_m[lane] : -INFINITY;
+        w.s = lane < kWarps ? sm.red_s[lane] : 0.f;
+        w.e = lane < kWarps ? sm.red_e[lane] : 0.f;
+        m = w.m;
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        w.raise(m, p.mul);
+        s = w.s;
+        e = w.e;
+        for (int o = 4; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            e += __shfl_xor_sync(0xffffffffu, e, o);
+        }
+        if (p.slices > 1 && lane == 0) p.stats[blockIdx.x] = make_float4(m, s, e, 0.f);
+    }
+
+    if (p.M > 0) {
+        // ---- candidates: the logits of the noted vectors that reach the threshold.  With more
+        // vectors noted than are kept all are looked at; with more candidates than are kept the
+        // threshold rises to the M-th largest of those held.
+        uint64_t thr = sm.thr_end ? static_cast<uint64_t>(sm.thr_end) << 32 : 1;
+        int n;
+        while (true) {
+            const int noted = sm.hit_count;
+            const bool all = noted > kHits;
+            const int elements = all ? end - begin : noted * E;
+#pragma unroll 1
+            for (int i = tid; i < elements; i += kThreads) {
+                const int c = all ? begin + i : sm.col[i / E] + i % E;
+                const float z = T::widen(all ? r.z[c] : reinterpret_cast<const typename T::raw*>(&sm.data[i / E])[i % E]);
+                // past V: -inf
+                if (z > -INFINITY && allowed(mask, c)) {
+                    const uint64_t k = key_of(z, c);
+                    if (k >= thr) {
+                        const int to = atomicAdd(&sm.count, 1);
+                        if (to < kCap) sm.buf[to] = k;
+                    }
+                }
+            }
+            __syncthreads();
+            n = sm.count;
+            if (n <= kCap) break;
+            thr = mth_largest(sm.buf, kCap, p.M, sm.counts);
+            __syncthreads();
+            if (tid == 0) sm.count = 0;
+            __syncthreads();
+        }
+        rank_best(sm, n, p.M);
+        if (p.slices > 1) {
+            uint64_t* out = p.keys + static_cast<int64_t>(blockIdx.x) * p.M;
+            for (int i = tid; i < p.M; i += kThreads) out[i] = sm.best[i];
+        }
+    }
+    if (p.slices == 1) {
+        write_row<T>(p, sm, row, m, s, 0.f, e);
+        return;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        sm.last = count_done(&p.done[row]) == static_cast<unsigned>(p.slices) - 1;
+        if (sm.last) p.done[row] = 0;
+    }
+    __syncthreads();
+    if (sm.last) join_row<T>(p, sm, row);
+}
+
+// ---------------------------------------------------------------- gradient
+struct GradParams {
+    const void* logits;
+    int64_t ld;
+    int T, V;
+    int n;
+    int parts;                   // of a row, kGradVecs * kThreads vectors each
+    float inv_hi, inv_lo;        // 1 / tau as an fp32 pair
+    const void* tokens;
+    int ids32;
+    const int32_t* mask;
+    int64_t mask_stride;
+    const float* lse;
+    const float* entropy;
+    const float* grad_logp;
+    const float* grad_entropy;
+    void* grad;
+    int64_t ld_grad;
+    int* err;
+};
+
+constexpr int kGradVecs = 4;     // vectors a thread
+
+struct __align__(16) GradShared {
+    int32_t token[LMLOSS_MAX_GIVEN];         // -1 = none
+    float g[LMLOSS_MAX_GIVEN];
+    uint32_t flag[kGradVecs * kThreads / 32];   // vectors of the part that hold a given token
+    float red[kWarps];
+};
+
+// A thread's vectors start on 16-byte boundaries of the row that it writes; at a row's ends,
+// where a vector reaches past them, columns go one by one.
+template <class T, bool ENT>
+__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_constant__ GradParams p)
+{
+    constexpr int E = Logits<T>::E;
+    using raw = typename T::raw;
+    __shared__ GradShared sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
+    const raw* z = static_cast<const raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
+    raw* g = static_cast<raw*>(p.grad) + static_cast<int64_t>(row) * p.ld_grad;
+    const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / T::kBytes);   // columns of the first vector before the row
+    const bool aligned = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(g)) & 15u) == 0;
+    const int v0 = part * (kGradVecs * kThreads);
+    const float lse = p.lse[row];
+    const bool none = lse == -INFINITY;
+
+    // ---- the given tokens: their gradients' sum, and which vectors hold one
+    if (tid < kGradVecs * kThreads / 32) sm.flag[tid] = 0;
+    __syncthreads();
+    float sum = 0.f;
+    for (int j = tid; j < p.n; j += kThreads) {
+        const int64_t o = static_cast<int64_t>(row) * p.n + j, t = load_token(p.tokens, p.ids32, o);
+        const bool in = t >= 0 && t < p.V;
+        if (!in && t != LMLOSS_IGNORE_INDEX) set_error(p.err, kErrBadTarget);
+        const float x = in ? p.grad_logp[o] : 0.f;
+        sm.token[j] = in ? static_cast<int>(t) : -1;
+        sm.g[j] = x;
+        sum += x;
+        if (in) {
+            const int64_t v = (t + off) / E - v0;
+            if (v >= 0 && v < kGradVecs * kThreads) atomicOr(&sm.flag[v >> 5], 1u << (v & 31));
+        }
+    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sm.red[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += sm.red[w];
+    const float ge = ENT ? p.grad_entropy[row] : 0.f;
+    // by(v) = sum + ge (ln p + H)
+    const float base = ENT ? fmaf(ge, p.entropy[row], sum) : sum;
+
+    auto one = [&](float x, int c, bool marked) {
+        if (none || !allowed(mask, c)) return 0.f;
+        float d = fmaf(x, p.inv_hi, -lse);
+        // (16-bit results do not show what 1 / tau loses as one fp32; -inf takes no second product)
+        if constexpr (T::kBytes == 4) d = fmaf(max_nan(x, -3.402823466e38f), p.inv_lo, d);
+        d = max_nan(d, kLeast);
+        const float pr = ex2(d * kLog2e);
+        float out = -pr * (ENT ? fmaf(ge, d, base) : base);
+        if (marked)
+            for (int j = 0; j < p.n; ++j)
+                if (sm.token[j] == c) out += sm.g[j];
+        return out * p.inv_hi;
+    };
+    auto column = [&](int c, bool marked) { g[c] = static_cast<raw>(T::round(one(T::widen(z[c]), c, marked))); };
+
+    uint4 x[kGradVecs];
+#pragma unroll
+    for (int k = 0; k < kGradVecs; ++k) {
+        const int64_t c = static_cast<int64_t>(v0 + k * kThreads + tid) * E - off;
+        if (aligned && c >= 0 && c + E <= p.V) x[k] = *reinterpret_cast<const uint4*>(z + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kGradVecs; ++k) {
+        const int v = k * kThreads + tid;
+        const int64_t c = static_cast<int64_t>(v0 + v) * E - off;
+        if (c >= p.V) break;
+        const bool marked = sm.flag[v >> 5] >> (v & 31) & 1u;
+        if (c < 0 || c + E > p.V || !aligned) {
+            for (int i = 0; i < E; ++i)
+                if (c + i >= 0 && c + i < p.V) column(static_cast<int>(c) + i, marked);
+            continue;
+        }
+        Pack<T, E> q;
+        q.w[0] = x[k].x; q.w[1] = x[k].y; q.w[2] = x[k].z; q.w[3] = x[k].w;
+        float out[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) out[i] = one(q.get(i), static_cast<int>(c) + i, marked);
+        q.set_all(out);
+        q.store(g + c);
+    }
+}
+
+// ------------------------------------------------------------------- host
+constexpr int kMaxRowsALaunch = kVocabCounters;
+constexpr int64_t kMaxCols = (int64_t(1) << 31) - (1 << 16);   // a block's columns run a little past V in 32 bits
+
+bool good_temperature(float t) { return t >= 0x1p-20f && t <= 0x1p20f; }
+
+lmloss_status check_logprobs(const lmloss_logprobs_args* a, bool pointers)
+{
+    if (!a) return LMLOSS_ERR_INVALID_ARG;
+    if (a->T < 0 || a->V < 1 || a->ld < a->V || a->n < 0) return LMLOSS_ERR_INVALID_ARG;
+    if (a->M < 0 || a->M > kMaxTop || !float_dtype(a->dtype)) return LMLOSS_ERR_INVALID_ARG;
+    if (a->ids_dtype != LMLOSS_INT64 && a->ids_dtype != LMLOSS_INT32) return LMLOSS_ERR_INVALID_ARG;
+    if (!good_temperature(a->temperature) || a->mask_stride < 0) return LMLOSS_ERR_INVALID_ARG;
+    if (a->V > kMaxCols || a->T >= (int64_t(1) << 30) || a->n > (int64_t(1) << 20)) return LMLOSS_ERR_UNSUPPORTED;
+    if (a->T > 0 && a->ld > INT64_MAX / 16 / a->T) return LMLOSS_ERR_INVALID_ARG;
+    if (!pointers) return LMLOSS_OK;
+    if (a->token_mask && a->mask_stride != 0 && a->mask_stride < (a->V + 31) / 32) return LMLOSS_ERR_INVALID_ARG;
+    if (a->T > 0) {
+        const int id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
+        if (!a->logits || reinterpret_cast<uintptr_t>(a->logits) % float_bytes(a->dtype)) return LMLOSS_ERR_INVALID_ARG;
+        if (a->n > 0 && (!a->tokens || !a->logp_out || reinterpret_cast<uintptr_t>(a->tokens) % id_bytes))
+            return LMLOSS_ERR_INVALID_ARG;
+        if (a->M > 0 && (!a->top_logp_out || !a->top_tokens_out)) return LMLOSS_ERR_INVALID_ARG;
+    }
+    return LMLOSS_OK;
+}
+
+struct LogprobsPlan {
+    int vpt, tiles, slices;
+    size_t keys, stats, total;
+};
+
+// As a beam step's: tiles of four vectors a thread, or of one where those would not give
+// every SM a block; a block costs its tiles and the fixed part.  Cut rows leave at most kMaxParts
+// parts in all.
+LogprobsPlan plan_logprobs(const lmloss_logprobs_args* a, int num_sms)
+{
+    LogprobsPlan P{};
+    const int64_t rows = std::min<int64_t>(std::max<int64_t>(a->T, 1), kMaxRowsALaunch), E = 16 / float_bytes(a->dtype);
+    auto tiles_of = [&](int vpt) { return (a->V + vpt * kThreads * E - 1) / (vpt * kThreads * E); };
+    P.vpt = rows * tiles_of(4) >= num_sms ? 4 : 1;
+    const int64_t all = tiles_of(P.vpt), fixed = P.vpt == 4 ? 8 : 32;
+    const int64_t most = std::min<int64_t>(std::max<int64_t>(kMaxParts / rows, 1), kMaxLists);
+    const int64_t least = (all + most - 1) / most;
+    int64_t tiles = all, best = INT64_MAX;
+    for (int64_t t = least; t <= all && t <= least + 63; ++t) {
+        const int64_t blocks = rows * ((all + t - 1) / t);
+        const int64_t cost = std::max<int64_t>((blocks + num_sms - 1) / num_sms, 3) * (t + fixed);
+        if (cost < best) {
+            best = cost;
+            tiles = t;
+        }
+    }
+    P.tiles = static_cast<int>(tiles);
+    P.slices = static_cast<int>((all + tiles - 1) / tiles);
+    const size_t parts = P.slices > 1 ? static_cast<size_t>(rows) * P.slices : 0;
+    P.stats = vocab_align(sizeof(uint64_t) * parts * a->M);
+    P.total = P.stats + vocab_align(sizeof(float4) * parts);
+    return P;
+}
+
+template <class T, int VPT, bool ALIGNED>
+void launch_rows(const LogprobsParams& p, cudaStream_t stream)
+{
+    const unsigned grid = static_cast<unsigned>(p.T) * static_cast<unsigned>(p.slices);
+    if (p.entropy_out) logprobs_kernel<T, VPT, ALIGNED, true><<<grid, kThreads, 0, stream>>>(p);
+    else logprobs_kernel<T, VPT, ALIGNED, false><<<grid, kThreads, 0, stream>>>(p);
+}
+template <class T>
+void launch_rows(const LogprobsParams& p, int vpt, bool aligned, cudaStream_t stream)
+{
+    if (vpt == 4) aligned ? launch_rows<T, 4, true>(p, stream) : launch_rows<T, 4, false>(p, stream);
+    else aligned ? launch_rows<T, 1, true>(p, stream) : launch_rows<T, 1, false>(p, stream);
+}
+
+lmloss_status check_grad(const lmloss_logprobs_grad_args* a)
+{
+    if (!a) return LMLOSS_ERR_INVALID_ARG;
+    if (a->T < 0 || a->V < 1 || a->ld < a->V || a->ld_grad < a->V || a->n < 0) return LMLOSS_ERR_INVALID_ARG;
+    if (!float_dtype(a->dtype) || (a->ids_dtype != LMLOSS_INT64 && a->ids_dtype != LMLOSS_INT32)) return LMLOSS_ERR_INVALID_ARG;
+    if (!good_temperature(a->temperature) || a->mask_stride < 0) return LMLOSS_ERR_INVALID_ARG;
+    if (a->V > kMaxCols || a->T >= (int64_t(1) << 30) || a->n > LMLOSS_MAX_GIVEN) return LMLOSS_ERR_UNSUPPORTED;
+    if (a->T > 0 && (a->ld > INT64_MAX / 16 / a->T || a->ld_grad > INT64_MAX / 16 / a->T)) return LMLOSS_ERR_INVALID_ARG;
+    if (a->token_mask && a->mask_stride != 0 && a->mask_stride < (a->V + 31) / 32) return LMLOSS_ERR_INVALID_ARG;
+    if (a->T > 0) {
+        const uintptr_t z = reinterpret_cast<uintptr_t>(a->logits), g = reinterpret_cast<uintptr_t>(a->grad_out);
+        const int es = float_bytes(a->dtype), id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
+        if (!z || !g || z % es || g % es || !a->lse) return LMLOSS_ERR_INVALID_ARG;
+        if (a->n > 0 && (!a->tokens || !a->grad_logp || reinterpret_cast<uintptr_t>(a->tokens) % id_bytes))
+            return LMLOSS_ERR_INVALID_ARG;
+        if (a->grad_entropy && !a->entropy) return LMLOSS_ERR_INVALID_ARG;
+        if (z == g) {
+            if (a->ld != a->ld_grad && a->T > 1) return LMLOSS_ERR_INVALID_ARG;
+        } else {
+            const uintptr_t z_end = z + static_cast<uintptr_t>(((a->T - 1) * a->ld + a->V) * es);
+            const uintptr_t g_end = g + static_cast<uintptr_t>(((a->T - 1) * a->ld_grad + a->V) * es);
+            if (z < g_end && g < z_end) return LMLOSS_ERR_INVALID_ARG;
+        }
+    }
+    return LMLOSS_OK;
+}
+
+template <class T>
+void launch_grad(const GradParams& p, cudaStream_t stream)
+{
+    const unsigned grid = static_cast<unsigned>(p.T) * static_cast<unsigned>(p.parts);
+    if (p.grad_entropy) logprobs_grad_kernel<T, true><<<grid, kThreads, 0, stream>>>(p);
+    else logprobs_grad_kernel<T, false><<<grid, kThreads, 0, stream>>>(p);
+}
+
+}  // namespace
+}  // namespace lmloss
+
+using namespace lmloss;
+
+extern "C" {
+
+lmloss_status lmloss_logprobs_check_args(const lmloss_logprobs_args* a) { return check_logprobs(a, true); }
+
+lmloss_status lmloss_logprobs_check_grad_args(const lmloss_logprobs_grad_args* a) { return check_grad(a); }
+
+lmloss_status lmloss_logprobs_workspace(const lmloss_logprobs_args* a, size_t* bytes)
+{
+    if (!bytes) return LMLOSS_ERR_INVALID_ARG;
+    const lmloss_status st = check_logprobs(a, false);
+    if (st != LMLOSS_OK) return st;
+    // enough for any plan of no more rows
+    const size_t parts = a->T > 0 ? kMaxParts : 0;
+    *bytes = vocab_align(sizeof(uint64_t) * parts * a->M) + vocab_align(sizeof(float4) * parts);
+    return LMLOSS_OK;
+}
+
+lmloss_status lmloss_logprobs_forward(lmloss_vocab_handle h, const lmloss_logprobs_args* a, cudaStream_t stream)
+{
+    if (!h) return LMLOSS_ERR_INVALID_ARG;
+    const lmloss_status st = check_logprobs(a, true);
+    if (st != LMLOSS_OK) return st;
+    if (a->T == 0) return LMLOSS_OK;
+    VocabDeviceGuard g(h->device);
+    if (!g.ok) return LMLOSS_ERR_CUDA;
+    const int es = float_bytes(a->dtype), id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
+    const bool aligned = aligned16(a->logits) && a->ld * es % 16 == 0;
+    // as many rows a launch as there are counters
+    for (int64_t r0 = 0; r0 < a->T; r0 += kMaxRowsALaunch) {
+        lmloss_logprobs_args part = *a;
+        part.T = std::min<int64_t>(a->T - r0, kMaxRowsALaunch);
+        const LogprobsPlan P = plan_logprobs(&part, h->num_sms);
+        if (P.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
+        LogprobsParams p{};
+        p.logits = static_cast<const unsigned char*>(a->logits) + r0 * a->ld * es;
+        p.ld = a->ld;
+        p.T = static_cast<int>(part.T);
+        p.V = static_cast<int>(a->V);
+        p.n = a->n;
+        p.M = a->M;
+        p.slices = P.slices;
+        p.tiles = P.tiles;
+        p.mul = static_cast<float>(1.4426950408889634074 / static_cast<double>(a->temperature));
+        p.inv_tau = 1.0 / static_cast<double>(a->temperature);
+        p.tokens = a->n ? static_cast<const unsigned char*>(a->tokens) + r0 * a->n * id_bytes : nullptr;
+        p.ids32 = a->ids_dtype == LMLOSS_INT32;
+        p.mask = a->token_mask ? a->token_mask + r0 * a->mask_stride : nullptr;
+        p.mask_stride = a->mask_stride;
+        p.logp_out = a->n ? a->logp_out + r0 * a->n : nullptr;
+        p.lse_out = a->lse_out ? a->lse_out + r0 : nullptr;
+        p.entropy_out = a->entropy_out ? a->entropy_out + r0 : nullptr;
+        p.top_logp_out = a->M ? a->top_logp_out + r0 * a->M : nullptr;
+        p.top_tokens_out = a->M ? a->top_tokens_out + r0 * a->M : nullptr;
+        p.keys = reinterpret_cast<uint64_t*>(h->ws);
+        p.stats = reinterpret_cast<float4*>(h->ws + P.stats);
+        p.done = h->counters;
+        p.err = h->err;
+        switch (a->dtype) {
+        case LMLOSS_BF16: launch_rows<Bf16>(p, P.vpt, aligned, stream); break;
+        case LMLOSS_FP16: launch_rows<Fp16>(p, P.vpt, aligned, stream); break;
+        default: launch_rows<Fp32>(p, P.vpt, aligned, stream); break;
+        }
+        const lmloss_status launched = vocab_launch_err();
+        if (launched != LMLOSS_OK) return launched;
+    }
+    return LMLOSS_OK;
+}
+
+lmloss_status lmloss_logprobs_backward(lmloss_vocab_handle h, const lmloss_logprobs_grad_args* a, cudaStream_t stream)
+{
+    if (!h) return LMLOSS_ERR_INVALID_ARG;
+    const lmloss_status st = check_grad(a);
+    if (st != LMLOSS_OK) return st;
+    if (a->T == 0) return LMLOSS_OK;
+    VocabDeviceGuard g(h->device);
+    if (!g.ok) return LMLOSS_ERR_CUDA;
+    const int es = float_bytes(a->dtype), id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
+    const int64_t E = 16 / es, vecs = (a->V + E - 1 + E - 1) / E, per = kGradVecs * kThreads;   // a vector more where rows start inside one
+    const int64_t parts = (vecs + per - 1) / per;
+    const int64_t most = std::max<int64_t>(((int64_t(1) << 31) - 1) / parts, 1);
+    for (int64_t r0 = 0; r0 < a->T; r0 += most) {
+        GradParams p{};
+        p.logits = static_cast<const unsigned char*>(a->logits) + r0 * a->ld * es;
+        p.ld = a->ld;
+        p.T = static_cast<int>(std::min<int64_t>(a->T - r0, most));
+        p.V = static_cast<int>(a->V);
+        p.n = static_cast<int>(a->n);
+        p.parts = static_cast<int>(parts);
+        const double inv = 1.0 / static_cast<double>(a->temperature);
+        p.inv_hi = static_cast<float>(inv);
+        p.inv_lo = static_cast<float>(inv - static_cast<double>(p.inv_hi));
+        p.tokens = a->n ? static_cast<const unsigned char*>(a->tokens) + r0 * a->n * id_bytes : nullptr;
+        p.ids32 = a->ids_dtype == LMLOSS_INT32;
+        p.mask = a->token_mask ? a->token_mask + r0 * a->mask_stride : nullptr;
+        p.mask_stride = a->mask_stride;
+        p.lse = a->lse + r0;
+        p.entropy = a->grad_entropy ? a->entropy + r0 : nullptr;
+        p.grad_logp = a->n ? a->grad_logp + r0 * a->n : nullptr;
+        p.grad_entropy = a->grad_entropy ? a->grad_entropy + r0 : nullptr;
+        p.grad = static_cast<unsigned char*>(a->grad_out) + r0 * a->ld_grad * es;
+        p.ld_grad = a->ld_grad;
+        p.err = h->err;
+        switch (a->dtype) {
+        case LMLOSS_BF16: launch_grad<Bf16>(p, stream); break;
+        case LMLOSS_FP16: launch_grad<Fp16>(p, stream); break;
+        default: launch_grad<Fp32>(p, stream); break;
+        }
+        const lmloss_status launched = vocab_launch_err();
+        if (launched != LMLOSS_OK) return launched;
+    }
+    return LMLOSS_OK;
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
 """PyTorch-facing wrapper of the vocabulary operators of the lmloss C ABI:
-embedding lookup and gradient, beam search's step, reordering of beam states.
+embedding lookup and gradient, beam search's step, reordering of beam states,
+log-probabilities of given tokens with their gradient, and vocabulary tables in 4 bits.
 
 Tensors only supply device pointers, strides and the current CUDA stream; every
 step runs in the library's kernels, and there is no CPU path.
@@ -79,10 +80,32 @@ class BeamStep:
     lengths: Optional[torch.Tensor] = None      # [B, M] int32
 
 
+@dataclass
+class TokenLogprobs:
+    logp: Optional[torch.Tensor]                # [T, n] float32 (the given tokens' shape)
+    lse: torch.Tensor                           # [T] float32
+    entropy: Optional[torch.Tensor]             # [T] float32
+    top_logp: Optional[torch.Tensor] = None     # [T, M] float32
+    top_tokens: Optional[torch.Tensor] = None   # [T, M] int64
+
+
+@dataclass
+class Table4:
+    """A [V, columns] table in 4 bits: scales[g, v] * (q - zeros[g, v]) with g = column // group_size,
+    zeros 8 where there are none.  Every row and every group begins on a 16-byte boundary
+    (`VocabOps.new_table4` makes such tensors, as views of wider ones)."""
+    values: torch.Tensor                        # [V, ceil(columns / 2)] uint8: the lower column in the low half
+    scales: torch.Tensor                        # [G, V] float16, bfloat16 or float32
+    zeros: Optional[torch.Tensor]               # [G, V] uint8
+    columns: int
+    group_size: int = 128
+
+
 class VocabOps:
     """One handle of the vocabulary operators, with workspace for embedding
-    gradients of up to max_tokens positions and max_dim columns and for beam
-    steps of up to max_rows rows of logits, at vocabularies of up to max_vocab.
+    gradients of up to max_tokens positions and max_dim columns, for beam steps and
+    log-probabilities of up to max_rows rows of logits at vocabularies of up to max_vocab,
+    and for logits from 4-bit tables of up to max_rows rows and max_dim columns.
 
     Calls run on `stream`, or on the current stream, and do not synchronise; calls
     on one handle must not overlap.  A `stream` other than the current one has to
@@ -102,6 +125,9 @@ class VocabOps:
         lib = _lib.load()
         self._forward, self._backward = lib.lmloss_embedding_forward, lib.lmloss_embedding_backward
         self._step, self._reorder = lib.lmloss_beam_step, lib.lmloss_beam_reorder
+        self._logprobs, self._logprobs_grad = lib.lmloss_logprobs_forward, lib.lmloss_logprobs_backward
+        self._quantize, self._lookup4, self._logits4 = (lib.lmloss_table4_quantize, lib.lmloss_table4_lookup,
+                                                        lib.lmloss_table4_logits)
         need = 0
         if max_tokens > 0:
             a = _lib.lmloss_embedding_args(T=max_tokens, V=max_vocab, D=max_dim, ld_table=max_dim, ld_rows=max_dim,
@@ -111,6 +137,12 @@ class VocabOps:
             b = _lib.lmloss_beam_args(B=max_rows, K=1, M=_lib.LMLOSS_MAX_BEAMS, V=max_vocab, ld=max_vocab,
                                       dtype=_lib.LMLOSS_FP32, eos_token=-1)
             need = max(need, _lib.lmloss_beam_workspace(b))
+            c = _lib.lmloss_logprobs_args(T=max_rows, V=max_vocab, ld=max_vocab, M=_lib.LMLOSS_MAX_ALTERNATIVES,
+                                          temperature=1.0)
+            need = max(need, _lib.lmloss_logprobs_workspace(c))
+            d = _lib.lmloss_table4_logits_args(T=max_rows)
+            d.table.V, d.table.D, d.table.group = max_vocab, max(max_dim, 1), 32
+            need = max(need, _lib.lmloss_table4_logits_workspace(d))
         self.workspace_bytes = need
         self.handle = _lib.lmloss_vocab_create(device, need)
 
@@ -391,3 +423,253 @@ class VocabOps:
         (s0, r0, n0), (s1, r1, n1), (s2, r2, n2) = outer
         return _lib.lmloss_beam_state(t.data_ptr(), o.data_ptr(), run * es, ts[d] * es, os_[d] * es, (n0, n1, n2),
                                       (r0 * es, r1 * es, r2 * es), (s0 * es, s1 * es, s2 * es))
+
+    # ----------------------------------------------------- log-probabilities
+    def _given(self, tokens: torch.Tensor, T: int):
+        """(type, tokens a row) of given tokens [T, n] or [T]."""
+        dtype = _IDS.get(tokens.dtype)
+        if dtype is None:
+            raise TypeError(f"tokens: must be int64 or int32, got {tokens.dtype}")
+        if tokens.dim() not in (1, 2) or tokens.size(0) != T:
+            raise ValueError(f"tokens: must be [{T}] or [{T}, n], got {tuple(tokens.shape)}")
+        if not tokens.is_contiguous():
+            raise ValueError("tokens: must be contiguous")
+        if tokens.get_device() != self._index:
+            raise ValueError(f"tokens: on {tokens.device}, the handle on {self.device}")
+        return dtype, 1 if tokens.dim() == 1 else tokens.size(1)
+
+    def _mask(self, token_mask: torch.Tensor, rows: int, V: int):
+        """(pointer, words between rows) of a token mask [rows or 1, ceil(V / 32)]."""
+        words = (V + 31) // 32
+        if token_mask.dim() != 2 or token_mask.size(0) not in (1, rows):
+            raise ValueError(f"token_mask: must be [{rows} or 1, {words}]")
+        _check(token_mask, "token_mask", torch.int32, token_mask.size(0), words, self._index)
+        return token_mask.data_ptr(), 0 if token_mask.size(0) == 1 else words
+
+    def token_logprobs(self, logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, num_top: int = 0,
+                       temperature: float = 1.0, token_mask: Optional[torch.Tensor] = None, entropy: bool = True,
+                       stream: Optional[torch.cuda.Stream] = None) -> TokenLogprobs:
+        """Log-probabilities of the given tokens [T, n] or [T] (int64 or int32, contiguous) under
+        softmax(logits / temperature), logits [T, V] (bfloat16, float16 or float32, unit column
+        stride), with the rows' logsumexp and entropy and the num_top (0 to 64) largest
+        log-probabilities with their tokens, equal ones by token.
+
+        token_mask [T or 1, ceil(V / 32)] int32: bit v % 32 of word v / 32 allows token v; the softmax is
+        over the allowed ones.  A token of -100 gives 0, another outside [0, V) NaN and the error word, one
+        that is not allowed -inf.  Fewer than num_top candidates: -inf and -100."""
+        index = self._index
+        dtype, T, V, ld = _matrix(logits, "logits", index)
+        if not 0 <= num_top <= _lib.LMLOSS_MAX_ALTERNATIVES:
+            raise ValueError(f"num_top: 0 to {_lib.LMLOSS_MAX_ALTERNATIVES}, got {num_top}")
+        ids, n = (_lib.LMLOSS_INT64, 0) if tokens is None else self._given(tokens, T)
+        mask, mask_stride = (None, 0) if token_mask is None else self._mask(token_mask, T, V)
+        if stream is None:
+            raw, r = _raw_stream(index), self._logprobs_out(tokens, T, num_top, entropy)
+        else:
+            raw, ctx = self._enter(stream, logits, tokens, token_mask)
+            with ctx:
+                r = self._logprobs_out(tokens, T, num_top, entropy)
+        a = _lib.lmloss_logprobs_args(logits.data_ptr(), T, V, ld, dtype, ids, tokens.data_ptr() if n else None, n,
+                                      temperature, num_top, mask, mask_stride, r.logp.data_ptr() if n else None,
+                                      r.lse.data_ptr(), r.entropy.data_ptr() if entropy else None,
+                                      r.top_logp.data_ptr() if num_top else None,
+                                      r.top_tokens.data_ptr() if num_top else None)
+        st = self._logprobs(self.handle, a, raw)
+        if st != _lib.LMLOSS_OK:
+            raise self._refused(st, "lmloss_logprobs_forward", a, _lib.lmloss_logprobs_check_args,
+                                _lib.lmloss_logprobs_workspace)
+        return r
+
+    def _logprobs_out(self, tokens, T, M, entropy):
+        empty, dev, f32 = torch.empty, self.device, torch.float32
+        return TokenLogprobs(None if tokens is None else empty(tokens.shape, dtype=f32, device=dev),
+                             empty((T,), dtype=f32, device=dev), empty((T,), dtype=f32, device=dev) if entropy else None,
+                             empty((T, M), dtype=f32, device=dev) if M else None,
+                             empty((T, M), dtype=torch.int64, device=dev) if M else None)
+
+    def token_logprobs_backward(self, logits: torch.Tensor, lse: torch.Tensor, tokens: Optional[torch.Tensor] = None,
+                                grad_logp: Optional[torch.Tensor] = None, *, entropy: Optional[torch.Tensor] = None,
+                                grad_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                                token_mask: Optional[torch.Tensor] = None,
+                                grad: Union[None, str, torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """The logits' gradient [T, V], in their type, from grad_logp (of the tokens' shape, float32, at most
+        1024 tokens a row) and grad_entropy [T]: with the forward call's logits, lse, entropy, temperature and mask.
+        Gradients of alternatives: give their tokens.  grad: a tensor to write, "inplace" (over the logits), or
+        None for a new one.  Columns that are not allowed, and rows in which nothing is, get 0."""
+        index = self._index
+        dtype, T, V, ld = _matrix(logits, "logits", index)
+        if (tokens is None) != (grad_logp is None):
+            raise ValueError("tokens and grad_logp: both or neither")
+        ids, n = (_lib.LMLOSS_INT64, 0) if tokens is None else self._given(tokens, T)
+        if n > _lib.LMLOSS_MAX_GIVEN:
+            raise ValueError(f"tokens: at most {_lib.LMLOSS_MAX_GIVEN} a row, got {n}")
+        vectors = [("lse", lse, (T,))]
+        if tokens is not None:
+            vectors.append(("grad_logp", grad_logp, tuple(tokens.shape)))
+        if grad_entropy is not None:
+            if entropy is None:
+                raise ValueError("grad_entropy: needs the forward call's entropy")
+            vectors += [("entropy", entropy, (T,)), ("grad_entropy", grad_entropy, (T,))]
+        for name, t, shape in vectors:
+            if t.dtype != torch.float32:
+                raise TypeError(f"{name}: expected {torch.float32}, got {t.dtype}")
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name}: expected contiguous {shape}, got {tuple(t.shape)}")
+            if t.get_device() != index:
+                raise ValueError(f"{name}: on {t.device}, the handle on {self.device}")
+        mask, mask_stride = (None, 0) if token_mask is None else self._mask(token_mask, T, V)
+        if stream is None:
+            raw, ctx = _raw_stream(index), contextlib.nullcontext()
+        else:
+            raw, ctx = self._enter(stream, logits, lse, tokens, grad_logp, entropy, grad_entropy, token_mask,
+                                   grad if isinstance(grad, torch.Tensor) else None)
+        if grad is None:
+            with ctx:
+                grad = torch.empty((T, V), dtype=logits.dtype, device=self.device)
+        elif isinstance(grad, str):
+            if grad != "inplace":
+                raise ValueError("grad: a tensor, 'inplace' or None")
+            grad = logits
+        g_type, rows, cols, ld_grad = _matrix(grad, "grad", index)
+        if g_type != dtype or rows != T or cols != V:
+            raise ValueError(f"grad: expected [{T}, {V}] of {logits.dtype}")
+        a = _lib.lmloss_logprobs_grad_args(logits.data_ptr(), T, V, ld, dtype, ids, tokens.data_ptr() if n else None, n,
+                                           temperature, mask, mask_stride, lse.data_ptr(),
+                                           grad_logp.data_ptr() if n else None,
+                                           None if grad_entropy is None else entropy.data_ptr(),
+                                           None if grad_entropy is None else grad_entropy.data_ptr(),
+                                           grad.data_ptr(), ld_grad)
+        st = self._logprobs_grad(self.handle, a, raw)
+        if st != _lib.LMLOSS_OK:
+            raise LMLossError(st, "lmloss_logprobs_backward")
+        return grad
+
+    # ------------------------------------------------------- tables in 4 bits
+    def new_table4(self, num_embeddings: int, columns: int, *, group_size: int = 128, zeros: bool = False,
+                   scale_dtype: torch.dtype = torch.float16) -> Table4:
+        """An unwritten 4-bit table of the layout that the calls below take."""
+        if num_embeddings < 1 or columns < 1 or group_size not in (32, 64, 128):
+            raise ValueError("a 4-bit table has at least one row and column, and groups of 32, 64 or 128")
+        if scale_dtype not in _FLOATS:
+            raise TypeError(f"scale_dtype: must be bfloat16, float16 or float32, got {scale_dtype}")
+        G, wide = (columns + group_size - 1) // group_size, (num_embeddings + 15) // 16 * 16
+        dev = self.device
+        values = torch.empty((num_embeddings, (columns + 31) // 32 * 16), dtype=torch.uint8, device=dev)
+        scales = torch.empty((G, wide), dtype=scale_dtype, device=dev)
+        z = torch.empty((G, wide), dtype=torch.uint8, device=dev) if zeros else None
+        return Table4(values[:, :(columns + 1) // 2], scales[:, :num_embeddings],
+                      None if z is None else z[:, :num_embeddings], columns, group_size)
+
+    def _table4(self, t: Table4):
+        """A table's lmloss_table4."""
+        values, scales, zeros, index = t.values, t.scales, t.zeros, self._index
+        V, D, g = values.size(0), t.columns, t.group_size
+        if g not in (32, 64, 128):
+            raise ValueError(f"table: groups of 32, 64 or 128 columns, got {g}")
+        dtype = _FLOATS.get(scales.dtype)
+        if values.dtype != torch.uint8 or dtype is None or (zeros is not None and zeros.dtype != torch.uint8):
+            raise TypeError("table: values and zeros are uint8, scales bfloat16, float16 or float32")
+        G = (D + g - 1) // g
+        if values.dim() != 2 or V < 1 or D < 1 or values.size(1) != (D + 1) // 2:
+            raise ValueError(f"table: values must be [V, {(D + 1) // 2}] for {D} columns, got {tuple(values.shape)}")
+        lds = []
+        for name, x, rows, es in (("values", values, V, 1), ("scales", scales, G, scales.element_size()),
+                                  ("zeros", zeros, G, 1)):
+            if x is None:
+                lds.append(0)
+                continue
+            if x.get_device() != index:
+                raise ValueError(f"table: {name} on {x.device}, the handle on {self.device}")
+            if x.dim() != 2 or x.size(0) != rows or (name != "values" and x.size(1) != V):
+                raise ValueError(f"table: {name} must be {[rows, 'columns / 2' if name == 'values' else V]}, "
+                                 f"got {tuple(x.shape)}")
+            ld, unit = x.stride()
+            cols = x.size(1)
+            if rows == 1:
+                ld = (cols * es + 15) // 16 * 16 // es
+            if (cols > 1 and unit != 1) or ld < cols or ld * es % 16 or x.data_ptr() % 16:
+                raise ValueError(f"table: {name} must have unit column stride and rows on 16-byte boundaries")
+            lds.append(ld)
+        return _lib.lmloss_table4(values.data_ptr(), lds[0], scales.data_ptr(), lds[1],
+                                  None if zeros is None else zeros.data_ptr(), lds[2], V, D, g, dtype)
+
+    def quantize_table(self, weight: torch.Tensor, out: Optional[Table4] = None, *, group_size: int = 128,
+                       zeros: bool = False, scale_dtype: torch.dtype = torch.float16,
+                       stream: Optional[torch.cuda.Stream] = None) -> Table4:
+        """The 4-bit table nearest to weight [V, D] (bfloat16, float16 or float32), group by group:
+        without zeros s = max |w| / 7 and q = w / s + 8; with zeros s = (max - min) / 15 over the weights and 0,
+        z = -min / s and q = w / s + z.  out: a table to write (its own groups, zeros and scales).  A
+        group whose weights or scale are not finite gets a scale of NaN and the error word."""
+        w_type, V, D, ld = _matrix(weight, "weight", self._index)
+        if stream is None:
+            raw, ctx = _raw_stream(self._index), contextlib.nullcontext()
+        else:
+            raw, ctx = self._enter(stream, weight, *(() if out is None else (out.values, out.scales, out.zeros)))
+        if out is None:
+            with ctx:
+                out = self.new_table4(V, D, group_size=group_size, zeros=zeros, scale_dtype=scale_dtype)
+        t = self._table4(out)
+        if t.V != V or t.D != D:
+            raise ValueError(f"out: a table of [{t.V}, {t.D}] for weights of [{V}, {D}]")
+        a = _lib.lmloss_table4_quantize_args(t, weight.data_ptr(), ld, w_type)
+        st = self._quantize(self.handle, a, raw)
+        if st != _lib.LMLOSS_OK:
+            raise LMLossError(st, "lmloss_table4_quantize")
+        return out
+
+    def table4_lookup(self, table: Table4, ids: torch.Tensor, *, scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """scale * table[ids], [*ids.shape, columns] in out_dtype (the scales' type if not said): ids and
+        out as for `embedding_forward`."""
+        id_type = self._ids(ids)
+        t = self._table4(table)
+        if stream is None:
+            raw, ctx = _raw_stream(self._index), contextlib.nullcontext()
+        else:
+            raw, ctx = self._enter(stream, table.values, table.scales, table.zeros, ids, out)
+        T, D = ids.numel(), table.columns
+        out, r_type, ld_rows = self._result(out, out_dtype or table.scales.dtype, out_dtype, (*ids.shape, D), T, D, ctx)
+        a = _lib.lmloss_table4_lookup_args(t, ids.data_ptr(), T, out.data_ptr(), ld_rows, id_type, r_type, scale)
+        st = self._lookup4(self.handle, a, raw)
+        if st != _lib.LMLOSS_OK:
+            raise LMLossError(st, "lmloss_table4_lookup")
+        return out
+
+    def _result(self, out, dtype, asked, shape, T, D, ctx):
+        """(out, its type, its row stride): one of `shape` and `dtype` made, or the caller's looked at."""
+        if out is None:
+            r_type = _FLOATS.get(dtype)
+            if r_type is None:
+                raise TypeError(f"out_dtype: must be bfloat16, float16 or float32, got {dtype}")
+            with ctx:
+                return torch.empty(shape, dtype=dtype, device=self.device), r_type, D
+        if out.shape != shape or (asked is not None and out.dtype != asked):
+            raise ValueError(f"out: expected {shape}{'' if asked is None else f' of {asked}'}")
+        r_type, _, _, ld = _matrix(_flat(out, "out", T, D), "out", self._index)
+        return out, r_type, ld
+
+    def table4_logits(self, table: Table4, hidden: torch.Tensor, *, scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """scale * hidden @ table^T: logits [..., V] of hidden rows [..., columns] (bfloat16, float16 or float32),
+        in out_dtype (hidden's if not said).  Rows of hidden and out may be strided, one stride between them all."""
+        t = self._table4(table)
+        D, V = table.columns, t.V
+        if hidden.dim() < 1 or hidden.size(-1) != D:
+            raise ValueError(f"hidden: must be [..., {D}], got {tuple(hidden.shape)}")
+        T = hidden.numel() // D
+        rows = _flat(hidden, "hidden", T, D)
+        x_type, _, _, ld = _matrix(rows, "hidden", self._index)
+        if stream is None:
+            raw, ctx = _raw_stream(self._index), contextlib.nullcontext()
+        else:
+            raw, ctx = self._enter(stream, table.values, table.scales, table.zeros, hidden, out)
+        out, o_type, ld_out = self._result(out, out_dtype or hidden.dtype, out_dtype, (*hidden.shape[:-1], V), T, V, ctx)
+        a = _lib.lmloss_table4_logits_args(t, rows.data_ptr(), T, ld, out.data_ptr(), ld_out, x_type, o_type, scale)
+        st = self._logits4(self.handle, a, raw)
+        if st != _lib.LMLOSS_OK:
+            raise self._refused(st, "lmloss_table4_logits", a, _lib.lmloss_table4_check_logits_args,
+                                _lib.lmloss_table4_logits_workspace)
+        return out
