@@ -25,7 +25,7 @@ UNITS = [("lmloss.cu", [], "lmloss.o")] + [
                                                "table4_logits")]
 DEPENDS = ["lmloss.cu", "fused_inst.cu", "fused_entry.cuh", "kernels.cuh", "aux_kernels.cuh", "ptx.cuh",
            "vocab_common.cuh", "vocab_handle.cu", "embedding.cu", "beam_math.cuh", "beam_plan.cuh", "row_stream.cuh", "beam_step.cu", "beam_reorder.cu",
-           "logprobs.cu", "table4.cuh", "table4.cu", "table4_logits.cu"]
+           "logprobs.cu", "table4.cuh", "tcgen05.cuh", "table4.cu", "table4_logits.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC"]

@@ -19,7 +19,7 @@ lmloss_status table4_check(const lmloss_table4& t, bool pointers)
     if (!pointers) return LMLOSS_OK;
     if (!t.values || !t.scales || !aligned16(t.values) || !aligned16(t.scales) || !aligned16(t.zeros))
         return LMLOSS_ERR_INVALID_ARG;
-    if (t.ld_values < (t.D + 1) / 2 || t.ld_values % 16 || t.ld_values > INT64_MAX / 16 / t.V) return LMLOSS_ERR_INVALID_ARG;
+    if (t.ld_values < (t.D + 1) / 2 || t.ld_values % 16 || t.ld_values > (int64_t(1) << 32)) return LMLOSS_ERR_INVALID_ARG;
     if (t.ld_scales < t.V || t.ld_scales > (int64_t(1) << 32) || t.ld_scales * float_bytes(t.scale_dtype) % 16)
         return LMLOSS_ERR_INVALID_ARG;
     if (t.zeros && (t.ld_zeros < t.V || t.ld_zeros > (int64_t(1) << 32) || t.ld_zeros % 16)) return LMLOSS_ERR_INVALID_ARG;
