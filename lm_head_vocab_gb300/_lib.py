@@ -22,10 +22,10 @@ UNITS = [("lmloss.cu", [], "lmloss.o")] + [
     ("fused_inst.cu", [f"-DLMLOSS_FUSED_VARIANT={k}"], f"fused_{k}.o") for k in range(8)] + [
     # the vocabulary operators
     (f"{name}.cu", [], f"{name}.o") for name in ("vocab_handle", "embedding", "beam_step", "beam_reorder", "logprobs", "table4",
-                                               "table4_logits")]
+                                               "table4_logits", "table4_rows")]
 DEPENDS = ["lmloss.cu", "fused_inst.cu", "fused_entry.cuh", "kernels.cuh", "aux_kernels.cuh", "ptx.cuh",
            "vocab_common.cuh", "vocab_handle.cu", "embedding.cu", "beam_math.cuh", "beam_plan.cuh", "row_stream.cuh", "beam_step.cu", "beam_reorder.cu",
-           "logprobs.cu", "table4.cuh", "tcgen05.cuh", "table4.cu", "table4_logits.cu"]
+           "logprobs.cu", "table4.cuh", "tcgen05.cuh", "table4.cu", "table4_logits.cuh", "table4_logits.cu", "table4_rows.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC"]

@@ -152,6 +152,19 @@ __device__ __forceinline__ void grid_dep_launch()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// -------------------------------------------------------------- registers
+// A warpgroup gives registers back, or takes some (within what the block was launched with).
+template <int REGS>
+__device__ __forceinline__ void reg_dealloc()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void reg_alloc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 // ---------------------------------------------------------------- memory
 __device__ __forceinline__ uint4 lds128(uint32_t addr)
 {

@@ -2,288 +2,254 @@
 //
 //   logits[t][v] = scale sum_g s[g][v] sum_{c in g} x[t][c] (q[v][c] - z[g][v])
 //
-// The whole numbers q - z are exact in fp16, and so is a hidden row in fp16 once a power of two
-// brings its largest value to 2^13 (bf16: what underflows is below 2^-38 of that; fp32 as a pair of fp16,
-// within 2^-24).  So the tensor cores sum exact products within a group, in fp32, and the group's sum is
-// scaled by s in fp32: no weight is rounded.
+// The whole numbers q are exact in fp16, and so is a hidden row in fp16 once a power of two brings its
+// largest value to 2^14 (bf16 and fp16: what underflows is below 2^-35 of that; fp32 as a pair of fp16,
+// within 2^-24).  So the tensor cores sum exact products within a group, in fp32; the zero point's part is
+// taken off, z sum_{c in g} x[t][c], and the rest scaled by s, in fp32: no weight is rounded.
 //
-// A block takes 256 rows of the table at a time and up to N hidden rows.  Its parts, each a step of a ring
-// ahead of the next:
-//   one warp    copies 256 rows x 128 bytes of the table, their scales and zeros    (TMA, HBM)
-//   one warp    copies the hidden rows' 128 columns, fp16, laid out for the product  (bulk copies, L2)
-//   8 warps     widen 4 bits to fp16, a thread a row, into tensor memory             (operand A)
-//   one thread  multiplies: [128 x 128] by [128 x N] for each half, a sum for each group
+// A first kernel lays the hidden rows out and sums their groups.  Up to 32 operand rows then go to a kernel of
+// independent warps (table4_rows.cu); more to the one here, in which a block takes 256 rows of the table and
+// 64 operand rows at a time.  Its parts, each a step of a ring ahead of the next:
+//   one warp    copies 256 rows x 128 bytes of the table, their scales and zeros     (TMA, HBM)
+//   one warp    copies the hidden rows' 128 columns, laid out for the product        (bulk copies, L2)
+//   16 warps    widen 4 bits to fp16, a thread a row, into tensor memory             (operand A)
+//   2 warps     multiply: [128 x 128] by [128 x 64] a half of the rows, a sum for each group
 //   8 warps     read a group's sums from tensor memory, a thread a row, and add them scaled
-// A first kernel lays the hidden rows out; the main one begins under its way.
 #include <algorithm>
 #include <cmath>
 
-#include <cuda.h>
-
-#include "table4.cuh"
-#include "tcgen05.cuh"
+#include "table4_logits.cuh"
 
 namespace lmloss {
 namespace {
 
-constexpr int kTile = 256;                   // rows of the table a block takes at once
-constexpr int kStageCols = 256;              // columns of the table a stage holds
-constexpr int kBlockCols = 128;              // columns a product takes
 constexpr int kMaxRows = 1024;               // hidden rows a launch
-constexpr int kMaxStages = 8;
-constexpr int kLoThreads = 19 * 32;          // 8 warps widen, 8 add, then: table, hidden rows, product
+constexpr int kWarpsOf = 28;                 // 16 warps widen, 8 add, then: table, hidden rows, a half's products each
+constexpr int kLogitsThreads = kWarpsOf * 32;
 constexpr uint32_t kHeader = 1024;           // barriers, before the stages
-
-struct LogitsParams {
-    Table4 t;
-    int scale_dtype, scale_bytes;
-    int groups;                  // of a row
-    int kblocks;                 // runs of kBlockCols columns of a row
-    int T;                       // hidden rows
-    int per;                     // hidden rows a block takes: N, or N / 2 as pairs
-    int tblocks;                 // runs of `per` hidden rows
-    int vtiles;
-    int pairs;                   // fp32: the first N / 2 rows the upper parts, the others the lower ones times 2^11
-    const unsigned char* x;      // [tblocks][2 kblocks][N][128 bytes], as mma_desc_128b wants them
-    const float* inverse;        // [T] by which a row's sums are multiplied
-    void* out;
-    int64_t ld_out;
-    int out_dtype;
-    float scale;
-    int qstages, xstages;
-    uint32_t stage_bytes;        // of a stage of the table: values, scales, zeros
-    int* err;
-};
+// Registers a thread of each part where 64 sums a thread do not fit an even share (72 of 896 threads):
+// in all what the block was launched with.
+constexpr int kWidenRegs = 64, kAddRegs = 104, kFewRegs = 40;
+static_assert(16 * kWidenRegs + 8 * kAddRegs + 4 * kFewRegs <= kWarpsOf * 72, "registers");
 
 // ------------------------------------------------------------- hidden rows
 struct HiddenParams {
     const void* x;
     int64_t ld;
-    int D, kblocks;
+    int D, kblocks, groups, shift;
     int N, per;
+    int few;                     // laid out for the kernel of independent warps
     unsigned char* out;
+    float* sums;
     float* inverse;
 };
 
-// A block a row.  Eight columns go to a 16-byte part in the order 0 4 1 5 2 6 3 7, as the table's words widen.
+// A block a row.  Eight columns go to a 16-byte part in the order 0 4 1 5 2 6 3 7, as the table's words widen, the
+// places 1 5 and 3 7 divided by 16.
 template <class X>
 __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ HiddenParams p)
 {
     grid_dep_launch();
     __shared__ float red[8];
+    __shared__ int odd[8];
     const int tid = threadIdx.x, row = blockIdx.x;
     const typename X::raw* x = static_cast<const typename X::raw*>(p.x) + row * p.ld;
     constexpr bool kPair = X::kBytes == 4;
-    float scale = 1.f;
-    if (!std::is_same<X, Fp16>::value) {
-        float top = 0.f;   // of what is finite
-        for (int c = tid; c < p.D; c += 256) {
-            const float a = fabsf(X::widen(x[c]));
-            if (a < INFINITY) top = fmaxf(top, a);
-        }
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if ((tid & 31) == 0) red[tid >> 5] = top;
-        __syncthreads();
-        for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
-        // 2^(13 - exponent), at most 2^126; (a subnormal's exponent counts as -127)
-        const int e = static_cast<int>(__float_as_uint(top) >> 23);
-        scale = top > 0.f ? __uint_as_float(static_cast<uint32_t>(min(13 + 254 - e, 253)) << 23) : 1.f;
+    float top = 0.f;   // of what is finite
+    bool finite = true;
+    for (int c = tid; c < p.D; c += 256) {
+        const float a = fabsf(X::widen(x[c]));
+        if (a < INFINITY) top = fmaxf(top, a);
+        else finite = false;
     }
-    if (tid == 0) p.inverse[row] = 1.f / scale;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    finite = __all_sync(0xffffffffu, finite);
+    if ((tid & 31) == 0) {
+        red[tid >> 5] = top;
+        odd[tid >> 5] = finite ? 0 : 1;
+    }
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) {
+        top = fmaxf(top, red[w]);
+        finite &= odd[w] == 0;
+    }
+    // 2^(14 - exponent), at most 2^126; (a subnormal's exponent counts as -127)
+    const int e = static_cast<int>(__float_as_uint(top) >> 23);
+    const float scale = top > 0.f ? __uint_as_float(static_cast<uint32_t>(min(14 + 254 - e, 253)) << 23) : 1.f;
+    if (tid == 0) p.inverse[row] = finite ? 1.f / scale : NAN;
     const int block = row / p.per, n = row - block * p.per;
-    unsigned char* out = p.out + static_cast<int64_t>(block) * (2 * p.kblocks) * p.N * 128;
+    unsigned char* out = p.out + static_cast<int64_t>(block) * p.kblocks * (p.N * 256);
+    float* sums = p.sums + static_cast<int64_t>(block) * p.groups * p.N;
+    const int lanes = (1 << p.shift) / 8;
     for (int u = tid; u < p.kblocks * 16; u += 256) {
         uint32_t hi[4], lo[4];
+        float sum = 0.f, sum_lo = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float v[2];
             __half h[2], l[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int c = 8 * u + i + 4 * k;
-                v[k] = c < p.D ? X::widen(x[c]) * scale : 0.f;
-                h[k] = __float2half_rn(v[k]);
-                const float rest = (v[k] - __half2float(h[k])) * 2048.f;
-                l[k] = __float2half_rn(fabsf(v[k]) < INFINITY ? rest : 0.f);
+                const float v = finite && c < p.D ? X::widen(x[c]) * scale * (i & 1 ? 0.0625f : 1.f) : 0.f;
+                const float back = i & 1 ? 16.f : 1.f;
+                h[k] = __float2half_rn(v);
+                sum += __half2float(h[k]) * back;
+                if (kPair) {
+                    l[k] = __float2half_rn((v - __half2float(h[k])) * 2048.f);
+                    sum_lo += __half2float(l[k]) * back;
+                }
             }
             hi[i] = static_cast<uint32_t>(__half_as_ushort(h[0])) | static_cast<uint32_t>(__half_as_ushort(h[1])) << 16;
-            lo[i] = static_cast<uint32_t>(__half_as_ushort(l[0])) | static_cast<uint32_t>(__half_as_ushort(l[1])) << 16;
+            if (kPair) lo[i] = static_cast<uint32_t>(__half_as_ushort(l[0])) | static_cast<uint32_t>(__half_as_ushort(l[1])) << 16;
         }
-        const int half = u >> 3, part = u & 7;
-        auto place = [&](int r) { return out + (static_cast<int64_t>(half) * p.N + r) * 128 + ((part ^ (r & 7)) << 4); };
-        *reinterpret_cast<uint4*>(place(n)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (kPair) *reinterpret_cast<uint4*>(place(n + p.N / 2)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int kb = u >> 4, part = u & 15;
+        auto place = [&](int r) -> uint4* {
+            unsigned char* b = out + static_cast<int64_t>(kb) * (p.N * 256);
+            // independent warps: [N][256 bytes]; the product of tensor memory: [2][N][128 bytes], swizzled
+            return reinterpret_cast<uint4*>(p.few ? b + r * 256 + ((part ^ ((r & 1) << 2)) << 4)
+                                                  : b + ((part >> 3) * p.N + r) * 128 + (((part & 7) ^ (r & 7)) << 4));
+        };
+        *place(n) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (kPair) *place(n + p.N / 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        // (16 threads a block of columns go through here together)
+        const uint32_t together = 0xffffu << (tid & 16);
+        for (int o = 1; o < lanes; o <<= 1) {
+            sum += __shfl_xor_sync(together, sum, o);
+            if (kPair) sum_lo += __shfl_xor_sync(together, sum_lo, o);
+        }
+        const int g = (8 * u) >> p.shift;
+        if ((u & (lanes - 1)) == 0 && g < p.groups) {
+            sums[static_cast<int64_t>(g) * p.N + n] = sum * 0x1p-24f;
+            if (kPair) sums[static_cast<int64_t>(g) * p.N + n + p.N / 2] = sum_lo * 0x1p-24f;
+        }
     }
 }
 
 // ------------------------------------------------------------------- main
 struct __align__(16) LogitsBarriers {
     uint64_t q_full[kMaxStages], q_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages];
-    uint64_t a_full[2][2], a_empty[2][2], d_full[2][4], d_empty[2][4];
+    uint64_t a_full[2][2], a_empty[2][2], d_full[2][2], d_empty[2][2];
     uint32_t tmem;
     int failed;
 };
 
-// A ring's position: which slot, and the parity of the round.
-struct Ring {
-    int slot = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void next(int n)
-    {
-        if (++slot == n) {
-            slot = 0;
-            parity ^= 1u;
-        }
-    }
-};
-
-// q - z of a word's eight numbers as fp16, in the order 0 4 1 5 2 6 3 7: 0x6400 | q is 1024 + q, and with q four
-// bits further up 1024 + 16 q.  low: 1024 + z twice; high: -(64 + z) twice.
-__device__ __forceinline__ void widen_word(uint32_t w, __half2 low, __half2 high, uint32_t* out)
-{
-    const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
-    const uint32_t w8 = w >> 8;
-    uint32_t a[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u, (w8 & 0x000f000fu) | 0x64006400u,
-                     (w8 & 0x00f000f0u) | 0x64006400u};
-    __half2* h = reinterpret_cast<__half2*>(a);
-    h[0] = __hsub2(h[0], low);
-    h[1] = __hfma2(h[1], sixteenth, high);
-    h[2] = __hsub2(h[2], low);
-    h[3] = __hfma2(h[3], sixteenth, high);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = a[i];
-}
-
-__device__ __forceinline__ void store_logit(const LogitsParams& p, int64_t t, int64_t v, float x)
-{
-    const int64_t at = t * p.ld_out + v;
-    if (p.out_dtype == LMLOSS_BF16) static_cast<uint16_t*>(p.out)[at] = Bf16::round(x);
-    else if (p.out_dtype == LMLOSS_FP16) static_cast<uint16_t*>(p.out)[at] = Fp16::round(x);
-    else static_cast<float*>(p.out)[at] = x;
-}
-
 template <int N>
-__global__ void __launch_bounds__(kLoThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ CUtensorMap map)
+__global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ CUtensorMap map)
 {
     // tensor memory: A two buffers of 64 columns for each half, D kSums of N columns for each half
-    constexpr int kSums = N == 64 ? 2 : 4;
-    constexpr uint32_t kColumns = 256 + 2 * kSums * N <= 512 ? 512 : 0;
-    static_assert(kColumns == 512, "tensor memory");
+    constexpr int kSums = 2;
+    constexpr uint32_t kColumns = 512;
+    static_assert(256 + 2 * kSums * N <= kColumns, "tensor memory");
     constexpr uint32_t kIdesc = mma_f16_idesc(N);
+    constexpr uint32_t kXBytes = N * 256;
     extern __shared__ __align__(1024) unsigned char smem[];
     LogitsBarriers& b = *reinterpret_cast<LogitsBarriers*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned char* const stages = smem + kHeader;
-    const uint32_t xbase = base + kHeader + p.qstages * p.stage_bytes;   // stage_bytes: a multiple of 1024
-    constexpr uint32_t kXBytes = N * 256;
-    const int gs = 1 << p.t.shift, per_block = kBlockCols >> p.t.shift, per_stage = kStageCols >> p.t.shift;
-    const int stages_a_tile = (p.kblocks + 1) / 2;
+    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N, 0);
+    const uint32_t xbase = base + kHeader + p.qstages * p.stage_bytes;
+    const int gs = 1 << p.shift, per_stage = kStageCols >> p.shift;
+    const int stages = (p.kblocks + 1) / 2;
     const int tiles = p.vtiles * p.tblocks;
 
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_addr(&b.q_full[i]), 1);
-            mbar_init(smem_addr(&b.q_empty[i]), 16);
+            mbar_init(smem_addr(&b.q_empty[i]), 24);
             mbar_init(smem_addr(&b.x_full[i]), 1);
-            mbar_init(smem_addr(&b.x_empty[i]), 1);
+            mbar_init(smem_addr(&b.x_empty[i]), 2);
         }
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_addr(&b.a_full[h][i]), 4);
                 mbar_init(smem_addr(&b.a_empty[h][i]), 1);
-            }
-            for (int i = 0; i < 4; ++i) {
                 mbar_init(smem_addr(&b.d_full[h][i]), 1);
                 mbar_init(smem_addr(&b.d_empty[h][i]), 4);
             }
-        }
         b.failed = 0;
         fence_mbar_init();
     }
-    if (warp == 18) tmem_alloc(smem_addr(&b.tmem), kColumns);
+    if (warp == 26) tmem_alloc(smem_addr(&b.tmem), kColumns);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = b.tmem;
 
-    // A wait that runs out ends the block: everyone's next wait runs out too.
     auto wait_one = [&](uint64_t& bar, uint32_t parity) {
-        if (mbar_wait_bounded(smem_addr(&bar), parity, kWaitLimitCycles)) return true;
-        b.failed = 1;
-        set_error(p.err, kErrTimeout);
-        return false;
+        if (!mbar_sleep_bounded(smem_addr(&bar), parity, kWaitLimitCycles, &b.failed)) set_error(p.err, kErrTimeout);
     };
     // by a whole warp, together again after it
-    auto wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+        wait_one(bar, parity);
+        __syncwarp();
+    };
 
-    if (warp < 8) {
-        // ---- widen: a thread a row of its half
-        const int half = warp >> 2, quarter = warp & 3, row = tid;   // 0 .. 255
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        Ring q, a;
+    if (warp < 16) {
+        // ---- widen: a thread a row of its half, every second block of columns
+        reg_dealloc<kWidenRegs>();
+        const int group = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = tid & 255;
+        const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128 + group * 64;
+        Ring q;
+        uint32_t parity = 1;   // of the group's buffer
+        int turn = 0;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            for (int st = 0; st < stages_a_tile; ++st) {
-                if (!wait(b.q_full[q.slot], q.parity)) goto done;
-                const unsigned char* const stage = stages + q.slot * p.stage_bytes;
-                const unsigned char* const zeros = stage + kTile * 128 + per_stage * kTile * p.scale_bytes;
+            for (int st = 0; st < stages; ++st) {
+                wait(b.q_full[q.slot], q.parity);
+                const unsigned char* const stage = smem + kHeader + q.slot * p.stage_bytes;
                 const int blocks = min(2, p.kblocks - 2 * st);
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if (!wait(b.a_empty[half][a.slot], a.parity ^ 1u)) goto done;
+                for (int kb = 0; kb < blocks; ++kb, turn ^= 1) {
+                    if (turn != group) continue;
+                    uint4 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(stage + row * 128 + (((kb * 4 + i) ^ (row & 7)) << 4));
+                    wait(b.a_empty[half][group], parity);
                     tcgen05_after_sync();
-                    const uint32_t to = tmem + lanes + half * 128 + a.slot * 64;
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
                         uint32_t r[32];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int unit = kb * 4 + part * 2 + i;   // 32 columns
-                            float z = 8.f;
-                            if (p.t.zeros) z = static_cast<float>(zeros[((unit * 32) >> p.t.shift) * kTile + row]);
-                            const __half2 low = __float2half2_rn(1024.f + z), high = __float2half2_rn(-64.f - z);
-                            const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 128 + ((unit ^ (row & 7)) << 4));
-                            widen_word(w.x, low, high, r + 16 * i);
-                            widen_word(w.y, low, high, r + 16 * i + 4);
-                            widen_word(w.z, low, high, r + 16 * i + 8);
-                            widen_word(w.w, low, high, r + 16 * i + 12);
+                            widen_word(w[part * 2 + i].x, r + 16 * i);
+                            widen_word(w[part * 2 + i].y, r + 16 * i + 4);
+                            widen_word(w[part * 2 + i].z, r + 16 * i + 8);
+                            widen_word(w[part * 2 + i].w, r + 16 * i + 12);
                         }
                         tmem_store32(to + part * 32, r);
                     }
                     tmem_wait_store();
                     tcgen05_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&b.a_full[half][a.slot]));
-                    a.next(2);
+                    if (lane == 0) mbar_arrive(smem_addr(&b.a_full[half][group]));
+                    parity ^= 1u;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&b.q_empty[q.slot]));
                 q.next(p.qstages);
             }
         }
-        for (int i = 0; i < 2; ++i, a.next(2))   // the products have read them
-            if (!wait(b.a_empty[half][a.slot], a.parity ^ 1u)) goto done;
-    } else if (warp < 16) {
+        wait(b.a_empty[half][group], parity);   // the products have read it: nothing arrives after the block's end
+    } else if (warp < 24) {
         // ---- add the groups' sums
-        const int half = (warp - 8) >> 2, quarter = warp & 3, row = tid - 256;
+        reg_alloc<kAddRegs>();
+        const int half = (warp >> 2) & 1, quarter = warp & 3, row = tid & 255;
         const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 + half * (kSums * N);
         Ring q, d;
         bool waited = false;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
-            float acc[N];
+            uint64_t acc[N / 2];
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = 0.f;
-            for (int st = 0; st < stages_a_tile; ++st) {
-                if (!wait(b.q_full[q.slot], q.parity)) goto done;
-                const unsigned char* const scales = stages + q.slot * p.stage_bytes + kTile * 128;
+            for (int i = 0; i < N / 2; ++i) acc[i] = f2_pack(0.f, 0.f);
+            for (int st = 0; st < stages; ++st) {
+                wait(b.q_full[q.slot], q.parity);
+                const unsigned char* const stage = smem + kHeader + q.slot * p.stage_bytes;
                 const int n = min(per_stage, p.groups - st * per_stage);
                 for (int g = 0; g < n; ++g) {
-                    const int at = g * kTile + row;
-                    float s;
-                    if (p.scale_dtype == LMLOSS_FP16) s = Fp16::widen(reinterpret_cast<const uint16_t*>(scales)[at]);
-                    else if (p.scale_dtype == LMLOSS_BF16) s = Bf16::widen(reinterpret_cast<const uint16_t*>(scales)[at]);
-                    else s = reinterpret_cast<const float*>(scales)[at];
-                    if (!wait(b.d_full[half][d.slot], d.parity)) goto done;
+                    const float s = widen_any(stage + lay.scales, p.scale_dtype, g * kTile + row);
+                    const float z = p.zeros ? -static_cast<float>((stage + lay.zeros)[g * kTile + row]) : -8.f;
+                    const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z);
+                    const ulonglong2* const sums = reinterpret_cast<const ulonglong2*>(stage + lay.sums + g * (N * 4));
+                    wait(b.d_full[half][d.slot], d.parity);
                     tcgen05_after_sync();
 #pragma unroll
                     for (int c = 0; c < N; c += 16) {
@@ -291,7 +257,13 @@ __global__ void __launch_bounds__(kLoThreads, 1) logits_kernel(const __grid_cons
                         tmem_load16(from + d.slot * N + c, f);
                         tmem_wait_load(f);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(s, f[i], acc[c + i]);
+                        for (int i = 0; i < 16; i += 4) {
+                            const ulonglong2 x = sums[(c + i) / 4];
+                            uint64_t& a0 = acc[(c + i) / 2];
+                            uint64_t& a1 = acc[(c + i) / 2 + 1];
+                            a0 = f2_fma(s2, f2_fma(z2, x.x, f2_pack(f[i], f[i + 1])), a0);
+                            a1 = f2_fma(s2, f2_fma(z2, x.y, f2_pack(f[i + 2], f[i + 3])), a1);
+                        }
                     }
                     tcgen05_before_sync();
                     __syncwarp();
@@ -307,117 +279,135 @@ __global__ void __launch_bounds__(kLoThreads, 1) logits_kernel(const __grid_cons
                 waited = true;
             }
             const int64_t v = static_cast<int64_t>(vt) * kTile + row;
-            if (v < p.t.V) {
+            if (v < p.V) {
                 const int t0 = tb * p.per;
+                auto put = [&](int i, float x) {
+                    if (t0 + i >= p.T) return;
+                    const float inverse = p.inverse[t0 + i];
+                    if (inverse == inverse) store_logit(p, t0 + i, v, x * 0x1p24f * inverse * p.scale);
+                    else store_plain(p, t0 + i, v);
+                };
                 if (p.pairs) {
 #pragma unroll
-                    for (int i = 0; i < N / 2; ++i)
-                        if (t0 + i < p.T)
-                            store_logit(p, t0 + i, v, fmaf(acc[i + N / 2], 1.f / 2048.f, acc[i]) * p.inverse[t0 + i] * p.scale);
+                    for (int i = 0; i < N / 4; ++i) {
+                        float a, c, e, f;
+                        f2_unpack(acc[i], a, c);
+                        f2_unpack(acc[i + N / 4], e, f);
+                        put(2 * i, fmaf(e, 1.f / 2048.f, a));
+                        put(2 * i + 1, fmaf(f, 1.f / 2048.f, c));
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (t0 + i < p.T) store_logit(p, t0 + i, v, acc[i] * p.inverse[t0 + i] * p.scale);
+                    for (int i = 0; i < N / 2; ++i) {
+                        float a, c;
+                        f2_unpack(acc[i], a, c);
+                        put(2 * i, a);
+                        put(2 * i + 1, c);
+                    }
                 }
             }
         }
-    } else if (warp == 16) {
-        // ---- the table
-        Ring q;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const int v0 = tile / p.tblocks * kTile;
-            // to the end of the 16 bytes that hold the last row's
-            const int rows = min(kTile, p.t.V - v0), whole = 16 / p.scale_bytes;
-            const uint32_t srows = (rows + whole - 1) / whole * whole, zrows = p.t.zeros ? (rows + 15) / 16 * 16 : 0u;
-            for (int st = 0; st < stages_a_tile; ++st) {
-                bool ok = true;
-                const uint32_t bar = smem_addr(&b.q_full[q.slot]), to = base + kHeader + q.slot * p.stage_bytes;
+    } else {
+        reg_dealloc<kFewRegs>();
+        if (warp == 24) {
+            // ---- the table.  Its first stages go out before the hidden rows' sums are waited for.
+            Ring q;
+            const int64_t mine = static_cast<int64_t>((tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * stages;
+            const int64_t early = min(mine, static_cast<int64_t>(p.qstages));
+            auto copy = [&](int64_t i, int slot, bool table, bool sums) {
+                const int tile = static_cast<int>(blockIdx.x + i / stages * gridDim.x), st = static_cast<int>(i % stages);
+                const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
                 const int n = min(per_stage, p.groups - st * per_stage);
-                if (lane == 0) {
-                    ok = wait_one(b.q_empty[q.slot], q.parity ^ 1u);
-                    if (ok) {
-                        mbar_arrive_expect_tx(bar, kTile * 128 + n * (srows * p.scale_bytes + zrows));
-                        tile_load_2d(to, &map, st * 128, v0, bar);
-                    }
+                const uint32_t to = base + kHeader + slot * p.stage_bytes, bar = smem_addr(&b.q_full[slot]);
+                if (table) {
+                    if (lane == 0) mbar_arrive_expect_tx(bar, stage_tx(p, n, vt * kTile));
+                    __syncwarp();
+                    copy_table(p, lay, map, st, n, vt * kTile, to, bar);
                 }
-                if (!__shfl_sync(0xffffffffu, ok, 0)) goto done;
-                if (lane < n) {
-                    const int64_t g = static_cast<int64_t>(st) * per_stage + lane;
-                    bulk_load(to + kTile * 128 + lane * kTile * p.scale_bytes,
-                              static_cast<const unsigned char*>(p.t.scales) + (g * p.t.ld_scales + v0) * p.scale_bytes,
-                              srows * p.scale_bytes, bar);
-                    if (p.t.zeros)
-                        bulk_load(to + kTile * 128 + per_stage * kTile * p.scale_bytes + lane * kTile,
-                                  p.t.zeros + g * p.t.ld_zeros + v0, zrows, bar);
-                }
-                q.next(p.qstages);
-            }
-        }
-    } else if (warp == 17) {
-        // ---- the hidden rows
-        if (lane == 0) {
+                if (sums && lane == 0) copy_sums(p, lay, st, n, tb, to, bar);
+            };
+            for (int64_t i = 0; i < early; ++i) copy(i, static_cast<int>(i), true, false);
             grid_dep_wait();
-            Ring x;
-            for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-                const unsigned char* from = p.x + static_cast<int64_t>(tile % p.tblocks) * p.kblocks * kXBytes;
-                for (int kb = 0; kb < p.kblocks; ++kb) {
-                    if (!wait_one(b.x_empty[x.slot], x.parity ^ 1u)) goto done;
-                    const uint32_t bar = smem_addr(&b.x_full[x.slot]);
-                    mbar_arrive_expect_tx(bar, kXBytes);
-                    bulk_load(xbase + x.slot * kXBytes, from + static_cast<int64_t>(kb) * kXBytes, kXBytes, bar);
-                    x.next(p.xstages);
-                }
+            for (int64_t i = 0; i < early; ++i) copy(i, static_cast<int>(i), false, true);
+            for (int64_t i = 0; i < mine; ++i, q.next(p.qstages)) {
+                if (i < early) continue;
+                wait(b.q_empty[q.slot], q.parity ^ 1u);
+                copy(i, q.slot, true, true);
             }
-            // the products have read them all: nothing arrives at a barrier after the block's end
-            for (int i = 0; i < p.xstages; ++i, x.next(p.xstages))
-                if (!wait_one(b.x_empty[x.slot], x.parity ^ 1u)) goto done;
-        }
-    } else if (lane == 0) {
-        // ---- the products
-        Ring x, a, d;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            for (int kb = 0; kb < p.kblocks; ++kb) {
-                if (!wait_one(b.x_full[x.slot], x.parity)) goto done;
-                const uint64_t desc = mma_desc_128b(xbase + x.slot * kXBytes);
-                const int n = min(per_block, p.groups - kb * per_block);
-                Ring d0 = d;
-                for (int half = 0; half < 2; ++half) {
-                    if (!wait_one(b.a_full[half][a.slot], a.parity)) goto done;
-                    tcgen05_after_sync();
-                    const uint32_t from = tmem + half * 128 + a.slot * 64;
-                    d = d0;
-                    for (int g = 0; g < n; ++g) {
-                        if (!wait_one(b.d_empty[half][d.slot], d.parity ^ 1u)) goto done;
-                        tcgen05_after_sync();
-                        const uint32_t to = tmem + 256 + (half * kSums + d.slot) * N;
-                        for (int k = 0; k < gs / 16; ++k) {
-                            const int step = g * (gs / 16) + k;   // 16 columns; 64 lie in one run of N rows
-                            mma_f16_ts(to, from + step * 8, desc + (step >> 2) * (N * 128 / 16) + (step & 3) * 2, kIdesc, k > 0);
-                        }
-                        mma_commit(smem_addr(&b.d_full[half][d.slot]));
-                        d.next(kSums);
+        } else if (warp == 25) {
+            // ---- the hidden rows
+            if (lane == 0) {
+                grid_dep_wait();
+                Ring x;
+                for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+                    const unsigned char* from = p.x + static_cast<int64_t>(tile % p.tblocks) * p.kblocks * kXBytes;
+                    for (int kb = 0; kb < p.kblocks; ++kb) {
+                        wait_one(b.x_empty[x.slot], x.parity ^ 1u);
+                        const uint32_t bar = smem_addr(&b.x_full[x.slot]);
+                        mbar_arrive_expect_tx(bar, kXBytes);
+                        bulk_load(xbase + x.slot * kXBytes, from + static_cast<int64_t>(kb) * kXBytes, kXBytes, bar);
+                        x.next(p.xstages);
                     }
-                    mma_commit(smem_addr(&b.a_empty[half][a.slot]));
                 }
-                mma_commit(smem_addr(&b.x_empty[x.slot]));
-                x.next(p.xstages);
-                a.next(2);
+                // the products have read them all: nothing arrives after the block's end
+                for (int i = 0; i < p.xstages; ++i, x.next(p.xstages)) wait_one(b.x_empty[x.slot], x.parity ^ 1u);
             }
+            __syncwarp();
+        } else {
+            // ---- the products of one half.  (One warp for both was late: its instructions took 1500 clocks a block
+            // of columns.)
+            const uint32_t leader = elect_one();
+            const int half = warp - 26;
+            auto multiply = [&](auto count) {
+                constexpr int kSteps = decltype(count)::value;   // a group's, 16 columns each
+                constexpr int kGroups = 8 / kSteps;              // of a block of columns
+                Ring x, a, d;
+                for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+                    int left = p.groups;
+                    for (int kb = 0; kb < p.kblocks; ++kb, left -= kGroups) {
+                        wait(b.x_full[x.slot], x.parity);
+                        const uint64_t desc = mma_desc_128b(xbase + x.slot * kXBytes);
+                        wait(b.a_full[half][a.slot], a.parity);
+                        const uint32_t from = tmem + half * 128 + a.slot * 64;
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) {
+                            if (g >= left) break;
+                            wait(b.d_empty[half][d.slot], d.parity ^ 1u);
+                            tcgen05_after_sync();
+                            const uint32_t to = tmem + 256 + (half * kSums + d.slot) * N;
+#pragma unroll
+                            for (int k = 0; k < kSteps; ++k) {
+                                const int step = g * kSteps + k;   // 64 columns lie in one run of N rows
+                                const uint64_t at = desc + (step >> 2) * (N * 128 / 16) + (step & 3) * 2;
+                                if (k == 0) mma_f16_ts<false>(to, from + step * 8, at, kIdesc, leader);
+                                else mma_f16_ts<true>(to, from + step * 8, at, kIdesc, leader);
+                            }
+                            mma_commit(smem_addr(&b.d_full[half][d.slot]), leader);
+                            d.next(kSums);
+                        }
+                        mma_commit(smem_addr(&b.a_empty[half][a.slot]), leader);
+                        mma_commit(smem_addr(&b.x_empty[x.slot]), leader);
+                        x.next(p.xstages);
+                        a.next(2);
+                    }
+                }
+            };
+            if (gs == 128) multiply(std::integral_constant<int, 8>{});
+            else if (gs == 64) multiply(std::integral_constant<int, 4>{});
+            else multiply(std::integral_constant<int, 2>{});
         }
     }
-done:
-    __syncwarp();
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
     if (b.failed && tid == 0) {
-        // copies may be in flight: no barrier's phase is known any more, so give them their time
+        // copies and products may be in flight: give them their time
         const long long start = clock64();
         while (clock64() - start < 20000000) {
         }
     }
     __syncthreads();
-    if (warp == 18) tmem_free(tmem, kColumns);
+    if (warp == 26) tmem_free(tmem, kColumns);
 }
 
 // ------------------------------------------------------------------- host
@@ -439,17 +429,25 @@ lmloss_status check_logits(const lmloss_table4_logits_args* a, bool pointers)
     return LMLOSS_OK;
 }
 
-// Columns of the product for `rows` operand rows (a pair counts twice).
-int columns_for(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+// Operand rows of a block's product for `rows` of them (a pair counts twice).
+int columns_for(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= kFewRows ? 32 : 64)); }
 
 int64_t kblocks_of(int64_t D) { return (D + kBlockCols - 1) / kBlockCols; }
 
-// Workspace of the hidden rows of a launch: operand rows, padded to whole blocks, and their factors.
-size_t hidden_bytes(int64_t T, int64_t D, bool pairs)
+// Workspace of a launch's hidden rows: the operand rows padded to whole blocks, as fp16 and as sums of groups
+// of any size, and a factor for each.
+struct HiddenSpace {
+    size_t sums, inverse, total;
+};
+HiddenSpace hidden_space(int64_t T, int64_t D, bool pairs)
 {
     const int64_t rows = std::min<int64_t>(T, kMaxRows) * (pairs ? 2 : 1);
-    const int64_t N = columns_for(rows), padded = (rows + N - 1) / N * N;
-    return vocab_align(static_cast<size_t>(padded * kblocks_of(D) * kBlockCols * 2));
+    const int64_t N = columns_for(rows), padded = (rows + N - 1) / N * N, k = kblocks_of(D);
+    HiddenSpace w{};
+    w.sums = vocab_align(static_cast<size_t>(padded * k * kBlockCols * 2));
+    w.inverse = w.sums + vocab_align(static_cast<size_t>(padded * k * (kBlockCols / 32) * 4));
+    w.total = w.inverse + vocab_align(static_cast<size_t>(rows) * 4);
+    return w;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -483,27 +481,25 @@ bool table_map(const lmloss_table4& t, CUtensorMap* map)
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr uint32_t kMaxShared = 227 * 1024;
-
-template <int N>
-lmloss_status launch_logits(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* h, cudaStream_t stream)
+lmloss_status launch_many_rows(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    const int per_stage = kStageCols >> p.t.shift;
-    p.stage_bytes = kTile * 128 + per_stage * kTile * (p.scale_bytes + (p.t.zeros ? 1 : 0));   // multiples of 1024
-    p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-    p.xstages = N == 64 ? 4 : 6;
-    const uint32_t left = kMaxShared - kHeader - p.xstages * N * 256;
-    p.qstages = std::min<int>(kMaxStages, left / p.stage_bytes);
-    const uint32_t bytes = kHeader + p.qstages * p.stage_bytes + p.xstages * N * 256;
-    // per device, and cheap: the attribute is the function's, whoever set it before
-    if (cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
-        cudaGetLastError();
-        return LMLOSS_ERR_CUDA;
+    constexpr int N = 64;
+    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N, 0);
+    p.stage_bytes = lay.bytes;
+    p.xstages = 4;
+    p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHeader - p.xstages * N * 256) / lay.bytes);
+    constexpr uint32_t bit = 1u << 17;
+    if (!(h->limits_raised & bit)) {
+        if (cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
+            cudaGetLastError();
+            return LMLOSS_ERR_CUDA;
+        }
+        h->limits_raised |= bit;
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.vtiles) * p.tblocks, h->num_sms)));
-    cfg.blockDim = dim3(kLoThreads);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.blockDim = dim3(kLogitsThreads);
+    cfg.dynamicSmemBytes = kHeader + p.qstages * lay.bytes + p.xstages * N * 256;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -533,8 +529,7 @@ lmloss_status lmloss_table4_logits_workspace(const lmloss_table4_logits_args* a,
     if (st != LMLOSS_OK) return st;
     *bytes = 0;
     if (a->T == 0) return LMLOSS_OK;
-    // pairs take the most
-    *bytes = hidden_bytes(a->T, a->table.D, true) + vocab_align(sizeof(float) * std::min<int64_t>(a->T, kMaxRows));
+    *bytes = hidden_space(a->T, a->table.D, true).total;   // pairs take the most
     return LMLOSS_OK;
 }
 
@@ -545,8 +540,8 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
     if (st != LMLOSS_OK) return st;
     if (a->T == 0) return LMLOSS_OK;
     const bool pairs = a->hidden_dtype == LMLOSS_FP32;
-    const size_t x_bytes = hidden_bytes(a->T, a->table.D, pairs);
-    if (x_bytes + vocab_align(sizeof(float) * std::min<int64_t>(a->T, kMaxRows)) > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
+    const HiddenSpace w = hidden_space(a->T, a->table.D, pairs);
+    if (w.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
     CUtensorMap map;
@@ -559,10 +554,14 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         x.ld = a->ld_hidden;
         x.D = static_cast<int>(a->table.D);
         x.kblocks = static_cast<int>(kblocks_of(a->table.D));
+        x.groups = static_cast<int>((a->table.D + a->table.group - 1) / a->table.group);
+        x.shift = table4_params(a->table).shift;
         x.N = N;
         x.per = pairs ? N / 2 : N;
+        x.few = N <= kFewRows;
         x.out = h->ws;
-        x.inverse = reinterpret_cast<float*>(h->ws + x_bytes);
+        x.sums = reinterpret_cast<float*>(h->ws + w.sums);
+        x.inverse = reinterpret_cast<float*>(h->ws + w.inverse);
         switch (a->hidden_dtype) {
         case LMLOSS_BF16: hidden_kernel<Bf16><<<T, 256, 0, stream>>>(x); break;
         case LMLOSS_FP16: hidden_kernel<Fp16><<<T, 256, 0, stream>>>(x); break;
@@ -570,24 +569,37 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         }
         if ((st = vocab_launch_err()) != LMLOSS_OK) return st;
         LogitsParams p{};
-        p.t = table4_params(a->table);
+        p.values = a->table.values;
+        p.ld_values = a->table.ld_values;
+        p.scales = static_cast<const unsigned char*>(a->table.scales);
+        p.ld_scales = a->table.ld_scales;
+        p.zeros = a->table.zeros;
+        p.ld_zeros = a->table.ld_zeros;
+        p.V = static_cast<int>(a->table.V);
+        p.D = x.D;
+        p.shift = x.shift;
         p.scale_dtype = a->table.scale_dtype;
         p.scale_bytes = float_bytes(a->table.scale_dtype);
-        p.groups = static_cast<int>((a->table.D + a->table.group - 1) / a->table.group);
+        p.groups = x.groups;
         p.kblocks = x.kblocks;
         p.T = T;
+        p.N = N;
         p.per = x.per;
         p.tblocks = (T + x.per - 1) / x.per;
         p.vtiles = static_cast<int>((a->table.V + kTile - 1) / kTile);
         p.pairs = pairs;
         p.x = x.out;
+        p.sums = x.sums;
         p.inverse = x.inverse;
+        p.hidden = x.x;
+        p.ld_hidden = a->ld_hidden;
+        p.hidden_dtype = a->hidden_dtype;
         p.out = static_cast<unsigned char*>(a->logits) + t0 * a->ld_logits * float_bytes(a->logits_dtype);
         p.ld_out = a->ld_logits;
         p.out_dtype = a->logits_dtype;
         p.scale = a->scale;
         p.err = h->err;
-        st = N == 16 ? launch_logits<16>(p, map, h, stream) : (N == 32 ? launch_logits<32>(p, map, h, stream) : launch_logits<64>(p, map, h, stream));
+        st = x.few ? launch_few_rows(p, map, h, stream) : launch_many_rows(p, map, h, stream);
         if (st != LMLOSS_OK) return st;
     }
     return LMLOSS_OK;

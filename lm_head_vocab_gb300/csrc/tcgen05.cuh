@@ -59,21 +59,38 @@ __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::
 __device__ __forceinline__ void tcgen05_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tcgen05_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// 1 in one thread of a whole warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one;
+}
+
 // ------------------------------------------------------------ the product
 // D [128 x n] fp32 (+)= A [128 x 16] B [n x 16]^T, both fp16: A in tensor memory, row i in lane i, two
-// neighbouring k to a column; B in shared memory by a descriptor.  By one thread.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+// neighbouring k to a column; B in shared memory by a descriptor.  A whole warp goes along, with uniform
+// operands, and the thread with `leader` issues: predicated, since in a branch of that thread alone the
+// operands' arithmetic leaves the uniform registers (8 products and a commit, n = 16: 200 clocks so, 250 there).
+template <bool ACCUMULATE>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %4, 0;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(leader), "n"(ACCUMULATE ? 1 : 0)
         : "memory");
 }
-// Arrives at a barrier of this block when every product that this thread has issued is done.
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+// Arrives at a barrier of this block when every product that the thread has issued is done.
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t leader)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
 }
 // fp16 by fp16 into fp32, 128 rows, n columns (a multiple of 16), both operands along k.
 __host__ __device__ constexpr uint32_t mma_f16_idesc(int n)
@@ -86,6 +103,35 @@ __device__ __forceinline__ uint64_t mma_desc_128b(uint32_t addr)
 {
     return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
            (uint64_t(2) << 61);
+}
+
+// ---------------------------------------------------------------- waiting
+// Waits for a phase, asleep in the barrier for up to 0.1 ms at a time.  After `limit_cycles` it sets *failed,
+// which ends every other such wait of the block at once: all go on, to a clean end with results that mean
+// nothing, and never wait for one another in vain.  False where it gave up itself.
+__device__ __forceinline__ bool mbar_sleep_bounded(uint32_t bar, uint32_t parity, long long limit_cycles, volatile int* failed)
+{
+    auto try_wait = [&] {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(100000u)
+            : "memory");
+        return done != 0;
+    };
+    if (try_wait()) return true;
+    const long long start = clock64();
+    while (!try_wait()) {
+        if (*failed) return true;
+        if (clock64() - start > limit_cycles) {
+            *failed = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // ------------------------------------------------------------ tiled copies
