@@ -24,6 +24,7 @@ namespace lmloss {
 namespace {
 
 constexpr int kMaxRows = 1024;               // hidden rows a launch
+constexpr int kMany = 64;                    // operand rows of a block's product here
 constexpr int kWarpsOf = 28;                 // 16 warps widen, 8 add, then: table, hidden rows, a half's products each
 constexpr int kLogitsThreads = kWarpsOf * 32;
 constexpr uint32_t kHeader = 1024;           // barriers, before the stages
@@ -38,7 +39,6 @@ struct HiddenParams {
     int64_t ld;
     int D, kblocks, groups, shift;
     int N, per;
-    int few;                     // laid out for the kernel of independent warps
     unsigned char* out;
     float* sums;
     float* inverse;
@@ -73,54 +73,26 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
         top = fmaxf(top, red[w]);
         finite &= odd[w] == 0;
     }
-    // 2^(14 - exponent), at most 2^126; (a subnormal's exponent counts as -127)
-    const int e = static_cast<int>(__float_as_uint(top) >> 23);
-    const float scale = top > 0.f ? __uint_as_float(static_cast<uint32_t>(min(14 + 254 - e, 253)) << 23) : 1.f;
+    const float scale = hidden_scale(top);
     if (tid == 0) p.inverse[row] = finite ? 1.f / scale : NAN;
     const int block = row / p.per, n = row - block * p.per;
     unsigned char* out = p.out + static_cast<int64_t>(block) * p.kblocks * (p.N * 256);
     float* sums = p.sums + static_cast<int64_t>(block) * p.groups * p.N;
     const int lanes = (1 << p.shift) / 8;
     for (int u = tid; u < p.kblocks * 16; u += 256) {
-        uint32_t hi[4], lo[4];
-        float sum = 0.f, sum_lo = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __half h[2], l[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int c = 8 * u + i + 4 * k;
-                const float v = finite && c < p.D ? X::widen(x[c]) * scale * (i & 1 ? 0.0625f : 1.f) : 0.f;
-                const float back = i & 1 ? 16.f : 1.f;
-                h[k] = __float2half_rn(v);
-                sum += __half2float(h[k]) * back;
-                if (kPair) {
-                    l[k] = __float2half_rn((v - __half2float(h[k])) * 2048.f);
-                    sum_lo += __half2float(l[k]) * back;
-                }
-            }
-            hi[i] = static_cast<uint32_t>(__half_as_ushort(h[0])) | static_cast<uint32_t>(__half_as_ushort(h[1])) << 16;
-            if (kPair) lo[i] = static_cast<uint32_t>(__half_as_ushort(l[0])) | static_cast<uint32_t>(__half_as_ushort(l[1])) << 16;
-        }
-        const int kb = u >> 4, part = u & 15;
-        auto place = [&](int r) -> uint4* {
-            unsigned char* b = out + static_cast<int64_t>(kb) * (p.N * 256);
-            // independent warps: [N][256 bytes]; the product of tensor memory: [2][N][128 bytes], swizzled
-            return reinterpret_cast<uint4*>(p.few ? b + r * 256 + ((part ^ ((r & 1) << 2)) << 4)
-                                                  : b + ((part >> 3) * p.N + r) * 128 + (((part & 7) ^ (r & 7)) << 4));
-        };
-        *place(n) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (kPair) *place(n + p.N / 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        // (16 threads a block of columns go through here together)
-        const uint32_t together = 0xffffu << (tid & 16);
-        for (int o = 1; o < lanes; o <<= 1) {
-            sum += __shfl_xor_sync(together, sum, o);
-            if (kPair) sum_lo += __shfl_xor_sync(together, sum_lo, o);
-        }
+        uint4 hi, lo;
+        float sum, sum_lo;
+        hidden_part<X>(x, 8 * u, p.D, finite ? scale : 0.f, hi, lo, sum, sum_lo);
+        // [2][N][128 bytes] for each block of columns, swizzled as mma_desc_128b wants it
+        const int part = u & 7;
+        auto place = [&](int r) { return reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u >> 3) * p.N + r) * 128 + ((part ^ (r & 7)) << 4)); };
+        *place(n) = hi;
+        if (kPair) *place(n + p.N / 2) = lo;
+        group_sums<kPair>(lanes, sum, sum_lo);
         const int g = (8 * u) >> p.shift;
         if ((u & (lanes - 1)) == 0 && g < p.groups) {
-            sums[static_cast<int64_t>(g) * p.N + n] = sum * 0x1p-24f;
-            if (kPair) sums[static_cast<int64_t>(g) * p.N + n + p.N / 2] = sum_lo * 0x1p-24f;
+            sums[static_cast<int64_t>(g) * p.N + n] = sum;
+            if (kPair) sums[static_cast<int64_t>(g) * p.N + n + p.N / 2] = sum_lo;
         }
     }
 }
@@ -134,7 +106,7 @@ struct __align__(16) LogitsBarriers {
 };
 
 template <int N>
-__global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ CUtensorMap map)
+__global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
 {
     // tensor memory: A two buffers of 64 columns for each half, D kSums of N columns for each half
     constexpr int kSums = 2;
@@ -146,7 +118,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
     LogitsBarriers& b = *reinterpret_cast<LogitsBarriers*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N, 0);
+    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
     const uint32_t xbase = base + kHeader + p.qstages * p.stage_bytes;
     const int gs = 1 << p.shift, per_stage = kStageCols >> p.shift;
     const int stages = (p.kblocks + 1) / 2;
@@ -311,29 +283,41 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
         reg_dealloc<kFewRegs>();
         if (warp == 24) {
             // ---- the table.  Its first stages go out before the hidden rows' sums are waited for.
-            Ring q;
-            const int64_t mine = static_cast<int64_t>((tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * stages;
-            const int64_t early = min(mine, static_cast<int64_t>(p.qstages));
-            auto copy = [&](int64_t i, int slot, bool table, bool sums) {
-                const int tile = static_cast<int>(blockIdx.x + i / stages * gridDim.x), st = static_cast<int>(i % stages);
-                const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
-                const int n = min(per_stage, p.groups - st * per_stage);
-                const uint32_t to = base + kHeader + slot * p.stage_bytes, bar = smem_addr(&b.q_full[slot]);
-                if (table) {
-                    if (lane == 0) mbar_arrive_expect_tx(bar, stage_tx(p, n, vt * kTile));
-                    __syncwarp();
-                    copy_table(p, lay, map, st, n, vt * kTile, to, bar);
+            if (lane == 0) {
+                const int64_t mine = static_cast<int64_t>((tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * stages;
+                const int early = static_cast<int>(min(mine, static_cast<int64_t>(p.qstages)));
+                int tile = blockIdx.x, st = 0;
+                auto step = [&] {
+                    if (++st == stages) {
+                        st = 0;
+                        tile += gridDim.x;
+                    }
+                };
+                auto table = [&](int slot) {
+                    const uint32_t bar = smem_addr(&b.q_full[slot]);
+                    mbar_arrive_expect_tx(bar, lay.copied + min(per_stage, p.groups - st * per_stage) * (N * 4));
+                    copy_table(p, lay, maps, st, tile / p.tblocks * kTile, base + kHeader + slot * p.stage_bytes, bar);
+                };
+                auto sums = [&](int slot) {   // the groups of a stage lie side by side
+                    bulk_load(base + kHeader + slot * p.stage_bytes + lay.sums,
+                              p.sums + (static_cast<int64_t>(tile % p.tblocks) * p.groups + st * per_stage) * N,
+                              min(per_stage, p.groups - st * per_stage) * (N * 4), smem_addr(&b.q_full[slot]));
+                };
+                for (int i = 0; i < early; ++i, step()) table(i);
+                grid_dep_wait();
+                tile = blockIdx.x;
+                st = 0;
+                for (int i = 0; i < early; ++i, step()) sums(i);
+                Ring q;
+                q.slot = early == p.qstages ? 0 : early;
+                for (int64_t i = early; i < mine; ++i, step()) {
+                    wait_one(b.q_empty[q.slot], q.parity);   // the stage before has been read
+                    table(q.slot);
+                    sums(q.slot);
+                    q.next(p.qstages);
                 }
-                if (sums && lane == 0) copy_sums(p, lay, st, n, tb, to, bar);
-            };
-            for (int64_t i = 0; i < early; ++i) copy(i, static_cast<int>(i), true, false);
-            grid_dep_wait();
-            for (int64_t i = 0; i < early; ++i) copy(i, static_cast<int>(i), false, true);
-            for (int64_t i = 0; i < mine; ++i, q.next(p.qstages)) {
-                if (i < early) continue;
-                wait(b.q_empty[q.slot], q.parity ^ 1u);
-                copy(i, q.slot, true, true);
             }
+            __syncwarp();
         } else if (warp == 25) {
             // ---- the hidden rows
             if (lane == 0) {
@@ -429,9 +413,6 @@ lmloss_status check_logits(const lmloss_table4_logits_args* a, bool pointers)
     return LMLOSS_OK;
 }
 
-// Operand rows of a block's product for `rows` of them (a pair counts twice).
-int columns_for(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= kFewRows ? 32 : 64)); }
-
 int64_t kblocks_of(int64_t D) { return (D + kBlockCols - 1) / kBlockCols; }
 
 // Workspace of a launch's hidden rows: the operand rows padded to whole blocks, as fp16 and as sums of groups
@@ -442,7 +423,7 @@ struct HiddenSpace {
 HiddenSpace hidden_space(int64_t T, int64_t D, bool pairs)
 {
     const int64_t rows = std::min<int64_t>(T, kMaxRows) * (pairs ? 2 : 1);
-    const int64_t N = columns_for(rows), padded = (rows + N - 1) / N * N, k = kblocks_of(D);
+    const int64_t padded = (rows + kMany - 1) / kMany * kMany, k = kblocks_of(D);
     HiddenSpace w{};
     w.sums = vocab_align(static_cast<size_t>(padded * k * kBlockCols * 2));
     w.inverse = w.sums + vocab_align(static_cast<size_t>(padded * k * (kBlockCols / 32) * 4));
@@ -469,22 +450,30 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-// [V, (D + 1) / 2] bytes, copied 128 bytes by kTile rows at a time.
-bool table_map(const lmloss_table4& t, CUtensorMap* map)
+bool table_maps(const lmloss_table4& t, TableMaps* maps)
 {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>((t.D + 1) / 2), static_cast<cuuint64_t>(t.V)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(t.ld_values)};
-    const cuuint32_t box[2] = {128, kTile}, steps[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, t.values, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto map = [&](CUtensorMap* to, CUtensorMapDataType type, void* base, int64_t across, int64_t down, int64_t stride, int box_across,
+                   int box_down, CUtensorMapSwizzle swizzle) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(across), static_cast<cuuint64_t>(down)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+        const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_across), static_cast<cuuint32_t>(box_down)}, steps[2] = {1, 1};
+        return encode(to, type, 2, base, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const int es = float_bytes(t.scale_dtype), n = kStageCols / t.group;
+    const int64_t G = (t.D + t.group - 1) / t.group;
+    return map(&maps->values, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.values, (t.D + 1) / 2, t.V, t.ld_values, 128, kTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           map(&maps->scales, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, t.scales, t.V, G, t.ld_scales * es, kTile,
+               n, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           (!t.zeros || map(&maps->zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.zeros, t.V, G, t.ld_zeros, kTile, n, CU_TENSOR_MAP_SWIZZLE_NONE));
 }
 
-lmloss_status launch_many_rows(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* h, cudaStream_t stream)
+lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    constexpr int N = 64;
-    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N, 0);
+    constexpr int N = kMany;
+    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
     p.stage_bytes = lay.bytes;
     p.xstages = 4;
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHeader - p.xstages * N * 256) / lay.bytes);
@@ -506,7 +495,7 @@ lmloss_status launch_many_rows(LogitsParams& p, const CUtensorMap& map, lmloss_v
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, logits_kernel<N>, p, map) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, logits_kernel<N>, p, maps) != cudaSuccess) {
         cudaGetLastError();
         return LMLOSS_ERR_CUDA;
     }
@@ -544,30 +533,10 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
     if (w.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
-    CUtensorMap map;
-    if (!table_map(a->table, &map)) return LMLOSS_ERR_CUDA;
+    TableMaps maps{};
+    if (!table_maps(a->table, &maps)) return LMLOSS_ERR_CUDA;
     for (int64_t t0 = 0; t0 < a->T; t0 += kMaxRows) {
         const int T = static_cast<int>(std::min<int64_t>(a->T - t0, kMaxRows));
-        const int N = columns_for(static_cast<int64_t>(T) * (pairs ? 2 : 1));
-        HiddenParams x{};
-        x.x = static_cast<const unsigned char*>(a->hidden) + t0 * a->ld_hidden * float_bytes(a->hidden_dtype);
-        x.ld = a->ld_hidden;
-        x.D = static_cast<int>(a->table.D);
-        x.kblocks = static_cast<int>(kblocks_of(a->table.D));
-        x.groups = static_cast<int>((a->table.D + a->table.group - 1) / a->table.group);
-        x.shift = table4_params(a->table).shift;
-        x.N = N;
-        x.per = pairs ? N / 2 : N;
-        x.few = N <= kFewRows;
-        x.out = h->ws;
-        x.sums = reinterpret_cast<float*>(h->ws + w.sums);
-        x.inverse = reinterpret_cast<float*>(h->ws + w.inverse);
-        switch (a->hidden_dtype) {
-        case LMLOSS_BF16: hidden_kernel<Bf16><<<T, 256, 0, stream>>>(x); break;
-        case LMLOSS_FP16: hidden_kernel<Fp16><<<T, 256, 0, stream>>>(x); break;
-        default: hidden_kernel<Fp32><<<T, 256, 0, stream>>>(x); break;
-        }
-        if ((st = vocab_launch_err()) != LMLOSS_OK) return st;
         LogitsParams p{};
         p.values = a->table.values;
         p.ld_values = a->table.ld_values;
@@ -576,22 +545,16 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.zeros = a->table.zeros;
         p.ld_zeros = a->table.ld_zeros;
         p.V = static_cast<int>(a->table.V);
-        p.D = x.D;
-        p.shift = x.shift;
+        p.D = static_cast<int>(a->table.D);
+        p.shift = table4_params(a->table).shift;
         p.scale_dtype = a->table.scale_dtype;
         p.scale_bytes = float_bytes(a->table.scale_dtype);
-        p.groups = x.groups;
-        p.kblocks = x.kblocks;
+        p.groups = static_cast<int>((a->table.D + a->table.group - 1) / a->table.group);
+        p.kblocks = static_cast<int>(kblocks_of(a->table.D));
         p.T = T;
-        p.N = N;
-        p.per = x.per;
-        p.tblocks = (T + x.per - 1) / x.per;
         p.vtiles = static_cast<int>((a->table.V + kTile - 1) / kTile);
         p.pairs = pairs;
-        p.x = x.out;
-        p.sums = x.sums;
-        p.inverse = x.inverse;
-        p.hidden = x.x;
+        p.hidden = static_cast<const unsigned char*>(a->hidden) + t0 * a->ld_hidden * float_bytes(a->hidden_dtype);
         p.ld_hidden = a->ld_hidden;
         p.hidden_dtype = a->hidden_dtype;
         p.out = static_cast<unsigned char*>(a->logits) + t0 * a->ld_logits * float_bytes(a->logits_dtype);
@@ -599,7 +562,32 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.out_dtype = a->logits_dtype;
         p.scale = a->scale;
         p.err = h->err;
-        st = x.few ? launch_few_rows(p, map, h, stream) : launch_many_rows(p, map, h, stream);
+        if (few_rows_fit(p)) {
+            st = launch_few_rows(p, maps, h, stream);
+        } else {
+            HiddenParams x{};
+            x.x = p.hidden;
+            x.ld = p.ld_hidden;
+            x.D = p.D;
+            x.kblocks = p.kblocks;
+            x.groups = p.groups;
+            x.shift = p.shift;
+            x.N = p.N = kMany;
+            x.per = p.per = pairs ? kMany / 2 : kMany;
+            x.out = h->ws;
+            x.sums = reinterpret_cast<float*>(h->ws + w.sums);
+            x.inverse = reinterpret_cast<float*>(h->ws + w.inverse);
+            p.tblocks = (T + p.per - 1) / p.per;
+            p.x = x.out;
+            p.sums = x.sums;
+            p.inverse = x.inverse;
+            switch (a->hidden_dtype) {
+            case LMLOSS_BF16: hidden_kernel<Bf16><<<T, 256, 0, stream>>>(x); break;
+            case LMLOSS_FP16: hidden_kernel<Fp16><<<T, 256, 0, stream>>>(x); break;
+            default: hidden_kernel<Fp32><<<T, 256, 0, stream>>>(x); break;
+            }
+            if ((st = vocab_launch_err()) == LMLOSS_OK) st = launch_many_rows(p, maps, h, stream);
+        }
         if (st != LMLOSS_OK) return st;
     }
     return LMLOSS_OK;

@@ -44,7 +44,7 @@ struct LogitsParams {
     int out_dtype;
     float scale;
     int qstages, xstages;
-    uint32_t stage_bytes;        // of a stage of the table: values, scales, zeros, sums (and hidden rows)
+    uint32_t stage_bytes;        // of a stage of the table
     int* err;
 };
 
@@ -74,6 +74,61 @@ __device__ __forceinline__ void store_logit(const LogitsParams& p, int64_t t, in
     if (p.out_dtype == LMLOSS_BF16) static_cast<uint16_t*>(p.out)[at] = Bf16::round(x);
     else if (p.out_dtype == LMLOSS_FP16) static_cast<uint16_t*>(p.out)[at] = Fp16::round(x);
     else static_cast<float*>(p.out)[at] = x;
+}
+
+// The power of two that brings a row's largest finite value to between 2^14 and 2^15, at most 2^126.  (A
+// subnormal's exponent counts as -127.)
+__device__ __forceinline__ float hidden_scale(float top)
+{
+    const int e = static_cast<int>(__float_as_uint(top) >> 23);
+    return top > 0.f ? __uint_as_float(static_cast<uint32_t>(min(14 + 254 - e, 253)) << 23) : 1.f;
+}
+// Eight columns of a hidden row from c on, scaled, as a 16-byte part: fp16 in the order 0 4 1 5 2 6 3 7, the places
+// 1 5 and 3 7 divided by 16.  lo: what fp32 leaves, times 2^11.  The sums are of what the parts stand for, in the
+// products' unit of 2^-24.  A scale of 0 is a row that is not finite.
+template <class X>
+__device__ __forceinline__ void hidden_part(const typename X::raw* x, int c, int D, float scale, uint4& hi, uint4& lo, float& sum, float& sum_lo)
+{
+    constexpr bool kPair = X::kBytes == 4;
+    float v[8];
+    if (c + 8 <= D && (reinterpret_cast<uintptr_t>(x + c) & 15u) == 0) {
+        Pack<X, 8> q;
+        q.load(x + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = q.get(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < D ? X::widen(x[c + i]) : 0.f;
+    }
+    uint32_t h[4], l[4] = {0, 0, 0, 0};
+    sum = sum_lo = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float by = i & 1 ? scale * 0.0625f : scale, back = i & 1 ? 0x1p-20f : 0x1p-24f;
+        const float a = scale > 0.f ? v[i] * by : 0.f, b = scale > 0.f ? v[i + 4] * by : 0.f;
+        const __half2 p = __floats2half2_rn(a, b);
+        h[i] = *reinterpret_cast<const uint32_t*>(&p);
+        const float2 f = __half22float2(p);
+        sum = fmaf(f.x, back, fmaf(f.y, back, sum));
+        if (kPair) {
+            const __half2 r = __floats2half2_rn((a - f.x) * 2048.f, (b - f.y) * 2048.f);
+            l[i] = *reinterpret_cast<const uint32_t*>(&r);
+            const float2 e = __half22float2(r);
+            sum_lo = fmaf(e.x, back, fmaf(e.y, back, sum_lo));
+        }
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// Sums over the `lanes` (4, 8 or 16) neighbouring threads of a group, 16 threads together.
+template <bool PAIR>
+__device__ __forceinline__ void group_sums(int lanes, float& sum, float& sum_lo)
+{
+    const uint32_t together = 0xffffu << (threadIdx.x & 16);
+    for (int o = 1; o < lanes; o <<= 1) {
+        sum += __shfl_xor_sync(together, sum, o);
+        if (PAIR) sum_lo += __shfl_xor_sync(together, sum_lo, o);
+    }
 }
 
 // One logit of a row with infinities or NaN, from the formula: operands that are all finite and sums taken
@@ -109,50 +164,40 @@ struct Ring {
 };
 
 // Where a stage's parts begin, and what they hold: values [256 rows][128 bytes, 16-byte parts at
-// (part ^ row % 8)], scales, zeros [groups of the stage][256 rows], sums [groups][N].
+// (part ^ row % 8)], scales and zeros [groups of the stage][256 rows], sums [groups][N] (where they are
+// copied by stages).
 struct StageLayout {
-    uint32_t scales, zeros, sums, x, bytes;
-    __host__ __device__ StageLayout(int shift, int scale_bytes, bool has_zeros, int N, uint32_t x_bytes)
+    uint32_t scales, zeros, sums, copied, bytes;   // copied: of values, scales and zeros
+    __host__ __device__ StageLayout(int shift, int scale_bytes, bool has_zeros, uint32_t sums_a_group)
     {
         const int n = kStageCols >> shift;
         scales = kTile * 128;
         zeros = scales + n * kTile * scale_bytes;
-        sums = zeros + (has_zeros ? n * kTile : 0);
-        x = sums + n * N * 4;
-        bytes = (x + x_bytes + 1023) / 1024 * 1024;
+        sums = copied = zeros + (has_zeros ? n * kTile : 0);
+        bytes = (sums + n * sums_a_group + 1023) / 1024 * 1024;
     }
 };
 
-// Copies of the table's part of stage `st` of the tile at row v0, by a whole warp; the barrier expects
-// stage_tx(...) bytes.
-__device__ __forceinline__ uint32_t stage_rows(int rows, int bytes)
+// A table's parts as tiles: [V, D / 2 bytes] by 256 x 128, [G, V] by a stage's groups x 256.  What lies
+// outside is 0.
+struct TableMaps {
+    CUtensorMap values, scales, zeros;
+};
+
+// Copies of stage `st` of the tile at row v0, `copied` bytes, by one thread.  (As bulk copies, one a group, scales
+// took longer than the values: 128256 x 4096, no arithmetic, 63 us with them and 46 without.)
+__device__ __forceinline__ void copy_table(const LogitsParams& p, const StageLayout& lay, const TableMaps& maps, int st, int v0, uint32_t to,
+                                           uint32_t bar)
 {
-    // to the end of the 16 bytes that hold the last row's
-    const int whole = 16 / bytes;
-    return static_cast<uint32_t>((min(rows, kTile) + whole - 1) / whole * whole);
-}
-__device__ __forceinline__ uint32_t stage_tx(const LogitsParams& p, int n, int v0)
-{
-    return kTile * 128 + n * (stage_rows(p.V - v0, p.scale_bytes) * p.scale_bytes + (p.zeros ? stage_rows(p.V - v0, 1) : 0u) + p.N * 4);
-}
-__device__ __forceinline__ void copy_table(const LogitsParams& p, const StageLayout& lay, const CUtensorMap& map, int st, int n, int v0,
-                                           uint32_t to, uint32_t bar)
-{
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) tile_load_2d(to, &map, st * 128, v0, bar);
-    if (lane < n) {
-        const int64_t g = static_cast<int64_t>(st) * (kStageCols >> p.shift) + lane;
-        bulk_load(to + lay.scales + lane * kTile * p.scale_bytes, p.scales + (g * p.ld_scales + v0) * p.scale_bytes,
-                  stage_rows(p.V - v0, p.scale_bytes) * p.scale_bytes, bar);
-        if (p.zeros) bulk_load(to + lay.zeros + lane * kTile, p.zeros + g * p.ld_zeros + v0, stage_rows(p.V - v0, 1), bar);
-    }
-}
-__device__ __forceinline__ void copy_sums(const LogitsParams& p, const StageLayout& lay, int st, int n, int tb, uint32_t to, uint32_t bar)
-{
-    // the groups of a stage lie side by side
-    bulk_load(to + lay.sums, p.sums + (static_cast<int64_t>(tb) * p.groups + st * (kStageCols >> p.shift)) * p.N, n * p.N * 4, bar);
+    const int g = st * (kStageCols >> p.shift);
+    tile_load_2d(to, &maps.values, st * 128, v0, bar);
+    tile_load_2d(to + lay.scales, &maps.scales, v0, g, bar);
+    if (p.zeros) tile_load_2d(to + lay.zeros, &maps.zeros, v0, g, bar);
 }
 
-lmloss_status launch_few_rows(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* h, cudaStream_t stream);
+// Whether the kernel of independent warps takes a call: up to kFewRows operand rows that fit into shared memory
+// beside two stages.
+bool few_rows_fit(const LogitsParams& p);
+lmloss_status launch_few_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream);
 
 }  // namespace lmloss

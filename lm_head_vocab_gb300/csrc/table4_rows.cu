@@ -6,6 +6,7 @@
 // operations widen a word, and a thread's group sums are scaled where they are.  For so few rows that is less
 // than tensor memory costs: there, what widens, multiplies and adds are different warps, and the barriers and
 // copies between them took more instructions than the numbers (128256 x 4096, one row: 90 us).
+// Each block lays the hidden rows out in its own shared memory, under the way of its first stages.
 #include <algorithm>
 
 #include "table4_logits.cuh"
@@ -14,12 +15,28 @@ namespace lmloss {
 namespace {
 
 constexpr int kSumWarps = 16;                // 32 rows of the tile each, and every second run of 128 columns
-constexpr int kRowsThreads = (kSumWarps + 1) * 32;
-constexpr uint32_t kHead = 1024;             // barriers, before the stages
+constexpr int kSumThreads = kSumWarps * 32;
+constexpr int kRowsThreads = kSumThreads + 32;
+constexpr uint32_t kHead = 1024;             // barriers and what is said of hidden rows, before the stages
 
-struct __align__(16) RowsBarriers {
+struct __align__(16) RowsHead {
     uint64_t full[kMaxStages], empty[kMaxStages];
+    uint32_t top[kFewRows];                  // bits of a hidden row's largest finite value
+    int odd[kFewRows];                       // whether it has others
     int failed;
+};
+static_assert(sizeof(RowsHead) <= kHead, "head");
+
+// Hidden rows [kblocks][N][256 bytes], 16-byte part i of a row at i ^ 4 (row % 2); sums [groups][N]; what warps
+// hand on [8][N][33].
+struct RowsLayout {
+    uint32_t sums, pads, bytes;
+    __host__ __device__ RowsLayout(int N, int kblocks, int groups)
+    {
+        sums = N * kblocks * 256;
+        pads = sums + groups * N * 4;
+        bytes = pads + 8 * N * 33 * 4;
+    }
 };
 
 // Four 8 x 16-byte matrices: lane l's address is row l % 8 of matrix l / 8; of each it gets word l % 4 of row l / 4.
@@ -32,23 +49,66 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
 }
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int NT, class S>
-__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ CUtensorMap map)
+// The hidden rows into shared memory, by the first kSumThreads threads.
+template <class X>
+__device__ __noinline__ void lay_out(const LogitsParams& p, RowsHead& head, unsigned char* x, float* sums, int N)
+{
+    constexpr bool kPair = X::kBytes == 4;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const typename X::raw* hidden = static_cast<const typename X::raw*>(p.hidden);
+    for (int r = 0; r < p.T; ++r) {
+        float top = 0.f;   // of what is finite
+        bool finite = true;
+        for (int c = tid; c < p.D; c += kSumThreads) {
+            const float a = fabsf(X::widen(hidden[r * p.ld_hidden + c]));
+            if (a < INFINITY) top = fmaxf(top, a);
+            else finite = false;
+        }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        finite = __all_sync(0xffffffffu, finite);
+        if (lane == 0) {
+            atomicMax(&head.top[r], most);
+            if (!finite) head.odd[r] = 1;
+        }
+    }
+    asm volatile("bar.sync 9, %0;" ::"n"(kSumThreads) : "memory");
+    const int parts = p.kblocks * 16, lanes = (1 << p.shift) / 8;
+    for (int i = tid; i < p.T * parts; i += kSumThreads) {
+        const int r = i / parts, u = i - r * parts;
+        uint4 hi, lo;
+        float sum, sum_lo;
+        hidden_part<X>(hidden + r * p.ld_hidden, 8 * u, p.D, head.odd[r] ? 0.f : hidden_scale(__uint_as_float(head.top[r])), hi, lo, sum, sum_lo);
+        auto place = [&](int n) { return reinterpret_cast<uint4*>(x + ((u >> 4) * N + n) * 256 + (((u & 15) ^ ((n & 1) << 2)) << 4)); };
+        *place(r) = hi;
+        if (kPair) *place(r + N / 2) = lo;
+        group_sums<kPair>(lanes, sum, sum_lo);
+        const int g = (8 * u) >> p.shift;
+        if ((u & (lanes - 1)) == 0 && g < p.groups) {
+            sums[g * N + r] = sum;
+            if (kPair) sums[g * N + r + N / 2] = sum_lo;
+        }
+    }
+    asm volatile("bar.sync 9, %0;" ::"n"(kSumThreads) : "memory");
+}
+
+template <int NT, int GROUP>
+__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
 {
     constexpr int N = 8 * NT;
+    constexpr int kPerStage = kStageCols / GROUP, kUnits = GROUP / 32;   // groups of a stage; runs of 32 columns of a group
     extern __shared__ __align__(1024) unsigned char smem[];
-    RowsBarriers& b = *reinterpret_cast<RowsBarriers*>(smem);
+    RowsHead& b = *reinterpret_cast<RowsHead*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const StageLayout lay(p.shift, S::kBytes, p.zeros != nullptr, N, 2 * N * 256);
-    float* const pads = reinterpret_cast<float*>(smem + kHead + p.qstages * p.stage_bytes);   // [8 warps][N][33]
-    const int per_stage = kStageCols >> p.shift, stages = (p.kblocks + 1) / 2;
-    const int tiles = p.vtiles * p.tblocks;
+    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, 0);
+    const RowsLayout rl(N, p.kblocks, p.groups);
+    unsigned char* const rows = smem + kHead + p.qstages * p.stage_bytes;
+    const int stages = (p.kblocks + 1) / 2;
 
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -58,107 +118,113 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         b.failed = 0;
         fence_mbar_init();
     }
+    if (tid < kFewRows) {
+        b.top[tid] = 0;
+        b.odd[tid] = 0;
+    }
     __syncthreads();
-    auto wait = [&](uint64_t& bar, uint32_t parity) {
+    auto wait_one = [&](uint64_t& bar, uint32_t parity) {
         if (!mbar_sleep_bounded(smem_addr(&bar), parity, kWaitLimitCycles, &b.failed)) set_error(p.err, kErrTimeout);
-        __syncwarp();
     };
 
     if (warp == kSumWarps) {
-        // ---- copies.  The table's first stages go out before the hidden rows are waited for.
-        Ring q;
-        const int64_t mine = static_cast<int64_t>((tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * stages;
-        const int64_t early = min(mine, static_cast<int64_t>(p.qstages));
-        auto copy = [&](int64_t i, int slot, bool table, bool rows) {
-            const int tile = static_cast<int>(blockIdx.x + i / stages * gridDim.x), st = static_cast<int>(i % stages);
-            const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
-            const int n = min(per_stage, p.groups - st * per_stage), blocks = min(2, p.kblocks - 2 * st);
-            const uint32_t to = base + kHead + slot * p.stage_bytes, bar = smem_addr(&b.full[slot]);
-            if (table) {
-                if (lane == 0) mbar_arrive_expect_tx(bar, stage_tx(p, n, vt * kTile) + blocks * N * 256);
-                __syncwarp();
-                copy_table(p, lay, map, st, n, vt * kTile, to, bar);
-            }
-            if (rows && lane == 0) {
-                copy_sums(p, lay, st, n, tb, to, bar);
-                bulk_load(to + lay.x, p.x + (static_cast<int64_t>(tb) * p.kblocks + 2 * st) * (N * 256), blocks * N * 256, bar);
-            }
-        };
-        for (int64_t i = 0; i < early; ++i) copy(i, static_cast<int>(i), true, false);
-        grid_dep_wait();
-        for (int64_t i = 0; i < early; ++i) copy(i, static_cast<int>(i), false, true);
-        for (int64_t i = 0; i < mine; ++i, q.next(p.qstages)) {
-            if (i < early) continue;
-            wait(b.empty[q.slot], q.parity ^ 1u);
-            copy(i, q.slot, true, true);
+        // ---- copies
+        if (lane == 0) {
+            Ring q;
+            for (int tile = blockIdx.x; tile < p.vtiles; tile += gridDim.x)
+                for (int st = 0; st < stages; ++st) {
+                    wait_one(b.empty[q.slot], q.parity ^ 1u);
+                    const uint32_t bar = smem_addr(&b.full[q.slot]);
+                    mbar_arrive_expect_tx(bar, lay.copied);
+                    copy_table(p, lay, maps, st, tile * kTile, base + kHead + q.slot * p.stage_bytes, bar);
+                    q.next(p.qstages);
+                }
         }
+        __syncwarp();
     } else {
+        float* const all_sums = reinterpret_cast<float*>(rows + rl.sums);
+        if (p.hidden_dtype == LMLOSS_BF16) lay_out<Bf16>(p, b, rows, all_sums, N);
+        else if (p.hidden_dtype == LMLOSS_FP16) lay_out<Fp16>(p, b, rows, all_sums, N);
+        else lay_out<Fp32>(p, b, rows, all_sums, N);
         const int half = warp >> 3, pair = warp & 7, g8 = lane >> 2, i4 = lane & 3;
         const int r0 = pair * 32;
-        float* const pad = pads + pair * (N * 33);
+        float* const pad = reinterpret_cast<float*>(rows + rl.pads) + pair * (N * 33);
         // of the matrices that ldmatrix takes: rows 0-7 and 8-15 of one part, then of the next
-        const int row_in = r0 + ((lane >> 3) & 1) * 8 + (lane & 7), part_in = lane >> 4;
+        const uint32_t words = base + kHead + (r0 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
+        uint32_t part_at[2];
+#pragma unroll
+        for (int u2 = 0; u2 < 2; ++u2) part_at[u2] = ((half * 4 + u2 * 2 + (lane >> 4)) ^ (lane & 7)) << 4;
+        // part 4 unit + i4 of a hidden row lies at 4 (unit ^ row % 2) + i4
+        const int odd = (g8 & 1) * 64;
+        const unsigned char* const x_even = rows + g8 * 256 + i4 * 16 + odd;
+        const unsigned char* const x_odd = x_even - 2 * odd;
         Ring q;
-        bool waited = false;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
+        for (int tile = blockIdx.x; tile < p.vtiles; tile += gridDim.x) {
             float acc[2][NT][4] = {};
             for (int st = 0; st < stages; ++st) {
-                wait(b.full[q.slot], q.parity);
-                if (2 * st + half < p.kblocks) {
-                    const unsigned char* const stage = smem + kHead + q.slot * p.stage_bytes;
-                    const uint32_t values = base + kHead + q.slot * p.stage_bytes;
-                    float d[2][NT][4] = {};
+                wait_one(b.full[q.slot], q.parity);
+                __syncwarp();
+                const int kb = 2 * st + half;
+                if (kb < p.kblocks) {
+                    const uint32_t offset = q.slot * p.stage_bytes;
+                    const unsigned char* const stage = smem + kHead + offset;
+                    uint32_t w[2][2][4];
 #pragma unroll
-                    for (int u2 = 0; u2 < 2; ++u2) {
-                        uint32_t w[2][4];
+                    for (int u2 = 0; u2 < 2; ++u2)
 #pragma unroll
-                        for (int mt = 0; mt < 2; ++mt)
-                            ldmatrix4(w[mt], values + (row_in + mt * 16) * 128 + (((half * 4 + u2 * 2 + part_in) ^ (lane & 7)) << 4));
+                        for (int mt = 0; mt < 2; ++mt) ldmatrix4(w[u2][mt], words + offset + mt * 16 * 128 + part_at[u2]);
+                    const int x_at = kb * (N * 256);
+                    const int g0 = half * (kPerStage / 2);   // the half's first group in the stage
+                    float d[2][NT][4];
 #pragma unroll
-                        for (int u1 = 0; u1 < 2; ++u1) {
-                            const int unit = u2 * 2 + u1;   // 32 columns
-                            uint32_t a[2][2][4];
+                    for (int unit = 0; unit < 4; ++unit) {   // 32 columns
+                        if (unit % kUnits == 0) {
+#pragma unroll
+                            for (int i = 0; i < 2 * NT * 4; ++i) d[i / (NT * 4)][i / 4 % NT][i % 4] = 0.f;
+                        }
+                        uint32_t a[2][2][4];
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            widen_word(w[unit >> 1][mt][2 * (unit & 1)], a[mt][0]);
+                            widen_word(w[unit >> 1][mt][2 * (unit & 1) + 1], a[mt][1]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 x = *reinterpret_cast<const uint4*>((unit & 1 ? x_odd : x_even) + x_at + nt * 8 * 256 + unit * 64);
 #pragma unroll
                             for (int mt = 0; mt < 2; ++mt) {
-                                widen_word(w[mt][2 * u1], a[mt][0]);
-                                widen_word(w[mt][2 * u1 + 1], a[mt][1]);
+                                mma_m16n8k16(d[mt][nt], a[mt][0][0], a[mt][1][0], a[mt][0][1], a[mt][1][1], x.x, x.y);
+                                mma_m16n8k16(d[mt][nt], a[mt][0][2], a[mt][1][2], a[mt][0][3], a[mt][1][3], x.z, x.w);
                             }
+                        }
+                        // ---- a group's end: its sums, less the zero points', scaled
+                        const int gl = g0 + unit / kUnits;
+                        if ((unit + 1) % kUnits == 0 && st * kPerStage + gl < p.groups) {
+                            const int at = gl * kTile + r0 + g8;
+                            float s[4], z[4];   // rows g8, + 8, + 16, + 24
+                            if (p.scale_dtype == LMLOSS_FP16) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) s[k] = Fp16::widen(reinterpret_cast<const uint16_t*>(stage + lay.scales)[at + 8 * k]);
+                            } else if (p.scale_dtype == LMLOSS_BF16) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) s[k] = Bf16::widen(reinterpret_cast<const uint16_t*>(stage + lay.scales)[at + 8 * k]);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) s[k] = reinterpret_cast<const float*>(stage + lay.scales)[at + 8 * k];
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) z[k] = p.zeros ? -static_cast<float>((stage + lay.zeros)[at + 8 * k]) : -8.f;
+                            const float* const sums = all_sums + (st * kPerStage + gl) * N + 2 * i4;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(stage + lay.x + (half * N + nt * 8 + g8) * 256 +
-                                                                                (((unit * 4 + i4) ^ ((g8 & 1) << 2)) << 4));
+                                const float2 x = *reinterpret_cast<const float2*>(sums + nt * 8);
 #pragma unroll
-                                for (int mt = 0; mt < 2; ++mt) {
-                                    mma_m16n8k16(d[mt][nt], a[mt][0][0], a[mt][1][0], a[mt][0][1], a[mt][1][1], x.x, x.y);
-                                    mma_m16n8k16(d[mt][nt], a[mt][0][2], a[mt][1][2], a[mt][0][3], a[mt][1][3], x.z, x.w);
-                                }
-                            }
-                            // ---- a group's end: its sums, less the zero points', scaled
-                            const int columns = (half * 4 + unit + 1) * 32, gl = (columns - 1) >> p.shift;
-                            if ((columns & ((1 << p.shift) - 1)) == 0 && st * per_stage + gl < p.groups) {
-                                const float* const sums = reinterpret_cast<const float*>(stage + lay.sums) + gl * N;
-                                const typename S::raw* const scales = reinterpret_cast<const typename S::raw*>(stage + lay.scales) + gl * kTile + r0 + g8;
-                                const unsigned char* const zeros = stage + lay.zeros + gl * kTile + r0 + g8;
-                                float s[4], sz[4];   // rows g8, + 8, + 16, + 24
+                                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    s[k] = S::widen(scales[8 * k]);
-                                    sz[k] = p.zeros ? -static_cast<float>(zeros[8 * k]) : -8.f;
-                                }
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    const float2 x = *reinterpret_cast<const float2*>(sums + nt * 8 + 2 * i4);
-#pragma unroll
-                                    for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-                                        for (int k = 0; k < 4; ++k) {
-                                            const int r = 2 * mt + (k >> 1);
-                                            acc[mt][nt][k] = fmaf(s[r], fmaf(sz[r], k & 1 ? x.y : x.x, d[mt][nt][k]), acc[mt][nt][k]);
-                                            d[mt][nt][k] = 0.f;
-                                        }
+                                    for (int k = 0; k < 4; ++k) {
+                                        const int r = 2 * mt + (k >> 1);
+                                        acc[mt][nt][k] = fmaf(s[r], fmaf(z[r], k & 1 ? x.y : x.x, d[mt][nt][k]), acc[mt][nt][k]);
                                     }
-                                }
                             }
                         }
                     }
@@ -171,35 +237,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             auto at = [&](int mt, int nt, int k) -> float& { return pad[(nt * 8 + 2 * i4 + (k & 1)) * 33 + mt * 16 + (k >> 1) * 8 + g8]; };
             if (half == 1) {
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) at(mt, nt, k) = acc[mt][nt][k];
+                for (int i = 0; i < 2 * NT * 4; ++i) at(i / (NT * 4), i / 4 % NT, i % 4) = acc[i / (NT * 4)][i / 4 % NT][i % 4];
             }
             asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
             if (half == 0) {
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) at(mt, nt, k) += acc[mt][nt][k];
+                for (int i = 0; i < 2 * NT * 4; ++i) at(i / (NT * 4), i / 4 % NT, i % 4) += acc[i / (NT * 4)][i / 4 % NT][i % 4];
             }
             asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
-            if (!waited) {
-                grid_dep_wait();
-                waited = true;
-            }
-            const int64_t v = static_cast<int64_t>(vt) * kTile + r0 + lane;
+            const int64_t v = static_cast<int64_t>(tile) * kTile + r0 + lane;
             if (v < p.V) {
-                const int t0 = tb * p.per, rows = min(p.per, p.T - t0);
-                for (int n = half; n < rows; n += 2) {
-                    const float inverse = p.inverse[t0 + n];
+                for (int n = half; n < p.T; n += 2) {
                     float x = pad[n * 33 + lane];
                     if (p.pairs) x = fmaf(pad[(n + N / 2) * 33 + lane], 1.f / 2048.f, x);
-                    if (inverse == inverse) store_logit(p, t0 + n, v, x * 0x1p24f * inverse * p.scale);
-                    else store_plain(p, t0 + n, v);
+                    if (b.odd[n]) store_plain(p, n, v);
+                    else store_logit(p, n, v, x * 0x1p24f / hidden_scale(__uint_as_float(b.top[n])) * p.scale);
                 }
             }
             asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");   // before the next tile's
@@ -215,16 +267,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     __syncthreads();
 }
 
-template <int NT, class S>
-lmloss_status launch(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* h, cudaStream_t stream)
+int columns_for(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
+
+template <int NT, int GROUP>
+lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    constexpr int N = 8 * NT;
-    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N, 2 * N * 256);
-    const uint32_t pads = 8 * N * 33 * 4;
+    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, 0);
+    const RowsLayout rl(8 * NT, p.kblocks, p.groups);
     p.stage_bytes = lay.bytes;
-    p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHead - pads) / lay.bytes);
-    auto* fn = rows_kernel<NT, S>;
-    const uint32_t bit = 1u << (8 + 3 * (NT == 1 ? 0 : (NT == 2 ? 1 : 2)) + S::kIndex);
+    p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHead - rl.bytes) / lay.bytes);
+    auto* fn = rows_kernel<NT, GROUP>;
+    const uint32_t bit = 1u << (8 + 3 * (NT == 1 ? 0 : (NT == 2 ? 1 : 2)) + (GROUP == 32 ? 0 : (GROUP == 64 ? 1 : 2)));
     if (!(h->limits_raised & bit)) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
             cudaGetLastError();
@@ -232,38 +285,35 @@ lmloss_status launch(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* 
         }
         h->limits_raised |= bit;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.vtiles) * p.tblocks, h->num_sms)));
-    cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = kHead + p.qstages * lay.bytes + pads;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fn, p, map) != cudaSuccess) {
-        cudaGetLastError();
-        return LMLOSS_ERR_CUDA;
-    }
-    return LMLOSS_OK;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.vtiles, h->num_sms));
+    fn<<<grid, kRowsThreads, kHead + p.qstages * lay.bytes + rl.bytes, stream>>>(p, maps);
+    return vocab_launch_err();
 }
 
 template <int NT>
-lmloss_status launch(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* h, cudaStream_t stream)
+lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    if (p.scale_dtype == LMLOSS_BF16) return launch<NT, Bf16>(p, map, h, stream);
-    if (p.scale_dtype == LMLOSS_FP16) return launch<NT, Fp16>(p, map, h, stream);
-    return launch<NT, Fp32>(p, map, h, stream);
+    if (p.shift == 5) return launch<NT, 32>(p, maps, h, stream);
+    if (p.shift == 6) return launch<NT, 64>(p, maps, h, stream);
+    return launch<NT, 128>(p, maps, h, stream);
 }
 
 }  // namespace
 
-lmloss_status launch_few_rows(LogitsParams& p, const CUtensorMap& map, lmloss_vocab_ctx* h, cudaStream_t stream)
+bool few_rows_fit(const LogitsParams& p)
 {
-    if (p.N == 8) return launch<1>(p, map, h, stream);
-    if (p.N == 16) return launch<2>(p, map, h, stream);
-    return launch<4>(p, map, h, stream);
+    const int64_t rows = static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1), N = columns_for(rows);
+    if (rows > kFewRows || N * p.kblocks * 256 > kMaxShared) return false;
+    return kHead + RowsLayout(static_cast<int>(N), p.kblocks, p.groups).bytes +
+               2 * StageLayout(p.shift, p.scale_bytes, p.zeros != nullptr, 0).bytes <= kMaxShared;
+}
+
+lmloss_status launch_few_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
+{
+    p.N = columns_for(static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1));
+    if (p.N == 8) return launch<1>(p, maps, h, stream);
+    if (p.N == 16) return launch<2>(p, maps, h, stream);
+    return launch<4>(p, maps, h, stream);
 }
 
 }  // namespace lmloss
