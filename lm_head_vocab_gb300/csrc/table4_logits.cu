@@ -24,10 +24,10 @@ namespace lmloss {
 namespace {
 
 constexpr int kMaxRows = 1024;               // hidden rows a launch
-constexpr int kMany = 64;                    // operand rows of a block's product here
+constexpr int kMany = 64;                    // operand rows of a block's product at most
 constexpr int kWarpsOf = 28;                 // 16 warps widen, 8 add, then: table, hidden rows, a half's products each
 constexpr int kLogitsThreads = kWarpsOf * 32;
-constexpr uint32_t kHeader = 1024;           // barriers, before the stages
+constexpr uint32_t kHeader = 5120;           // barriers and factors, before the stages
 // Registers a thread of each part where 64 sums a thread do not fit an even share (72 of 896 threads):
 // in all what the block was launched with.
 constexpr int kWidenRegs = 64, kAddRegs = 104, kFewRegs = 40;
@@ -98,18 +98,21 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
 }
 
 // ------------------------------------------------------------------- main
+// A block's head: barriers, and the factors of all hidden rows.
 struct __align__(16) LogitsBarriers {
     uint64_t q_full[kMaxStages], q_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages];
-    uint64_t a_full[2][2], a_empty[2][2], d_full[2][2], d_empty[2][2];
+    uint64_t a_full[2][2], a_empty[2][2], d_full[2][4], d_empty[2][4];
     uint32_t tmem;
     int failed;
+    float factor[kMaxRows];      // NaN: the row is not finite
 };
+static_assert(sizeof(LogitsBarriers) <= kHeader, "head");
 
 template <int N>
 __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
 {
     // tensor memory: A two buffers of 64 columns for each half, D kSums of N columns for each half
-    constexpr int kSums = 2;
+    constexpr int kSums = N == 64 ? 2 : 4;
     constexpr uint32_t kColumns = 512;
     static_assert(256 + 2 * kSums * N <= kColumns, "tensor memory");
     constexpr uint32_t kIdesc = mma_f16_idesc(N);
@@ -132,9 +135,11 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
             mbar_init(smem_addr(&b.x_empty[i]), 2);
         }
         for (int h = 0; h < 2; ++h)
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_addr(&b.a_full[h][i]), 4);
-                mbar_init(smem_addr(&b.a_empty[h][i]), 1);
+            for (int i = 0; i < 4; ++i) {
+                if (i < 2) {
+                    mbar_init(smem_addr(&b.a_full[h][i]), 4);
+                    mbar_init(smem_addr(&b.a_empty[h][i]), 1);
+                }
                 mbar_init(smem_addr(&b.d_full[h][i]), 1);
                 mbar_init(smem_addr(&b.d_empty[h][i]), 4);
             }
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
 
     if (warp < 16) {
         // ---- widen: a thread a row of its half, every second block of columns
-        reg_dealloc<kWidenRegs>();
+        if (N == 64) reg_dealloc<kWidenRegs>();
         const int group = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = tid & 255;
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128 + group * 64;
         Ring q;
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
         wait(b.a_empty[half][group], parity);   // the products have read it: nothing arrives after the block's end
     } else if (warp < 24) {
         // ---- add the groups' sums
-        reg_alloc<kAddRegs>();
+        if (N == 64) reg_alloc<kAddRegs>();
         const int half = (warp >> 2) & 1, quarter = warp & 3, row = tid & 255;
         const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 + half * (kSums * N);
         Ring q, d;
@@ -248,39 +253,53 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
             }
             if (!waited) {
                 grid_dep_wait();
+                // each warp for itself
+                for (int t = lane; t < p.T; t += 32) b.factor[t] = p.inverse[t] * 0x1p12f;
+                __syncwarp();
                 waited = true;
             }
             const int64_t v = static_cast<int64_t>(vt) * kTile + row;
             if (v < p.V) {
                 const int t0 = tb * p.per;
-                auto put = [&](int i, float x) {
-                    if (t0 + i >= p.T) return;
-                    const float inverse = p.inverse[t0 + i];
-                    if (inverse == inverse) store_logit(p, t0 + i, v, x * 0x1p24f * inverse * p.scale);
-                    else store_plain(p, t0 + i, v);
-                };
-                if (p.pairs) {
+                const int rows = min(p.per, p.T - t0);
+                auto all = [&](auto type) {
+                    using O = decltype(type);
+                    typename O::raw* out = static_cast<typename O::raw*>(p.out) + static_cast<int64_t>(t0) * p.ld_out + v;
+                    auto put = [&](int i, float x) {
+                        if (i < rows) *out = static_cast<typename O::raw>(O::round(x * 0x1p12f * b.factor[t0 + i] * p.scale));
+                        out += p.ld_out;
+                    };
 #pragma unroll
                     for (int i = 0; i < N / 4; ++i) {
                         float a, c, e, f;
                         f2_unpack(acc[i], a, c);
-                        f2_unpack(acc[i + N / 4], e, f);
-                        put(2 * i, fmaf(e, 1.f / 2048.f, a));
-                        put(2 * i + 1, fmaf(f, 1.f / 2048.f, c));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N / 2; ++i) {
-                        float a, c;
-                        f2_unpack(acc[i], a, c);
+                        if (p.pairs) {
+                            f2_unpack(acc[i + N / 4], e, f);
+                            a = fmaf(e, 1.f / 2048.f, a);
+                            c = fmaf(f, 1.f / 2048.f, c);
+                        }
                         put(2 * i, a);
                         put(2 * i + 1, c);
                     }
-                }
+                    if (!p.pairs) {
+#pragma unroll
+                        for (int i = N / 4; i < N / 2; ++i) {
+                            float a, c;
+                            f2_unpack(acc[i], a, c);
+                            put(2 * i, a);
+                            put(2 * i + 1, c);
+                        }
+                    }
+                };
+                if (p.out_dtype == LMLOSS_BF16) all(Bf16{});
+                else if (p.out_dtype == LMLOSS_FP16) all(Fp16{});
+                else all(Fp32{});
+                for (int i = 0; i < rows; ++i)
+                    if (b.factor[t0 + i] != b.factor[t0 + i]) store_plain(p, t0 + i, v);
             }
         }
     } else {
-        reg_dealloc<kFewRegs>();
+        if (N == 64) reg_dealloc<kFewRegs>();
         if (warp == 24) {
             // ---- the table.  Its first stages go out before the hidden rows' sums are waited for.
             if (lane == 0) {
@@ -470,14 +489,14 @@ bool table_maps(const lmloss_table4& t, TableMaps* maps)
            (!t.zeros || map(&maps->zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.zeros, t.V, G, t.ld_zeros, kTile, n, CU_TENSOR_MAP_SWIZZLE_NONE));
 }
 
+template <int N>
 lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    constexpr int N = kMany;
     const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
     p.stage_bytes = lay.bytes;
-    p.xstages = 4;
+    p.xstages = N == 64 ? 4 : 6;
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHeader - p.xstages * N * 256) / lay.bytes);
-    constexpr uint32_t bit = 1u << 17;
+    constexpr uint32_t bit = 1u << (N == 16 ? 17 : (N == 32 ? 18 : 19));
     if (!(h->limits_raised & bit)) {
         if (cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
             cudaGetLastError();
@@ -572,8 +591,9 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
             x.kblocks = p.kblocks;
             x.groups = p.groups;
             x.shift = p.shift;
-            x.N = p.N = kMany;
-            x.per = p.per = pairs ? kMany / 2 : kMany;
+            const int operands = T * (pairs ? 2 : 1);
+            x.N = p.N = operands <= 16 ? 16 : (operands <= 32 ? 32 : kMany);
+            x.per = p.per = pairs ? p.N / 2 : p.N;
             x.out = h->ws;
             x.sums = reinterpret_cast<float*>(h->ws + w.sums);
             x.inverse = reinterpret_cast<float*>(h->ws + w.inverse);
@@ -586,7 +606,9 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
             case LMLOSS_FP16: hidden_kernel<Fp16><<<T, 256, 0, stream>>>(x); break;
             default: hidden_kernel<Fp32><<<T, 256, 0, stream>>>(x); break;
             }
-            if ((st = vocab_launch_err()) == LMLOSS_OK) st = launch_many_rows(p, maps, h, stream);
+            if ((st = vocab_launch_err()) == LMLOSS_OK)
+                st = p.N == 16 ? launch_many_rows<16>(p, maps, h, stream)
+                               : (p.N == 32 ? launch_many_rows<32>(p, maps, h, stream) : launch_many_rows<kMany>(p, maps, h, stream));
         }
         if (st != LMLOSS_OK) return st;
     }

@@ -14,7 +14,7 @@ constexpr int kStageCols = 256;              // columns of the table a stage hol
 constexpr int kBlockCols = 128;              // columns that hidden rows are laid out by
 constexpr int kMaxStages = 8;
 constexpr uint32_t kMaxShared = 227 * 1024;
-constexpr int kFewRows = 32;                 // operand rows up to which warps multiply on their own
+constexpr int kFewRows = 8;                 // operand rows up to which warps multiply on their own
 
 struct LogitsParams {
     const uint8_t* values;
