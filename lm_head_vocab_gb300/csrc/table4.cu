@@ -28,98 +28,193 @@ lmloss_status table4_check(const lmloss_table4& t, bool pointers)
 
 namespace {
 
+// Rows and their vectors over threads without divisions: a block is `across` vectors (a power of two) of
+// 256 / across rows, kDeep times down.
+constexpr int kDeep = 4;
+
+struct Spread {
+    int log_across;
+    int blocks_across;           // blocks along a row
+    int64_t blocks_down;
+    Spread(int64_t vectors, int64_t rows)
+    {
+        log_across = 4;          // a group's threads are neighbours
+        while (log_across < 8 && (int64_t(1) << log_across) < vectors) ++log_across;
+        blocks_across = static_cast<int>((vectors + (int64_t(1) << log_across) - 1) >> log_across);
+        const int64_t down = kDeep << (8 - log_across);
+        blocks_down = (rows + down - 1) / down;
+    }
+};
+
+// max and min that keep a NaN
+__device__ __forceinline__ float keep_max(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float keep_min(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------- quantize
 struct QuantizeParams {
     Table4 t;
     const void* weight;
+    const unsigned char* weight_end;
     int64_t ld;
-    int64_t chunks;              // runs of 8 columns of a row, to whole groups
-    int64_t total;               // of all rows
+    int64_t rows;
+    int log_across, blocks_across;
     int* err;
 };
 
-// A thread takes 8 columns; a group's 4, 8 or 16 neighbouring threads share its extremes.
-template <class W, class S>
+// The whole number nearest to a quotient, halves to the even one, from q = a r + 1.5 2^23 rounded (r = 1 / s), which
+// may be one off next to a half.  The remainder a - q s is exact in fp32 there: a multiple of half a step of s,
+// and at most about s / 2.
+__device__ __forceinline__ float settle(float q, float a, float s)
+{
+    const float rest = fmaf(-q, s, a), half = 0.5f * s;
+    const bool odd = __float_as_uint(q + 12582912.f) & 1u;
+    if (fabsf(rest) > half || (fabsf(rest) == half && odd)) q += rest > 0.f ? 1.f : -1.f;
+    return q;
+}
+
+// A thread takes 8 columns; a group's 4, 8 or 16 neighbouring threads share its extremes.  Quotients come from
+// one reciprocal, and are settled where one of the eight lies within 2^-20 of a half: often, with bf16 weights, whose
+// largest is a multiple of seven in one group of seven.  (With IEEE quotients, and halves settled in fp64, 128256 x 4096
+// took 1.7 ms.)
+template <class W, class S, bool ZEROS>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantizeParams p)
 {
     const Table4& t = p.t;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const bool in = i < p.total;
-    const int64_t v = in ? i / p.chunks : 0;
-    const int c = static_cast<int>(in ? i - v * p.chunks : 0) * 8;
-    const int lanes = (1 << t.shift) / 8;
-    float x[8];
-    const typename W::raw* w = static_cast<const typename W::raw*>(p.weight) + v * p.ld + c;
-    if (in && c + 8 <= t.D && (reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
-        Pack<W, 8> q;
-        q.load(w);
+    const int64_t down = blockIdx.x / static_cast<unsigned>(p.blocks_across);
+    const int along = static_cast<int>(blockIdx.x - static_cast<unsigned>(down) * static_cast<unsigned>(p.blocks_across));
+    const int c = ((along << p.log_across) + (threadIdx.x & ((1 << p.log_across) - 1))) * 8;
+    const int rows_a_pass = 256 >> p.log_across;
+    const int64_t v0 = down * (kDeep * rows_a_pass) + (threadIdx.x >> p.log_across);
+    const int lanes = (1 << t.shift) / 8, g = c >> t.shift;
+    const unsigned char* const base = static_cast<const unsigned char*>(p.weight);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(p.ld * W::kBytes)) & 15u) == 0;
+
+    Pack<W, 8> in[kDeep];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = q.get(k);
-    } else {
+    for (int k = 0; k < kDeep; ++k) {
+        const int64_t v = v0 + k * rows_a_pass;
+        in[k].zero();
+        if (v >= p.rows || c >= t.D) continue;
+        const unsigned char* at = base + (v * p.ld + c) * W::kBytes;
+        if (aligned && c + 8 <= t.D) {
+            in[k].load(at);
+        } else if (inside_blocks<W, 8>(at, base, p.weight_end) && c + 8 <= t.D) {
+            constexpr int kVecs = 8 * W::kBytes / 16 + 1;
+            const uint4* a = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(15));
+            uint4 x[kVecs];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = in && c + k < t.D ? W::widen(w[k]) : 0.f;
-    }
-    // extremes; NaN and infinities show up in `sum`
-    float lo = 0.f, hi = 0.f, sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        lo = fminf(lo, x[k]);
-        hi = fmaxf(hi, x[k]);
-        sum += x[k] * 0.f;
-    }
-    for (int o = 1; o < lanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    const float ideal = t.zeros ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(fmaxf(hi, -lo), 7.f);
-    const typename S::raw sr = static_cast<typename S::raw>(S::round(ideal));
-    float s = S::widen(sr);
-    const bool bad = !(sum == 0.f) || !(s < INFINITY);
-    float z = 0.f;
-    if (bad || s == 0.f) {
-        // all weights count as 0
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = 0.f;
-    } else {
-        // nearest whole numbers of exact quotients: q = rint(x / s) may be one off where the quotient is within a
-        // rounding of a half; the remainder x - q s says so
-        auto nearest = [&](float a) {
-            float q = rintf(__fdiv_rn(a, s));
-            if (fabsf(q) < 64.f) {
-                const double r = fma(-static_cast<double>(q), static_cast<double>(s), static_cast<double>(a)), half = 0.5 * static_cast<double>(s);
-                const bool odd = fmodf(q, 2.f) != 0.f;
-                if (r > half || (r == half && odd)) q += 1.f;
-                else if (r < -half || (r == -half && odd)) q -= 1.f;
-            }
-            return q;
-        };
-        if (t.zeros) {
-            z = fminf(fmaxf(nearest(-lo), 0.f), 15.f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = fminf(fmaxf(nearest(x[k]) + z, 0.f), 15.f) - z;
+            for (int i = 0; i < kVecs; ++i) x[i] = __ldg(a + i);
+            shift_blocks<W, 8>(in[k], x, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)));
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = fminf(fmaxf(nearest(x[k]), -8.f), 7.f);
+            for (int i = 0; i < 8; ++i)
+                if (c + i < t.D) in[k].set(i, W::widen(reinterpret_cast<const typename W::raw*>(at)[i]));
         }
     }
-    if (!in) return;
-    const float zero = t.zeros ? z : 8.f;
-    uint32_t word = 0;
+    float lo[kDeep], hi[kDeep];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (c + k < t.D) word |= static_cast<uint32_t>(x[k] + zero) << (4 * k);
-    uint8_t* out = t.values + v * t.ld_values + c / 2;
-    if (c + 8 <= t.D) {
-        *reinterpret_cast<uint32_t*>(out) = word;
-    } else {
-        for (int k = 0; c + 2 * k < t.D; ++k) out[k] = static_cast<uint8_t>(word >> (8 * k));
+    for (int k = 0; k < kDeep; ++k) {
+        lo[k] = hi[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = in[k].get(i);
+            if (ZEROS) {
+                lo[k] = keep_min(lo[k], x);
+                hi[k] = keep_max(hi[k], x);
+            } else {
+                hi[k] = keep_max(hi[k], fabsf(x));
+            }
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+            hi[k] = keep_max(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
+            if (ZEROS) lo[k] = keep_min(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
+        }
     }
-    if ((c & ((1 << t.shift) - 1)) == 0) {
-        const int g = c >> t.shift;
-        static_cast<typename S::raw*>(t.scales)[g * t.ld_scales + v] = bad ? static_cast<typename S::raw>(S::round(NAN)) : sr;
-        if (t.zeros) t.zeros[g * t.ld_zeros + v] = static_cast<uint8_t>(z);
-        if (bad) set_error(p.err, kErrRange);
+    // scales and their reciprocals: of four neighbouring threads each divides for one of the rows
+    static_assert(kDeep == 4, "a quad's threads");
+    const int quad = threadIdx.x & 3;
+    const float range0 = ZEROS ? hi[0] - lo[0] : hi[0], range1 = ZEROS ? hi[1] - lo[1] : hi[1];
+    const float range2 = ZEROS ? hi[2] - lo[2] : hi[2], range3 = ZEROS ? hi[3] - lo[3] : hi[3];
+    const float range = quad & 2 ? (quad & 1 ? range3 : range2) : (quad & 1 ? range1 : range0);
+    const float own = S::widen(static_cast<typename S::raw>(S::round(__fdiv_rn(range, ZEROS ? 15.f : 7.f))));
+    // (a scale whose reciprocal passes fp32's range is brought up, with its weights)
+    const float own_r = __fdiv_rn(1.f, own < 0x1p-100f ? own * 0x1p100f : own);
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+        const int64_t v = v0 + k * rows_a_pass;
+        const float s = __shfl_sync(0xffffffffu, own, (threadIdx.x & 28) + k), r = __shfl_sync(0xffffffffu, own_r, (threadIdx.x & 28) + k);
+        // not finite: a weight, or the scale in its type.  (hi - lo may pass fp32's range too.)
+        const bool bad = !(s < INFINITY) || !(hi[k] < INFINITY) || (ZEROS && !(lo[k] > -INFINITY));
+        if (v >= p.rows || c >= t.D) continue;
+        float z = ZEROS ? 0.f : 8.f, x[8];
+        if (bad || s == 0.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.f;
+        } else {
+            float su = s;
+            if (s < 0x1p-100f && W::kIndex != Fp16::kIndex) {
+                float a[8];
+                su = s * 0x1p100f;
+                lo[k] *= 0x1p100f;
+                hi[k] *= 0x1p100f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] = in[k].get(i) * 0x1p100f;
+                in[k].set_all(a);
+            }
+            constexpr float kMagic = 12582912.f;
+            float most = 0.f, least = -8.f, largest = 7.f;
+            if (ZEROS) {
+                z = fmaf(-lo[k], r, kMagic) - kMagic;
+                most = fabsf(fmaf(-z, su, -lo[k]));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = in[k].get(i);
+                x[i] = fmaf(a, r, kMagic) - kMagic;
+                most = fmaxf(most, fabsf(fmaf(-x[i], su, a)));
+            }
+            // (next to a half, or with a scale that lost bits in its type's subnormals)
+            const bool settle_all = !(most < su * 0.4999995f);
+            if (settle_all || !((ZEROS ? hi[k] - lo[k] : hi[k]) < su * (ZEROS ? 15.2f : 7.4f))) {
+                if (ZEROS) {
+                    z = fminf(fmaxf(settle(z, -lo[k], su), 0.f), 15.f);
+                    least = -z;
+                    largest = 15.f - z;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(settle(x[i], in[k].get(i), su), least), largest);
+            } else if (ZEROS) {
+                // (one more than 15 where both ends round up)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fminf(x[i], 15.f - z);
+            }
+        }
+        // four numbers make one below 2^16, exact in fp32; z is added to all four at once
+        const float low = fmaf(z, 4369.f, fmaf(fmaf(fmaf(x[3], 16.f, x[2]), 16.f, x[1]), 16.f, x[0]));
+        const float high = fmaf(z, 4369.f, fmaf(fmaf(fmaf(x[7], 16.f, x[6]), 16.f, x[5]), 16.f, x[4]));
+        uint32_t word = __byte_perm(__float_as_uint(low + 8388608.f), __float_as_uint(high + 8388608.f), 0x5410);
+        uint8_t* out = t.values + v * t.ld_values + c / 2;
+        if (c + 8 <= t.D) {
+            *reinterpret_cast<uint32_t*>(out) = word;
+        } else {
+            word &= (1u << (4 * (t.D - c))) - 1u;
+            for (int i = 0; c + 2 * i < t.D; ++i) out[i] = static_cast<uint8_t>(word >> (8 * i));
+        }
+        if ((c & ((1 << t.shift) - 1)) == 0) {
+            static_cast<typename S::raw*>(t.scales)[g * t.ld_scales + v] = static_cast<typename S::raw>(S::round(bad ? NAN : s));
+            if (ZEROS) t.zeros[g * t.ld_zeros + v] = static_cast<uint8_t>(z);
+            if (bad) set_error(p.err, kErrRange);
+        }
     }
 }
 
@@ -128,49 +223,163 @@ struct LookupParams {
     Table4 t;
     const void* ids;
     int ids32;
+    int T;
     void* rows;
     int64_t ld_rows;
     float scale;
-    int64_t chunks;              // vectors of a row
-    int64_t total;
+    int log_across, blocks_across;
     int* err;
 };
 
-// A thread takes the 8 columns (4 of fp32) of one 16-byte vector of a row that is written; at a row's ends,
-// where a vector reaches past them, columns go one by one.
+// Whole aligned rows: a thread takes a word, 8 columns, of kDeep rows, and writes 16-byte vectors.  Of fp32 those are
+// two; neighbouring threads exchange words so that each of their stores fills a 32-byte sector together.
+template <class R, class S>
+__global__ void __launch_bounds__(256) lookup_words_kernel(const __grid_constant__ LookupParams p)
+{
+    const Table4& t = p.t;
+    const unsigned down = blockIdx.x / static_cast<unsigned>(p.blocks_across);
+    const int along = static_cast<int>(blockIdx.x - down * static_cast<unsigned>(p.blocks_across));
+    const int c = ((along << p.log_across) + (threadIdx.x & ((1 << p.log_across) - 1))) * 8;
+    const int rows_a_pass = 256 >> p.log_across;
+    const int row0 = static_cast<int>(down) * (kDeep * rows_a_pass) + (threadIdx.x >> p.log_across);
+    const bool in = c < t.D;
+    const typename S::raw* const scales = static_cast<const typename S::raw*>(t.scales) + static_cast<int64_t>(in ? c >> t.shift : 0) * t.ld_scales;
+    const uint8_t* const zeros = t.zeros ? t.zeros + static_cast<int64_t>(in ? c >> t.shift : 0) * t.ld_zeros : nullptr;
+    int64_t id[kDeep];
+    uint32_t word[kDeep];
+    float s[kDeep], z[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+        const int row = row0 + k * rows_a_pass;
+        id[k] = row >= p.T ? LMLOSS_IGNORE_INDEX
+                           : (p.ids32 ? static_cast<int64_t>(static_cast<const int32_t*>(p.ids)[row]) : static_cast<const int64_t*>(p.ids)[row]);
+    }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+        word[k] = 0;
+        s[k] = z[k] = 0.f;
+        if (!in || id[k] < 0 || id[k] >= t.V) {
+            if (id[k] != LMLOSS_IGNORE_INDEX && (id[k] < 0 || id[k] >= t.V)) {
+                set_error(p.err, kErrBadTarget);
+                s[k] = NAN;
+            }
+            continue;
+        }
+        word[k] = __ldg(reinterpret_cast<const uint32_t*>(t.values + id[k] * t.ld_values + (c >> 1)));
+        s[k] = S::widen(__ldg(scales + id[k]));
+        z[k] = zeros ? static_cast<float>(__ldg(zeros + id[k])) : 8.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+        const int row = row0 + k * rows_a_pass;
+        // 2^23 + q, less 2^23 + z: exact
+        const float off = 8388608.f + z[k];
+        auto value = [&](uint32_t w, int i) { return p.scale * (s[k] * (__uint_as_float((w >> (4 * i) & 15u) | 0x4b000000u) - off)); };
+        if constexpr (R::kBytes == 2) {
+            if (!in || row >= p.T) continue;
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = value(word[k], i);
+            Pack<R, 8> v;
+            v.set_all(x);
+            v.store(static_cast<typename R::raw*>(p.rows) + static_cast<int64_t>(row) * p.ld_rows + c);
+        } else {
+            const bool odd = threadIdx.x & 1;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, word[k], 1);
+            const uint32_t first = (odd ? other : word[k]) >> (odd ? 16 : 0), second = (odd ? word[k] : other) >> (odd ? 16 : 0);
+            if (row >= p.T) continue;
+            float* const out = static_cast<float*>(p.rows) + static_cast<int64_t>(row) * p.ld_rows + (c & ~15) + (odd ? 4 : 0);
+            Pack<R, 4> v;
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = value(first, i);
+            v.set_all(x);
+            if ((c & ~15) < t.D) v.store(out);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = value(second, i);
+            v.set_all(x);
+            if ((c | 8) < t.D) v.store(out + 8);
+        }
+    }
+}
+
+// A thread takes the 8 columns (4 of fp32) of one 16-byte vector of a row that is written, kDeep rows; where rows
+// start inside a vector, so does the first of a row, and its numbers come from two words and two groups.
 template <class R, class S>
 __global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ LookupParams p)
 {
     constexpr int E = 16 / R::kBytes;
     const Table4& t = p.t;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.total) return;
-    const int64_t row = i / p.chunks;
-    typename R::raw* out = static_cast<typename R::raw*>(p.rows) + row * p.ld_rows;
-    const int c0 = static_cast<int>(i - row * p.chunks) * E - static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / R::kBytes);
-    if (c0 >= t.D) return;
-    const int64_t id = p.ids32 ? static_cast<int64_t>(static_cast<const int32_t*>(p.ids)[row]) : static_cast<const int64_t*>(p.ids)[row];
-    const bool ok = id >= 0 && id < t.V;
-    if (!ok && id != LMLOSS_IGNORE_INDEX) set_error(p.err, kErrBadTarget);
-    const float other = ok || id == LMLOSS_IGNORE_INDEX ? 0.f : NAN;
-    const uint8_t* q = t.values + (ok ? id : 0) * t.ld_values;
-    auto column = [&](int c) {
-        if (!ok) return other;
-        const int g = c >> t.shift;
-        const float w = table4_scale<S>(t, g, id) * (static_cast<float>(q[c >> 1] >> (4 * (c & 1)) & 15) - table4_zero(t, g, id));
-        return p.scale * w;
-    };
-    if (c0 < 0 || c0 + E > t.D) {
-        for (int k = 0; k < E; ++k)
-            if (c0 + k >= 0 && c0 + k < t.D) out[c0 + k] = static_cast<typename R::raw>(R::round(column(c0 + k)));
-        return;
-    }
-    float x[E];
+    const unsigned down = blockIdx.x / static_cast<unsigned>(p.blocks_across);
+    const int along = static_cast<int>(blockIdx.x - down * static_cast<unsigned>(p.blocks_across));
+    const int vec = (along << p.log_across) + (threadIdx.x & ((1 << p.log_across) - 1));
+    const int rows_a_pass = 256 >> p.log_across;
+    const int64_t row0 = static_cast<int64_t>(down) * (kDeep * rows_a_pass) + (threadIdx.x >> p.log_across);
+
+    int64_t id[kDeep];
+    uint32_t word[kDeep];
+    float s[kDeep][2], z[kDeep][2];
+    int c0[kDeep], border[kDeep];   // columns from `border` on belong to the second group
 #pragma unroll
-    for (int k = 0; k < E; ++k) x[k] = column(c0 + k);
-    Pack<R, E> v;
-    v.set_all(x);
-    v.store(out + c0);
+    for (int k = 0; k < kDeep; ++k) {
+        const int64_t row = row0 + k * rows_a_pass;
+        id[k] = row >= p.T ? LMLOSS_IGNORE_INDEX
+                           : (p.ids32 ? static_cast<int64_t>(static_cast<const int32_t*>(p.ids)[row]) : static_cast<const int64_t*>(p.ids)[row]);
+    }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+        const int64_t row = row0 + k * rows_a_pass;
+        const uintptr_t out = reinterpret_cast<uintptr_t>(p.rows) + static_cast<uintptr_t>(row * p.ld_rows) * R::kBytes;
+        c0[k] = vec * E - static_cast<int>((out & 15u) / R::kBytes);
+        word[k] = 0;
+        s[k][0] = s[k][1] = z[k][0] = z[k][1] = 0.f;
+        border[k] = E;
+        if (id[k] < 0 || id[k] >= t.V || c0[k] >= t.D) continue;
+        const uint8_t* const q = t.values + id[k] * t.ld_values;
+        const int first = max(c0[k], 0), last = min(c0[k] + E, t.D) - 1;
+        const int at = first >> 3;
+        const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(q) + at);
+        const uint32_t w1 = (last >> 3) != at ? __ldg(reinterpret_cast<const uint32_t*>(q) + at + 1) : 0u;
+        word[k] = __funnelshift_r(w0, w1, 4 * (first & 7));
+        if (c0[k] < 0) word[k] <<= 4 * (first - c0[k]);   // the row's first column in its place of the vector
+        const int g0 = first >> t.shift, g1 = last >> t.shift;
+        s[k][0] = s[k][1] = table4_scale<S>(t, g0, id[k]);
+        z[k][0] = z[k][1] = table4_zero(t, g0, id[k]);
+        if (g1 != g0) {
+            s[k][1] = table4_scale<S>(t, g1, id[k]);
+            z[k][1] = table4_zero(t, g1, id[k]);
+            border[k] = (g1 << t.shift) - c0[k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+        const int64_t row = row0 + k * rows_a_pass;
+        if (row >= p.T || c0[k] >= t.D) continue;
+        typename R::raw* const out = static_cast<typename R::raw*>(p.rows) + row * p.ld_rows + c0[k];
+        const bool none = id[k] < 0 || id[k] >= t.V;
+        if (none && id[k] != LMLOSS_IGNORE_INDEX) {
+            set_error(p.err, kErrBadTarget);
+            s[k][0] = s[k][1] = NAN;
+        }
+        float x[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const bool second = i >= border[k];
+            // 2^23 + q, less 2^23 + z: exact
+            const float n = __uint_as_float((word[k] >> (4 * i) & 15u) | 0x4b000000u) - (8388608.f + (second ? z[k][1] : z[k][0]));
+            x[i] = p.scale * ((second ? s[k][1] : s[k][0]) * n);
+            if (none && !(s[k][0] != s[k][0])) x[i] = 0.f;
+        }
+        if (c0[k] >= 0 && c0[k] + E <= t.D) {
+            Pack<R, E> v;
+            v.set_all(x);
+            v.store(out);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (c0[k] + i >= 0 && c0[k] + i < t.D) out[i] = static_cast<typename R::raw>(R::round(x[i]));
+        }
+    }
 }
 
 lmloss_status check_quantize(const lmloss_table4_quantize_args* a)
@@ -225,24 +434,28 @@ lmloss_status lmloss_table4_quantize(lmloss_vocab_handle h, const lmloss_table4_
     if (st != LMLOSS_OK) return st;
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
-    const int64_t chunks = (a->table.D + a->table.group - 1) / a->table.group * (a->table.group / 8);
-    // whole rows a launch, within the grid's limit
-    const int64_t most = std::max<int64_t>(((int64_t(1) << 31) - 1) / chunks * 256, 1);
+    const Spread all((a->table.D + a->table.group - 1) / a->table.group * (a->table.group / 8), a->table.V);
+    // whole blocks of rows a launch, within the grid's limit
+    const int64_t down = kDeep << (8 - all.log_across), most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
     for (int64_t v0 = 0; v0 < a->table.V; v0 += most) {
         QuantizeParams p{};
         p.t = table4_params(a->table);
-        const int64_t rows = std::min<int64_t>(a->table.V - v0, most);
+        p.rows = std::min<int64_t>(a->table.V - v0, most);
         p.t.values += v0 * a->table.ld_values;
         p.t.scales = static_cast<unsigned char*>(p.t.scales) + v0 * float_bytes(a->table.scale_dtype);
         if (p.t.zeros) p.t.zeros += v0;
         p.weight = static_cast<const unsigned char*>(a->weight) + v0 * a->ld_weight * float_bytes(a->weight_dtype);
+        p.weight_end = static_cast<const unsigned char*>(p.weight) + ((p.rows - 1) * a->ld_weight + a->table.D) * float_bytes(a->weight_dtype);
         p.ld = a->ld_weight;
-        p.chunks = chunks;
-        p.total = rows * chunks;
+        p.log_across = all.log_across;
+        p.blocks_across = all.blocks_across;
         p.err = h->err;
-        const unsigned grid = static_cast<unsigned>((p.total + 255) / 256);
+        const unsigned grid = static_cast<unsigned>(all.blocks_across * ((p.rows + down - 1) / down));
         by_type(a->weight_dtype, [&](auto w) {
-            by_type(a->table.scale_dtype, [&](auto s) { quantize_kernel<decltype(w), decltype(s)><<<grid, 256, 0, stream>>>(p); });
+            by_type(a->table.scale_dtype, [&](auto s) {
+                if (p.t.zeros) quantize_kernel<decltype(w), decltype(s), true><<<grid, 256, 0, stream>>>(p);
+                else quantize_kernel<decltype(w), decltype(s), false><<<grid, 256, 0, stream>>>(p);
+            });
         });
         const lmloss_status launched = vocab_launch_err();
         if (launched != LMLOSS_OK) return launched;
@@ -259,22 +472,28 @@ lmloss_status lmloss_table4_lookup(lmloss_vocab_handle h, const lmloss_table4_lo
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
     const int E = 16 / float_bytes(a->rows_dtype);
-    const int64_t chunks = (a->table.D + 2 * E - 2) / E;   // one more where a row starts inside a vector
-    const int64_t most = ((int64_t(1) << 31) - 1) / chunks * 256;
+    // (a thread of the odd half of 16 columns past the end needs its neighbour's group: 16 columns lie in one)
+    const bool words = a->table.D % 8 == 0 && (a->table.D % 16 == 0 || E == 8) && aligned16(a->rows) && a->ld_rows % E == 0;
+    const Spread all(words ? a->table.D / 8 : (a->table.D + 2 * E - 2) / E, a->T);   // a vector more where a row starts inside one
+    const int64_t down = kDeep << (8 - all.log_across), most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
     for (int64_t t0 = 0; t0 < a->T; t0 += most) {
         LookupParams p{};
         p.t = table4_params(a->table);
         p.ids = static_cast<const unsigned char*>(a->ids) + t0 * (a->ids_dtype == LMLOSS_INT64 ? 8 : 4);
         p.ids32 = a->ids_dtype == LMLOSS_INT32;
+        p.T = static_cast<int>(std::min<int64_t>(a->T - t0, most));
         p.rows = static_cast<unsigned char*>(a->rows) + t0 * a->ld_rows * float_bytes(a->rows_dtype);
         p.ld_rows = a->ld_rows;
         p.scale = a->scale;
-        p.chunks = chunks;
-        p.total = std::min<int64_t>(a->T - t0, most) * chunks;
+        p.log_across = all.log_across;
+        p.blocks_across = all.blocks_across;
         p.err = h->err;
-        const unsigned grid = static_cast<unsigned>((p.total + 255) / 256);
+        const unsigned grid = static_cast<unsigned>(all.blocks_across * ((p.T + down - 1) / down));
         by_type(a->rows_dtype, [&](auto r) {
-            by_type(a->table.scale_dtype, [&](auto s) { lookup_kernel<decltype(r), decltype(s)><<<grid, 256, 0, stream>>>(p); });
+            by_type(a->table.scale_dtype, [&](auto s) {
+                if (words) lookup_words_kernel<decltype(r), decltype(s)><<<grid, 256, 0, stream>>>(p);
+                else lookup_kernel<decltype(r), decltype(s)><<<grid, 256, 0, stream>>>(p);
+            });
         });
         const lmloss_status launched = vocab_launch_err();
         if (launched != LMLOSS_OK) return launched;
