@@ -456,8 +456,8 @@ struct GradParams {
     int64_t ld;
     int T, V;
     int n;
-    int parts;                   // of a row, kGradVecs * kThreads vectors each
-    float inv_hi, inv_lo;        // 1 / tau as an fp32 pair
+    int parts, loops;            // parts of a row; a part is loops * kGradVecs * kThreads vectors
+    float tau_inv, tau_inv_lo;   // 1 / tau as an fp32 pair
     const void* tokens;
     int ids32;
     const int32_t* mask;
@@ -471,18 +471,62 @@ struct GradParams {
     int* err;
 };
 
-constexpr int kGradVecs = 4;     // vectors a thread
+constexpr int kGradVecs = 4;     // vectors a thread, on their way together
 
 struct __align__(16) GradShared {
     int32_t token[LMLOSS_MAX_GIVEN];         // -1 = none
-    float g[LMLOSS_MAX_GIVEN];
-    uint32_t flag[kGradVecs * kThreads / 32];   // vectors of the part that hold a given token
+    float g[LMLOSS_MAX_GIVEN], z[LMLOSS_MAX_GIVEN];
     float red[kWarps];
 };
 
-// A thread's vectors start on 16-byte boundaries of the row that it writes; at a row's ends,
-// where a vector reaches past them, columns go one by one.
+// -p (sum g + gH (ln p + H)) / tau for the columns without a given token's own part, p = e^d, d = z / tau - lse.  The
+// difference is taken in two fused operations, 1 / tau as a pair, before the change to base 2: of rows at the type's
+// lowest values it is all that is left.
+template <bool ENT>
+struct GradColumn {
+    float tau_inv, tau_inv_lo, less, base, ge;
+    __device__ __forceinline__ GradColumn(const GradParams& p, float lse, float sum, float h, float gh)
+        : tau_inv(p.tau_inv), tau_inv_lo(p.tau_inv_lo), less(-lse), base(-(ENT ? fmaf(gh, h, sum) : sum) * p.tau_inv), ge(-gh * p.tau_inv)
+    {
+    }
+    __device__ __forceinline__ void two(float& a, float& c) const
+    {
+        // (-inf takes no second product, and 0 * -inf would be NaN)
+        const uint64_t d2 = f2_fma(f2_pack(max_nan(a, -3.402823466e38f), max_nan(c, -3.402823466e38f)), f2_pack(tau_inv_lo, tau_inv_lo),
+                                   f2_fma(f2_pack(a, c), f2_pack(tau_inv, tau_inv), f2_pack(less, less)));
+        float da, dc, ua, uc;
+        f2_unpack(d2, da, dc);
+        if (ENT) {
+            da = max_nan(da, kLeast);
+            dc = max_nan(dc, kLeast);
+        }
+        f2_unpack(f2_mul(f2_pack(da, dc), f2_pack(kLog2e, kLog2e)), ua, uc);
+        const uint64_t by2 = ENT ? f2_fma(f2_pack(ge, ge), f2_pack(da, dc), f2_pack(base, base)) : f2_pack(base, base);
+        f2_unpack(f2_mul(f2_pack(ex2(ua), ex2(uc)), by2), a, c);
+    }
+    __device__ __forceinline__ float one(float a) const
+    {
+        float c = a;
+        two(a, c);
+        return a;
+    }
+};
+
+// Columns [c, c + E) of a row that reach past its ends, or past what may be read: one by one.
 template <class T, bool ENT>
+__device__ __noinline__ void grad_ends(const GradColumn<ENT>& f, const typename T::raw* z, typename T::raw* g, const int32_t* mask, int64_t c, int V,
+                                       bool none)
+{
+    for (int i = 0; i < Logits<T>::E; ++i)
+        if (c + i >= 0 && c + i < V) {
+            const bool in = !none && allowed(mask, static_cast<int>(c) + i);
+            g[c + i] = static_cast<typename T::raw>(T::round(in ? f.one(T::widen(z[c + i])) : 0.f));
+        }
+}
+
+// A thread's vectors start on 16-byte boundaries of the row that it writes; SAME: the logits' do too.  Given tokens'
+// columns are written again at the end, from logits looked at before anything is written (it may be in place).
+template <class T, bool ENT, bool SAME>
 __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_constant__ GradParams p)
 {
     constexpr int E = Logits<T>::E;
@@ -494,27 +538,43 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
     raw* g = static_cast<raw*>(p.grad) + static_cast<int64_t>(row) * p.ld_grad;
     const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / T::kBytes);   // columns of the first vector before the row
-    const bool aligned = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(g)) & 15u) == 0;
-    const int v0 = part * (kGradVecs * kThreads);
+    const int per = p.loops * kGradVecs * kThreads;
+    const int64_t c0 = static_cast<int64_t>(part) * per * E - off, c_end = min(c0 + static_cast<int64_t>(per) * E, static_cast<int64_t>(p.V));
     const float lse = p.lse[row];
     const bool none = lse == -INFINITY;
 
-    // ---- the given tokens: their gradients' sum, and which vectors hold one
-    if (tid < kGradVecs * kThreads / 32) sm.flag[tid] = 0;
-    __syncthreads();
+    // ---- the first vectors on their way, then the given tokens: the sum of their gradients
+    uint4 x[kGradVecs];
+    uint32_t w5[SAME ? 1 : kGradVecs];   // what unaligned logits need beside
+    // (unaligned: the words around the columns, inside the call's logits)
+    const int64_t safe_lo = SAME || row > 0 ? 0 : 2, safe_hi = SAME || row < p.T - 1 ? p.V : p.V - 2;
+    auto whole = [&](int64_t c) { return c >= safe_lo && c + E <= safe_hi; };
+    auto load = [&](int64_t first) {
+#pragma unroll
+        for (int k = 0; k < kGradVecs; ++k) {
+            const int64_t c = first + static_cast<int64_t>(k * kThreads + tid) * E;
+            if (!whole(c)) continue;
+            if constexpr (SAME) {
+                x[k] = *reinterpret_cast<const uint4*>(z + c);
+            } else {
+                const uint32_t* a = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(z + c) & ~uintptr_t(3));
+                x[k] = make_uint4(a[0], a[1], a[2], a[3]);
+                w5[k] = T::kBytes == 4 ? 0u : a[4];
+            }
+        }
+    };
+    load(c0);
     float sum = 0.f;
     for (int j = tid; j < p.n; j += kThreads) {
         const int64_t o = static_cast<int64_t>(row) * p.n + j, t = load_token(p.tokens, p.ids32, o);
         const bool in = t >= 0 && t < p.V;
         if (!in && t != LMLOSS_IGNORE_INDEX) set_error(p.err, kErrBadTarget);
-        const float x = in ? p.grad_logp[o] : 0.f;
-        sm.token[j] = in ? static_cast<int>(t) : -1;
-        sm.g[j] = x;
-        sum += x;
-        if (in) {
-            const int64_t v = (t + off) / E - v0;
-            if (v >= 0 && v < kGradVecs * kThreads) atomicOr(&sm.flag[v >> 5], 1u << (v & 31));
-        }
+        const float y = in ? p.grad_logp[o] : 0.f;
+        const bool here = in && t >= c0 && t < c_end;
+        sm.token[j] = here ? static_cast<int>(t) : -1;
+        sm.g[j] = y;
+        sm.z[j] = here ? T::widen(z[t]) : 0.f;
+        sum += y;
     }
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) sm.red[warp] = sum;
@@ -522,49 +582,63 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += sm.red[w];
-    const float ge = ENT ? p.grad_entropy[row] : 0.f;
-    // by(v) = sum + ge (ln p + H)
-    const float base = ENT ? fmaf(ge, p.entropy[row], sum) : sum;
+    const GradColumn<ENT> f(p, lse, sum, ENT ? p.entropy[row] : 0.f, ENT ? p.grad_entropy[row] : 0.f);
 
-    auto one = [&](float x, int c, bool marked) {
-        if (none || !allowed(mask, c)) return 0.f;
-        float d = fmaf(x, p.inv_hi, -lse);
-        // (16-bit results do not show what 1 / tau loses as one fp32; -inf takes no second product)
-        if constexpr (T::kBytes == 4) d = fmaf(max_nan(x, -3.402823466e38f), p.inv_lo, d);
-        d = max_nan(d, kLeast);
-        const float pr = ex2(d * kLog2e);
-        float out = -pr * (ENT ? fmaf(ge, d, base) : base);
-        if (marked)
-            for (int j = 0; j < p.n; ++j)
-                if (sm.token[j] == c) out += sm.g[j];
-        return out * p.inv_hi;
-    };
-    auto column = [&](int c, bool marked) { g[c] = static_cast<raw>(T::round(one(T::widen(z[c]), c, marked))); };
-
-    uint4 x[kGradVecs];
+    for (int64_t first = c0; first < c_end; first += kGradVecs * kThreads * E) {
+        if (first != c0) load(first);
 #pragma unroll
-    for (int k = 0; k < kGradVecs; ++k) {
-        const int64_t c = static_cast<int64_t>(v0 + k * kThreads + tid) * E - off;
-        if (aligned && c >= 0 && c + E <= p.V) x[k] = *reinterpret_cast<const uint4*>(z + c);
-    }
+        for (int k = 0; k < kGradVecs; ++k) {
+            const int64_t c = first + static_cast<int64_t>(k * kThreads + tid) * E;
+            if (c >= p.V) break;
+            if (!whole(c)) {
+                grad_ends<T, ENT>(f, z, g, mask, c, p.V, none);
+                continue;
+            }
+            Pack<T, E> q;
+            q.w[0] = x[k].x; q.w[1] = x[k].y; q.w[2] = x[k].z; q.w[3] = x[k].w;
+            if constexpr (!SAME && T::kBytes == 2) {
+                const uint32_t sh = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z + c)) & 2u) * 8u;
+                q.w[0] = __funnelshift_r(x[k].x, x[k].y, sh);
+                q.w[1] = __funnelshift_r(x[k].y, x[k].z, sh);
+                q.w[2] = __funnelshift_r(x[k].z, x[k].w, sh);
+                q.w[3] = __funnelshift_r(x[k].w, w5[k], sh);
+            }
+            float out[E];
 #pragma unroll
-    for (int k = 0; k < kGradVecs; ++k) {
-        const int v = k * kThreads + tid;
-        const int64_t c = static_cast<int64_t>(v0 + v) * E - off;
-        if (c >= p.V) break;
-        const bool marked = sm.flag[v >> 5] >> (v & 31) & 1u;
-        if (c < 0 || c + E > p.V || !aligned) {
-            for (int i = 0; i < E; ++i)
-                if (c + i >= 0 && c + i < p.V) column(static_cast<int>(c) + i, marked);
-            continue;
+            for (int i = 0; i < E; i += 2) {
+                out[i] = q.get(i);
+                out[i + 1] = q.get(i + 1);
+                f.two(out[i], out[i + 1]);
+            }
+            if (mask) {
+                // (rows begin inside a vector: its columns may lie in two words)
+                const int b = static_cast<int>(c);
+                const uint32_t m0 = static_cast<uint32_t>(mask[b >> 5]), m1 = ((b + E - 1) >> 5) != (b >> 5) ? static_cast<uint32_t>(mask[(b >> 5) + 1]) : 0u;
+                const uint32_t allow = __funnelshift_r(m0, m1, b & 31);
+#pragma unroll
+                for (int i = 0; i < E; ++i) out[i] = allow >> i & 1u ? out[i] : 0.f;
+            }
+            if (none) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) out[i] = 0.f;
+            }
+            q.set_all(out);
+            q.store(g + c);
         }
-        Pack<T, E> q;
-        q.w[0] = x[k].x; q.w[1] = x[k].y; q.w[2] = x[k].z; q.w[3] = x[k].w;
-        float out[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) out[i] = one(q.get(i), static_cast<int>(c) + i, marked);
-        q.set_all(out);
-        q.store(g + c);
+    }
+    if (none || p.n == 0) return;
+    __syncthreads();
+    for (int j = tid; j < p.n; j += kThreads) {
+        const int t = sm.token[j];
+        if (t < 0 || !allowed(mask, t)) continue;
+        // the first of equal tokens adds them all
+        bool before = false;
+        for (int i = 0; i < j; ++i) before = before || sm.token[i] == t;
+        if (before) continue;
+        float own = sm.g[j];
+        for (int i = j + 1; i < p.n; ++i)
+            if (sm.token[i] == t) own += sm.g[i];
+        g[t] = static_cast<raw>(T::round(fmaf(own, p.tau_inv, f.one(sm.z[j]))));
     }
 }
 
@@ -670,12 +744,18 @@ lmloss_status check_grad(const lmloss_logprobs_grad_args* a)
     return LMLOSS_OK;
 }
 
-template <class T>
+template <class T, bool SAME>
 void launch_grad(const GradParams& p, cudaStream_t stream)
 {
     const unsigned grid = static_cast<unsigned>(p.T) * static_cast<unsigned>(p.parts);
-    if (p.grad_entropy) logprobs_grad_kernel<T, true><<<grid, kThreads, 0, stream>>>(p);
-    else logprobs_grad_kernel<T, false><<<grid, kThreads, 0, stream>>>(p);
+    if (p.grad_entropy) logprobs_grad_kernel<T, true, SAME><<<grid, kThreads, 0, stream>>>(p);
+    else logprobs_grad_kernel<T, false, SAME><<<grid, kThreads, 0, stream>>>(p);
+}
+template <class T>
+void launch_grad(const GradParams& p, bool same, cudaStream_t stream)
+{
+    if (same) launch_grad<T, true>(p, stream);
+    else launch_grad<T, false>(p, stream);
 }
 
 }  // namespace
@@ -760,8 +840,14 @@ lmloss_status lmloss_logprobs_backward(lmloss_vocab_handle h, const lmloss_logpr
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
     const int es = float_bytes(a->dtype), id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
-    const int64_t E = 16 / es, vecs = (a->V + E - 1 + E - 1) / E, per = kGradVecs * kThreads;   // a vector more where rows start inside one
-    const int64_t parts = (vecs + per - 1) / per;
+    const int64_t E = 16 / es, vecs = (a->V + E - 1 + E - 1) / E;   // a vector more where rows start inside one
+    // a part's given tokens and its barriers cost about as much as a loop: four loops where that leaves
+    // every SM its blocks (four of each) all the same
+    int64_t loops = 1;
+    while (loops < 4 && a->T * ((vecs + 2 * loops * kGradVecs * kThreads - 1) / (2 * loops * kGradVecs * kThreads)) >= 8 * h->num_sms) loops *= 2;
+    const int64_t per = loops * kGradVecs * kThreads, parts = (vecs + per - 1) / per;
+    const bool same = ((reinterpret_cast<uintptr_t>(a->logits) ^ reinterpret_cast<uintptr_t>(a->grad_out)) & 15u) == 0 &&
+                      (a->T == 1 || (a->ld - a->ld_grad) * es % 16 == 0);
     const int64_t most = std::max<int64_t>(((int64_t(1) << 31) - 1) / parts, 1);
     for (int64_t r0 = 0; r0 < a->T; r0 += most) {
         GradParams p{};
@@ -771,9 +857,10 @@ lmloss_status lmloss_logprobs_backward(lmloss_vocab_handle h, const lmloss_logpr
         p.V = static_cast<int>(a->V);
         p.n = static_cast<int>(a->n);
         p.parts = static_cast<int>(parts);
+        p.loops = static_cast<int>(loops);
         const double inv = 1.0 / static_cast<double>(a->temperature);
-        p.inv_hi = static_cast<float>(inv);
-        p.inv_lo = static_cast<float>(inv - static_cast<double>(p.inv_hi));
+        p.tau_inv = static_cast<float>(inv);
+        p.tau_inv_lo = static_cast<float>(inv - static_cast<double>(p.tau_inv));
         p.tokens = a->n ? static_cast<const unsigned char*>(a->tokens) + r0 * a->n * id_bytes : nullptr;
         p.ids32 = a->ids_dtype == LMLOSS_INT32;
         p.mask = a->token_mask ? a->token_mask + r0 * a->mask_stride : nullptr;
@@ -786,9 +873,9 @@ lmloss_status lmloss_logprobs_backward(lmloss_vocab_handle h, const lmloss_logpr
         p.ld_grad = a->ld_grad;
         p.err = h->err;
         switch (a->dtype) {
-        case LMLOSS_BF16: launch_grad<Bf16>(p, stream); break;
-        case LMLOSS_FP16: launch_grad<Fp16>(p, stream); break;
-        default: launch_grad<Fp32>(p, stream); break;
+        case LMLOSS_BF16: launch_grad<Bf16>(p, same, stream); break;
+        case LMLOSS_FP16: launch_grad<Fp16>(p, same, stream); break;
+        default: launch_grad<Fp32>(p, same, stream); break;
         }
         const lmloss_status launched = vocab_launch_err();
         if (launched != LMLOSS_OK) return launched;
