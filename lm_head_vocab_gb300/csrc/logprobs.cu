@@ -7,8 +7,9 @@
 //   lse = m / tau + ln s,   H = ln s - ln2 e / s,   logp_j = z[t_j] / tau - lse
 //
 // so one pass with a running maximum gives all of it: a part of a row keeps (m, s, e), and
-// when m rises by d (in u's units) s becomes s 2^-d and e becomes (e - d s) 2^-d.  Alternatives
-// are kept as in a beam step: a threshold from group maxima, vectors noted against it.
+// when m rises by d (in u's units) s becomes s 2^-d and e becomes (e - d s) 2^-d.  In place of m log2(e) / tau
+// stands its fp32 value R, so that u is one fused operation; what R is off by goes into lse.
+// Alternatives are kept as in a beam step: a threshold from group maxima, vectors noted against it.
 //
 // The gradient is one more pass, from lse and H alone: p = e^(y - lse).
 #include <algorithm>
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kMaxTop = LMLOSS_MAX_ALTERNATIVES;
 constexpr int kCap = 1024;                   // candidate keys held at once
-constexpr int kHits = 512;                   // vectors of a part that reach its first threshold
+constexpr int kHits = 1024;                  // vectors of a part that reach its first threshold
 constexpr int kSmall = 256;                  // few enough to be ranked by counting
 constexpr int kMaxParts = 4096;              // parts of all rows, where rows are cut
 constexpr float kLeast = -1000.f;            // an exponent whose power is 0: 0 * -inf would be NaN
@@ -71,20 +72,85 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// A running sum of 2^u and u 2^u about a maximum.
+// A running sum of 2^u and u 2^u about r, the fp32 value of the maximum in base 2.
 struct Sums {
-    float m = -INFINITY, s = 0.f, e = 0.f;
-    __device__ __forceinline__ void raise(float top, float mul)
+    float r = -INFINITY, s = 0.f, e = 0.f;
+    __device__ __forceinline__ void raise(float top)
     {
-        if (top > m) {
+        if (top > r) {
             // (from -inf: s and e are 0)
-            const float d = fmaxf((m - top) * mul, kLeast), f = ex2(d);
+            const float d = fmaxf(r - top, kLeast), f = ex2(d);
             e = fmaf(s, d, e) * f;
             s *= f;
-            m = top;
+            r = top;
         }
     }
 };
+
+// Whether a maximum leaves room for z log2(e) / tau in fp32, and, of bf16, for what stands in the place of -inf in the
+// sum of u 2^u: -2^100, which is nothing beside it.  Parts of other maxima (rows at the type's lowest values) are
+// summed again, by sum_slowly.
+template <class T>
+__device__ __forceinline__ bool usual(float m)
+{
+    return T::kIndex == Fp16::kIndex || fabsf(m) < 0x1p99f;
+}
+template <class T>
+__device__ __forceinline__ uint32_t floor_pair(uint32_t w)
+{
+    if constexpr (T::kIndex == Bf16::kIndex) {
+        const uint32_t least = 0xf180f180u;
+        const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&least));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    return w;
+}
+
+// Largest of several vectors' logits; NaN are passed over here and show up in the sum.
+template <class T, int VPT>
+__device__ __forceinline__ float largest_of(const Pack<T, Logits<T>::E> (&q)[VPT])
+{
+    if constexpr (T::kBytes == 4) {
+        float r = Logits<T>::largest(q[0]);
+#pragma unroll
+        for (int j = 1; j < VPT; ++j) r = fmaxf(r, Logits<T>::largest(q[j]));
+        return r;
+    } else {
+        using H2 = typename std::conditional<std::is_same<T, Bf16>::value, __nv_bfloat162, __half2>::type;
+        H2 r = *reinterpret_cast<const H2*>(&q[0].w[0]);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r = __hmax2(r, *reinterpret_cast<const H2*>(&q[j].w[i]));
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&r);
+        return fmaxf(T::widen(static_cast<uint16_t>(w & 0xffffu)), T::widen(static_cast<uint16_t>(w >> 16)));
+    }
+}
+
+// For each of 8 (fp32: 4) bits all ones or zeros over its element, as words.
+template <int BYTES>
+__device__ __forceinline__ void spread_bits(uint32_t allow, uint32_t (&keep)[4])
+{
+    // bit k of four to the top of byte k, then the byte's top bit over whole bytes
+    auto prmt = [](uint32_t x, uint32_t sel) {
+        uint32_t r;
+        asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "r"(sel));
+        return r;
+    };
+    const uint32_t low = (allow & 15u) * 0x10204080u;
+    if (BYTES == 4) {
+        keep[0] = prmt(low, 0x8888u);
+        keep[1] = prmt(low, 0x9999u);
+        keep[2] = prmt(low, 0xaaaau);
+        keep[3] = prmt(low, 0xbbbbu);
+    } else {
+        const uint32_t high = (allow >> 4 & 15u) * 0x10204080u;
+        keep[0] = prmt(low, 0x9988u);
+        keep[1] = prmt(low, 0xbbaau);
+        keep[2] = prmt(high, 0x9988u);
+        keep[3] = prmt(high, 0xbbaau);
+    }
+}
 
 struct __align__(16) LogprobsShared {
     uint64_t buf[kCap];                      // candidates
@@ -95,20 +161,19 @@ struct __align__(16) LogprobsShared {
     uint32_t thr, thr_end;
     float red_m[kWarps], red_s[kWarps], red_e[kWarps];
     int count, hit_count, few, last;
+    uint64_t cut;
     double lse;
 };
 
-// The M best of the candidates in sm.buf (n of them, all different) into sm.best, best
-// first, 0 where there are none.
-__device__ __noinline__ void rank_best(LogprobsShared& sm, int n, int M)
+// The M best of n candidates (all different) into sm.best, best first, 0 where there are none.  `few` has
+// room for M of them.
+__device__ __noinline__ void rank_best(LogprobsShared& sm, const uint64_t* set, uint64_t* few, int n, int M)
 {
     const int tid = threadIdx.x;
-    const uint64_t cut = n > kSmall ? mth_largest(sm.buf, n, M, sm.counts) : 0;
-    const uint64_t* set = sm.buf;
+    const uint64_t cut = n > kSmall ? mth_largest(set, n, M, sm.counts) : 0;
     if (cut) {
-        uint64_t* few = reinterpret_cast<uint64_t*>(sm.data);
         for (int i = tid; i < n; i += kThreads)
-            if (sm.buf[i] >= cut) few[atomicAdd(&sm.few, 1)] = sm.buf[i];
+            if (set[i] >= cut) few[atomicAdd(&sm.few, 1)] = set[i];
         __syncthreads();
         n = M;
         set = few;
@@ -124,38 +189,59 @@ __device__ __noinline__ void rank_best(LogprobsShared& sm, int n, int M)
     __syncthreads();
 }
 
-// What follows a row's sums: its statistics (thread 0 holds them), given tokens and, from
-// sm.best, alternatives.
+// A row's statistics from its sums, by one thread.  m: the maximum's part of lse.
+__device__ __forceinline__ void write_sums(const LogprobsParams& p, LogprobsShared& sm, int row, double m, float hi, float lo, float e)
+{
+    const bool none = m == -INFINITY && hi == 0.f;
+    const double log_s = none ? 0.0 : log_of_sum(hi, lo);
+    const double lse = none ? -INFINITY : (m == INFINITY ? NAN : m + log_s);
+    sm.lse = lse;
+    if (p.lse_out) p.lse_out[row] = static_cast<float>(lse);
+    if (p.entropy_out) p.entropy_out[row] = none ? 0.f : (m == INFINITY ? NAN : static_cast<float>(log_s - kLn2 * static_cast<double>(e / hi)));
+}
+
+// The maximum's part of lse: m / tau, and what R = fl(m mul) is off from m mul, which the sums about R hold.
 template <class T>
-__device__ void write_row(const LogprobsParams& p, LogprobsShared& sm, int row, float m, float hi, float lo, float e)
+__device__ __forceinline__ double lse_part(const LogprobsParams& p, float m)
+{
+    const double at = static_cast<double>(m) * p.inv_tau;
+    return usual<T>(m) && fabsf(m) < INFINITY ? at + kLn2 * (static_cast<double>(__fmul_rn(m, p.mul)) - static_cast<double>(m) * static_cast<double>(p.mul)) : at;
+}
+
+// Given token j of a row: what stands for its log-probability until lse is known.
+struct Given {
+    float z;
+    int kind;                    // 0 a logit, 1 none, 2 not in the vocabulary
+};
+template <class T>
+__device__ __forceinline__ Given load_given(const LogprobsParams& p, int row, int64_t j)
+{
+    const int64_t t = load_token(p.tokens, p.ids32, static_cast<int64_t>(row) * p.n + j);
+    Given g{0.f, t == LMLOSS_IGNORE_INDEX ? 1 : (t < 0 || t >= p.V ? 2 : 0)};
+    if (g.kind == 0) {
+        const typename T::raw* z = static_cast<const typename T::raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
+        const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
+        g.z = allowed(mask, static_cast<int>(t)) ? T::widen(z[t]) : -INFINITY;
+    }
+    return g;
+}
+
+// What follows a row's statistics: its given tokens (each thread's first one is there already) and, from sm.best,
+// alternatives.  After a barrier that follows write_sums and rank_best.
+template <class T>
+__device__ __forceinline__ void write_row(const LogprobsParams& p, LogprobsShared& sm, int row, Given first)
 {
     const int tid = threadIdx.x;
-    if (tid == 0) {
-        const bool none = m == -INFINITY && hi == 0.f;
-        const double log_s = none ? 0.0 : log_of_sum(hi, lo);
-        const double lse = none ? -INFINITY : static_cast<double>(m) * p.inv_tau + log_s;
-        sm.lse = lse;
-        if (p.lse_out) p.lse_out[row] = static_cast<float>(lse);
-        if (p.entropy_out) p.entropy_out[row] = none ? 0.f : static_cast<float>(log_s - kLn2 * static_cast<double>(e / hi));
-    }
-    __syncthreads();
     const double lse = sm.lse;
-    const typename T::raw* z = static_cast<const typename T::raw*>(p.logits) + static_cast<int64_t>(row) * p.ld;
-    const int32_t* mask = p.mask ? p.mask + row * p.mask_stride : nullptr;
     for (int64_t j = tid; j < p.n; j += kThreads) {
-        const int64_t o = static_cast<int64_t>(row) * p.n + j, t = load_token(p.tokens, p.ids32, o);
-        float out;
-        if (t == LMLOSS_IGNORE_INDEX) {
-            out = 0.f;
-        } else if (t < 0 || t >= p.V) {
+        const Given g = j == tid ? first : load_given<T>(p, row, j);
+        float out = lse == -INFINITY ? -INFINITY : static_cast<float>(static_cast<double>(g.z) * p.inv_tau - lse);
+        if (g.kind == 1) out = 0.f;
+        if (g.kind == 2) {
             set_error(p.err, kErrBadTarget);
             out = NAN;
-        } else {
-            const float x = allowed(mask, static_cast<int>(t)) ? T::widen(z[t]) : -INFINITY;
-            const double y = static_cast<double>(x) * p.inv_tau - lse;
-            out = lse == -INFINITY ? -INFINITY : static_cast<float>(y);
         }
-        p.logp_out[o] = out;
+        p.logp_out[static_cast<int64_t>(row) * p.n + j] = out;
     }
     for (int i = tid; i < p.M; i += kThreads) {
         const uint64_t k = sm.best[i];
@@ -169,10 +255,16 @@ __device__ void write_row(const LogprobsParams& p, LogprobsShared& sm, int row, 
 
 // The block that finishes a row's last part joins the parts.
 template <class T>
-__device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& sm, int row)
+__device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& sm, int row, Given first)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = p.slices, M = p.M;
+    // the candidates on their way beside the sums
+    const uint64_t* const keys = p.keys + static_cast<int64_t>(row) * S * M;
+    uint64_t head = 0, mine[8];
+    if (M > 0 && tid < S) head = __ldcg(keys + static_cast<int64_t>(tid) * M);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine[i] = tid + i * kThreads < S * M ? __ldcg(keys + tid + i * kThreads) : 0;
     // sums: error-free pairs of fp32
     float m = -INFINITY, hi = 0.f, lo = 0.f, e = 0.f;
     if (warp == 0) {
@@ -186,7 +278,8 @@ __device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& s
         };
         for (int s = lane; s < S; s += 32) {
             const float4 q = __ldcg(&st[s]);
-            const float d = q.x == m ? 0.f : fmaxf((q.x - m) * p.mul, kLeast), f = exp2f(d);
+            const float apart = usual<T>(q.x) && usual<T>(m) ? __fmul_rn(q.x, p.mul) - __fmul_rn(m, p.mul) : (q.x - m) * p.mul;
+            const float d = q.x == m ? 0.f : fmaxf(apart, kLeast), f = exp2f(d);
             add(q.y * f, 0.f);
             e += fmaf(q.y, d, q.z) * f;
         }
@@ -196,40 +289,87 @@ __device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& s
             e += __shfl_xor_sync(0xffffffffu, e, o);
         }
     }
+    if (tid == 0) write_sums(p, sm, row, lse_part<T>(p, m), hi, lo, e);
     if (M > 0) {
-        // candidates: below the M-th largest of the parts' best there are none
-        const uint64_t* keys = p.keys + static_cast<int64_t>(row) * S * M;
-        uint64_t thr = 1;
         const int all = S * M;
-        if (all > kCap && S > M && S <= kCap) {
-            for (int s = tid; s < S; s += kThreads) sm.buf[s] = __ldcg(keys + static_cast<int64_t>(s) * M);
+        uint64_t* const held = reinterpret_cast<uint64_t*>(sm.data);
+        if (tid == 0) sm.count = sm.few = 0;
+        // candidates: below the M-th largest of the parts' best there are none
+        constexpr int kMine = 8;
+        uint64_t thr = 1;
+        bool done = false;
+        if (all <= kMine * kThreads && S <= kThreads) {
+            if (tid < S) sm.buf[tid] = head;
+            if (tid == 0) sm.cut = 1;
             __syncthreads();
-            // (equal zeros, of parts without a candidate, count as the smallest)
-            thr = max(mth_largest(sm.buf, S, M, sm.counts), uint64_t(1));
-            __syncthreads();
-        }
-        int n;
-        while (true) {
-            if (tid == 0) sm.count = 0;
-            __syncthreads();
-            for (int i = tid; i < all; i += kThreads) {
-                const uint64_t k = __ldcg(keys + i);
-                if (k >= thr) {
-                    const int to = atomicAdd(&sm.count, 1);
-                    if (to < kCap) sm.buf[to] = k;
-                }
+            if (S > M && tid < S) {
+                int above = 0;
+#pragma unroll 4
+                for (int o = 0; o < S; ++o) above += sm.buf[o] > head ? 1 : 0;
+                if (above == M - 1 && head) sm.cut = head;   // (equal ones are parts without a candidate)
             }
             __syncthreads();
-            n = sm.count;
-            if (n <= kCap) break;
-            thr = mth_largest(sm.buf, kCap, M, sm.counts);
+            thr = sm.cut;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                if (mine[i] >= thr) {
+                    const int to = atomicAdd(&sm.count, 1);
+                    if (to < kCap) held[to] = mine[i];
+                }
             __syncthreads();
+            done = sm.count <= kCap;
         }
-        if (tid == 0) sm.few = 0;
+        const uint64_t* set = held;
+        if (!done) {
+            set = sm.buf;
+            while (true) {
+                __syncthreads();
+                if (tid == 0) sm.count = 0;
+                __syncthreads();
+                for (int i = tid; i < all; i += kThreads) {
+                    const uint64_t k = __ldcg(keys + i);
+                    if (k >= thr) {
+                        const int to = atomicAdd(&sm.count, 1);
+                        if (to < kCap) sm.buf[to] = k;
+                    }
+                }
+                __syncthreads();
+                if (sm.count <= kCap) break;
+                thr = mth_largest(sm.buf, kCap, M, sm.counts);
+            }
+        }
+        rank_best(sm, set, set == held ? sm.buf : held, sm.count, M);
+    } else {
         __syncthreads();
-        rank_best(sm, n, M);
     }
-    write_row<T>(p, sm, row, m, hi, lo, e);
+    write_row<T>(p, sm, row, first);
+}
+
+// A part whose maximum is finite and not usual: 2^u about the maximum itself, taken off before the product.  Each warp's
+// into its place.
+template <class T>
+__device__ __noinline__ void sum_slowly(const LogprobsParams& p, LogprobsShared& sm, const typename T::raw* z, const int32_t* mask, int begin, int end,
+                                        float top)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float s = 0.f, e = 0.f;
+    for (int c = begin + tid; c < end; c += kThreads) {
+        if (!allowed(mask, c)) continue;
+        const float u = max_nan((T::widen(z[c]) - top) * p.mul, kLeast), w = ex2(u);
+        s += w;
+        e = fmaf(w, u, e);
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    __syncthreads();   // everyone has read the maxima
+    if (lane == 0) {
+        sm.red_m[warp] = top;
+        sm.red_s[warp] = s;
+        sm.red_e[warp] = e;
+    }
+    __syncthreads();
 }
 
 // A block takes `tiles` tiles of one row, one after the other, with the next tile's loads in
@@ -263,52 +403,49 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         sm.thr = 0;
         sm.thr_end = 0;
     }
+    const Given first = tid < p.n ? load_given<T>(p, row, tid) : Given{0.f, 1};   // under the way of the row
     Sums sum;
-    float best = -INFINITY, least = 0.f;
+    float m = -INFINITY, least = 0.f;   // m: the thread's largest allowed logit
     int tile = 0;
     auto use_tile = [&](Pack<T, E> (&q)[VPT], int c0) {
         if (mask) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int c = c0 + j * (kThreads * E);
-                const uint32_t allow = c < p.V ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0u;
+                uint32_t keep[4];
+                spread_bits<T::kBytes>(c < p.V ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0u, keep);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t keep;
-                    if constexpr (T::kBytes == 4) keep = 0u - (allow >> i & 1u);
-                    else keep = ((0u - (allow >> (2 * i) & 1u)) & 0xffffu) | ((0u - (allow >> (2 * i + 1) & 1u)) << 16);
-                    q[j].w[i] = (q[j].w[i] & keep) | (kNone & ~keep);
-                }
+                for (int i = 0; i < 4; ++i) q[j].w[i] = (q[j].w[i] & keep[i]) | (kNone & ~keep[i]);
             }
         }
-        float vmax[VPT], tmax;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) vmax[j] = Logits<T>::largest(q[j]);
-        tmax = vmax[0];
-#pragma unroll
-        for (int j = 1; j < VPT; ++j) tmax = fmaxf(tmax, vmax[j]);
+        const float tmax = largest_of<T, VPT>(q);
+        m = fmaxf(m, tmax);
         bool raise = false;
         if (p.M > 0) {
-            best = fmaxf(best, tmax);
             raise = (tile & (tile + 1)) == 0;   // tiles 0, 1, 3, 7, ... raise the threshold
             ++tile;
-            if (raise) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr);
+            if (raise) rank_groups(m > -INFINITY ? ordered(m == 0.f ? 0.f : m) : 0u, p.M, sm.group, &sm.thr);
         }
-        sum.raise(tmax, p.mul);
-        // (the maximum is taken off before the product: z log2 e alone would overflow at the
-        // type's lowest values)
-        const float shift = sum.m == -INFINITY ? 0.f : sum.m;
-        const uint64_t off2 = f2_pack(-shift, -shift), mul2 = f2_pack(p.mul, p.mul);
+        // (of a maximum that is not usual only rounding errors would be left: its logits count as 0 until it is)
+        sum.raise(usual<T>(m) ? __fmul_rn(m, p.mul) : -INFINITY);
+        const float less = sum.r == -INFINITY ? 0.f : -sum.r;
+        const uint64_t less2 = f2_pack(less, less), mul2 = f2_pack(p.mul, p.mul);
         uint64_t s2 = f2_pack(0.f, 0.f), e2 = f2_pack(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
+            Pack<T, E> y = q[j];
+            if (ENT) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y.w[i] = floor_pair<T>(y.w[i]);
+            }
 #pragma unroll
             for (int i = 0; i < E; i += 2) {
+                const uint64_t u2 = f2_fma(f2_pack(y.get(i), y.get(i + 1)), mul2, less2);
                 float a, c;
-                f2_unpack(f2_mul(f2_add(f2_pack(q[j].get(i), q[j].get(i + 1)), off2), mul2), a, c);
+                f2_unpack(u2, a, c);
                 const uint64_t w2 = f2_pack(ex2(a), ex2(c));
                 s2 = f2_add(s2, w2);
-                if (ENT) e2 = f2_fma(w2, f2_pack(max_nan(a, kLeast), max_nan(c, kLeast)), e2);
+                if (ENT) e2 = f2_fma(w2, T::kIndex == Bf16::kIndex ? u2 : f2_pack(max_nan(a, kLeast), max_nan(c, kLeast)), e2);
             }
         }
         float a, c;
@@ -326,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             if (tmax >= least) {
 #pragma unroll
                 for (int j = 0; j < VPT; ++j)
-                    if (vmax[j] >= least) {
+                    if (Logits<T>::largest(q[j]) >= least) {
                         const int to = atomicAdd(&sm.hit_count, 1);
                         if (to < kHits) {
                             sm.data[to] = make_uint4(q[j].w[0], q[j].w[1], q[j].w[2], q[j].w[3]);
@@ -368,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
 
     // ---- the part's sums
     {
-        const float top = warp_max(sum.m);
-        sum.raise(top, p.mul);
+        const float top = warp_max(m);
+        sum.raise(usual<T>(top) ? __fmul_rn(top, p.mul) : -INFINITY);
         for (int o = 16; o > 0; o >>= 1) {
             sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
             if (ENT) sum.e += __shfl_xor_sync(0xffffffffu, sum.e, o);
@@ -380,24 +517,27 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             sm.red_e[warp] = sum.e;
         }
     }
-    if (p.M > 0) rank_groups(best > -INFINITY ? ordered(best == 0.f ? 0.f : best) : 0u, p.M, sm.group, &sm.thr_end);
+    if (p.M > 0) rank_groups(m > -INFINITY ? ordered(m == 0.f ? 0.f : m) : 0u, p.M, sm.group, &sm.thr_end);
     __syncthreads();
-    float m = -INFINITY, s = 0.f, e = 0.f;
+    float top = sm.red_m[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.red_m[w]);
+    if (!usual<T>(top) && fabsf(top) < INFINITY) sum_slowly<T>(p, sm, r.z, mask, begin, end, top);
     if (warp == 0) {
         Sums w;
-        w.m = lane < kWarps ? sm.red_m[lane] : -INFINITY;
+        const float mw = lane < kWarps ? sm.red_m[lane] : -INFINITY;
+        w.r = usual<T>(top) ? __fmul_rn(mw, p.mul) : mw;
         w.s = lane < kWarps ? sm.red_s[lane] : 0.f;
         w.e = lane < kWarps ? sm.red_e[lane] : 0.f;
-        m = w.m;
-        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        w.raise(m, p.mul);
-        s = w.s;
-        e = w.e;
+        w.raise(usual<T>(top) ? __fmul_rn(top, p.mul) : top);
         for (int o = 4; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-            e += __shfl_xor_sync(0xffffffffu, e, o);
+            w.s += __shfl_xor_sync(0xffffffffu, w.s, o);
+            w.e += __shfl_xor_sync(0xffffffffu, w.e, o);
         }
-        if (p.slices > 1 && lane == 0) p.stats[blockIdx.x] = make_float4(m, s, e, 0.f);
+        if (lane == 0) {
+            if (p.slices > 1) p.stats[blockIdx.x] = make_float4(top, w.s, w.e, 0.f);
+            else write_sums(p, sm, row, lse_part<T>(p, top), w.s, 0.f, w.e);
+        }
     }
 
     if (p.M > 0) {
@@ -431,14 +571,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             if (tid == 0) sm.count = 0;
             __syncthreads();
         }
-        rank_best(sm, n, p.M);
+        rank_best(sm, sm.buf, reinterpret_cast<uint64_t*>(sm.data), n, p.M);
         if (p.slices > 1) {
             uint64_t* out = p.keys + static_cast<int64_t>(blockIdx.x) * p.M;
             for (int i = tid; i < p.M; i += kThreads) out[i] = sm.best[i];
         }
     }
     if (p.slices == 1) {
-        write_row<T>(p, sm, row, m, s, 0.f, e);
+        if (p.M == 0) __syncthreads();
+        write_row<T>(p, sm, row, first);
         return;
     }
     __syncthreads();
@@ -447,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         if (sm.last) p.done[row] = 0;
     }
     __syncthreads();
-    if (sm.last) join_row<T>(p, sm, row);
+    if (sm.last) join_row<T>(p, sm, row, first);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -610,19 +751,20 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
                 out[i + 1] = q.get(i + 1);
                 f.two(out[i], out[i + 1]);
             }
-            if (mask) {
-                // (rows begin inside a vector: its columns may lie in two words)
-                const int b = static_cast<int>(c);
-                const uint32_t m0 = static_cast<uint32_t>(mask[b >> 5]), m1 = ((b + E - 1) >> 5) != (b >> 5) ? static_cast<uint32_t>(mask[(b >> 5) + 1]) : 0u;
-                const uint32_t allow = __funnelshift_r(m0, m1, b & 31);
-#pragma unroll
-                for (int i = 0; i < E; ++i) out[i] = allow >> i & 1u ? out[i] : 0.f;
-            }
             if (none) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) out[i] = 0.f;
             }
             q.set_all(out);
+            if (mask) {
+                // (rows begin inside a vector: its columns may lie in two words)
+                const int b = static_cast<int>(c);
+                const uint32_t m0 = static_cast<uint32_t>(mask[b >> 5]), m1 = ((b + E - 1) >> 5) != (b >> 5) ? static_cast<uint32_t>(mask[(b >> 5) + 1]) : 0u;
+                uint32_t keep[4];
+                spread_bits<T::kBytes>(__funnelshift_r(m0, m1, b & 31), keep);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q.w[i] &= keep[i];
+            }
             q.store(g + c);
         }
     }
