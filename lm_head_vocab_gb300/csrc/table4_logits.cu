@@ -24,21 +24,37 @@ namespace lmloss {
 namespace {
 
 constexpr int kMaxRows = 1024;               // hidden rows a launch
-constexpr int kMany = 64;                    // operand rows of a block's product at most
-constexpr int kWarpsOf = 28;                 // 16 warps widen, 8 add, then: table, hidden rows, a half's products each
-constexpr int kLogitsThreads = kWarpsOf * 32;
+constexpr int kMany = 128;                   // operand rows of a block's product at most
 constexpr uint32_t kHeader = 5120;           // barriers and factors, before the stages
-// Registers a thread of each part where 64 sums a thread do not fit an even share (72 of 896 threads):
-// in all what the block was launched with.
-constexpr int kWidenRegs = 64, kAddRegs = 104, kFewRegs = 40;
-static_assert(16 * kWidenRegs + 8 * kAddRegs + 4 * kFewRegs <= kWarpsOf * 72, "registers");
 
-// ------------------------------------------------------------- hidden rows
+// The two shapes of the kernel: N operand rows and HALVES x 128 rows of the table.  Up to 64 operand rows two halves
+// share what is copied of the hidden rows; 128 operand rows by one half widen a number half as often for each
+// of them (512 rows: 749 us by 64, twice 128 rows).
+template <int N>
+struct Shape {
+    static constexpr int kHalves = N > 64 ? 1 : 2;
+    static constexpr int kRows = 128 * kHalves;
+    static constexpr int kWidenWarps = 8 * kHalves;          // two groups, which take blocks of columns in turn
+    static constexpr int kAddWarps = 8;                      // of a half's rows, or of half the operand rows each
+    static constexpr int kFirstFew = kWidenWarps + kAddWarps;   // then: table, hidden rows, products of each half
+    static constexpr int kThreads = (kFirstFew + 4) * 32;
+    static constexpr int kSplit = kHalves == 1 ? 2 : 1;      // parts of the operand rows
+    static constexpr int kOwn = N / kSplit;                  // operand rows that a thread adds up
+    static constexpr int kSums = N >= 64 ? 2 : 4;            // D buffers
+    // registers a thread of each part where 64 sums do not fit an even share: in all what the block was launched with
+    static constexpr bool kUneven = kOwn == 64;
+    static constexpr int kEven = 65536 / kThreads / 8 * 8;
+    static constexpr int kWidenRegs = kHalves == 1 ? 72 : 64, kAddRegs = kHalves == 1 ? 136 : 104, kFewRegs = 40;
+    static_assert(!kUneven || kWidenWarps * kWidenRegs + kAddWarps * kAddRegs + 4 * kFewRegs <= kThreads / 32 * kEven, "registers");
+    static_assert(kHalves * 128 + kHalves * kSums * N <= 512, "tensor memory");
+};
+
 struct HiddenParams {
     const void* x;
     int64_t ld;
     int D, kblocks, groups, shift;
     int N, per;
+    int own;                     // operand rows of a thread's sums: pairs lie within them
     unsigned char* out;
     float* sums;
     float* inverse;
@@ -75,7 +91,9 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
     }
     const float scale = hidden_scale(top);
     if (tid == 0) p.inverse[row] = finite ? 1.f / scale : NAN;
-    const int block = row / p.per, n = row - block * p.per;
+    const int block = row / p.per;
+    int n = row - block * p.per;
+    if (kPair) n += n / (p.own / 2) * (p.own / 2);
     unsigned char* out = p.out + static_cast<int64_t>(block) * p.kblocks * (p.N * 256);
     float* sums = p.sums + static_cast<int64_t>(block) * p.groups * p.N;
     const int lanes = (1 << p.shift) / 8;
@@ -87,12 +105,12 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
         const int part = u & 7;
         auto place = [&](int r) { return reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u >> 3) * p.N + r) * 128 + ((part ^ (r & 7)) << 4)); };
         *place(n) = hi;
-        if (kPair) *place(n + p.N / 2) = lo;
+        if (kPair) *place(n + p.own / 2) = lo;
         group_sums<kPair>(lanes, sum, sum_lo);
         const int g = (8 * u) >> p.shift;
         if ((u & (lanes - 1)) == 0 && g < p.groups) {
             sums[static_cast<int64_t>(g) * p.N + n] = sum;
-            if (kPair) sums[static_cast<int64_t>(g) * p.N + n + p.N / 2] = sum_lo;
+            if (kPair) sums[static_cast<int64_t>(g) * p.N + n + p.own / 2] = sum_lo;
         }
     }
 }
@@ -109,19 +127,19 @@ struct __align__(16) LogitsBarriers {
 static_assert(sizeof(LogitsBarriers) <= kHeader, "head");
 
 template <int N>
-__global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
+__global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
 {
-    // tensor memory: A two buffers of 64 columns for each half, D kSums of N columns for each half
-    constexpr int kSums = N == 64 ? 2 : 4;
-    constexpr uint32_t kColumns = 512;
-    static_assert(256 + 2 * kSums * N <= kColumns, "tensor memory");
+    // tensor memory: A two buffers of 64 columns for each half, then D kSums of N columns for each half
+    using Sh = Shape<N>;
+    constexpr int kSums = Sh::kSums, kHalves = Sh::kHalves, kOwn = Sh::kOwn, kRows = Sh::kRows;
+    constexpr uint32_t kColumns = 512, kD = kHalves * 128;
     constexpr uint32_t kIdesc = mma_f16_idesc(N);
     constexpr uint32_t kXBytes = N * 256;
     extern __shared__ __align__(1024) unsigned char smem[];
     LogitsBarriers& b = *reinterpret_cast<LogitsBarriers*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
+    const StageLayout lay(kRows, p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
     const uint32_t xbase = base + kHeader + p.qstages * p.stage_bytes;
     const int gs = 1 << p.shift, per_stage = kStageCols >> p.shift;
     const int stages = (p.kblocks + 1) / 2;
@@ -130,23 +148,23 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_addr(&b.q_full[i]), 1);
-            mbar_init(smem_addr(&b.q_empty[i]), 24);
+            mbar_init(smem_addr(&b.q_empty[i]), Sh::kFirstFew);
             mbar_init(smem_addr(&b.x_full[i]), 1);
-            mbar_init(smem_addr(&b.x_empty[i]), 2);
+            mbar_init(smem_addr(&b.x_empty[i]), kHalves);
         }
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kHalves; ++h)
             for (int i = 0; i < 4; ++i) {
                 if (i < 2) {
                     mbar_init(smem_addr(&b.a_full[h][i]), 4);
                     mbar_init(smem_addr(&b.a_empty[h][i]), 1);
                 }
                 mbar_init(smem_addr(&b.d_full[h][i]), 1);
-                mbar_init(smem_addr(&b.d_empty[h][i]), 4);
+                mbar_init(smem_addr(&b.d_empty[h][i]), Sh::kAddWarps / kHalves);
             }
         b.failed = 0;
         fence_mbar_init();
     }
-    if (warp == 26) tmem_alloc(smem_addr(&b.tmem), kColumns);
+    if (warp == Sh::kFirstFew + 2) tmem_alloc(smem_addr(&b.tmem), kColumns);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -161,10 +179,10 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
         __syncwarp();
     };
 
-    if (warp < 16) {
+    if (warp < Sh::kWidenWarps) {
         // ---- widen: a thread a row of its half, every second block of columns
-        if (N == 64) reg_dealloc<kWidenRegs>();
-        const int group = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = tid & 255;
+        if (Sh::kUneven) reg_dealloc<Sh::kWidenRegs>();
+        const int group = warp / (4 * kHalves), half = (warp >> 2) % kHalves, quarter = warp & 3, row = tid % kRows;
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128 + group * 64;
         Ring q;
         uint32_t parity = 1;   // of the group's buffer
@@ -205,31 +223,32 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
             }
         }
         wait(b.a_empty[half][group], parity);   // the products have read it: nothing arrives after the block's end
-    } else if (warp < 24) {
+    } else if (warp < Sh::kFirstFew) {
         // ---- add the groups' sums
-        if (N == 64) reg_alloc<kAddRegs>();
-        const int half = (warp >> 2) & 1, quarter = warp & 3, row = tid & 255;
-        const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 + half * (kSums * N);
+        if (Sh::kUneven) reg_alloc<Sh::kAddRegs>();
+        const int which = (warp - Sh::kWidenWarps) >> 2, quarter = warp & 3;
+        const int half = kHalves == 2 ? which : 0, own0 = kHalves == 2 ? 0 : which * kOwn, row = half * 128 + quarter * 32 + lane;
+        const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kD + half * (kSums * N) + own0;
         Ring q, d;
         bool waited = false;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
-            uint64_t acc[N / 2];
+            uint64_t acc[kOwn / 2];
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) acc[i] = f2_pack(0.f, 0.f);
+            for (int i = 0; i < kOwn / 2; ++i) acc[i] = f2_pack(0.f, 0.f);
             for (int st = 0; st < stages; ++st) {
                 wait(b.q_full[q.slot], q.parity);
                 const unsigned char* const stage = smem + kHeader + q.slot * p.stage_bytes;
                 const int n = min(per_stage, p.groups - st * per_stage);
                 for (int g = 0; g < n; ++g) {
-                    const float s = widen_any(stage + lay.scales, p.scale_dtype, g * kTile + row);
-                    const float z = p.zeros ? -static_cast<float>((stage + lay.zeros)[g * kTile + row]) : -8.f;
+                    const float s = widen_any(stage + lay.scales, p.scale_dtype, g * kRows + row);
+                    const float z = p.zeros ? -static_cast<float>((stage + lay.zeros)[g * kRows + row]) : -8.f;
                     const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z);
-                    const ulonglong2* const sums = reinterpret_cast<const ulonglong2*>(stage + lay.sums + g * (N * 4));
+                    const ulonglong2* const sums = reinterpret_cast<const ulonglong2*>(stage + lay.sums + g * (N * 4) + own0 * 4);
                     wait(b.d_full[half][d.slot], d.parity);
                     tcgen05_after_sync();
 #pragma unroll
-                    for (int c = 0; c < N; c += 16) {
+                    for (int c = 0; c < kOwn; c += 16) {
                         float f[16];
                         tmem_load16(from + d.slot * N + c, f);
                         tmem_wait_load(f);
@@ -258,10 +277,11 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
                 __syncwarp();
                 waited = true;
             }
-            const int64_t v = static_cast<int64_t>(vt) * kTile + row;
+            const int64_t v = static_cast<int64_t>(vt) * kRows + row;
             if (v < p.V) {
-                const int t0 = tb * p.per;
-                const int rows = min(p.per, p.T - t0);
+                // this thread's hidden rows of the block's
+                const int own = p.pairs ? kOwn / 2 : kOwn, t0 = tb * p.per + own0 / kOwn * own;
+                const int rows = min(own, p.T - t0);
                 auto all = [&](auto type) {
                     using O = decltype(type);
                     typename O::raw* out = static_cast<typename O::raw*>(p.out) + static_cast<int64_t>(t0) * p.ld_out + v;
@@ -270,11 +290,11 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
                         out += p.ld_out;
                     };
 #pragma unroll
-                    for (int i = 0; i < N / 4; ++i) {
+                    for (int i = 0; i < kOwn / 4; ++i) {
                         float a, c, e, f;
                         f2_unpack(acc[i], a, c);
                         if (p.pairs) {
-                            f2_unpack(acc[i + N / 4], e, f);
+                            f2_unpack(acc[i + kOwn / 4], e, f);
                             a = fmaf(e, 1.f / 2048.f, a);
                             c = fmaf(f, 1.f / 2048.f, c);
                         }
@@ -283,7 +303,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
                     }
                     if (!p.pairs) {
 #pragma unroll
-                        for (int i = N / 4; i < N / 2; ++i) {
+                        for (int i = kOwn / 4; i < kOwn / 2; ++i) {
                             float a, c;
                             f2_unpack(acc[i], a, c);
                             put(2 * i, a);
@@ -299,8 +319,8 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
             }
         }
     } else {
-        if (N == 64) reg_dealloc<kFewRegs>();
-        if (warp == 24) {
+        if (Sh::kUneven) reg_dealloc<Sh::kFewRegs>();
+        if (warp == Sh::kFirstFew) {
             // ---- the table.  Its first stages go out before the hidden rows' sums are waited for.
             if (lane == 0) {
                 const int64_t mine = static_cast<int64_t>((tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * stages;
@@ -315,7 +335,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
                 auto table = [&](int slot) {
                     const uint32_t bar = smem_addr(&b.q_full[slot]);
                     mbar_arrive_expect_tx(bar, lay.copied + min(per_stage, p.groups - st * per_stage) * (N * 4));
-                    copy_table(p, lay, maps, st, tile / p.tblocks * kTile, base + kHeader + slot * p.stage_bytes, bar);
+                    copy_table(p, lay, maps, st, tile / p.tblocks * kRows, base + kHeader + slot * p.stage_bytes, bar);
                 };
                 auto sums = [&](int slot) {   // the groups of a stage lie side by side
                     bulk_load(base + kHeader + slot * p.stage_bytes + lay.sums,
@@ -337,7 +357,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
                 }
             }
             __syncwarp();
-        } else if (warp == 25) {
+        } else if (warp == Sh::kFirstFew + 1) {
             // ---- the hidden rows
             if (lane == 0) {
                 grid_dep_wait();
@@ -356,11 +376,11 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
                 for (int i = 0; i < p.xstages; ++i, x.next(p.xstages)) wait_one(b.x_empty[x.slot], x.parity ^ 1u);
             }
             __syncwarp();
-        } else {
+        } else if (warp - (Sh::kFirstFew + 2) < kHalves) {
             // ---- the products of one half.  (One warp for both was late: its instructions took 1500 clocks a block
             // of columns.)
             const uint32_t leader = elect_one();
-            const int half = warp - 26;
+            const int half = warp - (Sh::kFirstFew + 2);
             auto multiply = [&](auto count) {
                 constexpr int kSteps = decltype(count)::value;   // a group's, 16 columns each
                 constexpr int kGroups = 8 / kSteps;              // of a block of columns
@@ -377,7 +397,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
                             if (g >= left) break;
                             wait(b.d_empty[half][d.slot], d.parity ^ 1u);
                             tcgen05_after_sync();
-                            const uint32_t to = tmem + 256 + (half * kSums + d.slot) * N;
+                            const uint32_t to = tmem + kD + (half * kSums + d.slot) * N;
 #pragma unroll
                             for (int k = 0; k < kSteps; ++k) {
                                 const int step = g * kSteps + k;   // 64 columns lie in one run of N rows
@@ -410,7 +430,7 @@ __global__ void __launch_bounds__(kLogitsThreads, 1) logits_kernel(const __grid_
         }
     }
     __syncthreads();
-    if (warp == 26) tmem_free(tmem, kColumns);
+    if (warp == Sh::kFirstFew + 2) tmem_free(tmem, kColumns);
 }
 
 // ------------------------------------------------------------------- host
@@ -469,7 +489,7 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-bool table_maps(const lmloss_table4& t, TableMaps* maps)
+bool table_maps(const lmloss_table4& t, int rows, TableMaps* maps)
 {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
@@ -483,20 +503,20 @@ bool table_maps(const lmloss_table4& t, TableMaps* maps)
     };
     const int es = float_bytes(t.scale_dtype), n = kStageCols / t.group;
     const int64_t G = (t.D + t.group - 1) / t.group;
-    return map(&maps->values, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.values, (t.D + 1) / 2, t.V, t.ld_values, 128, kTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
-           map(&maps->scales, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, t.scales, t.V, G, t.ld_scales * es, kTile,
+    return map(&maps->values, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.values, (t.D + 1) / 2, t.V, t.ld_values, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           map(&maps->scales, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, t.scales, t.V, G, t.ld_scales * es, rows,
                n, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-           (!t.zeros || map(&maps->zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.zeros, t.V, G, t.ld_zeros, kTile, n, CU_TENSOR_MAP_SWIZZLE_NONE));
+           (!t.zeros || map(&maps->zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.zeros, t.V, G, t.ld_zeros, rows, n, CU_TENSOR_MAP_SWIZZLE_NONE));
 }
 
 template <int N>
 lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    const StageLayout lay(p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
+    const StageLayout lay(Shape<N>::kRows, p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
     p.stage_bytes = lay.bytes;
-    p.xstages = N == 64 ? 4 : 6;
+    p.xstages = N == 128 ? 3 : (N == 64 ? 4 : 6);
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHeader - p.xstages * N * 256) / lay.bytes);
-    constexpr uint32_t bit = 1u << (N == 16 ? 17 : (N == 32 ? 18 : 19));
+    constexpr uint32_t bit = 1u << (N == 16 ? 17 : (N == 32 ? 18 : (N == 64 ? 19 : 20)));
     if (!(h->limits_raised & bit)) {
         if (cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
             cudaGetLastError();
@@ -506,7 +526,7 @@ lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vo
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.vtiles) * p.tblocks, h->num_sms)));
-    cfg.blockDim = dim3(kLogitsThreads);
+    cfg.blockDim = dim3(Shape<N>::kThreads);
     cfg.dynamicSmemBytes = kHeader + p.qstages * lay.bytes + p.xstages * N * 256;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
@@ -552,8 +572,6 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
     if (w.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
-    TableMaps maps{};
-    if (!table_maps(a->table, &maps)) return LMLOSS_ERR_CUDA;
     for (int64_t t0 = 0; t0 < a->T; t0 += kMaxRows) {
         const int T = static_cast<int>(std::min<int64_t>(a->T - t0, kMaxRows));
         LogitsParams p{};
@@ -571,7 +589,6 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.groups = static_cast<int>((a->table.D + a->table.group - 1) / a->table.group);
         p.kblocks = static_cast<int>(kblocks_of(a->table.D));
         p.T = T;
-        p.vtiles = static_cast<int>((a->table.V + kTile - 1) / kTile);
         p.pairs = pairs;
         p.hidden = static_cast<const unsigned char*>(a->hidden) + t0 * a->ld_hidden * float_bytes(a->hidden_dtype);
         p.ld_hidden = a->ld_hidden;
@@ -581,7 +598,13 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.out_dtype = a->logits_dtype;
         p.scale = a->scale;
         p.err = h->err;
-        if (few_rows_fit(p)) {
+        const int operands = T * (pairs ? 2 : 1);
+        const bool few = few_rows_fit(p);
+        const int rows = few || operands <= 64 ? 256 : 128;
+        p.vtiles = static_cast<int>((a->table.V + rows - 1) / rows);
+        TableMaps maps{};
+        if (!table_maps(a->table, rows, &maps)) return LMLOSS_ERR_CUDA;
+        if (few) {
             st = launch_few_rows(p, maps, h, stream);
         } else {
             HiddenParams x{};
@@ -591,9 +614,9 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
             x.kblocks = p.kblocks;
             x.groups = p.groups;
             x.shift = p.shift;
-            const int operands = T * (pairs ? 2 : 1);
-            x.N = p.N = operands <= 16 ? 16 : (operands <= 32 ? 32 : kMany);
+            x.N = p.N = operands <= 16 ? 16 : (operands <= 32 ? 32 : (operands <= 64 ? 64 : kMany));
             x.per = p.per = pairs ? p.N / 2 : p.N;
+            x.own = p.N == kMany ? Shape<kMany>::kOwn : p.N;
             x.out = h->ws;
             x.sums = reinterpret_cast<float*>(h->ws + w.sums);
             x.inverse = reinterpret_cast<float*>(h->ws + w.inverse);
@@ -608,7 +631,8 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
             }
             if ((st = vocab_launch_err()) == LMLOSS_OK)
                 st = p.N == 16 ? launch_many_rows<16>(p, maps, h, stream)
-                               : (p.N == 32 ? launch_many_rows<32>(p, maps, h, stream) : launch_many_rows<kMany>(p, maps, h, stream));
+                               : (p.N == 32 ? launch_many_rows<32>(p, maps, h, stream)
+                                             : (p.N == 64 ? launch_many_rows<64>(p, maps, h, stream) : launch_many_rows<kMany>(p, maps, h, stream)));
         }
         if (st != LMLOSS_OK) return st;
     }

@@ -9,7 +9,6 @@
 
 namespace lmloss {
 
-constexpr int kTile = 256;                   // rows of the table a block takes at once
 constexpr int kStageCols = 256;              // columns of the table a stage holds
 constexpr int kBlockCols = 128;              // columns that hidden rows are laid out by
 constexpr int kMaxStages = 8;
@@ -163,22 +162,22 @@ struct Ring {
     }
 };
 
-// Where a stage's parts begin, and what they hold: values [256 rows][128 bytes, 16-byte parts at
-// (part ^ row % 8)], scales and zeros [groups of the stage][256 rows], sums [groups][N] (where they are
+// Where a stage's parts begin, and what they hold: values [rows][128 bytes, 16-byte parts at
+// (part ^ row % 8)], scales and zeros [groups of the stage][rows], sums [groups][N] (where they are
 // copied by stages).
 struct StageLayout {
     uint32_t scales, zeros, sums, copied, bytes;   // copied: of values, scales and zeros
-    __host__ __device__ StageLayout(int shift, int scale_bytes, bool has_zeros, uint32_t sums_a_group)
+    __host__ __device__ StageLayout(int rows, int shift, int scale_bytes, bool has_zeros, uint32_t sums_a_group)
     {
         const int n = kStageCols >> shift;
-        scales = kTile * 128;
-        zeros = scales + n * kTile * scale_bytes;
-        sums = copied = zeros + (has_zeros ? n * kTile : 0);
+        scales = rows * 128;
+        zeros = scales + n * rows * scale_bytes;
+        sums = copied = zeros + (has_zeros ? n * rows : 0);
         bytes = (sums + n * sums_a_group + 1023) / 1024 * 1024;
     }
 };
 
-// A table's parts as tiles: [V, D / 2 bytes] by 256 x 128, [G, V] by a stage's groups x 256.  What lies
+// A table's parts as tiles: [V, D / 2 bytes] by rows x 128, [G, V] by a stage's groups x rows.  What lies
 // outside is 0.
 struct TableMaps {
     CUtensorMap values, scales, zeros;
