@@ -52,11 +52,10 @@ struct Shape {
 struct HiddenParams {
     const void* x;
     int64_t ld;
-    int D, kblocks, groups, shift;
+    int D, kblocks;
     int N, per;
     int own;                     // operand rows of a thread's sums: pairs lie within them
     unsigned char* out;
-    float* sums;
     float* inverse;
 };
 
@@ -95,8 +94,6 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
     int n = row - block * p.per;
     if (kPair) n += n / (p.own / 2) * (p.own / 2);
     unsigned char* out = p.out + static_cast<int64_t>(block) * p.kblocks * (p.N * 256);
-    float* sums = p.sums + static_cast<int64_t>(block) * p.groups * p.N;
-    const int lanes = (1 << p.shift) / 8;
     for (int u = tid; u < p.kblocks * 16; u += 256) {
         uint4 hi, lo;
         float sum, sum_lo;
@@ -106,12 +103,6 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
         auto place = [&](int r) { return reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u >> 3) * p.N + r) * 128 + ((part ^ (r & 7)) << 4)); };
         *place(n) = hi;
         if (kPair) *place(n + p.own / 2) = lo;
-        group_sums<kPair>(lanes, sum, sum_lo);
-        const int g = (8 * u) >> p.shift;
-        if ((u & (lanes - 1)) == 0 && g < p.groups) {
-            sums[static_cast<int64_t>(g) * p.N + n] = sum;
-            if (kPair) sums[static_cast<int64_t>(g) * p.N + n + p.own / 2] = sum_lo;
-        }
     }
 }
 
@@ -139,7 +130,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
     LogitsBarriers& b = *reinterpret_cast<LogitsBarriers*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const StageLayout lay(kRows, p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
+    const StageLayout lay(kRows, p.shift, p.scale_bytes, p.zeros != nullptr);
     const uint32_t xbase = base + kHeader + p.qstages * p.stage_bytes;
     const int gs = 1 << p.shift, per_stage = kStageCols >> p.shift;
     const int stages = (p.kblocks + 1) / 2;
@@ -191,6 +182,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
             for (int st = 0; st < stages; ++st) {
                 wait(b.q_full[q.slot], q.parity);
                 const unsigned char* const stage = smem + kHeader + q.slot * p.stage_bytes;
+                const unsigned char* const zeros = stage + lay.zeros;
                 const int blocks = min(2, p.kblocks - 2 * st);
                 for (int kb = 0; kb < blocks; ++kb, turn ^= 1) {
                     if (turn != group) continue;
@@ -204,10 +196,14 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                         uint32_t r[32];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            widen_word(w[part * 2 + i].x, r + 16 * i);
-                            widen_word(w[part * 2 + i].y, r + 16 * i + 4);
-                            widen_word(w[part * 2 + i].z, r + 16 * i + 8);
-                            widen_word(w[part * 2 + i].w, r + 16 * i + 12);
+                            const int unit = part * 2 + i;   // 32 columns
+                            float z = 8.f;
+                            if (p.zeros) z = static_cast<float>(zeros[(((kb * 4 + unit) * 32) >> p.shift) * kRows + row]);
+                            const __half2 z1 = __float2half2_rn(z * 0x1p-24f), z16 = __float2half2_rn(z * 0x1p-20f);
+                            widen_word(w[unit].x, z1, z16, r + 16 * i);
+                            widen_word(w[unit].y, z1, z16, r + 16 * i + 4);
+                            widen_word(w[unit].z, z1, z16, r + 16 * i + 8);
+                            widen_word(w[unit].w, z1, z16, r + 16 * i + 12);
                         }
                         tmem_store32(to + part * 32, r);
                     }
@@ -242,9 +238,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                 const int n = min(per_stage, p.groups - st * per_stage);
                 for (int g = 0; g < n; ++g) {
                     const float s = widen_any(stage + lay.scales, p.scale_dtype, g * kRows + row);
-                    const float z = p.zeros ? -static_cast<float>((stage + lay.zeros)[g * kRows + row]) : -8.f;
-                    const uint64_t s2 = f2_pack(s, s), z2 = f2_pack(z, z);
-                    const ulonglong2* const sums = reinterpret_cast<const ulonglong2*>(stage + lay.sums + g * (N * 4) + own0 * 4);
+                    const uint64_t s2 = f2_pack(s, s);
                     wait(b.d_full[half][d.slot], d.parity);
                     tcgen05_after_sync();
 #pragma unroll
@@ -253,12 +247,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                         tmem_load16(from + d.slot * N + c, f);
                         tmem_wait_load(f);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const ulonglong2 x = sums[(c + i) / 4];
-                            uint64_t& a0 = acc[(c + i) / 2];
-                            uint64_t& a1 = acc[(c + i) / 2 + 1];
-                            a0 = f2_fma(s2, f2_fma(z2, x.x, f2_pack(f[i], f[i + 1])), a0);
-                            a1 = f2_fma(s2, f2_fma(z2, x.y, f2_pack(f[i + 2], f[i + 3])), a1);
+                        for (int i = 0; i < 16; i += 2) {
+                            uint64_t& a = acc[(c + i) / 2];
+                            a = f2_fma(s2, f2_pack(f[i], f[i + 1]), a);
                         }
                     }
                     tcgen05_before_sync();
@@ -321,40 +312,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
     } else {
         if (Sh::kUneven) reg_dealloc<Sh::kFewRegs>();
         if (warp == Sh::kFirstFew) {
-            // ---- the table.  Its first stages go out before the hidden rows' sums are waited for.
+            // ---- the table
             if (lane == 0) {
-                const int64_t mine = static_cast<int64_t>((tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * stages;
-                const int early = static_cast<int>(min(mine, static_cast<int64_t>(p.qstages)));
-                int tile = blockIdx.x, st = 0;
-                auto step = [&] {
-                    if (++st == stages) {
-                        st = 0;
-                        tile += gridDim.x;
-                    }
-                };
-                auto table = [&](int slot) {
-                    const uint32_t bar = smem_addr(&b.q_full[slot]);
-                    mbar_arrive_expect_tx(bar, lay.copied + min(per_stage, p.groups - st * per_stage) * (N * 4));
-                    copy_table(p, lay, maps, st, tile / p.tblocks * kRows, base + kHeader + slot * p.stage_bytes, bar);
-                };
-                auto sums = [&](int slot) {   // the groups of a stage lie side by side
-                    bulk_load(base + kHeader + slot * p.stage_bytes + lay.sums,
-                              p.sums + (static_cast<int64_t>(tile % p.tblocks) * p.groups + st * per_stage) * N,
-                              min(per_stage, p.groups - st * per_stage) * (N * 4), smem_addr(&b.q_full[slot]));
-                };
-                for (int i = 0; i < early; ++i, step()) table(i);
-                grid_dep_wait();
-                tile = blockIdx.x;
-                st = 0;
-                for (int i = 0; i < early; ++i, step()) sums(i);
                 Ring q;
-                q.slot = early == p.qstages ? 0 : early;
-                for (int64_t i = early; i < mine; ++i, step()) {
-                    wait_one(b.q_empty[q.slot], q.parity);   // the stage before has been read
-                    table(q.slot);
-                    sums(q.slot);
-                    q.next(p.qstages);
-                }
+                for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x)
+                    for (int st = 0; st < stages; ++st) {
+                        wait_one(b.q_empty[q.slot], q.parity ^ 1u);
+                        const uint32_t bar = smem_addr(&b.q_full[q.slot]);
+                        mbar_arrive_expect_tx(bar, lay.copied);
+                        copy_table(p, lay, maps, st, tile / p.tblocks * kRows, base + kHeader + q.slot * p.stage_bytes, bar);
+                        q.next(p.qstages);
+                    }
             }
             __syncwarp();
         } else if (warp == Sh::kFirstFew + 1) {
@@ -454,18 +422,16 @@ lmloss_status check_logits(const lmloss_table4_logits_args* a, bool pointers)
 
 int64_t kblocks_of(int64_t D) { return (D + kBlockCols - 1) / kBlockCols; }
 
-// Workspace of a launch's hidden rows: the operand rows padded to whole blocks, as fp16 and as sums of groups
-// of any size, and a factor for each.
+// Workspace of a launch's hidden rows: the operand rows as fp16, padded to whole blocks, and a factor for each.
 struct HiddenSpace {
-    size_t sums, inverse, total;
+    size_t inverse, total;
 };
 HiddenSpace hidden_space(int64_t T, int64_t D, bool pairs)
 {
     const int64_t rows = std::min<int64_t>(T, kMaxRows) * (pairs ? 2 : 1);
     const int64_t padded = (rows + kMany - 1) / kMany * kMany, k = kblocks_of(D);
     HiddenSpace w{};
-    w.sums = vocab_align(static_cast<size_t>(padded * k * kBlockCols * 2));
-    w.inverse = w.sums + vocab_align(static_cast<size_t>(padded * k * (kBlockCols / 32) * 4));
+    w.inverse = vocab_align(static_cast<size_t>(padded * k * kBlockCols * 2));
     w.total = w.inverse + vocab_align(static_cast<size_t>(rows) * 4);
     return w;
 }
@@ -512,7 +478,7 @@ bool table_maps(const lmloss_table4& t, int rows, TableMaps* maps)
 template <int N>
 lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    const StageLayout lay(Shape<N>::kRows, p.shift, p.scale_bytes, p.zeros != nullptr, N * 4);
+    const StageLayout lay(Shape<N>::kRows, p.shift, p.scale_bytes, p.zeros != nullptr);
     p.stage_bytes = lay.bytes;
     p.xstages = N == 128 ? 3 : (N == 64 ? 4 : 6);
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHeader - p.xstages * N * 256) / lay.bytes);
@@ -612,17 +578,13 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
             x.ld = p.ld_hidden;
             x.D = p.D;
             x.kblocks = p.kblocks;
-            x.groups = p.groups;
-            x.shift = p.shift;
             x.N = p.N = operands <= 16 ? 16 : (operands <= 32 ? 32 : (operands <= 64 ? 64 : kMany));
             x.per = p.per = pairs ? p.N / 2 : p.N;
             x.own = p.N == kMany ? Shape<kMany>::kOwn : p.N;
             x.out = h->ws;
-            x.sums = reinterpret_cast<float*>(h->ws + w.sums);
             x.inverse = reinterpret_cast<float*>(h->ws + w.inverse);
             p.tblocks = (T + p.per - 1) / p.per;
             p.x = x.out;
-            p.sums = x.sums;
             p.inverse = x.inverse;
             switch (a->hidden_dtype) {
             case LMLOSS_BF16: hidden_kernel<Bf16><<<T, 256, 0, stream>>>(x); break;

@@ -33,7 +33,6 @@ struct LogitsParams {
     int vtiles;
     int pairs;                   // fp32: operand rows 0 .. N / 2 - 1 the upper parts, the others the lower ones times 2^11
     const unsigned char* x;      // [tblocks][kblocks][N * 256 bytes]: the hidden rows as fp16
-    const float* sums;           // [tblocks][groups][N]: sums of their groups, as the products count them
     const float* inverse;        // [T] by which a row's sums are multiplied; NaN: the row is not finite
     const void* hidden;          // the rows as they came
     int64_t ld_hidden;
@@ -49,8 +48,7 @@ struct LogitsParams {
 
 // A word's eight numbers as fp16 pairs in the order 0 4 1 5 2 6 3 7.  The bits of a number in an fp16's low
 // bits ARE q 2^-24, a subnormal; four bits further up q 2^-20.  So the odd places' hidden values are laid out
-// divided by 16, and five operations widen eight numbers.  (q - z by magic numbers: nine.)  The zero points
-// are taken off the sums: sum (q - z) x = sum q x - z sum x.
+// divided by 16, and five operations widen eight numbers.  (By magic numbers: nine.)
 __device__ __forceinline__ void widen_word(uint32_t w, uint32_t* out)
 {
     const uint32_t w8 = w >> 8;
@@ -58,6 +56,16 @@ __device__ __forceinline__ void widen_word(uint32_t w, uint32_t* out)
     out[1] = w & 0x00f000f0u;
     out[2] = w8 & 0x000f000fu;
     out[3] = w8 & 0x00f000f0u;
+}
+// The same less a zero point, z 2^-24 and z 2^-20 twice each: exact.
+__device__ __forceinline__ void widen_word(uint32_t w, __half2 z, __half2 z16, uint32_t* out)
+{
+    widen_word(w, out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(out + i), i & 1 ? z16 : z);
+        out[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
 }
 
 __device__ __forceinline__ float widen_any(const void* base, int dtype, int64_t i)
@@ -163,17 +171,16 @@ struct Ring {
 };
 
 // Where a stage's parts begin, and what they hold: values [rows][128 bytes, 16-byte parts at
-// (part ^ row % 8)], scales and zeros [groups of the stage][rows], sums [groups][N] (where they are
-// copied by stages).
+// (part ^ row % 8)], scales and zeros [groups of the stage][rows].
 struct StageLayout {
-    uint32_t scales, zeros, sums, copied, bytes;   // copied: of values, scales and zeros
-    __host__ __device__ StageLayout(int rows, int shift, int scale_bytes, bool has_zeros, uint32_t sums_a_group)
+    uint32_t scales, zeros, copied, bytes;
+    __host__ __device__ StageLayout(int rows, int shift, int scale_bytes, bool has_zeros)
     {
         const int n = kStageCols >> shift;
         scales = rows * 128;
         zeros = scales + n * rows * scale_bytes;
-        sums = copied = zeros + (has_zeros ? n * rows : 0);
-        bytes = (sums + n * sums_a_group + 1023) / 1024 * 1024;
+        copied = zeros + (has_zeros ? n * rows : 0);
+        bytes = (copied + 1023) / 1024 * 1024;
     }
 };
 

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     RowsHead& b = *reinterpret_cast<RowsHead*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const StageLayout lay(kTile, p.shift, p.scale_bytes, p.zeros != nullptr, 0);
+    const StageLayout lay(kTile, p.shift, p.scale_bytes, p.zeros != nullptr);
     const RowsLayout rl(N, p.kblocks, p.groups);
     unsigned char* const rows = smem + kHead + p.qstages * p.stage_bytes;
     const int stages = (p.kblocks + 1) / 2;
@@ -273,7 +273,7 @@ int columns_for(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
 template <int NT, int GROUP>
 lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    const StageLayout lay(kTile, p.shift, p.scale_bytes, p.zeros != nullptr, 0);
+    const StageLayout lay(kTile, p.shift, p.scale_bytes, p.zeros != nullptr);
     const RowsLayout rl(8 * NT, p.kblocks, p.groups);
     p.stage_bytes = lay.bytes;
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHead - rl.bytes) / lay.bytes);
@@ -306,7 +306,7 @@ bool few_rows_fit(const LogitsParams& p)
     const int64_t rows = static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1), N = columns_for(rows);
     if (rows > kFewRows || N * p.kblocks * 256 > kMaxShared) return false;
     return kHead + RowsLayout(static_cast<int>(N), p.kblocks, p.groups).bytes +
-               2 * StageLayout(kTile, p.shift, p.scale_bytes, p.zeros != nullptr, 0).bytes <= kMaxShared;
+               2 * StageLayout(kTile, p.shift, p.scale_bytes, p.zeros != nullptr).bytes <= kMaxShared;
 }
 
 lmloss_status launch_few_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
