@@ -27,26 +27,26 @@ constexpr int kMaxRows = 1024;               // hidden rows a launch
 constexpr int kMany = 128;                   // operand rows of a block's product at most
 constexpr uint32_t kHeader = 5120;           // barriers and factors, before the stages
 
-// The two shapes of the kernel: N operand rows and HALVES x 128 rows of the table.  Up to 64 operand rows two halves
-// share what is copied of the hidden rows; 128 operand rows by one half widen a number half as often for each
-// of them (512 rows: 749 us by 64, twice 128 rows).
+constexpr int kRows = 128;                   // rows of the table a block takes at once
+
+// The kernel's shapes, by N operand rows.  Up to 32 two blocks share an SM.
 template <int N>
 struct Shape {
-    static constexpr int kHalves = N > 64 ? 1 : 2;
-    static constexpr int kRows = 128 * kHalves;
-    static constexpr int kWidenWarps = 8 * kHalves;          // two groups, which take blocks of columns in turn
-    static constexpr int kAddWarps = 8;                      // of a half's rows, or of half the operand rows each
-    static constexpr int kFirstFew = kWidenWarps + kAddWarps;   // then: table, hidden rows, products of each half
-    static constexpr int kThreads = (kFirstFew + 4) * 32;
-    static constexpr int kSplit = kHalves == 1 ? 2 : 1;      // parts of the operand rows
+    static constexpr int kBlocks = N > 32 ? 1 : 2;           // of an SM
+    static constexpr int kWidenWarps = 8;                    // two groups, which take blocks of columns in turn
+    static constexpr int kSplit = N > 32 ? 2 : 1;            // parts of the operand rows
     static constexpr int kOwn = N / kSplit;                  // operand rows that a thread adds up
-    static constexpr int kSums = N >= 64 ? 2 : 4;            // D buffers
+    static constexpr int kAddWarps = 4 * kSplit;
+    static constexpr int kFirstFew = kWidenWarps + kAddWarps;   // then: table, hidden rows, products of either turn
+    static constexpr int kThreads = (kFirstFew + 4) * 32;
+    // tensor memory: A of either turn, D kSums of either turn, then sums on their way out
+    static constexpr int kSums = N == 64 || N == 16 ? 2 : 1;
+    static constexpr uint32_t kD = 128, kOut = kD + 2 * kSums * N, kColumns = N > 32 ? 512 : 256;
+    static_assert(kOut + N <= kColumns, "tensor memory");
     // registers a thread of each part where 64 sums do not fit an even share: in all what the block was launched with
     static constexpr bool kUneven = kOwn == 64;
-    static constexpr int kEven = 65536 / kThreads / 8 * 8;
-    static constexpr int kWidenRegs = kHalves == 1 ? 72 : 64, kAddRegs = kHalves == 1 ? 136 : 104, kFewRegs = 40;
-    static_assert(!kUneven || kWidenWarps * kWidenRegs + kAddWarps * kAddRegs + 4 * kFewRegs <= kThreads / 32 * kEven, "registers");
-    static_assert(kHalves * 128 + kHalves * kSums * N <= 512, "tensor memory");
+    static constexpr int kWidenRegs = 72, kAddRegs = 136, kFewRegs = 40;
+    static_assert(!kUneven || kWidenWarps * kWidenRegs + kAddWarps * kAddRegs + 4 * kFewRegs <= kThreads / 32 * (65536 / kThreads / 8 * 8), "registers");
 };
 
 struct HiddenParams {
@@ -110,20 +110,20 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
 // A block's head: barriers, and the factors of all hidden rows.
 struct __align__(16) LogitsBarriers {
     uint64_t q_full[kMaxStages], q_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages];
-    uint64_t a_full[2][2], a_empty[2][2], d_full[2][4], d_empty[2][4];
+    uint64_t a_full[2], a_empty[2], d_full[2][2], d_empty[2][2];   // of either turn
     uint32_t tmem;
     int failed;
+    int odd;                     // whether any row is not finite
     float factor[kMaxRows];      // NaN: the row is not finite
 };
 static_assert(sizeof(LogitsBarriers) <= kHeader, "head");
 
 template <int N>
-__global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
+__global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
+    logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
 {
-    // tensor memory: A two buffers of 64 columns for each half, then D kSums of N columns for each half
     using Sh = Shape<N>;
-    constexpr int kSums = Sh::kSums, kHalves = Sh::kHalves, kOwn = Sh::kOwn, kRows = Sh::kRows;
-    constexpr uint32_t kColumns = 512, kD = kHalves * 128;
+    constexpr int kSums = Sh::kSums, kOwn = Sh::kOwn;
     constexpr uint32_t kIdesc = mma_f16_idesc(N);
     constexpr uint32_t kXBytes = N * 256;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -141,21 +141,21 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
             mbar_init(smem_addr(&b.q_full[i]), 1);
             mbar_init(smem_addr(&b.q_empty[i]), Sh::kFirstFew);
             mbar_init(smem_addr(&b.x_full[i]), 1);
-            mbar_init(smem_addr(&b.x_empty[i]), kHalves);
+            mbar_init(smem_addr(&b.x_empty[i]), 1);
         }
-        for (int h = 0; h < kHalves; ++h)
-            for (int i = 0; i < 4; ++i) {
-                if (i < 2) {
-                    mbar_init(smem_addr(&b.a_full[h][i]), 4);
-                    mbar_init(smem_addr(&b.a_empty[h][i]), 1);
-                }
-                mbar_init(smem_addr(&b.d_full[h][i]), 1);
-                mbar_init(smem_addr(&b.d_empty[h][i]), Sh::kAddWarps / kHalves);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&b.a_full[i]), 4);
+            mbar_init(smem_addr(&b.a_empty[i]), 1);
+            for (int d = 0; d < 2; ++d) {
+                mbar_init(smem_addr(&b.d_full[i][d]), 1);
+                mbar_init(smem_addr(&b.d_empty[i][d]), Sh::kAddWarps);
             }
+        }
         b.failed = 0;
+        b.odd = 0;
         fence_mbar_init();
     }
-    if (warp == Sh::kFirstFew + 2) tmem_alloc(smem_addr(&b.tmem), kColumns);
+    if (warp == Sh::kFirstFew + 2) tmem_alloc(smem_addr(&b.tmem), Sh::kColumns);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -171,12 +171,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
     };
 
     if (warp < Sh::kWidenWarps) {
-        // ---- widen: a thread a row of its half, every second block of columns
+        // ---- widen: a thread a row, every second block of columns
         if (Sh::kUneven) reg_dealloc<Sh::kWidenRegs>();
-        const int group = warp / (4 * kHalves), half = (warp >> 2) % kHalves, quarter = warp & 3, row = tid % kRows;
-        const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128 + group * 64;
+        const int mine = warp >> 2, row = tid & 127;
+        const uint32_t to = tmem + (static_cast<uint32_t>(warp & 3) << 21) + mine * 64;
         Ring q;
-        uint32_t parity = 1;   // of the group's buffer
+        uint32_t parity = 1;
         int turn = 0;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             for (int st = 0; st < stages; ++st) {
@@ -185,11 +185,11 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                 const unsigned char* const zeros = stage + lay.zeros;
                 const int blocks = min(2, p.kblocks - 2 * st);
                 for (int kb = 0; kb < blocks; ++kb, turn ^= 1) {
-                    if (turn != group) continue;
+                    if (turn != mine) continue;
                     uint4 w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(stage + row * 128 + (((kb * 4 + i) ^ (row & 7)) << 4));
-                    wait(b.a_empty[half][group], parity);
+                    wait(b.a_empty[mine], parity);
                     tcgen05_after_sync();
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                     tmem_wait_store();
                     tcgen05_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&b.a_full[half][group]));
+                    if (lane == 0) mbar_arrive(smem_addr(&b.a_full[mine]));
                     parity ^= 1u;
                 }
                 __syncwarp();
@@ -218,15 +218,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                 q.next(p.qstages);
             }
         }
-        wait(b.a_empty[half][group], parity);   // the products have read it: nothing arrives after the block's end
+        wait(b.a_empty[mine], parity);   // the products have read it: nothing arrives after the block's end
     } else if (warp < Sh::kFirstFew) {
         // ---- add the groups' sums
         if (Sh::kUneven) reg_alloc<Sh::kAddRegs>();
-        const int which = (warp - Sh::kWidenWarps) >> 2, quarter = warp & 3;
-        const int half = kHalves == 2 ? which : 0, own0 = kHalves == 2 ? 0 : which * kOwn, row = half * 128 + quarter * 32 + lane;
-        const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kD + half * (kSums * N) + own0;
-        Ring q, d;
+        const int own0 = ((warp - Sh::kWidenWarps) >> 2) * kOwn, row = tid & 127;
+        const uint32_t quarter = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const uint32_t from = quarter + Sh::kD + own0, out = quarter + Sh::kOut + own0;
+        Ring q;
         bool waited = false;
+        int turn = 0;                        // of the block of columns
+        uint32_t taken0 = 0, taken1 = 0;     // sums read so far of either turn
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
             uint64_t acc[kOwn / 2];
@@ -235,16 +237,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
             for (int st = 0; st < stages; ++st) {
                 wait(b.q_full[q.slot], q.parity);
                 const unsigned char* const stage = smem + kHeader + q.slot * p.stage_bytes;
-                const int n = min(per_stage, p.groups - st * per_stage);
-                for (int g = 0; g < n; ++g) {
+                const int n = min(per_stage, p.groups - st * per_stage), a_block = per_stage / 2;
+                auto group = [&](int g) {
                     const float s = widen_any(stage + lay.scales, p.scale_dtype, g * kRows + row);
                     const uint64_t s2 = f2_pack(s, s);
-                    wait(b.d_full[half][d.slot], d.parity);
+                    const uint32_t taken = turn ? taken1 : taken0, slot = taken % static_cast<uint32_t>(kSums);
+                    wait(b.d_full[turn][slot], taken / static_cast<uint32_t>(kSums) & 1u);
                     tcgen05_after_sync();
 #pragma unroll
                     for (int c = 0; c < kOwn; c += 16) {
                         float f[16];
-                        tmem_load16(from + d.slot * N + c, f);
+                        tmem_load16(from + (turn * kSums + slot) * N + c, f);
                         tmem_wait_load(f);
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
@@ -254,9 +257,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                     }
                     tcgen05_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&b.d_empty[half][d.slot]));
-                    d.next(kSums);
-                }
+                    if (lane == 0) mbar_arrive(smem_addr(&b.d_empty[turn][slot]));
+                    taken0 += turn ^ 1;
+                    taken1 += turn;
+                };
+                for (int g0 = 0; g0 < n; g0 += a_block, turn ^= 1)
+                    for (int g = g0; g < min(n, g0 + a_block); ++g) group(g);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&b.q_empty[q.slot]));
                 q.next(p.qstages);
@@ -264,50 +270,64 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
             if (!waited) {
                 grid_dep_wait();
                 // each warp for itself
-                for (int t = lane; t < p.T; t += 32) b.factor[t] = p.inverse[t] * 0x1p12f;
+                bool odd = false;
+                for (int t = lane; t < p.T; t += 32) {
+                    const float f = p.inverse[t];
+                    odd = odd || f != f;
+                    b.factor[t] = f * 0x1p12f;
+                }
+                if (odd) b.odd = 1;
                 __syncwarp();
                 waited = true;
             }
+            // ---- out, by way of tensor memory: registers have no index, and straight code for 64 sums, run once a
+            // tile, waited for its instructions (15000 clocks)
+#pragma unroll
+            for (int c = 0; c < kOwn; c += 16) {
+                uint32_t r[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    float lo, hi;
+                    f2_unpack(acc[(c + i) / 2], lo, hi);
+                    r[i] = __float_as_uint(lo);
+                    r[i + 1] = __float_as_uint(hi);
+                }
+                tmem_store16(out + c, r);
+            }
+            tmem_wait_store();
+            // this thread's hidden rows of the block's
+            const int own = p.pairs ? kOwn / 2 : kOwn, t0 = tb * p.per + own0 / kOwn * own, rows = min(own, p.T - t0);
             const int64_t v = static_cast<int64_t>(vt) * kRows + row;
-            if (v < p.V) {
-                // this thread's hidden rows of the block's
-                const int own = p.pairs ? kOwn / 2 : kOwn, t0 = tb * p.per + own0 / kOwn * own;
-                const int rows = min(own, p.T - t0);
-                auto all = [&](auto type) {
-                    using O = decltype(type);
-                    typename O::raw* out = static_cast<typename O::raw*>(p.out) + static_cast<int64_t>(t0) * p.ld_out + v;
-                    auto put = [&](int i, float x) {
-                        if (i < rows) *out = static_cast<typename O::raw>(O::round(x * 0x1p12f * b.factor[t0 + i] * p.scale));
-                        out += p.ld_out;
-                    };
+#pragma unroll 1
+            for (int c = 0; c < rows; c += 8) {
+                float x[8];
+                tmem_load8(out + c, x);
+                tmem_wait_load(x);
+                if (p.pairs) {
+                    float lo[8];
+                    tmem_load8(out + kOwn / 2 + c, lo);
+                    tmem_wait_load(lo);
 #pragma unroll
-                    for (int i = 0; i < kOwn / 4; ++i) {
-                        float a, c, e, f;
-                        f2_unpack(acc[i], a, c);
-                        if (p.pairs) {
-                            f2_unpack(acc[i + kOwn / 4], e, f);
-                            a = fmaf(e, 1.f / 2048.f, a);
-                            c = fmaf(f, 1.f / 2048.f, c);
-                        }
-                        put(2 * i, a);
-                        put(2 * i + 1, c);
-                    }
-                    if (!p.pairs) {
+                    for (int i = 0; i < 8; ++i) x[i] = fmaf(lo[i], 1.f / 2048.f, x[i]);
+                }
 #pragma unroll
-                        for (int i = kOwn / 4; i < kOwn / 2; ++i) {
-                            float a, c;
-                            f2_unpack(acc[i], a, c);
-                            put(2 * i, a);
-                            put(2 * i + 1, c);
-                        }
-                    }
-                };
-                if (p.out_dtype == LMLOSS_BF16) all(Bf16{});
-                else if (p.out_dtype == LMLOSS_FP16) all(Fp16{});
-                else all(Fp32{});
+                for (int i = 0; i < 8; ++i) x[i] = c + i < rows ? x[i] * 0x1p12f * b.factor[t0 + c + i] * p.scale : 0.f;
+                if (v >= p.V) continue;
+                const int64_t at = static_cast<int64_t>(t0 + c) * p.ld_out + v;
+                if (p.out_dtype == LMLOSS_FP32) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < rows) static_cast<float*>(p.out)[at + i * p.ld_out] = x[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < rows) static_cast<uint16_t*>(p.out)[at + i * p.ld_out] = p.out_dtype == LMLOSS_BF16 ? Bf16::round(x[i]) : Fp16::round(x[i]);
+                }
+            }
+            if (b.odd && v < p.V)
                 for (int i = 0; i < rows; ++i)
                     if (b.factor[t0 + i] != b.factor[t0 + i]) store_plain(p, t0 + i, v);
-            }
+            __syncwarp();
         }
     } else {
         if (Sh::kUneven) reg_dealloc<Sh::kFewRegs>();
@@ -344,28 +364,32 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                 for (int i = 0; i < p.xstages; ++i, x.next(p.xstages)) wait_one(b.x_empty[x.slot], x.parity ^ 1u);
             }
             __syncwarp();
-        } else if (warp - (Sh::kFirstFew + 2) < kHalves) {
-            // ---- the products of one half.  (One warp for both was late: its instructions took 1500 clocks a block
-            // of columns.)
+        } else {
+            // ---- the products, every second block of columns: one warp waits for its operands while the other's
+            // products run.  (The tensor cores take few products ahead: by one warp, three waits a block of
+            // columns left them idle half the time.)
             const uint32_t leader = elect_one();
-            const int half = warp - (Sh::kFirstFew + 2);
+            const int mine = warp - (Sh::kFirstFew + 2);
             auto multiply = [&](auto count) {
                 constexpr int kSteps = decltype(count)::value;   // a group's, 16 columns each
                 constexpr int kGroups = 8 / kSteps;              // of a block of columns
-                Ring x, a, d;
+                Ring x, d;
+                uint32_t parity = 0;
+                int turn = 0;
+                const uint32_t from = tmem + mine * 64;
                 for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
                     int left = p.groups;
-                    for (int kb = 0; kb < p.kblocks; ++kb, left -= kGroups) {
+                    for (int kb = 0; kb < p.kblocks; ++kb, left -= kGroups, turn ^= 1, x.next(p.xstages)) {
+                        if (turn != mine) continue;
                         wait(b.x_full[x.slot], x.parity);
                         const uint64_t desc = mma_desc_128b(xbase + x.slot * kXBytes);
-                        wait(b.a_full[half][a.slot], a.parity);
-                        const uint32_t from = tmem + half * 128 + a.slot * 64;
+                        wait(b.a_full[mine], parity);
 #pragma unroll
                         for (int g = 0; g < kGroups; ++g) {
                             if (g >= left) break;
-                            wait(b.d_empty[half][d.slot], d.parity ^ 1u);
+                            wait(b.d_empty[mine][d.slot], d.parity ^ 1u);
                             tcgen05_after_sync();
-                            const uint32_t to = tmem + kD + (half * kSums + d.slot) * N;
+                            const uint32_t to = tmem + Sh::kD + (mine * kSums + d.slot) * N;
 #pragma unroll
                             for (int k = 0; k < kSteps; ++k) {
                                 const int step = g * kSteps + k;   // 64 columns lie in one run of N rows
@@ -373,13 +397,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
                                 if (k == 0) mma_f16_ts<false>(to, from + step * 8, at, kIdesc, leader);
                                 else mma_f16_ts<true>(to, from + step * 8, at, kIdesc, leader);
                             }
-                            mma_commit(smem_addr(&b.d_full[half][d.slot]), leader);
+                            mma_commit(smem_addr(&b.d_full[mine][d.slot]), leader);
                             d.next(kSums);
                         }
-                        mma_commit(smem_addr(&b.a_empty[half][a.slot]), leader);
+                        mma_commit(smem_addr(&b.a_empty[mine]), leader);
                         mma_commit(smem_addr(&b.x_empty[x.slot]), leader);
-                        x.next(p.xstages);
-                        a.next(2);
+                        parity ^= 1u;
                     }
                 }
             };
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) logits_kernel(const __g
         }
     }
     __syncthreads();
-    if (warp == Sh::kFirstFew + 2) tmem_free(tmem, kColumns);
+    if (warp == Sh::kFirstFew + 2) tmem_free(tmem, Sh::kColumns);
 }
 
 // ------------------------------------------------------------------- host
@@ -478,10 +501,12 @@ bool table_maps(const lmloss_table4& t, int rows, TableMaps* maps)
 template <int N>
 lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    const StageLayout lay(Shape<N>::kRows, p.shift, p.scale_bytes, p.zeros != nullptr);
+    const StageLayout lay(kRows, p.shift, p.scale_bytes, p.zeros != nullptr);
+    // of the SM's 228 KB each block takes 1 more than it asks for
+    const uint32_t shared = Shape<N>::kBlocks == 1 ? kMaxShared : kMaxShared / 2 - 1024;
     p.stage_bytes = lay.bytes;
-    p.xstages = N == 128 ? 3 : (N == 64 ? 4 : 6);
-    p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHeader - p.xstages * N * 256) / lay.bytes);
+    p.xstages = N == 128 ? 3 : (N == 32 ? 4 : 6);
+    p.qstages = std::min<int>(kMaxStages, (shared - kHeader - p.xstages * N * 256) / lay.bytes);
     constexpr uint32_t bit = 1u << (N == 16 ? 17 : (N == 32 ? 18 : (N == 64 ? 19 : 20)));
     if (!(h->limits_raised & bit)) {
         if (cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
@@ -491,7 +516,7 @@ lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vo
         h->limits_raised |= bit;
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.vtiles) * p.tblocks, h->num_sms)));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.vtiles) * p.tblocks, Shape<N>::kBlocks * h->num_sms)));
     cfg.blockDim = dim3(Shape<N>::kThreads);
     cfg.dynamicSmemBytes = kHeader + p.qstages * lay.bytes + p.xstages * N * 256;
     cfg.stream = stream;
@@ -566,7 +591,7 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.err = h->err;
         const int operands = T * (pairs ? 2 : 1);
         const bool few = few_rows_fit(p);
-        const int rows = few || operands <= 64 ? 256 : 128;
+        const int rows = few ? 256 : kRows;
         p.vtiles = static_cast<int>((a->table.V + rows - 1) / rows);
         TableMaps maps{};
         if (!table_maps(a->table, rows, &maps)) return LMLOSS_ERR_CUDA;
@@ -580,7 +605,7 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
             x.kblocks = p.kblocks;
             x.N = p.N = operands <= 16 ? 16 : (operands <= 32 ? 32 : (operands <= 64 ? 64 : kMany));
             x.per = p.per = pairs ? p.N / 2 : p.N;
-            x.own = p.N == kMany ? Shape<kMany>::kOwn : p.N;
+            x.own = p.N > 32 ? p.N / 2 : p.N;
             x.out = h->ws;
             x.inverse = reinterpret_cast<float*>(h->ws + w.inverse);
             p.tblocks = (T + p.per - 1) / p.per;
