@@ -39,10 +39,10 @@ struct Shape {
     static constexpr int kAddWarps = 4 * kSplit;
     static constexpr int kFirstFew = kWidenWarps + kAddWarps;   // then: table, hidden rows, products of either turn
     static constexpr int kThreads = (kFirstFew + 4) * 32;
-    // tensor memory: A of either turn, D kSums of either turn, then sums on their way out
-    static constexpr int kSums = N == 64 || N == 16 ? 2 : 1;
-    static constexpr uint32_t kD = 128, kOut = kD + 2 * kSums * N, kColumns = N > 32 ? 512 : 256;
-    static_assert(kOut + N <= kColumns, "tensor memory");
+    // tensor memory: A of either turn, then D kSums of either turn
+    static constexpr int kSums = N > 64 ? 1 : 2;
+    static constexpr uint32_t kD = 128, kColumns = N > 32 ? 512 : 256;
+    static_assert(kD + 2 * kSums * N <= kColumns, "tensor memory");
     // registers a thread of each part where 64 sums do not fit an even share: in all what the block was launched with
     static constexpr bool kUneven = kOwn == 64;
     static constexpr int kWidenRegs = 72, kAddRegs = 136, kFewRegs = 40;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
         if (Sh::kUneven) reg_alloc<Sh::kAddRegs>();
         const int own0 = ((warp - Sh::kWidenWarps) >> 2) * kOwn, row = tid & 127;
         const uint32_t quarter = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-        const uint32_t from = quarter + Sh::kD + own0, out = quarter + Sh::kOut + own0;
+        const uint32_t from = quarter + Sh::kD + own0;
         Ring q;
         bool waited = false;
         int turn = 0;                        // of the block of columns
@@ -280,49 +280,42 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                 __syncwarp();
                 waited = true;
             }
-            // ---- out, by way of tensor memory: registers have no index, and straight code for 64 sums, run once a
-            // tile, waited for its instructions (15000 clocks)
-#pragma unroll
-            for (int c = 0; c < kOwn; c += 16) {
-                uint32_t r[16];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    float lo, hi;
-                    f2_unpack(acc[(c + i) / 2], lo, hi);
-                    r[i] = __float_as_uint(lo);
-                    r[i + 1] = __float_as_uint(hi);
-                }
-                tmem_store16(out + c, r);
-            }
-            tmem_wait_store();
             // this thread's hidden rows of the block's
             const int own = p.pairs ? kOwn / 2 : kOwn, t0 = tb * p.per + own0 / kOwn * own, rows = min(own, p.T - t0);
             const int64_t v = static_cast<int64_t>(vt) * kRows + row;
-#pragma unroll 1
-            for (int c = 0; c < rows; c += 8) {
-                float x[8];
-                tmem_load8(out + c, x);
-                tmem_wait_load(x);
-                if (p.pairs) {
-                    float lo[8];
-                    tmem_load8(out + kOwn / 2 + c, lo);
-                    tmem_wait_load(lo);
+            if (v < p.V) {
+                auto all = [&](auto type) {
+                    using O = decltype(type);
+                    typename O::raw* to = static_cast<typename O::raw*>(p.out) + static_cast<int64_t>(t0) * p.ld_out + v;
+                    auto put = [&](int i, float x) {
+                        if (i < rows) *to = static_cast<typename O::raw>(O::round(x * 0x1p12f * b.factor[t0 + i] * p.scale));
+                        to += p.ld_out;
+                    };
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = fmaf(lo[i], 1.f / 2048.f, x[i]);
-                }
+                    for (int i = 0; i < kOwn / 4; ++i) {
+                        float a, c, e, f;
+                        f2_unpack(acc[i], a, c);
+                        if (p.pairs) {
+                            f2_unpack(acc[i + kOwn / 4], e, f);
+                            a = fmaf(e, 1.f / 2048.f, a);
+                            c = fmaf(f, 1.f / 2048.f, c);
+                        }
+                        put(2 * i, a);
+                        put(2 * i + 1, c);
+                    }
+                    if (!p.pairs) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = c + i < rows ? x[i] * 0x1p12f * b.factor[t0 + c + i] * p.scale : 0.f;
-                if (v >= p.V) continue;
-                const int64_t at = static_cast<int64_t>(t0 + c) * p.ld_out + v;
-                if (p.out_dtype == LMLOSS_FP32) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c + i < rows) static_cast<float*>(p.out)[at + i * p.ld_out] = x[i];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c + i < rows) static_cast<uint16_t*>(p.out)[at + i * p.ld_out] = p.out_dtype == LMLOSS_BF16 ? Bf16::round(x[i]) : Fp16::round(x[i]);
-                }
+                        for (int i = kOwn / 4; i < kOwn / 2; ++i) {
+                            float a, c;
+                            f2_unpack(acc[i], a, c);
+                            put(2 * i, a);
+                            put(2 * i + 1, c);
+                        }
+                    }
+                };
+                if (p.out_dtype == LMLOSS_BF16) all(Bf16{});
+                else if (p.out_dtype == LMLOSS_FP16) all(Fp16{});
+                else all(Fp32{});
             }
             if (b.odd && v < p.V)
                 for (int i = 0; i < rows; ++i)

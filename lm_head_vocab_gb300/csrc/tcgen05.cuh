@@ -32,29 +32,6 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&f)[8])
-{
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(addr)
-                 : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait_load(float (&f)[8])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7])
-                 :
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&f)[16])
 {
     uint32_t r[16];
@@ -146,15 +123,18 @@ __device__ __forceinline__ bool mbar_sleep_bounded(uint32_t bar, uint32_t parity
         return done != 0;
     };
     if (try_wait()) return true;
+    // (few instructions between tries: a dozen waiting warps share the issue slots with those that work)
     const long long start = clock64();
-    while (!try_wait()) {
-        if (*failed) return true;
-        if (clock64() - start > limit_cycles) {
-            *failed = 1;
-            return false;
+    for (uint32_t tries = 1;; ++tries) {
+        if (try_wait()) return true;
+        if ((tries & 63u) == 0) {
+            if (*failed) return true;
+            if (clock64() - start > limit_cycles) {
+                *failed = 1;
+                return false;
+            }
         }
     }
-    return true;
 }
 
 // ------------------------------------------------------------ tiled copies
