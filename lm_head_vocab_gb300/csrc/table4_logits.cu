@@ -39,9 +39,10 @@ struct Shape {
     static constexpr int kAddWarps = 4 * kSplit;
     static constexpr int kFirstFew = kWidenWarps + kAddWarps;   // then: table, hidden rows, products of either turn
     static constexpr int kThreads = (kFirstFew + 4) * 32;
-    // tensor memory: A of either turn, then D kSums of either turn
-    static constexpr int kSums = N > 64 ? 1 : 2;
-    static constexpr uint32_t kD = 128, kColumns = N > 32 ? 512 : 256;
+    // tensor memory: A kAhead of either turn, then D kSums of either turn.  (With one A of a turn what widens waited
+    // for its products: 1100 clocks a block of columns, for 64 operand rows as for 128.)
+    static constexpr int kSums = N > 64 ? 1 : 2, kAhead = N > 32 ? 2 : 1;
+    static constexpr uint32_t kD = 128 * kAhead, kColumns = N > 32 ? 512 : 256;
     static_assert(kD + 2 * kSums * N <= kColumns, "tensor memory");
     // registers a thread of each part where 64 sums do not fit an even share: in all what the block was launched with
     static constexpr bool kUneven = kOwn == 64;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
 // A block's head: barriers, and the factors of all hidden rows.
 struct __align__(16) LogitsBarriers {
     uint64_t q_full[kMaxStages], q_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages];
-    uint64_t a_full[2], a_empty[2], d_full[2][2], d_empty[2][2];   // of either turn
+    uint64_t a_full[2][2], a_empty[2][2], d_full[2][2], d_empty[2][2];   // of either turn
     uint32_t tmem;
     int failed;
     int odd;                     // whether any row is not finite
@@ -144,9 +145,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
             mbar_init(smem_addr(&b.x_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&b.a_full[i]), 4);
-            mbar_init(smem_addr(&b.a_empty[i]), 1);
             for (int d = 0; d < 2; ++d) {
+                mbar_init(smem_addr(&b.a_full[i][d]), 4);
+                mbar_init(smem_addr(&b.a_empty[i][d]), 1);
                 mbar_init(smem_addr(&b.d_full[i][d]), 1);
                 mbar_init(smem_addr(&b.d_empty[i][d]), Sh::kAddWarps);
             }
@@ -174,23 +175,25 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
         // ---- widen: a thread a row, every second block of columns
         if (Sh::kUneven) reg_dealloc<Sh::kWidenRegs>();
         const int mine = warp >> 2, row = tid & 127;
-        const uint32_t to = tmem + (static_cast<uint32_t>(warp & 3) << 21) + mine * 64;
-        Ring q;
-        uint32_t parity = 1;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + mine * Sh::kAhead * 64;
+        Ring q, a;
         int turn = 0;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+#pragma unroll 1
             for (int st = 0; st < stages; ++st) {
                 wait(b.q_full[q.slot], q.parity);
                 const unsigned char* const stage = smem + kHeader + q.slot * p.stage_bytes;
                 const unsigned char* const zeros = stage + lay.zeros;
                 const int blocks = min(2, p.kblocks - 2 * st);
+#pragma unroll 1
                 for (int kb = 0; kb < blocks; ++kb, turn ^= 1) {
                     if (turn != mine) continue;
                     uint4 w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(stage + row * 128 + (((kb * 4 + i) ^ (row & 7)) << 4));
-                    wait(b.a_empty[mine], parity);
+                    wait(b.a_empty[mine][a.slot], a.parity ^ 1u);
                     tcgen05_after_sync();
+                    const uint32_t to = lanes + a.slot * 64;
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
                         uint32_t r[32];
@@ -210,15 +213,16 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                     tmem_wait_store();
                     tcgen05_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&b.a_full[mine]));
-                    parity ^= 1u;
+                    if (lane == 0) mbar_arrive(smem_addr(&b.a_full[mine][a.slot]));
+                    a.next(Sh::kAhead);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&b.q_empty[q.slot]));
                 q.next(p.qstages);
             }
         }
-        wait(b.a_empty[mine], parity);   // the products have read it: nothing arrives after the block's end
+        // the products have read them: nothing arrives after the block's end
+        for (int i = 0; i < Sh::kAhead; ++i, a.next(Sh::kAhead)) wait(b.a_empty[mine][a.slot], a.parity ^ 1u);
     } else if (warp < Sh::kFirstFew) {
         // ---- add the groups' sums
         if (Sh::kUneven) reg_alloc<Sh::kAddRegs>();
@@ -234,14 +238,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
             uint64_t acc[kOwn / 2];
 #pragma unroll
             for (int i = 0; i < kOwn / 2; ++i) acc[i] = f2_pack(0.f, 0.f);
+#pragma unroll 1
             for (int st = 0; st < stages; ++st) {
                 wait(b.q_full[q.slot], q.parity);
-                const unsigned char* const stage = smem + kHeader + q.slot * p.stage_bytes;
-                const int n = min(per_stage, p.groups - st * per_stage), a_block = per_stage / 2;
-                auto group = [&](int g) {
-                    const float s = widen_any(stage + lay.scales, p.scale_dtype, g * kRows + row);
-                    const uint64_t s2 = f2_pack(s, s);
+                const unsigned char* const scales = smem + kHeader + q.slot * p.stage_bytes + lay.scales;
+                const int n = min(per_stage, p.groups - st * per_stage);
+                // one loop, little code: the five parts of a block share the instruction cache
+#pragma unroll 1
+                for (int g = 0; g < n; ++g) {
                     const uint32_t taken = turn ? taken1 : taken0, slot = taken % static_cast<uint32_t>(kSums);
+                    const float s = widen_any(scales, p.scale_dtype, g * kRows + row);
+                    const uint64_t s2 = f2_pack(s, s);
                     wait(b.d_full[turn][slot], taken / static_cast<uint32_t>(kSums) & 1u);
                     tcgen05_after_sync();
 #pragma unroll
@@ -260,10 +267,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                     if (lane == 0) mbar_arrive(smem_addr(&b.d_empty[turn][slot]));
                     taken0 += turn ^ 1;
                     taken1 += turn;
-                };
-                for (int g0 = 0; g0 < n; g0 += a_block, turn ^= 1)
-                    for (int g = g0; g < min(n, g0 + a_block); ++g) group(g);
-                __syncwarp();
+                    if (((g + 1) << p.shift) % kBlockCols == 0 || g + 1 == n) turn ^= 1;   // the block of columns' last
+                }
                 if (lane == 0) mbar_arrive(smem_addr(&b.q_empty[q.slot]));
                 q.next(p.qstages);
             }
@@ -366,17 +371,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
             auto multiply = [&](auto count) {
                 constexpr int kSteps = decltype(count)::value;   // a group's, 16 columns each
                 constexpr int kGroups = 8 / kSteps;              // of a block of columns
-                Ring x, d;
-                uint32_t parity = 0;
+                Ring x, a, d;
                 int turn = 0;
-                const uint32_t from = tmem + mine * 64;
                 for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
                     int left = p.groups;
+#pragma unroll 1
                     for (int kb = 0; kb < p.kblocks; ++kb, left -= kGroups, turn ^= 1, x.next(p.xstages)) {
                         if (turn != mine) continue;
                         wait(b.x_full[x.slot], x.parity);
                         const uint64_t desc = mma_desc_128b(xbase + x.slot * kXBytes);
-                        wait(b.a_full[mine], parity);
+                        wait(b.a_full[mine][a.slot], a.parity);
+                        const uint32_t from = tmem + (mine * Sh::kAhead + a.slot) * 64;
 #pragma unroll
                         for (int g = 0; g < kGroups; ++g) {
                             if (g >= left) break;
@@ -393,9 +398,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                             mma_commit(smem_addr(&b.d_full[mine][d.slot]), leader);
                             d.next(kSums);
                         }
-                        mma_commit(smem_addr(&b.a_empty[mine]), leader);
+                        mma_commit(smem_addr(&b.a_empty[mine][a.slot]), leader);
                         mma_commit(smem_addr(&b.x_empty[x.slot]), leader);
-                        parity ^= 1u;
+                        a.next(Sh::kAhead);
                     }
                 }
             };

@@ -106,27 +106,27 @@ __device__ __forceinline__ uint64_t mma_desc_128b(uint32_t addr)
 }
 
 // ---------------------------------------------------------------- waiting
-// Waits for a phase, asleep in the barrier for up to 0.1 ms at a time.  After `limit_cycles` it sets *failed,
-// which ends every other such wait of the block at once: all go on, to a clean end with results that mean
-// nothing, and never wait for one another in vain.  False where it gave up itself.
-__device__ __forceinline__ bool mbar_sleep_bounded(uint32_t bar, uint32_t parity, long long limit_cycles, volatile int* failed)
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity)
 {
-    auto try_wait = [&] {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(100000u)
-            : "memory");
-        return done != 0;
-    };
-    if (try_wait()) return true;
-    // (few instructions between tries: a dozen waiting warps share the issue slots with those that work)
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    return done != 0;
+}
+// (few instructions between tries: a dozen waiting warps share the issue slots and the
+// instruction cache with those that work)
+__device__ __forceinline__ bool mbar_sleep_slowly(uint32_t bar, uint32_t parity, long long limit_cycles, volatile int* failed)
+{
     const long long start = clock64();
+#pragma unroll 1
     for (uint32_t tries = 1;; ++tries) {
-        if (try_wait()) return true;
+        if (mbar_sleep(bar, parity)) return true;
+        __nanosleep(20);
         if ((tries & 63u) == 0) {
             if (*failed) return true;
             if (clock64() - start > limit_cycles) {
@@ -135,6 +135,13 @@ __device__ __forceinline__ bool mbar_sleep_bounded(uint32_t bar, uint32_t parity
             }
         }
     }
+}
+// Waits for a phase.  After `limit_cycles` it sets *failed, which ends every other such wait of the block at once: all
+// go on, to a clean end with results that mean nothing, and never wait for one another in vain.  False where it
+// gave up itself.
+__device__ __forceinline__ bool mbar_sleep_bounded(uint32_t bar, uint32_t parity, long long limit_cycles, volatile int* failed)
+{
+    return mbar_sleep(bar, parity) || mbar_sleep_slowly(bar, parity, limit_cycles, failed);
 }
 
 // ------------------------------------------------------------ tiled copies
