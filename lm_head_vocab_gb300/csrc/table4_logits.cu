@@ -73,10 +73,12 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
     constexpr bool kPair = X::kBytes == 4;
     float top = 0.f;   // of what is finite
     bool finite = true;
-    for (int c = tid; c < p.D; c += 256) {
-        const float a = fabsf(X::widen(x[c]));
-        if (a < INFINITY) top = fmaxf(top, a);
-        else finite = false;
+    for (int c = tid * 8; c < p.D; c += 256 * 8) {
+        Pack<X, 8> v;
+        bool others;
+        load_part<X>(x, c, p.D, v);
+        top = fmaxf(top, part_top<X>(v, others));
+        finite = finite && !others;
     }
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     finite = __all_sync(0xffffffffu, finite);
@@ -98,7 +100,9 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
     for (int u = tid; u < p.kblocks * 16; u += 256) {
         uint4 hi, lo;
         float sum, sum_lo;
-        hidden_part<X>(x, 8 * u, p.D, finite ? scale : 0.f, hi, lo, sum, sum_lo);
+        Pack<X, 8> v;
+        load_part<X>(x, 8 * u, p.D, v);
+        hidden_part<X>(v, finite ? scale : 0.f, hi, lo, sum, sum_lo);
         // [2][N][128 bytes] for each block of columns, swizzled as mma_desc_128b wants it
         const int part = u & 7;
         auto place = [&](int r) { return reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u >> 3) * p.N + r) * 128 + ((part ^ (r & 7)) << 4)); };

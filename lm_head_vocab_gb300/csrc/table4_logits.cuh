@@ -90,29 +90,32 @@ __device__ __forceinline__ float hidden_scale(float top)
     const int e = static_cast<int>(__float_as_uint(top) >> 23);
     return top > 0.f ? __uint_as_float(static_cast<uint32_t>(min(14 + 254 - e, 253)) << 23) : 1.f;
 }
-// Eight columns of a hidden row from c on, scaled, as a 16-byte part: fp16 in the order 0 4 1 5 2 6 3 7, the places
-// 1 5 and 3 7 divided by 16.  lo: what fp32 leaves, times 2^11.  The sums are of what the parts stand for, in the
-// products' unit of 2^-24.  A scale of 0 is a row that is not finite.
+// Eight columns of a hidden row from c on, 0 past the last.
 template <class X>
-__device__ __forceinline__ void hidden_part(const typename X::raw* x, int c, int D, float scale, uint4& hi, uint4& lo, float& sum, float& sum_lo)
+__device__ __forceinline__ void load_part(const typename X::raw* x, int c, int D, Pack<X, 8>& q)
+{
+    if (c + 8 <= D && (reinterpret_cast<uintptr_t>(x + c) & 15u) == 0) {
+        q.load(x + c);
+    } else {
+        q.zero();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < D) q.set(i, X::widen(x[c + i]));
+    }
+}
+// They scaled as a 16-byte part: fp16 in the order 0 4 1 5 2 6 3 7, the places 1 5 and 3 7 divided by 16.  lo: what fp32
+// leaves, times 2^11.  The sums are of what the parts stand for, in the products' unit of 2^-24.  A scale of 0 is a
+// row that is not finite.
+template <class X>
+__device__ __forceinline__ void hidden_part(const Pack<X, 8>& v, float scale, uint4& hi, uint4& lo, float& sum, float& sum_lo)
 {
     constexpr bool kPair = X::kBytes == 4;
-    float v[8];
-    if (c + 8 <= D && (reinterpret_cast<uintptr_t>(x + c) & 15u) == 0) {
-        Pack<X, 8> q;
-        q.load(x + c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = q.get(i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < D ? X::widen(x[c + i]) : 0.f;
-    }
     uint32_t h[4], l[4] = {0, 0, 0, 0};
     sum = sum_lo = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float by = i & 1 ? scale * 0.0625f : scale, back = i & 1 ? 0x1p-20f : 0x1p-24f;
-        const float a = scale > 0.f ? v[i] * by : 0.f, b = scale > 0.f ? v[i + 4] * by : 0.f;
+        const float a = scale > 0.f ? v.get(i) * by : 0.f, b = scale > 0.f ? v.get(i + 4) * by : 0.f;
         const __half2 p = __floats2half2_rn(a, b);
         h[i] = *reinterpret_cast<const uint32_t*>(&p);
         const float2 f = __half22float2(p);
@@ -126,6 +129,20 @@ __device__ __forceinline__ void hidden_part(const typename X::raw* x, int c, int
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// The largest finite magnitude of eight columns, and whether there are others.
+template <class X>
+__device__ __forceinline__ float part_top(const Pack<X, 8>& v, bool& odd)
+{
+    float top = 0.f;
+    odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(v.get(i));
+        if (a < INFINITY) top = fmaxf(top, a);
+        else odd = true;
+    }
+    return top;
 }
 // Sums over the `lanes` (4, 8 or 16) neighbouring threads of a group, 16 threads together.
 template <bool PAIR>

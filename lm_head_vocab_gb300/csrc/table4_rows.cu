@@ -55,43 +55,55 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The hidden rows into shared memory, by the first kSumThreads threads.
+// The hidden rows into shared memory, by the first kSumThreads threads: read once, as many rows at a time as their
+// registers hold.
 template <class X>
 __device__ __noinline__ void lay_out(const LogitsParams& p, RowsHead& head, unsigned char* x, float* sums, int N)
 {
     constexpr bool kPair = X::kBytes == 4;
-    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int kHold = 16 / X::kBytes;
+    const int tid = threadIdx.x;
+    const uint32_t together = 0xffffu << (tid & 16);   // 16 threads have parts of the same row
     const typename X::raw* hidden = static_cast<const typename X::raw*>(p.hidden);
-    for (int r = 0; r < p.T; ++r) {
-        float top = 0.f;   // of what is finite
-        bool finite = true;
-        for (int c = tid; c < p.D; c += kSumThreads) {
-            const float a = fabsf(X::widen(hidden[r * p.ld_hidden + c]));
-            if (a < INFINITY) top = fmaxf(top, a);
-            else finite = false;
+    const int parts = p.kblocks * 16, lanes = (1 << p.shift) / 8, rows = kHold * kSumThreads / parts;   // few_rows_fit: at least one
+    for (int r0 = 0; r0 < p.T; r0 += rows) {
+        const int n = min(rows, p.T - r0) * parts;
+        Pack<X, 8> v[kHold];
+        int r[kHold];
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int at = tid + i * kSumThreads;
+            r[i] = at < n ? r0 + at / parts : -1;
+            if (r[i] >= 0) load_part<X>(hidden + r[i] * p.ld_hidden, (at - (r[i] - r0) * parts) * 8, p.D, v[i]);
         }
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        finite = __all_sync(0xffffffffu, finite);
-        if (lane == 0) {
-            atomicMax(&head.top[r], most);
-            if (!finite) head.odd[r] = 1;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            if (r[i] < 0) continue;
+            bool odd;
+            const uint32_t top = __reduce_max_sync(together, __float_as_uint(part_top<X>(v[i], odd)));
+            odd = __any_sync(together, odd);
+            if ((tid & 15) == 0) {
+                atomicMax(&head.top[r[i]], top);
+                if (odd) head.odd[r[i]] = 1;
+            }
         }
-    }
-    asm volatile("bar.sync 9, %0;" ::"n"(kSumThreads) : "memory");
-    const int parts = p.kblocks * 16, lanes = (1 << p.shift) / 8;
-    for (int i = tid; i < p.T * parts; i += kSumThreads) {
-        const int r = i / parts, u = i - r * parts;
-        uint4 hi, lo;
-        float sum, sum_lo;
-        hidden_part<X>(hidden + r * p.ld_hidden, 8 * u, p.D, head.odd[r] ? 0.f : hidden_scale(__uint_as_float(head.top[r])), hi, lo, sum, sum_lo);
-        auto place = [&](int n) { return reinterpret_cast<uint4*>(x + ((u >> 4) * N + n) * 256 + (((u & 15) ^ ((n & 1) << 2)) << 4)); };
-        *place(r) = hi;
-        if (kPair) *place(r + N / 2) = lo;
-        group_sums<kPair>(lanes, sum, sum_lo);
-        const int g = (8 * u) >> p.shift;
-        if ((u & (lanes - 1)) == 0 && g < p.groups) {
-            sums[g * N + r] = sum;
-            if (kPair) sums[g * N + r + N / 2] = sum_lo;
+        asm volatile("bar.sync 9, %0;" ::"n"(kSumThreads) : "memory");
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            if (r[i] < 0) continue;
+            const int u = tid + i * kSumThreads - (r[i] - r0) * parts;
+            uint4 hi, lo;
+            float sum, sum_lo;
+            hidden_part<X>(v[i], head.odd[r[i]] ? 0.f : hidden_scale(__uint_as_float(head.top[r[i]])), hi, lo, sum, sum_lo);
+            auto place = [&](int k) { return reinterpret_cast<uint4*>(x + ((u >> 4) * N + k) * 256 + (((u & 15) ^ ((k & 1) << 2)) << 4)); };
+            *place(r[i]) = hi;
+            if (kPair) *place(r[i] + N / 2) = lo;
+            group_sums<kPair>(lanes, sum, sum_lo);
+            const int g = (8 * u) >> p.shift;
+            if ((u & (lanes - 1)) == 0 && g < p.groups) {
+                sums[g * N + r[i]] = sum;
+                if (kPair) sums[g * N + r[i] + N / 2] = sum_lo;
+            }
         }
     }
     asm volatile("bar.sync 9, %0;" ::"n"(kSumThreads) : "memory");
@@ -268,7 +280,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     __syncthreads();
 }
 
-int columns_for(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
+
 
 template <int NT, int GROUP>
 lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
@@ -278,7 +290,7 @@ lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h
     p.stage_bytes = lay.bytes;
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHead - rl.bytes) / lay.bytes);
     auto* fn = rows_kernel<NT, GROUP>;
-    const uint32_t bit = 1u << (8 + 3 * (NT == 1 ? 0 : (NT == 2 ? 1 : 2)) + (GROUP == 32 ? 0 : (GROUP == 64 ? 1 : 2)));
+    constexpr uint32_t bit = 1u << (8 + (GROUP == 32 ? 0 : (GROUP == 64 ? 1 : 2)));
     if (!(h->limits_raised & bit)) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
             cudaGetLastError();
@@ -291,30 +303,22 @@ lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h
     return vocab_launch_err();
 }
 
-template <int NT>
-lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
-{
-    if (p.shift == 5) return launch<NT, 32>(p, maps, h, stream);
-    if (p.shift == 6) return launch<NT, 64>(p, maps, h, stream);
-    return launch<NT, 128>(p, maps, h, stream);
-}
-
 }  // namespace
 
 bool few_rows_fit(const LogitsParams& p)
 {
-    const int64_t rows = static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1), N = columns_for(rows);
-    if (rows > kFewRows || N * p.kblocks * 256 > kMaxShared) return false;
+    const int64_t rows = static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1), N = kFewRows;
+    if (rows > kFewRows || N * p.kblocks * 256 > kMaxShared) return false;   // (which leaves 1800 parts of a row)
     return kHead + RowsLayout(static_cast<int>(N), p.kblocks, p.groups).bytes +
                2 * StageLayout(kTile, p.shift, p.scale_bytes, p.zeros != nullptr).bytes <= kMaxShared;
 }
 
 lmloss_status launch_few_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    p.N = columns_for(static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1));
-    if (p.N == 8) return launch<1>(p, maps, h, stream);
-    if (p.N == 16) return launch<2>(p, maps, h, stream);
-    return launch<4>(p, maps, h, stream);
+    p.N = kFewRows;
+    if (p.shift == 5) return launch<kFewRows / 8, 32>(p, maps, h, stream);
+    if (p.shift == 6) return launch<kFewRows / 8, 64>(p, maps, h, stream);
+    return launch<kFewRows / 8, 128>(p, maps, h, stream);
 }
 
 }  // namespace lmloss
