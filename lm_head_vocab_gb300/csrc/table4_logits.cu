@@ -28,6 +28,7 @@ constexpr int kMany = 128;                   // operand rows of a block's produc
 constexpr uint32_t kHeader = 5120;           // barriers and factors, before the stages
 
 constexpr int kRows = 128;                   // rows of the table a block takes at once
+constexpr int kStageCols = 256;              // columns of it that a stage holds
 
 // The kernel's shapes, by N operand rows.  Up to 32 two blocks share an SM.
 template <int N>
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
     LogitsBarriers& b = *reinterpret_cast<LogitsBarriers*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const StageLayout lay(kRows, p.shift, p.scale_bytes, p.zeros != nullptr);
+    const StageLayout lay(kRows, kStageCols, p.shift, p.scale_bytes, p.zeros != nullptr);
     const uint32_t xbase = base + kHeader + p.qstages * p.stage_bytes;
     const int gs = 1 << p.shift, per_stage = kStageCols >> p.shift;
     const int stages = (p.kblocks + 1) / 2;
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                         wait_one(b.q_empty[q.slot], q.parity ^ 1u);
                         const uint32_t bar = smem_addr(&b.q_full[q.slot]);
                         mbar_arrive_expect_tx(bar, lay.copied);
-                        copy_table(p, lay, maps, st, tile / p.tblocks * kRows, base + kHeader + q.slot * p.stage_bytes, bar);
+                        copy_table(p, lay, maps, kRows, st, 1, tile / p.tblocks * kRows, base + kHeader + q.slot * p.stage_bytes, bar);
                         q.next(p.qstages);
                     }
             }
@@ -480,7 +481,7 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-bool table_maps(const lmloss_table4& t, int rows, TableMaps* maps)
+bool table_maps(const lmloss_table4& t, int rows, int columns, TableMaps* maps)
 {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
@@ -492,7 +493,7 @@ bool table_maps(const lmloss_table4& t, int rows, TableMaps* maps)
         return encode(to, type, 2, base, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
-    const int es = float_bytes(t.scale_dtype), n = kStageCols / t.group;
+    const int es = float_bytes(t.scale_dtype), n = columns / t.group;
     const int64_t G = (t.D + t.group - 1) / t.group;
     return map(&maps->values, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.values, (t.D + 1) / 2, t.V, t.ld_values, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B) &&
            map(&maps->scales, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, t.scales, t.V, G, t.ld_scales * es, rows,
@@ -503,7 +504,7 @@ bool table_maps(const lmloss_table4& t, int rows, TableMaps* maps)
 template <int N>
 lmloss_status launch_many_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    const StageLayout lay(kRows, p.shift, p.scale_bytes, p.zeros != nullptr);
+    const StageLayout lay(kRows, kStageCols, p.shift, p.scale_bytes, p.zeros != nullptr);
     // of the SM's 228 KB each block takes 1 more than it asks for
     const uint32_t shared = Shape<N>::kBlocks == 1 ? kMaxShared : kMaxShared / 2 - 1024;
     p.stage_bytes = lay.bytes;
@@ -593,10 +594,10 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.err = h->err;
         const int operands = T * (pairs ? 2 : 1);
         const bool few = few_rows_fit(p);
-        const int rows = few ? 256 : kRows;
+        const int rows = few ? kFewTile : kRows;
         p.vtiles = static_cast<int>((a->table.V + rows - 1) / rows);
         TableMaps maps{};
-        if (!table_maps(a->table, rows, &maps)) return LMLOSS_ERR_CUDA;
+        if (!table_maps(a->table, rows, few ? kFewCols : kStageCols, &maps)) return LMLOSS_ERR_CUDA;
         if (few) {
             st = launch_few_rows(p, maps, h, stream);
         } else {

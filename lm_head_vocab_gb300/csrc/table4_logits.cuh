@@ -9,7 +9,6 @@
 
 namespace lmloss {
 
-constexpr int kStageCols = 256;              // columns of the table a stage holds
 constexpr int kBlockCols = 128;              // columns that hidden rows are laid out by
 constexpr int kMaxStages = 8;
 constexpr uint32_t kMaxShared = 227 * 1024;
@@ -187,14 +186,14 @@ struct Ring {
     }
 };
 
-// Where a stage's parts begin, and what they hold: values [rows][128 bytes, 16-byte parts at
+// Where a stage's parts begin, and what they hold: values [runs of 256 columns][rows][128 bytes, 16-byte parts at
 // (part ^ row % 8)], scales and zeros [groups of the stage][rows].
 struct StageLayout {
     uint32_t scales, zeros, copied, bytes;
-    __host__ __device__ StageLayout(int rows, int shift, int scale_bytes, bool has_zeros)
+    __host__ __device__ StageLayout(int rows, int columns, int shift, int scale_bytes, bool has_zeros)
     {
-        const int n = kStageCols >> shift;
-        scales = rows * 128;
+        const int n = columns >> shift;
+        scales = rows * (columns / 2);
         zeros = scales + n * rows * scale_bytes;
         copied = zeros + (has_zeros ? n * rows : 0);
         bytes = (copied + 1023) / 1024 * 1024;
@@ -207,13 +206,14 @@ struct TableMaps {
     CUtensorMap values, scales, zeros;
 };
 
-// Copies of stage `st` of the tile at row v0, `copied` bytes, by one thread.  (As bulk copies, one a group, scales
-// took longer than the values: 128256 x 4096, no arithmetic, 63 us with them and 46 without.)
-__device__ __forceinline__ void copy_table(const LogitsParams& p, const StageLayout& lay, const TableMaps& maps, int st, int v0, uint32_t to,
-                                           uint32_t bar)
+// Copies of `runs` runs of 256 columns from 256 `run` on and their groups, for the tile at row v0, by one thread:
+// lay.copied bytes less the values of missing runs.  (As bulk copies, one a group, scales took longer than the
+// values: 128256 x 4096, no arithmetic, 63 us with them and 46 without.)
+__device__ __forceinline__ void copy_table(const LogitsParams& p, const StageLayout& lay, const TableMaps& maps, int rows, int run, int runs, int v0,
+                                           uint32_t to, uint32_t bar)
 {
-    const int g = st * (kStageCols >> p.shift);
-    tile_load_2d(to, &maps.values, st * 128, v0, bar);
+    const int g = (run * 256) >> p.shift;
+    for (int i = 0; i < runs; ++i) tile_load_2d(to + i * rows * 128, &maps.values, (run + i) * 128, v0, bar);
     tile_load_2d(to + lay.scales, &maps.scales, v0, g, bar);
     if (p.zeros) tile_load_2d(to + lay.zeros, &maps.zeros, v0, g, bar);
 }
@@ -221,6 +221,8 @@ __device__ __forceinline__ void copy_table(const LogitsParams& p, const StageLay
 // Whether the kernel of independent warps takes a call: up to kFewRows operand rows that fit into shared memory
 // beside two stages.
 bool few_rows_fit(const LogitsParams& p);
+// Its tiles, for the maps: rows, and columns of a stage.
+constexpr int kFewTile = 64, kFewCols = 1024;
 lmloss_status launch_few_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream);
 
 }  // namespace lmloss

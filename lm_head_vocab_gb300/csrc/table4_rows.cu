@@ -14,8 +14,7 @@
 namespace lmloss {
 namespace {
 
-constexpr int kTile = 256;                   // rows of the table a block takes at once
-constexpr int kSumWarps = 16;                // 32 rows of the tile each, and every second run of 128 columns
+constexpr int kSumWarps = 16;                // 32 of the tile's 64 rows each, and 128 of a stage's 1024 columns
 constexpr int kSumThreads = kSumWarps * 32;
 constexpr int kRowsThreads = kSumThreads + 32;
 constexpr uint32_t kHead = 1024;             // barriers and what is said of hidden rows, before the stages
@@ -29,14 +28,14 @@ struct __align__(16) RowsHead {
 static_assert(sizeof(RowsHead) <= kHead, "head");
 
 // Hidden rows [kblocks][N][256 bytes], 16-byte part i of a row at i ^ 4 (row % 2); sums [groups][N]; what warps
-// hand on [8][N][33].
+// hand on [16][N][33].
 struct RowsLayout {
     uint32_t sums, pads, bytes;
     __host__ __device__ RowsLayout(int N, int kblocks, int groups)
     {
         sums = N * kblocks * 256;
         pads = sums + groups * N * 4;
-        bytes = pads + 8 * N * 33 * 4;
+        bytes = pads + kSumWarps * N * 33 * 4;
     }
 };
 
@@ -113,15 +112,15 @@ template <int NT, int GROUP>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
 {
     constexpr int N = 8 * NT;
-    constexpr int kPerStage = kStageCols / GROUP, kUnits = GROUP / 32;   // groups of a stage; runs of 32 columns of a group
+    constexpr int kPerStage = kFewCols / GROUP, kUnits = GROUP / 32;   // groups of a stage; runs of 32 columns of a group
     extern __shared__ __align__(1024) unsigned char smem[];
     RowsHead& b = *reinterpret_cast<RowsHead*>(smem);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const StageLayout lay(kTile, p.shift, p.scale_bytes, p.zeros != nullptr);
+    const StageLayout lay(kFewTile, kFewCols, p.shift, p.scale_bytes, p.zeros != nullptr);
     const RowsLayout rl(N, p.kblocks, p.groups);
     unsigned char* const rows = smem + kHead + p.qstages * p.stage_bytes;
-    const int stages = (p.kblocks + 1) / 2;
+    const int stages = (p.kblocks + 7) / 8;
 
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -148,8 +147,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 for (int st = 0; st < stages; ++st) {
                     wait_one(b.empty[q.slot], q.parity ^ 1u);
                     const uint32_t bar = smem_addr(&b.full[q.slot]);
-                    mbar_arrive_expect_tx(bar, lay.copied);
-                    copy_table(p, lay, maps, st, tile * kTile, base + kHead + q.slot * p.stage_bytes, bar);
+                    const int runs = min(4, (p.kblocks - st * 8 + 1) / 2);
+                    mbar_arrive_expect_tx(bar, lay.copied - (4 - runs) * (kFewTile * 128));
+                    copy_table(p, lay, maps, kFewTile, st * 4, runs, tile * kFewTile, base + kHead + q.slot * p.stage_bytes, bar);
                     q.next(p.qstages);
                 }
         }
@@ -159,11 +159,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         if (p.hidden_dtype == LMLOSS_BF16) lay_out<Bf16>(p, b, rows, all_sums, N);
         else if (p.hidden_dtype == LMLOSS_FP16) lay_out<Fp16>(p, b, rows, all_sums, N);
         else lay_out<Fp32>(p, b, rows, all_sums, N);
-        const int half = warp >> 3, pair = warp & 7, g8 = lane >> 2, i4 = lane & 3;
-        const int r0 = pair * 32;
-        float* const pad = reinterpret_cast<float*>(rows + rl.pads) + pair * (N * 33);
+        const int half = warp & 1, block = warp & 7, team = warp >> 3, g8 = lane >> 2, i4 = lane & 3;   // block: of 128 columns of a stage
+        const int r0 = team * 32;
+        float* const pads = reinterpret_cast<float*>(rows + rl.pads) + team * 8 * (N * 33);
         // of the matrices that ldmatrix takes: rows 0-7 and 8-15 of one part, then of the next
-        const uint32_t words = base + kHead + (r0 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
+        const uint32_t words = base + kHead + (block >> 1) * (kFewTile * 128) + (r0 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
         uint32_t part_at[2];
 #pragma unroll
         for (int u2 = 0; u2 < 2; ++u2) part_at[u2] = ((half * 4 + u2 * 2 + (lane >> 4)) ^ (lane & 7)) << 4;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             for (int st = 0; st < stages; ++st) {
                 wait_one(b.full[q.slot], q.parity);
                 __syncwarp();
-                const int kb = 2 * st + half;
+                const int kb = 8 * st + block;
                 if (kb < p.kblocks) {
                     const uint32_t offset = q.slot * p.stage_bytes;
                     const unsigned char* const stage = smem + kHead + offset;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 #pragma unroll
                         for (int mt = 0; mt < 2; ++mt) ldmatrix4(w[u2][mt], words + offset + mt * 16 * 128 + part_at[u2]);
                     const int x_at = kb * (N * 256);
-                    const int g0 = half * (kPerStage / 2);   // the half's first group in the stage
+                    const int g0 = block * (kBlockCols / GROUP);   // the block's first group in the stage
                     float d[2][NT][4];
 #pragma unroll
                     for (int unit = 0; unit < 4; ++unit) {   // 32 columns
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                         // ---- a group's end: its sums, less the zero points', scaled
                         const int gl = g0 + unit / kUnits;
                         if ((unit + 1) % kUnits == 0 && st * kPerStage + gl < p.groups) {
-                            const int at = gl * kTile + r0 + g8;
+                            const int at = gl * kFewTile + r0 + g8;
                             float s[4], z[4];   // rows g8, + 8, + 16, + 24
                             if (p.scale_dtype == LMLOSS_FP16) {
 #pragma unroll
@@ -246,28 +246,32 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 if (lane == 0) mbar_arrive(smem_addr(&b.empty[q.slot]));
                 q.next(p.qstages);
             }
-            // ---- the two halves of the columns together, and out along the table's rows
-            auto at = [&](int mt, int nt, int k) -> float& { return pad[(nt * 8 + 2 * i4 + (k & 1)) * 33 + mt * 16 + (k >> 1) * 8 + g8]; };
-            if (half == 1) {
+            // ---- a team's eight warps together, and out along the table's rows: a warp a hidden row
+            {
+                float* const pad = pads + block * (N * 33);
 #pragma unroll
-                for (int i = 0; i < 2 * NT * 4; ++i) at(i / (NT * 4), i / 4 % NT, i % 4) = acc[i / (NT * 4)][i / 4 % NT][i % 4];
+                for (int i = 0; i < 2 * NT * 4; ++i) {
+                    const int mt = i / (NT * 4), nt = i / 4 % NT, k = i % 4;
+                    pad[(nt * 8 + 2 * i4 + (k & 1)) * 33 + mt * 16 + (k >> 1) * 8 + g8] = acc[mt][nt][k];
+                }
             }
-            asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
-            if (half == 0) {
+            asm volatile("bar.sync %0, 256;" ::"r"(team + 1) : "memory");
+            const int64_t v = static_cast<int64_t>(tile) * kFewTile + r0 + lane;
+            for (int n = block; n < p.T; n += 8) {
+                auto total = [&](int column) {
+                    float x = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2 * NT * 4; ++i) at(i / (NT * 4), i / 4 % NT, i % 4) += acc[i / (NT * 4)][i / 4 % NT][i % 4];
-            }
-            asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
-            const int64_t v = static_cast<int64_t>(tile) * kTile + r0 + lane;
-            if (v < p.V) {
-                for (int n = half; n < p.T; n += 2) {
-                    float x = pad[n * 33 + lane];
-                    if (p.pairs) x = fmaf(pad[(n + N / 2) * 33 + lane], 1.f / 2048.f, x);
+                    for (int w = 0; w < 8; ++w) x += pads[w * (N * 33) + column * 33 + lane];
+                    return x;
+                };
+                float x = total(n);
+                if (p.pairs) x = fmaf(total(n + N / 2), 1.f / 2048.f, x);
+                if (v < p.V) {
                     if (b.odd[n]) store_plain(p, n, v);
                     else store_logit(p, n, v, x * 0x1p24f / hidden_scale(__uint_as_float(b.top[n])) * p.scale);
                 }
             }
-            asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");   // before the next tile's
+            asm volatile("bar.sync %0, 256;" ::"r"(team + 1) : "memory");   // before the next tile's
         }
     }
     __syncthreads();
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 template <int NT, int GROUP>
 lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
-    const StageLayout lay(kTile, p.shift, p.scale_bytes, p.zeros != nullptr);
+    const StageLayout lay(kFewTile, kFewCols, p.shift, p.scale_bytes, p.zeros != nullptr);
     const RowsLayout rl(8 * NT, p.kblocks, p.groups);
     p.stage_bytes = lay.bytes;
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHead - rl.bytes) / lay.bytes);
@@ -310,7 +314,7 @@ bool few_rows_fit(const LogitsParams& p)
     const int64_t rows = static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1), N = kFewRows;
     if (rows > kFewRows || N * p.kblocks * 256 > kMaxShared) return false;   // (which leaves 1800 parts of a row)
     return kHead + RowsLayout(static_cast<int>(N), p.kblocks, p.groups).bytes +
-               2 * StageLayout(kTile, p.shift, p.scale_bytes, p.zeros != nullptr).bytes <= kMaxShared;
+               2 * StageLayout(kFewTile, kFewCols, p.shift, p.scale_bytes, p.zeros != nullptr).bytes <= kMaxShared;
 }
 
 lmloss_status launch_few_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
