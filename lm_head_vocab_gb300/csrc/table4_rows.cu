@@ -28,14 +28,14 @@ struct __align__(16) RowsHead {
 static_assert(sizeof(RowsHead) <= kHead, "head");
 
 // Hidden rows [kblocks][N][256 bytes], 16-byte part i of a row at i ^ 4 (row % 2); sums [groups][N]; what warps
-// hand on [16][N][33].
+// hand on, of tiles in turn [2][16][operand rows in use][33].
 struct RowsLayout {
     uint32_t sums, pads, bytes;
-    __host__ __device__ RowsLayout(int N, int kblocks, int groups)
+    __host__ __device__ RowsLayout(int N, int used, int kblocks, int groups)
     {
         sums = N * kblocks * 256;
         pads = sums + groups * N * 4;
-        bytes = pads + kSumWarps * N * 33 * 4;
+        bytes = pads + 2 * kSumWarps * used * 33 * 4;
     }
 };
 
@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const StageLayout lay(kFewTile, kFewCols, p.shift, p.scale_bytes, p.zeros != nullptr);
-    const RowsLayout rl(N, p.kblocks, p.groups);
+    const int used = p.pairs ? 2 * p.T : p.T;   // operand rows
+    const RowsLayout rl(N, used, p.kblocks, p.groups);
     unsigned char* const rows = smem + kHead + p.qstages * p.stage_bytes;
     const int stages = (p.kblocks + 7) / 8;
 
@@ -161,7 +162,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         else lay_out<Fp32>(p, b, rows, all_sums, N);
         const int half = warp & 1, block = warp & 7, team = warp >> 3, g8 = lane >> 2, i4 = lane & 3;   // block: of 128 columns of a stage
         const int r0 = team * 32;
-        float* const pads = reinterpret_cast<float*>(rows + rl.pads) + team * 8 * (N * 33);
+        float* pads = reinterpret_cast<float*>(rows + rl.pads) + team * 8 * (used * 33);
+        const int other_pads = kSumWarps * used * 33;
+        int turn = 0;
         // of the matrices that ldmatrix takes: rows 0-7 and 8-15 of one part, then of the next
         const uint32_t words = base + kHead + (block >> 1) * (kFewTile * 128) + (r0 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
         uint32_t part_at[2];
@@ -246,32 +249,33 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 if (lane == 0) mbar_arrive(smem_addr(&b.empty[q.slot]));
                 q.next(p.qstages);
             }
-            // ---- a team's eight warps together, and out along the table's rows: a warp a hidden row
-            {
-                float* const pad = pads + block * (N * 33);
+            // ---- a team's eight warps together, and out along the table's rows, a warp a hidden row; the other warps
+            // go on to the next tile, whose sums go elsewhere
+            float* const here = pads + turn * other_pads;
+            turn ^= 1;
 #pragma unroll
-                for (int i = 0; i < 2 * NT * 4; ++i) {
-                    const int mt = i / (NT * 4), nt = i / 4 % NT, k = i % 4;
-                    pad[(nt * 8 + 2 * i4 + (k & 1)) * 33 + mt * 16 + (k >> 1) * 8 + g8] = acc[mt][nt][k];
-                }
+            for (int i = 0; i < 2 * NT * 4; ++i) {
+                const int mt = i / (NT * 4), nt = i / 4 % NT, k = i % 4, n = nt * 8 + 2 * i4 + (k & 1);
+                // the place of a pair's lower part: behind all upper ones
+                const int slot = p.pairs && n >= N / 2 ? n - N / 2 + p.T : n;
+                if (p.pairs ? n % (N / 2) < p.T : n < p.T) here[(block * used + slot) * 33 + mt * 16 + (k >> 1) * 8 + g8] = acc[mt][nt][k];
             }
             asm volatile("bar.sync %0, 256;" ::"r"(team + 1) : "memory");
             const int64_t v = static_cast<int64_t>(tile) * kFewTile + r0 + lane;
             for (int n = block; n < p.T; n += 8) {
-                auto total = [&](int column) {
+                auto total = [&](int slot) {
                     float x = 0.f;
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) x += pads[w * (N * 33) + column * 33 + lane];
+                    for (int w = 0; w < 8; ++w) x += here[(w * used + slot) * 33 + lane];
                     return x;
                 };
                 float x = total(n);
-                if (p.pairs) x = fmaf(total(n + N / 2), 1.f / 2048.f, x);
+                if (p.pairs) x = fmaf(total(n + p.T), 1.f / 2048.f, x);
                 if (v < p.V) {
                     if (b.odd[n]) store_plain(p, n, v);
                     else store_logit(p, n, v, x * 0x1p24f / hidden_scale(__uint_as_float(b.top[n])) * p.scale);
                 }
             }
-            asm volatile("bar.sync %0, 256;" ::"r"(team + 1) : "memory");   // before the next tile's
         }
     }
     __syncthreads();
@@ -290,7 +294,7 @@ template <int NT, int GROUP>
 lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
     const StageLayout lay(kFewTile, kFewCols, p.shift, p.scale_bytes, p.zeros != nullptr);
-    const RowsLayout rl(8 * NT, p.kblocks, p.groups);
+    const RowsLayout rl(8 * NT, p.pairs ? 2 * p.T : p.T, p.kblocks, p.groups);
     p.stage_bytes = lay.bytes;
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHead - rl.bytes) / lay.bytes);
     auto* fn = rows_kernel<NT, GROUP>;
@@ -313,7 +317,7 @@ bool few_rows_fit(const LogitsParams& p)
 {
     const int64_t rows = static_cast<int64_t>(p.T) * (p.pairs ? 2 : 1), N = kFewRows;
     if (rows > kFewRows || N * p.kblocks * 256 > kMaxShared) return false;   // (which leaves 1800 parts of a row)
-    return kHead + RowsLayout(static_cast<int>(N), p.kblocks, p.groups).bytes +
+    return kHead + RowsLayout(static_cast<int>(N), static_cast<int>(rows), p.kblocks, p.groups).bytes +
                2 * StageLayout(kFewTile, kFewCols, p.shift, p.scale_bytes, p.zeros != nullptr).bytes <= kMaxShared;
 }
 
