@@ -303,81 +303,99 @@ __global__ void __launch_bounds__(256) lookup_words_kernel(const __grid_constant
     }
 }
 
-// A thread takes the 8 columns (4 of fp32) of one 16-byte vector of a row that is written, kDeep rows; where rows
-// start inside a vector, so does the first of a row, and its numbers come from two words and two groups.
+// Rows at any alignment: a warp takes 32 neighbouring words of kDeep rows and writes the 31 vectors (of fp32, pairs of
+// vectors) that lie on 16-byte boundaries of the row, each put together from a word's numbers and the last of the word
+// before, which the neighbouring thread has.  The warp before ends with this one's first word.
+// (By vectors on their own, with two words, two groups and a scale for each number, it took 45 instructions a
+// number: 32003 x 1001 to fp32, 79 us.)
 template <class R, class S>
-__global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ LookupParams p)
+__global__ void __launch_bounds__(256) lookup_shifted_kernel(const __grid_constant__ LookupParams p)
 {
-    constexpr int E = 16 / R::kBytes;
+    constexpr int kWords = 8 * R::kBytes / 4;                // of 8 numbers in the result's type
+    constexpr int kUnit = 16 / R::kBytes;                    // numbers of a vector
     const Table4& t = p.t;
-    const unsigned down = blockIdx.x / static_cast<unsigned>(p.blocks_across);
-    const int along = static_cast<int>(blockIdx.x - down * static_cast<unsigned>(p.blocks_across));
-    const int vec = (along << p.log_across) + (threadIdx.x & ((1 << p.log_across) - 1));
-    const int rows_a_pass = 256 >> p.log_across;
-    const int64_t row0 = static_cast<int64_t>(down) * (kDeep * rows_a_pass) + (threadIdx.x >> p.log_across);
-
+    const int lane = threadIdx.x & 31;
+    const unsigned warp = blockIdx.x * 8u + (threadIdx.x >> 5), down = warp / static_cast<unsigned>(p.blocks_across);
+    const int along = static_cast<int>(warp - down * static_cast<unsigned>(p.blocks_across));
+    const int k8 = along * 31 + lane - 1, c = k8 * 8;        // the thread's word and its first column
+    const bool in = k8 >= 0 && c < t.D;
+    const int row0 = static_cast<int>(down) * kDeep;
+    if (row0 >= p.T) return;
+    const typename S::raw* const scales = static_cast<const typename S::raw*>(t.scales) + static_cast<int64_t>(in ? c >> t.shift : 0) * t.ld_scales;
+    const uint8_t* const zeros = t.zeros ? t.zeros + static_cast<int64_t>(in ? c >> t.shift : 0) * t.ld_zeros : nullptr;
     int64_t id[kDeep];
     uint32_t word[kDeep];
-    float s[kDeep][2], z[kDeep][2];
-    int c0[kDeep], border[kDeep];   // columns from `border` on belong to the second group
+    float s[kDeep], z[kDeep];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
-        const int64_t row = row0 + k * rows_a_pass;
+        const int row = row0 + k;
         id[k] = row >= p.T ? LMLOSS_IGNORE_INDEX
                            : (p.ids32 ? static_cast<int64_t>(static_cast<const int32_t*>(p.ids)[row]) : static_cast<const int64_t*>(p.ids)[row]);
     }
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
-        const int64_t row = row0 + k * rows_a_pass;
-        const uintptr_t out = reinterpret_cast<uintptr_t>(p.rows) + static_cast<uintptr_t>(row * p.ld_rows) * R::kBytes;
-        c0[k] = vec * E - static_cast<int>((out & 15u) / R::kBytes);
         word[k] = 0;
-        s[k][0] = s[k][1] = z[k][0] = z[k][1] = 0.f;
-        border[k] = E;
-        if (id[k] < 0 || id[k] >= t.V || c0[k] >= t.D) continue;
-        const uint8_t* const q = t.values + id[k] * t.ld_values;
-        const int first = max(c0[k], 0), last = min(c0[k] + E, t.D) - 1;
-        const int at = first >> 3;
-        const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(q) + at);
-        const uint32_t w1 = (last >> 3) != at ? __ldg(reinterpret_cast<const uint32_t*>(q) + at + 1) : 0u;
-        word[k] = __funnelshift_r(w0, w1, 4 * (first & 7));
-        if (c0[k] < 0) word[k] <<= 4 * (first - c0[k]);   // the row's first column in its place of the vector
-        const int g0 = first >> t.shift, g1 = last >> t.shift;
-        s[k][0] = s[k][1] = table4_scale<S>(t, g0, id[k]);
-        z[k][0] = z[k][1] = table4_zero(t, g0, id[k]);
-        if (g1 != g0) {
-            s[k][1] = table4_scale<S>(t, g1, id[k]);
-            z[k][1] = table4_zero(t, g1, id[k]);
-            border[k] = (g1 << t.shift) - c0[k];
+        s[k] = z[k] = 0.f;
+        if (id[k] != LMLOSS_IGNORE_INDEX && (id[k] < 0 || id[k] >= t.V)) {
+            set_error(p.err, kErrBadTarget);
+            s[k] = NAN;
+        } else if (in && id[k] >= 0) {
+            word[k] = __ldg(reinterpret_cast<const uint32_t*>(t.values + id[k] * t.ld_values + (c >> 1)));
+            s[k] = S::widen(__ldg(scales + id[k]));
+            z[k] = zeros ? static_cast<float>(__ldg(zeros + id[k])) : 8.f;
         }
     }
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
-        const int64_t row = row0 + k * rows_a_pass;
-        if (row >= p.T || c0[k] >= t.D) continue;
-        typename R::raw* const out = static_cast<typename R::raw*>(p.rows) + row * p.ld_rows + c0[k];
-        const bool none = id[k] < 0 || id[k] >= t.V;
-        if (none && id[k] != LMLOSS_IGNORE_INDEX) {
-            set_error(p.err, kErrBadTarget);
-            s[k][0] = s[k][1] = NAN;
-        }
-        float x[E];
+        const int row = row0 + k;
+        if (row >= p.T) break;
+        typename R::raw* const out = static_cast<typename R::raw*>(p.rows) + static_cast<int64_t>(row) * p.ld_rows;
+        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / R::kBytes);   // numbers of the row's first vector before it
+        // 2^23 + q, less 2^23 + z: exact
+        const float less = 8388608.f + z[k];
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const bool second = i >= border[k];
-            // 2^23 + q, less 2^23 + z: exact
-            const float n = __uint_as_float((word[k] >> (4 * i) & 15u) | 0x4b000000u) - (8388608.f + (second ? z[k][1] : z[k][0]));
-            x[i] = p.scale * ((second ? s[k][1] : s[k][0]) * n);
-            if (none && !(s[k][0] != s[k][0])) x[i] = 0.f;
-        }
-        if (c0[k] >= 0 && c0[k] + E <= t.D) {
-            Pack<R, E> v;
-            v.set_all(x);
-            v.store(out);
-        } else {
+        for (int i = 0; i < 8; ++i) x[i] = p.scale * (s[k] * (__uint_as_float((word[k] >> (4 * i) & 15u) | 0x4b000000u) - less));
+        Pack<R, 8> own;
+        own.set_all(x);
+        // the last `off` of the word before, then this one's: w[0] begins 16 bytes before this word's numbers
+        uint32_t w[kWords + 4];
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (c0[k] + i >= 0 && c0[k] + i < t.D) out[i] = static_cast<typename R::raw>(R::round(x[i]));
+        for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, own.w[kWords - 4 + i], 1);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[4 + i] = own.w[i];
+        const int sh = 16 - off * R::kBytes;   // bytes to leave out: 16 where rows are aligned
+        if (sh & 16) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = w[i + 4];
+        }
+        if (sh & 8) {
+#pragma unroll
+            for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
+        }
+        if (sh & 4) {
+#pragma unroll
+            for (int i = 0; i < kWords + 3; ++i) w[i] = w[i + 1];
+        }
+        Pack<R, 8> v;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v.w[i] = R::kBytes == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], (sh & 2) * 8);
+        // numbers [first, first + 8) of the row; the thread behind its last word has what that word leaves
+        const int first = c - off;
+        if (lane == 0 || first >= t.D) continue;
+#pragma unroll
+        for (int u = 0; u < 8 / kUnit; ++u) {
+            const int from = first + u * kUnit;
+            if (from >= 0 && from + kUnit <= t.D) {
+                *reinterpret_cast<uint4*>(out + from) = make_uint4(v.w[4 * u], v.w[4 * u + 1], v.w[4 * u + 2], v.w[4 * u + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kUnit; ++i)
+                    if (from + i >= 0 && from + i < t.D) {
+                        if constexpr (R::kBytes == 4) out[from + i] = v.w[4 * u + i];
+                        else out[from + i] = static_cast<typename R::raw>(v.w[4 * u + i / 2] >> (16 * (i & 1)));
+                    }
+            }
         }
     }
 }
@@ -472,10 +490,16 @@ lmloss_status lmloss_table4_lookup(lmloss_vocab_handle h, const lmloss_table4_lo
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
     const int E = 16 / float_bytes(a->rows_dtype);
-    // (a thread of the odd half of 16 columns past the end needs its neighbour's group: 16 columns lie in one)
+    // (of fp32, 16 columns at a time: they lie in one group)
     const bool words = a->table.D % 8 == 0 && (a->table.D % 16 == 0 || E == 8) && aligned16(a->rows) && a->ld_rows % E == 0;
-    const Spread all(words ? a->table.D / 8 : (a->table.D + 2 * E - 2) / E, a->T);   // a vector more where a row starts inside one
-    const int64_t down = kDeep << (8 - all.log_across), most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
+    Spread all(a->table.D / 8, a->T);
+    int64_t down = kDeep << (8 - all.log_across), most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
+    if (!words) {
+        // warps: 31 words each, and one behind the last for what shifts out of it
+        all.blocks_across = static_cast<int>(((a->table.D + 7) / 8 + 1 + 30) / 31);
+        down = kDeep;
+        most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
+    }
     for (int64_t t0 = 0; t0 < a->T; t0 += most) {
         LookupParams p{};
         p.t = table4_params(a->table);
@@ -488,11 +512,12 @@ lmloss_status lmloss_table4_lookup(lmloss_vocab_handle h, const lmloss_table4_lo
         p.log_across = all.log_across;
         p.blocks_across = all.blocks_across;
         p.err = h->err;
-        const unsigned grid = static_cast<unsigned>(all.blocks_across * ((p.T + down - 1) / down));
+        const int64_t pieces = all.blocks_across * ((p.T + down - 1) / down);   // blocks, or warps
+        const unsigned grid = static_cast<unsigned>(words ? pieces : (pieces + 7) / 8);
         by_type(a->rows_dtype, [&](auto r) {
             by_type(a->table.scale_dtype, [&](auto s) {
                 if (words) lookup_words_kernel<decltype(r), decltype(s)><<<grid, 256, 0, stream>>>(p);
-                else lookup_kernel<decltype(r), decltype(s)><<<grid, 256, 0, stream>>>(p);
+                else lookup_shifted_kernel<decltype(r), decltype(s)><<<grid, 256, 0, stream>>>(p);
             });
         });
         const lmloss_status launched = vocab_launch_err();
