@@ -82,10 +82,56 @@ __device__ __forceinline__ float settle(float q, float a, float s)
     return q;
 }
 
-// A thread takes 8 columns; a group's 4, 8 or 16 neighbouring threads share its extremes.  Quotients come from
-// one reciprocal, and are settled where one of the eight lies within 2^-20 of a half: often, with bf16 weights, whose
-// largest is a multiple of seven in one group of seven.  (With IEEE quotients, and halves settled in fp64, 128256 x 4096
-// took 1.7 ms.)
+// x / D rounded once, where the remainder does not underflow: a product with the rounded reciprocal is one step off at
+// most, and its exact remainder settles that (Markstein, 1990; checked for 7 and 15 over all significands).
+template <int D>
+__device__ __forceinline__ float quotient_by(float x)
+{
+    if (x < 0x1p-90f) return __fdiv_rn(x, static_cast<float>(D));
+    constexpr float r = 1.f / D;
+    const float q = __fmul_rn(x, r);
+    return fmaf(fmaf(-q, static_cast<float>(D), x), r, q);
+}
+
+// The largest (or least) of each of kDeep rows over a group's threads: the thread of quad q leaves with row q's.
+template <class F>
+__device__ __forceinline__ float over_group(const float (&x)[kDeep], int lanes, F&& most)
+{
+    static_assert(kDeep == 4, "a quad's threads");
+    const bool two = threadIdx.x & 2, one = threadIdx.x & 1;
+    const float a = most(two ? x[2] : x[0], __shfl_xor_sync(0xffffffffu, two ? x[0] : x[2], 2));
+    const float b = most(two ? x[3] : x[1], __shfl_xor_sync(0xffffffffu, two ? x[1] : x[3], 2));
+    float m = most(one ? b : a, __shfl_xor_sync(0xffffffffu, one ? a : b, 1));
+    for (int o = 4; o < lanes; o <<= 1) m = most(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// Two numbers of 16 bits at once, as max and min that keep a NaN
+template <class W>
+__device__ __forceinline__ uint32_t keep_max2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (W::kIndex == Bf16::kIndex) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <class W>
+__device__ __forceinline__ uint32_t keep_min2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (W::kIndex == Bf16::kIndex) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A thread takes 8 columns of kDeep rows; a group's 4, 8 or 16 neighbouring threads share its extremes, and of each
+// quad a thread works out one row's scale, reciprocal and zero point.  The quotients, in pairs:
+//   weights and scales of 16 bits   two corrections bring a quotient within 2^-22 of a w / s that is n + 1/2 or at
+//                                   least 2^-14 away from it (of significands below 2^11, w / s - n - 1/2 has a
+//                                   denominator below 2^14), and exactly to n + 1/2: nothing is left to settle
+//   others                          one product, settled where one of the eight lies within 2^-20 of a half
+// Quotients of 16-bit weights are halves often (their largest is a multiple of seven in one group of seven): with one
+// product, settled, and extremes of one row at a time, 128256 x 4096 took 418 us.
 template <class W, class S, bool ZEROS>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantizeParams p)
 {
@@ -124,96 +170,111 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
     float lo[kDeep], hi[kDeep];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
-        lo[k] = hi[k] = 0.f;
+        if constexpr (W::kBytes == 2) {
+            uint32_t high = 0, low = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = in[k].get(i);
-            if (ZEROS) {
-                lo[k] = keep_min(lo[k], x);
-                hi[k] = keep_max(hi[k], x);
-            } else {
-                hi[k] = keep_max(hi[k], fabsf(x));
+            for (int i = 0; i < 4; ++i) {
+                high = keep_max2<W>(high, ZEROS ? in[k].w[i] : in[k].w[i] & 0x7fff7fffu);
+                if (ZEROS) low = keep_min2<W>(low, in[k].w[i]);
+            }
+            hi[k] = keep_max(W::widen(static_cast<uint16_t>(high)), W::widen(static_cast<uint16_t>(high >> 16)));
+            lo[k] = ZEROS ? keep_min(W::widen(static_cast<uint16_t>(low)), W::widen(static_cast<uint16_t>(low >> 16))) : 0.f;
+        } else {
+            lo[k] = hi[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = in[k].get(i);
+                hi[k] = keep_max(hi[k], ZEROS ? x : fabsf(x));
+                if (ZEROS) lo[k] = keep_min(lo[k], x);
             }
         }
-        for (int o = 1; o < lanes; o <<= 1) {
-            hi[k] = keep_max(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
-            if (ZEROS) lo[k] = keep_min(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
+    }
+    // this thread's row of the group
+    constexpr float kMagic = 12582912.f;   // x + kMagic - kMagic is the whole number nearest to x
+    const int quad = threadIdx.x & 3;
+    const float top = over_group(hi, lanes, keep_max), bottom = ZEROS ? over_group(lo, lanes, keep_min) : 0.f, range = top - bottom;
+    float own = S::widen(static_cast<typename S::raw>(S::round(quotient_by<ZEROS ? 15 : 7>(range)))), own_z = ZEROS ? 0.f : 8.f;
+    // not finite: a weight, or the scale in its type.  (top - bottom may pass fp32's range too.)
+    const bool bad = !(own < INFINITY) || !(top < INFINITY) || !(bottom > -INFINITY);
+    // a scale whose reciprocal passes fp32's range is brought up, with its weights
+    const float up = own < 0x1p-100f && W::kIndex != Fp16::kIndex ? 0x1p100f : 1.f;
+    float own_r = __frcp_rn(own * up);
+    if (ZEROS && !bad && own > 0.f) {
+        const float below = -bottom * up;
+        own_z = fminf(fmaxf(settle(fmaf(below, own_r, kMagic) - kMagic, below, own * up), 0.f), 15.f);
+    }
+    // a scale that lost bits in its type's subnormals leaves quotients out of range: told by the sign
+    if (!(range * up < own * up * (ZEROS ? 15.2f : 7.4f))) own_r = -own_r;
+    {
+        const int64_t v = v0 + quad * rows_a_pass;
+        if ((threadIdx.x & (lanes - 1)) < 4 && v < p.rows && c - quad * 8 < t.D) {
+            static_cast<typename S::raw*>(t.scales)[g * t.ld_scales + v] = static_cast<typename S::raw>(S::round(bad ? NAN : own));
+            if (ZEROS) t.zeros[g * t.ld_zeros + v] = static_cast<uint8_t>(own_z);
+            if (bad) set_error(p.err, kErrRange);
         }
     }
-    // scales and their reciprocals: of four neighbouring threads each divides for one of the rows
-    static_assert(kDeep == 4, "a quad's threads");
-    const int quad = threadIdx.x & 3;
-    const float range0 = ZEROS ? hi[0] - lo[0] : hi[0], range1 = ZEROS ? hi[1] - lo[1] : hi[1];
-    const float range2 = ZEROS ? hi[2] - lo[2] : hi[2], range3 = ZEROS ? hi[3] - lo[3] : hi[3];
-    const float range = quad & 2 ? (quad & 1 ? range3 : range2) : (quad & 1 ? range1 : range0);
-    const float own = S::widen(static_cast<typename S::raw>(S::round(__fdiv_rn(range, ZEROS ? 15.f : 7.f))));
-    // (a scale whose reciprocal passes fp32's range is brought up, with its weights)
-    const float own_r = __fdiv_rn(1.f, own < 0x1p-100f ? own * 0x1p100f : own);
+    if (bad) own = 0.f;
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
         const int64_t v = v0 + k * rows_a_pass;
-        const float s = __shfl_sync(0xffffffffu, own, (threadIdx.x & 28) + k), r = __shfl_sync(0xffffffffu, own_r, (threadIdx.x & 28) + k);
-        // not finite: a weight, or the scale in its type.  (hi - lo may pass fp32's range too.)
-        const bool bad = !(s < INFINITY) || !(hi[k] < INFINITY) || (ZEROS && !(lo[k] > -INFINITY));
+        const int from = (threadIdx.x & 28) + k;
+        float s = __shfl_sync(0xffffffffu, own, from), r = __shfl_sync(0xffffffffu, own_r, from);
+        const float z = ZEROS ? __shfl_sync(0xffffffffu, own_z, from) : 8.f;
         if (v >= p.rows || c >= t.D) continue;
-        float z = ZEROS ? 0.f : 8.f, x[8];
-        if (bad || s == 0.f) {
+        const bool none = s == 0.f, lost = r < 0.f;
+        r = fabsf(r);
+        if (s < 0x1p-100f && W::kIndex != Fp16::kIndex) {
+            float a[8];
+            s *= 0x1p100f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        } else {
-            float su = s;
-            if (s < 0x1p-100f && W::kIndex != Fp16::kIndex) {
-                float a[8];
-                su = s * 0x1p100f;
-                lo[k] *= 0x1p100f;
-                hi[k] *= 0x1p100f;
+            for (int i = 0; i < 8; ++i) a[i] = in[k].get(i) * 0x1p100f;
+            in[k].set_all(a);
+        }
+        // pairs of columns i and i + 4
+        const uint64_t s2 = f2_pack(-s, -s), r2 = f2_pack(r, r), magic2 = f2_pack(kMagic, kMagic), unmagic2 = f2_pack(-kMagic, -kMagic);
+        uint64_t x2[4];
+        float most = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] = in[k].get(i) * 0x1p100f;
-                in[k].set_all(a);
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t a = f2_pack(in[k].get(i), in[k].get(i + 4));
+            if constexpr (W::kBytes == 2 && S::kBytes == 2) {
+                const uint64_t q = f2_mul(a, r2);
+                x2[i] = f2_add(f2_add(f2_fma(f2_fma(q, s2, a), r2, q), magic2), unmagic2);
+            } else {
+                x2[i] = f2_add(f2_fma(a, r2, magic2), unmagic2);
+                float e0, e1;
+                f2_unpack(f2_fma(x2[i], s2, a), e0, e1);
+                most = fmaxf(fmaxf(most, fabsf(e0)), fabsf(e1));
             }
-            constexpr float kMagic = 12582912.f;
-            float most = 0.f, least = -8.f, largest = 7.f;
-            if (ZEROS) {
-                z = fmaf(-lo[k], r, kMagic) - kMagic;
-                most = fabsf(fmaf(-z, su, -lo[k]));
-            }
+        }
+        const bool half = (W::kBytes != 2 || S::kBytes != 2) && !(most < s * 0.4999995f);
+        if (ZEROS || half || lost) {
+            // (the sum is one more than 15 where both ends round up)
+            const float least = -z, largest = 15.f - z;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = in[k].get(i);
-                x[i] = fmaf(a, r, kMagic) - kMagic;
-                most = fmaxf(most, fabsf(fmaf(-x[i], su, a)));
-            }
-            // (next to a half, or with a scale that lost bits in its type's subnormals)
-            const bool settle_all = !(most < su * 0.4999995f);
-            if (settle_all || !((ZEROS ? hi[k] - lo[k] : hi[k]) < su * (ZEROS ? 15.2f : 7.4f))) {
-                if (ZEROS) {
-                    z = fminf(fmaxf(settle(z, -lo[k], su), 0.f), 15.f);
-                    least = -z;
-                    largest = 15.f - z;
+            for (int i = 0; i < 4; ++i) {
+                float x[2];
+                f2_unpack(x2[i], x[0], x[1]);
+                if (half || lost) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) x[e] = fmaxf(settle(x[e], in[k].get(i + 4 * e), s), least);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(settle(x[i], in[k].get(i), su), least), largest);
-            } else if (ZEROS) {
-                // (one more than 15 where both ends round up)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fminf(x[i], 15.f - z);
+                x2[i] = f2_pack(fminf(x[0], largest), fminf(x[1], largest));
             }
         }
         // four numbers make one below 2^16, exact in fp32; z is added to all four at once
-        const float low = fmaf(z, 4369.f, fmaf(fmaf(fmaf(x[3], 16.f, x[2]), 16.f, x[1]), 16.f, x[0]));
-        const float high = fmaf(z, 4369.f, fmaf(fmaf(fmaf(x[7], 16.f, x[6]), 16.f, x[5]), 16.f, x[4]));
-        uint32_t word = __byte_perm(__float_as_uint(low + 8388608.f), __float_as_uint(high + 8388608.f), 0x5410);
+        const uint64_t sixteen2 = f2_pack(16.f, 16.f);
+        const float base = fmaf(z, 4369.f, 8388608.f);
+        float low, high;
+        f2_unpack(f2_add(f2_fma(f2_fma(f2_fma(x2[3], sixteen2, x2[2]), sixteen2, x2[1]), sixteen2, x2[0]), f2_pack(base, base)), low, high);
+        uint32_t word = __byte_perm(__float_as_uint(low), __float_as_uint(high), 0x5410);
+        if (none) word = ZEROS ? 0u : 0x88888888u;   // zeros, or not finite
         uint8_t* out = t.values + v * t.ld_values + c / 2;
         if (c + 8 <= t.D) {
             *reinterpret_cast<uint32_t*>(out) = word;
         } else {
             word &= (1u << (4 * (t.D - c))) - 1u;
             for (int i = 0; c + 2 * i < t.D; ++i) out[i] = static_cast<uint8_t>(word >> (8 * i));
-        }
-        if ((c & ((1 << t.shift) - 1)) == 0) {
-            static_cast<typename S::raw*>(t.scales)[g * t.ld_scales + v] = static_cast<typename S::raw>(S::round(bad ? NAN : s));
-            if (ZEROS) t.zeros[g * t.ld_zeros + v] = static_cast<uint8_t>(z);
-            if (bad) set_error(p.err, kErrRange);
         }
     }
 }
