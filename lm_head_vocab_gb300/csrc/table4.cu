@@ -67,6 +67,7 @@ struct QuantizeParams {
     const unsigned char* weight_end;
     int64_t ld;
     int64_t rows;
+    int aligned;                 // rows begin on 16-byte boundaries
     int log_across, blocks_across;
     int* err;
 };
@@ -102,7 +103,8 @@ __device__ __forceinline__ float over_group(const float (&x)[kDeep], int lanes, 
     const float a = most(two ? x[2] : x[0], __shfl_xor_sync(0xffffffffu, two ? x[0] : x[2], 2));
     const float b = most(two ? x[3] : x[1], __shfl_xor_sync(0xffffffffu, two ? x[1] : x[3], 2));
     float m = most(one ? b : a, __shfl_xor_sync(0xffffffffu, one ? a : b, 1));
-    for (int o = 4; o < lanes; o <<= 1) m = most(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lanes > 4) m = most(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    if (lanes > 8) m = most(m, __shfl_xor_sync(0xffffffffu, m, 8));
     return m;
 }
 
@@ -142,19 +144,20 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
     const int rows_a_pass = 256 >> p.log_across;
     const int64_t v0 = down * (kDeep * rows_a_pass) + (threadIdx.x >> p.log_across);
     const int lanes = (1 << t.shift) / 8, g = c >> t.shift;
+    const int rows = static_cast<int>(min(p.rows - v0, static_cast<int64_t>(kDeep * rows_a_pass)));   // from v0 on
+    const bool whole = c + 8 <= t.D;
     const unsigned char* const base = static_cast<const unsigned char*>(p.weight);
-    const bool aligned = ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(p.ld * W::kBytes)) & 15u) == 0;
+    const unsigned char* at = base + (v0 * p.ld + c) * W::kBytes;
+    const int64_t step = p.ld * rows_a_pass * W::kBytes;
 
     Pack<W, 8> in[kDeep];
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-        const int64_t v = v0 + k * rows_a_pass;
+    for (int k = 0; k < kDeep; ++k, at += step) {
         in[k].zero();
-        if (v >= p.rows || c >= t.D) continue;
-        const unsigned char* at = base + (v * p.ld + c) * W::kBytes;
-        if (aligned && c + 8 <= t.D) {
+        if (k * rows_a_pass >= rows) continue;
+        if (p.aligned && whole) {
             in[k].load(at);
-        } else if (inside_blocks<W, 8>(at, base, p.weight_end) && c + 8 <= t.D) {
+        } else if (whole && inside_blocks<W, 8>(at, base, p.weight_end)) {
             constexpr int kVecs = 8 * W::kBytes / 16 + 1;
             const uint4* a = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(15));
             uint4 x[kVecs];
@@ -197,80 +200,74 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Q
     // not finite: a weight, or the scale in its type.  (top - bottom may pass fp32's range too.)
     const bool bad = !(own < INFINITY) || !(top < INFINITY) || !(bottom > -INFINITY);
     // a scale whose reciprocal passes fp32's range is brought up, with its weights
-    const float up = own < 0x1p-100f && W::kIndex != Fp16::kIndex ? 0x1p100f : 1.f;
+    const bool tiny = own < 0x1p-100f && W::kIndex != Fp16::kIndex;
+    const float up = tiny ? 0x1p100f : 1.f;
     float own_r = __frcp_rn(own * up);
     if (ZEROS && !bad && own > 0.f) {
         const float below = -bottom * up;
         own_z = fminf(fmaxf(settle(fmaf(below, own_r, kMagic) - kMagic, below, own * up), 0.f), 15.f);
     }
-    // a scale that lost bits in its type's subnormals leaves quotients out of range: told by the sign
-    if (!(range * up < own * up * (ZEROS ? 15.2f : 7.4f))) own_r = -own_r;
-    {
+    if ((threadIdx.x & (lanes - 1)) < 4 && quad * rows_a_pass < rows && c - quad * 8 < t.D) {
         const int64_t v = v0 + quad * rows_a_pass;
-        if ((threadIdx.x & (lanes - 1)) < 4 && v < p.rows && c - quad * 8 < t.D) {
-            static_cast<typename S::raw*>(t.scales)[g * t.ld_scales + v] = static_cast<typename S::raw>(S::round(bad ? NAN : own));
-            if (ZEROS) t.zeros[g * t.ld_zeros + v] = static_cast<uint8_t>(own_z);
-            if (bad) set_error(p.err, kErrRange);
-        }
+        static_cast<typename S::raw*>(t.scales)[g * t.ld_scales + v] = static_cast<typename S::raw>(S::round(bad ? NAN : own));
+        if (ZEROS) t.zeros[g * t.ld_zeros + v] = static_cast<uint8_t>(own_z);
+        if (bad) set_error(p.err, kErrRange);
     }
+    // Taken one by one, told by the sign: a group of zeros or with a number that is not finite; one brought up; one
+    // whose scale lost bits in its type's subnormals, so that quotients may be out of range.
     if (bad) own = 0.f;
+    if (own == 0.f || tiny || !(range < own * (ZEROS ? 15.2f : 7.4f))) own_r = -own_r;
+    uint8_t* out = t.values + v0 * t.ld_values + c / 2;
+    const int64_t out_step = t.ld_values * rows_a_pass;
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-        const int64_t v = v0 + k * rows_a_pass;
+    for (int k = 0; k < kDeep; ++k, out += out_step) {
         const int from = (threadIdx.x & 28) + k;
-        float s = __shfl_sync(0xffffffffu, own, from), r = __shfl_sync(0xffffffffu, own_r, from);
-        const float z = ZEROS ? __shfl_sync(0xffffffffu, own_z, from) : 8.f;
-        if (v >= p.rows || c >= t.D) continue;
-        const bool none = s == 0.f, lost = r < 0.f;
-        r = fabsf(r);
-        if (s < 0x1p-100f && W::kIndex != Fp16::kIndex) {
-            float a[8];
-            s *= 0x1p100f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = in[k].get(i) * 0x1p100f;
-            in[k].set_all(a);
-        }
-        // pairs of columns i and i + 4
-        const uint64_t s2 = f2_pack(-s, -s), r2 = f2_pack(r, r), magic2 = f2_pack(kMagic, kMagic), unmagic2 = f2_pack(-kMagic, -kMagic);
-        uint64_t x2[4];
-        float most = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint64_t a = f2_pack(in[k].get(i), in[k].get(i + 4));
-            if constexpr (W::kBytes == 2 && S::kBytes == 2) {
-                const uint64_t q = f2_mul(a, r2);
-                x2[i] = f2_add(f2_add(f2_fma(f2_fma(q, s2, a), r2, q), magic2), unmagic2);
-            } else {
-                x2[i] = f2_add(f2_fma(a, r2, magic2), unmagic2);
-                float e0, e1;
-                f2_unpack(f2_fma(x2[i], s2, a), e0, e1);
-                most = fmaxf(fmaxf(most, fabsf(e0)), fabsf(e1));
-            }
-        }
-        const bool half = (W::kBytes != 2 || S::kBytes != 2) && !(most < s * 0.4999995f);
-        if (ZEROS || half || lost) {
-            // (the sum is one more than 15 where both ends round up)
-            const float least = -z, largest = 15.f - z;
+        const float s = __shfl_sync(0xffffffffu, own, from), r = __shfl_sync(0xffffffffu, own_r, from);
+        const float z = ZEROS ? __shfl_sync(0xffffffffu, own_z, from) : 8.f, least = -z, largest = 15.f - z;
+        if (k * rows_a_pass >= rows || c >= t.D) continue;
+        uint64_t x2[4];   // of columns i and i + 4
+        bool one_by_one = r < 0.f;
+        if (!one_by_one) {
+            const uint64_t s2 = f2_pack(-s, -s), r2 = f2_pack(r, r), magic2 = f2_pack(kMagic, kMagic), unmagic2 = f2_pack(-kMagic, -kMagic);
+            float most = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x[2];
-                f2_unpack(x2[i], x[0], x[1]);
-                if (half || lost) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) x[e] = fmaxf(settle(x[e], in[k].get(i + 4 * e), s), least);
+                const uint64_t a = f2_pack(in[k].get(i), in[k].get(i + 4));
+                if constexpr (W::kBytes == 2 && S::kBytes == 2) {
+                    const uint64_t q = f2_mul(a, r2);
+                    x2[i] = f2_add(f2_add(f2_fma(f2_fma(q, s2, a), r2, q), magic2), unmagic2);
+                } else {
+                    x2[i] = f2_add(f2_fma(a, r2, magic2), unmagic2);
+                    float e0, e1;
+                    f2_unpack(f2_fma(x2[i], s2, a), e0, e1);
+                    most = fmaxf(fmaxf(most, fabsf(e0)), fabsf(e1));
                 }
-                x2[i] = f2_pack(fminf(x[0], largest), fminf(x[1], largest));
+                if (ZEROS) {   // (one more than 15 where both ends round up)
+                    float x0, x1;
+                    f2_unpack(x2[i], x0, x1);
+                    x2[i] = f2_pack(fminf(x0, largest), fminf(x1, largest));
+                }
             }
+            one_by_one = (W::kBytes != 2 || S::kBytes != 2) && !(most < s * 0.4999995f);
+        }
+        if (one_by_one) {
+            float x[8];
+            const float lift = s < 0x1p-100f && W::kIndex != Fp16::kIndex ? 0x1p100f : 1.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = in[k].get(i) * lift;
+                x[i] = s == 0.f ? 0.f : fminf(fmaxf(settle(fmaf(a, fabsf(r), kMagic) - kMagic, a, s * lift), least), largest);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x2[i] = f2_pack(x[i], x[i + 4]);
         }
         // four numbers make one below 2^16, exact in fp32; z is added to all four at once
         const uint64_t sixteen2 = f2_pack(16.f, 16.f);
-        const float base = fmaf(z, 4369.f, 8388608.f);
+        const float more = fmaf(z, 4369.f, 8388608.f);
         float low, high;
-        f2_unpack(f2_add(f2_fma(f2_fma(f2_fma(x2[3], sixteen2, x2[2]), sixteen2, x2[1]), sixteen2, x2[0]), f2_pack(base, base)), low, high);
+        f2_unpack(f2_add(f2_fma(f2_fma(f2_fma(x2[3], sixteen2, x2[2]), sixteen2, x2[1]), sixteen2, x2[0]), f2_pack(more, more)), low, high);
         uint32_t word = __byte_perm(__float_as_uint(low), __float_as_uint(high), 0x5410);
-        if (none) word = ZEROS ? 0u : 0x88888888u;   // zeros, or not finite
-        uint8_t* out = t.values + v * t.ld_values + c / 2;
-        if (c + 8 <= t.D) {
+        if (whole) {
             *reinterpret_cast<uint32_t*>(out) = word;
         } else {
             word &= (1u << (4 * (t.D - c))) - 1u;
@@ -526,6 +523,7 @@ lmloss_status lmloss_table4_quantize(lmloss_vocab_handle h, const lmloss_table4_
         p.weight = static_cast<const unsigned char*>(a->weight) + v0 * a->ld_weight * float_bytes(a->weight_dtype);
         p.weight_end = static_cast<const unsigned char*>(p.weight) + ((p.rows - 1) * a->ld_weight + a->table.D) * float_bytes(a->weight_dtype);
         p.ld = a->ld_weight;
+        p.aligned = aligned16(p.weight) && a->ld_weight * float_bytes(a->weight_dtype) % 16 == 0;
         p.log_across = all.log_across;
         p.blocks_across = all.blocks_across;
         p.err = h->err;
