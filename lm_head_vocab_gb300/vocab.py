@@ -137,19 +137,26 @@ class VocabOps:
             b = _lib.lmloss_beam_args(B=max_rows, K=1, M=_lib.LMLOSS_MAX_BEAMS, V=max_vocab, ld=max_vocab,
                                       dtype=_lib.LMLOSS_FP32, eos_token=-1)
             need = max(need, _lib.lmloss_beam_workspace(b))
+        self.workspace_bytes = need
+        self.handle = _lib.lmloss_vocab_create(device, need)
+        # Log-probabilities and 4-bit tables have a handle of their own, so that what the other operators
+        # accept goes by their maxima alone.
+        need = 0
+        if max_rows > 0:
             c = _lib.lmloss_logprobs_args(T=max_rows, V=max_vocab, ld=max_vocab, M=_lib.LMLOSS_MAX_ALTERNATIVES,
                                           temperature=1.0)
-            need = max(need, _lib.lmloss_logprobs_workspace(c))
+            need = _lib.lmloss_logprobs_workspace(c)
             d = _lib.lmloss_table4_logits_args(T=max_rows)
             d.table.V, d.table.D, d.table.group = max_vocab, max(max_dim, 1), 32
             need = max(need, _lib.lmloss_table4_logits_workspace(d))
-        self.workspace_bytes = need
-        self.handle = _lib.lmloss_vocab_create(device, need)
+        self.scores_workspace_bytes = need
+        self.scores_handle = _lib.lmloss_vocab_create(device, need)
 
     def close(self):
-        if getattr(self, "handle", None) is not None:
-            _lib.lmloss_vocab_destroy(self.handle)
-            self.handle = None
+        for name in ("handle", "scores_handle"):
+            if getattr(self, name, None) is not None:
+                _lib.lmloss_vocab_destroy(getattr(self, name))
+                setattr(self, name, None)
 
     def __del__(self):
         try:
@@ -159,14 +166,16 @@ class VocabOps:
 
     def device_error(self) -> int:
         """Read and clear the handle's error word (synchronises the device)."""
-        return _lib.lmloss_vocab_get_device_error(self.handle)
+        first, second = (_lib.lmloss_vocab_get_device_error(h) for h in (self.handle, self.scores_handle))
+        return first or second
 
-    def _refused(self, status, where, args, check, workspace):
+    def _refused(self, status, where, args, check, workspace, there=None):
         """The error for a refused call: where the arguments are in order, what the workspace lacks."""
+        there = self.workspace_bytes if there is None else there
         if status == _lib.LMLOSS_ERR_INVALID_ARG and check(args) == _lib.LMLOSS_OK:
             need = workspace(args)
-            if need > self.workspace_bytes:
-                where += (f" ({need} bytes of workspace needed, {self.workspace_bytes} there: the handle's max_tokens, "
+            if need > there:
+                where += (f" ({need} bytes of workspace needed, {there} there: the handle's max_tokens, "
                           f"max_dim, max_rows or max_vocab is too small)")
         return LMLossError(status, where)
 
@@ -474,10 +483,10 @@ class VocabOps:
                                       r.lse.data_ptr(), r.entropy.data_ptr() if entropy else None,
                                       r.top_logp.data_ptr() if num_top else None,
                                       r.top_tokens.data_ptr() if num_top else None)
-        st = self._logprobs(self.handle, a, raw)
+        st = self._logprobs(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise self._refused(st, "lmloss_logprobs_forward", a, _lib.lmloss_logprobs_check_args,
-                                _lib.lmloss_logprobs_workspace)
+                                _lib.lmloss_logprobs_workspace, self.scores_workspace_bytes)
         return r
 
     def _logprobs_out(self, tokens, T, M, entropy):
@@ -540,7 +549,7 @@ class VocabOps:
                                            None if grad_entropy is None else entropy.data_ptr(),
                                            None if grad_entropy is None else grad_entropy.data_ptr(),
                                            grad.data_ptr(), ld_grad)
-        st = self._logprobs_grad(self.handle, a, raw)
+        st = self._logprobs_grad(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_logprobs_backward")
         return grad
@@ -613,7 +622,7 @@ class VocabOps:
         if t.V != V or t.D != D:
             raise ValueError(f"out: a table of [{t.V}, {t.D}] for weights of [{V}, {D}]")
         a = _lib.lmloss_table4_quantize_args(t, weight.data_ptr(), ld, w_type)
-        st = self._quantize(self.handle, a, raw)
+        st = self._quantize(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_table4_quantize")
         return out
@@ -632,7 +641,7 @@ class VocabOps:
         T, D = ids.numel(), table.columns
         out, r_type, ld_rows = self._result(out, out_dtype or table.scales.dtype, out_dtype, (*ids.shape, D), T, D, ctx)
         a = _lib.lmloss_table4_lookup_args(t, ids.data_ptr(), T, out.data_ptr(), ld_rows, id_type, r_type, scale)
-        st = self._lookup4(self.handle, a, raw)
+        st = self._lookup4(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_table4_lookup")
         return out
@@ -668,8 +677,8 @@ class VocabOps:
             raw, ctx = self._enter(stream, table.values, table.scales, table.zeros, hidden, out)
         out, o_type, ld_out = self._result(out, out_dtype or hidden.dtype, out_dtype, (*hidden.shape[:-1], V), T, V, ctx)
         a = _lib.lmloss_table4_logits_args(t, rows.data_ptr(), T, ld, out.data_ptr(), ld_out, x_type, o_type, scale)
-        st = self._logits4(self.handle, a, raw)
+        st = self._logits4(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise self._refused(st, "lmloss_table4_logits", a, _lib.lmloss_table4_check_logits_args,
-                                _lib.lmloss_table4_logits_workspace)
+                                _lib.lmloss_table4_logits_workspace, self.scores_workspace_bytes)
         return out
