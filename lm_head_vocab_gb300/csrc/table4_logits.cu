@@ -56,6 +56,7 @@ struct HiddenParams {
     int64_t ld;
     int D, kblocks;
     int N, per;
+    int lanes;                   // 8 columns each, of a table's group
     int own;                     // operand rows of a thread's sums: pairs lie within them
     unsigned char* out;
     float* inverse;
@@ -103,7 +104,9 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
         float sum, sum_lo;
         Pack<X, 8> v;
         load_part<X>(x, 8 * u, p.D, v);
-        hidden_part<X>(v, finite ? scale : 0.f, hi, lo, sum, sum_lo);
+        bool others;
+        const float largest = kPair ? group_top(p.lanes, part_top<X>(v, others)) : 0.f;
+        hidden_part<X, kPair>(v, finite ? scale : 0.f, largest, hi, lo, sum, sum_lo);
         // [2][N][128 bytes] for each block of columns, swizzled as mma_desc_128b wants it
         const int part = u & 7;
         auto place = [&](int r) { return reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u >> 3) * p.N + r) * 128 + ((part ^ (r & 7)) << 4)); };
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                             const int unit = part * 2 + i;   // 32 columns
                             float z = 8.f;
                             if (p.zeros) z = static_cast<float>(zeros[(((kb * 4 + unit) * 32) >> p.shift) * kRows + row]);
-                            const __half2 z1 = __float2half2_rn(z * 0x1p-24f), z16 = __float2half2_rn(z * 0x1p-20f);
+                            const __half2 z1 = __float2half2_rn(fmaf(z, 0x1p-14f, 0x1p-4f)), z16 = __float2half2_rn(fmaf(z, 0x1p-10f, 0x1p-4f));
                             widen_word(w[unit].x, z1, z16, r + 16 * i);
                             widen_word(w[unit].y, z1, z16, r + 16 * i + 4);
                             widen_word(w[unit].z, z1, z16, r + 16 * i + 8);
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                 for (int t = lane; t < p.T; t += 32) {
                     const float f = p.inverse[t];
                     odd = odd || f != f;
-                    b.factor[t] = f * 0x1p12f;
+                    b.factor[t] = f * 0x1p7f;
                 }
                 if (odd) b.odd = 1;
                 __syncwarp();
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                     using O = decltype(type);
                     typename O::raw* to = static_cast<typename O::raw*>(p.out) + static_cast<int64_t>(t0) * p.ld_out + v;
                     auto put = [&](int i, float x) {
-                        if (i < rows) *to = static_cast<typename O::raw>(O::round(x * 0x1p12f * b.factor[t0 + i] * p.scale));
+                        if (i < rows) *to = static_cast<typename O::raw>(O::round(x * 0x1p7f * b.factor[t0 + i] * p.scale));
                         to += p.ld_out;
                     };
 #pragma unroll
@@ -593,7 +596,10 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.scale = a->scale;
         p.err = h->err;
         const int operands = T * (pairs ? 2 : 1);
+        // (fp32 logits of few rows are of pairs whatever the rows' type: their table's numbers are subnormal)
+        p.pairs = pairs || a->logits_dtype == LMLOSS_FP32;
         const bool few = few_rows_fit(p);
+        if (!few) p.pairs = pairs;
         const int rows = few ? kFewTile : kRows;
         p.vtiles = static_cast<int>((a->table.V + rows - 1) / rows);
         TableMaps maps{};
@@ -606,6 +612,7 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
             x.ld = p.ld_hidden;
             x.D = p.D;
             x.kblocks = p.kblocks;
+            x.lanes = (1 << p.shift) / 8;
             x.N = p.N = operands <= 16 ? 16 : (operands <= 32 ? 32 : (operands <= 64 ? 64 : kMany));
             x.per = p.per = pairs ? p.N / 2 : p.N;
             x.own = p.N > 32 ? p.N / 2 : p.N;

@@ -30,7 +30,7 @@ struct LogitsParams {
     int per;                     // hidden rows a block takes: N, or N / 2 as pairs
     int tblocks;                 // runs of `per` hidden rows
     int vtiles;
-    int pairs;                   // fp32: operand rows 0 .. N / 2 - 1 the upper parts, the others the lower ones times 2^11
+    int pairs;                   // operand rows 0 .. N / 2 - 1 the upper parts, the others the lower ones times 2^11
     const unsigned char* x;      // [tblocks][kblocks][N * 256 bytes]: the hidden rows as fp16
     const float* inverse;        // [T] by which a row's sums are multiplied; NaN: the row is not finite
     const void* hidden;          // the rows as they came
@@ -56,10 +56,23 @@ __device__ __forceinline__ void widen_word(uint32_t w, uint32_t* out)
     out[2] = w8 & 0x000f000fu;
     out[3] = w8 & 0x00f000f0u;
 }
-// The same less a zero point, z 2^-24 and z 2^-20 twice each: exact.
+// (a & b) | c as one operation
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// The same less a zero point, (q - z) 2^-14 and (q - z) 2^-10, exact: under an exponent whose last place is 2^-14, less
+// 2^-4 + z 2^-14 or 2^-4 + z 2^-10.  As fp16's normal numbers: of subnormal ones the tensor cores cut sums off at some
+// 2^-24 of what their exponent could hold, 2^6 to 2^10 times what they do (logits of bf16 rows 5e-7 off, not 2e-7).
 __device__ __forceinline__ void widen_word(uint32_t w, __half2 z, __half2 z16, uint32_t* out)
 {
-    widen_word(w, out);
+    const uint32_t w8 = w >> 8;
+    out[0] = and_or(w, 0x000f000fu, 0x2c002c00u);
+    out[1] = and_or(w, 0x00f000f0u, 0x2c002c00u);
+    out[2] = and_or(w8, 0x000f000fu, 0x2c002c00u);
+    out[3] = and_or(w8, 0x00f000f0u, 0x2c002c00u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(out + i), i & 1 ? z16 : z);
@@ -102,24 +115,31 @@ __device__ __forceinline__ void load_part(const typename X::raw* x, int c, int D
             if (c + i < D) q.set(i, X::widen(x[c + i]));
     }
 }
-// They scaled as a 16-byte part: fp16 in the order 0 4 1 5 2 6 3 7, the places 1 5 and 3 7 divided by 16.  lo: what fp32
-// leaves, times 2^11.  The sums are of what the parts stand for, in the products' unit of 2^-24.  A scale of 0 is a
-// row that is not finite.
-template <class X>
-__device__ __forceinline__ void hidden_part(const Pack<X, 8>& v, float scale, uint4& hi, uint4& lo, float& sum, float& sum_lo)
+// They scaled as a 16-byte part: fp16 in the order 0 4 1 5 2 6 3 7, the places 1 5 and 3 7 divided by 16.  The sums are of
+// what the parts stand for, in the products' unit of 2^-24.  A scale of 0 is a row that is not finite.
+// Of a pair, lo is what hi leaves, times 2^11, and hi a whole number of steps, the same for all columns of a table's
+// group, 2^11 of which reach its largest: then a group's sum of products, below 15 * 2^11 * 128 < 2^22 steps, is exact.
+// The tensor cores cut their sums off, one way, at some 2^-24 of the largest term: with hi rounded by each value's own
+// exponent logits of 1001 columns were up to 2e-6 off, ten times as far as sums in fp32.
+template <class X, bool PAIR>
+__device__ __forceinline__ void hidden_part(const Pack<X, 8>& v, float scale, float group_top, uint4& hi, uint4& lo, float& sum, float& sum_lo)
 {
-    constexpr bool kPair = X::kBytes == 4;
     uint32_t h[4], l[4] = {0, 0, 0, 0};
     sum = sum_lo = 0.f;
+    // x + magic - magic: x in steps of 2^-10 of the power of two at or below the group's largest, or of 2^-20 (fp16's
+    // last place, for the places divided by 16)
+    const uint32_t e = __float_as_uint(group_top * scale) >> 23;
+    const float magic = 1.5f * __uint_as_float((max(e, 117u) + 13u) << 23);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float by = i & 1 ? scale * 0.0625f : scale, back = i & 1 ? 0x1p-20f : 0x1p-24f;
         const float a = scale > 0.f ? v.get(i) * by : 0.f, b = scale > 0.f ? v.get(i + 4) * by : 0.f;
-        const __half2 p = __floats2half2_rn(a, b);
+        const float m = i & 1 ? magic * 0.0625f : magic;
+        const __half2 p = PAIR ? __floats2half2_rn(__fadd_rn(__fadd_rn(a, m), -m), __fadd_rn(__fadd_rn(b, m), -m)) : __floats2half2_rn(a, b);
         h[i] = *reinterpret_cast<const uint32_t*>(&p);
         const float2 f = __half22float2(p);
         sum = fmaf(f.x, back, fmaf(f.y, back, sum));
-        if (kPair) {
+        if (PAIR) {
             const __half2 r = __floats2half2_rn((a - f.x) * 2048.f, (b - f.y) * 2048.f);
             l[i] = *reinterpret_cast<const uint32_t*>(&r);
             const float2 e = __half22float2(r);
@@ -141,6 +161,13 @@ __device__ __forceinline__ float part_top(const Pack<X, 8>& v, bool& odd)
         if (a < INFINITY) top = fmaxf(top, a);
         else odd = true;
     }
+    return top;
+}
+// The largest over the `lanes` (4, 8 or 16) neighbouring threads of a group, 16 threads together.
+__device__ __forceinline__ float group_top(int lanes, float top)
+{
+    const uint32_t together = 0xffffu << (threadIdx.x & 16);
+    for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(together, top, o));
     return top;
 }
 // Sums over the `lanes` (4, 8 or 16) neighbouring threads of a group, 16 threads together.

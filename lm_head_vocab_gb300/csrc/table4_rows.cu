@@ -56,10 +56,9 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_
 
 // The hidden rows into shared memory, by the first kSumThreads threads: read once, as many rows at a time as their
 // registers hold.
-template <class X>
+template <class X, bool PAIR>
 __device__ __noinline__ void lay_out(const LogitsParams& p, RowsHead& head, unsigned char* x, float* sums, int N)
 {
-    constexpr bool kPair = X::kBytes == 4;
     constexpr int kHold = 16 / X::kBytes;
     const int tid = threadIdx.x;
     const uint32_t together = 0xffffu << (tid & 16);   // 16 threads have parts of the same row
@@ -93,15 +92,17 @@ __device__ __noinline__ void lay_out(const LogitsParams& p, RowsHead& head, unsi
             const int u = tid + i * kSumThreads - (r[i] - r0) * parts;
             uint4 hi, lo;
             float sum, sum_lo;
-            hidden_part<X>(v[i], head.odd[r[i]] ? 0.f : hidden_scale(__uint_as_float(head.top[r[i]])), hi, lo, sum, sum_lo);
+            bool odd;
+            const float largest = PAIR ? group_top(lanes, part_top<X>(v[i], odd)) : 0.f;
+            hidden_part<X, PAIR>(v[i], head.odd[r[i]] ? 0.f : hidden_scale(__uint_as_float(head.top[r[i]])), largest, hi, lo, sum, sum_lo);
             auto place = [&](int k) { return reinterpret_cast<uint4*>(x + ((u >> 4) * N + k) * 256 + (((u & 15) ^ ((k & 1) << 2)) << 4)); };
             *place(r[i]) = hi;
-            if (kPair) *place(r[i] + N / 2) = lo;
-            group_sums<kPair>(lanes, sum, sum_lo);
+            if (PAIR) *place(r[i] + N / 2) = lo;
+            group_sums<PAIR>(lanes, sum, sum_lo);
             const int g = (8 * u) >> p.shift;
             if ((u & (lanes - 1)) == 0 && g < p.groups) {
                 sums[g * N + r[i]] = sum;
-                if (kPair) sums[g * N + r[i] + N / 2] = sum_lo;
+                if (PAIR) sums[g * N + r[i] + N / 2] = sum_lo;
             }
         }
     }
@@ -157,9 +158,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         __syncwarp();
     } else {
         float* const all_sums = reinterpret_cast<float*>(rows + rl.sums);
-        if (p.hidden_dtype == LMLOSS_BF16) lay_out<Bf16>(p, b, rows, all_sums, N);
-        else if (p.hidden_dtype == LMLOSS_FP16) lay_out<Fp16>(p, b, rows, all_sums, N);
-        else lay_out<Fp32>(p, b, rows, all_sums, N);
+        if (p.hidden_dtype == LMLOSS_BF16) p.pairs ? lay_out<Bf16, true>(p, b, rows, all_sums, N) : lay_out<Bf16, false>(p, b, rows, all_sums, N);
+        else if (p.hidden_dtype == LMLOSS_FP16) p.pairs ? lay_out<Fp16, true>(p, b, rows, all_sums, N) : lay_out<Fp16, false>(p, b, rows, all_sums, N);
+        else lay_out<Fp32, true>(p, b, rows, all_sums, N);
         const int half = warp & 1, block = warp & 7, team = warp >> 3, g8 = lane >> 2, i4 = lane & 3;   // block: of 128 columns of a stage
         const int r0 = team * 32;
         float* pads = reinterpret_cast<float*>(rows + rl.pads) + team * 8 * (used * 33);
