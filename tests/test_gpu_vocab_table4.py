@@ -1,10 +1,13 @@
 """4-bit vocabulary tables on the GPU against fp64: made, looked up, multiplied with hidden rows.
 
 A lookup is one product (q - z) s of an exact whole number and an fp32 value, and one with the
-scale, each rounded once in fp32, then to the type.  Logits, from the arithmetic: hidden values as fp16
-pairs leave 2^-24 of a row's largest and 2^-23 of each value; within a group products are exact and their
-fp32 sums lose at most 2^-23 of the group's sum of magnitudes for each addition, group + 2 of them;
-the groups' scaled sums 2^-24 for each of G + 4 operations; the type's rounding.  Quantized values are exact.
+scale, each rounded once in fp32, then to the type.  Logits, from the arithmetic: a hidden value's upper part is
+off by half a step of 2^-10 of the power of two at or below its group's largest, 2^-11 of that largest at most;
+the lower part rounds this to 11 bits, so a pair leaves 2^-23 of a group's, thus of a row's largest; an fp16
+alone 2^-24 of a row's largest and nothing else, as 16-bit values fit it.  Within a group products are
+exact and their fp32 sums lose at most 2^-23 of the group's sum of magnitudes for each addition, group + 2
+of them; the groups' scaled sums 2^-24 for each of G + 4 operations; the type's rounding.  Quantized values
+are exact.
 """
 import numpy as np
 import pytest
@@ -191,7 +194,7 @@ def check_logits(ops, t, x, out=F, scale=1.0, into=None):
     want = xd @ w.t() * float(np.float32(scale))
     mag = xd.abs() @ w.abs().t() * abs(float(np.float32(scale)))
     tops = xd.abs().amax(1, keepdim=True) * w.abs().sum(1)[None] * abs(float(np.float32(scale)))
-    tol = mag * ((group + 2) * 2.0 ** -23 + 2.0 ** -23 + (G + 4) * EPS) + tops * 2.0 ** -24
+    tol = mag * ((group + 2) * 2.0 ** -23 + 2.0 ** -23 + (G + 4) * EPS) + tops * 2.0 ** -23
     tol += want.abs() * half_step(out) + (2.0 ** -25 if out is H else 2.0 ** -126)
     got = got.reshape(want.shape).double()
     over = (got - want).abs() > tol
@@ -298,6 +301,109 @@ def test_logits_repeat_and_do_not_depend_on_neighbours(ops):
     assert torch.equal(a, ops.table4_logits(t, x, out_dtype=F))
 
 
+@pytest.mark.parametrize("x", [BF, H, F])
+@pytest.mark.parametrize("T", [1, 6, 12, 40, 100])
+def test_fp32_logits_have_fp32_precision(ops, x, T):
+    # Of normal inputs a pair's rounding is uniform within 2^-23 of a group's largest, some three standard
+    # deviations: 3 * 2^-23 / sqrt(3) a column, 2^-22 of the logits' size; the 32 groups' additions add less than
+    # sqrt(32) 2^-24 / sqrt(3) = 2^-22.3 of it.  Together less than 2^-21; products cut off at some 2^-24 of
+    # what a subnormal's exponent could hold are past it.
+    for group, D, zeros in ((32, 1024, True), (128, 4096, False)):
+        t = table(ops, 600, D, group, F, zeros)
+        rows = hidden(T, D, x)
+        n, s = parts(t)
+        want = rows.double() @ (n * s).t()
+        got = ops.table4_logits(t, rows, out_dtype=F).double()
+        assert (got - want).pow(2).mean().sqrt().item() < 2.0 ** -21 * want.pow(2).mean().sqrt().item()
+
+
+@pytest.mark.parametrize("x", [BF, F])
+def test_logits_of_more_rows_than_a_launch_takes(ops, x):
+    check_logits(ops, table(ops, 131, 70, 32, H, True), hidden(2100, 70, x), x)
+
+
+@pytest.mark.parametrize("x", [BF, F])
+@pytest.mark.parametrize("T", [1, 3, 8])
+def test_few_rows_too_long_for_shared_memory(ops, x, T):
+    check_logits(ops, table(ops, 200, 30001, 128, BF, True), hidden(T, 30001, x), F)
+
+
+@pytest.mark.parametrize("T", [3, 8, 12, 30, 60, 90, 300])
+@pytest.mark.parametrize("V", [1, 63, 64, 65, 127, 128, 129, 513])
+def test_logits_at_tile_borders(ops, V, T):
+    t = table(ops, V, 160, 32, BF, True)
+    flat = torch.full((T * (V + 3) + 64,), 5.0, device="cuda")
+    out = flat[1:1 + T * (V + 3)].view(T, V + 3)[:, :V]
+    check_logits(ops, t, hidden(T, 160, F), F, into=out)
+    out.fill_(5.0)
+    assert bool((flat == 5.0).all())   # nothing beside the rows
+
+
+@pytest.mark.parametrize("x", [BF, H, F])
+@pytest.mark.parametrize("T", [4, 8, 14, 20, 50, 130])
+def test_a_row_that_is_not_finite_among_others(ops, x, T):
+    t = table(ops, 300, 200, 64, H, False)
+    rows = hidden(T, 200, x)
+    clean = ops.table4_logits(t, rows, out_dtype=F)
+    bad = [0, T // 2, T - 1]
+    for i, r in enumerate(bad):
+        rows[r, 199 - i] = (INF, -INF, float("nan"))[i]
+    got = ops.table4_logits(t, rows, out_dtype=F)
+    n, s = parts(t)
+    want = rows.double() @ (n * s).t()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got == INF, want == INF) and torch.equal(got == -INF, want == -INF)
+    others = [r for r in range(T) if r not in bad]
+    assert torch.equal(got[others], clean[others])
+
+
+@pytest.mark.parametrize("T", [3, 8, 20, 100])
+def test_a_row_does_not_depend_on_its_neighbours(ops, T):
+    t = table(ops, 500, 384, 128, F, True)
+    x = hidden(T, 384, F)
+    a = ops.table4_logits(t, x)
+    y = x * 1e20
+    y[T // 2] = x[T // 2]
+    assert torch.equal(ops.table4_logits(t, y)[T // 2], a[T // 2])
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("D", [1, 7, 8, 9, 33, 241, 247, 248, 249, 256, 257, 500])
+def test_lookup_at_every_alignment(ops, dtype, D):
+    t = table(ops, 100, D, 32, H, True)
+    ids = torch.randint(0, 100, (9,), device="cuda", generator=gen(61))
+    n, s = parts(t)
+    want = (n * s)[ids].to(dtype)          # fp64 to the type: the product is exact in fp32 (8 and 11 bits)
+    for shift in range(16 // dtype.itemsize):
+        for extra in (0, 1, 3):
+            flat = torch.full((32 + shift + 9 * (D + extra),), 5.0, device="cuda", dtype=dtype)
+            at = 16 + shift
+            out = flat[at:at + 9 * (D + extra)].view(-1)[:9 * (D + extra)].view(9, D + extra)[:, :D]
+            ops.table4_lookup(t, ids, out=out)
+            assert torch.equal(out, want)
+            out.fill_(5.0)
+            assert bool((flat == 5.0).all())
+
+
+@pytest.mark.parametrize("dtype,scales", [(F, F), (F, H), (BF, BF), (BF, H), (BF, F), (H, H), (H, F)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quantize_at_the_ends_of_the_types(ops, dtype, scales, zeros):
+    # scales that are subnormal or round to zero, weights next to the largest, groups of equal and of zero weights
+    lo, hi = (-24, 15) if H in (dtype, scales) else (-149 if dtype is F else -133, 127)
+    sizes = [2.0 ** e for e in (lo, lo + 1, lo + 2, lo + 3, lo + 4, lo + 7, lo + 12, lo + 25, lo + 31, hi - 3)]
+    w = torch.randn(len(sizes) * 4, 64, device="cuda", generator=gen(71)).clamp_(-3.9, 3.9).double()
+    for i, size in enumerate(sizes):
+        w[4 * i:4 * i + 4] *= size
+        w[4 * i + 2] = size * 3
+        w[4 * i + 3, ::2] = 0
+    w = w.to(dtype)
+    t = ops.quantize_table(w, group_size=32, zeros=zeros, scale_dtype=scales)
+    q, s, z = quantized(w, 32, zeros, scales)
+    got = torch.stack([t.values & 15, t.values >> 4], -1).flatten(1)[:, :64]
+    assert torch.equal(t.scales, s) and torch.equal(got.double(), q)
+    assert not zeros or torch.equal(t.zeros.double(), z)
+    assert ops.device_error() == 0
+
+
 # ------------------------------------------------- together, streams, graphs
 def test_a_decoding_step(ops):
     # a tied 4-bit vocabulary: embeddings of the last tokens in, log-probabilities and beams out
@@ -357,3 +463,35 @@ def test_more_rows_than_the_handle():
     except L.LMLossError as e:
         assert "bytes of workspace needed" in str(e)
     h.close()
+
+
+def test_handles_of_several_threads():
+    import threading
+    from lm_head_vocab_gb300 import VocabOps
+    w = torch.randn(3000, 256, device="cuda", generator=gen(81))
+    xs = [hidden(n, 256, BF, seed=90 + n) for n in (1, 20, 70)]
+    h = VocabOps(0, max_tokens=0, max_dim=256, max_rows=128, max_vocab=3000)
+    t = h.quantize_table(w)
+    want = [(h.table4_logits(t, x), h.token_logprobs(h.table4_logits(t, x, out_dtype=F), num_top=5)) for x in xs]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            mine = VocabOps(0, max_tokens=0, max_dim=256, max_rows=128, max_vocab=3000)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    z = mine.table4_logits(t, xs[i])
+                    r = mine.token_logprobs(mine.table4_logits(t, xs[i], out_dtype=F), num_top=5)
+                torch.cuda.current_stream().synchronize()
+            assert torch.equal(z, want[i][0]) and torch.equal(r.top_tokens, want[i][1].top_tokens) and torch.equal(r.lse, want[i][1].lse)
+            mine.close()
+        except BaseException as e:
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(i % 3,)) for i in range(6)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    h.close()
+    assert not failed, failed
