@@ -42,7 +42,10 @@ struct Shape {
     static constexpr int kThreads = (kFirstFew + 4) * 32;
     // tensor memory: A kAhead of either turn, then D kSums of either turn.  (With one A of a turn what widens waited
     // for its products: 1100 clocks a block of columns, for 64 operand rows as for 128.)
-    static constexpr int kSums = N > 64 ? 1 : 2, kAhead = N > 32 ? 2 : 1;
+    static constexpr int kSums = N > 64 ? 1 : (N > 16 ? 2 : 4), kAhead = N > 32 ? 2 : 1;
+    // whether sums of small groups go by lots, with one barrier a lot: where there is room for more than one, and
+    // registers for the loop
+    static constexpr bool kLots = N == 16 || N == 64;
     static constexpr uint32_t kD = 128 * kAhead, kColumns = N > 32 ? 512 : 256;
     static_assert(kD + 2 * kSums * N <= kColumns, "tensor memory");
     // registers a thread of each part where 64 sums do not fit an even share: in all what the block was launched with
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(256) hidden_kernel(const __grid_constant__ Hid
 // A block's head: barriers, and the factors of all hidden rows.
 struct __align__(16) LogitsBarriers {
     uint64_t q_full[kMaxStages], q_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages];
-    uint64_t a_full[2][2], a_empty[2][2], d_full[2][2], d_empty[2][2];   // of either turn
+    uint64_t a_full[2][2], a_empty[2][2], d_full[2][4], d_empty[2][4];   // of either turn
     uint32_t tmem;
     int failed;
     int odd;                     // whether any row is not finite
@@ -156,6 +159,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
             for (int d = 0; d < 2; ++d) {
                 mbar_init(smem_addr(&b.a_full[i][d]), 4);
                 mbar_init(smem_addr(&b.a_empty[i][d]), 1);
+            }
+            for (int d = 0; d < 4; ++d) {
                 mbar_init(smem_addr(&b.d_full[i][d]), 1);
                 mbar_init(smem_addr(&b.d_empty[i][d]), Sh::kAddWarps);
             }
@@ -240,7 +245,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
         Ring q;
         bool waited = false;
         int turn = 0;                        // of the block of columns
-        uint32_t taken0 = 0, taken1 = 0;     // sums read so far of either turn
+        uint32_t taken0 = 0, taken1 = 0;     // lots read so far of either turn
+        const int of_block = kBlockCols >> p.shift, lot = Sh::kLots ? min(kSums, of_block) : 1;
+        const uint32_t slots = kSums / lot;  // (of lots of more than one group: 1 or 2)
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const int vt = tile / p.tblocks, tb = tile - vt * p.tblocks;
             uint64_t acc[kOwn / 2];
@@ -251,31 +258,59 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                 wait(b.q_full[q.slot], q.parity);
                 const unsigned char* const scales = smem + kHeader + q.slot * p.stage_bytes + lay.scales;
                 const int n = min(per_stage, p.groups - st * per_stage);
-                // one loop, little code: the five parts of a block share the instruction cache
-#pragma unroll 1
-                for (int g = 0; g < n; ++g) {
-                    const uint32_t taken = turn ? taken1 : taken0, slot = taken % static_cast<uint32_t>(kSums);
-                    const float s = widen_any(scales, p.scale_dtype, g * kRows + row);
+                // small loops: the five parts of a block share the instruction cache
+                auto scale_of = [&](int g) { return widen_any(scales, p.scale_dtype, g * kRows + row); };
+                auto add = [&](uint32_t at, float s) {
                     const uint64_t s2 = f2_pack(s, s);
-                    wait(b.d_full[turn][slot], taken / static_cast<uint32_t>(kSums) & 1u);
-                    tcgen05_after_sync();
 #pragma unroll
                     for (int c = 0; c < kOwn; c += 16) {
                         float f[16];
-                        tmem_load16(from + (turn * kSums + slot) * N + c, f);
+                        tmem_load16(at + c, f);
                         tmem_wait_load(f);
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            uint64_t& a = acc[(c + i) / 2];
-                            a = f2_fma(s2, f2_pack(f[i], f[i + 1]), a);
+                            uint64_t& x = acc[(c + i) / 2];
+                            x = f2_fma(s2, f2_pack(f[i], f[i + 1]), x);
                         }
                     }
-                    tcgen05_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&b.d_empty[turn][slot]));
-                    taken0 += turn ^ 1;
-                    taken1 += turn;
-                    if (((g + 1) << p.shift) % kBlockCols == 0 || g + 1 == n) turn ^= 1;   // the block of columns' last
+                };
+                if (!Sh::kLots || lot == 1) {
+#pragma unroll 1
+                    for (int g = 0; g < n; ++g) {
+                        const uint32_t taken = turn ? taken1 : taken0, slot = taken % static_cast<uint32_t>(kSums);
+                        const float s = scale_of(g);
+                        wait(b.d_full[turn][slot], taken / static_cast<uint32_t>(kSums) & 1u);
+                        tcgen05_after_sync();
+                        add(from + (turn * kSums + slot) * N, s);
+                        tcgen05_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&b.d_empty[turn][slot]));
+                        taken0 += turn ^ 1;
+                        taken1 += turn;
+                        if (((g + 1) << p.shift) % kBlockCols == 0 || g + 1 == n) turn ^= 1;   // the block of columns' last
+                    }
+                } else {
+                    // the lots of the stage's two blocks of columns in turn, so that the one's products run while the
+                    // other's sums are read
+#pragma unroll 1
+                    for (int i = 0; i < 2 * of_block; i += lot) {
+                        const int second = i & lot ? 1 : 0, side = turn ^ second;
+                        int g = second * of_block + (i - second * lot) / 2;
+                        if (g >= n) continue;
+                        const uint32_t taken = side ? taken1 : taken0, slot = taken & (slots - 1);
+                        wait(b.d_full[side][slot], taken >> (slots - 1) & 1u);
+                        tcgen05_after_sync();
+                        uint32_t at = from + (side * kSums + slot * lot) * N;
+                        const int end = min(g + lot, n);
+#pragma unroll 1
+                        for (; g < end; ++g, at += N) add(at, scale_of(g));
+                        tcgen05_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&b.d_empty[side][slot]));
+                        taken0 += side ^ 1;
+                        taken1 += side;
+                    }
+                    if (p.kblocks - 2 * st == 1) turn ^= 1;   // a stage of one block of columns
                 }
                 if (lane == 0) mbar_arrive(smem_addr(&b.q_empty[q.slot]));
                 q.next(p.qstages);
@@ -379,6 +414,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
             auto multiply = [&](auto count) {
                 constexpr int kSteps = decltype(count)::value;   // a group's, 16 columns each
                 constexpr int kGroups = 8 / kSteps;              // of a block of columns
+                constexpr int kLot = Sh::kLots ? (kGroups < kSums ? kGroups : kSums) : 1, kSlots = kSums / kLot;
                 Ring x, a, d;
                 int turn = 0;
                 for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -391,20 +427,24 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kBlocks)
                         wait(b.a_full[mine][a.slot], a.parity);
                         const uint32_t from = tmem + (mine * Sh::kAhead + a.slot) * 64;
 #pragma unroll
-                        for (int g = 0; g < kGroups; ++g) {
-                            if (g >= left) break;
+                        for (int g0 = 0; g0 < kGroups; g0 += kLot) {
+                            if (g0 >= left) break;
                             wait(b.d_empty[mine][d.slot], d.parity ^ 1u);
                             tcgen05_after_sync();
-                            const uint32_t to = tmem + Sh::kD + (mine * kSums + d.slot) * N;
 #pragma unroll
-                            for (int k = 0; k < kSteps; ++k) {
-                                const int step = g * kSteps + k;   // 64 columns lie in one run of N rows
-                                const uint64_t at = desc + (step >> 2) * (N * 128 / 16) + (step & 3) * 2;
-                                if (k == 0) mma_f16_ts<false>(to, from + step * 8, at, kIdesc, leader);
-                                else mma_f16_ts<true>(to, from + step * 8, at, kIdesc, leader);
+                            for (int g = g0; g < g0 + kLot; ++g) {
+                                if (g >= left) break;
+                                const uint32_t to = tmem + Sh::kD + (mine * kSums + d.slot * kLot + g - g0) * N;
+#pragma unroll
+                                for (int k = 0; k < kSteps; ++k) {
+                                    const int step = g * kSteps + k;   // 64 columns lie in one run of N rows
+                                    const uint64_t at = desc + (step >> 2) * (N * 128 / 16) + (step & 3) * 2;
+                                    if (k == 0) mma_f16_ts<false>(to, from + step * 8, at, kIdesc, leader);
+                                    else mma_f16_ts<true>(to, from + step * 8, at, kIdesc, leader);
+                                }
                             }
                             mma_commit(smem_addr(&b.d_full[mine][d.slot]), leader);
-                            d.next(kSums);
+                            d.next(kSlots);
                         }
                         mma_commit(smem_addr(&b.a_empty[mine][a.slot]), leader);
                         mma_commit(smem_addr(&b.x_empty[x.slot]), leader);
