@@ -49,7 +49,8 @@ typedef enum {
     LMLOSS_ERR_CUDA = 3,          /* a CUDA runtime call failed                            */
     LMLOSS_ERR_BAD_TARGET = 4,    /* device: target not in [0, V) and not -100             */
     LMLOSS_ERR_BAD_SEGMENT = 5,   /* device: segment id >= num_segments                    */
-    LMLOSS_ERR_RANGE = 6,         /* device: GSPO log-ratio sum beyond +-2^31              */
+    LMLOSS_ERR_RANGE = 6,         /* device: GSPO log-ratio sum beyond +-2^31; a 4-bit     */
+                                  /* table's weight or scale that is not finite            */
     LMLOSS_ERR_TIMEOUT = 7,       /* device: a bounded wait on a copy expired              */
     LMLOSS_ERR_BAD_PARENT = 8     /* device: a beam's parent outside [0, K)                */
 } lmloss_status;
@@ -660,6 +661,11 @@ lmloss_status lmloss_table4_logits_workspace(const lmloss_table4_logits_args* ar
  * logits[t][v] = scale * sum_c hidden[t][c] * w[v][c]: from one row (a decoding step) to a
  * prompt's.  Within a group the products with the whole numbers q - z are summed, and the sum
  * is scaled by the group's scale: no weight is rounded.  Sums in fp32, one rounding at the end.
+ * fp32 hidden values count with an error of at most 2^-23 of the largest in their group of
+ * columns, 16-bit ones with none down to 2^-35 of their row's largest.  A row with an
+ * infinity or NaN gives what the formula gives, slowly, and does not disturb the others.  A
+ * row's logits depend on that row, the table and T alone.  `logits` overlaps neither `hidden`
+ * nor the table.  A wait inside that expires sets LMLOSS_ERR_TIMEOUT; the logits mean nothing then.
  */
 lmloss_status lmloss_table4_logits(lmloss_vocab_handle handle, const lmloss_table4_logits_args* args,
                                    cudaStream_t stream);

@@ -2,8 +2,11 @@
 //
 //   w[v][c] = s[g][v] (q[v][c] - z[g][v]),  g = c / group
 //
-// Both are bound by memory: making a table reads the weights and writes half a byte for each; the lookup reads half a byte for each column
-// and writes the row.
+// Making a table reads the weights and writes half a byte for each; the lookup reads half a byte for each column
+// and writes the row.  Both would be bound by memory, and are where elements are wide: 128256 x 4096 made from fp32
+// in groups of 32, 361 us (1.00 of the copy's rate); the whole table to fp32, 355 us (1.00).  Otherwise by
+// instructions: made from bf16 in groups of 128, 258 us (0.76; 77% of the issue slots, 15 instructions a
+// weight and lane); 32767 of 151936 x 2048 to bf16, 41 us (0.62; 70%).
 #include <algorithm>
 #include <cmath>
 

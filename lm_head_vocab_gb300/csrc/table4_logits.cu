@@ -2,19 +2,26 @@
 //
 //   logits[t][v] = scale sum_g s[g][v] sum_{c in g} x[t][c] (q[v][c] - z[g][v])
 //
-// The whole numbers q are exact in fp16, and so is a hidden row in fp16 once a power of two brings its
+// The whole numbers q - z are exact in fp16, and so is a hidden row in fp16 once a power of two brings its
 // largest value to 2^14 (bf16 and fp16: what underflows is below 2^-35 of that; fp32 as a pair of fp16,
-// within 2^-24).  So the tensor cores sum exact products within a group, in fp32; the zero point's part is
-// taken off, z sum_{c in g} x[t][c], and the rest scaled by s, in fp32: no weight is rounded.
+// within 2^-23).  So the tensor cores sum exact products within a group, in fp32, and a group's sum is scaled
+// by s and added to the others in fp32 registers: no weight is rounded.
 //
-// A first kernel lays the hidden rows out and sums their groups.  Up to 32 operand rows then go to a kernel of
-// independent warps (table4_rows.cu); more to the one here, in which a block takes 256 rows of the table and
-// 64 operand rows at a time.  Its parts, each a step of a ring ahead of the next:
-//   one warp    copies 256 rows x 128 bytes of the table, their scales and zeros     (TMA, HBM)
-//   one warp    copies the hidden rows' 128 columns, laid out for the product        (bulk copies, L2)
-//   16 warps    widen 4 bits to fp16, a thread a row, into tensor memory             (operand A)
-//   2 warps     multiply: [128 x 128] by [128 x 64] a half of the rows, a sum for each group
-//   8 warps     read a group's sums from tensor memory, a thread a row, and add them scaled
+// Up to 8 operand rows go to a kernel of independent warps (table4_rows.cu); a pair counts as two.  For more a first
+// kernel lays the hidden rows out, and in the one here a block takes 128 rows of the table and 16, 32, 64 or 128
+// operand rows at a time.  Its parts, each a step of a ring ahead of the next:
+//   one warp        copies 128 rows x 256 columns of the table, their scales and zeros  (TMA, HBM)
+//   one warp        copies the hidden rows' 128 columns, laid out for the product       (bulk copies, L2)
+//   8 warps         widen 4 bits to fp16, a thread a row, into tensor memory            (operand A)
+//   2 warps         multiply, [128 x 128] by [128 x N] in turn, a sum for each group
+//   4 or 8 warps    read a group's sums from tensor memory, a thread a row, and add them scaled
+//
+// 128256 x 4096 in groups of 128: 16 rows 74 us, 64 rows 117, 512 rows 454 (1180 TFLOP/s, 0.60 of what a bf16 product
+// reaches), 1024 rows 892.  Bound by the instructions of the parts together, 60% of the issue slots, and by the
+// handing on between them: without the products, the reading of sums or the writing of operands it takes 2 to 5%
+// less.  So, too, smaller groups cost (512 rows by 64: 785 us, by 32: 1245): a sum's barriers take as long as its
+// products, some 500 clocks a block.  With 8 groups' columns added before they are scaled that would be gone, and
+// so would the exactness.
 #include <algorithm>
 #include <cmath>
 

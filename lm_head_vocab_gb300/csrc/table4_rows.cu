@@ -3,10 +3,15 @@
 // Bound by memory, as long as the instructions that widen 4 bits stay beside it: an SM gets about 46 numbers a
 // clock.  So each warp goes on its own, from one barrier a stage to the next: ldmatrix brings a warp's words in
 // the order in which mma.sync takes its A operand (a thread's word is eight columns of one row), five
-// operations widen a word, and a thread's group sums are scaled where they are.  For so few rows that is less
-// than tensor memory costs: there, what widens, multiplies and adds are different warps, and the barriers and
-// copies between them took more instructions than the numbers (128256 x 4096, one row: 90 us).
+// operations widen a word, and a thread's group sums, less the zero points' part z sum x, are scaled where they
+// are.  For so few rows that is less than tensor memory costs: there, what widens, multiplies and adds are
+// different warps, and the barriers and copies between them took more instructions than the numbers (128256 x 4096,
+// one row, by the kernel for more rows: 71 us, 51 here).
 // Each block lays the hidden rows out in its own shared memory, under the way of its first stages.
+//
+// 128256 x 4096 in groups of 128: one row 51 us, 8 rows 64 (5.3 and 4.2 TB/s; 41 us at the copy's rate), by 32 79.  Half
+// of the issue slots are used (some 240 instructions for 32 rows x 128 columns, the smaller the group the more), and
+// the DRAM 68% of the time: neither alone bounds it.
 #include <algorithm>
 
 #include "table4_logits.cuh"
