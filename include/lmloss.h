@@ -662,10 +662,10 @@ lmloss_status lmloss_table4_logits_workspace(const lmloss_table4_logits_args* ar
  * prompt's.  Within a group the products with the whole numbers q - z are summed, and the sum
  * is scaled by the group's scale: no weight is rounded.  Sums in fp32, one rounding at the end.
  * fp32 hidden values count with an error of at most 2^-23 of the largest in their group of
- * columns, 16-bit ones with none down to 2^-35 of their row's largest.  A row with an
+ * columns, 16-bit ones of at most 2^-35 of the largest in their row.  A row with an
  * infinity or NaN gives what the formula gives, slowly, and does not disturb the others.  A
- * row's logits depend on that row, the table and T alone.  `logits` overlaps neither `hidden`
- * nor the table.  A wait inside that expires sets LMLOSS_ERR_TIMEOUT; the logits mean nothing then.
+ * row's logits depend on that row, its index, the table and T alone.  `logits` overlaps neither
+ * `hidden` nor the table.  A wait inside that expires sets LMLOSS_ERR_TIMEOUT; the logits mean nothing then.
  */
 lmloss_status lmloss_table4_logits(lmloss_vocab_handle handle, const lmloss_table4_logits_args* args,
                                    cudaStream_t stream);
