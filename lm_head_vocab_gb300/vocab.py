@@ -490,11 +490,12 @@ class VocabOps:
         return r
 
     def _logprobs_out(self, tokens, T, M, entropy):
-        empty, dev, f32 = torch.empty, self.device, torch.float32
-        return TokenLogprobs(None if tokens is None else empty(tokens.shape, dtype=f32, device=dev),
-                             empty((T,), dtype=f32, device=dev), empty((T,), dtype=f32, device=dev) if entropy else None,
-                             empty((T, M), dtype=f32, device=dev) if M else None,
-                             empty((T, M), dtype=torch.int64, device=dev) if M else None)
+        # (a tensor like another costs the host half of what one of a shape does)
+        empty, like, dev, f32 = torch.empty, torch.empty_like, self.device, torch.float32
+        lse = empty((T,), dtype=f32, device=dev)
+        top = empty((T, M), dtype=f32, device=dev) if M else None
+        return TokenLogprobs(None if tokens is None else like(tokens, dtype=f32), lse, like(lse) if entropy else None,
+                             top, like(top, dtype=torch.int64) if M else None)
 
     def token_logprobs_backward(self, logits: torch.Tensor, lse: torch.Tensor, tokens: Optional[torch.Tensor] = None,
                                 grad_logp: Optional[torch.Tensor] = None, *, entropy: Optional[torch.Tensor] = None,
@@ -572,6 +573,25 @@ class VocabOps:
 
     def _table4(self, t: Table4):
         """A table's lmloss_table4."""
+        values, scales, zeros, D, g, index = t.values, t.scales, t.zeros, t.columns, t.group_size, self._index
+        shape, s_shape, v_stride, s_stride, s_type = values.shape, scales.shape, values.stride(), scales.stride(), scales.dtype
+        # what is in order, at once
+        if len(shape) == 2 and g in (32, 64, 128) and D > 0 and values.dtype is torch.uint8 and s_type in _FLOATS:
+            V, G = shape[0], (D + g - 1) // g
+            bytes_, ld, v_at, s_at = v_stride[0], s_stride[0], values.data_ptr(), scales.data_ptr()
+            if V > 1 and G > 1 and shape[1] == (D + 1) // 2 and s_shape == (G, V) and v_stride[1] == s_stride[1] == 1 and \
+                    bytes_ >= shape[1] and ld >= V and (bytes_ | ld * s_type.itemsize | v_at | s_at) % 16 == 0 and \
+                    values.get_device() == scales.get_device() == index:
+                if zeros is None:
+                    return _lib.lmloss_table4(v_at, bytes_, s_at, ld, None, 0, V, D, g, _FLOATS[s_type])
+                z_stride, z_at = zeros.stride(), zeros.data_ptr()
+                if zeros.dtype is torch.uint8 and zeros.shape == s_shape and z_stride[1] == 1 and z_stride[0] >= V and \
+                        (z_stride[0] | z_at) % 16 == 0 and zeros.get_device() == index:
+                    return _lib.lmloss_table4(v_at, bytes_, s_at, ld, z_at, z_stride[0], V, D, g, _FLOATS[s_type])
+        return self._table4_looked_at(t)
+
+    def _table4_looked_at(self, t: Table4):
+        """The same for a table of one row or group, or the error of one that is not in order."""
         values, scales, zeros, index = t.values, t.scales, t.zeros, self._index
         V, D, g = values.size(0), t.columns, t.group_size
         if g not in (32, 64, 128):
