@@ -323,9 +323,10 @@ lmloss_status lmloss_shard_grad(lmloss_handle handle, const lmloss_args* args, i
 typedef struct lmloss_vocab_ctx* lmloss_vocab_handle;
 
 /* A handle on `device` with `workspace_bytes` of workspace: the most that any of
- * its calls needs by lmloss_embedding_workspace / lmloss_beam_workspace (0 serves
- * the lookup, the reordering and gradients of up to 1024 positions, which need
- * none). */
+ * its calls needs by lmloss_embedding_workspace / lmloss_beam_workspace /
+ * lmloss_logprobs_workspace / lmloss_table4_logits_workspace (0 serves the lookups, the
+ * reordering, gradients of up to 1024 positions and of log-probabilities, and the making of
+ * 4-bit tables, which need none). */
 lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_t workspace_bytes);
 
 /* Free the handle and its workspace.  Synchronises the handle's device. */
