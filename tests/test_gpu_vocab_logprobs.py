@@ -394,3 +394,22 @@ def test_on_a_stream_of_the_callers(ops):
     s.synchronize()
     assert torch.equal(r.logp, want.logp) and torch.equal(r.top_tokens, want.top_tokens)
     assert torch.equal(d, ops.token_logprobs_backward(z, want.lse, t, torch.ones_like(want.logp)))
+
+
+def test_offsets_past_32_bits(ops):
+    # 2.6e9 logits: the last rows are those of the same rows alone
+    T, V, far = 20000, 128256, 300
+    z = torch.empty(T, V, device="cuda", dtype=BF)
+    z.normal_(0.0, 2.0, generator=gen(103))
+    tokens = torch.randint(0, V, (T, 3), device="cuda", generator=gen(104))
+    r = ops.token_logprobs(z, tokens, num_top=5)
+    e = ops.token_logprobs(z[-far:], tokens[-far:], num_top=5)
+    for a, b in ((r.logp, e.logp), (r.lse, e.lse), (r.entropy, e.entropy), (r.top_logp, e.top_logp)):
+        # (a row alone is cut into other parts: a few steps of fp32)
+        assert bool(((a[-far:] - b).abs() <= 2.0 ** -19 * b.abs().clamp(min=1)).all())
+    assert torch.equal(r.top_tokens[-far:], e.top_tokens)
+    g, ge = torch.randn(T, 3, device="cuda", generator=gen(105)), torch.randn(T, device="cuda", generator=gen(106))
+    want = ops.token_logprobs_backward(z[-far:], r.lse[-far:], tokens[-far:], g[-far:], entropy=r.entropy[-far:], grad_entropy=ge[-far:])
+    got = ops.token_logprobs_backward(z, r.lse, tokens, g, entropy=r.entropy, grad_entropy=ge, grad="inplace")
+    assert torch.equal(got[-far:], want)
+    assert ops.device_error() == 0

@@ -495,3 +495,52 @@ def test_handles_of_several_threads():
         th.join()
     h.close()
     assert not failed, failed
+
+
+def test_offsets_past_32_bits(ops):
+    # weights of 2.5e9 elements, rows of as many, logits of 2.4e9: the far ends are those of the same rows alone
+    V, D, far = 600064, 4160, 4000
+    w = torch.empty(V, D, device="cuda", dtype=BF)
+    w.normal_(0.0, 0.02, generator=gen(101))
+    t = ops.quantize_table(w, group_size=64, zeros=True)
+    end = ops.quantize_table(w[-far:], group_size=64, zeros=True)
+    assert torch.equal(t.values[-far:], end.values) and torch.equal(t.scales[:, -far:], end.scales)
+    assert torch.equal(t.zeros[:, -far:], end.zeros)
+    ids = torch.arange(V, device="cuda")
+    rows = ops.table4_lookup(t, ids, out=w)
+    assert torch.equal(rows[-far:], ops.table4_lookup(end, ids[:far], out_dtype=BF))
+    del w, rows
+    x = hidden(4000, D, BF)
+    z = ops.table4_logits(t, x)
+    assert torch.equal(z[:, -far:], ops.table4_logits(end, x))
+    one = ops.table4_logits(t, x[:1])
+    assert torch.equal(one[:, -far:], ops.table4_logits(end, x[:1]))
+    assert ops.device_error() == 0
+
+
+def test_two_graphs_of_one_handle_in_turn(ops):
+    # they share the handle's workspace and counters, and run one after the other
+    t = table(ops, 5003, 768, 64, H, True)
+    xs = [hidden(T, 768, BF, seed=110 + T) for T in (20, 90)]
+    runs = []
+    for x in xs:
+        def step(x=x):
+            z = ops.table4_logits(t, x, out_dtype=F)
+            return z, ops.token_logprobs(z[:3], num_top=20)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        runs.append((graph, out, step))
+    for i, x in enumerate(xs):
+        x.copy_(hidden(len(x), 768, BF, seed=120 + i))
+    for _ in range(3):
+        for graph, _, _ in runs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, step in runs:
+        z, r = step()
+        assert torch.equal(out[0], z) and torch.equal(out[1].top_tokens, r.top_tokens) and torch.equal(out[1].lse, r.lse)
+        assert torch.equal(out[1].top_logp, r.top_logp) and torch.equal(out[1].entropy, r.entropy)
+    assert ops.device_error() == 0
