@@ -563,13 +563,12 @@ class VocabOps:
             raise ValueError("a 4-bit table has at least one row and column, and groups of 32, 64 or 128")
         if scale_dtype not in _FLOATS:
             raise TypeError(f"scale_dtype: must be bfloat16, float16 or float32, got {scale_dtype}")
-        G, wide = (columns + group_size - 1) // group_size, (num_embeddings + 15) // 16 * 16
-        dev = self.device
-        values = torch.empty((num_embeddings, (columns + 31) // 32 * 16), dtype=torch.uint8, device=dev)
-        scales = torch.empty((G, wide), dtype=scale_dtype, device=dev)
-        z = torch.empty((G, wide), dtype=torch.uint8, device=dev) if zeros else None
-        return Table4(values[:, :(columns + 1) // 2], scales[:, :num_embeddings],
-                      None if z is None else z[:, :num_embeddings], columns, group_size)
+        G, wide, half = (columns + group_size - 1) // group_size, (num_embeddings + 15) // 16 * 16, (columns + 1) // 2
+        ld, dev = (half + 15) // 16 * 16, self.device
+        values = torch.empty((num_embeddings, ld), dtype=torch.uint8, device=dev).as_strided((num_embeddings, half), (ld, 1))
+        scales = torch.empty((G, wide), dtype=scale_dtype, device=dev).as_strided((G, num_embeddings), (wide, 1))
+        z = torch.empty((G, wide), dtype=torch.uint8, device=dev).as_strided((G, num_embeddings), (wide, 1)) if zeros else None
+        return Table4(values, scales, z, columns, group_size)
 
     def _table4(self, t: Table4):
         """A table's lmloss_table4."""
