@@ -9,6 +9,7 @@
 // weight and lane); 32767 of 151936 x 2048 to bf16, 39 us (0.66).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "table4.cuh"
 
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(256) lookup_words_kernel(const __grid_constant
 // vectors) that lie on 16-byte boundaries of the row, each put together from a word's numbers and the last of the word
 // before, which the neighbouring thread has.  The warp before ends with this one's first word.
 // (By vectors on their own, with two words, two groups and a scale for each number, it took 45 instructions a
-// number: 32003 x 1001 to fp32, 79 us.)
+// number: 32003 x 1001 to fp32, 79 us.  Of fp32, with half a sector written at a time, 37.6, and 33.6 so.)
 template <class R, class S>
 __global__ void __launch_bounds__(256) lookup_shifted_kernel(const __grid_constant__ LookupParams p)
 {
@@ -436,37 +437,47 @@ __global__ void __launch_bounds__(256) lookup_shifted_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[4 + i] = own.w[i];
         const int sh = 16 - off * R::kBytes;   // bytes to leave out: 16 where rows are aligned
-        if (sh & 16) {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) w[i] = w[i + 4];
-        }
-        if (sh & 8) {
-#pragma unroll
-            for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
-        }
-        if (sh & 4) {
-#pragma unroll
-            for (int i = 0; i < kWords + 3; ++i) w[i] = w[i + 1];
-        }
         Pack<R, 8> v;
+        auto leave_out = [&](auto words) {     // (a row's, so that a warp goes one way)
+            constexpr int kOut = decltype(words)::value;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) v.w[i] = R::kBytes == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], (sh & 2) * 8);
+            for (int i = 0; i < kWords; ++i) {
+                const int next = i + kOut + 1 < kWords + 4 ? i + kOut + 1 : kWords + 3;   // (of 16 bytes none is needed)
+                v.w[i] = R::kBytes == 4 ? w[i + kOut] : __funnelshift_r(w[i + kOut], w[next], (sh & 2) * 8);
+            }
+        };
+        switch (sh >> 2) {
+        case 0: leave_out(std::integral_constant<int, 0>{}); break;
+        case 1: leave_out(std::integral_constant<int, 1>{}); break;
+        case 2: leave_out(std::integral_constant<int, 2>{}); break;
+        case 3: leave_out(std::integral_constant<int, 3>{}); break;
+        default: leave_out(std::integral_constant<int, 4>{});
+        }
         // numbers [first, first + 8) of the row; the thread behind its last word has what that word leaves
         const int first = c - off;
-        if (lane == 0 || first >= t.D) continue;
-#pragma unroll
-        for (int u = 0; u < 8 / kUnit; ++u) {
-            const int from = first + u * kUnit;
+        auto put = [&](int from, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
             if (from >= 0 && from + kUnit <= t.D) {
-                *reinterpret_cast<uint4*>(out + from) = make_uint4(v.w[4 * u], v.w[4 * u + 1], v.w[4 * u + 2], v.w[4 * u + 3]);
+                *reinterpret_cast<uint4*>(out + from) = make_uint4(w0, w1, w2, w3);
             } else {
+                const uint32_t some[4] = {w0, w1, w2, w3};
 #pragma unroll
                 for (int i = 0; i < kUnit; ++i)
                     if (from + i >= 0 && from + i < t.D) {
-                        if constexpr (R::kBytes == 4) out[from + i] = v.w[4 * u + i];
-                        else out[from + i] = static_cast<typename R::raw>(v.w[4 * u + i / 2] >> (16 * (i & 1)));
+                        if constexpr (R::kBytes == 4) out[from + i] = some[i];
+                        else out[from + i] = static_cast<typename R::raw>(some[i / 2] >> (16 * (i & 1)));
                     }
             }
+        };
+        if constexpr (R::kBytes == 2) {
+            if (lane > 0) put(first, v.w[0], v.w[1], v.w[2], v.w[3]);
+        } else {
+            // two neighbours write the one's 32 bytes, then the other's: whole sectors at once
+            const bool odd = lane & 1;
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = __shfl_xor_sync(0xffffffffu, odd ? v.w[i] : v.w[4 + i], 1);
+            if (lane > 1) put(odd ? first - 4 : first, odd ? y[0] : v.w[0], odd ? y[1] : v.w[1], odd ? y[2] : v.w[2], odd ? y[3] : v.w[3]);
+            put(odd ? first + 4 : first + 8, odd ? v.w[4] : y[0], odd ? v.w[5] : y[1], odd ? v.w[6] : y[2], odd ? v.w[7] : y[3]);
         }
     }
 }
