@@ -8,7 +8,8 @@
 //
 // so one pass with a running maximum gives all of it: a part of a row keeps (m, s, e), and
 // when m rises by d (in u's units) s becomes s 2^-d and e becomes (e - d s) 2^-d.  In place of m log2(e) / tau
-// stands its fp32 value R, so that u is one fused operation; what R is off by goes into lse.
+// stands its fp32 value R, so that u is one fused operation; what R is off by goes into lse.  (Maxima for which R is off
+// by more than 2 are taken off before the product.)
 // Alternatives are kept as in a beam step: a threshold from group maxima, vectors noted against it.
 //
 // The gradient is one more pass, from lse and H alone: p = e^(y - lse).
@@ -44,6 +45,7 @@ struct LogprobsParams {
     int M;
     int slices, tiles;           // parts of a row, tiles of a part
     float mul;                   // log2(e) / tau
+    float near, counted;         // 2^26 and 2^27 over mul: see usual and counts
     double inv_tau;
     const void* tokens;
     int ids32;
@@ -93,14 +95,17 @@ struct Sums {
     }
 };
 
-// Whether a maximum leaves room for z log2(e) / tau in fp32, and, of bf16, for what stands in the place of -inf in the
-// sum of u 2^u: -2^100, which is nothing beside it.  Parts of other maxima (rows at the type's lowest values) are
-// summed again, by sum_slowly.
-template <class T>
-__device__ __forceinline__ bool usual(float m)
-{
-    return T::kIndex == Fp16::kIndex || fabsf(m) < 0x1p99f;
-}
+// Whether a part's sums may go about R = fl(m mul).  What R is off, half of its last place at most, stands in every
+// exponent: from m mul = 2^30 on 2^(m mul - R) leaves fp32's range, and well before the entropy loses its last places, as
+// ln s and e / s both hold it.  Up to 2^26 (logits of 46 at a temperature of 1e-6) it is 2 at most.  Parts of larger maxima
+// are summed again, by sum_slowly.
+__device__ __forceinline__ bool usual(const LogprobsParams& p, float m) { return fabsf(m) < p.near; }
+// Whether a thread's or a warp's logits count yet.  Those of a lower maximum than -2^27 / mul are left out: they lie 2^26 below
+// any maximum that is usual, and the others' parts are summed again.
+__device__ __forceinline__ bool counts(const LogprobsParams& p, float m) { return fabsf(m) < p.counted; }
+
+// Of bf16 -2^100 stands in the place of -inf (and of what lies below) in the sum of u 2^u: nothing beside a maximum that
+// counts.
 template <class T>
 __device__ __forceinline__ uint32_t floor_pair(uint32_t w)
 {
@@ -233,12 +238,16 @@ __device__ __forceinline__ void write_sums(const LogprobsParams& p, LogprobsShar
     if (p.entropy_out) p.entropy_out[row] = none ? 0.f : (m == INFINITY ? NAN : static_cast<float>(log_s - kLn2 * static_cast<double>(e / hi)));
 }
 
-// The maximum's part of lse: m / tau, and what R = fl(m mul) is off from m mul, which the sums about R hold.
-template <class T>
+// What R = fl(m mul) is off from m mul, which the sums of a part about R hold: exact.  0 for sums about m itself.
+__device__ __forceinline__ float off_by(const LogprobsParams& p, float m)
+{
+    return usual(p, m) ? fmaf(-m, p.mul, __fmul_rn(m, p.mul)) : 0.f;
+}
+
+// The maximum's part of lse: m / tau, and what the sums hold beside.
 __device__ __forceinline__ double lse_part(const LogprobsParams& p, float m)
 {
-    const double at = static_cast<double>(m) * p.inv_tau;
-    return usual<T>(m) && fabsf(m) < INFINITY ? at + kLn2 * (static_cast<double>(__fmul_rn(m, p.mul)) - static_cast<double>(m) * static_cast<double>(p.mul)) : at;
+    return static_cast<double>(m) * p.inv_tau + kLn2 * static_cast<double>(off_by(p, m));
 }
 
 // Given token j of a row: what stands for its log-probability until lse is known.
@@ -311,7 +320,9 @@ __device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& s
         };
         for (int s = lane; s < S; s += 32) {
             const float4 q = __ldcg(&st[s]);
-            const float apart = usual<T>(q.x) && usual<T>(m) ? __fmul_rn(q.x, p.mul) - __fmul_rn(m, p.mul) : (q.x - m) * p.mul;
+            // (of two values of R the difference is exact where it matters; next to where sums go about m itself what R is off counts)
+            const float apart = usual(p, q.x) && usual(p, m) ? __fmul_rn(q.x, p.mul) - __fmul_rn(m, p.mul)
+                                                             : (q.x - m) * p.mul + (off_by(p, q.x) - off_by(p, m));
             const float d = q.x == m ? 0.f : fmaxf(apart, kLeast), f = exp2f(d);
             add(q.y * f, 0.f);
             e += fmaf(q.y, d, q.z) * f;
@@ -322,7 +333,7 @@ __device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& s
             e += __shfl_xor_sync(0xffffffffu, e, o);
         }
     }
-    if (tid == 0) write_sums(p, sm, row, lse_part<T>(p, m), hi, lo, e);
+    if (tid == 0) write_sums(p, sm, row, lse_part(p, m), hi, lo, e);
     if (M > 0) {
         const int all = S * M;
         uint64_t* const held = reinterpret_cast<uint64_t*>(sm.data);
@@ -379,18 +390,25 @@ __device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& s
 }
 
 // A part whose maximum is finite and not usual: 2^u about the maximum itself, taken off before the product.  Each warp's
-// into its place.
-template <class T>
-__device__ __noinline__ void sum_slowly(const LogprobsParams& p, LogprobsShared& sm, const typename T::raw* z, const int32_t* mask, int begin, int end,
+// sums into its place.
+template <class T, bool ALIGNED>
+__device__ __noinline__ void sum_slowly(const LogprobsParams& p, LogprobsShared& sm, const RowLogits<T> r, const int32_t* mask, int begin, int end,
                                         float top)
 {
+    constexpr int E = Logits<T>::E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float s = 0.f, e = 0.f;
-    for (int c = begin + tid; c < end; c += kThreads) {
-        if (!allowed(mask, c)) continue;
-        const float u = max_nan((T::widen(z[c]) - top) * p.mul, kLeast), w = ex2(u);
-        s += w;
-        e = fmaf(w, u, e);
+#pragma unroll 2
+    for (int c = begin + tid * E; c < end; c += kThreads * E) {
+        Pack<T, E> q;
+        load_logits<T, ALIGNED>(q, r, c);
+        const uint32_t allow = mask ? static_cast<uint32_t>(mask[c >> 5]) >> (c & 31) : 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float z = allow >> i & 1u ? q.get(i) : -INFINITY, u = max_nan((z - top) * p.mul, kLeast), w = ex2(u);
+            s += w;
+            e = fmaf(w, u, e);
+        }
     }
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -460,8 +478,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             ++tile;
             if (raise) rank_keys(m > -INFINITY ? ordered(m == 0.f ? 0.f : m) : 0u, p.M, sm.group, &sm.thr);
         }
-        // (of a maximum that is not usual only rounding errors would be left: its logits count as 0 until it is)
-        sum.raise(usual<T>(m) ? __fmul_rn(m, p.mul) : -INFINITY);
+        sum.raise(counts(p, m) ? __fmul_rn(m, p.mul) : -INFINITY);
         const float less = sum.r == -INFINITY ? 0.f : -sum.r;
         const uint64_t less2 = f2_pack(less, less), mul2 = f2_pack(p.mul, p.mul);
         uint64_t s2 = f2_pack(0.f, 0.f), e2 = f2_pack(0.f, 0.f);
@@ -540,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     // ---- the part's sums
     {
         const float top = warp_max(m);
-        sum.raise(usual<T>(top) ? __fmul_rn(top, p.mul) : -INFINITY);
+        sum.raise(counts(p, top) ? __fmul_rn(top, p.mul) : -INFINITY);
         for (int o = 16; o > 0; o >>= 1) {
             sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
             if (ENT) sum.e += __shfl_xor_sync(0xffffffffu, sum.e, o);
@@ -556,21 +573,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     float top = sm.red_m[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.red_m[w]);
-    if (!usual<T>(top) && fabsf(top) < INFINITY) sum_slowly<T>(p, sm, r.z, mask, begin, end, top);
+    if (!usual(p, top) && fabsf(top) < INFINITY) sum_slowly<T, ALIGNED>(p, sm, r, mask, begin, end, top);
     if (warp == 0) {
         Sums w;
         const float mw = lane < kWarps ? sm.red_m[lane] : -INFINITY;
-        w.r = usual<T>(top) ? __fmul_rn(mw, p.mul) : mw;
+        w.r = usual(p, top) ? __fmul_rn(mw, p.mul) : mw;
         w.s = lane < kWarps ? sm.red_s[lane] : 0.f;
         w.e = lane < kWarps ? sm.red_e[lane] : 0.f;
-        w.raise(usual<T>(top) ? __fmul_rn(top, p.mul) : top);
+        w.raise(usual(p, top) ? __fmul_rn(top, p.mul) : top);
         for (int o = 4; o > 0; o >>= 1) {
             w.s += __shfl_xor_sync(0xffffffffu, w.s, o);
             w.e += __shfl_xor_sync(0xffffffffu, w.e, o);
         }
         if (lane == 0) {
             if (p.slices > 1) p.stats[blockIdx.x] = make_float4(top, w.s, w.e, 0.f);
-            else write_sums(p, sm, row, lse_part<T>(p, top), w.s, 0.f, w.e);
+            else write_sums(p, sm, row, lse_part(p, top), w.s, 0.f, w.e);
         }
     }
 
@@ -982,6 +999,8 @@ lmloss_status lmloss_logprobs_forward(lmloss_vocab_handle h, const lmloss_logpro
         p.slices = P.slices;
         p.tiles = P.tiles;
         p.mul = static_cast<float>(1.4426950408889634074 / static_cast<double>(a->temperature));
+        p.near = 0x1p26f / p.mul;
+        p.counted = 0x1p27f / p.mul;
         p.inv_tau = 1.0 / static_cast<double>(a->temperature);
         p.tokens = a->n ? static_cast<const unsigned char*>(a->tokens) + r0 * a->n * id_bytes : nullptr;
         p.ids32 = a->ids_dtype == LMLOSS_INT32;
