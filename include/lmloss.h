@@ -515,6 +515,8 @@ typedef struct {
     float* entropy_out;          /* optional [T]                                           */
     float* top_logp_out;         /* [T, M]                                                 */
     int64_t* top_tokens_out;     /* [T, M]                                                 */
+    float* row_max_out;          /* optional [T]: the row's largest allowed logit          */
+    float* log_sum_out;          /* optional [T]: lse - row_max / tau                      */
 } lmloss_logprobs_args;
 
 /* Host-only validation of `args` (no CUDA call). */
@@ -533,10 +535,10 @@ lmloss_status lmloss_logprobs_workspace(const lmloss_logprobs_args* args, size_t
  *   - Alternatives come in the exact order of their logits, equal ones by token.  Where
  *     fewer than M have a finite logit and are allowed, the rest gets -inf and
  *     LMLOSS_IGNORE_INDEX.
- *   - A row in which nothing is allowed (or every allowed logit is -inf): lse -inf, entropy 0,
- *     log-probabilities -inf.
- *   - NaN or +inf in an allowed column: lse, entropy and log-probabilities are NaN, and the
- *     row has no alternatives.  What stands in columns that are not allowed has no effect.
+ *   - A row in which nothing is allowed (or every allowed logit is -inf): lse, row_max and
+ *     log_sum -inf, entropy 0, log-probabilities -inf.
+ *   - NaN or +inf in an allowed column: lse, log_sum, entropy and log-probabilities are NaN, and
+ *     the row has no alternatives.  What stands in columns that are not allowed has no effect.
  */
 lmloss_status lmloss_logprobs_forward(lmloss_vocab_handle handle, const lmloss_logprobs_args* args,
                                       cudaStream_t stream);
@@ -553,13 +555,15 @@ typedef struct {
     float temperature;
     const int32_t* token_mask;
     int64_t mask_stride;
-    const float* lse;            /* [T] of the forward call                                */
+    const float* lse;            /* [T] of the forward call; not looked at beside log_sum  */
     const float* grad_logp;      /* [T, n] or NULL with n = 0                              */
     const float* entropy;        /* [T] of the forward call, with grad_entropy             */
     const float* grad_entropy;   /* optional [T]                                           */
     void* grad_out;              /* [T, ld_grad] dtype, written whole; == logits with the  */
                                  /* same ld writes in place, otherwise no overlap          */
     int64_t ld_grad;             /* row stride in elements, >= V                           */
+    const float* row_max;        /* optional [T] of the forward call, both or neither      */
+    const float* log_sum;        /* optional [T]                                           */
 } lmloss_logprobs_grad_args;
 
 /* Host-only validation of `args` (no CUDA call). */
@@ -567,10 +571,14 @@ lmloss_status lmloss_logprobs_check_grad_args(const lmloss_logprobs_grad_args* a
 
 /*
  * grad_out[r][v] = ( sum_{j: t_j = v} g_j - p_v (sum_j g_j + gH (ln p_v + H)) ) / tau
- * in fp32, rounded once; 0 in columns that are not allowed, and in a whole row whose lse
- * is -inf.  A token given twice counts twice; one that is not allowed still takes its
- * -g p from the others, as its logp = -inf - lse does.  Tokens outside [0, V) that are not
- * LMLOSS_IGNORE_INDEX set LMLOSS_ERR_BAD_TARGET and add nothing.  No workspace.
+ * in fp32, rounded once; 0 in columns that are not allowed, and in a whole row whose log_sum
+ * (without it: lse) is -inf.  With row_max and log_sum, ln p_v = (z_v - row_max) / tau - log_sum,
+ * as good at every temperature.  With lse alone, ln p_v = y_v - lse: p is off by a factor of
+ * e to what fp32 leaves of lse (2^-24 of it: 1e-6 for an lse of 15, 1e-3 for 15000), and a row
+ * whose lse passes fp32's range gets 0.  A token given twice counts twice; one that is not
+ * allowed still takes its -g p from the others, as its logp = -inf - lse does.  Tokens outside
+ * [0, V) that are not LMLOSS_IGNORE_INDEX set LMLOSS_ERR_BAD_TARGET and add nothing.  No
+ * workspace.
  */
 lmloss_status lmloss_logprobs_backward(lmloss_vocab_handle handle, const lmloss_logprobs_grad_args* args,
                                        cudaStream_t stream);

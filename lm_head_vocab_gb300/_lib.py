@@ -209,6 +209,8 @@ class lmloss_logprobs_args(ctypes.Structure):
         ("entropy_out", ctypes.c_void_p),
         ("top_logp_out", ctypes.c_void_p),
         ("top_tokens_out", ctypes.c_void_p),
+        ("row_max_out", ctypes.c_void_p),
+        ("log_sum_out", ctypes.c_void_p),
     ]
 
 
@@ -231,6 +233,8 @@ class lmloss_logprobs_grad_args(ctypes.Structure):
         ("grad_entropy", ctypes.c_void_p),
         ("grad_out", ctypes.c_void_p),
         ("ld_grad", ctypes.c_int64),
+        ("row_max", ctypes.c_void_p),
+        ("log_sum", ctypes.c_void_p),
     ]
 
 

@@ -12,7 +12,7 @@
 // by more than 2 are taken off before the product.)
 // Alternatives are kept as in a beam step: a threshold from group maxima, vectors noted against it.
 //
-// The gradient is one more pass, from lse and H alone: p = e^(y - lse).
+// The gradient is one more pass, from m, ln s and H alone: p = e^((z - m) / tau - ln s), or, given only lse, e^(y - lse).
 //
 // 4096 x 128256 bf16: forward 172 us without alternatives (0.91 of the copy's rate), 182 with 5, 244 with 64; the
 // gradient with entropies 310 us (1.01).  One row of 128256 with 20 alternatives: 11 us, the latency of two dependent
@@ -56,6 +56,8 @@ struct LogprobsParams {
     float* entropy_out;
     float* top_logp_out;
     int64_t* top_tokens_out;
+    float* row_max_out;
+    float* log_sum_out;
     uint64_t* keys;              // [T][slices][M] where rows are cut: each part's best, 0 = none
     float4* stats;               // [T][slices] (m, s, e, -)
     unsigned* done;              // [T] parts finished; 0 between calls
@@ -227,27 +229,24 @@ __device__ __noinline__ void rank_best(LogprobsShared& sm, const uint64_t* set, 
     __syncthreads();
 }
 
-// A row's statistics from its sums, by one thread.  m: the maximum's part of lse.
-__device__ __forceinline__ void write_sums(const LogprobsParams& p, LogprobsShared& sm, int row, double m, float hi, float lo, float e)
-{
-    const bool none = m == -INFINITY && hi == 0.f;
-    const double log_s = none ? 0.0 : log_of_sum(hi, lo);
-    const double lse = none ? -INFINITY : (m == INFINITY ? NAN : m + log_s);
-    sm.lse = lse;
-    if (p.lse_out) p.lse_out[row] = static_cast<float>(lse);
-    if (p.entropy_out) p.entropy_out[row] = none ? 0.f : (m == INFINITY ? NAN : static_cast<float>(log_s - kLn2 * static_cast<double>(e / hi)));
-}
-
 // What R = fl(m mul) is off from m mul, which the sums of a part about R hold: exact.  0 for sums about m itself.
 __device__ __forceinline__ float off_by(const LogprobsParams& p, float m)
 {
     return usual(p, m) ? fmaf(-m, p.mul, __fmul_rn(m, p.mul)) : 0.f;
 }
 
-// The maximum's part of lse: m / tau, and what the sums hold beside.
-__device__ __forceinline__ double lse_part(const LogprobsParams& p, float m)
+// A row's statistics from its maximum and sums, by one thread.
+__device__ __forceinline__ void write_sums(const LogprobsParams& p, LogprobsShared& sm, int row, float m, float hi, float lo, float e)
 {
-    return static_cast<double>(m) * p.inv_tau + kLn2 * static_cast<double>(off_by(p, m));
+    const bool none = m == -INFINITY && hi == 0.f;
+    const double log_s = none ? -INFINITY : (m == INFINITY ? NAN : log_of_sum(hi, lo));
+    const double log_sum = log_s + kLn2 * static_cast<double>(off_by(p, m));
+    const double lse = static_cast<double>(m) * p.inv_tau + log_sum;
+    sm.lse = lse;
+    if (p.lse_out) p.lse_out[row] = static_cast<float>(lse);
+    if (p.entropy_out) p.entropy_out[row] = none ? 0.f : static_cast<float>(log_s - kLn2 * static_cast<double>(e / hi));
+    if (p.row_max_out) p.row_max_out[row] = m;
+    if (p.log_sum_out) p.log_sum_out[row] = static_cast<float>(log_sum);
 }
 
 // Given token j of a row: what stands for its log-probability until lse is known.
@@ -333,7 +332,7 @@ __device__ __noinline__ void join_row(const LogprobsParams& p, LogprobsShared& s
             e += __shfl_xor_sync(0xffffffffu, e, o);
         }
     }
-    if (tid == 0) write_sums(p, sm, row, lse_part(p, m), hi, lo, e);
+    if (tid == 0) write_sums(p, sm, row, m, hi, lo, e);
     if (M > 0) {
         const int all = S * M;
         uint64_t* const held = reinterpret_cast<uint64_t*>(sm.data);
@@ -587,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         }
         if (lane == 0) {
             if (p.slices > 1) p.stats[blockIdx.x] = make_float4(top, w.s, w.e, 0.f);
-            else write_sums(p, sm, row, lse_part(p, top), w.s, 0.f, w.e);
+            else write_sums(p, sm, row, top, w.s, 0.f, w.e);
         }
     }
 
@@ -654,7 +653,8 @@ struct GradParams {
     int ids32;
     const int32_t* mask;
     int64_t mask_stride;
-    const float* lse;
+    const float* row_max;        // with log_sum; NULL: 0, with lse
+    const float* less;           // log_sum, or lse
     const float* entropy;
     const float* grad_logp;
     const float* grad_entropy;
@@ -671,18 +671,20 @@ struct __align__(16) GradShared {
     float red[kWarps];
 };
 
-// -p (sum g + gH (ln p + H)) / tau for the columns without a given token's own part, p = e^d, d = z / tau - lse.  The
-// difference is taken in two fused operations, 1 / tau as a pair, before the change to base 2: of rows at the type's
-// lowest values it is all that is left.
+// -p (sum g + gH (ln p + H)) / tau for the columns without a given token's own part, p = e^d, d = (z - m) / tau - less: m the
+// row's maximum and less its ln s, or 0 and lse.  lse alone has 2^-24 of itself for all that p is to be known by:
+// nothing at temperatures near 1e-6.  The difference is taken in two fused operations, 1 / tau as a pair, before the
+// change to base 2: of rows at the type's lowest values it is all that is left.
 template <bool ENT>
 struct GradColumn {
-    float tau_inv, tau_inv_lo, less, base, ge;
-    __device__ __forceinline__ GradColumn(const GradParams& p, float lse, float sum, float h, float gh)
-        : tau_inv(p.tau_inv), tau_inv_lo(p.tau_inv_lo), less(-lse), base(-(ENT ? fmaf(gh, h, sum) : sum) * p.tau_inv), ge(-gh * p.tau_inv)
+    float tau_inv, tau_inv_lo, max, less, base, ge;
+    __device__ __forceinline__ GradColumn(const GradParams& p, float m, float less, float sum, float h, float gh)
+        : tau_inv(p.tau_inv), tau_inv_lo(p.tau_inv_lo), max(-m), less(-less), base(-(ENT ? fmaf(gh, h, sum) : sum) * p.tau_inv), ge(-gh * p.tau_inv)
     {
     }
     __device__ __forceinline__ void two(float& a, float& c) const
     {
+        f2_unpack(f2_add(f2_pack(a, c), f2_pack(max, max)), a, c);
         // (-inf takes no second product, and 0 * -inf would be NaN)
         const uint64_t d2 = f2_fma(f2_pack(max_nan(a, -3.402823466e38f), max_nan(c, -3.402823466e38f)), f2_pack(tau_inv_lo, tau_inv_lo),
                                    f2_fma(f2_pack(a, c), f2_pack(tau_inv, tau_inv), f2_pack(less, less)));
@@ -732,8 +734,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / T::kBytes);   // columns of the first vector before the row
     const int per = p.loops * kGradVecs * kThreads;
     const int64_t c0 = static_cast<int64_t>(part) * per * E - off, c_end = min(c0 + static_cast<int64_t>(per) * E, static_cast<int64_t>(p.V));
-    const float lse = p.lse[row];
-    const bool none = lse == -INFINITY;
+    const float less = p.less[row];
+    const bool none = less == -INFINITY;
 
     // ---- the first vectors on their way, then the given tokens: the sum of their gradients
     uint4 x[kGradVecs];
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += sm.red[w];
-    const GradColumn<ENT> f(p, lse, sum, ENT ? p.entropy[row] : 0.f, ENT ? p.grad_entropy[row] : 0.f);
+    const GradColumn<ENT> f(p, p.row_max ? p.row_max[row] : 0.f, less, sum, ENT ? p.entropy[row] : 0.f, ENT ? p.grad_entropy[row] : 0.f);
 
     for (int64_t first = c0; first < c_end; first += kGradVecs * kThreads * E) {
         if (first != c0) load(first);
@@ -922,7 +924,8 @@ lmloss_status check_grad(const lmloss_logprobs_grad_args* a)
     if (a->T > 0) {
         const uintptr_t z = reinterpret_cast<uintptr_t>(a->logits), g = reinterpret_cast<uintptr_t>(a->grad_out);
         const int es = float_bytes(a->dtype), id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
-        if (!z || !g || z % es || g % es || !a->lse) return LMLOSS_ERR_INVALID_ARG;
+        if (!z || !g || z % es || g % es || (!a->lse && !a->log_sum)) return LMLOSS_ERR_INVALID_ARG;
+        if ((a->row_max == nullptr) != (a->log_sum == nullptr)) return LMLOSS_ERR_INVALID_ARG;
         if (a->n > 0 && (!a->tokens || !a->grad_logp || reinterpret_cast<uintptr_t>(a->tokens) % id_bytes))
             return LMLOSS_ERR_INVALID_ARG;
         if (a->grad_entropy && !a->entropy) return LMLOSS_ERR_INVALID_ARG;
@@ -1011,6 +1014,8 @@ lmloss_status lmloss_logprobs_forward(lmloss_vocab_handle h, const lmloss_logpro
         p.entropy_out = a->entropy_out ? a->entropy_out + r0 : nullptr;
         p.top_logp_out = a->M ? a->top_logp_out + r0 * a->M : nullptr;
         p.top_tokens_out = a->M ? a->top_tokens_out + r0 * a->M : nullptr;
+        p.row_max_out = a->row_max_out ? a->row_max_out + r0 : nullptr;
+        p.log_sum_out = a->log_sum_out ? a->log_sum_out + r0 : nullptr;
         p.keys = reinterpret_cast<uint64_t*>(h->ws);
         p.stats = reinterpret_cast<float4*>(h->ws + P.stats);
         p.done = h->counters;
@@ -1060,7 +1065,8 @@ lmloss_status lmloss_logprobs_backward(lmloss_vocab_handle h, const lmloss_logpr
         p.ids32 = a->ids_dtype == LMLOSS_INT32;
         p.mask = a->token_mask ? a->token_mask + r0 * a->mask_stride : nullptr;
         p.mask_stride = a->mask_stride;
-        p.lse = a->lse + r0;
+        p.row_max = a->row_max ? a->row_max + r0 : nullptr;
+        p.less = (a->log_sum ? a->log_sum : a->lse) + r0;
         p.entropy = a->grad_entropy ? a->entropy + r0 : nullptr;
         p.grad_logp = a->n ? a->grad_logp + r0 * a->n : nullptr;
         p.grad_entropy = a->grad_entropy ? a->grad_entropy + r0 : nullptr;

@@ -87,6 +87,8 @@ class TokenLogprobs:
     entropy: Optional[torch.Tensor]             # [T] float32
     top_logp: Optional[torch.Tensor] = None     # [T, M] float32
     top_tokens: Optional[torch.Tensor] = None   # [T, M] int64
+    row_max: Optional[torch.Tensor] = None      # [T] float32: the largest allowed logit
+    log_sum: Optional[torch.Tensor] = None      # [T] float32: lse - row_max / temperature
 
 
 @dataclass
@@ -457,10 +459,11 @@ class VocabOps:
 
     def token_logprobs(self, logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, num_top: int = 0,
                        temperature: float = 1.0, token_mask: Optional[torch.Tensor] = None, entropy: bool = True,
-                       stream: Optional[torch.cuda.Stream] = None) -> TokenLogprobs:
+                       for_gradient: bool = False, stream: Optional[torch.cuda.Stream] = None) -> TokenLogprobs:
         """Log-probabilities of the given tokens [T, n] or [T] (int64 or int32, contiguous) under
         softmax(logits / temperature), logits [T, V] (bfloat16, float16 or float32, unit column
-        stride), with the rows' logsumexp and entropy and the num_top (0 to 64) largest
+        stride), with the rows' logsumexp and entropy, for_gradient its two parts that the gradient takes (row_max and
+        log_sum), and the num_top (0 to 64) largest
         log-probabilities with their tokens, equal ones by token.
 
         token_mask [T or 1, ceil(V / 32)] int32: bit v % 32 of word v / 32 allows token v; the softmax is
@@ -473,39 +476,47 @@ class VocabOps:
         ids, n = (_lib.LMLOSS_INT64, 0) if tokens is None else self._given(tokens, T)
         mask, mask_stride = (None, 0) if token_mask is None else self._mask(token_mask, T, V)
         if stream is None:
-            raw, r = _raw_stream(index), self._logprobs_out(tokens, T, num_top, entropy)
+            raw, r = _raw_stream(index), self._logprobs_out(tokens, T, num_top, entropy, for_gradient)
         else:
             raw, ctx = self._enter(stream, logits, tokens, token_mask)
             with ctx:
-                r = self._logprobs_out(tokens, T, num_top, entropy)
+                r = self._logprobs_out(tokens, T, num_top, entropy, for_gradient)
         a = _lib.lmloss_logprobs_args(logits.data_ptr(), T, V, ld, dtype, ids, tokens.data_ptr() if n else None, n,
                                       temperature, num_top, mask, mask_stride, r.logp.data_ptr() if n else None,
                                       r.lse.data_ptr(), r.entropy.data_ptr() if entropy else None,
                                       r.top_logp.data_ptr() if num_top else None,
                                       r.top_tokens.data_ptr() if num_top else None)
+        if for_gradient:
+            a.row_max_out, a.log_sum_out = r.row_max.data_ptr(), r.log_sum.data_ptr()
         st = self._logprobs(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise self._refused(st, "lmloss_logprobs_forward", a, _lib.lmloss_logprobs_check_args,
                                 _lib.lmloss_logprobs_workspace, self.scores_workspace_bytes)
         return r
 
-    def _logprobs_out(self, tokens, T, M, entropy):
+    def _logprobs_out(self, tokens, T, M, entropy, for_gradient):
         # (a tensor like another costs the host half of what one of a shape does)
         empty, like, dev, f32 = torch.empty, torch.empty_like, self.device, torch.float32
         lse = empty((T,), dtype=f32, device=dev)
         top = empty((T, M), dtype=f32, device=dev) if M else None
-        return TokenLogprobs(None if tokens is None else like(tokens, dtype=f32), lse, like(lse) if entropy else None,
-                             top, like(top, dtype=torch.int64) if M else None)
+        r = TokenLogprobs(None if tokens is None else like(tokens, dtype=f32), lse, like(lse) if entropy else None,
+                          top, like(top, dtype=torch.int64) if M else None)
+        if for_gradient:
+            r.row_max, r.log_sum = like(lse), like(lse)
+        return r
 
-    def token_logprobs_backward(self, logits: torch.Tensor, lse: torch.Tensor, tokens: Optional[torch.Tensor] = None,
-                                grad_logp: Optional[torch.Tensor] = None, *, entropy: Optional[torch.Tensor] = None,
+    def token_logprobs_backward(self, logits: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                                tokens: Optional[torch.Tensor] = None, grad_logp: Optional[torch.Tensor] = None, *,
+                                row_max: Optional[torch.Tensor] = None, log_sum: Optional[torch.Tensor] = None,
+                                entropy: Optional[torch.Tensor] = None,
                                 grad_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
                                 token_mask: Optional[torch.Tensor] = None,
                                 grad: Union[None, str, torch.Tensor] = None,
                                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """The logits' gradient [T, V], in their type, from grad_logp (of the tokens' shape, float32, at most
-        1024 tokens a row) and grad_entropy [T]: with the forward call's logits, lse, entropy, temperature and mask.
-        Gradients of alternatives: give their tokens.  grad: a tensor to write, "inplace" (over the logits), or
+        1024 tokens a row) and grad_entropy [T]: with the forward call's logits, row_max and log_sum (or lse), entropy,
+        temperature and mask.  lse is not looked at beside row_max and log_sum; alone it leaves the probabilities off by
+        a factor of e to 2^-24 of itself (1e-3 at an lse of 15000, as low temperatures have).  Gradients of alternatives: give their tokens.  grad: a tensor to write, "inplace" (over the logits), or
         None for a new one.  Columns that are not allowed, and rows in which nothing is, get 0."""
         index = self._index
         dtype, T, V, ld = _matrix(logits, "logits", index)
@@ -514,7 +525,11 @@ class VocabOps:
         ids, n = (_lib.LMLOSS_INT64, 0) if tokens is None else self._given(tokens, T)
         if n > _lib.LMLOSS_MAX_GIVEN:
             raise ValueError(f"tokens: at most {_lib.LMLOSS_MAX_GIVEN} a row, got {n}")
-        vectors = [("lse", lse, (T,))]
+        if (row_max is None) != (log_sum is None):
+            raise ValueError("row_max and log_sum: both or neither")
+        if lse is None and log_sum is None:
+            raise ValueError("the forward call's row_max and log_sum, or its lse, are needed")
+        vectors = [("lse", lse, (T,))] if log_sum is None else [("row_max", row_max, (T,)), ("log_sum", log_sum, (T,))]
         if tokens is not None:
             vectors.append(("grad_logp", grad_logp, tuple(tokens.shape)))
         if grad_entropy is not None:
@@ -532,7 +547,7 @@ class VocabOps:
         if stream is None:
             raw, ctx = _raw_stream(index), contextlib.nullcontext()
         else:
-            raw, ctx = self._enter(stream, logits, lse, tokens, grad_logp, entropy, grad_entropy, token_mask,
+            raw, ctx = self._enter(stream, logits, lse, row_max, log_sum, tokens, grad_logp, entropy, grad_entropy, token_mask,
                                    grad if isinstance(grad, torch.Tensor) else None)
         if grad is None:
             with ctx:
@@ -545,11 +560,12 @@ class VocabOps:
         if g_type != dtype or rows != T or cols != V:
             raise ValueError(f"grad: expected [{T}, {V}] of {logits.dtype}")
         a = _lib.lmloss_logprobs_grad_args(logits.data_ptr(), T, V, ld, dtype, ids, tokens.data_ptr() if n else None, n,
-                                           temperature, mask, mask_stride, lse.data_ptr(),
+                                           temperature, mask, mask_stride, None if lse is None else lse.data_ptr(),
                                            grad_logp.data_ptr() if n else None,
                                            None if grad_entropy is None else entropy.data_ptr(),
                                            None if grad_entropy is None else grad_entropy.data_ptr(),
-                                           grad.data_ptr(), ld_grad)
+                                           grad.data_ptr(), ld_grad, None if log_sum is None else row_max.data_ptr(),
+                                           None if log_sum is None else log_sum.data_ptr())
         st = self._logprobs_grad(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
             raise LMLossError(st, "lmloss_logprobs_backward")
