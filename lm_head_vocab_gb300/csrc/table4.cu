@@ -39,15 +39,16 @@ constexpr int kDeep = 4;
 struct Spread {
     int log_across;
     int blocks_across;           // blocks along a row
-    int64_t blocks_down;
-    Spread(int64_t vectors, int64_t rows)
+    int64_t down;                // rows of a block
+    explicit Spread(int64_t vectors)   // at least one
     {
         log_across = 4;          // a group's threads are neighbours
         while (log_across < 8 && (int64_t(1) << log_across) < vectors) ++log_across;
         blocks_across = static_cast<int>((vectors + (int64_t(1) << log_across) - 1) >> log_across);
-        const int64_t down = kDeep << (8 - log_across);
-        blocks_down = (rows + down - 1) / down;
+        down = kDeep << (8 - log_across);
     }
+    // rows of a launch: whole blocks within the grid's limit
+    int64_t most() const { return ((int64_t(1) << 31) - 1) / blocks_across * down; }
 };
 
 // max and min that keep a NaN
@@ -534,9 +535,8 @@ lmloss_status lmloss_table4_quantize(lmloss_vocab_handle h, const lmloss_table4_
     if (st != LMLOSS_OK) return st;
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
-    const Spread all((a->table.D + a->table.group - 1) / a->table.group * (a->table.group / 8), a->table.V);
-    // whole blocks of rows a launch, within the grid's limit
-    const int64_t down = kDeep << (8 - all.log_across), most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
+    const Spread all((a->table.D + a->table.group - 1) / a->table.group * (a->table.group / 8));
+    const int64_t most = all.most();
     for (int64_t v0 = 0; v0 < a->table.V; v0 += most) {
         QuantizeParams p{};
         p.t = table4_params(a->table);
@@ -551,7 +551,7 @@ lmloss_status lmloss_table4_quantize(lmloss_vocab_handle h, const lmloss_table4_
         p.log_across = all.log_across;
         p.blocks_across = all.blocks_across;
         p.err = h->err;
-        const unsigned grid = static_cast<unsigned>(all.blocks_across * ((p.rows + down - 1) / down));
+        const unsigned grid = static_cast<unsigned>(all.blocks_across * ((p.rows + all.down - 1) / all.down));
         by_type(a->weight_dtype, [&](auto w) {
             by_type(a->table.scale_dtype, [&](auto s) {
                 if (p.t.zeros) quantize_kernel<decltype(w), decltype(s), true><<<grid, 256, 0, stream>>>(p);
@@ -575,14 +575,13 @@ lmloss_status lmloss_table4_lookup(lmloss_vocab_handle h, const lmloss_table4_lo
     const int E = 16 / float_bytes(a->rows_dtype);
     // (of fp32, 16 columns at a time: they lie in one group)
     const bool words = a->table.D % 8 == 0 && (a->table.D % 16 == 0 || E == 8) && aligned16(a->rows) && a->ld_rows % E == 0;
-    Spread all(a->table.D / 8, a->T);
-    int64_t down = kDeep << (8 - all.log_across), most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
+    Spread all((a->table.D + 7) / 8);
     if (!words) {
         // warps: 31 words each, and one behind the last for what shifts out of it
         all.blocks_across = static_cast<int>(((a->table.D + 7) / 8 + 1 + 30) / 31);
-        down = kDeep;
-        most = ((int64_t(1) << 31) - 1) / all.blocks_across * down;
+        all.down = kDeep;
     }
+    const int64_t most = all.most();
     for (int64_t t0 = 0; t0 < a->T; t0 += most) {
         LookupParams p{};
         p.t = table4_params(a->table);
@@ -595,7 +594,7 @@ lmloss_status lmloss_table4_lookup(lmloss_vocab_handle h, const lmloss_table4_lo
         p.log_across = all.log_across;
         p.blocks_across = all.blocks_across;
         p.err = h->err;
-        const int64_t pieces = all.blocks_across * ((p.T + down - 1) / down);   // blocks, or warps
+        const int64_t pieces = all.blocks_across * ((p.T + all.down - 1) / all.down);   // blocks, or warps
         const unsigned grid = static_cast<unsigned>(words ? pieces : (pieces + 7) / 8);
         by_type(a->rows_dtype, [&](auto r) {
             by_type(a->table.scale_dtype, [&](auto s) {
