@@ -663,7 +663,8 @@ lmloss_status lmloss_table4_check_lookup_args(const lmloss_table4_lookup_args* a
 lmloss_status lmloss_table4_check_logits_args(const lmloss_table4_logits_args* args);
 
 /* The workspace that lmloss_table4_logits needs for `args` (pointers are not looked at)
- * and for any call of no more rows and columns, whatever its types. */
+ * and for any call of no more rows and columns, whatever its types.  (Calls of up to 8 rows, 4
+ * where hidden values or logits are fp32, need none up to 6144 columns, and some beyond.) */
 lmloss_status lmloss_table4_logits_workspace(const lmloss_table4_logits_args* args, size_t* bytes);
 
 /*

@@ -613,7 +613,6 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
     if (a->T == 0) return LMLOSS_OK;
     const bool pairs = a->hidden_dtype == LMLOSS_FP32;
     const HiddenSpace w = hidden_space(a->T, a->table.D, pairs);
-    if (w.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
     VocabDeviceGuard g(h->device);
     if (!g.ok) return LMLOSS_ERR_CUDA;
     for (int64_t t0 = 0; t0 < a->T; t0 += kMaxRows) {
@@ -646,7 +645,11 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         // (fp32 logits of few rows are of pairs whatever the rows' type: their table's numbers are subnormal)
         p.pairs = pairs || a->logits_dtype == LMLOSS_FP32;
         const bool few = few_rows_fit(p);
-        if (!few) p.pairs = pairs;
+        if (!few) {
+            // (a first launch that is not of few rows is the call's: nothing has been launched yet)
+            if (w.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
+            p.pairs = pairs;
+        }
         const int rows = few ? kFewTile : kRows;
         p.vtiles = static_cast<int>((a->table.V + rows - 1) / rows);
         TableMaps maps{};
