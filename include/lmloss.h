@@ -329,6 +329,11 @@ typedef struct lmloss_vocab_ctx* lmloss_vocab_handle;
  * 4-bit tables, which need none). */
 lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_t workspace_bytes);
 
+/* At least `workspace_bytes` of workspace for the calls that follow.  Allocates where the handle has
+ * less; what it had lives as long as the handle, so that graphs captured with it can be replayed.
+ * Allowed while a stream is captured, and not part of the graph. */
+lmloss_status lmloss_vocab_reserve(lmloss_vocab_handle handle, size_t workspace_bytes);
+
 /* Free the handle and its workspace.  Synchronises the handle's device. */
 lmloss_status lmloss_vocab_destroy(lmloss_vocab_handle handle);
 

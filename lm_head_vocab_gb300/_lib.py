@@ -322,6 +322,7 @@ def load() -> ctypes.CDLL:
                                 ctypes.c_void_p], st),
         "lmloss_shard_grad": ([h, ctypes.POINTER(lmloss_args), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p], st),
         "lmloss_vocab_create": ([ctypes.POINTER(h), ctypes.c_int, ctypes.c_size_t], st),
+        "lmloss_vocab_reserve": ([h, ctypes.c_size_t], st),
         "lmloss_vocab_destroy": ([h], st),
         "lmloss_vocab_get_device_error": ([h], st),
         "lmloss_embedding_check_args": ([ctypes.POINTER(lmloss_embedding_args)], st),
@@ -460,6 +461,10 @@ def lmloss_vocab_create(device: int, workspace_bytes: int) -> ctypes.c_void_p:
     if st != LMLOSS_OK:
         raise LMLossError(st, "lmloss_vocab_create")
     return h
+
+
+def lmloss_vocab_reserve(handle, workspace_bytes: int) -> int:
+    return load().lmloss_vocab_reserve(handle, workspace_bytes)
 
 
 def lmloss_vocab_destroy(handle) -> int:

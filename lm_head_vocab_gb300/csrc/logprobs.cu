@@ -986,12 +986,15 @@ lmloss_status lmloss_logprobs_forward(lmloss_vocab_handle h, const lmloss_logpro
     if (!g.ok) return LMLOSS_ERR_CUDA;
     const int es = float_bytes(a->dtype), id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
     const bool aligned = aligned16(a->logits) && a->ld * es % 16 == 0;
-    // as many rows a launch as there are counters
+    // as many rows a launch as there are counters; whether the workspace serves all of them is known before the first
+    lmloss_logprobs_args part = *a;
+    for (int64_t rows : {std::min<int64_t>(a->T, kMaxRowsALaunch), (a->T - 1) % kMaxRowsALaunch + 1}) {
+        part.T = rows;
+        if (plan_logprobs(&part, h->num_sms).total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
+    }
     for (int64_t r0 = 0; r0 < a->T; r0 += kMaxRowsALaunch) {
-        lmloss_logprobs_args part = *a;
         part.T = std::min<int64_t>(a->T - r0, kMaxRowsALaunch);
         const LogprobsPlan P = plan_logprobs(&part, h->num_sms);
-        if (P.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
         LogprobsParams p{};
         p.logits = static_cast<const unsigned char*>(a->logits) + r0 * a->ld * es;
         p.ld = a->ld;

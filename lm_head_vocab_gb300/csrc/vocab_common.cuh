@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <vector>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,6 +24,7 @@ struct lmloss_vocab_ctx {
     unsigned* counters = nullptr;    // [kVocabCounters]
     unsigned char* ws = nullptr;     // [ws_bytes]
     size_t ws_bytes = 0;
+    std::vector<unsigned char*> more;   // workspaces of lmloss_vocab_reserve
     uint32_t limits_raised = 0;      // sorting kernels whose launch limits were raised
 };
 

@@ -43,14 +43,45 @@ lmloss_status lmloss_vocab_create(lmloss_vocab_handle* handle, int device, size_
     return LMLOSS_OK;
 }
 
+lmloss_status lmloss_vocab_reserve(lmloss_vocab_handle h, size_t workspace_bytes)
+{
+    if (!h || workspace_bytes > SIZE_MAX / 2) return LMLOSS_ERR_INVALID_ARG;
+    if (workspace_bytes <= h->ws_bytes) return LMLOSS_OK;
+    VocabDeviceGuard g(h->device);
+    if (!g.ok) return LMLOSS_ERR_CUDA;
+    const size_t bytes = vocab_align(workspace_bytes);
+    // a capture forbids allocations unless the thread says that it knows about them
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) {
+        cudaGetLastError();
+        return LMLOSS_ERR_CUDA;
+    }
+    unsigned char* ws = nullptr;
+    const bool there = cudaMalloc(&ws, bytes) == cudaSuccess;
+    if (!there) cudaGetLastError();
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!there) return LMLOSS_ERR_CUDA;
+    try {
+        h->more.push_back(ws);
+    } catch (...) {
+        cudaFree(ws);
+        return LMLOSS_ERR_CUDA;
+    }
+    // (what a workspace holds when a call begins is of no matter: the counters lie apart from it)
+    h->ws = ws;
+    h->ws_bytes = bytes;
+    return LMLOSS_OK;
+}
+
 lmloss_status lmloss_vocab_destroy(lmloss_vocab_handle h)
 {
     if (!h) return LMLOSS_ERR_INVALID_ARG;
     VocabDeviceGuard g(h->device);
     cudaDeviceSynchronize();
-    const cudaError_t e = cudaFree(h->mem);
+    bool freed = cudaFree(h->mem) == cudaSuccess;
+    for (unsigned char* ws : h->more) freed &= cudaFree(ws) == cudaSuccess;
     delete h;
-    return e == cudaSuccess ? LMLOSS_OK : LMLOSS_ERR_CUDA;
+    return freed ? LMLOSS_OK : LMLOSS_ERR_CUDA;
 }
 
 lmloss_status lmloss_vocab_get_device_error(lmloss_vocab_handle h)

@@ -105,9 +105,10 @@ class Table4:
 
 class VocabOps:
     """One handle of the vocabulary operators, with workspace for embedding
-    gradients of up to max_tokens positions and max_dim columns, for beam steps and
-    log-probabilities of up to max_rows rows of logits at vocabularies of up to max_vocab,
-    and for logits from 4-bit tables of up to max_rows rows and max_dim columns.
+    gradients of up to max_tokens positions and max_dim columns, for beam steps of
+    up to max_rows rows of logits at vocabularies of up to max_vocab and, allocated
+    by the first call that needs it, for log-probabilities of the same and for logits from
+    4-bit tables of up to max_rows rows and max_dim columns.
 
     Calls run on `stream`, or on the current stream, and do not synchronise; calls
     on one handle must not overlap.  A `stream` other than the current one has to
@@ -142,17 +143,19 @@ class VocabOps:
         self.workspace_bytes = need
         self.handle = _lib.lmloss_vocab_create(device, need)
         # Log-probabilities and 4-bit tables have a handle of their own, so that what the other operators
-        # accept goes by their maxima alone.
-        need = 0
+        # accept goes by their maxima alone; and a workspace from the first call on that needs one, so that
+        # who never makes such a call pays nothing for it.  Of maxima past what those calls take, what they take.
+        self.logprobs_workspace_bytes = self.scores_workspace_bytes = 0
         if max_rows > 0:
-            c = _lib.lmloss_logprobs_args(T=max_rows, V=max_vocab, ld=max_vocab, M=_lib.LMLOSS_MAX_ALTERNATIVES,
+            V, D = min(max_vocab, (1 << 31) - (1 << 16)), min(max(max_dim, 1), 1 << 20)
+            c = _lib.lmloss_logprobs_args(T=min(max_rows, (1 << 30) - 1), V=V, ld=V, M=_lib.LMLOSS_MAX_ALTERNATIVES,
                                           temperature=1.0)
-            need = _lib.lmloss_logprobs_workspace(c)
-            d = _lib.lmloss_table4_logits_args(T=max_rows)
-            d.table.V, d.table.D, d.table.group = max_vocab, max(max_dim, 1), 32
-            need = max(need, _lib.lmloss_table4_logits_workspace(d))
-        self.scores_workspace_bytes = need
-        self.scores_handle = _lib.lmloss_vocab_create(device, need)
+            self.logprobs_workspace_bytes = _lib.lmloss_logprobs_workspace(c)
+            d = _lib.lmloss_table4_logits_args(T=min(max_rows, (1 << 24) - 1))
+            d.table.V, d.table.D, d.table.group = V, D, 32
+            self.scores_workspace_bytes = max(self.logprobs_workspace_bytes, _lib.lmloss_table4_logits_workspace(d))
+        self.scores_handle = _lib.lmloss_vocab_create(device, 0)
+        self._reserved = 0
 
     def close(self):
         for name in ("handle", "scores_handle"):
@@ -180,6 +183,18 @@ class VocabOps:
                 where += (f" ({need} bytes of workspace needed, {there} there: the handle's max_tokens, "
                           f"max_dim, max_rows or max_vocab is too small)")
         return LMLossError(status, where)
+
+    def _with_workspace(self, status, call, args, raw, where, check, workspace, bytes_):
+        """A log-probability's or a 4-bit table's call that was refused, again with the operator's workspace of
+        `bytes_` if it is the first that needs it; else its error."""
+        if self._reserved < bytes_ and status == _lib.LMLOSS_ERR_INVALID_ARG and check(args) == _lib.LMLOSS_OK:
+            status = _lib.lmloss_vocab_reserve(self.scores_handle, bytes_)
+            if status != _lib.LMLOSS_OK:
+                raise LMLossError(status, f"{where} ({bytes_} bytes of workspace)")
+            self._reserved = bytes_
+            status = call(self.scores_handle, args, raw)
+        if status != _lib.LMLOSS_OK:
+            raise self._refused(status, where, args, check, workspace, self._reserved)
 
     # ------------------------------------------------------------- streams
     def _enter(self, stream, *tensors):
@@ -490,8 +505,8 @@ class VocabOps:
             a.row_max_out, a.log_sum_out = r.row_max.data_ptr(), r.log_sum.data_ptr()
         st = self._logprobs(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
-            raise self._refused(st, "lmloss_logprobs_forward", a, _lib.lmloss_logprobs_check_args,
-                                _lib.lmloss_logprobs_workspace, self.scores_workspace_bytes)
+            self._with_workspace(st, self._logprobs, a, raw, "lmloss_logprobs_forward", _lib.lmloss_logprobs_check_args,
+                                 _lib.lmloss_logprobs_workspace, self.logprobs_workspace_bytes)
         return r
 
     def _logprobs_out(self, tokens, T, M, entropy, for_gradient):
@@ -714,6 +729,6 @@ class VocabOps:
         a = _lib.lmloss_table4_logits_args(t, rows.data_ptr(), T, ld, out.data_ptr(), ld_out, x_type, o_type, scale)
         st = self._logits4(self.scores_handle, a, raw)
         if st != _lib.LMLOSS_OK:
-            raise self._refused(st, "lmloss_table4_logits", a, _lib.lmloss_table4_check_logits_args,
-                                _lib.lmloss_table4_logits_workspace, self.scores_workspace_bytes)
+            self._with_workspace(st, self._logits4, a, raw, "lmloss_table4_logits", _lib.lmloss_table4_check_logits_args,
+                                 _lib.lmloss_table4_logits_workspace, self.scores_workspace_bytes)
         return out
