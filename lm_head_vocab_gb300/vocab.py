@@ -170,9 +170,10 @@ class VocabOps:
             pass
 
     def device_error(self) -> int:
-        """Read and clear the handle's error word (synchronises the device)."""
-        first, second = (_lib.lmloss_vocab_get_device_error(h) for h in (self.handle, self.scores_handle))
-        return first or second
+        """Read and clear an error of the calls so far, 0 if there is none (synchronises the device).  The embedding's and
+        the beams' calls keep one, log-probabilities and 4-bit tables another: with both there, the second is read by
+        the next call."""
+        return _lib.lmloss_vocab_get_device_error(self.handle) or _lib.lmloss_vocab_get_device_error(self.scores_handle)
 
     def _refused(self, status, where, args, check, workspace, there=None):
         """The error for a refused call: where the arguments are in order, what the workspace lacks."""
