@@ -677,7 +677,8 @@ lmloss_status lmloss_table4_logits_workspace(const lmloss_table4_logits_args* ar
  * prompt's.  Within a group the products with the whole numbers q - z are summed, and the sum
  * is scaled by the group's scale: no weight is rounded.  Sums in fp32, one rounding at the end.
  * fp32 hidden values count with an error of at most 2^-23 of the largest in their group of
- * columns, 16-bit ones of at most 2^-35 of the largest in their row.  A row with an
+ * columns plus 2^-46 of the largest in their row (two fp16 hold one: beside a column 2^11 times as
+ * large a value keeps 11 bits), 16-bit ones of at most 2^-35 of the largest in their row.  A row with an
  * infinity or NaN gives what the formula gives, slowly, and does not disturb the others.  A
  * row's logits depend on that row, its index, the table and T alone.  `logits` overlaps neither
  * `hidden` nor the table.  A wait inside that expires sets LMLOSS_ERR_TIMEOUT; the logits mean nothing then.

@@ -4,7 +4,7 @@
 //
 // The whole numbers q - z are exact in fp16, and so is a hidden row in fp16 once a power of two brings its
 // largest value to 2^14 (bf16 and fp16: what underflows is below 2^-35 of that; fp32 as a pair of fp16,
-// within 2^-23).  So the tensor cores sum exact products within a group, in fp32, and a group's sum is scaled
+// within 2^-23 of the largest of a group of columns and 2^-46 of the row's).  So the tensor cores sum exact products within a group, in fp32, and a group's sum is scaled
 // by s and added to the others in fp32 registers: no weight is rounded.
 //
 // Up to 8 operand rows go to a kernel of independent warps (table4_rows.cu); a pair counts as two.  For more a first

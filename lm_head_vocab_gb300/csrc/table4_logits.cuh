@@ -121,6 +121,10 @@ __device__ __forceinline__ void load_part(const typename X::raw* x, int c, int D
 // group, 2^11 of which reach its largest: then a group's sum of products, below 15 * 2^11 * 128 < 2^22 steps, is exact.
 // The tensor cores cut their sums off, one way, at some 2^-24 of the largest term: with hi rounded by each value's own
 // exponent logits of 1001 columns were up to 2e-6 off, ten times as far as sums in fp32.
+// What is left out: lo has 11 bits of a rest below 2^-11 of the power of two at or below the group's largest, 2^-23 of
+// that largest, down to half a subnormal's step, 2^-36 (2^-32 in the places divided by 16), or hi's least step's:
+// 2^-46 of the row's largest.  A third part would hold the rest, for half as many operand rows again; where one
+// column is thousands of times the others only logits that it does not enter (q = z there) show the difference.
 template <class X, bool PAIR>
 __device__ __forceinline__ void hidden_part(const Pack<X, 8>& v, float scale, float group_top, uint4& hi, uint4& lo, float& sum, float& sum_lo)
 {
