@@ -934,7 +934,11 @@ lmloss_status check_grad(const lmloss_logprobs_grad_args* a)
         } else {
             const uintptr_t z_end = z + static_cast<uintptr_t>(((a->T - 1) * a->ld + a->V) * es);
             const uintptr_t g_end = g + static_cast<uintptr_t>(((a->T - 1) * a->ld_grad + a->V) * es);
-            if (z < g_end && g < z_end) return LMLOSS_ERR_INVALID_ARG;
+            // (side by side in the rows of one tensor they do not meet either)
+            const uintptr_t row = static_cast<uintptr_t>(a->ld) * es, cols = static_cast<uintptr_t>(a->V) * es;
+            const uintptr_t apart = z < g ? (g - z) % row : (row - (z - g) % row) % row;
+            const bool beside = a->ld == a->ld_grad && apart >= cols && row - apart >= cols;
+            if (z < g_end && g < z_end && !beside) return LMLOSS_ERR_INVALID_ARG;
         }
     }
     return LMLOSS_OK;

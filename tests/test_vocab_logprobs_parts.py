@@ -34,3 +34,31 @@ def test_they_are_made_on_request(ops, monkeypatch):  # noqa: F811
     assert r.row_max is None and r.log_sum is None and seen == [(None, None)]
     r = ops.token_logprobs(torch.zeros(3, 40), for_gradient=True)
     assert seen[1] == (r.row_max.data_ptr(), r.log_sum.data_ptr()) and r.row_max.shape == r.log_sum.shape == (3,)
+
+
+# rows of 2-byte logits 208 elements apart, 100 used
+@pytest.mark.parametrize("columns,expect", [
+    (100, OK), (104, OK), (108, OK), (99, BAD), (109, BAD), (1, BAD), (208, BAD), (416, BAD), (208 + 100, OK), (208 + 108, OK),
+    (208 + 99, BAD), (-100, OK), (-108, OK), (-99, BAD), (-109, BAD), (-208 - 104, OK), (3 * 208, OK), (-3 * 208, OK),
+])
+def test_gradient_beside_the_logits(lib, columns, expect):  # noqa: F811
+    assert L.lmloss_logprobs_check_grad_args(_grad(logits=0x10000, ld=208, ld_grad=208, grad_out=0x10000 + 2 * columns)) == expect
+    if abs(columns) < 2 * 208:
+        assert L.lmloss_logprobs_check_grad_args(_grad(logits=0x10000, ld=208, ld_grad=200, grad_out=0x10000 + 2 * columns)) == BAD
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,V,wide", [(torch.bfloat16, 3001, 6002), (torch.bfloat16, 3000, 6008), (torch.float32, 1000, 2001)])
+def test_halves_of_one_tensor(dtype, V, wide):
+    import __graft_entry__
+    __graft_entry__.build()
+    h = VocabOps(0, max_tokens=0, max_rows=64)
+    both = torch.randn(9, wide, device="cuda").to(dtype)
+    z, d = both[:, :V], both[:, wide - V:]
+    tokens, g = torch.randint(0, V, (9, 3), device="cuda"), torch.randn(9, 3, device="cuda")
+    r = h.token_logprobs(z, tokens, for_gradient=True)
+    alone = z.clone()
+    want = h.token_logprobs_backward(alone, None, tokens, g, row_max=r.row_max, log_sum=r.log_sum)
+    h.token_logprobs_backward(z, None, tokens, g, row_max=r.row_max, log_sum=r.log_sum, grad=d)
+    assert torch.equal(d, want) and torch.equal(z, alone)
+    h.close()
