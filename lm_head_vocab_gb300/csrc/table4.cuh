@@ -32,10 +32,6 @@ inline Table4 table4_params(const lmloss_table4& t)
     p.shift = t.group == 32 ? 5 : (t.group == 64 ? 6 : 7);
     return p;
 }
-__device__ __forceinline__ float table4_zero(const Table4& t, int g, int64_t v)
-{
-    return t.zeros ? static_cast<float>(t.zeros[g * t.ld_zeros + v]) : 8.f;
-}
 
 }  // namespace
 

@@ -114,10 +114,11 @@ __device__ __noinline__ void lay_out(const LogitsParams& p, RowsHead& head, unsi
     asm volatile("bar.sync 9, %0;" ::"n"(kSumThreads) : "memory");
 }
 
-template <int NT, int GROUP>
+template <int GROUP>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ TableMaps maps)
 {
-    constexpr int N = 8 * NT;
+    constexpr int N = kFewRows;
+    static_assert(N == 8, "columns of one mma.sync");
     constexpr int kPerStage = kFewCols / GROUP, kUnits = GROUP / 32;   // groups of a stage; runs of 32 columns of a group
     extern __shared__ __align__(1024) unsigned char smem[];
     RowsHead& b = *reinterpret_cast<RowsHead*>(smem);
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         const unsigned char* const x_odd = x_even - 2 * odd;
         Ring q;
         for (int tile = blockIdx.x; tile < p.vtiles; tile += gridDim.x) {
-            float acc[2][NT][4] = {};
+            float acc[2][4] = {};
             for (int st = 0; st < stages; ++st) {
                 wait_one(b.full[q.slot], q.parity);
                 __syncwarp();
@@ -197,12 +198,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                         for (int mt = 0; mt < 2; ++mt) ldmatrix4(w[u2][mt], words + offset + mt * 16 * 128 + part_at[u2]);
                     const int x_at = kb * (N * 256);
                     const int g0 = block * (kBlockCols / GROUP);   // the block's first group in the stage
-                    float d[2][NT][4];
+                    float d[2][4];
 #pragma unroll
                     for (int unit = 0; unit < 4; ++unit) {   // 32 columns
                         if (unit % kUnits == 0) {
 #pragma unroll
-                            for (int i = 0; i < 2 * NT * 4; ++i) d[i / (NT * 4)][i / 4 % NT][i % 4] = 0.f;
+                            for (int i = 0; i < 8; ++i) d[i / 4][i % 4] = 0.f;
                         }
                         uint32_t a[2][2][4];
 #pragma unroll
@@ -210,14 +211,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                             widen_word(w[unit >> 1][mt][2 * (unit & 1)], a[mt][0]);
                             widen_word(w[unit >> 1][mt][2 * (unit & 1) + 1], a[mt][1]);
                         }
+                        const uint4 x = *reinterpret_cast<const uint4*>((unit & 1 ? x_odd : x_even) + x_at + unit * 64);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint4 x = *reinterpret_cast<const uint4*>((unit & 1 ? x_odd : x_even) + x_at + nt * 8 * 256 + unit * 64);
-#pragma unroll
-                            for (int mt = 0; mt < 2; ++mt) {
-                                mma_m16n8k16(d[mt][nt], a[mt][0][0], a[mt][1][0], a[mt][0][1], a[mt][1][1], x.x, x.y);
-                                mma_m16n8k16(d[mt][nt], a[mt][0][2], a[mt][1][2], a[mt][0][3], a[mt][1][3], x.z, x.w);
-                            }
+                        for (int mt = 0; mt < 2; ++mt) {
+                            mma_m16n8k16(d[mt], a[mt][0][0], a[mt][1][0], a[mt][0][1], a[mt][1][1], x.x, x.y);
+                            mma_m16n8k16(d[mt], a[mt][0][2], a[mt][1][2], a[mt][0][3], a[mt][1][3], x.z, x.w);
                         }
                         // ---- a group's end: its sums, less the zero points', scaled
                         const int gl = g0 + unit / kUnits;
@@ -236,18 +234,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                             }
 #pragma unroll
                             for (int k = 0; k < 4; ++k) z[k] = p.zeros ? -static_cast<float>((stage + lay.zeros)[at + 8 * k]) : -8.f;
-                            const float* const sums = all_sums + (st * kPerStage + gl) * N + 2 * i4;
+                            const float2 sums = *reinterpret_cast<const float2*>(all_sums + (st * kPerStage + gl) * N + 2 * i4);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const float2 x = *reinterpret_cast<const float2*>(sums + nt * 8);
+                            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const int r = 2 * mt + (k >> 1);
-                                        acc[mt][nt][k] = fmaf(s[r], fmaf(z[r], k & 1 ? x.y : x.x, d[mt][nt][k]), acc[mt][nt][k]);
-                                    }
-                            }
+                                for (int k = 0; k < 4; ++k) {
+                                    const int r = 2 * mt + (k >> 1);
+                                    acc[mt][k] = fmaf(s[r], fmaf(z[r], k & 1 ? sums.y : sums.x, d[mt][k]), acc[mt][k]);
+                                }
                         }
                     }
                 }
@@ -260,11 +254,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             float* const here = pads + turn * other_pads;
             turn ^= 1;
 #pragma unroll
-            for (int i = 0; i < 2 * NT * 4; ++i) {
-                const int mt = i / (NT * 4), nt = i / 4 % NT, k = i % 4, n = nt * 8 + 2 * i4 + (k & 1);
+            for (int i = 0; i < 8; ++i) {
+                const int mt = i / 4, k = i % 4, n = 2 * i4 + (k & 1);
                 // the place of a pair's lower part: behind all upper ones
                 const int slot = p.pairs && n >= N / 2 ? n - N / 2 + p.T : n;
-                if (p.pairs ? n % (N / 2) < p.T : n < p.T) here[(block * used + slot) * 33 + mt * 16 + (k >> 1) * 8 + g8] = acc[mt][nt][k];
+                if (p.pairs ? n % (N / 2) < p.T : n < p.T) here[(block * used + slot) * 33 + mt * 16 + (k >> 1) * 8 + g8] = acc[mt][k];
             }
             asm volatile("bar.sync %0, 256;" ::"r"(team + 1) : "memory");
             const int64_t v = static_cast<int64_t>(tile) * kFewTile + r0 + lane;
@@ -294,16 +288,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     __syncthreads();
 }
 
-
-
-template <int NT, int GROUP>
+template <int GROUP>
 lmloss_status launch(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
     const StageLayout lay(kFewTile, kFewCols, p.shift, p.scale_bytes, p.zeros != nullptr);
-    const RowsLayout rl(8 * NT, p.pairs ? 2 * p.T : p.T, p.kblocks, p.groups);
+    const RowsLayout rl(kFewRows, p.pairs ? 2 * p.T : p.T, p.kblocks, p.groups);
     p.stage_bytes = lay.bytes;
     p.qstages = std::min<int>(kMaxStages, (kMaxShared - kHead - rl.bytes) / lay.bytes);
-    auto* fn = rows_kernel<NT, GROUP>;
+    auto* fn = rows_kernel<GROUP>;
     constexpr uint32_t bit = 1u << (8 + (GROUP == 32 ? 0 : (GROUP == 64 ? 1 : 2)));
     if (!(h->limits_raised & bit)) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess) {
@@ -330,9 +322,9 @@ bool few_rows_fit(const LogitsParams& p)
 lmloss_status launch_few_rows(LogitsParams& p, const TableMaps& maps, lmloss_vocab_ctx* h, cudaStream_t stream)
 {
     p.N = kFewRows;
-    if (p.shift == 5) return launch<kFewRows / 8, 32>(p, maps, h, stream);
-    if (p.shift == 6) return launch<kFewRows / 8, 64>(p, maps, h, stream);
-    return launch<kFewRows / 8, 128>(p, maps, h, stream);
+    if (p.shift == 5) return launch<32>(p, maps, h, stream);
+    if (p.shift == 6) return launch<64>(p, maps, h, stream);
+    return launch<128>(p, maps, h, stream);
 }
 
 }  // namespace lmloss
