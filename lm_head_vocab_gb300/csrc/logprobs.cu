@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / T::kBytes);   // columns of the first vector before the row
     const int per = p.loops * kGradVecs * kThreads;
     const int64_t c0 = static_cast<int64_t>(part) * per * E - off, c_end = min(c0 + static_cast<int64_t>(per) * E, static_cast<int64_t>(p.V));
-    const float less = p.less[row];
+    const float less = p.less[row], row_max = p.row_max ? p.row_max[row] : 0.f;
     const bool none = less == -INFINITY;
 
     // ---- the first vectors on their way, then the given tokens: the sum of their gradients
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(const __grid_co
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += sm.red[w];
-    const GradColumn<ENT> f(p, p.row_max ? p.row_max[row] : 0.f, less, sum, ENT ? p.entropy[row] : 0.f, ENT ? p.grad_entropy[row] : 0.f);
+    const GradColumn<ENT> f(p, row_max, less, sum, ENT ? p.entropy[row] : 0.f, ENT ? p.grad_entropy[row] : 0.f);
 
     for (int64_t first = c0; first < c_end; first += kGradVecs * kThreads * E) {
         if (first != c0) load(first);
@@ -990,15 +990,17 @@ lmloss_status lmloss_logprobs_forward(lmloss_vocab_handle h, const lmloss_logpro
     if (!g.ok) return LMLOSS_ERR_CUDA;
     const int es = float_bytes(a->dtype), id_bytes = a->ids_dtype == LMLOSS_INT64 ? 8 : 4;
     const bool aligned = aligned16(a->logits) && a->ld * es % 16 == 0;
-    // as many rows a launch as there are counters; whether the workspace serves all of them is known before the first
+    // as many rows a launch as there are counters: whole rows, which need no workspace, but for the last launch's, which
+    // are looked at before the first
     lmloss_logprobs_args part = *a;
-    for (int64_t rows : {std::min<int64_t>(a->T, kMaxRowsALaunch), (a->T - 1) % kMaxRowsALaunch + 1}) {
-        part.T = rows;
+    if (a->T > kMaxRowsALaunch) {
+        part.T = (a->T - 1) % kMaxRowsALaunch + 1;
         if (plan_logprobs(&part, h->num_sms).total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
     }
     for (int64_t r0 = 0; r0 < a->T; r0 += kMaxRowsALaunch) {
         part.T = std::min<int64_t>(a->T - r0, kMaxRowsALaunch);
         const LogprobsPlan P = plan_logprobs(&part, h->num_sms);
+        if (P.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;
         LogprobsParams p{};
         p.logits = static_cast<const unsigned char*>(a->logits) + r0 * a->ld * es;
         p.ld = a->ld;
