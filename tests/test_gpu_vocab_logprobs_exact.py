@@ -160,3 +160,33 @@ def test_captured_on_another_stream(ops):  # noqa: F811
                                     temperature=1e-3, stream=s)
     s.synchronize()
     assert torch.equal(d, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, H, F])
+def test_rows_with_nan_and_infinities(ops, dtype):  # noqa: F811
+    # such a row's gradient is NaN where columns are allowed, and disturbs no other
+    T, V = 8, 5003
+    z, tokens, (g, ge) = make(T, V, dtype, 360), some_tokens(T, 3, V, 361), grads(T, 3, 363)
+    mask = random_mask(T, V, 365)
+    mask[6] = 0
+    may = torch.from_numpy(allowed(mask, T, V).copy()).cuda()
+    clean, want = check(ops, z, tokens, g, ge, 0.1, mask)
+    at = [int(may[i].nonzero()[9]) for i in range(6)]
+    z[1, at[1]] = float("nan")
+    z[2, at[2]] = INF
+    z[4] = float("nan")
+    z[5, at[5]] = INF
+    z[5, ::2] = -INF
+    z[3][~may[3]] = float("nan")                             # nothing that counts
+    z[0][~may[0]] = INF
+    for m in (None, mask):
+        r = ops.token_logprobs(z, tokens, temperature=0.1, token_mask=m, for_gradient=True)
+        d = ops.token_logprobs_backward(z, None, tokens, g, row_max=r.row_max, log_sum=r.log_sum, entropy=r.entropy,
+                                        grad_entropy=ge, temperature=0.1, token_mask=m)
+        ok = torch.ones(V, dtype=torch.bool, device="cuda")
+        for i in (1, 2, 4, 5):
+            inside = ok if m is None else may[i]
+            assert bool(d[i][inside].isnan().all()) and not d[i][~inside].any()
+        assert bool(r.log_sum[[1, 2, 4, 5]].isnan().all())
+    assert torch.equal(d[[0, 3, 6, 7]], want[[0, 3, 6, 7]])
+    assert ops.device_error() == 0
