@@ -642,9 +642,9 @@ lmloss_status lmloss_table4_logits(lmloss_vocab_handle h, const lmloss_table4_lo
         p.scale = a->scale;
         p.err = h->err;
         const int operands = T * (pairs ? 2 : 1);
-        // (fp32 logits of few rows are of pairs whatever the rows' type: their table's numbers are subnormal)
-        p.pairs = pairs || a->logits_dtype == LMLOSS_FP32;
-        const bool few = few_rows_fit(p);
+        // (few rows are pairs whatever their type where these fit: see table4_rows.cu)
+        p.pairs = pairs || 2 * T <= kFewRows;
+        const bool few = few_rows_fit(p) && (p.pairs || a->logits_dtype != LMLOSS_FP32);
         if (!few) {
             // (a first launch that is not of few rows is the call's: nothing has been launched yet)
             if (w.total > h->ws_bytes) return LMLOSS_ERR_INVALID_ARG;

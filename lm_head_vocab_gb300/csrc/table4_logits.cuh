@@ -175,13 +175,12 @@ __device__ __forceinline__ float group_top(int lanes, float top)
     return top;
 }
 // Sums over the `lanes` (4, 8 or 16) neighbouring threads of a group, 16 threads together.
-template <bool PAIR>
 __device__ __forceinline__ void group_sums(int lanes, float& sum, float& sum_lo)
 {
     const uint32_t together = 0xffffu << (threadIdx.x & 16);
     for (int o = 1; o < lanes; o <<= 1) {
         sum += __shfl_xor_sync(together, sum, o);
-        if (PAIR) sum_lo += __shfl_xor_sync(together, sum_lo, o);
+        sum_lo += __shfl_xor_sync(together, sum_lo, o);
     }
 }
 
