@@ -14,11 +14,11 @@
 //
 // The gradient is one more pass, from m, ln s and H alone: p = e^((z - m) / tau - ln s), or, given only lse, e^(y - lse).
 //
-// 4096 x 128256 bf16: forward 172 us without alternatives (0.91 of the copy's rate), 182 with 5, 244 with 64; the
-// gradient with entropies 310 us (1.01).  One row of 128256 with 20 alternatives: 11 us, the latency of two dependent
+// 4096 x 128256 bf16: forward 172 us without alternatives (0.91 of the copy's rate), 183 with 5, 245 with 64, 429 where
+// every row is summed again; the gradient with entropies 312 us (1.01).  One row of 128256 with 20 alternatives: 11 us, the latency of two dependent
 // steps (a part's threshold and ranking, the join).  The forward is bound by memory and instructions together (64%
 // of the issue slots: unpacking, maximum, ex2, two sums); alternatives add the work at a part's end, when few
-// loads are on their way.  Rows at odd elements: 2048 x 128251, 116 us (0.68), by their shifts.
+// loads are on their way.  Rows at odd elements: 2048 x 128251, 118 us (0.66), by their shifts.
 #include <algorithm>
 #include <cmath>
 

@@ -64,8 +64,9 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c)
     return r;
 }
 // The same less a zero point, (q - z) 2^-14 and (q - z) 2^-10, exact: under an exponent whose last place is 2^-14, less
-// 2^-4 + z 2^-14 or 2^-4 + z 2^-10.  As fp16's normal numbers: of subnormal ones the tensor cores cut sums off at some
-// 2^-24 of what their exponent could hold, 2^6 to 2^10 times what they do (logits of bf16 rows 5e-7 off, not 2e-7).
+// 2^-4 + z 2^-14 or 2^-4 + z 2^-10, exact.  As fp16's normal numbers: of subnormal ones the tensor cores cut sums off at some
+// 2^-24 of what their exponent could hold, 2^6 to 2^10 times what they do (logits of bf16 rows 5e-7 off, not 2e-7, and
+// far more beside one large column).
 __device__ __forceinline__ void widen_word(uint32_t w, __half2 z, __half2 z16, uint32_t* out)
 {
     const uint32_t w8 = w >> 8;
